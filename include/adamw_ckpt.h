@@ -97,7 +97,15 @@ extern "C" {
 #define CKPT_ACTION_WRITING 1 /* packed; being written in the background    */
 #define CKPT_ACTION_EXIT 2    /* written and durable; the caller should exit */
 
+/* Elements that share the scales of an 8-bit state (adamw_list_*).         */
+#define ADAMW_STATE_BLOCK 256
+
+/* layernorm_backward flags. */
+#define LAYERNORM_ACCUMULATE 1 /* add into dweight and dbias, do not replace  */
+
 typedef struct adamw_ctx adamw_ctx;
+typedef struct adamw_list adamw_list;
+typedef struct layernorm_ctx layernorm_ctx;
 
 /*
  * Creates a context for a flat state of n_params float32 values split into
@@ -676,6 +684,112 @@ ADAMW_API int ckpt_read_range(adamw_ctx* ctx, const char* path, int64_t offset,
  */
 ADAMW_API int ckpt_sha256_hex(const void* data, int64_t bytes, char* hex_out);
 ADAMW_API int ckpt_sha256_backend(void);
+
+/*
+ * The optimizer step over a list of tensors that live apart ([B] "Where the
+ * gradients live": one gradient buffer per weight tensor; [T]: all gradients
+ * joined into one vector g for the norm), with the Adam moments of each
+ * tensor in 32 or in 8 bits.  The formulas are adamw_clip_step's: one norm
+ * and one clip factor over the whole list, then the update of every tensor,
+ * in two kernels whatever the number of tensors.
+ *
+ * adamw_list_create: n_tensors tensors of numels[k] elements (each in
+ *   [0, 2^31 - 1]); state8[k] != 0 keeps tensor k's m and v in 8 bits (NULL:
+ *   none).  Allocates the table, the norm's scratch and a pinned mirror of
+ *   its result on the current device.  beta1 = 0.9, beta2 = 0.999,
+ *   eps = 1e-8 (adamw_list_set_hparams replaces them); decay on every tensor
+ *   (adamw_list_set_decay: one flag per tensor, NULL restores the default).
+ * adamw_list_bind: the arrays' device addresses, one per tensor in each
+ *   table (entries of empty tensors are not read).  w: float32.  g: g_dtype.
+ *   32-bit states: m, v float32, scales ignored.  8-bit states: m holds e4m3
+ *   values, v e5m2 values, d_m_scale[k] and d_v_scale[k] one float32 per
+ *   block of ADAMW_STATE_BLOCK elements (the last may be shorter): the state
+ *   is value times scale; all zero bytes are the zero state.  d_w_lp (may be
+ *   NULL): a copy of the new weights rounded to w_lp_dtype (BF16 or F16).
+ *   Every array must be aligned to its elements and none may overlap another.
+ *   Tensors whose w (and 32-bit m, v, g) lie on 16-byte, 16-bit arrays on
+ *   8-byte and 8-bit arrays on 4-byte boundaries take the vectorised path;
+ *   others are accepted and take a scalar one.  The caller owns the arrays
+ *   and keeps them while the list is bound to them.
+ * adamw_list_set_decay, adamw_list_bind: setup calls, which wait for all
+ *   work on the device before they change what a step reads.
+ * adamw_list_step: update t >= 1 on `stream`; the arguments mean what they
+ *   mean for adamw_clip_step_ex; flags: ADAMW_ZERO_GRAD.  The call does not
+ *   wait.  Steps of one list must be ordered on the device (one stream, or
+ *   events).  A non-finite norm leaves everything untouched, reported by
+ *   adamw_list_last_norm, which waits for the last step (ADAMW_ESTATE if
+ *   there was none; a step captured into a graph is not counted).
+ *
+ * 8-bit states.  After the update (from the moments in float32) a block's
+ * scale becomes the power of two that puts its largest |m| into [2^7, 2^8)
+ * and its largest v into [2^14, 2^15), not below 2^-126; each value is
+ * rounded at random to one of its two neighbours in the 8-bit format, with
+ * itself as the mean, because rounding to nearest would stop v: its change
+ * per step, about 1 - beta2, is far below half a spacing.  A positive v does
+ * not become 0.  The random number of element i of tensor k is a 32-bit hash
+ * of (seed, t, 256 B_k + i), B_k the number of blocks of the tensors before
+ * it: the same seed, steps and inputs give the same bytes, so a run resumed
+ * from copies of w, m, v and the scales continues bit for bit.
+ * Errors: ADAMW_EINVAL, ADAMW_ECUDA, ADAMW_ESTATE (a step before the arrays
+ * are bound), ADAMW_ENONFINITE (adamw_list_last_norm).
+ */
+ADAMW_API int adamw_list_create(int32_t n_tensors, const int64_t* numels,
+                                const uint8_t* state8, adamw_list** out);
+ADAMW_API int adamw_list_destroy(adamw_list* list);
+ADAMW_API int adamw_list_set_hparams(adamw_list* list, double beta1, double beta2, double eps);
+ADAMW_API int adamw_list_set_decay(adamw_list* list, const uint8_t* decay, int32_t n_tensors);
+ADAMW_API int adamw_list_bind(adamw_list* list, float* const* d_w, void* const* d_g,
+                              int32_t g_dtype, void* const* d_m, void* const* d_v,
+                              float* const* d_m_scale, float* const* d_v_scale,
+                              void* const* d_w_lp, int32_t w_lp_dtype);
+ADAMW_API int adamw_list_step(adamw_list* list, int32_t t, double lr, double wd, double clip,
+                              double grad_scale, uint32_t seed, int32_t flags, void* stream);
+ADAMW_API int adamw_list_last_norm(adamw_list* list, double* norm_out, float* scale_out);
+
+/*
+ * Layer norm, forward and backward ([B] "Every forward op gets a backward
+ * twin": k_layernorm_fwd and k_layernorm_bwd, the latter reading the saved
+ * mean and variance; "One gradient per weight tensor"; "Accumulation across
+ * micro-batches": backward adds into the gradient buffers).  For each of
+ * `rows` rows x of cols elements:
+ *   mean = sum(x) / cols;  rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps)
+ *   y = (x - mean) rstd weight + bias
+ * and, for the gradient dy of y, with xhat = (x - mean) rstd, a = dy weight:
+ *   dx = rstd (a - sum(a) / cols - xhat sum(a xhat) / cols)
+ *   dweight = sum over rows of dy xhat;  dbias = sum over rows of dy.
+ * Statistics, sums and products are float32 (the variance from the
+ * differences, in a second look at the row in registers); inputs are widened
+ * exactly and each output is rounded once.
+ *
+ * layernorm_create: for rows of cols elements, 1 <= cols <= 2^18; owns the
+ *   backward pass's partial sums (the only allocation), so calls of
+ *   layernorm_backward with one context must be ordered on the device.
+ * x, y, dy, dx: x_dtype; rows are x_stride (..., in elements, >= cols) apart,
+ *   elements of a row adjacent.  weight, bias: w_dtype (float32 or x_dtype);
+ *   weight NULL: 1, bias NULL: 0.  mean, rstd: float32, one per row; NULL in
+ *   the forward pass when no backward pass follows.  dweight, dbias:
+ *   grad_dtype (any), each may be NULL; summed in float32 in an order fixed
+ *   by rows and cols (the same bits every time), then rounded once;
+ *   LAYERNORM_ACCUMULATE adds the sum to what is there, in float32.
+ *   rows = 0 is accepted: dweight and dbias become 0 (or stay, accumulating).
+ * Every array must be aligned to its elements; outputs must not overlap
+ * inputs.  Rows whose arrays start at the same place within 16 bytes (8
+ * elements of float32: 32 bytes) are read and written in vectors, whatever
+ * that place is; otherwise the array that differs goes element by element.
+ * Asynchronous on `stream`.  Errors: ADAMW_EINVAL, ADAMW_ECUDA.
+ */
+ADAMW_API int layernorm_create(int32_t cols, layernorm_ctx** out);
+ADAMW_API int layernorm_destroy(layernorm_ctx* ctx);
+ADAMW_API int layernorm_forward(layernorm_ctx* ctx, const void* d_x, int64_t x_stride,
+                                int32_t x_dtype, const void* d_weight, const void* d_bias,
+                                int32_t w_dtype, void* d_y, int64_t y_stride, float* d_mean,
+                                float* d_rstd, int64_t rows, double eps, void* stream);
+ADAMW_API int layernorm_backward(layernorm_ctx* ctx, const void* d_dy, int64_t dy_stride,
+                                 const void* d_x, int64_t x_stride, int32_t x_dtype,
+                                 const void* d_weight, int32_t w_dtype, const float* d_mean,
+                                 const float* d_rstd, void* d_dx, int64_t dx_stride,
+                                 void* d_dweight, void* d_dbias, int32_t grad_dtype,
+                                 int64_t rows, int32_t flags, void* stream);
 
 /* Name of a status code, and the last failure's explanation (this thread). */
 ADAMW_API const char* adamw_strerror(int status);

@@ -25,6 +25,8 @@ CKPT_COPY_ENGINE = 2
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 ZERO_GRAD = 1
 TENSOR_NORMS = 2
+STATE_BLOCK = 256
+LAYERNORM_ACCUMULATE = 1
 LAUNCH_NO_PDL = 1
 LAUNCH_NO_ONEPASS = 2
 LAUNCH_TEST_BARRIER_TIMEOUT = 4
@@ -110,6 +112,22 @@ SIGNATURES = {
                                    _vp, _vp, _vp]),
     "ckpt_sha256_hex": (_c.c_int, [_vp, _c.c_int64, _c.c_char_p]),
     "ckpt_sha256_backend": (_c.c_int, []),
+    "adamw_list_create": (_c.c_int, [_c.c_int32, _vp, _vp, _c.POINTER(_vp)]),
+    "adamw_list_destroy": (_c.c_int, [_vp]),
+    "adamw_list_set_hparams": (_c.c_int, [_vp, _c.c_double, _c.c_double, _c.c_double]),
+    "adamw_list_set_decay": (_c.c_int, [_vp, _vp, _c.c_int32]),
+    "adamw_list_bind": (_c.c_int, [_vp, _vp, _vp, _c.c_int32, _vp, _vp, _vp, _vp, _vp,
+                                   _c.c_int32]),
+    "adamw_list_step": (_c.c_int, [_vp, _c.c_int32, _c.c_double, _c.c_double, _c.c_double,
+                                   _c.c_double, _c.c_uint32, _c.c_int32, _vp]),
+    "adamw_list_last_norm": (_c.c_int, [_vp, _c.POINTER(_c.c_double), _c.POINTER(_c.c_float)]),
+    "layernorm_create": (_c.c_int, [_c.c_int32, _c.POINTER(_vp)]),
+    "layernorm_destroy": (_c.c_int, [_vp]),
+    "layernorm_forward": (_c.c_int, [_vp, _vp, _c.c_int64, _c.c_int32, _vp, _vp, _c.c_int32, _vp,
+                                     _c.c_int64, _vp, _vp, _c.c_int64, _c.c_double, _vp]),
+    "layernorm_backward": (_c.c_int, [_vp, _vp, _c.c_int64, _vp, _c.c_int64, _c.c_int32, _vp,
+                                      _c.c_int32, _vp, _vp, _vp, _c.c_int64, _vp, _vp,
+                                      _c.c_int32, _c.c_int64, _c.c_int32, _vp]),
     "adamw_strerror": (_c.c_char_p, [_c.c_int]),
     "adamw_last_error": (_c.c_char_p, []),
 }
@@ -191,21 +209,18 @@ def _dev_ptr(t, n: int, name: str, ctx=None) -> int:
     return t.data_ptr()
 
 
-class Context:
-    """Owner of one ``adamw_ctx*``; freed by ``adamw_destroy`` or on GC."""
+class _Owner:
+    """Owner of one handle of the library; freed by close() or on GC."""
 
-    def __init__(self, handle: int, n: int, device=None):
+    _destroy = None
+
+    def __init__(self, handle: int, device=None):
         self.handle = handle
-        self.n = n
-        self.device = device  # CUDA device index the context was created on
-
-    @property
-    def num_tensors(self) -> int:
-        return library().adamw_num_tensors(self.handle)
+        self.device = device  # CUDA device index the handle was created on
 
     def close(self):
         if self.handle:
-            library().adamw_destroy(self.handle)
+            getattr(library(), self._destroy)(self.handle)
             self.handle = None
 
     def __del__(self):
@@ -219,6 +234,20 @@ class Context:
 
     def __exit__(self, *exc):
         self.close()
+
+
+class Context(_Owner):
+    """Owner of one ``adamw_ctx*``; freed by ``adamw_destroy`` or on GC."""
+
+    _destroy = "adamw_destroy"
+
+    def __init__(self, handle: int, n: int, device=None):
+        super().__init__(handle, device)
+        self.n = n
+
+    @property
+    def num_tensors(self) -> int:
+        return library().adamw_num_tensors(self.handle)
 
 
 def adamw_create(n_params: int, offsets=None, numels=None, flags: int = 0) -> Context:
@@ -500,6 +529,248 @@ def adamw_record_events(ctx: Context, ev_begin=None, ev_mid=None, ev_end=None):
     recorded once, so that they exist) around its two kernels."""
     h = [e.cuda_event if e is not None else None for e in (ev_begin, ev_mid, ev_end)]
     _check(library().adamw_record_events(ctx.handle, *h), "adamw_record_events")
+
+
+# ---------------------------------------------------------------------------
+# The step over a list of tensors
+# ---------------------------------------------------------------------------
+class TensorList(_Owner):
+    """Owner of one ``adamw_list*`` and of references to the tensors bound
+    to it."""
+
+    _destroy = "adamw_list_destroy"
+
+    def __init__(self, handle: int, numels, state8, device=None):
+        super().__init__(handle, device)
+        self.numels = numels
+        self.state8 = state8
+        self.tensors = None
+
+
+def adamw_list_create(w, g, m, v, m_scale=None, v_scale=None, w_lp=None,
+                      decay=None) -> TensorList:
+    """A list of tensors to be stepped together, bound to its arrays.
+
+    w, g, m, v: sequences of contiguous CUDA tensors, one entry per tensor.
+    w float32; g float32, bfloat16 or float16 (one type for the list); m and
+    v float32, or float8_e4m3fn and float8_e5m2 with m_scale and v_scale
+    float32 of ceil(numel / STATE_BLOCK) elements (entries of 32-bit states
+    may be None).  w_lp: an optional 16-bit copy of the weights.  decay: a
+    flag per tensor; None decays every tensor.  Tensors of both kinds of
+    state may share a list."""
+    import torch
+    n = len(w)
+    numels = [t.numel() if isinstance(t, torch.Tensor) else -1 for t in w]
+    state8 = [isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn for t in m]
+    if len(m) != n:
+        raise ValueError(f"m has {len(m)} tensors, w has {n}")
+    out = ctypes.c_void_p()
+    st = library().adamw_list_create(n, (_c.c_int64 * n)(*numels), (_c.c_uint8 * n)(*state8),
+                                     ctypes.byref(out))
+    _check(st, "adamw_list_create")
+    lst = TensorList(out.value, numels, state8, torch.cuda.current_device())
+    adamw_list_bind(lst, w, g, m, v, m_scale, v_scale, w_lp)
+    if decay is not None:
+        adamw_list_set_decay(lst, decay)
+    return lst
+
+
+def adamw_list_destroy(lst: TensorList):
+    lst.close()
+
+
+def _ptr_table(tensors, lst: TensorList, name: str, dtypes, counts, needed=None):
+    """The tensors' addresses as a C array; None where needed[k] is false."""
+    import torch
+    if len(tensors) != len(lst.numels):
+        raise ValueError(f"{name} has {len(tensors)} tensors, the list has {len(lst.numels)}")
+    table = (_vp * len(tensors))()
+    for k, t in enumerate(tensors):
+        if needed is not None and not needed[k]:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"{name}[{k}] must be a contiguous CUDA tensor")
+        if t.dtype != dtypes[k]:
+            raise TypeError(f"{name}[{k}] is {t.dtype}, not {dtypes[k]}")
+        if t.numel() != counts[k]:
+            raise ValueError(f"{name}[{k}] has {t.numel()} elements, not {counts[k]}")
+        _same_device(t, f"{name}[{k}]", lst)
+        table[k] = t.data_ptr()
+    return table
+
+
+def adamw_list_bind(lst: TensorList, w, g, m, v, m_scale=None, v_scale=None, w_lp=None):
+    """Binds the list to other arrays of the same sizes and state types (for
+    example gradients that were allocated anew); waits for the device."""
+    import torch
+    n = len(lst.numels)
+    f32 = [torch.float32] * n
+    gt = g[0].dtype if n and isinstance(g[0], torch.Tensor) else torch.float32
+    lt = w_lp[0].dtype if w_lp is not None and n and isinstance(w_lp[0], torch.Tensor) else None
+    table = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+    if gt not in table:
+        raise TypeError(f"g[0] is {gt}, not float32, bfloat16 or float16")
+    if w_lp is not None and n and lt not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"w_lp[0] is {lt}, not bfloat16 or float16")
+    m_type = [torch.float8_e4m3fn if s else torch.float32 for s in lst.state8]
+    v_type = [torch.float8_e5m2 if s else torch.float32 for s in lst.state8]
+    blocks = [-(-c // STATE_BLOCK) for c in lst.numels]
+    if any(lst.state8) and (m_scale is None or v_scale is None):
+        raise TypeError("8-bit states need m_scale and v_scale")
+    args = [_ptr_table(w, lst, "w", f32, lst.numels),
+            _ptr_table(g, lst, "g", [gt] * n, lst.numels), table[gt],
+            _ptr_table(m, lst, "m", m_type, lst.numels),
+            _ptr_table(v, lst, "v", v_type, lst.numels)]
+    for s, name in ((m_scale, "m_scale"), (v_scale, "v_scale")):
+        args.append(None if s is None
+                    else _ptr_table(s, lst, name, f32, blocks, lst.state8))
+    args.append(None if w_lp is None else _ptr_table(w_lp, lst, "w_lp", [lt] * n, lst.numels))
+    args.append(table[lt] if w_lp is not None and n else DTYPE_BF16)
+    _check(library().adamw_list_bind(lst.handle, *args), "adamw_list_bind")
+    lst.tensors = [list(x) for x in (w, g, m, v, m_scale or (), v_scale or (), w_lp or ())]
+
+
+def adamw_list_set_hparams(lst: TensorList, beta1: float, beta2: float, eps: float):
+    _check(library().adamw_list_set_hparams(lst.handle, beta1, beta2, eps),
+           "adamw_list_set_hparams")
+
+
+def adamw_list_set_decay(lst: TensorList, decay=None):
+    """Per-tensor decay flags; None restores decay on every tensor."""
+    flags = None if decay is None else (_c.c_uint8 * len(decay))(*[1 if f else 0 for f in decay])
+    _check(library().adamw_list_set_decay(lst.handle, flags, 0 if decay is None else len(decay)),
+           "adamw_list_set_decay")
+
+
+def adamw_list_step(lst: TensorList, t: int, lr: float, wd: float, clip: float,
+                    grad_scale: float = 1.0, seed: int = 0, zero_grad: bool = False,
+                    stream=None):
+    """Update t of every tensor of the list, in place; seed: of the random
+    rounding of 8-bit states (the step t enters it too)."""
+    st = library().adamw_list_step(lst.handle, t, lr, wd, clip, grad_scale, seed & 0xFFFFFFFF,
+                                   ZERO_GRAD if zero_grad else 0, _stream(stream))
+    if st != OK:
+        _check(st, "adamw_list_step")
+
+
+def adamw_list_last_norm(lst: TensorList):
+    """(norm, clip factor) of the last step; raises NonFiniteGradient."""
+    norm, scale = ctypes.c_double(), ctypes.c_float()
+    st = library().adamw_list_last_norm(lst.handle, ctypes.byref(norm), ctypes.byref(scale))
+    _check(st, "adamw_list_last_norm")
+    return norm.value, scale.value
+
+
+# ---------------------------------------------------------------------------
+# Layer norm
+# ---------------------------------------------------------------------------
+class LayerNorm(_Owner):
+    """Owner of one ``layernorm_ctx*``: rows of ``cols`` elements."""
+
+    _destroy = "layernorm_destroy"
+
+    def __init__(self, handle: int, cols: int, device=None):
+        super().__init__(handle, device)
+        self.cols = cols
+
+
+def layernorm_create(cols: int) -> LayerNorm:
+    import torch
+    out = ctypes.c_void_p()
+    _check(library().layernorm_create(int(cols), ctypes.byref(out)), "layernorm_create")
+    return LayerNorm(out.value, int(cols), torch.cuda.current_device())
+
+
+def layernorm_destroy(ln: LayerNorm):
+    ln.close()
+
+
+def _rows(t, ln: LayerNorm, name: str):
+    """(address, row stride, rows) of a tensor of shape (..., cols) whose rows
+    are evenly spaced."""
+    if not t.is_cuda or t.dim() < 1 or t.shape[-1] != ln.cols:
+        raise TypeError(f"{name} must be a CUDA tensor of shape (..., {ln.cols})")
+    _same_device(t, name, ln)
+    if t.is_contiguous():
+        return t.data_ptr(), ln.cols, t.numel() // ln.cols
+    if t.dim() > 2:
+        try:
+            t = t.view(-1, ln.cols)
+        except RuntimeError:
+            raise TypeError(f"{name}: rows must be evenly spaced") from None
+    if t.dim() < 2 or (t.stride(1) != 1 and ln.cols > 1):
+        raise TypeError(f"{name}: the elements of a row must be adjacent")
+    return t.data_ptr(), t.stride(0), t.shape[0]
+
+
+def _vector(t, n: int, name: str, ln: LayerNorm, dtype=None):
+    """Address of a contiguous tensor of n elements; None stays None."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be a contiguous CUDA tensor"
+                        + (f" of {dtype}" if dtype is not None else ""))
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+    _same_device(t, name, ln)
+    return t.data_ptr()
+
+
+def layernorm_forward(ln: LayerNorm, x, weight=None, bias=None, eps: float = 1e-5, y=None,
+                      mean=None, rstd=None, stream=None):
+    """(y, mean, rstd) of the rows of x (..., cols); outputs not given are
+    allocated.  weight and bias: float32 or the type of x; None: 1 and 0."""
+    import torch
+    xp, xs, rows = _rows(x, ln, "x")
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif y.dtype != x.dtype or y.shape != x.shape:
+        raise TypeError("y must have the type and shape of x")
+    if mean is None:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    yp, ys, _ = _rows(y, ln, "y")
+    wt = weight if weight is not None else bias
+    if bias is not None and bias.dtype != wt.dtype:
+        raise TypeError("weight and bias must have one type")
+    st = library().layernorm_forward(
+        ln.handle, xp, xs, _dtype_of(x), _vector(weight, ln.cols, "weight", ln),
+        _vector(bias, ln.cols, "bias", ln), DTYPE_F32 if wt is None else _dtype_of(wt), yp, ys,
+        _vector(mean, rows, "mean", ln, torch.float32),
+        _vector(rstd, rows, "rstd", ln, torch.float32), rows, eps, _stream(stream))
+    if st != OK:
+        _check(st, "layernorm_forward")
+    return y, mean, rstd
+
+
+def layernorm_backward(ln: LayerNorm, dy, x, weight, mean, rstd, dx=None, dweight=None,
+                       dbias=None, accumulate: bool = False, stream=None):
+    """(dx, dweight, dbias) from the gradient dy of y and the forward pass's
+    x, mean, rstd; dx is allocated if not given, dweight and dbias are
+    computed if given.  accumulate: add into dweight and dbias."""
+    import torch
+    xp, xs, rows = _rows(x, ln, "x")
+    gp, gs, _ = _rows(dy, ln, "dy")
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if dy.dtype != x.dtype or dx.dtype != x.dtype or dy.shape != x.shape or dx.shape != x.shape:
+        raise TypeError("dy and dx must have the type and shape of x")
+    dp, ds, _ = _rows(dx, ln, "dx")
+    gt = dweight if dweight is not None else dbias
+    if dbias is not None and dbias.dtype != gt.dtype:
+        raise TypeError("dweight and dbias must have one type")
+    st = library().layernorm_backward(
+        ln.handle, gp, gs, xp, xs, _dtype_of(x), _vector(weight, ln.cols, "weight", ln),
+        DTYPE_F32 if weight is None else _dtype_of(weight),
+        _vector(mean, rows, "mean", ln, torch.float32),
+        _vector(rstd, rows, "rstd", ln, torch.float32), dp, ds,
+        _vector(dweight, ln.cols, "dweight", ln), _vector(dbias, ln.cols, "dbias", ln),
+        DTYPE_F32 if gt is None else _dtype_of(gt), rows,
+        LAYERNORM_ACCUMULATE if accumulate else 0, _stream(stream))
+    if st != OK:
+        _check(st, "layernorm_backward")
+    return dx, dweight, dbias
 
 
 def ckpt_pack(ctx: Context, step: int, w, m, v, main_stream=None, side_stream=None):

@@ -25,7 +25,9 @@ CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
              "-I" + INCLUDE]
 
 CUDA_SOURCES = ["norm.cu", "step.cu", "onepass.cu", "ranks.cu", "pack.cu", "api.cu",
-                "writer.cu", "graph.cu", "noalloc.cu"]
+                "writer.cu", "graph.cu", "noalloc.cu", "list_step.cu", "list_api.cu",
+                "layernorm_fwd.cu", "layernorm_bwd.cu", "layernorm_bwd_f32.cu",
+                "layernorm_bwd_bf16.cu", "layernorm_bwd_f16.cu", "layernorm_api.cu"]
 CXX_SOURCES = ["ckpt_io.cpp", "manifest.cpp", "sha256.cpp"]
 
 
@@ -38,7 +40,9 @@ def nvcc() -> str:
 def _sources():
     return ([os.path.join(CSRC, s) for s in CUDA_SOURCES + CXX_SOURCES]
             + [os.path.join(CSRC, h) for h in ("internal.h", "ckpt_io.h", "common.cuh", "context.h",
-                                                 "norm_dev.cuh", "adamw_dev.cuh")]
+                                                 "norm_dev.cuh", "adamw_dev.cuh", "api_util.h",
+                                                 "list.h", "state8_dev.cuh", "layernorm.h",
+                                                 "layernorm_dev.cuh", "layernorm_bwd.cuh")]
             + [os.path.join(INCLUDE, "adamw_ckpt.h")])
 
 

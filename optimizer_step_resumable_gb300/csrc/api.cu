@@ -11,47 +11,17 @@
 #include <cuda_runtime.h>
 #include <unistd.h>
 
+#include "api_util.h"
 #include "context.h"
 #include "internal.h"
 
 namespace {
 
+using osr::cuda_fail;
+using osr::DeviceScope;
 using osr::fail;
 
 constexpr size_t kScratchHead = 256;  // NormResult + counter, padded
-
-int cuda_fail(cudaError_t e, const char* what)
-{
-    return fail(ADAMW_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-#define CUDA_TRY(expr)                                       \
-    do {                                                     \
-        cudaError_t e_ = (expr);                             \
-        if (e_ != cudaSuccess) return cuda_fail(e_, #expr);  \
-    } while (0)
-
-// Makes ctx->device current for the scope of one call and restores the
-// caller's device afterwards.
-class DeviceScope {
-public:
-    explicit DeviceScope(int device)
-    {
-        if (cudaGetDevice(&prev_) != cudaSuccess)
-            prev_ = -1;
-        if (prev_ != device && cudaSetDevice(device) == cudaSuccess)
-            switched_ = true;
-    }
-    ~DeviceScope()
-    {
-        if (switched_ && prev_ >= 0)
-            cudaSetDevice(prev_);
-    }
-
-private:
-    int prev_ = -1;
-    bool switched_ = false;
-};
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -203,25 +173,33 @@ int read_norm(adamw_ctx* c, double* norm_out, float* scale_out)
 
 namespace osr {
 
-StepScalars make_step_scalars(const adamw_ctx* c, int32_t t, double lr, double wd)
+StepScalars step_scalars(double beta1, double beta2, double eps, int32_t t, double lr, double wd)
 {
     // Bias-correction and decay scalars, in double on the host, rounded to
     // float once.
-    const double bc1 = 1.0 - std::pow(c->beta1, double(t));
-    const double bc2 = 1.0 - std::pow(c->beta2, double(t));
+    const double bc1 = 1.0 - std::pow(beta1, double(t));
+    const double bc2 = 1.0 - std::pow(beta2, double(t));
     StepScalars k;
-    k.beta1 = float(c->beta1);
-    k.omb1 = float(1.0 - c->beta1);
-    k.beta2 = float(c->beta2);
-    k.omb2 = float(1.0 - c->beta2);
-    k.eps = float(c->eps);
+    k.beta1 = float(beta1);
+    k.omb1 = float(1.0 - beta1);
+    k.beta2 = float(beta2);
+    k.omb2 = float(1.0 - beta2);
+    k.eps = float(eps);
     k.step_size = float(lr / bc1);
     k.inv_sqrt_bc2 = float(1.0 / std::sqrt(bc2));
     k.decay = float(1.0 - lr * wd);
     k.scale = 1.0f;
+    k.decay_mask = nullptr;
+    k.chunk_ctr = nullptr;
+    k.fin = NormFinish{nullptr, 0, 0.0, 1.0, nullptr, nullptr};
+    return k;
+}
+
+StepScalars make_step_scalars(const adamw_ctx* c, int32_t t, double lr, double wd)
+{
+    StepScalars k = step_scalars(c->beta1, c->beta2, c->eps, t, lr, wd);
     k.decay_mask = c->decay_mask_on ? c->d_decay_mask : nullptr;
     k.chunk_ctr = (c->dynamic_chunks && c->n >= kDynamicChunksMinN) ? c->d_chunk_ctr : nullptr;
-    k.fin = NormFinish{nullptr, 0, 0.0, 1.0, nullptr, nullptr};
     return k;
 }
 

@@ -63,6 +63,10 @@ struct StepScalars {
     NormFinish fin;
 };
 
+// The scalars of update t from the hyperparameters (api.cu): computed in
+// double, rounded to float once; no decay flags, no chunk counter, no norm.
+StepScalars step_scalars(double beta1, double beta2, double eps, int32_t t, double lr, double wd);
+
 // Tunables of the kernels (fixed at compile time; used in norm.cu, step.cu).
 constexpr int kNormThreads = 256;
 constexpr int kNormVecPerThread = 8;                 // float4 per thread per tile

@@ -1,0 +1,84 @@
+// list.h -- the step over a list of tensors: what its entry points
+// (list_api.cu) and its kernels (list_step.cu) share.  Not part of the ABI.
+#pragma once
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace osr {
+
+// 8-bit states keep one scale per block of this many elements of a tensor.
+constexpr int kBlockElems = ADAMW_STATE_BLOCK;
+
+// A warp's unit of work: up to kUnitBlocks consecutive blocks of one tensor.
+constexpr int kUnitBlocks = 4;
+constexpr int kUnitElems = kUnitBlocks * kBlockElems;
+
+constexpr uint32_t kListState8 = 1u;  // m, v in 8 bits with block scales
+constexpr uint32_t kListDecay = 2u;   // weight decay applies
+constexpr uint32_t kListVec = 4u;     // every array at its vector alignment
+
+// One tensor of the list, in device memory.
+struct ListTensor {
+    float* w;
+    void* g;
+    void* m;
+    void* v;
+    float* m_scale;  // 8-bit states: one per block
+    float* v_scale;
+    void* w_lp;      // 16-bit copy of the weights, or NULL
+    int64_t numel;
+    int64_t block0;  // blocks of the tensors before it: its place in the random sequence
+    uint32_t flags;
+    uint32_t pad;
+};
+
+// Unit u covers elements [unit * kUnitElems, ...) of tensor `tensor`.
+struct ListUnit {
+    int32_t tensor;
+    int32_t unit;
+};
+
+struct ListView {
+    const ListTensor* tensors;
+    const ListUnit* units;
+    int64_t n_units;
+};
+
+// Blocks of the norm reduction: a function of the number of units alone, so
+// that the order of the sum, and with it every bit of the norm, is too.
+inline int list_norm_blocks(int64_t n_units)
+{
+    const int64_t want = (n_units + kNormThreads / 32 - 1) / (kNormThreads / 32);
+    return int(want < 1 ? 1 : want > kNormBlocksMax ? kNormBlocksMax : want);
+}
+
+int query_list_blocks(int sm_count, int* blocks_out);
+// Per-block partial sums of g^2 over the list (one double per block).
+int launch_list_norm(const ListView& list, int32_t g_dtype, double* partials, void* stream);
+// The update; k.fin finishes the norm from those partials.  key: the random
+// numbers' key of this step (8-bit states).  blocks: resident blocks.
+int launch_list_step(const ListView& list, int32_t g_dtype, int32_t w_lp_dtype,
+                     const StepScalars& k, uint32_t key, bool zero_grad, int blocks,
+                     void* stream);
+
+// The 32-bit hash behind the random rounding: xor-shifts and odd
+// multipliers, each invertible, so distinct words stay distinct.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline uint32_t hash32(uint32_t x)
+{
+    x = (x ^ (x >> 16)) * 0x9E3779B1u;
+    x = (x ^ (x >> 15)) * 0x85EBCA77u;
+    return x ^ (x >> 16);
+}
+
+// The key of step t: the random number of position p is hash32(p ^ key).
+inline uint32_t rounding_key(uint32_t seed, int32_t t)
+{
+    return hash32(hash32(uint32_t(t)) ^ seed);
+}
+
+}  // namespace osr

@@ -1,0 +1,96 @@
+// state8_dev.cuh -- Adam moments in 8 bits: the values, the block scales and
+// the random rounding.
+//
+// A block is kBlockElems consecutive elements of one tensor, held by one
+// warp.  m is an e4m3 value (sign, 4 exponent, 3 significand bits) and v an
+// e5m2 value (5 exponent, 2 significand bits; never negative), each times
+// the block's scale.  The scale is the power of two that puts the block's
+// largest magnitude into [2^7, 2^8) for m and [2^14, 2^15) for v -- below
+// the formats' largest finite values 448 and 57344 by at least the factor
+// rounding can add -- so scaling is exact both ways and the only rounding
+// is the one to the 8-bit value.  v gets the wider format: it ranges over
+// the square of the gradients' range.
+//
+// That rounding is random, up or down to a neighbour with the value as the
+// mean.  With beta2 = 0.999 one step changes v by about 0.1%, against a
+// spacing of 12-25% between neighbours: rounded to nearest, v would never
+// move again; rounded at random it moves rarely but right on average.  The
+// random numbers are a hash of (key of the step, position), so a run is
+// reproducible bit for bit.  A positive v rounds to at least the smallest
+// e5m2 value: with v = 0 the update would be m / eps.
+//
+// Every operation is a single IEEE rounding in a fixed order (no fused
+// multiply-add), so the stored bytes follow from the formulas on any machine.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "list.h"
+
+namespace osr {
+namespace state8 {
+
+constexpr int kMTop = 7, kVTop = 14;  // exponent of a block's largest value
+
+// The biased binary32 exponent of the scale of a block whose largest
+// magnitude has the bits `most`; at least 1, so that the scale and its
+// reciprocal (biased exponent 254 - e) are normal numbers.
+__device__ __forceinline__ uint32_t scale_exponent(uint32_t most, int top)
+{
+    const int e = int(most >> 23) - top;
+    return uint32_t(e < 1 ? 1 : e);
+}
+__device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
+__device__ __forceinline__ float inverse_of(uint32_t e) { return __uint_as_float((254u - e) << 23); }
+
+// Two values of one format, widened exactly.
+__device__ __forceinline__ float2 widen_m(uint32_t two)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(two), __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+__device__ __forceinline__ float2 widen_v(uint32_t two)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(two), __NV_E5M2);
+    return __half22float2(__half2(h));
+}
+
+// |x| / scale moved down by the two formats' difference in exponent bias:
+// the 8-bit format's subnormal range then is binary32's, so that in either
+// range the bits below the last kept one are the low 20 (e4m3) or 21 (e5m2)
+// bits of the word; adding a random number of that many bits and cutting
+// them off rounds up with the right probability.  16 random bits are used
+// (their unit is 2^-16 of the spacing).
+__device__ __forceinline__ uint32_t narrow_m(float x, float inverse, uint32_t random)
+{
+    const float y = __fmul_rn(__fmul_rn(fabsf(x), inverse), 0x1p-120f);
+    uint32_t c = (__float_as_uint(y) + ((random >> 16) << 4)) >> 20;
+    c = c > 0x7fu ? 0x7fu : c;  // inf, nan: nan
+    return c | ((__float_as_uint(x) >> 24) & 0x80u);
+}
+__device__ __forceinline__ uint32_t narrow_v(float x, float inverse, uint32_t random)
+{
+    const float y = __fmul_rn(__fmul_rn(x, inverse), 0x1p-112f);
+    uint32_t c = (__float_as_uint(y) + ((random & 0xffffu) << 5)) >> 21;
+    c = c > 0x7cu ? 0x7cu : c;  // inf stays inf
+    return (c == 0u && x > 0.0f) ? 1u : c;
+}
+
+// One element's moments and weight (the formulas of adamw_elem, with every
+// product and sum rounded on its own).
+__device__ __forceinline__ void moments(float gh, float& m, float& v, const StepScalars& k)
+{
+    m = __fadd_rn(__fmul_rn(k.beta1, m), __fmul_rn(k.omb1, gh));
+    v = __fadd_rn(__fmul_rn(k.beta2, v), __fmul_rn(__fmul_rn(k.omb2, gh), gh));
+}
+__device__ __forceinline__ float weight(float w, float m, float v, const StepScalars& k, float d)
+{
+    const float denom = __fmaf_rn(__fsqrt_rn(v), k.inv_sqrt_bc2, k.eps);
+    return __fmaf_rn(w, d, -__fmul_rn(k.step_size, __fdiv_rn(m, denom)));
+}
+
+}  // namespace state8
+}  // namespace osr
