@@ -70,6 +70,19 @@ __device__ __forceinline__ float4 load4_cs<__half>(const __half* p)
                        __half2float(__ushort_as_half(static_cast<unsigned short>(r.y >> 16))));
 }
 
+// four 16-bit elements of two words, widened exactly
+__device__ __forceinline__ float4 widen4_bits(uint2 r, const __nv_bfloat16*)
+{
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
+                       __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+}
+__device__ __forceinline__ float4 widen4_bits(uint2 r, const __half*)
+{
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
 // 4 elements with the default L2 caching (ld.global.cg): for data that a
 // following kernel reads again (the norm's read of g, which the fused kernel
 // reads next), so that it may still find it in L2

@@ -11,8 +11,9 @@ namespace osr {
 // 8-bit states keep one scale per block of this many elements of a tensor.
 constexpr int kBlockElems = ADAMW_STATE_BLOCK;
 
-// A warp's unit of work: up to kUnitBlocks consecutive blocks of one tensor.
-constexpr int kUnitBlocks = 4;
+// A block's unit of work: up to 8 consecutive blocks of elements of one
+// tensor, one for each of its warps.
+constexpr int kUnitBlocks = kNormThreads / 32;
 constexpr int kUnitElems = kUnitBlocks * kBlockElems;
 
 constexpr uint32_t kListState8 = 1u;  // m, v in 8 bits with block scales
@@ -20,7 +21,7 @@ constexpr uint32_t kListDecay = 2u;   // weight decay applies
 constexpr uint32_t kListVec = 4u;     // every array at its vector alignment
 
 // One tensor of the list, in device memory.
-struct ListTensor {
+struct alignas(16) ListTensor {
     float* w;
     void* g;
     void* m;
@@ -28,13 +29,14 @@ struct ListTensor {
     float* m_scale;  // 8-bit states: one per block
     float* v_scale;
     void* w_lp;      // 16-bit copy of the weights, or NULL
-    int64_t numel;
     int64_t block0;  // blocks of the tensors before it: its place in the random sequence
+    int32_t numel;
     uint32_t flags;
-    uint32_t pad;
+    uint64_t pad;  // a multiple of 16 bytes
 };
 
-// Unit u covers elements [unit * kUnitElems, ...) of tensor `tensor`.
+// Unit u covers elements [unit * kUnitElems, ...) of tensor `tensor`.  The
+// units of tensors with 32-bit states come first, in the tensors' order.
 struct ListUnit {
     int32_t tensor;
     int32_t unit;
@@ -43,25 +45,24 @@ struct ListUnit {
 struct ListView {
     const ListTensor* tensors;
     const ListUnit* units;
-    int64_t n_units;
+    int32_t n_units;
 };
 
 // Blocks of the norm reduction: a function of the number of units alone, so
 // that the order of the sum, and with it every bit of the norm, is too.
-inline int list_norm_blocks(int64_t n_units)
+inline int list_norm_blocks(int32_t n_units)
 {
-    const int64_t want = (n_units + kNormThreads / 32 - 1) / (kNormThreads / 32);
-    return int(want < 1 ? 1 : want > kNormBlocksMax ? kNormBlocksMax : want);
+    return n_units < 1 ? 1 : n_units > kNormBlocksMax ? kNormBlocksMax : n_units;
 }
 
-int query_list_blocks(int sm_count, int* blocks_out);
 // Per-block partial sums of g^2 over the list (one double per block).
 int launch_list_norm(const ListView& list, int32_t g_dtype, double* partials, void* stream);
-// The update; k.fin finishes the norm from those partials.  key: the random
-// numbers' key of this step (8-bit states).  blocks: resident blocks.
-int launch_list_step(const ListView& list, int32_t g_dtype, int32_t w_lp_dtype,
-                     const StepScalars& k, uint32_t key, bool zero_grad, int blocks,
-                     void* stream);
+// The update of the units with 32-bit (plain) and with 8-bit states; k.fin
+// finishes the norm from the partials.  key: the random numbers' key of this
+// step (8-bit states).
+int launch_list_step(const ListView& plain, const ListView& eight, int32_t g_dtype,
+                     int32_t w_lp_dtype, const StepScalars& k, uint32_t key, bool zero_grad,
+                     int sm_count, void* stream);
 
 // The 32-bit hash behind the random rounding: xor-shifts and odd
 // multipliers, each invertible, so distinct words stay distinct.

@@ -16,16 +16,16 @@
 
 struct adamw_list {
     int device = -1;
-    int blocks = 0;  // resident blocks of the update kernel
+    int sm_count = 0;
     std::vector<int64_t> numels;
     std::vector<uint8_t> state8, decay;
     std::vector<osr::ListTensor> tensors;
-    int64_t n_units = 0;
+    int32_t n_units = 0, n_plain = 0;  // units, and those of 32-bit states
     double beta1 = 0.9, beta2 = 0.999, eps = 1e-8;
 
     osr::ListTensor* d_tensors = nullptr;
     osr::ListUnit* d_units = nullptr;
-    unsigned char* d_scratch = nullptr;  // [NormResult | pad][partials]
+    unsigned char* d_scratch = nullptr;  // [NormResult | counters x 4 | pad][partials]
     osr::NormResult* h_res = nullptr;    // pinned, mapped
     osr::NormResult* h_res_dev = nullptr;
     cudaEvent_t ev_norm = nullptr;
@@ -34,6 +34,7 @@ struct adamw_list {
 
     static constexpr size_t kHead = 256;
     osr::NormResult* d_res() const { return reinterpret_cast<osr::NormResult*>(d_scratch); }
+    uint32_t* d_counters() const { return reinterpret_cast<uint32_t*>(d_scratch + kHead / 2); }
     double* d_partials() const { return reinterpret_cast<double*>(d_scratch + kHead); }
 };
 
@@ -62,7 +63,7 @@ void free_list(adamw_list* l)
 
 int create_list(int32_t n_tensors, const int64_t* numels, const uint8_t* state8, adamw_list* l)
 {
-    std::vector<osr::ListUnit> units;
+    std::vector<osr::ListUnit> units, eight;
     int64_t block0 = 0;
     for (int32_t k = 0; k < n_tensors; ++k) {
         if (numels[k] < 0 || numels[k] > INT32_MAX)
@@ -72,25 +73,29 @@ int create_list(int32_t n_tensors, const int64_t* numels, const uint8_t* state8,
         l->state8.push_back(state8 && state8[k] ? 1 : 0);
         l->decay.push_back(1);
         osr::ListTensor t{};
-        t.numel = numels[k];
+        t.numel = int32_t(numels[k]);
         t.block0 = block0;
         l->tensors.push_back(t);
         block0 += (numels[k] + osr::kBlockElems - 1) / osr::kBlockElems;
         const int64_t n_units = (numels[k] + osr::kUnitElems - 1) / osr::kUnitElems;
         for (int64_t u = 0; u < n_units; ++u)
-            units.push_back(osr::ListUnit{k, int32_t(u)});
+            (l->state8.back() ? eight : units).push_back(osr::ListUnit{k, int32_t(u)});
     }
-    l->n_units = int64_t(units.size());
+    // the kernels count units in int32 and look a few grid strides ahead
+    if (units.size() + eight.size() > size_t(1) << 30)
+        return fail(ADAMW_EINVAL, "the list has more than 2^30 units of %d elements",
+                    osr::kUnitElems);
+    l->n_plain = int32_t(units.size());
+    units.insert(units.end(), eight.begin(), eight.end());
+    l->n_units = int32_t(units.size());
 
     cudaError_t e = cudaGetDevice(&l->device);
     if (e != cudaSuccess) {
         l->device = -1;
         return cuda_fail(e, "cudaGetDevice");
     }
-    int sm_count = 0;
-    CUDA_TRY(cudaDeviceGetAttribute(&sm_count, cudaDevAttrMultiProcessorCount, l->device));
-    CUDA_TRY(cudaError_t(osr::query_list_blocks(sm_count, &l->blocks)));
-    static_assert(sizeof(osr::NormResult) <= adamw_list::kHead, "scratch head layout");
+    CUDA_TRY(cudaDeviceGetAttribute(&l->sm_count, cudaDevAttrMultiProcessorCount, l->device));
+    static_assert(sizeof(osr::NormResult) <= adamw_list::kHead / 2, "scratch head layout");
     const size_t scratch = adamw_list::kHead + sizeof(double) * osr::kNormBlocksMax;
     CUDA_TRY(cudaMalloc(&l->d_tensors, sizeof(osr::ListTensor) * std::max(n_tensors, 1)));
     CUDA_TRY(cudaMalloc(&l->d_units, sizeof(osr::ListUnit) * std::max<size_t>(units.size(), 1)));
@@ -179,7 +184,7 @@ int bind_list(adamw_list* l, float* const* d_w, void* const* d_g, int32_t g_dtyp
             t.w_lp = d_w_lp[i];
         }
         auto at = [](const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; };
-        if (at(t.w, 16) && at(t.g, 4 * gs) && at(t.m, 4 * ss) && at(t.v, 4 * ss) && at(t.w_lp, 8))
+        if (at(t.w, 16) && at(t.g, 16) && at(t.m, 16) && at(t.v, 16) && at(t.w_lp, 8))
             t.flags |= osr::kListVec;
     }
     std::sort(ranges.begin(), ranges.end(),
@@ -307,15 +312,19 @@ int adamw_list_step(adamw_list* list, int32_t t, double lr, double wd, double cl
         return fail(ADAMW_EINVAL, "unknown flags 0x%x", flags);
     DeviceScope scope(list->device);
     osr::StepScalars k = osr::step_scalars(list->beta1, list->beta2, list->eps, t, lr, wd);
+    k.chunk_ctr = list->d_counters();
     k.fin = osr::NormFinish{list->d_partials(), osr::list_norm_blocks(list->n_units), clip,
                             grad_scale,         list->d_res(),
                             list->h_res_dev};
     const osr::ListView view{list->d_tensors, list->d_units, list->n_units};
+    const osr::ListView plain{list->d_tensors, list->d_units, list->n_plain};
+    const osr::ListView eight{list->d_tensors, list->d_units + list->n_plain,
+                              list->n_units - list->n_plain};
     int e = osr::launch_list_norm(view, list->g_dtype, list->d_partials(), stream);
     if (e == cudaSuccess)
-        e = osr::launch_list_step(view, list->g_dtype, list->w_lp_dtype, k,
+        e = osr::launch_list_step(plain, eight, list->g_dtype, list->w_lp_dtype, k,
                                   osr::rounding_key(seed, t), (flags & ADAMW_ZERO_GRAD) != 0,
-                                  list->blocks, stream);
+                                  list->sm_count, stream);
     if (e != cudaSuccess)
         return cuda_fail(cudaError_t(e), "list step launch");
     // for adamw_list_last_norm; a captured step is not one the host can wait for
