@@ -707,8 +707,9 @@ ADAMW_API int ckpt_sha256_backend(void);
  *   is value times scale; all zero bytes are the zero state.  d_w_lp (may be
  *   NULL): a copy of the new weights rounded to w_lp_dtype (BF16 or F16).
  *   Every array must be aligned to its elements and none may overlap another.
- *   Tensors whose arrays all lie on 16-byte boundaries (the copy: 8-byte)
- *   take the vectorised path; others are accepted and take a scalar one.  The caller owns the arrays
+ *   Tensors whose arrays all lie on boundaries of 8 of their elements (32
+ *   bytes of float32) take the vectorised path; others are accepted and go
+ *   element by element.  The caller owns the arrays
  *   and keeps them while the list is bound to them.
  * adamw_list_set_decay, adamw_list_bind: setup calls, which wait for all
  *   work on the device before they change what a step reads.

@@ -67,14 +67,18 @@ int launch_list_step(const ListView& plain, const ListView& eight, int32_t g_dty
 // The 32-bit hash behind the random rounding: xor-shifts and odd
 // multipliers, each invertible, so distinct words stay distinct.
 #ifdef __CUDACC__
-__host__ __device__
+#define OSR_BOTH __host__ __device__
+#else
+#define OSR_BOTH
 #endif
-inline uint32_t hash32(uint32_t x)
+OSR_BOTH inline uint32_t hash32_begin(uint32_t x) { return x ^ (x >> 16); }
+OSR_BOTH inline uint32_t hash32_end(uint32_t x)
 {
-    x = (x ^ (x >> 16)) * 0x9E3779B1u;
+    x *= 0x9E3779B1u;
     x = (x ^ (x >> 15)) * 0x85EBCA77u;
     return x ^ (x >> 16);
 }
+OSR_BOTH inline uint32_t hash32(uint32_t x) { return hash32_end(hash32_begin(x)); }
 
 // The key of step t: the random number of position p is hash32(p ^ key).
 inline uint32_t rounding_key(uint32_t seed, int32_t t)

@@ -184,7 +184,7 @@ int bind_list(adamw_list* l, float* const* d_w, void* const* d_g, int32_t g_dtyp
             t.w_lp = d_w_lp[i];
         }
         auto at = [](const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; };
-        if (at(t.w, 16) && at(t.g, 16) && at(t.m, 16) && at(t.v, 16) && at(t.w_lp, 8))
+        if (at(t.w, 32) && at(t.g, 8 * gs) && at(t.m, 8 * ss) && at(t.v, 8 * ss) && at(t.w_lp, 16))
             t.flags |= osr::kListVec;
     }
     std::sort(ranges.begin(), ranges.end(),

@@ -28,73 +28,33 @@
 #ifndef NORMB
 #define NORMB 4
 #endif
-#ifndef NRUN
-#define NRUN 4
-#endif
 namespace osr {
 namespace {
 
 constexpr int kWarps = kNormThreads / 32;
 constexpr int kLane = kBlockElems / 32;  // elements of a block per lane
 
-// Element j (of kLane) of a lane within its block: four consecutive ones and
-// four more half a block on (16-byte accesses, a warp's 512 in a row), or, for
-// arrays at other alignments and the last block of a tensor, one per stride
-// of 32.
-__device__ __forceinline__ int element(bool vec, int lane, int j)
-{
-    return vec ? (j >> 2) * (kBlockElems / 2) + lane * 4 + (j & 3) : j * 32 + lane;
-}
-
-__device__ __forceinline__ float4 as_float4(const float (&x)[kLane], int h)
-{
-    return make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
-}
-__device__ __forceinline__ void put4(float (&x)[kLane], int h, float4 a)
-{
-    x[4 * h] = a.x;
-    x[4 * h + 1] = a.y;
-    x[4 * h + 2] = a.z;
-    x[4 * h + 3] = a.w;
-}
+// A lane's kLane elements of a block are adjacent: lane * kLane, ...  In a
+// vector access a lane moves all of them (32 bytes of float32 in one
+// instruction), and a warp's accesses lie in a row.
 
 // ---------------------------------------------------------------------------
 // The norm.
 // ---------------------------------------------------------------------------
 
-// A lane's gradient elements of one block (`left` elements to the end of the
-// tensor; it may be none).
-template <typename G>
-__device__ __forceinline__ void load_norm(const G* g, bool aligned, int lane, int32_t left,
-                                          float4* x)
-{
-    if (aligned && left >= kBlockElems) {
-        x[0] = detail::load4_cg<G>(g + lane * 4);
-        x[1] = detail::load4_cg<G>(g + kBlockElems / 2 + lane * 4);
-    } else {
-        float y[kLane];
-#pragma unroll
-        for (int j = 0; j < kLane; ++j) {
-            const int i = j * 32 + lane;
-            y[j] = i < left ? detail::load1(g + i) : 0.0f;
-        }
-        x[0] = make_float4(y[0], y[1], y[2], y[3]);
-        x[1] = make_float4(y[4], y[5], y[6], y[7]);
-    }
-}
-
 // Level 1 of the norm: block b takes units b, b + the grid, ..., kRun at a
-// time; a thread's share of them is one run of squares (normdev::run_sumsq),
-// added up in double.
-constexpr int kRun = NRUN;
-
+// time, all of whose loads are on the way together (128 bytes a thread); a
+// thread's share of four blocks of elements is one run of squares
+// (normdev::run_sumsq), added up in double.  Default L2 priority: the update
+// reads g next.
 template <typename G>
 __global__ void __launch_bounds__(kNormThreads, NORMB)
     k_list_norm(ListView list, double* __restrict__ partials)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int kRun = 16 / int(sizeof(G));
     const int lane = threadIdx.x & 31;
-    const int32_t warp_e0 = int32_t(threadIdx.x >> 5) * kBlockElems;
+    const int32_t lane_e0 = int32_t(threadIdx.x >> 5) * kBlockElems + lane * kLane;
     const int32_t stride = int32_t(gridDim.x);
     const ListUnit none{0, -1};
     ListUnit next[kRun];
@@ -104,22 +64,29 @@ __global__ void __launch_bounds__(kNormThreads, NORMB)
         next[p] = u + p * stride < list.n_units ? list.units[u + p * stride] : none;
     double acc = 0.0;
     for (; u < list.n_units; u += kRun * stride) {
-        float4 x[2 * kRun];
-        ListUnit now[kRun];
+        detail::Raw8<G> x[kRun];
 #pragma unroll
         for (int p = 0; p < kRun; ++p) {
-            now[p] = next[p];
+            const ListUnit now = next[p];
             const int32_t v = u + (p + kRun) * stride;
             next[p] = v < list.n_units ? list.units[v] : none;
+            const ListTensor& t = list.tensors[now.tensor];
+            const int32_t e0 = now.unit * kUnitElems + lane_e0;
+            const int32_t left = now.unit < 0 ? 0 : t.numel - e0;
+            const G* const g = static_cast<const G*>(t.g) + e0;
+            if ((t.flags & kListVec) && left >= kLane)
+                x[p] = detail::load8_cg(g);
+            else
+                x[p] = detail::load8_part(g, left);
         }
 #pragma unroll
-        for (int p = 0; p < kRun; ++p) {
-            const ListTensor& t = list.tensors[now[p].tensor];
-            const int32_t e0 = now[p].unit * kUnitElems + warp_e0;
-            load_norm<G>(static_cast<const G*>(t.g) + e0, t.flags & kListVec, lane,
-                         now[p].unit < 0 ? 0 : t.numel - e0, x + 2 * p);
+        for (int q = 0; q < kRun; q += 4) {
+            float4 y[8];
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                detail::widen8(x[q + p], y[2 * p], y[2 * p + 1]);
+            acc += normdev::run_sumsq<8>(y);
         }
-        acc += normdev::run_sumsq<2 * kRun>(x);
     }
     acc = detail::block_sum<kNormThreads>(acc);
     if (threadIdx.x == 0)
@@ -139,92 +106,85 @@ struct Moments<false> {
 };
 template <>
 struct Moments<true> {
-    uint32_t m[2], v[2];  // four values a word
+    uint32_t m[kLane / 4], v[kLane / 4];  // four values a word
     float m_scale, v_scale;
 };
 
+// i: the lane's first element; left: from there to the end of the tensor.
 template <typename G, bool k8>
-__device__ __forceinline__ void load_block(const ListTensor& t, int32_t e0, int32_t left, bool vec,
-                                           int lane, float (&w)[kLane], float (&g)[kLane],
-                                           Moments<k8>& s)
+__device__ __forceinline__ void load_block(const ListTensor& t, int32_t i, int32_t left, bool vec,
+                                           float (&w)[kLane], float (&g)[kLane], Moments<k8>& s)
 {
-    const float* const wp = t.w + e0;
-    const G* const gp = static_cast<const G*>(t.g) + e0;
+    const float* const wp = t.w + i;
+    const G* const gp = static_cast<const G*>(t.g) + i;
     using State = typename std::conditional<k8, uint8_t, float>::type;
-    const State* const mp = static_cast<const State*>(t.m) + e0;
-    const State* const vp = static_cast<const State*>(t.v) + e0;
+    const State* const mp = static_cast<const State*>(t.m) + i;
+    const State* const vp = static_cast<const State*>(t.v) + i;
     if (vec) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = h * (kBlockElems / 2) + lane * 4;
-            put4(w, h, __ldcs(reinterpret_cast<const float4*>(wp + i)));
-            put4(g, h, detail::load4_cs<G>(gp + i));
-            if constexpr (k8) {
-                s.m[h] = __ldcs(reinterpret_cast<const uint32_t*>(mp + i));
-                s.v[h] = __ldcs(reinterpret_cast<const uint32_t*>(vp + i));
-            } else {
-                put4(s.m, h, __ldcs(reinterpret_cast<const float4*>(mp + i)));
-                put4(s.v, h, __ldcs(reinterpret_cast<const float4*>(vp + i)));
-            }
+        const detail::Raw8<float> a = detail::load8_cs(wp);
+        const detail::Raw8<G> b = detail::load8_cs(gp);
+        if constexpr (k8) {
+            const uint2 c = __ldcs(reinterpret_cast<const uint2*>(mp));
+            const uint2 d = __ldcs(reinterpret_cast<const uint2*>(vp));
+            s.m[0] = c.x, s.m[1] = c.y, s.v[0] = d.x, s.v[1] = d.y;
+        } else {
+            const detail::Raw8<float> c = detail::load8_cs(mp), d = detail::load8_cs(vp);
+            detail::widen8(c, s.m);
+            detail::widen8(d, s.v);
         }
+        detail::widen8(a, w);
+        detail::widen8(b, g);
     } else {
         if constexpr (k8)
             s.m[0] = s.m[1] = s.v[0] = s.v[1] = 0u;
 #pragma unroll
         for (int j = 0; j < kLane; ++j) {
-            const int i = j * 32 + lane;
-            const bool in = i < left;
-            w[j] = in ? wp[i] : 0.0f;
-            g[j] = in ? detail::load1(gp + i) : 0.0f;
+            const bool in = j < left;
+            w[j] = in ? wp[j] : 0.0f;
+            g[j] = in ? detail::load1(gp + j) : 0.0f;
             if constexpr (k8) {
-                s.m[j >> 2] |= in ? uint32_t(mp[i]) << (8 * (j & 3)) : 0u;
-                s.v[j >> 2] |= in ? uint32_t(vp[i]) << (8 * (j & 3)) : 0u;
+                s.m[j >> 2] |= in ? uint32_t(mp[j]) << (8 * (j & 3)) : 0u;
+                s.v[j >> 2] |= in ? uint32_t(vp[j]) << (8 * (j & 3)) : 0u;
             } else {
-                s.m[j] = in ? mp[i] : 0.0f;
-                s.v[j] = in ? vp[i] : 0.0f;
+                s.m[j] = in ? mp[j] : 0.0f;
+                s.v[j] = in ? vp[j] : 0.0f;
             }
         }
     }
     if constexpr (k8) {
-        s.m_scale = t.m_scale[e0 / kBlockElems];
-        s.v_scale = t.v_scale[e0 / kBlockElems];
+        s.m_scale = left > 0 ? t.m_scale[i / kBlockElems] : 0.0f;
+        s.v_scale = left > 0 ? t.v_scale[i / kBlockElems] : 0.0f;
     }
 }
 
 // The update of a block, in registers.  8-bit states: m, v become the new
 // bytes and scales; everything past the end of a partial block is 0 and
 // leaves the block's largest values alone.
-__device__ __forceinline__ void update_block(const ListTensor&, int32_t, bool, int,
-                                             float (&w)[kLane], const float (&g)[kLane],
-                                             Moments<false>& x, float s, const StepScalars& k,
+__device__ __forceinline__ void update_block(const ListTensor&, int32_t, float (&w)[kLane],
+                                             const float (&g)[kLane], Moments<false>& x, float s, const StepScalars& k,
                                              float d, uint32_t)
 {
 #pragma unroll
     for (int j = 0; j < kLane; ++j)
         adamwdev::adamw_elem(w[j], g[j], x.m[j], x.v[j], s, k, d);
 }
-__device__ __forceinline__ void update_block(const ListTensor& t, int32_t e0, bool vec, int lane,
-                                             float (&w)[kLane], const float (&g)[kLane],
-                                             Moments<true>& x, float s, const StepScalars& k,
+__device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, float (&w)[kLane],
+                                             const float (&g)[kLane], Moments<true>& x, float s, const StepScalars& k,
                                              float d, uint32_t key)
 {
+    // A scale is a power of two, so beta times the scale times the value is
+    // rounded as beta times the widened value is.
+    const float b1 = __fmul_rn(k.beta1, x.m_scale), b2 = __fmul_rn(k.beta2, x.v_scale);
     float m[kLane], v[kLane];
     float m_most = 0.0f, v_most = 0.0f;
 #pragma unroll
     for (int j = 0; j < kLane; j += 2) {
         const float2 m2 = state8::widen_m((x.m[j >> 2] >> (8 * (j & 3))) & 0xffffu);
         const float2 v2 = state8::widen_v((x.v[j >> 2] >> (8 * (j & 3))) & 0xffffu);
-        m[j] = __fmul_rn(m2.x, x.m_scale);
-        m[j + 1] = __fmul_rn(m2.y, x.m_scale);
-        v[j] = __fmul_rn(v2.x, x.v_scale);
-        v[j + 1] = __fmul_rn(v2.y, x.v_scale);
-    }
-#pragma unroll
-    for (int j = 0; j < kLane; ++j) {
-        state8::moments(__fmul_rn(g[j], s), m[j], v[j], k);
-        w[j] = state8::weight(w[j], m[j], v[j], k, d);
-        m_most = fmaxf(m_most, fabsf(m[j]));
-        v_most = fmaxf(v_most, v[j]);
+        state8::moments(__fmul_rn(g[j], s), m2.x, v2.x, b1, b2, k, m[j], v[j]);
+        state8::moments(__fmul_rn(g[j + 1], s), m2.y, v2.y, b1, b2, k, m[j + 1], v[j + 1]);
+        m_most = state8::largest(m_most, fabsf(m[j]), fabsf(m[j + 1]));
+        v_most = state8::largest(v_most, v[j], v[j + 1]);
     }
     // non-negative floats order as their bits do
     const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m_most));
@@ -233,84 +193,94 @@ __device__ __forceinline__ void update_block(const ListTensor& t, int32_t e0, bo
     const uint32_t ve = state8::scale_exponent(vb, state8::kVTop);
     x.m_scale = state8::scale_of(me);
     x.v_scale = state8::scale_of(ve);
-    const uint64_t p0 = uint64_t(t.block0) * kBlockElems + uint32_t(e0);
-    const uint32_t here = key ^ (uint32_t(p0 >> 32) * 0x9E3779B1u);
-    uint32_t r[kLane];
+    // The random numbers: the hash of position ^ key.  The elements of a lane
+    // differ in the lowest three bits only, which the hash's first step
+    // (x ^ x >> 16) leaves in place: it is done once for all of them.
+    const uint64_t p0 = uint64_t(t.block0) * kBlockElems + uint32_t(i);
+    const uint32_t first = hash32_begin(uint32_t(p0) ^ key ^
+                                        (uint32_t(p0 >> 32) * 0x9E3779B1u));
+    const bool fast = mb < state8::kMFast && vb < state8::kVFast;  // the same in every lane
+    const float inv = fast ? k.inv_sqrt_bc2 * state8::kRootUnit : k.inv_sqrt_bc2;
 #pragma unroll
-    for (int j = 0; j < kLane; ++j)
-        r[j] = hash32((uint32_t(p0) + uint32_t(element(vec, lane, j))) ^ here);
-    if (mb < state8::kMFast && vb < state8::kVFast) {  // the same in every lane
+    for (int h = 0; h < 2; ++h) {
+        uint32_t r[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            x.m[h] = state8::narrow4_m(m + 4 * h, state8::move_m(me), r + 4 * h);
-            x.v[h] = state8::narrow4_v(v + 4 * h, state8::move_v(ve), r + 4 * h);
-        }
-    } else {
-        x.m[0] = x.m[1] = x.v[0] = x.v[1] = 0u;
+        for (int j = 0; j < 4; ++j)
+            r[j] = hash32_end(first ^ uint32_t(4 * h + j));
+        const float* const mh = m + 4 * h;
+        const float* const vh = v + 4 * h;
+        float* const wh = w + 4 * h;
+        if (fast) {
 #pragma unroll
-        for (int j = 0; j < kLane; ++j) {
-            x.m[j >> 2] |= state8::narrow_m(m[j], state8::inverse_of(me), r[j]) << (8 * (j & 3));
-            x.v[j >> 2] |= state8::narrow_v(v[j], state8::inverse_of(ve), r[j]) << (8 * (j & 3));
+            for (int j = 0; j < 4; ++j)
+                wh[j] = state8::weight(wh[j], mh[j], __fmaf_rn(state8::root_fast(vh[j]), inv, k.eps),
+                                       k, d);
+            x.m[h] = state8::narrow4_m(mh, state8::move_m(me), r);
+            x.v[h] = state8::narrow4_v(vh, state8::move_v(ve), r);
+        } else {
+            x.m[h] = x.v[h] = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                wh[j] = state8::weight(wh[j], mh[j], __fmaf_rn(__fsqrt_rn(vh[j]), inv, k.eps), k, d);
+                x.m[h] |= state8::narrow_m(mh[j], state8::inverse_of(me), r[j]) << (8 * j);
+                x.v[h] |= state8::narrow_v(vh[j], state8::inverse_of(ve), r[j]) << (8 * j);
+            }
         }
     }
 }
 
 template <typename G, bool k8>
-__device__ __forceinline__ void store_block(const ListTensor& t, int32_t e0, int32_t left,
-                                            bool vec, int lane, const float (&w)[kLane],
-                                            const Moments<k8>& s, bool zero_grad,
-                                            int32_t w_lp_dtype)
+__device__ __forceinline__ void store_block(const ListTensor& t, int32_t i, int32_t left, bool vec,
+                                            const float (&w)[kLane], const Moments<k8>& s,
+                                            bool zero_grad, int32_t w_lp_dtype)
 {
-    float* const wp = t.w + e0;
-    G* const gp = static_cast<G*>(t.g) + e0;
+    float* const wp = t.w + i;
+    G* const gp = static_cast<G*>(t.g) + i;
     using State = typename std::conditional<k8, uint8_t, float>::type;
-    State* const mp = static_cast<State*>(t.m) + e0;
-    State* const vp = static_cast<State*>(t.v) + e0;
+    State* const mp = static_cast<State*>(t.m) + i;
+    State* const vp = static_cast<State*>(t.v) + i;
     if (vec) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = h * (kBlockElems / 2) + lane * 4;
-            __stcs(reinterpret_cast<float4*>(wp + i), as_float4(w, h));
-            if constexpr (k8) {
-                __stcs(reinterpret_cast<uint32_t*>(mp + i), s.m[h]);
-                __stcs(reinterpret_cast<uint32_t*>(vp + i), s.v[h]);
-            } else {
-                __stcs(reinterpret_cast<float4*>(mp + i), as_float4(s.m, h));
-                __stcs(reinterpret_cast<float4*>(vp + i), as_float4(s.v, h));
-            }
-            if (t.w_lp && w_lp_dtype == kDtypeF16)
-                detail::store4_lp_cs(static_cast<__half*>(t.w_lp) + e0 + i, as_float4(w, h));
-            else if (t.w_lp)
-                detail::store4_lp_cs(static_cast<__nv_bfloat16*>(t.w_lp) + e0 + i, as_float4(w, h));
-            if (zero_grad)
-                detail::store4_zero_cs(gp + i);
+        detail::store8_cs(wp, w);
+        if constexpr (k8) {
+            __stcs(reinterpret_cast<uint2*>(mp), make_uint2(s.m[0], s.m[1]));
+            __stcs(reinterpret_cast<uint2*>(vp), make_uint2(s.v[0], s.v[1]));
+        } else {
+            detail::store8_cs(mp, s.m);
+            detail::store8_cs(vp, s.v);
+        }
+        if (t.w_lp && w_lp_dtype == kDtypeF16)
+            detail::store8_cs(static_cast<__half*>(t.w_lp) + i, w);
+        else if (t.w_lp)
+            detail::store8_cs(static_cast<__nv_bfloat16*>(t.w_lp) + i, w);
+        if (zero_grad) {
+            const float zero[kLane] = {};
+            detail::store8_cs(gp, zero);
         }
     } else {
 #pragma unroll
         for (int j = 0; j < kLane; ++j) {
-            const int i = j * 32 + lane;
-            if (i >= left)
+            if (j >= left)
                 continue;
-            wp[i] = w[j];
+            wp[j] = w[j];
             if constexpr (k8) {
-                mp[i] = uint8_t(s.m[j >> 2] >> (8 * (j & 3)));
-                vp[i] = uint8_t(s.v[j >> 2] >> (8 * (j & 3)));
+                mp[j] = uint8_t(s.m[j >> 2] >> (8 * (j & 3)));
+                vp[j] = uint8_t(s.v[j >> 2] >> (8 * (j & 3)));
             } else {
-                mp[i] = s.m[j];
-                vp[i] = s.v[j];
+                mp[j] = s.m[j];
+                vp[j] = s.v[j];
             }
             if (t.w_lp && w_lp_dtype == kDtypeF16)
-                detail::store1_lp(static_cast<__half*>(t.w_lp) + e0 + i, w[j]);
+                detail::store1_lp(static_cast<__half*>(t.w_lp) + i + j, w[j]);
             else if (t.w_lp)
-                detail::store1_lp(static_cast<__nv_bfloat16*>(t.w_lp) + e0 + i, w[j]);
+                detail::store1_lp(static_cast<__nv_bfloat16*>(t.w_lp) + i + j, w[j]);
             if (zero_grad)
-                detail::store1_zero(gp + i);
+                detail::store1_zero(gp + j);
         }
     }
     if constexpr (k8) {
-        if (lane == 0) {
-            t.m_scale[e0 / kBlockElems] = s.m_scale;
-            t.v_scale[e0 / kBlockElems] = s.v_scale;
+        if (i % kBlockElems == 0 && left > 0) {  // one lane of the warp
+            t.m_scale[i / kBlockElems] = s.m_scale;
+            t.v_scale[i / kBlockElems] = s.v_scale;
         }
     }
 }
@@ -333,7 +303,7 @@ __global__ void __launch_bounds__(kNormThreads, MINB)
                 int32_t w_lp_dtype)
 {
     const int lane = threadIdx.x & 31;
-    const int32_t warp_e0 = int32_t(threadIdx.x >> 5) * kBlockElems;
+    const int32_t lane_e0 = int32_t(threadIdx.x >> 5) * kBlockElems + lane * kLane;
     __shared__ ListTensor s_tensor[2];
     __shared__ int32_t s_unit[2];  // its unit, or -1: no more
     __shared__ float s_scale;
@@ -364,13 +334,15 @@ __global__ void __launch_bounds__(kNormThreads, MINB)
         __syncthreads();
         const ListTensor& t = s_tensor[i & 1];
         const int32_t unit = s_unit[i & 1];
-        const int32_t e0 = unit * kUnitElems + warp_e0;
-        const int32_t left = unit < 0 ? 0 : t.numel - e0;
-        const bool vec = left >= kBlockElems && (t.flags & kListVec);
+        const int32_t e = unit * kUnitElems + lane_e0;  // the lane's first element
+        const int32_t left = unit < 0 ? 0 : t.numel - e;
+        const bool vec = left >= kLane && (t.flags & kListVec);
+        // whether the warp has any element: its lanes meet in the block's sums
+        const bool any = unit >= 0 && left + lane * kLane > 0;
         float w[kLane], g[kLane];
         Moments<k8> x;
-        if (left > 0)
-            load_block<G, k8>(t, e0, left, vec, lane, w, g, x);
+        if (any)
+            load_block<G, k8>(t, e, left, vec, w, g, x);
         if (threadIdx.x < 32 && unit >= 0)
             fetch((i + 1) & 1);
         if (i == 0) {
@@ -392,10 +364,9 @@ __global__ void __launch_bounds__(kNormThreads, MINB)
         }
         if (unit < 0)
             break;
-        if (left > 0) {
-            update_block(t, e0, vec, lane, w, g, x, s, k, (t.flags & kListDecay) ? k.decay : 1.0f,
-                         key);
-            store_block<G, k8>(t, e0, left, vec, lane, w, x, zero_grad, w_lp_dtype);
+        if (any) {
+            update_block(t, e, w, g, x, s, k, (t.flags & kListDecay) ? k.decay : 1.0f, key);
+            store_block<G, k8>(t, e, left, vec, w, x, zero_grad, w_lp_dtype);
         }
     }
     if (ctr && threadIdx.x == 0) {

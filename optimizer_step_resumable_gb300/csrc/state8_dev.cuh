@@ -122,21 +122,33 @@ __device__ __forceinline__ uint32_t narrow4_v(const float* x, float move, const 
 }
 
 // One element's moments and weight (the formulas of adamw_elem, with every
-// product and sum rounded on its own).
-__device__ __forceinline__ void moments(float gh, float& m, float& v, const StepScalars& k)
+// product and sum of the moments rounded on its own).  b1 and b2: the betas
+// times the block's old scales; denom: sqrt(v_hat) + eps.
+__device__ __forceinline__ void moments(float gh, float m_old, float v_old, float b1, float b2,
+                                        const StepScalars& k, float& m, float& v)
 {
-    m = __fadd_rn(__fmul_rn(k.beta1, m), __fmul_rn(k.omb1, gh));
-    v = __fadd_rn(__fmul_rn(k.beta2, v), __fmul_rn(__fmul_rn(k.omb2, gh), gh));
+    m = __fadd_rn(__fmul_rn(b1, m_old), __fmul_rn(k.omb1, gh));
+    v = __fadd_rn(__fmul_rn(b2, v_old), __fmul_rn(__fmul_rn(k.omb2, gh), gh));
 }
-__device__ __forceinline__ float weight(float w, float m, float v, const StepScalars& k, float d)
+__device__ __forceinline__ float weight(float w, float m, float denom, const StepScalars& k,
+                                        float d)
 {
-    // square root and quotient to 2 units of 2^-23 (the update is a small
-    // part of w; both correctly rounded cost 20 of 100 instructions)
-    float root;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
-    const float denom = __fmaf_rn(root, k.inv_sqrt_bc2, k.eps);
-    return __fmaf_rn(w, d, -__fmul_rn(k.step_size, __fdividef(m, denom)));
+    // the quotient to 2 units of 2^-23 (denom is 0 or a normal number): the
+    // update is a small part of w
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(denom));
+    return __fmaf_rn(w, d, -__fmul_rn(k.step_size, __fmul_rn(m, r)));
 }
+// sqrt(v) / kRootUnit for v below kVFast, to 2^-23: moved up by 2^32 first,
+// so that the square root, which takes subnormal numbers for 0, meets none.
+constexpr float kRootUnit = 0x1p-16f;
+__device__ __forceinline__ float root_fast(float v)
+{
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmul_rn(v, 0x1p32f)));
+    return r;
+}
+__device__ __forceinline__ float largest(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 }  // namespace state8
 }  // namespace osr
