@@ -6,6 +6,9 @@
 
 #include "internal.h"
 
+#ifndef STEPT
+#define STEPT 256
+#endif
 namespace osr {
 
 // 8-bit states keep one scale per block of this many elements of a tensor.
@@ -13,7 +16,7 @@ constexpr int kBlockElems = ADAMW_STATE_BLOCK;
 
 // A block's unit of work: up to 8 consecutive blocks of elements of one
 // tensor, one for each of its warps.
-constexpr int kUnitBlocks = kNormThreads / 32;
+constexpr int kUnitBlocks = STEPT / 32;
 constexpr int kUnitElems = kUnitBlocks * kBlockElems;
 
 constexpr uint32_t kListState8 = 1u;  // m, v in 8 bits with block scales

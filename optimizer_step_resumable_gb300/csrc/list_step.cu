@@ -31,7 +31,7 @@
 namespace osr {
 namespace {
 
-constexpr int kWarps = kNormThreads / 32;
+constexpr int kStepThreads = kUnitElems / (kBlockElems / 32);
 constexpr int kLane = kBlockElems / 32;  // elements of a block per lane
 
 // A lane's kLane elements of a block are adjacent: lane * kLane, ...  In a
@@ -42,53 +42,67 @@ constexpr int kLane = kBlockElems / 32;  // elements of a block per lane
 // The norm.
 // ---------------------------------------------------------------------------
 
-// Level 1 of the norm: block b takes units b, b + the grid, ..., kRun at a
-// time, all of whose loads are on the way together (128 bytes a thread); a
-// thread's share of four blocks of elements is one run of squares
-// (normdev::run_sumsq), added up in double.  Default L2 priority: the update
-// reads g next.
+// Level 1 of the norm.  Block b takes the contiguous units [U b / P,
+// U (b + 1) / P), tensor by tensor: within a tensor it streams, with no table
+// between two loads.  Each thread has two sets of kSet loads, one on the way
+// while the other is summed: a run of normdev::run_sumsq, added to a sum of
+// two floats (48 bits; binary64 additions run at 1/64 of the rate and took a
+// third of the kernel's time).  Default L2 priority: the update reads g next.
 template <typename G>
 __global__ void __launch_bounds__(kNormThreads, NORMB)
     k_list_norm(ListView list, double* __restrict__ partials)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kRun = 16 / int(sizeof(G));
-    const int lane = threadIdx.x & 31;
-    const int32_t lane_e0 = int32_t(threadIdx.x >> 5) * kBlockElems + lane * kLane;
-    const int32_t stride = int32_t(gridDim.x);
-    const ListUnit none{0, -1};
-    ListUnit next[kRun];
-    int32_t u = int32_t(blockIdx.x);
-#pragma unroll
-    for (int p = 0; p < kRun; ++p)
-        next[p] = u + p * stride < list.n_units ? list.units[u + p * stride] : none;
+    constexpr int kSet = sizeof(G) == 2 ? 4 : 2;
+    constexpr int kTile = kNormThreads * kLane;  // elements of the block's one load
+    const int32_t lo = int32_t(int64_t(list.n_units) * blockIdx.x / gridDim.x);
+    const int32_t hi = int32_t(int64_t(list.n_units) * (blockIdx.x + 1) / gridDim.x);
     double acc = 0.0;
-    for (; u < list.n_units; u += kRun * stride) {
-        detail::Raw8<G> x[kRun];
+    float sum_hi = 0.0f, sum_lo = 0.0f;
+    for (int32_t u = lo; u < hi;) {
+        const ListUnit unit = list.units[u];
+        const ListTensor& t = list.tensors[unit.tensor];
+        const int32_t e0 = unit.unit * kUnitElems, left = t.numel - e0;
+        const int32_t units = (left - 1) / kUnitElems + 1;  // to the tensor's end
+        const int32_t mine = units < hi - u ? units : hi - u;
+        const int32_t end = mine < units ? mine * kUnitElems : left;
+        u += mine;
+        const G* const g = static_cast<const G*>(t.g) + e0;
+        const bool aligned = t.flags & kListVec;
+        int32_t i = int32_t(threadIdx.x) * kLane;
+        detail::Raw8<G> x[2][kSet];
+        auto load = [&](detail::Raw8<G>(&to)[kSet]) {
 #pragma unroll
-        for (int p = 0; p < kRun; ++p) {
-            const ListUnit now = next[p];
-            const int32_t v = u + (p + kRun) * stride;
-            next[p] = v < list.n_units ? list.units[v] : none;
-            const ListTensor& t = list.tensors[now.tensor];
-            const int32_t e0 = now.unit * kUnitElems + lane_e0;
-            const int32_t left = now.unit < 0 ? 0 : t.numel - e0;
-            const G* const g = static_cast<const G*>(t.g) + e0;
-            if ((t.flags & kListVec) && left >= kLane)
-                x[p] = detail::load8_cg(g);
-            else
-                x[p] = detail::load8_part(g, left);
-        }
+            for (int p = 0; p < kSet; ++p, i += kTile)
+                to[p] = aligned && end - i >= kLane ? detail::load8_cg(g + i)
+                                                    : detail::load8_part(g + i, end - i);
+        };
+        auto sum = [&](const detail::Raw8<G>(&from)[kSet]) {
+            float4 y[2 * kSet];
 #pragma unroll
-        for (int q = 0; q < kRun; q += 4) {
-            float4 y[8];
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                detail::widen8(x[q + p], y[2 * p], y[2 * p + 1]);
-            acc += normdev::run_sumsq<8>(y);
+            for (int p = 0; p < kSet; ++p)
+                detail::widen8(from[p], y[2 * p], y[2 * p + 1]);
+            float r;
+            if (normdev::run_sumsq_fast<2 * kSet>(y, r) && r <= 0x1p100f) {
+                // sum + part is the exact sum of the runs but for 2^-24 of part
+                const float next = __fadd_rn(sum_hi, r);
+                const float back = __fsub_rn(next, sum_hi);
+                sum_lo = __fadd_rn(sum_lo, __fadd_rn(__fsub_rn(sum_hi, __fsub_rn(next, back)),
+                                                     __fsub_rn(r, back)));
+                sum_hi = next;
+            } else {
+                acc += normdev::run_sumsq<2 * kSet>(y);
+            }
+        };
+        load(x[0]);
+        for (int32_t done = 0; done < end; done += 2 * kSet * kTile) {
+            load(x[1]);
+            sum(x[0]);
+            load(x[0]);
+            sum(x[1]);
         }
     }
-    acc = detail::block_sum<kNormThreads>(acc);
+    acc = detail::block_sum<kNormThreads>(acc + (double(sum_hi) + double(sum_lo)));
     if (threadIdx.x == 0)
         partials[blockIdx.x] = acc;
 }
@@ -179,12 +193,14 @@ __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, flo
     float m_most = 0.0f, v_most = 0.0f;
 #pragma unroll
     for (int j = 0; j < kLane; j += 2) {
-        const float2 m2 = state8::widen_m((x.m[j >> 2] >> (8 * (j & 3))) & 0xffffu);
-        const float2 v2 = state8::widen_v((x.v[j >> 2] >> (8 * (j & 3))) & 0xffffu);
-        state8::moments(__fmul_rn(g[j], s), m2.x, v2.x, b1, b2, k, m[j], v[j]);
-        state8::moments(__fmul_rn(g[j + 1], s), m2.y, v2.y, b1, b2, k, m[j + 1], v[j + 1]);
-        m_most = state8::largest(m_most, fabsf(m[j]), fabsf(m[j + 1]));
-        v_most = state8::largest(v_most, v[j], v[j + 1]);
+        const float2 gh = state8::mul2(make_float2(g[j], g[j + 1]), state8::both(s));
+        float2 mn, vn;
+        state8::moments(gh, state8::widen_m((x.m[j >> 2] >> (8 * (j & 3))) & 0xffffu),
+                        state8::widen_v((x.v[j >> 2] >> (8 * (j & 3))) & 0xffffu), b1, b2, k, mn,
+                        vn);
+        m[j] = mn.x, m[j + 1] = mn.y, v[j] = vn.x, v[j + 1] = vn.y;
+        m_most = state8::largest(m_most, fabsf(mn.x), fabsf(mn.y));
+        v_most = state8::largest(v_most, vn.x, vn.y);
     }
     // non-negative floats order as their bits do
     const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m_most));
@@ -210,18 +226,22 @@ __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, flo
         const float* const mh = m + 4 * h;
         const float* const vh = v + 4 * h;
         float* const wh = w + 4 * h;
-        if (fast) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                wh[j] = state8::weight(wh[j], mh[j], __fmaf_rn(state8::root_fast(vh[j]), inv, k.eps),
-                                       k, d);
+        for (int j = 0; j < 4; j += 2) {
+            const float2 v2 = make_float2(vh[j], vh[j + 1]);
+            const float2 root = fast ? state8::root_fast(v2)
+                                     : make_float2(__fsqrt_rn(v2.x), __fsqrt_rn(v2.y));
+            const float2 wn = state8::weight(make_float2(wh[j], wh[j + 1]),
+                                             make_float2(mh[j], mh[j + 1]), root, inv, k, d);
+            wh[j] = wn.x, wh[j + 1] = wn.y;
+        }
+        if (fast) {
             x.m[h] = state8::narrow4_m(mh, state8::move_m(me), r);
             x.v[h] = state8::narrow4_v(vh, state8::move_v(ve), r);
         } else {
             x.m[h] = x.v[h] = 0u;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                wh[j] = state8::weight(wh[j], mh[j], __fmaf_rn(__fsqrt_rn(vh[j]), inv, k.eps), k, d);
                 x.m[h] |= state8::narrow_m(mh[j], state8::inverse_of(me), r[j]) << (8 * j);
                 x.v[h] |= state8::narrow_v(vh[j], state8::inverse_of(ve), r[j]) << (8 * j);
             }
@@ -292,48 +312,68 @@ __device__ __forceinline__ void store_block(const ListTensor& t, int32_t i, int3
 // asked for before that: the norm kernel writes none of them.
 //
 // A block takes one unit after another, a warp of it one block of elements.
-// While a unit is updated, the block's first warp fetches the next one's
-// tensor into shared memory and draws the one after that: neither table's
-// latency is waited for, and the pointers take no registers.  Long lists
+// Its first warp keeps the tables ahead of it through shared memory: in the
+// round of unit i it asks for the tensor of unit i + 2, the table entry of
+// unit i + 3 and the number of unit i + 4, each known from an earlier round,
+// so no round waits for a chain of loads, and the pointers take no
+// registers.  (One chain a round cost the 8-bit update 15%.)  Long lists
 // hand the units out by a counter, which keeps the blocks close to one
 // another in memory.
+constexpr int kRing = 4;
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* to, const void* from)
+{
+    const uint32_t d = uint32_t(__cvta_generic_to_shared(to));
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(from), "n"(kBytes)
+                     : "memory");
+}
+
 template <typename G, bool k8>
-__global__ void __launch_bounds__(kNormThreads, MINB)
+__global__ void __launch_bounds__(kStepThreads, MINB * 256 / kStepThreads)
     k_list_step(ListView list, StepScalars k, uint32_t key, bool publish, bool zero_grad,
                 int32_t w_lp_dtype)
 {
     const int lane = threadIdx.x & 31;
     const int32_t lane_e0 = int32_t(threadIdx.x >> 5) * kBlockElems + lane * kLane;
-    __shared__ ListTensor s_tensor[2];
-    __shared__ int32_t s_unit[2];  // its unit, or -1: no more
+    __shared__ ListTensor s_tensor[kRing];
+    __shared__ ListUnit s_unit[kRing];  // unit < 0: no more
     __shared__ float s_scale;
     __shared__ int s_skip;
     uint32_t* const ctr = k.chunk_ctr;
-    int32_t u = int32_t(blockIdx.x);  // the unit fetched next (the first warp's)
-    auto fetch = [&](int to) {
-        // lane 0 draws the number of the unit after this one meanwhile
-        int32_t after = u + int32_t(gridDim.x);
-        if (ctr && lane == 0)
-            after = int32_t(gridDim.x + atomicAdd(ctr, 1u));
-        ListUnit unit{0, -1};
-        if (u < list.n_units) {
-            unit = list.units[u];
-            constexpr int kWords = int(sizeof(ListTensor) / 16);
-            if (lane < kWords)
-                reinterpret_cast<uint4*>(&s_tensor[to])[lane] =
-                    reinterpret_cast<const uint4*>(list.tensors + unit.tensor)[lane];
-        }
-        if (lane == 0)
-            s_unit[to] = unit.unit;
-        u = ctr ? __shfl_sync(0xffffffffu, after, 0) : after;
+    const int32_t grid = int32_t(gridDim.x);
+    auto ask_unit = [&](int slot, int32_t u) {  // one lane
+        if (u < list.n_units)
+            copy_async<8>(&s_unit[slot], list.units + u);
+        else
+            s_unit[slot] = ListUnit{0, -1};
     };
-    if (threadIdx.x < 32)
-        fetch(0);
+    auto ask_tensor = [&](int slot) {  // a warp
+        constexpr int kWords = int(sizeof(ListTensor) / 16);
+        const ListUnit unit = s_unit[slot];
+        if (unit.unit >= 0 && lane < kWords)
+            copy_async<16>(reinterpret_cast<uint4*>(&s_tensor[slot]) + lane,
+                           reinterpret_cast<const uint4*>(list.tensors + unit.tensor) + lane);
+    };
+    // the first units are those of a plain stride; the counter goes on from there
+    int32_t u = int32_t(blockIdx.x) + (kRing - 1) * grid;  // number of unit i + 3
+    if (threadIdx.x < 32) {
+        if (lane < kRing - 1)
+            ask_unit(lane, int32_t(blockIdx.x) + lane * grid);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        ask_tensor(0);
+        ask_tensor(1);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
     float s = 0.0f;
     for (int i = 0;; ++i) {
         __syncthreads();
-        const ListTensor& t = s_tensor[i & 1];
-        const int32_t unit = s_unit[i & 1];
+        const ListTensor& t = s_tensor[i % kRing];
+        const int32_t unit = s_unit[i % kRing].unit;
         const int32_t e = unit * kUnitElems + lane_e0;  // the lane's first element
         const int32_t left = unit < 0 ? 0 : t.numel - e;
         const bool vec = left >= kLane && (t.flags & kListVec);
@@ -343,11 +383,20 @@ __global__ void __launch_bounds__(kNormThreads, MINB)
         Moments<k8> x;
         if (any)
             load_block<G, k8>(t, e, left, vec, w, g, x);
-        if (threadIdx.x < 32 && unit >= 0)
-            fetch((i + 1) & 1);
+        if (threadIdx.x < 32 && unit >= 0) {
+            ask_tensor((i + 2) % kRing);
+            if (lane == 0) {
+                ask_unit((i + 3) % kRing, u);
+                u = !ctr ? u + grid
+                    : u < list.n_units ? kRing * grid + int32_t(atomicAdd(ctr, 1u)) : u;
+            }
+        }
         if (i == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            const double total = normdev::sum_partials(k.fin.partials, k.fin.nparts);
+            double total = 0.0;
+            for (int q = threadIdx.x; q < k.fin.nparts; q += kStepThreads)
+                total += __ldcg(k.fin.partials + q);
+            total = detail::block_sum<kStepThreads>(total);
             if (threadIdx.x == 0) {
                 const bool mine = publish && blockIdx.x == 0;
                 const NormResult r = normdev::make_result(total, k.fin.clip, k.fin.grad_scale,
@@ -368,7 +417,10 @@ __global__ void __launch_bounds__(kNormThreads, MINB)
             update_block(t, e, w, g, x, s, k, (t.flags & kListDecay) ? k.decay : 1.0f, key);
             store_block<G, k8>(t, e, left, vec, w, x, zero_grad, w_lp_dtype);
         }
+        if (threadIdx.x < 32)
+            asm volatile("cp.async.wait_all;" ::: "memory");
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (ctr && threadIdx.x == 0) {
         // the last block out resets the counters for the next launch
         __threadfence();
@@ -386,11 +438,11 @@ int launch_step_typed(const ListView& list, int32_t w_lp_dtype, const StepScalar
     auto* const kernel = &k_list_step<G, k8>;
     cudaError_t err = cudaSuccess;
     static const int per_sm = detail::resident_blocks(reinterpret_cast<const void*>(kernel),
-                                                      kNormThreads, 1, &err);
+                                                      kStepThreads, 1, &err);
     const int32_t most = per_sm * sm_count;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(list.n_units < 1 ? 1 : list.n_units > most ? most : list.n_units));
-    cfg.blockDim = dim3(kNormThreads);
+    cfg.blockDim = dim3(kStepThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

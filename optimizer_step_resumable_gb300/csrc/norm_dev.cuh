@@ -36,7 +36,7 @@ __device__ __forceinline__ float sumsq4(float4 a)
 // underflow) are recomputed exactly in double; all-zero runs (common for
 // embedding rows no token touched) skip that and contribute 0.
 template <int U>
-__device__ __forceinline__ double run_sumsq(const float4 (&x)[U])
+__device__ __forceinline__ bool run_sumsq_fast(const float4 (&x)[U], float& r)
 {
     float q[U];
 #pragma unroll
@@ -47,8 +47,15 @@ __device__ __forceinline__ double run_sumsq(const float4 (&x)[U])
 #pragma unroll
         for (int j = 0; j + s < U; j += 2 * s)
             q[j] = __fadd_rn(q[j], q[j + s]);
-    const float r = q[0];
-    if (r >= 0x1p-100f && r <= FLT_MAX)
+    r = q[0];
+    return r >= 0x1p-100f && r <= FLT_MAX;
+}
+
+template <int U>
+__device__ __forceinline__ double run_sumsq(const float4 (&x)[U])
+{
+    float r;
+    if (run_sumsq_fast<U>(x, r))
         return double(r);
     unsigned bits = 0;
 #pragma unroll

@@ -92,13 +92,50 @@ __device__ __forceinline__ uint32_t gather_byte2(uint32_t a, uint32_t b, uint32_
 {
     return __byte_perm(__byte_perm(a, b, 0x0062), __byte_perm(c, d, 0x0062), 0x5410);
 }
+// Two float32 operations in one instruction (sm_100 and later), each rounded
+// on its own: the 8-bit update is bound by instructions as much as by memory.
+__device__ __forceinline__ uint64_t pair(float2 a)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+    return unpair(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 __device__ __forceinline__ uint32_t narrow4_m(const float* x, float move, const uint32_t* random)
 {
     uint32_t s[4], sign[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        s[j] = (__float_as_uint(__fmul_rn(fabsf(x[j]), move)) >> 4) + (random[j] >> 16);
-        sign[j] = __float_as_uint(x[j]);
+    for (int j = 0; j < 4; j += 2) {
+        const float2 y = mul2(make_float2(x[j], x[j + 1]), both(move));
+        sign[j] = __float_as_uint(y.x);
+        sign[j + 1] = __float_as_uint(y.y);
+        s[j] = ((sign[j] >> 4) & 0x07ffffffu) + (random[j] >> 16);
+        s[j + 1] = ((sign[j + 1] >> 4) & 0x07ffffffu) + (random[j + 1] >> 16);
     }
     // byte 3 of each: its highest bit is the sign
     const uint32_t signs = __byte_perm(__byte_perm(sign[0], sign[1], 0x0073),
@@ -109,8 +146,11 @@ __device__ __forceinline__ uint32_t narrow4_v(const float* x, float move, const 
 {
     uint32_t s[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        s[j] = (__float_as_uint(__fmul_rn(x[j], move)) >> 5) + (random[j] & 0xffffu);
+    for (int j = 0; j < 4; j += 2) {
+        const float2 y = mul2(make_float2(x[j], x[j + 1]), both(move));
+        s[j] = (__float_as_uint(y.x) >> 5) + (random[j] & 0xffffu);
+        s[j + 1] = (__float_as_uint(y.y) >> 5) + (random[j + 1] & 0xffffu);
+    }
     uint32_t c = gather_byte2(s[0], s[1], s[2], s[3]);
     if ((c - 0x01010101u) & ~c & 0x80808080u) {  // some code is 0
 #pragma unroll
@@ -121,34 +161,44 @@ __device__ __forceinline__ uint32_t narrow4_v(const float* x, float move, const 
     return c;
 }
 
-// One element's moments and weight (the formulas of adamw_elem, with every
-// product and sum of the moments rounded on its own).  b1 and b2: the betas
-// times the block's old scales; denom: sqrt(v_hat) + eps.
-__device__ __forceinline__ void moments(float gh, float m_old, float v_old, float b1, float b2,
-                                        const StepScalars& k, float& m, float& v)
+// Two elements' moments (the formulas of adamw_elem, with every product and
+// sum rounded on its own).  b1 and b2: the betas times the block's old scales.
+__device__ __forceinline__ void moments(float2 gh, float2 m_old, float2 v_old, float b1, float b2,
+                                        const StepScalars& k, float2& m, float2& v)
 {
-    m = __fadd_rn(__fmul_rn(b1, m_old), __fmul_rn(k.omb1, gh));
-    v = __fadd_rn(__fmul_rn(b2, v_old), __fmul_rn(__fmul_rn(k.omb2, gh), gh));
+    m = add2(mul2(both(b1), m_old), mul2(both(k.omb1), gh));
+    v = add2(mul2(both(b2), v_old), mul2(mul2(both(k.omb2), gh), gh));
 }
-__device__ __forceinline__ float weight(float w, float m, float denom, const StepScalars& k,
-                                        float d)
+
+// Two elements' weights.  root: sqrt(v) in units of 1 / inv; the quotient to
+// 2 units of 2^-23 (the denominator is 0 or a normal number): the update is a
+// small part of w.
+__device__ __forceinline__ float2 weight(float2 w, float2 m, float2 root, float inv,
+                                         const StepScalars& k, float d)
 {
-    // the quotient to 2 units of 2^-23 (denom is 0 or a normal number): the
-    // update is a small part of w
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(denom));
-    return __fmaf_rn(w, d, -__fmul_rn(k.step_size, __fmul_rn(m, r)));
+    const float2 denom = fma2(root, both(inv), both(k.eps));
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(denom.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(denom.y));
+    return fma2(w, both(d), mul2(both(-k.step_size), mul2(m, r)));
 }
 // sqrt(v) / kRootUnit for v below kVFast, to 2^-23: moved up by 2^32 first,
 // so that the square root, which takes subnormal numbers for 0, meets none.
 constexpr float kRootUnit = 0x1p-16f;
-__device__ __forceinline__ float root_fast(float v)
+__device__ __forceinline__ float2 root_fast(float2 v)
 {
-    float r;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmul_rn(v, 0x1p32f)));
+    const float2 u = mul2(v, both(0x1p32f));
+    float2 r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(u.x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(u.y));
     return r;
 }
-__device__ __forceinline__ float largest(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float largest(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 }  // namespace state8
 }  // namespace osr
