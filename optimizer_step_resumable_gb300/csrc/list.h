@@ -75,10 +75,14 @@ int launch_list_step(const ListView& plain, const ListView& eight, int32_t g_dty
 #define OSR_BOTH
 #endif
 OSR_BOTH inline uint32_t hash32_begin(uint32_t x) { return x ^ (x >> 16); }
-OSR_BOTH inline uint32_t hash32_end(uint32_t x)
+OSR_BOTH inline uint32_t hash32_middle(uint32_t x)
 {
     x *= 0x9E3779B1u;
-    x = (x ^ (x >> 15)) * 0x85EBCA77u;
+    return (x ^ (x >> 15)) * 0x85EBCA77u;
+}
+OSR_BOTH inline uint32_t hash32_end(uint32_t x)
+{
+    x = hash32_middle(x);
     return x ^ (x >> 16);
 }
 OSR_BOTH inline uint32_t hash32(uint32_t x) { return hash32_end(hash32_begin(x)); }

@@ -222,7 +222,7 @@ __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, flo
         uint32_t r[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            r[j] = hash32_end(first ^ uint32_t(4 * h + j));
+            r[j] = first ^ uint32_t(4 * h + j);
         const float* const mh = m + 4 * h;
         const float* const vh = v + 4 * h;
         float* const wh = w + 4 * h;
@@ -236,14 +236,14 @@ __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, flo
             wh[j] = wn.x, wh[j + 1] = wn.y;
         }
         if (fast) {
-            x.m[h] = state8::narrow4_m(mh, state8::move_m(me), r);
-            x.v[h] = state8::narrow4_v(vh, state8::move_v(ve), r);
+            state8::narrow4(mh, state8::move_m(me), vh, state8::move_v(ve), r, x.m[h], x.v[h]);
         } else {
             x.m[h] = x.v[h] = 0u;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                x.m[h] |= state8::narrow_m(mh[j], state8::inverse_of(me), r[j]) << (8 * j);
-                x.v[h] |= state8::narrow_v(vh[j], state8::inverse_of(ve), r[j]) << (8 * j);
+                const uint32_t hash = hash32_end(r[j]);
+                x.m[h] |= state8::narrow_m(mh[j], state8::inverse_of(me), hash) << (8 * j);
+                x.v[h] |= state8::narrow_v(vh[j], state8::inverse_of(ve), hash) << (8 * j);
             }
         }
     }
@@ -297,12 +297,6 @@ __device__ __forceinline__ void store_block(const ListTensor& t, int32_t i, int3
                 detail::store1_zero(gp + j);
         }
     }
-    if constexpr (k8) {
-        if (i % kBlockElems == 0 && left > 0) {  // one lane of the warp
-            t.m_scale[i / kBlockElems] = s.m_scale;
-            t.v_scale[i / kBlockElems] = s.v_scale;
-        }
-    }
 }
 
 // The update of the list's units of one kind of state.  Every block first
@@ -343,6 +337,7 @@ __global__ void __launch_bounds__(kStepThreads, MINB * 256 / kStepThreads)
     __shared__ ListUnit s_unit[kRing];  // unit < 0: no more
     __shared__ float s_scale;
     __shared__ int s_skip;
+    __shared__ float s_block_scales[2][2][kUnitBlocks];
     uint32_t* const ctr = k.chunk_ctr;
     const int32_t grid = int32_t(gridDim.x);
     auto ask_unit = [&](int slot, int32_t u) {  // one lane
@@ -370,8 +365,19 @@ __global__ void __launch_bounds__(kStepThreads, MINB * 256 / kStepThreads)
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
     float s = 0.0f;
+    int32_t done = -1;  // the unit before
     for (int i = 0;; ++i) {
         __syncthreads();
+        if (k8 && done >= 0 && threadIdx.x >= kStepThreads - 32 && lane < 2 * kUnitBlocks) {
+            // The block scales of the unit before, all of one moment in one
+            // store: one 4-byte store a warp, each a partial write of a
+            // sector that the neighbours write too, cost 50 of 280 us.
+            const ListTensor& p = s_tensor[(i + kRing - 1) % kRing];
+            const int32_t b = done * kUnitBlocks + lane % kUnitBlocks;
+            if (b <= (p.numel - 1) / kBlockElems)
+                (lane < kUnitBlocks ? p.m_scale : p.v_scale)[b] =
+                    s_block_scales[(i + 1) & 1][lane / kUnitBlocks][lane % kUnitBlocks];
+        }
         const ListTensor& t = s_tensor[i % kRing];
         const int32_t unit = s_unit[i % kRing].unit;
         const int32_t e = unit * kUnitElems + lane_e0;  // the lane's first element
@@ -416,7 +422,14 @@ __global__ void __launch_bounds__(kStepThreads, MINB * 256 / kStepThreads)
         if (any) {
             update_block(t, e, w, g, x, s, k, (t.flags & kListDecay) ? k.decay : 1.0f, key);
             store_block<G, k8>(t, e, left, vec, w, x, zero_grad, w_lp_dtype);
+            if constexpr (k8) {
+                if (lane == 0) {
+                    s_block_scales[i & 1][0][threadIdx.x >> 5] = x.m_scale;
+                    s_block_scales[i & 1][1][threadIdx.x >> 5] = x.v_scale;
+                }
+            }
         }
+        done = unit;
         if (threadIdx.x < 32)
             asm volatile("cp.async.wait_all;" ::: "memory");
     }

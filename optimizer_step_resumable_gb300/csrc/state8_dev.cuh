@@ -79,19 +79,6 @@ __device__ __forceinline__ uint32_t narrow_v(float x, float inverse, uint32_t ra
     return (c == 0u && x > 0.0f) ? 1u : c;
 }
 
-// The same bytes for four elements at once in half the instructions, for
-// blocks whose scale's reciprocal and the move down are one normal number:
-// largest |m| below 2^14 and largest v below 2^29 (any state but a diverging
-// one).  The word's low bits are dropped before the random number is added,
-// which then ends at bit 16, so that byte 2 of each sum is a code.
-constexpr uint32_t kMFast = (127u + 14u) << 23, kVFast = (127u + 29u) << 23;
-__device__ __forceinline__ float move_m(uint32_t e) { return __uint_as_float((134u - e) << 23); }
-__device__ __forceinline__ float move_v(uint32_t e) { return __uint_as_float((142u - e) << 23); }
-
-__device__ __forceinline__ uint32_t gather_byte2(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
-{
-    return __byte_perm(__byte_perm(a, b, 0x0062), __byte_perm(c, d, 0x0062), 0x5410);
-}
 // Two float32 operations in one instruction (sm_100 and later), each rounded
 // on its own: the 8-bit update is bound by instructions as much as by memory.
 __device__ __forceinline__ uint64_t pair(float2 a)
@@ -126,39 +113,46 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-__device__ __forceinline__ uint32_t narrow4_m(const float* x, float move, const uint32_t* random)
+// The same bytes for four elements at once in half the instructions, for
+// blocks whose scale's reciprocal and the move down are one normal number:
+// largest |m| below 2^14 and largest v below 2^29 (any state but a diverging
+// one).  The sum is formed 4 (e4m3) or 3 (e5m2) bits further up, in one
+// integer multiply-add whose random number lies in bits 8 to 23, so that
+// byte 3 of each sum is a code.
+constexpr uint32_t kMFast = (127u + 14u) << 23, kVFast = (127u + 29u) << 23;
+__device__ __forceinline__ float move_m(uint32_t e) { return __uint_as_float((134u - e) << 23); }
+__device__ __forceinline__ float move_v(uint32_t e) { return __uint_as_float((142u - e) << 23); }
+
+__device__ __forceinline__ uint32_t gather_byte3(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    uint32_t s[4], sign[4];
-#pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-        const float2 y = mul2(make_float2(x[j], x[j + 1]), both(move));
-        sign[j] = __float_as_uint(y.x);
-        sign[j + 1] = __float_as_uint(y.y);
-        s[j] = ((sign[j] >> 4) & 0x07ffffffu) + (random[j] >> 16);
-        s[j + 1] = ((sign[j + 1] >> 4) & 0x07ffffffu) + (random[j + 1] >> 16);
-    }
-    // byte 3 of each: its highest bit is the sign
-    const uint32_t signs = __byte_perm(__byte_perm(sign[0], sign[1], 0x0073),
-                                       __byte_perm(sign[2], sign[3], 0x0073), 0x5410);
-    return gather_byte2(s[0], s[1], s[2], s[3]) | (signs & 0x80808080u);
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
-__device__ __forceinline__ uint32_t narrow4_v(const float* x, float move, const uint32_t* random)
+// The codes of x[0..4) as m and y[0..4) as v, rounded by the hashes of four
+// words begun as `begun`[j].
+__device__ __forceinline__ void narrow4(const float* x, float move_x, const float* y, float move_y,
+                                        const uint32_t* begun, uint32_t& cx, uint32_t& cy)
 {
-    uint32_t s[4];
+    uint32_t s[4], z[4];
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-        const float2 y = mul2(make_float2(x[j], x[j + 1]), both(move));
-        s[j] = (__float_as_uint(y.x) >> 5) + (random[j] & 0xffffu);
-        s[j + 1] = (__float_as_uint(y.y) >> 5) + (random[j + 1] & 0xffffu);
+    for (int j = 0; j < 4; ++j) {
+        // hash32_end's last step, for each half in its place: the high half
+        // of h ^ h >> 16 is h's, the low one the exclusive or of both
+        const uint32_t h = hash32_middle(begun[j]);
+        const uint32_t high = __byte_perm(h, 0u, 0x4324);
+        const uint32_t low = __byte_perm(h, 0u, 0x4104) ^ high;
+        s[j] = __float_as_uint(__fmul_rn(fabsf(x[j]), move_x)) * 16u + high;
+        z[j] = __float_as_uint(__fmul_rn(y[j], move_y)) * 8u + low;
     }
-    uint32_t c = gather_byte2(s[0], s[1], s[2], s[3]);
-    if ((c - 0x01010101u) & ~c & 0x80808080u) {  // some code is 0
+    const uint32_t signs = gather_byte3(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                        __float_as_uint(x[2]), __float_as_uint(x[3]));
+    cx = gather_byte3(s[0], s[1], s[2], s[3]) | (signs & 0x80808080u);
+    cy = gather_byte3(z[0], z[1], z[2], z[3]);
+    if ((cy - 0x01010101u) & ~cy & 0x80808080u) {  // some code is 0
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (x[j] > 0.0f && !((c >> (8 * j)) & 0xffu))
-                c |= 1u << (8 * j);
+            if (y[j] > 0.0f && !((cy >> (8 * j)) & 0xffu))
+                cy |= 1u << (8 * j);
     }
-    return c;
 }
 
 // Two elements' moments (the formulas of adamw_elem, with every product and
