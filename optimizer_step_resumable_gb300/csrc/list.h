@@ -6,9 +6,6 @@
 
 #include "internal.h"
 
-#ifndef STEPT
-#define STEPT 256
-#endif
 namespace osr {
 
 // 8-bit states keep one scale per block of this many elements of a tensor.
@@ -16,7 +13,7 @@ constexpr int kBlockElems = ADAMW_STATE_BLOCK;
 
 // A block's unit of work: up to 8 consecutive blocks of elements of one
 // tensor, one for each of its warps.
-constexpr int kUnitBlocks = STEPT / 32;
+constexpr int kUnitBlocks = 8;
 constexpr int kUnitElems = kUnitBlocks * kBlockElems;
 
 constexpr uint32_t kListState8 = 1u;  // m, v in 8 bits with block scales

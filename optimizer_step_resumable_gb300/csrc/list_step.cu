@@ -22,12 +22,6 @@
 #include "norm_dev.cuh"
 #include "state8_dev.cuh"
 
-#ifndef MINB
-#define MINB 4
-#endif
-#ifndef NORMB
-#define NORMB 4
-#endif
 namespace osr {
 namespace {
 
@@ -49,7 +43,7 @@ constexpr int kLane = kBlockElems / 32;  // elements of a block per lane
 // two floats (48 bits; binary64 additions run at 1/64 of the rate and took a
 // third of the kernel's time).  Default L2 priority: the update reads g next.
 template <typename G>
-__global__ void __launch_bounds__(kNormThreads, NORMB)
+__global__ void __launch_bounds__(kNormThreads, 4)
     k_list_norm(ListView list, double* __restrict__ partials)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -327,7 +321,7 @@ __device__ __forceinline__ void copy_async(void* to, const void* from)
 }
 
 template <typename G, bool k8>
-__global__ void __launch_bounds__(kStepThreads, MINB * 256 / kStepThreads)
+__global__ void __launch_bounds__(kStepThreads, 4)
     k_list_step(ListView list, StepScalars k, uint32_t key, bool publish, bool zero_grad,
                 int32_t w_lp_dtype)
 {
