@@ -14,10 +14,10 @@ int launch_ln_backward_typed(const LnBackward& a, int sm_count, int32_t* parts, 
 
 namespace {
 
-constexpr int kCols = 32, kSlices = 8;  // of a block
+constexpr int kCols = 32, kSlices = 32;  // of a block
 
 // Adds the blocks' partial sums up, column by column: slice q of a block
-// takes partials q, q + 8, ..., then the slices are added in order; blockIdx.y
+// takes partials q, q + 32, ..., then the slices are added in order; blockIdx.y
 // 0: dweight, 1: dbias.
 __global__ void __launch_bounds__(kCols * kSlices) k_ln_grads(LnGrads g)
 {

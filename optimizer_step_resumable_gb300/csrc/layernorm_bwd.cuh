@@ -25,13 +25,29 @@ namespace {
 
 using namespace ln;
 
+// Resident blocks the kernel is compiled for: 16 kVecs registers hold a
+// thread's column sums, 8 kVecs its weights.
+template <int kGroup, int kVecs>
+constexpr int kBackwardBlocks = (kVecs == 1 ? 768 : kVecs == 2 ? 640 : 512) / kBlockThreads<kGroup>;
+
+template <typename T, int kGroup, int kVecs>
+using BackwardRing =
+    Ring<T, kBlockThreads<kGroup>, kVecs, 2,
+         stages_for(2 * kVecs * kBlockThreads<kGroup> * kE * int(sizeof(T)),
+                    kBackwardBlocks<kGroup, kVecs>)>;
+
+// A row is looked at twice in shared memory, for the sums and for dx, rather
+// than kept widened in 16 kVecs more registers.
 template <typename T, int kGroup, int kVecs, bool kRagged>
-__global__ void __launch_bounds__(kBlockThreads<kGroup>)
+__global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup, kVecs>))
     k_ln_backward(LnBackward a)
 {
     constexpr int kThreads = kBlockThreads<kGroup>;
     constexpr int kGroups = kThreads / kGroup;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ __align__(16) unsigned char raw[];
+    const BackwardRing<T, kGroup, kVecs> ring{reinterpret_cast<uint4*>(raw)};
+    constexpr int kStages = BackwardRing<T, kGroup, kVecs>::kDepth;
     __shared__ float2 slots[2][32];
     int turn = 0;
     const int lane = threadIdx.x % kGroup;
@@ -44,55 +60,108 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>)
     const int off = kRagged ? offset_of(x + group * a.x_stride) : 0;
     const bool dy_whole = !kRagged || offset_of(dy + group * a.dy_stride) == off;
     const bool dx_whole = !kRagged || offset_of(dx + group * a.dx_stride) == off;
+    auto column = [&](int v) { return (v * kGroup + lane) * kE - off; };
+    float next_mean[kStages], next_rstd[kStages];  // [i]: of the row i + 1 turns ahead
+    auto fetch = [&](int stage, int64_t r, float& mean, float& rstd) {
+        const bool live = r < a.rows;
+        if (live) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                const int c = column(v);
+                if (is_full<kRagged>(c, cols)) {
+                    ring.copy(stage, 0, v, x + r * a.x_stride + c);
+                    if (dy_whole)
+                        ring.copy(stage, 1, v, dy + r * a.dy_stride + c);
+                }
+            }
+        }
+        mean = live ? a.mean[r] : 0.0f;
+        rstd = live ? a.rstd[r] : 0.0f;
+        commit_copies();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+        fetch(i, group + i * groups, next_mean[i], next_rstd[i]);
 
     float w[kVecs][kE], dw[kVecs][kE], db[kVecs][kE];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-        load_weight<T>(a.weight, a.w_f32, (v * kGroup + lane) * kE - off, cols, 1.0f, w[v]);
+        load_weight<T>(a.weight, a.w_f32, column(v), cols, 1.0f, w[v]);
 #pragma unroll
         for (int i = 0; i < kE; ++i)
             dw[v][i] = db[v][i] = 0.0f;
     }
     const float inv = 1.0f / float(cols);
+    int stage = 0;
     for (int64_t first = group - threadIdx.x / kGroup; first < a.rows; first += groups) {
         const int64_t r = first + threadIdx.x / kGroup;
         const bool live = r < a.rows;
-        const float mean = live ? a.mean[r] : 0.0f, rstd = live ? a.rstd[r] : 0.0f;
-        const int end = live ? cols : INT32_MIN;
-        float xh[kVecs][kE], g[kVecs][kE];
+        fetch(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * groups,
+              next_mean[kStages - 1], next_rstd[kStages - 1]);
+        const float mean = next_mean[0], rstd = next_rstd[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kStages; ++i) {
+            next_mean[i] = next_mean[i + 1];
+            next_rstd[i] = next_rstd[i + 1];
+        }
+        wait_copies<kStages - 1>();
+        // one vector of the row, as xhat and dy; outside the row dy is 0, and
+        // so are all sums
+        auto take = [&](int v, float(&xh)[kE], float(&g)[kE]) {
+            const int c = column(v);
+            const bool full = live && is_full<kRagged>(c, cols);
+            if (full) {
+                ring.read(stage, 0, v, xh);
+            } else if (kRagged && live) {
+                load_elements(x + r * a.x_stride, c, cols, xh);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kE; ++i)
+                    xh[i] = 0.0f;
+            }
+            if (full && dy_whole) {
+                ring.read(stage, 1, v, g);
+            } else if (kRagged && live) {
+                load_elements(dy + r * a.dy_stride, c, cols, g);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kE; ++i)
+                    g[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < kE; ++i)
+                xh[i] = (xh[i] - mean) * rstd;
+        };
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
-            const int c = (v * kGroup + lane) * kE - off;
-            load8<kRagged>(x + r * a.x_stride, c, end, true, xh[v]);
-            load8<kRagged>(dy + r * a.dy_stride, c, end, dy_whole, g[v]);
-        }
+            float xh[kE], g[kE];
+            take(v, xh, g);
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-            for (int i = 0; i < kE; ++i) {  // outside the row dy is 0, and so are all sums
-                xh[v][i] = (xh[v][i] - mean) * rstd;
-                dw[v][i] += g[v][i] * xh[v][i];
-                db[v][i] += g[v][i];
-                g[v][i] *= w[v][i];
-                s1 += g[v][i];
-                s2 += g[v][i] * xh[v][i];
+            for (int i = 0; i < kE; ++i) {
+                dw[v][i] += g[i] * xh[i];
+                db[v][i] += g[i];
+                g[i] *= w[v][i];
+                s1 += g[i];
+                s2 += g[i] * xh[i];
             }
-        const float2 s = group_sum<kGroup>(s1, s2, slots, turn);
-        if (!live)
-            continue;
-        const float m1 = s.x * inv, m2 = s.y * inv;
-        T* const dxr = dx + r * a.dx_stride;
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-            const int c = (v * kGroup + lane) * kE - off;
-            float o[kE];
-#pragma unroll
-            for (int i = 0; i < kE; ++i)
-                o[i] = rstd * (g[v][i] - m1 - xh[v][i] * m2);
-            store8<kRagged>(dxr, c, cols, dx_whole, o);
         }
+        const float2 s = group_sum<kGroup>(s1, s2, slots, turn);
+        const float m1 = s.x * inv, m2 = s.y * inv;
+        if (live) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                float xh[kE], g[kE];
+                take(v, xh, g);
+#pragma unroll
+                for (int i = 0; i < kE; ++i)
+                    g[i] = rstd * (g[i] * w[v][i] - m1 - xh[i] * m2);
+                store_vec<kRagged>(dx + r * a.dx_stride, column(v), cols, dx_whole, g);
+            }
+        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    wait_copies<0>();
     if (!a.sums)
         return;
 
@@ -102,16 +171,19 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>)
         for (int v = 0; v < kVecs; ++v)
 #pragma unroll
             for (int i = 0; i < kE; ++i) {
-                const int c = (v * kGroup + lane) * kE - off + i;
+                const int c = column(v) + i;
                 if (c >= 0 && c < cols) {
                     mine[c] = dw[v][i];
                     mine[cols + c] = db[v][i];
                 }
             }
     } else {
-        // the block's groups join by columns: their offsets may differ
+        // the block's groups join by columns (their offsets may differ), in
+        // the memory of the ring
         constexpr int kSpan = kGroup * kVecs * kE;
-        __shared__ float part[kGroups][kSpan];
+        float* const part = reinterpret_cast<float*>(raw);
+        static_assert(kGroups * kSpan * 4 <= BackwardRing<T, kGroup, kVecs>::kBytes,
+                      "the sums fit the ring");
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
             __syncthreads();
@@ -119,16 +191,16 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>)
             for (int v = 0; v < kVecs; ++v)
 #pragma unroll
                 for (int i = 0; i < kE; ++i) {
-                    const int c = (v * kGroup + lane) * kE - off + i;
+                    const int c = column(v) + i;
                     if (c >= 0 && c < cols)
-                        part[threadIdx.x / kGroup][c] = pass ? db[v][i] : dw[v][i];
+                        part[threadIdx.x / kGroup * kSpan + c] = pass ? db[v][i] : dw[v][i];
                 }
             __syncthreads();
             for (int c = threadIdx.x; c < cols; c += kThreads) {
                 float s = 0.0f;
 #pragma unroll
                 for (int q = 0; q < kGroups; ++q)
-                    s += part[q][c];
+                    s += part[q * kSpan + c];
                 mine[pass * cols + c] = s;
             }
         }
@@ -200,9 +272,9 @@ template <typename T, int G, int V, bool kRagged>
 int launch_one(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s)
 {
     constexpr int kThreads = kBlockThreads<G>;
-    cudaError_t err = cudaSuccess;
-    static const int cap = detail::resident_blocks(
-        reinterpret_cast<const void*>(&k_ln_backward<T, G, V, kRagged>), kThreads, 1, &err);
+    constexpr int kSmem = BackwardRing<T, G, V>::kBytes;
+    auto* const kernel = &k_ln_backward<T, G, V, kRagged>;
+    static const int cap = resident_blocks(kernel, kThreads, kSmem);
     int64_t blocks = detail::ceil_div(a.rows, kThreads / G);
     if (kThreads / G < kE)
         blocks = detail::ceil_div(blocks, kE) * kE;  // groups step by a multiple of 8
@@ -212,7 +284,7 @@ int launch_one(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s
     most = most / kE * kE;
     blocks = blocks > most ? most : blocks;
     *parts = int32_t(blocks);
-    k_ln_backward<T, G, V, kRagged><<<unsigned(blocks), kThreads, 0, s>>>(a);
+    kernel<<<unsigned(blocks), kThreads, kSmem, s>>>(a);
     return int(cudaGetLastError());
 }
 

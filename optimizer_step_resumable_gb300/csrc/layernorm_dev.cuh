@@ -25,82 +25,13 @@ namespace ln {
 
 constexpr int kE = 8;  // elements of a vector
 
-// 8 adjacent elements as they lie in memory.
-template <typename T>
-struct Raw {  // 16-bit types
-    uint4 q;
-};
-template <>
-struct Raw<float> {
-    float4 a, b;
-};
-
-template <typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T* p)
-{
-    return Raw<T>{__ldcs(reinterpret_cast<const uint4*>(p))};
-}
-template <>
-__device__ __forceinline__ Raw<float> load_raw<float>(const float* p)
-{
-    const float4* q = reinterpret_cast<const float4*>(p);
-    return Raw<float>{__ldcs(q), __ldcs(q + 1)};
-}
-
-__device__ __forceinline__ void pair(uint32_t u, float& lo, float& hi, const __nv_bfloat16*)
-{
-    lo = __uint_as_float(u << 16);
-    hi = __uint_as_float(u & 0xffff0000u);
-}
-__device__ __forceinline__ void pair(uint32_t u, float& lo, float& hi, const __half*)
-{
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-    lo = f.x;
-    hi = f.y;
-}
-template <typename T>
-__device__ __forceinline__ void widen(const Raw<T>& r, float (&f)[kE])
-{
-    pair(r.q.x, f[0], f[1], static_cast<const T*>(nullptr));
-    pair(r.q.y, f[2], f[3], static_cast<const T*>(nullptr));
-    pair(r.q.z, f[4], f[5], static_cast<const T*>(nullptr));
-    pair(r.q.w, f[6], f[7], static_cast<const T*>(nullptr));
-}
-template <>
-__device__ __forceinline__ void widen<float>(const Raw<float>& r, float (&f)[kE])
-{
-    f[0] = r.a.x, f[1] = r.a.y, f[2] = r.a.z, f[3] = r.a.w;
-    f[4] = r.b.x, f[5] = r.b.y, f[6] = r.b.z, f[7] = r.b.w;
-}
-
-__device__ __forceinline__ uint32_t pack(float lo, float hi, const __nv_bfloat16*)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack(float lo, float hi, const __half*)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <typename T>
-__device__ __forceinline__ void store_vec(T* p, const float (&f)[kE])
-{
-    const T* t = nullptr;
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack(f[0], f[1], t), pack(f[2], f[3], t),
-                                                   pack(f[4], f[5], t), pack(f[6], f[7], t)));
-}
-template <>
-__device__ __forceinline__ void store_vec<float>(float* p, const float (&f)[kE])
-{
-    float4* q = reinterpret_cast<float4*>(p);
-    __stcs(q, make_float4(f[0], f[1], f[2], f[3]));
-    __stcs(q + 1, make_float4(f[4], f[5], f[6], f[7]));
-}
-
 __device__ __forceinline__ void store_one(float* p, float f) { *p = f; }
 __device__ __forceinline__ void store_one(__nv_bfloat16* p, float f) { *p = __float2bfloat16_rn(f); }
 __device__ __forceinline__ void store_one(__half* p, float f) { *p = __float2half_rn(f); }
+
+using detail::Raw8;
+using detail::store8_cs;
+using detail::widen8;
 
 // How many elements p lies past a vector's boundary.
 template <typename T>
@@ -109,39 +40,82 @@ __device__ __forceinline__ int offset_of(const T* p)
     return int((reinterpret_cast<uintptr_t>(p) / sizeof(T)) & (kE - 1));
 }
 
-// A thread's vector starting at column c of a row, c0 = -off .. cols - 1.
-// kRagged: the vector may hang over either end of the row, and `whole` says
-// whether this array's rows are cut at the same places; elements outside the
-// row read as 0 and are not written.
-template <bool kRagged, typename T>
-__device__ __forceinline__ void load8(const T* row, int c, int cols, bool whole, float (&f)[kE])
+// A thread's vector starts at column c of a row, c = -off .. cols - 1 or past
+// the end.  kRagged: it may hang over either end of the row.  Elements outside
+// the row count as 0 and are not written.
+template <bool kRagged>
+__device__ __forceinline__ bool is_full(int c, int cols)
 {
-    if (!kRagged || (whole && c >= 0 && c + kE <= cols)) {
-        if (!kRagged && c >= cols) {
-#pragma unroll
-            for (int i = 0; i < kE; ++i)
-                f[i] = 0.0f;
-            return;
-        }
-        widen<T>(load_raw<T>(row + c), f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kE; ++i)
-            f[i] = c + i >= 0 && c + i < cols ? detail::load1(row + c + i) : 0.0f;
-    }
+    return kRagged ? c >= 0 && c + kE <= cols : c < cols;
 }
-template <bool kRagged, typename T>
-__device__ __forceinline__ void store8(T* row, int c, int cols, bool whole, const float (&f)[kE])
+template <typename T>
+__device__ __forceinline__ void load_elements(const T* row, int c, int cols, float (&f)[kE])
 {
-    if (!kRagged || (whole && c >= 0 && c + kE <= cols)) {
-        if (kRagged || c < cols)
-            store_vec<T>(row + c, f);
-    } else {
+#pragma unroll
+    for (int i = 0; i < kE; ++i)
+        f[i] = c + i >= 0 && c + i < cols ? detail::load1(row + c + i) : 0.0f;
+}
+// whole: this array's rows are cut where the vectors are.
+template <bool kRagged, typename T>
+__device__ __forceinline__ void store_vec(T* row, int c, int cols, bool whole, const float (&f)[kE])
+{
+    if (is_full<kRagged>(c, cols) && (!kRagged || whole)) {
+        store8_cs(row + c, f);
+    } else if (kRagged) {
 #pragma unroll
         for (int i = 0; i < kE; ++i)
             if (c + i >= 0 && c + i < cols)
                 store_one(row + c + i, f[i]);
     }
+}
+
+// A thread's vectors of kStages rows of kArrays arrays, on their way through
+// shared memory (cp.async): every thread copies what it will read itself, so
+// it waits for its own copies only and no barrier is needed.
+template <typename T, int kThreads, int kVecs, int kArrays, int kStages>
+struct Ring {
+    static constexpr int kDepth = kStages;
+    static constexpr int kHalves = int(sizeof(T)) / 2;  // 16-byte pieces of a vector
+    static constexpr int kBytes = kStages * kArrays * kVecs * kHalves * kThreads * 16;
+    uint4* base;
+
+    __device__ __forceinline__ uint4* at(int stage, int array, int vec, int half) const
+    {
+        return base + (((stage * kArrays + array) * kVecs + vec) * kHalves + half) * kThreads +
+               threadIdx.x;
+    }
+    __device__ __forceinline__ void copy(int stage, int array, int vec, const T* from) const
+    {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             uint32_t(__cvta_generic_to_shared(at(stage, array, vec, h)))),
+                         "l"(reinterpret_cast<const char*>(from) + 16 * h)
+                         : "memory");
+    }
+    __device__ __forceinline__ void read(int stage, int array, int vec, float (&f)[kE]) const
+    {
+        if constexpr (kHalves == 1) {
+            widen8(Raw8<T>{*at(stage, array, vec, 0)}, f);
+        } else {
+            const float4 a = *reinterpret_cast<const float4*>(at(stage, array, vec, 0));
+            const float4 b = *reinterpret_cast<const float4*>(at(stage, array, vec, 1));
+            widen8(Raw8<float>{a, b}, f);
+        }
+    }
+};
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void wait_copies()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// Stages that fit `blocks` resident blocks, at most 3.
+constexpr int stages_for(int stage_bytes, int blocks)
+{
+    const int n = 208 * 1024 / blocks / stage_bytes;
+    return n < 1 ? 1 : n > 3 ? 3 : n;
 }
 
 // Whether element i of a thread's vector at column c lies in the row.
@@ -218,6 +192,19 @@ int with_layout(int span, F f)
     if (span <= 4096) return f(Layout<128, 4>());
     if (span <= 8192) return f(Layout<256, 4>());
     return f(Layout<512, 4>());
+}
+
+// Resident blocks of a kernel per SM, which is allowed its shared memory
+// first.
+template <typename F>
+inline int resident_blocks(F* kernel, int threads, int smem)
+{
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess)
+        return 1;
+    return n < 1 ? 1 : n;
 }
 
 // Whether every row of an array starts at a vector's boundary.

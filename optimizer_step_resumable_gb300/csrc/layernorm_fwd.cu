@@ -17,50 +17,88 @@ namespace {
 
 using namespace ln;
 
+// Resident blocks the kernel is compiled for: 24 kVecs registers hold a
+// thread's weights, biases and elements.
+template <int kGroup, int kVecs>
+constexpr int kForwardBlocks = (kVecs == 1 ? 1024 : 512) / kBlockThreads<kGroup>;
+
+template <typename T, int kGroup, int kVecs>
+using ForwardRing =
+    Ring<T, kBlockThreads<kGroup>, kVecs, 1,
+         stages_for(kVecs * kBlockThreads<kGroup> * kE * int(sizeof(T)),
+                    kForwardBlocks<kGroup, kVecs>)>;
+
 template <typename T, int kGroup, int kVecs, bool kRagged>
-__global__ void __launch_bounds__(kBlockThreads<kGroup>)
+__global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup, kVecs>))
     k_ln_forward(LnForward a)
 {
     constexpr int kThreads = kBlockThreads<kGroup>;
+    constexpr int kGroups = kThreads / kGroup;
+    extern __shared__ __align__(16) unsigned char raw[];
+    const ForwardRing<T, kGroup, kVecs> ring{reinterpret_cast<uint4*>(raw)};
+    constexpr int kStages = ForwardRing<T, kGroup, kVecs>::kDepth;
     __shared__ float2 slots[2][32];
     int turn = 0;
     const int lane = threadIdx.x % kGroup;
-    const int64_t group = int64_t(blockIdx.x) * (kThreads / kGroup) + threadIdx.x / kGroup;
-    const int64_t groups = int64_t(gridDim.x) * (kThreads / kGroup);
+    const int64_t group = int64_t(blockIdx.x) * kGroups + threadIdx.x / kGroup;
+    const int64_t groups = int64_t(gridDim.x) * kGroups;
     const T* const x = static_cast<const T*>(a.x);
     T* const y = static_cast<T*>(a.y);
     const int cols = a.cols;
     const int off = kRagged ? offset_of(x + group * a.x_stride) : 0;
     const bool y_whole = !kRagged || offset_of(y + group * a.y_stride) == off;
+    auto column = [&](int v) { return (v * kGroup + lane) * kE - off; };
+    auto fetch = [&](int stage, int64_t r) {
+        if (r < a.rows) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+                if (is_full<kRagged>(column(v), cols))
+                    ring.copy(stage, 0, v, x + r * a.x_stride + column(v));
+        }
+        commit_copies();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+        fetch(i, group + i * groups);
 
     float w[kVecs][kE], b[kVecs][kE];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-        const int c = (v * kGroup + lane) * kE - off;
-        load_weight<T>(a.weight, a.w_f32, c, cols, 1.0f, w[v]);
-        load_weight<T>(a.bias, a.w_f32, c, cols, 0.0f, b[v]);
+        load_weight<T>(a.weight, a.w_f32, column(v), cols, 1.0f, w[v]);
+        load_weight<T>(a.bias, a.w_f32, column(v), cols, 0.0f, b[v]);
     }
     // every thread takes part in every sum: the rows past the end are empty
     const float inv = 1.0f / float(cols);
+    int stage = 0;
     for (int64_t first = group - threadIdx.x / kGroup; first < a.rows; first += groups) {
         const int64_t r = first + threadIdx.x / kGroup;
         const bool live = r < a.rows;
-        const T* const xr = x + r * a.x_stride;
+        fetch(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * groups);
+        wait_copies<kStages - 1>();
         float f[kVecs][kE];
         float sum = 0.0f;
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
-            const int c = (v * kGroup + lane) * kE - off;
-            load8<kRagged>(xr, c, live ? cols : INT32_MIN, true, f[v]);
+            const int c = column(v);
+            if (live && is_full<kRagged>(c, cols)) {
+                ring.read(stage, 0, v, f[v]);
+            } else if (kRagged && live) {
+                load_elements(x + r * a.x_stride, c, cols, f[v]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kE; ++i)
+                    f[v][i] = 0.0f;
+            }
 #pragma unroll
             for (int i = 0; i < kE; ++i)
                 sum += f[v][i];
         }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         const float mean = group_sum<kGroup>(sum, 0.0f, slots, turn).x * inv;
         float squares = 0.0f;
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
-            const int c = (v * kGroup + lane) * kE - off;
+            const int c = column(v);
 #pragma unroll
             for (int i = 0; i < kE; ++i) {
                 f[v][i] -= mean;
@@ -75,12 +113,11 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>)
         T* const yr = y + r * a.y_stride;
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
-            const int c = (v * kGroup + lane) * kE - off;
             float o[kE];
 #pragma unroll
             for (int i = 0; i < kE; ++i)
                 o[i] = f[v][i] * rstd * w[v][i] + b[v][i];
-            store8<kRagged>(yr, c, cols, y_whole, o);
+            store_vec<kRagged>(yr, column(v), cols, y_whole, o);
         }
         if (lane == 0) {
             if (a.mean)
@@ -137,15 +174,15 @@ template <typename T, int G, int V, bool kRagged>
 int launch_one(const LnForward& a, int sm_count, cudaStream_t s)
 {
     constexpr int kThreads = kBlockThreads<G>;
-    cudaError_t err = cudaSuccess;
-    static const int cap = detail::resident_blocks(
-        reinterpret_cast<const void*>(&k_ln_forward<T, G, V, kRagged>), kThreads, 1, &err);
+    constexpr int kSmem = ForwardRing<T, G, V>::kBytes;
+    auto* const kernel = &k_ln_forward<T, G, V, kRagged>;
+    static const int cap = resident_blocks(kernel, kThreads, kSmem);
     int64_t blocks = detail::ceil_div(a.rows, kThreads / G);
     if (kThreads / G < kE)
         blocks = detail::ceil_div(blocks, kE) * kE;  // groups step by a multiple of 8
     const int64_t most = int64_t(cap) * sm_count / kE * kE;
     blocks = blocks > most ? most : blocks;
-    k_ln_forward<T, G, V, kRagged><<<unsigned(blocks), kThreads, 0, s>>>(a);
+    kernel<<<unsigned(blocks), kThreads, kSmem, s>>>(a);
     return int(cudaGetLastError());
 }
 
