@@ -42,7 +42,8 @@ def _sources():
             + [os.path.join(CSRC, h) for h in ("internal.h", "ckpt_io.h", "common.cuh", "context.h",
                                                  "norm_dev.cuh", "adamw_dev.cuh", "api_util.h",
                                                  "list.h", "state8_dev.cuh", "layernorm.h",
-                                                 "layernorm_dev.cuh", "layernorm_bwd.cuh")]
+                                                 "layernorm_dev.cuh", "layernorm_bwd.cuh",
+                                                 "packed_dev.cuh")]
             + [os.path.join(INCLUDE, "adamw_ckpt.h")])
 
 

@@ -25,183 +25,203 @@ namespace {
 
 using namespace ln;
 
-// Resident blocks the kernel is compiled for: 16 kVecs registers hold a
-// thread's column sums, 8 kVecs its weights.
-template <int kGroup, int kVecs>
-constexpr int kBackwardBlocks = (kVecs == 1 ? 768 : kVecs == 2 ? 640 : 512) / kBlockThreads<kGroup>;
+// Threads an SM keeps resident, and so the registers of each: 16 a unit hold
+// a thread's column sums, 8 its weights.
+template <int kGroup, int kUnits>
+constexpr int kBackwardBlocks = (kUnits == 1   ? 768
+                                 : kUnits == 2 ? 640
+                                 : kUnits == 3 ? 512
+                                               : (kGroup > 256 ? kGroup : 256)) /
+                                kBlockThreads<kGroup>;
 
-template <typename T, int kGroup, int kVecs>
+template <typename T, int kGroup, int kUnits>
 using BackwardRing =
-    Ring<T, kBlockThreads<kGroup>, kVecs, 2,
-         stages_for(2 * kVecs * kBlockThreads<kGroup> * kE * int(sizeof(T)),
-                    kBackwardBlocks<kGroup, kVecs>)>;
+    Ring<T, kBlockThreads<kGroup>, kUnits * 8 / kE<T>, 2,
+         stages_for(2 * kUnits * 8 * int(sizeof(T)) * kBlockThreads<kGroup>,
+                    kBackwardBlocks<kGroup, kUnits>, 120 * 1024, 4)>;
+
+// A thread's column sums to their places in a row of cols floats.
+template <typename C, int kVecs, int kPairs>
+__device__ __forceinline__ void spread(const C& at, const float2 (&sum)[kVecs][kPairs], float edge,
+                                       float* row)
+{
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+        if (at.has(v)) {
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) {
+                row[at.column(v) + 2 * p] = sum[v][p].x;
+                row[at.column(v) + 2 * p + 1] = sum[v][p].y;
+            }
+        }
+    if (at.has_edge())
+        row[at.edge] = edge;
+}
 
 // A row is looked at twice in shared memory, for the sums and for dx, rather
-// than kept widened in 16 kVecs more registers.
-template <typename T, int kGroup, int kVecs, bool kRagged>
-__global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup, kVecs>))
+// than kept widened in 16 registers more a unit.
+template <typename T, int kGroup, int kUnits, bool kRagged>
+__global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup, kUnits>))
     k_ln_backward(LnBackward a)
 {
     constexpr int kThreads = kBlockThreads<kGroup>;
     constexpr int kGroups = kThreads / kGroup;
+    constexpr int kVecs = kUnits * 8 / kE<T>;
+    constexpr int kPairs = kP<T>;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(16) unsigned char raw[];
-    const BackwardRing<T, kGroup, kVecs> ring{reinterpret_cast<uint4*>(raw)};
-    constexpr int kStages = BackwardRing<T, kGroup, kVecs>::kDepth;
-    __shared__ float2 slots[2][32];
+    const BackwardRing<T, kGroup, kUnits> ring{reinterpret_cast<uint4*>(raw)};
+    constexpr int kStages = BackwardRing<T, kGroup, kUnits>::kDepth;
+    __shared__ float slots[2][2][16];
     int turn = 0;
-    const int lane = threadIdx.x % kGroup;
-    const int64_t group = int64_t(blockIdx.x) * kGroups + threadIdx.x / kGroup;
+    const int64_t first = int64_t(blockIdx.x) * kGroups;
     const int64_t groups = int64_t(gridDim.x) * kGroups;
-    const T* const x = static_cast<const T*>(a.x);
-    const T* const dy = static_cast<const T*>(a.dy);
-    T* const dx = static_cast<T*>(a.dx);
-    const int cols = a.cols;
-    const int off = kRagged ? offset_of(x + group * a.x_stride) : 0;
-    const bool dy_whole = !kRagged || offset_of(dy + group * a.dy_stride) == off;
-    const bool dx_whole = !kRagged || offset_of(dx + group * a.dx_stride) == off;
-    auto column = [&](int v) { return (v * kGroup + lane) * kE - off; };
-    float next_mean[kStages], next_rstd[kStages];  // [i]: of the row i + 1 turns ahead
-    auto fetch = [&](int stage, int64_t r, float& mean, float& rstd) {
-        const bool live = r < a.rows;
-        if (live) {
+    int64_t r = first + threadIdx.x / kGroup;
+    const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
+    const T* dy = static_cast<const T*>(a.dy) + r * a.dy_stride;
+    T* dx = static_cast<T*>(a.dx) + r * a.dx_stride;
+    const Columns<T, kGroup, kVecs, kRagged> at(a.cols, threadIdx.x % kGroup, x);
+    const bool dy_cut = at.cut_alike(dy), dx_cut = at.cut_alike(dx);
+    struct Scalars {
+        float mean, rstd, x, dy;  // of a row; of this thread's edge element
+    };
+    Scalars next[kStages];  // [i]: of the row i + 1 turns ahead
+    auto fetch = [&](int stage, int ahead, Scalars& s) {
+        const T* const xr = x + ahead * groups * a.x_stride;
+        const T* const gr = dy + ahead * groups * a.dy_stride;
+        const int64_t row = r + ahead * groups;
+        s = Scalars{0.0f, 0.0f, 0.0f, 0.0f};
+        if (row < a.rows) {
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v) {
-                const int c = column(v);
-                if (is_full<kRagged>(c, cols)) {
-                    ring.copy(stage, 0, v, x + r * a.x_stride + c);
-                    if (dy_whole)
-                        ring.copy(stage, 1, v, dy + r * a.dy_stride + c);
+            for (int v = 0; v < kVecs; ++v)
+                if (at.has(v)) {
+                    ring.copy(stage, 0, v, xr + at.column(v));
+                    if (dy_cut)
+                        ring.copy(stage, 1, v, gr + at.column(v));
                 }
+            s.mean = a.mean[row];
+            s.rstd = a.rstd[row];
+            if (at.has_edge()) {
+                s.x = detail::load1(xr + at.edge);
+                s.dy = detail::load1(gr + at.edge);
             }
         }
-        mean = live ? a.mean[r] : 0.0f;
-        rstd = live ? a.rstd[r] : 0.0f;
         commit_copies();
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i)
-        fetch(i, group + i * groups, next_mean[i], next_rstd[i]);
+        fetch(i, i, next[i]);
 
-    float w[kVecs][kE], dw[kVecs][kE], db[kVecs][kE];
+    float2 w[kVecs][kPairs], dw[kVecs][kPairs], db[kVecs][kPairs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-        load_weight<T>(a.weight, a.w_f32, column(v), cols, 1.0f, w[v]);
-#pragma unroll
-        for (int i = 0; i < kE; ++i)
-            dw[v][i] = db[v][i] = 0.0f;
+        load_weights<T>(a.weight, a.w_f32, at.column(v), at.has(v), 1.0f, w[v]);
+        clear(dw[v]);
+        clear(db[v]);
     }
-    const float inv = 1.0f / float(cols);
+    float we = 0.0f, dwe = 0.0f, dbe = 0.0f;
+    if (at.has_edge())
+        we = weight_at<T>(a.weight, a.w_f32, at.edge, 1.0f);
+    const float inv = 1.0f / float(a.cols);
     int stage = 0;
-    for (int64_t first = group - threadIdx.x / kGroup; first < a.rows; first += groups) {
-        const int64_t r = first + threadIdx.x / kGroup;
+    for (int64_t block_r = first; block_r < a.rows; block_r += groups) {
         const bool live = r < a.rows;
-        fetch(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * groups,
-              next_mean[kStages - 1], next_rstd[kStages - 1]);
-        const float mean = next_mean[0], rstd = next_rstd[0];
+        fetch(stage == 0 ? kStages - 1 : stage - 1, kStages - 1, next[kStages - 1]);
+        const Scalars now = next[0];
 #pragma unroll
-        for (int i = 0; i + 1 < kStages; ++i) {
-            next_mean[i] = next_mean[i + 1];
-            next_rstd[i] = next_rstd[i + 1];
-        }
+        for (int i = 0; i + 1 < kStages; ++i)
+            next[i] = next[i + 1];
         wait_copies<kStages - 1>();
-        // one vector of the row, as xhat and dy; outside the row dy is 0, and
-        // so are all sums
-        auto take = [&](int v, float(&xh)[kE], float(&g)[kE]) {
-            const int c = column(v);
-            const bool full = live && is_full<kRagged>(c, cols);
-            if (full) {
-                ring.read(stage, 0, v, xh);
-            } else if (kRagged && live) {
-                load_elements(x + r * a.x_stride, c, cols, xh);
+        // one vector of the row, as x - mean and dy; outside the row dy is 0,
+        // and so are all sums
+        auto take = [&](int v, float2(&d)[kPairs], float2(&g)[kPairs]) {
+            if (live && at.has(v)) {
+                ring.read(stage, 0, v, d);
+                if (!kRagged || dy_cut)
+                    ring.read(stage, 1, v, g);
+                else
+                    load_vec<kRagged>(dy + at.column(v), false, g);
             } else {
-#pragma unroll
-                for (int i = 0; i < kE; ++i)
-                    xh[i] = 0.0f;
-            }
-            if (full && dy_whole) {
-                ring.read(stage, 1, v, g);
-            } else if (kRagged && live) {
-                load_elements(dy + r * a.dy_stride, c, cols, g);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kE; ++i)
-                    g[i] = 0.0f;
+                clear(d);
+                clear(g);
             }
 #pragma unroll
-            for (int i = 0; i < kE; ++i)
-                xh[i] = (xh[i] - mean) * rstd;
+            for (int p = 0; p < kPairs; ++p)
+                d[p] = add2(d[p], both(-now.mean));
         };
-        float s1 = 0.0f, s2 = 0.0f;
+        const float de = now.x - now.mean, ge = now.dy * we;
+        dwe += now.dy * (de * now.rstd);
+        dbe += now.dy;
+        float2 s1 = make_float2(ge, 0.0f), s2 = make_float2(ge * (de * now.rstd), 0.0f);
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
-            float xh[kE], g[kE];
-            take(v, xh, g);
+            float2 d[kPairs], g[kPairs];
+            take(v, d, g);
 #pragma unroll
-            for (int i = 0; i < kE; ++i) {
-                dw[v][i] += g[i] * xh[i];
-                db[v][i] += g[i];
-                g[i] *= w[v][i];
-                s1 += g[i];
-                s2 += g[i] * xh[i];
+            for (int p = 0; p < kPairs; ++p) {
+                const float2 xh = mul2(d[p], both(now.rstd));
+                dw[v][p] = fma2(g[p], xh, dw[v][p]);
+                db[v][p] = add2(g[p], db[v][p]);
+                const float2 gw = mul2(g[p], w[v][p]);
+                s1 = add2(s1, gw);
+                s2 = fma2(gw, xh, s2);
             }
         }
-        const float2 s = group_sum<kGroup>(s1, s2, slots, turn);
-        const float m1 = s.x * inv, m2 = s.y * inv;
+        float s[2] = {s1.x + s1.y, s2.x + s2.y};
+        group_sum<kGroup>(s, slots, turn);
+        // dx = rstd (dy w - m1 - (x - mean) rstd m2)
+        const float m1 = s[0] * inv, slope = -now.rstd * (s[1] * inv);
         if (live) {
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) {
-                float xh[kE], g[kE];
-                take(v, xh, g);
+                float2 d[kPairs], g[kPairs];
+                take(v, d, g);
 #pragma unroll
-                for (int i = 0; i < kE; ++i)
-                    g[i] = rstd * (g[i] * w[v][i] - m1 - xh[i] * m2);
-                store_vec<kRagged>(dx + r * a.dx_stride, column(v), cols, dx_whole, g);
+                for (int p = 0; p < kPairs; ++p)
+                    g[p] = mul2(both(now.rstd),
+                                fma2(d[p], both(slope), fma2(g[p], w[v][p], both(-m1))));
+                if (at.has(v))
+                    store_vec<kRagged>(dx + at.column(v), dx_cut, g);
             }
+            if (at.has_edge())
+                store_one(dx + at.edge, now.rstd * (de * slope + (ge - m1)));
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
+        r += groups;
+        x += groups * a.x_stride;
+        dy += groups * a.dy_stride;
+        dx += groups * a.dx_stride;
     }
     wait_copies<0>();
     if (!a.sums)
         return;
 
-    float* const mine = a.partials + int64_t(blockIdx.x) * 2 * cols;
+    float* const mine = a.partials + int64_t(blockIdx.x) * 2 * a.cols;
     if constexpr (kGroups == 1) {
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-            for (int i = 0; i < kE; ++i) {
-                const int c = column(v) + i;
-                if (c >= 0 && c < cols) {
-                    mine[c] = dw[v][i];
-                    mine[cols + c] = db[v][i];
-                }
-            }
+        spread(at, dw, dwe, mine);
+        spread(at, db, dbe, mine + a.cols);
     } else {
-        // the block's groups join by columns (their offsets may differ), in
-        // the memory of the ring
-        constexpr int kSpan = kGroup * kVecs * kE;
-        float* const part = reinterpret_cast<float*>(raw);
-        static_assert(kGroups * kSpan * 4 <= BackwardRing<T, kGroup, kVecs>::kBytes,
+        // the block's groups join by columns (their heads may differ), in the
+        // memory of the ring
+        constexpr int kSpan = kGroup * kUnits * 8;
+        static_assert(kGroups * kSpan * 4 <= BackwardRing<T, kGroup, kUnits>::kBytes,
                       "the sums fit the ring");
+        float* const part = reinterpret_cast<float*>(raw);
+        float* const own = part + threadIdx.x / kGroup * kSpan;
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
             __syncthreads();
-#pragma unroll
-            for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-                for (int i = 0; i < kE; ++i) {
-                    const int c = column(v) + i;
-                    if (c >= 0 && c < cols)
-                        part[threadIdx.x / kGroup * kSpan + c] = pass ? db[v][i] : dw[v][i];
-                }
+            if (pass == 0)
+                spread(at, dw, dwe, own);
+            else
+                spread(at, db, dbe, own);
             __syncthreads();
-            for (int c = threadIdx.x; c < cols; c += kThreads) {
+            for (int c = threadIdx.x; c < a.cols; c += kThreads) {
                 float s = 0.0f;
 #pragma unroll
                 for (int q = 0; q < kGroups; ++q)
                     s += part[q * kSpan + c];
-                mine[pass * cols + c] = s;
+                mine[pass * a.cols + c] = s;
             }
         }
     }
@@ -212,17 +232,9 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
 constexpr int kWideThreads = 512;
 
 template <typename T>
-__device__ __forceinline__ float weight_at(const LnBackward& a, int c)
-{
-    return !a.weight ? 1.0f
-           : a.w_f32 ? static_cast<const float*>(a.weight)[c]
-                     : detail::load1(static_cast<const T*>(a.weight) + c);
-}
-
-template <typename T>
 __global__ void __launch_bounds__(kWideThreads) k_ln_backward_wide(LnBackward a)
 {
-    __shared__ float2 slots[2][32];
+    __shared__ float slots[2][2][16];
     int turn = 0;
     const int cols = a.cols;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -232,14 +244,15 @@ __global__ void __launch_bounds__(kWideThreads) k_ln_backward_wide(LnBackward a)
         const float mean = a.mean[r], rstd = a.rstd[r];
         float s1 = 0.0f, s2 = 0.0f;
         for (int c = threadIdx.x; c < cols; c += kWideThreads) {
-            const float g = detail::load1(dy + c) * weight_at<T>(a, c);
+            const float g = detail::load1(dy + c) * weight_at<T>(a.weight, a.w_f32, c, 1.0f);
             s1 += g;
             s2 += g * (detail::load1(x + c) - mean) * rstd;
         }
-        const float2 s = group_sum<kWideThreads>(s1, s2, slots, turn);
-        const float m1 = s.x / float(cols), m2 = s.y / float(cols);
+        float s[2] = {s1, s2};
+        group_sum<kWideThreads>(s, slots, turn);
+        const float m1 = s[0] / float(cols), m2 = s[1] / float(cols);
         for (int c = threadIdx.x; c < cols; c += kWideThreads) {
-            const float g = detail::load1(dy + c) * weight_at<T>(a, c);
+            const float g = detail::load1(dy + c) * weight_at<T>(a.weight, a.w_f32, c, 1.0f);
             store_one(dx + c, rstd * (g - m1 - (detail::load1(x + c) - mean) * rstd * m2));
         }
     }
@@ -268,21 +281,17 @@ __global__ void __launch_bounds__(256) k_ln_columns_wide(LnBackward a)
     mine[a.cols + c] = db;
 }
 
-template <typename T, int G, int V, bool kRagged>
+template <typename T, int G, int U, bool kRagged>
 int launch_one(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s)
 {
     constexpr int kThreads = kBlockThreads<G>;
-    constexpr int kSmem = BackwardRing<T, G, V>::kBytes;
-    auto* const kernel = &k_ln_backward<T, G, V, kRagged>;
+    constexpr int kSmem = BackwardRing<T, G, U>::kBytes;
+    auto* const kernel = &k_ln_backward<T, G, U, kRagged>;
     static const int cap = resident_blocks(kernel, kThreads, kSmem);
-    int64_t blocks = detail::ceil_div(a.rows, kThreads / G);
-    if (kThreads / G < kE)
-        blocks = detail::ceil_div(blocks, kE) * kE;  // groups step by a multiple of 8
     int64_t most = int64_t(cap) * sm_count;
     if (most > ln_parts_max(a.cols))
         most = ln_parts_max(a.cols);
-    most = most / kE * kE;
-    blocks = blocks > most ? most : blocks;
+    const int64_t blocks = row_blocks(a.rows, kThreads / G, most);
     *parts = int32_t(blocks);
     kernel<<<unsigned(blocks), kThreads, kSmem, s>>>(a);
     return int(cudaGetLastError());
@@ -293,10 +302,7 @@ int launch_one(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s
 template <typename T>
 int launch_ln_backward_typed(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s)
 {
-    const bool aligned = a.cols % kE == 0 && rows_aligned<T>(a.x, a.x_stride) &&
-                         rows_aligned<T>(a.dy, a.dy_stride) && rows_aligned<T>(a.dx, a.dx_stride);
-    const int span = aligned ? a.cols : a.cols + kE - 1;
-    if (span > kLnRegisterCols) {
+    if (a.cols > kLnRegisterCols) {
         const int64_t most = int64_t(sm_count) * 4;
         k_ln_backward_wide<T>
             <<<unsigned(a.rows < most ? a.rows : most), kWideThreads, 0, s>>>(a);
@@ -308,10 +314,13 @@ int launch_ln_backward_typed(const LnBackward& a, int sm_count, int32_t* parts, 
             <<<dim3(unsigned(detail::ceil_div(a.cols, 256)), unsigned(*parts)), 256, 0, s>>>(a);
         return int(cudaGetLastError());
     }
-    return with_layout(span, [&](auto layout) {
-        constexpr int G = decltype(layout)::kGroup, V = decltype(layout)::kVecs;
-        return aligned ? launch_one<T, G, V, false>(a, sm_count, parts, s)
-                       : launch_one<T, G, V, true>(a, sm_count, parts, s);
+    const bool aligned = a.cols % kE<T> == 0 && rows_aligned(a.x, a.x_stride, sizeof(T)) &&
+                         rows_aligned(a.dy, a.dy_stride, sizeof(T)) &&
+                         rows_aligned(a.dx, a.dx_stride, sizeof(T));
+    return with_layout(a.cols, aligned, [&](auto layout) {
+        constexpr int G = decltype(layout)::kGroup, U = decltype(layout)::kUnits;
+        return aligned ? launch_one<T, G, U, false>(a, sm_count, parts, s)
+                       : launch_one<T, (G > 8 ? G : 16), U, true>(a, sm_count, parts, s);
     });
 }
 

@@ -1,16 +1,22 @@
 // layernorm_dev.cuh -- the layout of rows over threads that the forward and
 // the backward pass share.
 //
-// A row is held in the registers of one group of kGroup threads (8, 16 or 32
-// lanes of a warp, or a whole block of 128 and more), each with up to kVecs
-// vectors of 8 adjacent elements.  Vectors are cut at multiples of 8
-// elements of the address, not of the row: a row of any width at any place
-// is read in 16-byte (32-byte for float32) accesses but for its first and
-// last vector.  The vectors start `off` elements before the row, off in
-// 0..7.  Groups step through the rows by a multiple of 8, so off -- which
-// has at most 8 values over the rows -- is the same for all rows of a group,
-// and a thread keeps the same columns, their weights and their gradient sums
-// in registers throughout.
+// A row is held by one group of kGroup threads (8, 16 or 32 lanes of a warp,
+// or a whole block of 128 and more), each with up to kVecs vectors of 16
+// bytes.  Vectors are cut at 16-byte boundaries of the address, not of the
+// row: a row of any width at any place is a head of up to kE - 1 elements, a
+// body of whole vectors, and a tail of up to kE - 1 elements; head and tail
+// are one more element for each of 16 lanes.  Groups step through the rows
+// by a multiple of 8, so the head's length -- which has at most 8 values over
+// the rows -- is the same for all rows of a group, and a thread keeps the
+// same columns, their weights and their gradient sums in registers
+// throughout.
+//
+// Rows come through a ring in shared memory (cp.async).  How many bytes are
+// on their way matters in both directions: too few leave the memory idle, too
+// many make it jump between rows (65536 x 4096 bf16 on GB300: forward 213,
+// 166, 190 us with 32, 64, 96 KB an SM; backward 308, 251, 269, 315 with 64,
+// 96, 160, 192).
 #pragma once
 
 #include <cstdint>
@@ -19,89 +25,191 @@
 
 #include "common.cuh"
 #include "layernorm.h"
+#include "packed_dev.cuh"
 
 namespace osr {
 namespace ln {
 
-constexpr int kE = 8;  // elements of a vector
+using packed::add2;
+using packed::both;
+using packed::fma2;
+using packed::mul2;
+
+template <typename T>
+constexpr int kE = 16 / int(sizeof(T));  // elements of a vector
+template <typename T>
+constexpr int kP = kE<T> / 2;  // pairs of a vector
+constexpr int kRowStep = 8;    // groups step by a multiple of this: of kE for every type
+
+__device__ __forceinline__ void widen(uint4 q, float2 (&f)[2])  // float32
+{
+    f[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+    f[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+}
+template <typename T>
+__device__ __forceinline__ void widen16(uint4 q, float2 (&f)[4])  // 16-bit types
+{
+    const T* const t = nullptr;
+    f[0] = detail::widen2(q.x, t);
+    f[1] = detail::widen2(q.y, t);
+    f[2] = detail::widen2(q.z, t);
+    f[3] = detail::widen2(q.w, t);
+}
+template <typename T>
+__device__ __forceinline__ void widen_as(uint4 q, float2 (&f)[kP<T>])
+{
+    if constexpr (sizeof(T) == 4)
+        widen(q, f);
+    else
+        widen16<T>(q, f);
+}
+template <typename T>
+__device__ __forceinline__ uint4 narrow_as(const float2 (&f)[kP<T>])
+{
+    if constexpr (sizeof(T) == 4) {
+        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y),
+                          __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+    } else {
+        const T* const t = nullptr;
+        return make_uint4(detail::pack2(f[0].x, f[0].y, t), detail::pack2(f[1].x, f[1].y, t),
+                          detail::pack2(f[2].x, f[2].y, t), detail::pack2(f[3].x, f[3].y, t));
+    }
+}
+template <int kPairs>
+__device__ __forceinline__ void clear(float2 (&f)[kPairs])
+{
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p)
+        f[p] = make_float2(0.0f, 0.0f);
+}
 
 __device__ __forceinline__ void store_one(float* p, float f) { *p = f; }
 __device__ __forceinline__ void store_one(__nv_bfloat16* p, float f) { *p = __float2bfloat16_rn(f); }
 __device__ __forceinline__ void store_one(__half* p, float f) { *p = __float2half_rn(f); }
 
-using detail::Raw8;
-using detail::store8_cs;
-using detail::widen8;
-
-// How many elements p lies past a vector's boundary.
+// Elements from p to the next 16-byte boundary.
 template <typename T>
-__device__ __forceinline__ int offset_of(const T* p)
+__device__ __forceinline__ int head_of(const T* p)
 {
-    return int((reinterpret_cast<uintptr_t>(p) / sizeof(T)) & (kE - 1));
+    return int((0 - reinterpret_cast<uintptr_t>(p) / sizeof(T)) & (kE<T> - 1));
 }
 
-// A thread's vector starts at column c of a row, c = -off .. cols - 1 or past
-// the end.  kRagged: it may hang over either end of the row.  Elements outside
-// the row count as 0 and are not written.
-template <bool kRagged>
-__device__ __forceinline__ bool is_full(int c, int cols)
-{
-    return kRagged ? c >= 0 && c + kE <= cols : c < cols;
-}
-template <typename T>
-__device__ __forceinline__ void load_elements(const T* row, int c, int cols, float (&f)[kE])
-{
-#pragma unroll
-    for (int i = 0; i < kE; ++i)
-        f[i] = c + i >= 0 && c + i < cols ? detail::load1(row + c + i) : 0.0f;
-}
-// whole: this array's rows are cut where the vectors are.
+// Which columns a thread holds: vectors at column(v), and (kRagged) one
+// element of the head or the tail at edge, or -1.
+template <typename T, int kGroup, int kVecs, bool kRagged>
+struct Columns {
+    int cols, lane, head = 0, body, edge = -1;
+
+    // row: any row of the group
+    __device__ __forceinline__ Columns(int cols_, int lane_, const T* row) : cols(cols_), lane(lane_)
+    {
+        if constexpr (kRagged) {
+            head = head_of(row);
+            head = head < cols ? head : cols;
+            body = (cols - head) / kE<T> * kE<T>;
+            const int tail = cols - head - body;
+            if (lane < 8)
+                edge = lane < head ? lane : -1;
+            else if (lane < 16)
+                edge = lane - 8 < tail ? head + body + lane - 8 : -1;
+        } else {
+            body = cols;
+        }
+    }
+    __device__ __forceinline__ int column(int v) const { return head + (v * kGroup + lane) * kE<T>; }
+    __device__ __forceinline__ bool has(int v) const { return (v * kGroup + lane) * kE<T> < body; }
+    __device__ __forceinline__ bool has_edge() const { return kRagged && edge >= 0; }
+    // Whether the vectors of an array with this row are whole 16-byte pieces.
+    __device__ __forceinline__ bool cut_alike(const T* row) const
+    {
+        return !kRagged || ((reinterpret_cast<uintptr_t>(row + head)) & 15u) == 0;
+    }
+};
+
+// A vector at p, 16-byte aligned or (kRagged) not.
 template <bool kRagged, typename T>
-__device__ __forceinline__ void store_vec(T* row, int c, int cols, bool whole, const float (&f)[kE])
+__device__ __forceinline__ void load_vec(const T* p, bool aligned, float2 (&f)[kP<T>])
 {
-    if (is_full<kRagged>(c, cols) && (!kRagged || whole)) {
-        store8_cs(row + c, f);
-    } else if (kRagged) {
+    if (!kRagged || aligned) {
+        widen_as<T>(__ldg(reinterpret_cast<const uint4*>(p)), f);
+    } else {
 #pragma unroll
-        for (int i = 0; i < kE; ++i)
-            if (c + i >= 0 && c + i < cols)
-                store_one(row + c + i, f[i]);
+        for (int i = 0; i < kP<T>; ++i)
+            f[i] = make_float2(detail::load1(p + 2 * i), detail::load1(p + 2 * i + 1));
+    }
+}
+template <bool kRagged, typename T>
+__device__ __forceinline__ void store_vec(T* p, bool aligned, const float2 (&f)[kP<T>])
+{
+    if (!kRagged || aligned) {
+        __stcs(reinterpret_cast<uint4*>(p), narrow_as<T>(f));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kP<T>; ++i) {
+            store_one(p + 2 * i, f[i].x);
+            store_one(p + 2 * i + 1, f[i].y);
+        }
+    }
+}
+
+// One weight (or bias); `none` where there is no array.
+template <typename T>
+__device__ __forceinline__ float weight_at(const void* w, bool f32, int c, float none)
+{
+    return !w    ? none
+           : f32 ? __ldg(static_cast<const float*>(w) + c)
+                 : detail::load1(static_cast<const T*>(w) + c);
+}
+// A thread's weights for the vector at column c.
+template <typename T>
+__device__ __forceinline__ void load_weights(const void* w, bool f32, int c, bool has, float none,
+                                             float2 (&f)[kP<T>])
+{
+    const char* const at = static_cast<const char*>(w) + int64_t(c) * (f32 ? 4 : int(sizeof(T)));
+    if (!w || !has) {
+#pragma unroll
+        for (int p = 0; p < kP<T>; ++p)
+            f[p] = both(none);
+    } else if (reinterpret_cast<uintptr_t>(at) & 15u) {
+#pragma unroll
+        for (int p = 0; p < kP<T>; ++p)
+            f[p] = make_float2(weight_at<T>(w, f32, c + 2 * p, none),
+                               weight_at<T>(w, f32, c + 2 * p + 1, none));
+    } else if (f32) {
+#pragma unroll
+        for (int p = 0; p < kP<T>; p += 2) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(at) + p / 2);
+            f[p] = make_float2(q.x, q.y);
+            f[p + 1] = make_float2(q.z, q.w);
+        }
+    } else {
+        widen_as<T>(__ldg(reinterpret_cast<const uint4*>(at)), f);
     }
 }
 
 // A thread's vectors of kStages rows of kArrays arrays, on their way through
-// shared memory (cp.async): every thread copies what it will read itself, so
-// it waits for its own copies only and no barrier is needed.
+// shared memory: every thread copies what it will read itself, so it waits
+// for its own copies only and no barrier is needed.
 template <typename T, int kThreads, int kVecs, int kArrays, int kStages>
 struct Ring {
     static constexpr int kDepth = kStages;
-    static constexpr int kHalves = int(sizeof(T)) / 2;  // 16-byte pieces of a vector
-    static constexpr int kBytes = kStages * kArrays * kVecs * kHalves * kThreads * 16;
+    static constexpr int kBytes = kStages * kArrays * kVecs * kThreads * 16;
     uint4* base;
 
-    __device__ __forceinline__ uint4* at(int stage, int array, int vec, int half) const
+    __device__ __forceinline__ uint4* at(int stage, int array, int vec) const
     {
-        return base + (((stage * kArrays + array) * kVecs + vec) * kHalves + half) * kThreads +
-               threadIdx.x;
+        return base + ((stage * kArrays + array) * kVecs + vec) * kThreads + threadIdx.x;
     }
     __device__ __forceinline__ void copy(int stage, int array, int vec, const T* from) const
     {
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                             uint32_t(__cvta_generic_to_shared(at(stage, array, vec, h)))),
-                         "l"(reinterpret_cast<const char*>(from) + 16 * h)
-                         : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         uint32_t(__cvta_generic_to_shared(at(stage, array, vec)))),
+                     "l"(from)
+                     : "memory");
     }
-    __device__ __forceinline__ void read(int stage, int array, int vec, float (&f)[kE]) const
+    __device__ __forceinline__ void read(int stage, int array, int vec, float2 (&f)[kP<T>]) const
     {
-        if constexpr (kHalves == 1) {
-            widen8(Raw8<T>{*at(stage, array, vec, 0)}, f);
-        } else {
-            const float4 a = *reinterpret_cast<const float4*>(at(stage, array, vec, 0));
-            const float4 b = *reinterpret_cast<const float4*>(at(stage, array, vec, 1));
-            widen8(Raw8<float>{a, b}, f);
-        }
+        widen_as<T>(*at(stage, array, vec), f);
     }
 };
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -111,86 +219,67 @@ __device__ __forceinline__ void wait_copies()
     asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// Stages that fit `blocks` resident blocks, at most 3.
-constexpr int stages_for(int stage_bytes, int blocks)
+// Stages for about `want` bytes of ring per SM, 2 to `most` where they fit.
+constexpr int stages_for(int stage_bytes, int blocks, int want, int most)
 {
-    const int n = 208 * 1024 / blocks / stage_bytes;
-    return n < 1 ? 1 : n > 3 ? 3 : n;
+    const int fit = 208 * 1024 / blocks / stage_bytes;
+    int n = want / blocks / stage_bytes;
+    n = n < 2 ? 2 : n > most ? most : n;
+    n = n > fit ? fit : n;
+    return n < 1 ? 1 : n;
 }
 
-// Whether element i of a thread's vector at column c lies in the row.
-template <bool kRagged>
-__device__ __forceinline__ bool in_row(int c, int i, int cols)
-{
-    return kRagged ? (c + i >= 0 && c + i < cols) : c < cols;
-}
-
-// A thread's weights (or biases) for one of its vectors; `none` where there
-// is no array and outside the row.
-template <typename T>
-__device__ __forceinline__ void load_weight(const void* w, bool f32, int c, int cols, float none,
-                                            float (&f)[kE])
-{
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-        const bool in = w && c + i >= 0 && c + i < cols;
-        f[i] = !in   ? none
-               : f32 ? static_cast<const float*>(w)[c + i]
-                     : detail::load1(static_cast<const T*>(w) + c + i);
-    }
-}
-
-// The sums of a and b over a group, in a fixed order, in every thread.
-// `slots`: for groups of a block, 2 x (kGroup / 32) float2 in shared memory,
-// used in turn, so that one barrier per sum is enough.
-template <int kGroup>
-__device__ __forceinline__ float2 group_sum(float a, float b, float2 (*slots)[32], int& turn)
+// The sums of kCount values over a group, in a fixed order, in every thread.
+// `slots` (groups of a block): the warps' sums, two sets used in turn, so that
+// one barrier per call is enough.
+template <int kGroup, int kCount>
+__device__ __forceinline__ void group_sum(float (&s)[kCount], float (*slots)[kCount][16], int& turn)
 {
     constexpr int kLanes = kGroup < 32 ? kGroup : 32;
 #pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, d);
-        b += __shfl_xor_sync(0xffffffffu, b, d);
-    }
-    if constexpr (kGroup > 32) {
-        if ((threadIdx.x & 31) == 0)
-            slots[turn][threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        a = b = 0.0f;
+    for (int d = kLanes / 2; d > 0; d >>= 1)
 #pragma unroll
-        for (int w = 0; w < kGroup / 32; ++w) {
-            const float2 s = slots[turn][w];
-            a += s.x;
-            b += s.y;
+        for (int i = 0; i < kCount; ++i)
+            s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+    if constexpr (kGroup > 32) {
+#pragma unroll
+        for (int i = 0; i < kCount; ++i)
+            if ((threadIdx.x & 31) == 0)
+                slots[turn][i][threadIdx.x >> 5] = s[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) {
+            s[i] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kGroup / 32; ++w)
+                s[i] += slots[turn][i][w];
         }
         turn ^= 1;
     }
-    return make_float2(a, b);
 }
 
 // Threads of a block that holds such groups.
 template <int kGroup>
 constexpr int kBlockThreads = kGroup > 32 ? kGroup : 256;
 
-// Calls f(Layout<kGroup, kVecs>) for the layout of rows that span `span`
-// columns (cols, or cols + 7 where rows may start between boundaries); span
-// <= kLnRegisterCols.
-template <int G, int V>
+// Calls f(Layout<kGroup, kUnits>) for rows of cols elements, cols <=
+// kLnRegisterCols: kUnits x 8 elements a thread.
+template <int G, int U>
 struct Layout {
-    static constexpr int kGroup = G, kVecs = V;
+    static constexpr int kGroup = G, kUnits = U;
 };
 template <typename F>
-int with_layout(int span, F f)
+int with_layout(int cols, bool aligned, F f)
 {
-    if (span <= 64) return f(Layout<8, 1>());
-    if (span <= 128) return f(Layout<16, 1>());
-    if (span <= 256) return f(Layout<32, 1>());
-    if (span <= 512) return f(Layout<32, 2>());
-    if (span <= 768) return f(Layout<32, 3>());
-    if (span <= 1024) return f(Layout<32, 4>());
-    if (span <= 2048) return f(Layout<128, 2>());
-    if (span <= 4096) return f(Layout<128, 4>());
-    if (span <= 8192) return f(Layout<256, 4>());
+    if (cols <= 64 && aligned) return f(Layout<8, 1>());  // no lanes for head and tail
+    if (cols <= 128) return f(Layout<16, 1>());
+    if (cols <= 256) return f(Layout<32, 1>());
+    if (cols <= 512) return f(Layout<32, 2>());
+    if (cols <= 768) return f(Layout<32, 3>());
+    if (cols <= 1024) return f(Layout<32, 4>());
+    if (cols <= 2048) return f(Layout<128, 2>());
+    if (cols <= 4096) return f(Layout<128, 4>());
+    if (cols <= 8192) return f(Layout<256, 4>());
     return f(Layout<512, 4>());
 }
 
@@ -207,11 +296,21 @@ inline int resident_blocks(F* kernel, int threads, int smem)
     return n < 1 ? 1 : n;
 }
 
-// Whether every row of an array starts at a vector's boundary.
-template <typename T>
-inline bool rows_aligned(const void* p, int64_t stride)
+// Blocks for `rows` rows, of `most` at once: the groups step by a multiple of
+// kRowStep.
+inline int64_t row_blocks(int64_t rows, int groups_per_block, int64_t most)
 {
-    return reinterpret_cast<uintptr_t>(p) % (kE * sizeof(T)) == 0 && stride % kE == 0;
+    const int unit = groups_per_block < kRowStep ? kRowStep / groups_per_block : 1;
+    int64_t blocks = detail::ceil_div(rows, groups_per_block);
+    blocks = detail::ceil_div(blocks, unit) * unit;
+    most = most / unit * unit;
+    return blocks > most ? (most < unit ? unit : most) : blocks;
+}
+
+// Whether every row of an array starts at a 16-byte boundary.
+inline bool rows_aligned(const void* p, int64_t stride, size_t size)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && uint64_t(stride) * size % 16 == 0;
 }
 
 }  // namespace ln

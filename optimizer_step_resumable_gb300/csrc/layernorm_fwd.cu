@@ -17,114 +17,130 @@ namespace {
 
 using namespace ln;
 
-// Resident blocks the kernel is compiled for: 24 kVecs registers hold a
+// Resident blocks the kernel is compiled for: 24 registers a unit hold a
 // thread's weights, biases and elements.
-template <int kGroup, int kVecs>
-constexpr int kForwardBlocks = (kVecs == 1 ? 1024 : 512) / kBlockThreads<kGroup>;
+template <int kGroup, int kUnits>
+constexpr int kForwardBlocks = (kUnits == 1 ? 1024 : 512) / kBlockThreads<kGroup>;
 
-template <typename T, int kGroup, int kVecs>
+template <typename T, int kGroup, int kUnits>
 using ForwardRing =
-    Ring<T, kBlockThreads<kGroup>, kVecs, 1,
-         stages_for(kVecs * kBlockThreads<kGroup> * kE * int(sizeof(T)),
-                    kForwardBlocks<kGroup, kVecs>)>;
+    Ring<T, kBlockThreads<kGroup>, kUnits * 8 / kE<T>, 1,
+         stages_for(kUnits * 8 * int(sizeof(T)) * kBlockThreads<kGroup>,
+                    kForwardBlocks<kGroup, kUnits>, 64 * 1024, 3)>;
 
-template <typename T, int kGroup, int kVecs, bool kRagged>
-__global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup, kVecs>))
+template <typename T, int kGroup, int kUnits, bool kRagged>
+__global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup, kUnits>))
     k_ln_forward(LnForward a)
 {
     constexpr int kThreads = kBlockThreads<kGroup>;
     constexpr int kGroups = kThreads / kGroup;
+    constexpr int kVecs = kUnits * 8 / kE<T>;
     extern __shared__ __align__(16) unsigned char raw[];
-    const ForwardRing<T, kGroup, kVecs> ring{reinterpret_cast<uint4*>(raw)};
-    constexpr int kStages = ForwardRing<T, kGroup, kVecs>::kDepth;
-    __shared__ float2 slots[2][32];
+    const ForwardRing<T, kGroup, kUnits> ring{reinterpret_cast<uint4*>(raw)};
+    constexpr int kStages = ForwardRing<T, kGroup, kUnits>::kDepth;
+    __shared__ float slots[2][1][16];
     int turn = 0;
-    const int lane = threadIdx.x % kGroup;
-    const int64_t group = int64_t(blockIdx.x) * kGroups + threadIdx.x / kGroup;
+    const int64_t first = int64_t(blockIdx.x) * kGroups;
     const int64_t groups = int64_t(gridDim.x) * kGroups;
-    const T* const x = static_cast<const T*>(a.x);
-    T* const y = static_cast<T*>(a.y);
-    const int cols = a.cols;
-    const int off = kRagged ? offset_of(x + group * a.x_stride) : 0;
-    const bool y_whole = !kRagged || offset_of(y + group * a.y_stride) == off;
-    auto column = [&](int v) { return (v * kGroup + lane) * kE - off; };
-    auto fetch = [&](int stage, int64_t r) {
-        if (r < a.rows) {
+    int64_t r = first + threadIdx.x / kGroup;
+    const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
+    T* y = static_cast<T*>(a.y) + r * a.y_stride;
+    const Columns<T, kGroup, kVecs, kRagged> at(a.cols, threadIdx.x % kGroup, x);
+    const bool y_cut = at.cut_alike(y);
+    float next_edge[kStages];  // [i]: of the row i + 1 turns ahead
+    auto fetch = [&](int stage, int ahead, float& edge) {
+        const T* const row = x + ahead * groups * a.x_stride;
+        edge = 0.0f;
+        if (r + ahead * groups < a.rows) {
 #pragma unroll
             for (int v = 0; v < kVecs; ++v)
-                if (is_full<kRagged>(column(v), cols))
-                    ring.copy(stage, 0, v, x + r * a.x_stride + column(v));
+                if (at.has(v))
+                    ring.copy(stage, 0, v, row + at.column(v));
+            if (at.has_edge())
+                edge = detail::load1(row + at.edge);
         }
         commit_copies();
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i)
-        fetch(i, group + i * groups);
+        fetch(i, i, next_edge[i]);
 
-    float w[kVecs][kE], b[kVecs][kE];
+    float2 w[kVecs][kP<T>], b[kVecs][kP<T>];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-        load_weight<T>(a.weight, a.w_f32, column(v), cols, 1.0f, w[v]);
-        load_weight<T>(a.bias, a.w_f32, column(v), cols, 0.0f, b[v]);
+        load_weights<T>(a.weight, a.w_f32, at.column(v), at.has(v), 1.0f, w[v]);
+        load_weights<T>(a.bias, a.w_f32, at.column(v), at.has(v), 0.0f, b[v]);
     }
-    // every thread takes part in every sum: the rows past the end are empty
-    const float inv = 1.0f / float(cols);
+    float we = 0.0f, be = 0.0f;
+    if (at.has_edge()) {
+        we = weight_at<T>(a.weight, a.w_f32, at.edge, 1.0f);
+        be = weight_at<T>(a.bias, a.w_f32, at.edge, 0.0f);
+    }
+    const float inv = 1.0f / float(a.cols);
     int stage = 0;
-    for (int64_t first = group - threadIdx.x / kGroup; first < a.rows; first += groups) {
-        const int64_t r = first + threadIdx.x / kGroup;
+    // every thread takes part in every sum: the rows past the end are empty
+    for (int64_t block_r = first; block_r < a.rows; block_r += groups) {
         const bool live = r < a.rows;
-        fetch(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * groups);
+        fetch(stage == 0 ? kStages - 1 : stage - 1, kStages - 1, next_edge[kStages - 1]);
+        float fe = next_edge[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kStages; ++i)
+            next_edge[i] = next_edge[i + 1];
         wait_copies<kStages - 1>();
-        float f[kVecs][kE];
-        float sum = 0.0f;
+        float2 f[kVecs][kP<T>];
+        float2 sums = make_float2(fe, 0.0f);
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
-            const int c = column(v);
-            if (live && is_full<kRagged>(c, cols)) {
+            if (live && at.has(v))
                 ring.read(stage, 0, v, f[v]);
-            } else if (kRagged && live) {
-                load_elements(x + r * a.x_stride, c, cols, f[v]);
-            } else {
+            else
+                clear(f[v]);
 #pragma unroll
-                for (int i = 0; i < kE; ++i)
-                    f[v][i] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < kE; ++i)
-                sum += f[v][i];
+            for (int p = 0; p < kP<T>; ++p)
+                sums = add2(sums, f[v][p]);
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
-        const float mean = group_sum<kGroup>(sum, 0.0f, slots, turn).x * inv;
-        float squares = 0.0f;
+        float total[1] = {sums.x + sums.y};
+        group_sum<kGroup>(total, slots, turn);
+        const float mean = total[0] * inv;
+        fe = at.has_edge() ? fe - mean : 0.0f;
+        float2 squares = make_float2(fe * fe, 0.0f);
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
-            const int c = column(v);
 #pragma unroll
-            for (int i = 0; i < kE; ++i) {
-                f[v][i] -= mean;
-                if (in_row<kRagged>(c, i, cols))
-                    squares += f[v][i] * f[v][i];
+            for (int p = 0; p < kP<T>; ++p)
+                f[v][p] = add2(f[v][p], both(-mean));
+            if (!at.has(v))
+                clear(f[v]);
+#pragma unroll
+            for (int p = 0; p < kP<T>; ++p)
+                squares = fma2(f[v][p], f[v][p], squares);
+        }
+        total[0] = squares.x + squares.y;
+        group_sum<kGroup>(total, slots, turn);
+        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(total[0] * inv + a.eps));
+        if (live) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                float2 o[kP<T>];
+#pragma unroll
+                for (int p = 0; p < kP<T>; ++p)
+                    o[p] = fma2(mul2(f[v][p], both(rstd)), w[v][p], b[v][p]);
+                if (at.has(v))
+                    store_vec<kRagged>(y + at.column(v), y_cut, o);
+            }
+            if (at.has_edge())
+                store_one(y + at.edge, fe * rstd * we + be);
+            if (at.lane == 0) {
+                if (a.mean)
+                    a.mean[r] = mean;
+                if (a.rstd)
+                    a.rstd[r] = rstd;
             }
         }
-        const float var = group_sum<kGroup>(squares, 0.0f, slots, turn).x * inv;
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
-        if (!live)
-            continue;
-        T* const yr = y + r * a.y_stride;
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-            float o[kE];
-#pragma unroll
-            for (int i = 0; i < kE; ++i)
-                o[i] = f[v][i] * rstd * w[v][i] + b[v][i];
-            store_vec<kRagged>(yr, column(v), cols, y_whole, o);
-        }
-        if (lane == 0) {
-            if (a.mean)
-                a.mean[r] = mean;
-            if (a.rstd)
-                a.rstd[r] = rstd;
-        }
+        r += groups;
+        x += groups * a.x_stride;
+        y += groups * a.y_stride;
     }
 }
 
@@ -132,10 +148,17 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
 // later two from L2 or L1.
 constexpr int kWideThreads = 512;
 
+__device__ __forceinline__ float wide_sum(float x, float (*slots)[1][16], int& turn)
+{
+    float s[1] = {x};
+    group_sum<kWideThreads>(s, slots, turn);
+    return s[0];
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) k_ln_forward_wide(LnForward a)
 {
-    __shared__ float2 slots[2][32];
+    __shared__ float slots[2][1][16];
     int turn = 0;
     const int cols = a.cols;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -144,21 +167,17 @@ __global__ void __launch_bounds__(kWideThreads) k_ln_forward_wide(LnForward a)
         float sum = 0.0f;
         for (int c = threadIdx.x; c < cols; c += kWideThreads)
             sum += detail::load1(x + c);
-        const float mean = group_sum<kWideThreads>(sum, 0.0f, slots, turn).x / float(cols);
+        const float mean = wide_sum(sum, slots, turn) / float(cols);
         float squares = 0.0f;
         for (int c = threadIdx.x; c < cols; c += kWideThreads) {
             const float d = detail::load1(x + c) - mean;
             squares += d * d;
         }
-        const float var = group_sum<kWideThreads>(squares, 0.0f, slots, turn).x / float(cols);
+        const float var = wide_sum(squares, slots, turn) / float(cols);
         const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
         for (int c = threadIdx.x; c < cols; c += kWideThreads) {
-            const float w = !a.weight ? 1.0f
-                            : a.w_f32 ? static_cast<const float*>(a.weight)[c]
-                                      : detail::load1(static_cast<const T*>(a.weight) + c);
-            const float b = !a.bias  ? 0.0f
-                            : a.w_f32 ? static_cast<const float*>(a.bias)[c]
-                                      : detail::load1(static_cast<const T*>(a.bias) + c);
+            const float w = weight_at<T>(a.weight, a.w_f32, c, 1.0f);
+            const float b = weight_at<T>(a.bias, a.w_f32, c, 0.0f);
             store_one(y + c, (detail::load1(x + c) - mean) * rstd * w + b);
         }
         if (threadIdx.x == 0) {
@@ -170,18 +189,14 @@ __global__ void __launch_bounds__(kWideThreads) k_ln_forward_wide(LnForward a)
     }
 }
 
-template <typename T, int G, int V, bool kRagged>
+template <typename T, int G, int U, bool kRagged>
 int launch_one(const LnForward& a, int sm_count, cudaStream_t s)
 {
     constexpr int kThreads = kBlockThreads<G>;
-    constexpr int kSmem = ForwardRing<T, G, V>::kBytes;
-    auto* const kernel = &k_ln_forward<T, G, V, kRagged>;
+    constexpr int kSmem = ForwardRing<T, G, U>::kBytes;
+    auto* const kernel = &k_ln_forward<T, G, U, kRagged>;
     static const int cap = resident_blocks(kernel, kThreads, kSmem);
-    int64_t blocks = detail::ceil_div(a.rows, kThreads / G);
-    if (kThreads / G < kE)
-        blocks = detail::ceil_div(blocks, kE) * kE;  // groups step by a multiple of 8
-    const int64_t most = int64_t(cap) * sm_count / kE * kE;
-    blocks = blocks > most ? most : blocks;
+    const int64_t blocks = row_blocks(a.rows, kThreads / G, int64_t(cap) * sm_count);
     kernel<<<unsigned(blocks), kThreads, kSmem, s>>>(a);
     return int(cudaGetLastError());
 }
@@ -189,18 +204,17 @@ int launch_one(const LnForward& a, int sm_count, cudaStream_t s)
 template <typename T>
 int launch_typed(const LnForward& a, int sm_count, cudaStream_t s)
 {
-    const bool aligned = a.cols % kE == 0 && rows_aligned<T>(a.x, a.x_stride) &&
-                         rows_aligned<T>(a.y, a.y_stride);
-    const int span = aligned ? a.cols : a.cols + kE - 1;
-    if (span > kLnRegisterCols) {
+    if (a.cols > kLnRegisterCols) {
         const int64_t most = int64_t(sm_count) * 4;
         k_ln_forward_wide<T><<<unsigned(a.rows < most ? a.rows : most), kWideThreads, 0, s>>>(a);
         return int(cudaGetLastError());
     }
-    return with_layout(span, [&](auto layout) {
-        constexpr int G = decltype(layout)::kGroup, V = decltype(layout)::kVecs;
-        return aligned ? launch_one<T, G, V, false>(a, sm_count, s)
-                       : launch_one<T, G, V, true>(a, sm_count, s);
+    const bool aligned = a.cols % kE<T> == 0 && rows_aligned(a.x, a.x_stride, sizeof(T)) &&
+                         rows_aligned(a.y, a.y_stride, sizeof(T));
+    return with_layout(a.cols, aligned, [&](auto layout) {
+        constexpr int G = decltype(layout)::kGroup, U = decltype(layout)::kUnits;
+        return aligned ? launch_one<T, G, U, false>(a, sm_count, s)
+                       : launch_one<T, (G > 8 ? G : 16), U, true>(a, sm_count, s);
     });
 }
 

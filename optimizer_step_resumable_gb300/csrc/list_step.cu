@@ -187,7 +187,7 @@ __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, flo
     float m_most = 0.0f, v_most = 0.0f;
 #pragma unroll
     for (int j = 0; j < kLane; j += 2) {
-        const float2 gh = state8::mul2(make_float2(g[j], g[j + 1]), state8::both(s));
+        const float2 gh = packed::mul2(make_float2(g[j], g[j + 1]), packed::both(s));
         float2 mn, vn;
         state8::moments(gh, state8::widen_m((x.m[j >> 2] >> (8 * (j & 3))) & 0xffffu),
                         state8::widen_v((x.v[j >> 2] >> (8 * (j & 3))) & 0xffffu), b1, b2, k, mn,

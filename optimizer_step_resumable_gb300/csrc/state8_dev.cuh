@@ -29,9 +29,15 @@
 #include <cuda_runtime.h>
 
 #include "list.h"
+#include "packed_dev.cuh"
 
 namespace osr {
 namespace state8 {
+
+using packed::add2;
+using packed::both;
+using packed::fma2;
+using packed::mul2;
 
 constexpr int kMTop = 7, kVTop = 14;  // exponent of a block's largest value
 
@@ -78,40 +84,6 @@ __device__ __forceinline__ uint32_t narrow_v(float x, float inverse, uint32_t ra
     c = c > 0x7cu ? 0x7cu : c;  // inf stays inf
     return (c == 0u && x > 0.0f) ? 1u : c;
 }
-
-// Two float32 operations in one instruction (sm_100 and later), each rounded
-// on its own: the 8-bit update is bound by instructions as much as by memory.
-__device__ __forceinline__ uint64_t pair(float2 a)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t a)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
-    return unpair(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
-    return unpair(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
-    return unpair(r);
-}
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // The same bytes for four elements at once in half the instructions, for
 // blocks whose scale's reciprocal and the move down are one normal number:
