@@ -29,8 +29,7 @@ using namespace ln;
 // a thread's column sums, 8 its weights.
 template <int kGroup, int kUnits>
 constexpr int kBackwardBlocks = (kUnits == 1   ? 768
-                                 : kUnits == 2 ? 640
-                                 : kUnits == 3 ? 512
+                                 : kUnits <= 3 ? 512
                                                : (kGroup > 256 ? kGroup : 256)) /
                                 kBlockThreads<kGroup>;
 
@@ -38,7 +37,7 @@ template <typename T, int kGroup, int kUnits>
 using BackwardRing =
     Ring<T, kBlockThreads<kGroup>, kUnits * 8 / kE<T>, 2,
          stages_for(2 * kUnits * 8 * int(sizeof(T)) * kBlockThreads<kGroup>,
-                    kBackwardBlocks<kGroup, kUnits>, 120 * 1024, 4)>;
+                    kBackwardBlocks<kGroup, kUnits>, 96 * 1024, 4)>;
 
 // A thread's column sums to their places in a row of cols floats.
 template <typename C, int kVecs, int kPairs>
@@ -60,7 +59,7 @@ __device__ __forceinline__ void spread(const C& at, const float2 (&sum)[kVecs][k
 
 // A row is looked at twice in shared memory, for the sums and for dx, rather
 // than kept widened in 16 registers more a unit.
-template <typename T, int kGroup, int kUnits, bool kRagged>
+template <typename T, int kGroup, int kUnits, Rows kRows>
 __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup, kUnits>))
     k_ln_backward(LnBackward a)
 {
@@ -80,30 +79,37 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
     const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
     const T* dy = static_cast<const T*>(a.dy) + r * a.dy_stride;
     T* dx = static_cast<T*>(a.dx) + r * a.dx_stride;
-    const Columns<T, kGroup, kVecs, kRagged> at(a.cols, threadIdx.x % kGroup, x);
-    const bool dy_cut = at.cut_alike(dy), dx_cut = at.cut_alike(dx);
+    const Columns<T, kGroup, kRows> at(a.cols, threadIdx.x % kGroup, x);
+    constexpr int kStride = Columns<T, kGroup, kRows>::kStride;
+    x += at.start;  // this thread's first vector of row r
+    dy += at.start;
+    dx += at.start;
+    const int edge = at.edge - at.start;
+    const bool dy_cut = kRows != kRagged || is_cut(dy), dx_cut = is_cut(dx);
+    const int64_t x_step = groups * a.x_stride, dy_step = groups * a.dy_stride,
+                  dx_step = groups * a.dx_stride;
     struct Scalars {
         float mean, rstd, x, dy;  // of a row; of this thread's edge element
     };
     Scalars next[kStages];  // [i]: of the row i + 1 turns ahead
     auto fetch = [&](int stage, int ahead, Scalars& s) {
-        const T* const xr = x + ahead * groups * a.x_stride;
-        const T* const gr = dy + ahead * groups * a.dy_stride;
+        const T* const xr = x + ahead * x_step;
+        const T* const gr = dy + ahead * dy_step;
         const int64_t row = r + ahead * groups;
         s = Scalars{0.0f, 0.0f, 0.0f, 0.0f};
         if (row < a.rows) {
 #pragma unroll
             for (int v = 0; v < kVecs; ++v)
                 if (at.has(v)) {
-                    ring.copy(stage, 0, v, xr + at.column(v));
+                    ring.copy(stage, 0, v, xr + v * kStride);
                     if (dy_cut)
-                        ring.copy(stage, 1, v, gr + at.column(v));
+                        ring.copy(stage, 1, v, gr + v * kStride);
                 }
             s.mean = a.mean[row];
             s.rstd = a.rstd[row];
             if (at.has_edge()) {
-                s.x = detail::load1(xr + at.edge);
-                s.dy = detail::load1(gr + at.edge);
+                s.x = detail::load1(xr + edge);
+                s.dy = detail::load1(gr + edge);
             }
         }
         commit_copies();
@@ -137,10 +143,10 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
         auto take = [&](int v, float2(&d)[kPairs], float2(&g)[kPairs]) {
             if (live && at.has(v)) {
                 ring.read(stage, 0, v, d);
-                if (!kRagged || dy_cut)
+                if (dy_cut)
                     ring.read(stage, 1, v, g);
                 else
-                    load_vec<kRagged>(dy + at.column(v), false, g);
+                    load_vec<kRows>(dy + v * kStride, false, g);
             } else {
                 clear(d);
                 clear(g);
@@ -181,16 +187,16 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
                     g[p] = mul2(both(now.rstd),
                                 fma2(d[p], both(slope), fma2(g[p], w[v][p], both(-m1))));
                 if (at.has(v))
-                    store_vec<kRagged>(dx + at.column(v), dx_cut, g);
+                    store_vec<kRows>(dx + v * kStride, dx_cut, g);
             }
             if (at.has_edge())
-                store_one(dx + at.edge, now.rstd * (de * slope + (ge - m1)));
+                store_one(dx + edge, now.rstd * (de * slope + (ge - m1)));
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
         r += groups;
-        x += groups * a.x_stride;
-        dy += groups * a.dy_stride;
-        dx += groups * a.dx_stride;
+        x += x_step;
+        dy += dy_step;
+        dx += dx_step;
     }
     wait_copies<0>();
     if (!a.sums)
@@ -281,12 +287,12 @@ __global__ void __launch_bounds__(256) k_ln_columns_wide(LnBackward a)
     mine[a.cols + c] = db;
 }
 
-template <typename T, int G, int U, bool kRagged>
+template <typename T, int G, int U, Rows kRows>
 int launch_one(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s)
 {
     constexpr int kThreads = kBlockThreads<G>;
     constexpr int kSmem = BackwardRing<T, G, U>::kBytes;
-    auto* const kernel = &k_ln_backward<T, G, U, kRagged>;
+    auto* const kernel = &k_ln_backward<T, G, U, kRows>;
     static const int cap = resident_blocks(kernel, kThreads, kSmem);
     int64_t most = int64_t(cap) * sm_count;
     if (most > ln_parts_max(a.cols))
@@ -319,8 +325,10 @@ int launch_ln_backward_typed(const LnBackward& a, int sm_count, int32_t* parts, 
                          rows_aligned(a.dx, a.dx_stride, sizeof(T));
     return with_layout(a.cols, aligned, [&](auto layout) {
         constexpr int G = decltype(layout)::kGroup, U = decltype(layout)::kUnits;
-        return aligned ? launch_one<T, G, U, false>(a, sm_count, parts, s)
-                       : launch_one<T, (G > 8 ? G : 16), U, true>(a, sm_count, parts, s);
+        if (!aligned)
+            return launch_one<T, (G > 8 ? G : 16), U, kRagged>(a, sm_count, parts, s);
+        return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, parts, s)
+                                   : launch_one<T, G, U, kAligned>(a, sm_count, parts, s);
     });
 }
 

@@ -94,43 +94,52 @@ __device__ __forceinline__ int head_of(const T* p)
     return int((0 - reinterpret_cast<uintptr_t>(p) / sizeof(T)) & (kE<T> - 1));
 }
 
-// Which columns a thread holds: vectors at column(v), and (kRagged) one
-// element of the head or the tail at edge, or -1.
-template <typename T, int kGroup, int kVecs, bool kRagged>
+// How a row lies: kFull: it fills the group's vectors, each at a 16-byte
+// boundary; kAligned: it ends before the last of them; kRagged: any other.
+enum Rows { kFull, kAligned, kRagged };
+
+// Which columns a thread holds: vectors at column(v) = start + v kStride, and
+// (kRagged) one element of the head or the tail at edge, or -1.
+template <typename T, int kGroup, Rows kRows>
 struct Columns {
-    int cols, lane, head = 0, body, edge = -1;
+    static constexpr int kStride = kGroup * kE<T>;
+    int lane, start, end, edge = -1;
 
     // row: any row of the group
-    __device__ __forceinline__ Columns(int cols_, int lane_, const T* row) : cols(cols_), lane(lane_)
+    __device__ __forceinline__ Columns(int cols, int lane_, const T* row) : lane(lane_)
     {
-        if constexpr (kRagged) {
+        int head = 0;
+        end = cols;
+        if constexpr (kRows == kRagged) {
             head = head_of(row);
             head = head < cols ? head : cols;
-            body = (cols - head) / kE<T> * kE<T>;
+            const int body = (cols - head) / kE<T> * kE<T>;
             const int tail = cols - head - body;
+            end = head + body;
             if (lane < 8)
                 edge = lane < head ? lane : -1;
             else if (lane < 16)
-                edge = lane - 8 < tail ? head + body + lane - 8 : -1;
-        } else {
-            body = cols;
+                edge = lane - 8 < tail ? end + lane - 8 : -1;
         }
+        start = head + lane * kE<T>;
     }
-    __device__ __forceinline__ int column(int v) const { return head + (v * kGroup + lane) * kE<T>; }
-    __device__ __forceinline__ bool has(int v) const { return (v * kGroup + lane) * kE<T> < body; }
-    __device__ __forceinline__ bool has_edge() const { return kRagged && edge >= 0; }
-    // Whether the vectors of an array with this row are whole 16-byte pieces.
-    __device__ __forceinline__ bool cut_alike(const T* row) const
-    {
-        return !kRagged || ((reinterpret_cast<uintptr_t>(row + head)) & 15u) == 0;
-    }
+    __device__ __forceinline__ int column(int v) const { return start + v * kStride; }
+    __device__ __forceinline__ bool has(int v) const { return kRows == kFull || column(v) < end; }
+    __device__ __forceinline__ bool has_edge() const { return kRows == kRagged && edge >= 0; }
 };
 
+// Whether p lies at a vector's boundary.
+template <typename T>
+__device__ __forceinline__ bool is_cut(const T* p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
 // A vector at p, 16-byte aligned or (kRagged) not.
-template <bool kRagged, typename T>
+template <Rows kRows, typename T>
 __device__ __forceinline__ void load_vec(const T* p, bool aligned, float2 (&f)[kP<T>])
 {
-    if (!kRagged || aligned) {
+    if (kRows != kRagged || aligned) {
         widen_as<T>(__ldg(reinterpret_cast<const uint4*>(p)), f);
     } else {
 #pragma unroll
@@ -138,10 +147,10 @@ __device__ __forceinline__ void load_vec(const T* p, bool aligned, float2 (&f)[k
             f[i] = make_float2(detail::load1(p + 2 * i), detail::load1(p + 2 * i + 1));
     }
 }
-template <bool kRagged, typename T>
+template <Rows kRows, typename T>
 __device__ __forceinline__ void store_vec(T* p, bool aligned, const float2 (&f)[kP<T>])
 {
-    if (!kRagged || aligned) {
+    if (kRows != kRagged || aligned) {
         __stcs(reinterpret_cast<uint4*>(p), narrow_as<T>(f));
     } else {
 #pragma unroll
@@ -279,6 +288,7 @@ int with_layout(int cols, bool aligned, F f)
     if (cols <= 1024) return f(Layout<32, 4>());
     if (cols <= 2048) return f(Layout<128, 2>());
     if (cols <= 4096) return f(Layout<128, 4>());
+    if (cols <= 6144) return f(Layout<256, 3>());
     if (cols <= 8192) return f(Layout<256, 4>());
     return f(Layout<512, 4>());
 }

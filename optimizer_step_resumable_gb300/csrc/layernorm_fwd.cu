@@ -20,7 +20,7 @@ using namespace ln;
 // Resident blocks the kernel is compiled for: 24 registers a unit hold a
 // thread's weights, biases and elements.
 template <int kGroup, int kUnits>
-constexpr int kForwardBlocks = (kUnits == 1 ? 1024 : 512) / kBlockThreads<kGroup>;
+constexpr int kForwardBlocks = (kUnits == 1 ? 768 : 512) / kBlockThreads<kGroup>;
 
 template <typename T, int kGroup, int kUnits>
 using ForwardRing =
@@ -28,7 +28,7 @@ using ForwardRing =
          stages_for(kUnits * 8 * int(sizeof(T)) * kBlockThreads<kGroup>,
                     kForwardBlocks<kGroup, kUnits>, 64 * 1024, 3)>;
 
-template <typename T, int kGroup, int kUnits, bool kRagged>
+template <typename T, int kGroup, int kUnits, Rows kRows>
 __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup, kUnits>))
     k_ln_forward(LnForward a)
 {
@@ -45,19 +45,24 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
     int64_t r = first + threadIdx.x / kGroup;
     const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
     T* y = static_cast<T*>(a.y) + r * a.y_stride;
-    const Columns<T, kGroup, kVecs, kRagged> at(a.cols, threadIdx.x % kGroup, x);
-    const bool y_cut = at.cut_alike(y);
+    const Columns<T, kGroup, kRows> at(a.cols, threadIdx.x % kGroup, x);
+    constexpr int kStride = Columns<T, kGroup, kRows>::kStride;
+    x += at.start;  // this thread's first vector of row r
+    y += at.start;
+    const int edge = at.edge - at.start;
+    const bool y_cut = is_cut(y);
+    const int64_t x_step = groups * a.x_stride, y_step = groups * a.y_stride;
     float next_edge[kStages];  // [i]: of the row i + 1 turns ahead
-    auto fetch = [&](int stage, int ahead, float& edge) {
-        const T* const row = x + ahead * groups * a.x_stride;
-        edge = 0.0f;
+    auto fetch = [&](int stage, int ahead, float& e) {
+        const T* const row = x + ahead * x_step;
+        e = 0.0f;
         if (r + ahead * groups < a.rows) {
 #pragma unroll
             for (int v = 0; v < kVecs; ++v)
                 if (at.has(v))
-                    ring.copy(stage, 0, v, row + at.column(v));
+                    ring.copy(stage, 0, v, row + v * kStride);
             if (at.has_edge())
-                edge = detail::load1(row + at.edge);
+                e = detail::load1(row + edge);
         }
         commit_copies();
     };
@@ -127,10 +132,10 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
                 for (int p = 0; p < kP<T>; ++p)
                     o[p] = fma2(mul2(f[v][p], both(rstd)), w[v][p], b[v][p]);
                 if (at.has(v))
-                    store_vec<kRagged>(y + at.column(v), y_cut, o);
+                    store_vec<kRows>(y + v * kStride, y_cut, o);
             }
             if (at.has_edge())
-                store_one(y + at.edge, fe * rstd * we + be);
+                store_one(y + edge, fe * rstd * we + be);
             if (at.lane == 0) {
                 if (a.mean)
                     a.mean[r] = mean;
@@ -139,8 +144,8 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
             }
         }
         r += groups;
-        x += groups * a.x_stride;
-        y += groups * a.y_stride;
+        x += x_step;
+        y += y_step;
     }
 }
 
@@ -189,12 +194,12 @@ __global__ void __launch_bounds__(kWideThreads) k_ln_forward_wide(LnForward a)
     }
 }
 
-template <typename T, int G, int U, bool kRagged>
+template <typename T, int G, int U, Rows kRows>
 int launch_one(const LnForward& a, int sm_count, cudaStream_t s)
 {
     constexpr int kThreads = kBlockThreads<G>;
     constexpr int kSmem = ForwardRing<T, G, U>::kBytes;
-    auto* const kernel = &k_ln_forward<T, G, U, kRagged>;
+    auto* const kernel = &k_ln_forward<T, G, U, kRows>;
     static const int cap = resident_blocks(kernel, kThreads, kSmem);
     const int64_t blocks = row_blocks(a.rows, kThreads / G, int64_t(cap) * sm_count);
     kernel<<<unsigned(blocks), kThreads, kSmem, s>>>(a);
@@ -213,8 +218,10 @@ int launch_typed(const LnForward& a, int sm_count, cudaStream_t s)
                          rows_aligned(a.y, a.y_stride, sizeof(T));
     return with_layout(a.cols, aligned, [&](auto layout) {
         constexpr int G = decltype(layout)::kGroup, U = decltype(layout)::kUnits;
-        return aligned ? launch_one<T, G, U, false>(a, sm_count, s)
-                       : launch_one<T, (G > 8 ? G : 16), U, true>(a, sm_count, s);
+        if (!aligned)
+            return launch_one<T, (G > 8 ? G : 16), U, kRagged>(a, sm_count, s);
+        return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, s)
+                                   : launch_one<T, G, U, kAligned>(a, sm_count, s);
     });
 }
 
