@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
     dy += at.start;
     dx += at.start;
     const int edge = at.edge - at.start;
-    const bool dy_cut = kRows != kRagged || is_cut(dy), dx_cut = is_cut(dx);
+    const bool dy_cut = is_cut<kRows>(dy), dx_cut = is_cut<kRows>(dx);
     const int64_t x_step = groups * a.x_stride, dy_step = groups * a.dy_stride,
                   dx_step = groups * a.dx_stride;
     struct Scalars {
@@ -325,8 +325,12 @@ int launch_ln_backward_typed(const LnBackward& a, int sm_count, int32_t* parts, 
                          rows_aligned(a.dx, a.dx_stride, sizeof(T));
     return with_layout(a.cols, aligned, [&](auto layout) {
         constexpr int G = decltype(layout)::kGroup, U = decltype(layout)::kUnits;
+        constexpr int R = G > 8 ? G : 16;  // lanes for head and tail
         if (!aligned)
-            return launch_one<T, (G > 8 ? G : 16), U, kRagged>(a, sm_count, parts, s);
+            return rows_alike(a.x, a.x_stride, a.dy, a.dy_stride, sizeof(T)) &&
+                           rows_alike(a.x, a.x_stride, a.dx, a.dx_stride, sizeof(T))
+                       ? launch_one<T, R, U, kRagged>(a, sm_count, parts, s)
+                       : launch_one<T, R, U, kMixed>(a, sm_count, parts, s);
         return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, parts, s)
                                    : launch_one<T, G, U, kAligned>(a, sm_count, parts, s);
     });

@@ -94,12 +94,14 @@ __device__ __forceinline__ int head_of(const T* p)
     return int((0 - reinterpret_cast<uintptr_t>(p) / sizeof(T)) & (kE<T> - 1));
 }
 
-// How a row lies: kFull: it fills the group's vectors, each at a 16-byte
-// boundary; kAligned: it ends before the last of them; kRagged: any other.
-enum Rows { kFull, kAligned, kRagged };
+// How the rows lie.  kFull: they fill the group's vectors, each at a 16-byte
+// boundary.  kAligned: they end before the last of them.  kRagged: anywhere,
+// but those of all arrays alike (mod 16 bytes).  kMixed: anywhere; arrays
+// other than x may be cut elsewhere and then go element by element.
+enum Rows { kFull, kAligned, kRagged, kMixed };
 
 // Which columns a thread holds: vectors at column(v) = start + v kStride, and
-// (kRagged) one element of the head or the tail at edge, or -1.
+// (kRagged, kMixed) one element of the head or the tail at edge, or -1.
 template <typename T, int kGroup, Rows kRows>
 struct Columns {
     static constexpr int kStride = kGroup * kE<T>;
@@ -110,7 +112,7 @@ struct Columns {
     {
         int head = 0;
         end = cols;
-        if constexpr (kRows == kRagged) {
+        if constexpr (kRows >= kRagged) {
             head = head_of(row);
             head = head < cols ? head : cols;
             const int body = (cols - head) / kE<T> * kE<T>;
@@ -125,21 +127,21 @@ struct Columns {
     }
     __device__ __forceinline__ int column(int v) const { return start + v * kStride; }
     __device__ __forceinline__ bool has(int v) const { return kRows == kFull || column(v) < end; }
-    __device__ __forceinline__ bool has_edge() const { return kRows == kRagged && edge >= 0; }
+    __device__ __forceinline__ bool has_edge() const { return kRows >= kRagged && edge >= 0; }
 };
 
-// Whether p lies at a vector's boundary.
-template <typename T>
+// Whether p lies at a vector's boundary; known but for kMixed.
+template <Rows kRows, typename T>
 __device__ __forceinline__ bool is_cut(const T* p)
 {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+    return kRows != kMixed || (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-// A vector at p, 16-byte aligned or (kRagged) not.
+// A vector at p, 16-byte aligned or (kMixed) not.
 template <Rows kRows, typename T>
 __device__ __forceinline__ void load_vec(const T* p, bool aligned, float2 (&f)[kP<T>])
 {
-    if (kRows != kRagged || aligned) {
+    if (kRows != kMixed || aligned) {
         widen_as<T>(__ldg(reinterpret_cast<const uint4*>(p)), f);
     } else {
 #pragma unroll
@@ -150,7 +152,7 @@ __device__ __forceinline__ void load_vec(const T* p, bool aligned, float2 (&f)[k
 template <Rows kRows, typename T>
 __device__ __forceinline__ void store_vec(T* p, bool aligned, const float2 (&f)[kP<T>])
 {
-    if (kRows != kRagged || aligned) {
+    if (kRows != kMixed || aligned) {
         __stcs(reinterpret_cast<uint4*>(p), narrow_as<T>(f));
     } else {
 #pragma unroll
@@ -321,6 +323,12 @@ inline int64_t row_blocks(int64_t rows, int groups_per_block, int64_t most)
 inline bool rows_aligned(const void* p, int64_t stride, size_t size)
 {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && uint64_t(stride) * size % 16 == 0;
+}
+// Whether the rows of two arrays lie alike, mod 16 bytes.
+inline bool rows_alike(const void* p, int64_t p_stride, const void* q, int64_t q_stride, size_t size)
+{
+    return (reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q)) % 16 == 0 &&
+           (uint64_t(p_stride) - uint64_t(q_stride)) * size % 16 == 0;
 }
 
 }  // namespace ln

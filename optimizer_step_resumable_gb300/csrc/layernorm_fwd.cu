@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
     x += at.start;  // this thread's first vector of row r
     y += at.start;
     const int edge = at.edge - at.start;
-    const bool y_cut = is_cut(y);
+    const bool y_cut = is_cut<kRows>(y);
     const int64_t x_step = groups * a.x_stride, y_step = groups * a.y_stride;
     float next_edge[kStages];  // [i]: of the row i + 1 turns ahead
     auto fetch = [&](int stage, int ahead, float& e) {
@@ -218,8 +218,11 @@ int launch_typed(const LnForward& a, int sm_count, cudaStream_t s)
                          rows_aligned(a.y, a.y_stride, sizeof(T));
     return with_layout(a.cols, aligned, [&](auto layout) {
         constexpr int G = decltype(layout)::kGroup, U = decltype(layout)::kUnits;
+        constexpr int R = G > 8 ? G : 16;  // lanes for head and tail
         if (!aligned)
-            return launch_one<T, (G > 8 ? G : 16), U, kRagged>(a, sm_count, s);
+            return rows_alike(a.x, a.x_stride, a.y, a.y_stride, sizeof(T))
+                       ? launch_one<T, R, U, kRagged>(a, sm_count, s)
+                       : launch_one<T, R, U, kMixed>(a, sm_count, s);
         return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, s)
                                    : launch_one<T, G, U, kAligned>(a, sm_count, s);
     });

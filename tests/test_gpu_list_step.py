@@ -30,6 +30,7 @@ TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 @pytest.fixture(autouse=True)
 def _lib(lib):
     assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    torch.manual_seed(0)
 
 
 def blocks(n):
