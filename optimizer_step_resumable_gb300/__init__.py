@@ -154,6 +154,8 @@ _lib = None
 def library(path: str = None) -> ctypes.CDLL:
     """The loaded C library (loaded once, on first use)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIBRARY
@@ -180,11 +182,15 @@ def _check(status: int, where: str):
         raise cls(status, where, detail)
 
 
-def _stream(stream):
-    """cudaStream_t of a torch stream (None: torch's current stream)."""
-    import torch
+def _stream(stream, device: int = None):
+    """cudaStream_t of a torch stream (None: torch's current stream on the
+    given or the current device)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle without a Stream object around it, which takes 3 us to
+        # make where the call that needs it takes 5
+        import torch
+        return torch._C._cuda_getCurrentRawStream(
+            torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -648,7 +654,7 @@ def adamw_list_step(lst: TensorList, t: int, lr: float, wd: float, clip: float,
     """Update t of every tensor of the list, in place; seed: of the random
     rounding of 8-bit states (the step t enters it too)."""
     st = library().adamw_list_step(lst.handle, t, lr, wd, clip, grad_scale, seed & 0xFFFFFFFF,
-                                   ZERO_GRAD if zero_grad else 0, _stream(stream))
+                                   ZERO_GRAD if zero_grad else 0, _stream(stream, lst.device))
     if st != OK:
         _check(st, "adamw_list_step")
 
@@ -688,32 +694,56 @@ def layernorm_destroy(ln: LayerNorm):
 def _rows(t, ln: LayerNorm, name: str):
     """(address, row stride, rows) of a tensor of shape (..., cols) whose rows
     are evenly spaced."""
-    if not t.is_cuda or t.dim() < 1 or t.shape[-1] != ln.cols:
-        raise TypeError(f"{name} must be a CUDA tensor of shape (..., {ln.cols})")
-    _same_device(t, name, ln)
+    cols = ln.cols
+    if t.get_device() != ln.device or t.dim() < 1 or t.shape[-1] != cols:
+        _refuse_rows(t, ln, name)
     if t.is_contiguous():
-        return t.data_ptr(), ln.cols, t.numel() // ln.cols
+        return t.data_ptr(), cols, t.numel() // cols
     if t.dim() > 2:
         try:
-            t = t.view(-1, ln.cols)
+            t = t.view(-1, cols)
         except RuntimeError:
             raise TypeError(f"{name}: rows must be evenly spaced") from None
-    if t.dim() < 2 or (t.stride(1) != 1 and ln.cols > 1):
+    if t.dim() < 2 or (t.stride(1) != 1 and cols > 1):
         raise TypeError(f"{name}: the elements of a row must be adjacent")
     return t.data_ptr(), t.stride(0), t.shape[0]
 
 
-def _vector(t, n: int, name: str, ln: LayerNorm, dtype=None):
-    """Address of a contiguous tensor of n elements; None stays None."""
-    if t is None:
-        return None
-    if not t.is_cuda or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} must be a contiguous CUDA tensor"
-                        + (f" of {dtype}" if dtype is not None else ""))
-    if t.numel() != n:
-        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+def _refuse_rows(t, ln: LayerNorm, name: str):
+    if not t.is_cuda or t.dim() < 1 or t.shape[-1] != ln.cols:
+        raise TypeError(f"{name} must be a CUDA tensor of shape (..., {ln.cols})")
     _same_device(t, name, ln)
+
+
+def _vector(t, n: int, name: str, ln: LayerNorm) -> int:
+    """Address of a contiguous tensor of n elements."""
+    if t.get_device() != ln.device or not t.is_contiguous() or t.numel() != n:
+        if not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous CUDA tensor")
+        if t.numel() != n:
+            raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+        _same_device(t, name, ln)
     return t.data_ptr()
+
+
+def _row_values(t, rows: int, name: str, ln: LayerNorm) -> int:
+    if _code(t) != DTYPE_F32:
+        raise TypeError(f"{name} must be float32")
+    return _vector(t, rows, name, ln)
+
+
+_DTYPES = {}  # torch dtype -> DTYPE_*
+
+
+def _code(t) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
+                        torch.float16: DTYPE_F16})
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def layernorm_forward(ln: LayerNorm, x, weight=None, bias=None, eps: float = 1e-5, y=None,
@@ -722,23 +752,28 @@ def layernorm_forward(ln: LayerNorm, x, weight=None, bias=None, eps: float = 1e-
     allocated.  weight and bias: float32 or the type of x; None: 1 and 0."""
     import torch
     xp, xs, rows = _rows(x, ln, "x")
+    code = _code(x)
     if y is None:
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif y.dtype != x.dtype or y.shape != x.shape:
+    elif y.dtype is not x.dtype or y.shape != x.shape:
         raise TypeError("y must have the type and shape of x")
     if mean is None:
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     if rstd is None:
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     yp, ys, _ = _rows(y, ln, "y")
-    wt = weight if weight is not None else bias
-    if bias is not None and bias.dtype != wt.dtype:
-        raise TypeError("weight and bias must have one type")
+    wp = bp = None
+    w_code = DTYPE_F32
+    if weight is not None:
+        wp, w_code = _vector(weight, ln.cols, "weight", ln), _code(weight)
+    if bias is not None:
+        bp, b_code = _vector(bias, ln.cols, "bias", ln), _code(bias)
+        if wp is not None and b_code != w_code:
+            raise TypeError("weight and bias must have one type")
+        w_code = b_code
     st = library().layernorm_forward(
-        ln.handle, xp, xs, _dtype_of(x), _vector(weight, ln.cols, "weight", ln),
-        _vector(bias, ln.cols, "bias", ln), DTYPE_F32 if wt is None else _dtype_of(wt), yp, ys,
-        _vector(mean, rows, "mean", ln, torch.float32),
-        _vector(rstd, rows, "rstd", ln, torch.float32), rows, eps, _stream(stream))
+        ln.handle, xp, xs, code, wp, bp, w_code, yp, ys, _row_values(mean, rows, "mean", ln),
+        _row_values(rstd, rows, "rstd", ln), rows, eps, _stream(stream, ln.device))
     if st != OK:
         _check(st, "layernorm_forward")
     return y, mean, rstd
@@ -751,23 +786,29 @@ def layernorm_backward(ln: LayerNorm, dy, x, weight, mean, rstd, dx=None, dweigh
     computed if given.  accumulate: add into dweight and dbias."""
     import torch
     xp, xs, rows = _rows(x, ln, "x")
-    gp, gs, _ = _rows(dy, ln, "dy")
+    code = _code(x)
     if dx is None:
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if dy.dtype != x.dtype or dx.dtype != x.dtype or dy.shape != x.shape or dx.shape != x.shape:
+    if (dy.dtype is not x.dtype or dx.dtype is not x.dtype or dy.shape != x.shape
+            or dx.shape != x.shape):
         raise TypeError("dy and dx must have the type and shape of x")
+    gp, gs, _ = _rows(dy, ln, "dy")
     dp, ds, _ = _rows(dx, ln, "dx")
-    gt = dweight if dweight is not None else dbias
-    if dbias is not None and dbias.dtype != gt.dtype:
-        raise TypeError("dweight and dbias must have one type")
+    wp = dwp = dbp = None
+    w_code = g_code = DTYPE_F32
+    if weight is not None:
+        wp, w_code = _vector(weight, ln.cols, "weight", ln), _code(weight)
+    if dweight is not None:
+        dwp, g_code = _vector(dweight, ln.cols, "dweight", ln), _code(dweight)
+    if dbias is not None:
+        dbp, b_code = _vector(dbias, ln.cols, "dbias", ln), _code(dbias)
+        if dwp is not None and b_code != g_code:
+            raise TypeError("dweight and dbias must have one type")
+        g_code = b_code
     st = library().layernorm_backward(
-        ln.handle, gp, gs, xp, xs, _dtype_of(x), _vector(weight, ln.cols, "weight", ln),
-        DTYPE_F32 if weight is None else _dtype_of(weight),
-        _vector(mean, rows, "mean", ln, torch.float32),
-        _vector(rstd, rows, "rstd", ln, torch.float32), dp, ds,
-        _vector(dweight, ln.cols, "dweight", ln), _vector(dbias, ln.cols, "dbias", ln),
-        DTYPE_F32 if gt is None else _dtype_of(gt), rows,
-        LAYERNORM_ACCUMULATE if accumulate else 0, _stream(stream))
+        ln.handle, gp, gs, xp, xs, code, wp, w_code, _row_values(mean, rows, "mean", ln),
+        _row_values(rstd, rows, "rstd", ln), dp, ds, dwp, dbp, g_code, rows,
+        LAYERNORM_ACCUMULATE if accumulate else 0, _stream(stream, ln.device))
     if st != OK:
         _check(st, "layernorm_backward")
     return dx, dweight, dbias

@@ -37,7 +37,7 @@ template <typename T, int kGroup, int kUnits>
 using BackwardRing =
     Ring<T, kBlockThreads<kGroup>, kUnits * 8 / kE<T>, 2,
          stages_for(2 * kUnits * 8 * int(sizeof(T)) * kBlockThreads<kGroup>,
-                    kBackwardBlocks<kGroup, kUnits>, 96 * 1024, 4)>;
+                    kBackwardBlocks<kGroup, kUnits>, 144 * 1024, 3)>;
 
 // A thread's column sums to their places in a row of cols floats.
 template <typename C, int kVecs, int kPairs>
