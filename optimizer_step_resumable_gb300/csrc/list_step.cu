@@ -187,14 +187,12 @@ __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, flo
     float m_most = 0.0f, v_most = 0.0f;
 #pragma unroll
     for (int j = 0; j < kLane; j += 2) {
-        const float2 gh = packed::mul2(make_float2(g[j], g[j + 1]), packed::both(s));
-        float2 mn, vn;
-        state8::moments(gh, state8::widen_m((x.m[j >> 2] >> (8 * (j & 3))) & 0xffffu),
-                        state8::widen_v((x.v[j >> 2] >> (8 * (j & 3))) & 0xffffu), b1, b2, k, mn,
-                        vn);
-        m[j] = mn.x, m[j + 1] = mn.y, v[j] = vn.x, v[j + 1] = vn.y;
-        m_most = state8::largest(m_most, fabsf(mn.x), fabsf(mn.y));
-        v_most = state8::largest(v_most, vn.x, vn.y);
+        state8::moments(packed::mul2(make_float2(g[j], g[j + 1]), packed::both(s)),
+                        state8::widen_m((x.m[j >> 2] >> (8 * (j & 3))) & 0xffffu),
+                        state8::widen_v((x.v[j >> 2] >> (8 * (j & 3))) & 0xffffu), b1, b2, k,
+                        m + j, v + j);
+        m_most = state8::largest(m_most, fabsf(m[j]), fabsf(m[j + 1]));
+        v_most = state8::largest(v_most, v[j], v[j + 1]);
     }
     // non-negative floats order as their bits do
     const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m_most));

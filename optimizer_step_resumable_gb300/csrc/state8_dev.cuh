@@ -34,7 +34,6 @@
 namespace osr {
 namespace state8 {
 
-using packed::add2;
 using packed::both;
 using packed::fma2;
 using packed::mul2;
@@ -128,12 +127,17 @@ __device__ __forceinline__ void narrow4(const float* x, float move_x, const floa
 }
 
 // Two elements' moments (the formulas of adamw_elem, with every product and
-// sum rounded on its own).  b1 and b2: the betas times the block's old scales.
+// sum rounded on its own: packed sums would be joined with the products into
+// fused multiply-adds).  b1 and b2: the betas times the block's old scales.
 __device__ __forceinline__ void moments(float2 gh, float2 m_old, float2 v_old, float b1, float b2,
-                                        const StepScalars& k, float2& m, float2& v)
+                                        const StepScalars& k, float* m, float* v)
 {
-    m = add2(mul2(both(b1), m_old), mul2(both(k.omb1), gh));
-    v = add2(mul2(both(b2), v_old), mul2(mul2(both(k.omb2), gh), gh));
+    const float2 p = mul2(both(b1), m_old), q = mul2(both(k.omb1), gh);
+    m[0] = __fadd_rn(p.x, q.x);
+    m[1] = __fadd_rn(p.y, q.y);
+    const float2 r = mul2(both(b2), v_old), u = mul2(mul2(both(k.omb2), gh), gh);
+    v[0] = __fadd_rn(r.x, u.x);
+    v[1] = __fadd_rn(r.y, u.y);
 }
 
 // Two elements' weights.  root: sqrt(v) in units of 1 / inv; the quotient to

@@ -284,6 +284,23 @@ def test_8_bit_states_byte_for_byte(shift, g):
                     assert not bad.size, (t, k, name, bad.size, int(bad[0]), got[bad[0]], want[bad[0]])
 
 
+def test_8_bit_states_of_16_bit_gradients_byte_for_byte():
+    """beta1 m + (1 - beta1) g of operands with few bits is often a power of
+    two or a stored value to the last bit (about one block in a thousand), and
+    there a fused multiply-add would round to the other side."""
+    n = 300_000
+    st = State([n], 12, "bf16", [1])
+    grad = st.g[0].float().cpu().numpy()
+    model = ((np.zeros(n, np.uint8), np.zeros(blocks(n), np.float32)),) * 2
+    with st.make() as lst:
+        for t in (1, 2, 3):
+            osr.adamw_list_step(lst, t, LR, WD, float("inf"), seed=5)
+            model = model_step(model, grad, t, 5, 0)
+            for c, s, (want, scale) in zip((st.m[0], st.v[0]), (st.ms[0], st.vs[0]), model):
+                assert np.array_equal(s.cpu().numpy(), scale)
+                assert np.array_equal(c.view(torch.uint8).cpu().numpy(), want)
+
+
 def test_rounding_has_the_value_as_its_mean():
     """65,536 equal moments between two neighbours: the stored ones' mean is
     within 6 standard deviations (spacing / 2 / sqrt(n) at most) of it, and a
