@@ -165,6 +165,30 @@ __device__ __forceinline__ void load_block(const ListTensor& t, int32_t i, int32
     }
 }
 
+// adamw_elem with a shorter way for moments that have died away (rows no token
+// has touched for hundreds of steps) or never lived: the correctly rounded
+// square root and quotient take a slow path for zeros and subnormal numbers
+// (an update of such a state took 232 us, not 188).  The approximate ones, to
+// 2^-23, change the denominator by less than 2^-70 and the update by less than
+// 2^-120 / denom: w gets the same bits unless eps or w itself is as small.
+__device__ __forceinline__ void adamw_elem_any(float& w, float g, float& m, float& v, float s,
+                                               const StepScalars& k, float d)
+{
+    const float gh = __fmul_rn(g, s);
+    const float m1 = __fmaf_rn(k.beta1, m, __fmul_rn(k.omb1, gh));
+    const float v1 = __fmaf_rn(k.beta2, v, __fmul_rn(__fmul_rn(k.omb2, gh), gh));
+    if (fabsf(m1) < 0x1p-100f || v1 < 0x1p-96f) {
+        float root;
+        asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v1));
+        const float denom = __fmaf_rn(root, k.inv_sqrt_bc2, k.eps);
+        w = __fmaf_rn(w, d, -__fmul_rn(k.step_size, __fdividef(m1, denom)));
+        m = m1;
+        v = v1;
+    } else {
+        adamwdev::adamw_elem(w, g, m, v, s, k, d);
+    }
+}
+
 // The update of a block, in registers.  8-bit states: m, v become the new
 // bytes and scales; everything past the end of a partial block is 0 and
 // leaves the block's largest values alone.
@@ -174,7 +198,7 @@ __device__ __forceinline__ void update_block(const ListTensor&, int32_t, float (
 {
 #pragma unroll
     for (int j = 0; j < kLane; ++j)
-        adamwdev::adamw_elem(w[j], g[j], x.m[j], x.v[j], s, k, d);
+        adamw_elem_any(w[j], g[j], x.m[j], x.v[j], s, k, d);
 }
 __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, float (&w)[kLane],
                                              const float (&g)[kLane], Moments<true>& x, float s, const StepScalars& k,
