@@ -65,13 +65,16 @@ __global__ void __launch_bounds__(kNormThreads, 4)
         const bool aligned = t.flags & kListVec;
         int32_t i = int32_t(threadIdx.x) * kLane;
         detail::Raw8<G> x[2][kSet];
+        constexpr int32_t kSpan = kSet * kTile;
         auto load = [&](detail::Raw8<G>(&to)[kSet]) {
 #pragma unroll
             for (int p = 0; p < kSet; ++p, i += kTile)
                 to[p] = aligned && end - i >= kLane ? detail::load8_cg(g + i)
                                                     : detail::load8_part(g + i, end - i);
         };
-        auto sum = [&](const detail::Raw8<G>(&from)[kSet]) {
+        auto sum = [&](const detail::Raw8<G>(&from)[kSet], int32_t begin) {
+            if (begin + int32_t(threadIdx.x) * kLane >= end)
+                return;  // nothing of it is this thread's
             float4 y[2 * kSet];
 #pragma unroll
             for (int p = 0; p < kSet; ++p)
@@ -89,11 +92,14 @@ __global__ void __launch_bounds__(kNormThreads, 4)
             }
         };
         load(x[0]);
-        for (int32_t done = 0; done < end; done += 2 * kSet * kTile) {
-            load(x[1]);
-            sum(x[0]);
-            load(x[0]);
-            sum(x[1]);
+        for (int32_t done = 0; done < end; done += 2 * kSpan) {
+            if (done + kSpan < end)
+                load(x[1]);
+            sum(x[0], done);
+            if (done + 2 * kSpan < end)
+                load(x[0]);
+            if (done + kSpan < end)
+                sum(x[1], done + kSpan);
         }
     }
     acc = detail::block_sum<kNormThreads>(acc + (double(sum_hi) + double(sum_lo)));
