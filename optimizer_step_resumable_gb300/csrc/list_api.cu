@@ -23,9 +23,10 @@ struct adamw_list {
     int32_t n_units = 0, n_plain = 0;  // units, and those of 32-bit states
     double beta1 = 0.9, beta2 = 0.999, eps = 1e-8;
 
+    // one allocation: [NormResult | counters x 4 | pad][partials][tensors][units]
+    unsigned char* d_scratch = nullptr;
     osr::ListTensor* d_tensors = nullptr;
     osr::ListUnit* d_units = nullptr;
-    unsigned char* d_scratch = nullptr;  // [NormResult | counters x 4 | pad][partials]
     osr::NormResult* h_res = nullptr;    // pinned, mapped
     osr::NormResult* h_res_dev = nullptr;
     cudaEvent_t ev_norm = nullptr;
@@ -53,8 +54,6 @@ void free_list(adamw_list* l)
         if (l->ev_norm && l->launched)
             cudaEventSynchronize(l->ev_norm);
         if (l->ev_norm) cudaEventDestroy(l->ev_norm);
-        if (l->d_tensors) cudaFree(l->d_tensors);
-        if (l->d_units) cudaFree(l->d_units);
         if (l->d_scratch) cudaFree(l->d_scratch);
         if (l->h_res) cudaFreeHost(l->h_res);
     }
@@ -96,11 +95,18 @@ int create_list(int32_t n_tensors, const int64_t* numels, const uint8_t* state8,
     }
     CUDA_TRY(cudaDeviceGetAttribute(&l->sm_count, cudaDevAttrMultiProcessorCount, l->device));
     static_assert(sizeof(osr::NormResult) <= adamw_list::kHead / 2, "scratch head layout");
-    const size_t scratch = adamw_list::kHead + sizeof(double) * osr::kNormBlocksMax;
-    CUDA_TRY(cudaMalloc(&l->d_tensors, sizeof(osr::ListTensor) * std::max(n_tensors, 1)));
-    CUDA_TRY(cudaMalloc(&l->d_units, sizeof(osr::ListUnit) * std::max<size_t>(units.size(), 1)));
-    CUDA_TRY(cudaMalloc(&l->d_scratch, scratch));
-    CUDA_TRY(cudaMemset(l->d_scratch, 0, scratch));
+    static_assert(alignof(osr::ListTensor) <= 16 && adamw_list::kHead % 16 == 0 &&
+                      sizeof(double) * osr::kNormBlocksMax % 16 == 0,
+                  "scratch layout");
+    const size_t partials = sizeof(double) * osr::kNormBlocksMax;
+    const size_t table = sizeof(osr::ListTensor) * size_t(n_tensors);
+    CUDA_TRY(cudaMalloc(&l->d_scratch, adamw_list::kHead + partials + table +
+                                           sizeof(osr::ListUnit) * units.size()));
+    l->d_tensors =
+        reinterpret_cast<osr::ListTensor*>(l->d_scratch + adamw_list::kHead + partials);
+    l->d_units = reinterpret_cast<osr::ListUnit*>(l->d_tensors + n_tensors);
+    // adamw_list_bind waits for these before the first step
+    CUDA_TRY(cudaMemset(l->d_scratch, 0, adamw_list::kHead + partials));
     CUDA_TRY(cudaMemcpy(l->d_units, units.data(), sizeof(osr::ListUnit) * units.size(),
                         cudaMemcpyHostToDevice));
     CUDA_TRY(cudaHostAlloc(reinterpret_cast<void**>(&l->h_res), sizeof(osr::NormResult),
@@ -108,17 +114,18 @@ int create_list(int32_t n_tensors, const int64_t* numels, const uint8_t* state8,
     std::memset(l->h_res, 0, sizeof(osr::NormResult));
     CUDA_TRY(cudaHostGetDevicePointer(reinterpret_cast<void**>(&l->h_res_dev), l->h_res, 0));
     CUDA_TRY(cudaEventCreateWithFlags(&l->ev_norm, cudaEventDisableTiming));
-    CUDA_TRY(cudaDeviceSynchronize());
     return ADAMW_OK;
 }
 
-// Copies the host's table to the device, once no step still reads the old one.
+// Copies the host's table to the device, once no step still reads the old
+// one, and waits for it: a step may follow on any stream.
 int upload(adamw_list* l)
 {
     DeviceScope scope(l->device);
     CUDA_TRY(cudaDeviceSynchronize());
     CUDA_TRY(cudaMemcpy(l->d_tensors, l->tensors.data(),
                         sizeof(osr::ListTensor) * l->tensors.size(), cudaMemcpyHostToDevice));
+    CUDA_TRY(cudaDeviceSynchronize());
     return ADAMW_OK;
 }
 
