@@ -182,15 +182,23 @@ def _check(status: int, where: str):
         raise cls(status, where, detail)
 
 
+_raw_stream = None  # torch's own call for the current stream's handle
+
+
 def _stream(stream, device: int = None):
     """cudaStream_t of a torch stream (None: torch's current stream on the
     given or the current device)."""
+    global _raw_stream
     if stream is None:
         # the handle without a Stream object around it, which takes 3 us to
         # make where the call that needs it takes 5
-        import torch
-        return torch._C._cuda_getCurrentRawStream(
-            torch.cuda.current_device() if device is None else device)
+        if _raw_stream is None:
+            import torch
+            _raw_stream = torch._C._cuda_getCurrentRawStream
+        if device is None:
+            import torch
+            device = torch.cuda.current_device()
+        return _raw_stream(device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -691,12 +699,18 @@ def layernorm_destroy(ln: LayerNorm):
     ln.close()
 
 
+# A call's launch takes 2 us, so the checks below read each attribute of a
+# tensor once (60 to 200 ns each) and make no calls of their own unless one
+# fails.
+
 def _rows(t, ln: LayerNorm, name: str):
     """(address, row stride, rows) of a tensor of shape (..., cols) whose rows
     are evenly spaced."""
     cols = ln.cols
     if t.get_device() != ln.device or t.dim() < 1 or t.shape[-1] != cols:
-        _refuse_rows(t, ln, name)
+        if not t.is_cuda or t.dim() < 1 or t.shape[-1] != cols:
+            raise TypeError(f"{name} must be a CUDA tensor of shape (..., {cols})")
+        _same_device(t, name, ln)
     if t.is_contiguous():
         return t.data_ptr(), cols, t.numel() // cols
     if t.dim() > 2:
@@ -709,40 +723,43 @@ def _rows(t, ln: LayerNorm, name: str):
     return t.data_ptr(), t.stride(0), t.shape[0]
 
 
-def _refuse_rows(t, ln: LayerNorm, name: str):
-    if not t.is_cuda or t.dim() < 1 or t.shape[-1] != ln.cols:
-        raise TypeError(f"{name} must be a CUDA tensor of shape (..., {ln.cols})")
+def _refuse_vector(t, n: int, name: str, ln: LayerNorm):
+    """Raises what is wrong with a vector of n elements."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA tensor")
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
     _same_device(t, name, ln)
 
 
-def _vector(t, n: int, name: str, ln: LayerNorm) -> int:
-    """Address of a contiguous tensor of n elements."""
-    if t.get_device() != ln.device or not t.is_contiguous() or t.numel() != n:
-        if not t.is_cuda or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous CUDA tensor")
-        if t.numel() != n:
-            raise ValueError(f"{name} has {t.numel()} elements, not {n}")
-        _same_device(t, name, ln)
-    return t.data_ptr()
+def _vector(t, n: int, name: str, ln: LayerNorm):
+    """(address, type code) of a contiguous tensor of n elements."""
+    if t.get_device() != ln.device or t.numel() != n or not t.is_contiguous():
+        _refuse_vector(t, n, name, ln)
+    return t.data_ptr(), _code(t)
 
 
 def _row_values(t, rows: int, name: str, ln: LayerNorm) -> int:
+    """Address of a contiguous float32 tensor of one value a row."""
+    if t.get_device() != ln.device or t.numel() != rows or not t.is_contiguous():
+        _refuse_vector(t, rows, name, ln)
     if _code(t) != DTYPE_F32:
         raise TypeError(f"{name} must be float32")
-    return _vector(t, rows, name, ln)
+    return t.data_ptr()
 
 
 _DTYPES = {}  # torch dtype -> DTYPE_*
 
 
 def _code(t) -> int:
-    if not _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         import torch
         _DTYPES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
                         torch.float16: DTYPE_F16})
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
+        code = _DTYPES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
     return code
 
 
@@ -750,28 +767,27 @@ def layernorm_forward(ln: LayerNorm, x, weight=None, bias=None, eps: float = 1e-
                       mean=None, rstd=None, stream=None):
     """(y, mean, rstd) of the rows of x (..., cols); outputs not given are
     allocated.  weight and bias: float32 or the type of x; None: 1 and 0."""
-    import torch
     xp, xs, rows = _rows(x, ln, "x")
     code = _code(x)
-    if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif y.dtype is not x.dtype or y.shape != x.shape:
+    if y is None or mean is None or rstd is None:
+        import torch
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
+        y = new(x.shape, x.dtype) if y is None else y
+        mean = new(x.shape[:-1], torch.float32) if mean is None else mean
+        rstd = new(x.shape[:-1], torch.float32) if rstd is None else rstd
+    if y.dtype is not x.dtype or y.shape != x.shape:
         raise TypeError("y must have the type and shape of x")
-    if mean is None:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    if rstd is None:
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     yp, ys, _ = _rows(y, ln, "y")
     wp = bp = None
     w_code = DTYPE_F32
     if weight is not None:
-        wp, w_code = _vector(weight, ln.cols, "weight", ln), _code(weight)
+        wp, w_code = _vector(weight, ln.cols, "weight", ln)
     if bias is not None:
-        bp, b_code = _vector(bias, ln.cols, "bias", ln), _code(bias)
+        bp, b_code = _vector(bias, ln.cols, "bias", ln)
         if wp is not None and b_code != w_code:
             raise TypeError("weight and bias must have one type")
         w_code = b_code
-    st = library().layernorm_forward(
+    st = (_lib or library()).layernorm_forward(
         ln.handle, xp, xs, code, wp, bp, w_code, yp, ys, _row_values(mean, rows, "mean", ln),
         _row_values(rstd, rows, "rstd", ln), rows, eps, _stream(stream, ln.device))
     if st != OK:
@@ -784,28 +800,28 @@ def layernorm_backward(ln: LayerNorm, dy, x, weight, mean, rstd, dx=None, dweigh
     """(dx, dweight, dbias) from the gradient dy of y and the forward pass's
     x, mean, rstd; dx is allocated if not given, dweight and dbias are
     computed if given.  accumulate: add into dweight and dbias."""
-    import torch
     xp, xs, rows = _rows(x, ln, "x")
     code = _code(x)
     if dx is None:
+        import torch
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if (dy.dtype is not x.dtype or dx.dtype is not x.dtype or dy.shape != x.shape
-            or dx.shape != x.shape):
+    kind, shape = x.dtype, x.shape
+    if dy.dtype is not kind or dx.dtype is not kind or dy.shape != shape or dx.shape != shape:
         raise TypeError("dy and dx must have the type and shape of x")
     gp, gs, _ = _rows(dy, ln, "dy")
     dp, ds, _ = _rows(dx, ln, "dx")
     wp = dwp = dbp = None
     w_code = g_code = DTYPE_F32
     if weight is not None:
-        wp, w_code = _vector(weight, ln.cols, "weight", ln), _code(weight)
+        wp, w_code = _vector(weight, ln.cols, "weight", ln)
     if dweight is not None:
-        dwp, g_code = _vector(dweight, ln.cols, "dweight", ln), _code(dweight)
+        dwp, g_code = _vector(dweight, ln.cols, "dweight", ln)
     if dbias is not None:
-        dbp, b_code = _vector(dbias, ln.cols, "dbias", ln), _code(dbias)
+        dbp, b_code = _vector(dbias, ln.cols, "dbias", ln)
         if dwp is not None and b_code != g_code:
             raise TypeError("dweight and dbias must have one type")
         g_code = b_code
-    st = library().layernorm_backward(
+    st = (_lib or library()).layernorm_backward(
         ln.handle, gp, gs, xp, xs, code, wp, w_code, _row_values(mean, rows, "mean", ln),
         _row_values(rstd, rows, "rstd", ln), dp, ds, dwp, dbp, g_code, rows,
         LAYERNORM_ACCUMULATE if accumulate else 0, _stream(stream, ln.device))

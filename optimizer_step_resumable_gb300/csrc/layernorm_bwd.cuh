@@ -11,6 +11,10 @@
 // the same columns in every row it sees, so the two column sums stay in its
 // registers until the end; each block then writes its share (2 cols floats),
 // and k_ln_grads (layernorm_bwd.cu) joins the blocks' shares in a fixed order.
+// (A second kernel's many blocks are faster at it than the last block of the
+// first: 14.5 against 23.8 us for 8192 x 768 bf16.)  On GB300 65536 x 4096
+// bf16 takes 242 us, 6.6 TB/s; 5003 x 1021 float32, whose rows start anywhere,
+// 19 us, of which the second kernel and its wait are 5.
 #pragma once
 
 #include <cstdint>
@@ -25,8 +29,10 @@ namespace {
 
 using namespace ln;
 
-// Threads an SM keeps resident, and so the registers of each: 16 a unit hold
-// a thread's column sums, 8 its weights.
+// Blocks an SM keeps resident, and so the registers of a thread: 16 a unit
+// hold its column sums, 8 its weights.  Four units want 200 and more: at 128,
+// with twice the rows on their way, 1024 columns took 84 us instead of 70
+// (65536 rows, bf16), 4096 columns 315 instead of 251.
 template <int kGroup, int kUnits>
 constexpr int kBackwardBlocks = (kUnits == 1   ? 768
                                  : kUnits <= 3 ? 512

@@ -14,9 +14,9 @@
 //
 // Rows come through a ring in shared memory (cp.async).  How many bytes are
 // on their way matters in both directions: too few leave the memory idle, too
-// many make it jump between rows (65536 x 4096 bf16 on GB300: forward 213,
-// 166, 190 us with 32, 64, 96 KB an SM; backward 308, 251, 269, 315 with 64,
-// 96, 160, 192).
+// many make it jump between rows.  65536 x 4096 bf16 on GB300: forward 171 and
+// 187 us with a ring of 64 and 96 KB an SM; backward 280 and 242 with 64 and
+// 96, and 315 with 192 in twice the blocks.
 #pragma once
 
 #include <cstdint>

@@ -1,16 +1,21 @@
 // list_step.cu -- the clip + AdamW step over a list of tensors, for sm_103a:
-// one reduction and one update launch for all of them, whatever their number.
+// one reduction and one update launch for all tensors of a kind of state,
+// whatever their number.
 //
 // "Training as a Recoverable State Transition" (aihero.club), section "The
 // Exact Targets of Clipping and AdamW": the norm of all gradients joined into
 // one vector, the clip factor, the AdamW update.  Here the vector is never
-// joined: a table of units (up to 1024 consecutive elements of one tensor)
-// built once per list gives every warp its work, so a list costs two launches
-// and a tensor of one element one warp's unit.
+// joined: a table of units (up to 2048 consecutive elements of one tensor)
+// built once per list tells every block what to work on.
 //
-// HBM-bound.  Bytes per parameter with a 32-bit gradient: 28 for 32-bit
-// states; 16 + 16/256 for 8-bit ones (w 8, g 4, m and v 2 + 2, scales); the
-// norm reads g once more, from L2 where it still lies there.
+// HBM-bound: streams read once and written once.  Bytes per parameter of the
+// update with a 16-bit gradient and weight copy: 28 with 32-bit states (w 8,
+// m and v 16, g 2, copy 2), 16.06 with 8-bit ones (w 8, m and v 4, scales
+// 16/256, g 2, copy 2); the norm reads g once more.  On GB300, 110M
+// parameters in 196 tensors: 493 us and 326 us a step (the copy's bandwidth
+// would take 489 and 294 for these bytes); 570M in 8 bits 1607 us (1523).  The
+// norm kernel's share is 46 us: 33 for g, the rest for writing back what the
+// step before left in L2.
 #include <cstdint>
 #include <type_traits>
 
@@ -30,7 +35,8 @@ constexpr int kLane = kBlockElems / 32;  // elements of a block per lane
 
 // A lane's kLane elements of a block are adjacent: lane * kLane, ...  In a
 // vector access a lane moves all of them (32 bytes of float32 in one
-// instruction), and a warp's accesses lie in a row.
+// instruction), and a warp's accesses lie in a row.  (Two 16-byte accesses
+// half a block apart: 389 us instead of 351 for 110M parameters in 8 bits.)
 
 // ---------------------------------------------------------------------------
 // The norm.
@@ -199,16 +205,16 @@ __device__ __forceinline__ void adamw_elem_any(float& w, float g, float& m, floa
 // bytes and scales; everything past the end of a partial block is 0 and
 // leaves the block's largest values alone.
 __device__ __forceinline__ void update_block(const ListTensor&, int32_t, float (&w)[kLane],
-                                             const float (&g)[kLane], Moments<false>& x, float s, const StepScalars& k,
-                                             float d, uint32_t)
+                                             const float (&g)[kLane], Moments<false>& x, float s,
+                                             const StepScalars& k, float d, uint32_t)
 {
 #pragma unroll
     for (int j = 0; j < kLane; ++j)
         adamw_elem_any(w[j], g[j], x.m[j], x.v[j], s, k, d);
 }
 __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, float (&w)[kLane],
-                                             const float (&g)[kLane], Moments<true>& x, float s, const StepScalars& k,
-                                             float d, uint32_t key)
+                                             const float (&g)[kLane], Moments<true>& x, float s,
+                                             const StepScalars& k, float d, uint32_t key)
 {
     // A scale is a power of two, so beta times the scale times the value is
     // rounded as beta times the widened value is.
@@ -332,9 +338,11 @@ __device__ __forceinline__ void store_block(const ListTensor& t, int32_t i, int3
 // round of unit i it asks for the tensor of unit i + 2, the table entry of
 // unit i + 3 and the number of unit i + 4, each known from an earlier round,
 // so no round waits for a chain of loads, and the pointers take no
-// registers.  (One chain a round cost the 8-bit update 15%.)  Long lists
-// hand the units out by a counter, which keeps the blocks close to one
-// another in memory.
+// registers.  Long lists hand the units out by a counter, which keeps the
+// blocks close to one another in memory.  That closeness is what the update
+// lives on: units of 4096 or 8192 elements, or a ring with the next unit's
+// inputs on their way (cp.async), which widen the stretch of memory in flight,
+// took 423 and 369 us where this form took 334 (110M parameters, 8 bits).
 constexpr int kRing = 4;
 
 template <int kBytes>
