@@ -721,8 +721,9 @@ ADAMW_API int ckpt_sha256_backend(void);
  *   there was none; a step captured into a graph is not counted).
  *
  * 8-bit states.  After the update (from the moments in float32) a block's
- * scale becomes the power of two that puts its largest |m| into [2^7, 2^8)
- * and its largest v into [2^14, 2^15), not below 2^-126; each value is
+ * scale becomes the power of two that puts its largest finite |m| into
+ * [2^7, 2^8) and its largest finite v into [2^14, 2^15), not below 2^-126
+ * (an infinite or NaN moment stays that, m as NaN); each value is
  * rounded at random to one of its two neighbours in the 8-bit format, with
  * itself as the mean, because rounding to nearest would stop v: its change
  * per step, about 1 - beta2, is far below half a spacing.  A positive v does
@@ -769,13 +770,14 @@ ADAMW_API int adamw_list_last_norm(adamw_list* list, double* norm_out, float* sc
  *   weight NULL: 1, bias NULL: 0.  mean, rstd: float32, one per row; NULL in
  *   the forward pass when no backward pass follows.  dweight, dbias:
  *   grad_dtype (any), each may be NULL; summed in float32 in an order fixed
- *   by rows and cols (the same bits every time), then rounded once;
+ *   by rows, cols, type and alignment (the same bits every time), then
+ *   rounded once;
  *   LAYERNORM_ACCUMULATE adds the sum to what is there, in float32.
  *   rows = 0 is accepted: dweight and dbias become 0 (or stay, accumulating).
  * Every array must be aligned to its elements; outputs must not overlap
- * inputs.  Rows whose arrays start at the same place within 16 bytes (8
- * elements of float32: 32 bytes) are read and written in vectors, whatever
- * that place is; otherwise the array that differs goes element by element.
+ * inputs.  Rows whose arrays all start at the same place within 16 bytes are
+ * read and written in vectors, whatever that place is; otherwise the array
+ * that differs from x goes element by element.
  * Asynchronous on `stream`.  Errors: ADAMW_EINVAL, ADAMW_ECUDA.
  */
 ADAMW_API int layernorm_create(int32_t cols, layernorm_ctx** out);

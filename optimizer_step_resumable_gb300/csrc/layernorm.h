@@ -51,8 +51,7 @@ struct LnGrads {
     bool accumulate;
 };
 
-// Rows wider than this (less up to 7 elements by which a row may miss its
-// 16-byte boundary) do not fit the registers of one block.
+// Rows wider than this do not fit the registers of one block.
 constexpr int kLnRegisterCols = 16384;
 // Blocks of the backward pass that write partial sums, at most.
 inline int ln_parts_max(int32_t cols) { return cols <= 4096 ? 608 : 304; }

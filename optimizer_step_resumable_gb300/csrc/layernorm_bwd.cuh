@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
         for (int i = 0; i + 1 < kStages; ++i)
             next[i] = next[i + 1];
         wait_copies<kStages - 1>();
-        // one vector of the row, as x - mean and dy; outside the row dy is 0,
-        // and so are all sums
+        // one vector of the row, as x - mean and dy; both are 0 outside the
+        // row, and so are all products (rstd may be large)
         auto take = [&](int v, float2(&d)[kPairs], float2(&g)[kPairs]) {
             if (live && at.has(v)) {
                 ring.read(stage, 0, v, d);
@@ -153,15 +153,15 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
                     ring.read(stage, 1, v, g);
                 else
                     load_vec<kRows>(dy + v * kStride, false, g);
+#pragma unroll
+                for (int p = 0; p < kPairs; ++p)
+                    d[p] = add2(d[p], both(-now.mean));
             } else {
                 clear(d);
                 clear(g);
             }
-#pragma unroll
-            for (int p = 0; p < kPairs; ++p)
-                d[p] = add2(d[p], both(-now.mean));
         };
-        const float de = now.x - now.mean, ge = now.dy * we;
+        const float de = at.has_edge() ? now.x - now.mean : 0.0f, ge = now.dy * we;
         dwe += now.dy * (de * now.rstd);
         dbe += now.dy;
         float2 s1 = make_float2(ge, 0.0f), s2 = make_float2(ge * (de * now.rstd), 0.0f);

@@ -230,9 +230,21 @@ __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, flo
         m_most = state8::largest(m_most, fabsf(m[j]), fabsf(m[j + 1]));
         v_most = state8::largest(v_most, v[j], v[j + 1]);
     }
-    // non-negative floats order as their bits do
-    const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m_most));
-    const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(v_most));
+    // non-negative floats order as their bits do, infinity and NaN above all
+    uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m_most));
+    uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(v_most));
+    const bool fast = mb < state8::kMFast && vb < state8::kVFast;  // the same in every lane
+    if (mb >= state8::kInfinity || vb >= state8::kInfinity) {
+        mb = vb = 0u;
+#pragma unroll
+        for (int j = 0; j < kLane; ++j) {
+            const uint32_t a = __float_as_uint(fabsf(m[j])), b = __float_as_uint(v[j]);
+            mb = a < state8::kInfinity && a > mb ? a : mb;
+            vb = b < state8::kInfinity && b > vb ? b : vb;
+        }
+        mb = __reduce_max_sync(0xffffffffu, mb);
+        vb = __reduce_max_sync(0xffffffffu, vb);
+    }
     const uint32_t me = state8::scale_exponent(mb, state8::kMTop);
     const uint32_t ve = state8::scale_exponent(vb, state8::kVTop);
     x.m_scale = state8::scale_of(me);
@@ -243,7 +255,6 @@ __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, flo
     const uint64_t p0 = uint64_t(t.block0) * kBlockElems + uint32_t(i);
     const uint32_t first = hash32_begin(uint32_t(p0) ^ key ^
                                         (uint32_t(p0 >> 32) * 0x9E3779B1u));
-    const bool fast = mb < state8::kMFast && vb < state8::kVFast;  // the same in every lane
     const float inv = fast ? k.inv_sqrt_bc2 * state8::kRootUnit : k.inv_sqrt_bc2;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

@@ -8,7 +8,8 @@
 // largest magnitude into [2^7, 2^8) for m and [2^14, 2^15) for v -- below
 // the formats' largest finite values 448 and 57344 by at least the factor
 // rounding can add -- so scaling is exact both ways and the only rounding
-// is the one to the 8-bit value.  v gets the wider format: it ranges over
+// is the one to the 8-bit value.  Infinities and NaNs do not count for the
+// scale: they spoil no element but their own (m keeps both as NaN).  v gets the wider format: it ranges over
 // the square of the gradients' range.
 //
 // That rounding is random, up or down to a neighbour with the value as the
@@ -41,6 +42,7 @@ using packed::fma2;
 using packed::mul2;
 
 constexpr int kMTop = 7, kVTop = 14;  // exponent of a block's largest value
+constexpr uint32_t kInfinity = 0x7f800000u;
 
 // The biased binary32 exponent of the scale of a block whose largest
 // magnitude has the bits `most`; at least 1, so that the scale and its
@@ -83,7 +85,7 @@ __device__ __forceinline__ uint32_t narrow_v(float x, float inverse, uint32_t ra
     const float y = __fmul_rn(__fmul_rn(x, inverse), 0x1p-112f);
     uint32_t c = (__float_as_uint(y) + ((random & 0xffffu) << 5)) >> 21;
     c = c > 0x7cu ? 0x7cu : c;  // inf stays inf
-    return (c == 0u && x > 0.0f) ? 1u : c;
+    return x != x ? 0x7fu : (c == 0u && x > 0.0f) ? 1u : c;
 }
 
 // The same bytes for four elements at once in half the instructions, for
@@ -165,10 +167,11 @@ __device__ __forceinline__ float2 root_fast(float2 v)
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(u.y));
     return r;
 }
+// NaN if one of them is.
 __device__ __forceinline__ float largest(float a, float b, float c)
 {
     float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 

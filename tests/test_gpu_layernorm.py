@@ -186,6 +186,19 @@ def test_constant_rows_and_eps():
                 assert not bool(y.any())
 
 
+@pytest.mark.parametrize("kind,cols", [("f32", 40), ("bf16", 41), ("bf16", 600), ("f32", 1021),
+                                       ("f32", 3000)])
+def test_backward_of_large_means_and_factors(kind, cols):
+    """mean x rstd past float32 must not reach the lanes that the row does not fill."""
+    x = torch.full((5, cols), 2.0 ** 80, device="cuda", dtype=TYPES[kind])
+    dy = torch.randn(5, cols, device="cuda").to(TYPES[kind])
+    mean, rstd = torch.full((5,), 2.0 ** 80, device="cuda"), torch.full((5,), 2.0 ** 50, device="cuda")
+    dw, db = (torch.empty(cols, device="cuda") for _ in range(2))
+    with osr.layernorm_create(cols) as ln:
+        dx, _, _ = osr.layernorm_backward(ln, dy, x, None, mean, rstd, dweight=dw, dbias=db)
+    check_backward(dy, x, None, mean, rstd, dx, dw, db)
+
+
 def test_non_finite_rows_stay_rows():
     """A row with inf or nan gives a row of nan and leaves the others alone;
     its columns' gradient sums are nan where the formula's are."""

@@ -301,6 +301,35 @@ def test_8_bit_states_of_16_bit_gradients_byte_for_byte():
                 assert np.array_equal(c.view(torch.uint8).cpu().numpy(), want)
 
 
+def test_8_bit_moments_that_are_not_finite_spoil_only_themselves():
+    """A NaN or infinite stored moment, away from its block's largest, leaves
+    every other element's bytes and its block's scale as they were (weights:
+    the root and the quotient may come from the other form, 1e-6 of the update)."""
+    n = 1000
+    a, b = State([n], 6, "f32", [1]), State([n], 6, "f32", [1])
+    with a.make() as la, b.make() as lb:
+        for st, lst in ((a, la), (b, lb)):
+            st.g[0][[5, 300, 600]] = 1e-4
+            osr.adamw_list_step(lst, 1, LR, WD, float("inf"), seed=2)
+        b.m[0].view(torch.uint8)[5] = 0x7F  # nan
+        b.v[0].view(torch.uint8)[300] = 0x7D  # nan
+        b.v[0].view(torch.uint8)[600] = 0x7C  # inf
+        for st, lst in ((a, la), (b, lb)):
+            osr.adamw_list_step(lst, 2, LR, WD, float("inf"), seed=2)
+    am, av, bm, bv = (t.view(torch.uint8).cpu().numpy() for t in (a.m[0], a.v[0], b.m[0], b.v[0]))
+    assert torch.equal(a.ms[0], b.ms[0]) and torch.equal(a.vs[0], b.vs[0])
+    assert np.isnan(b.m[0].float().cpu().numpy()[5])
+    assert np.isnan(b.v[0].float().cpu().numpy()[300])
+    assert np.isinf(b.v[0].float().cpu().numpy()[600])
+    assert np.array_equal(np.nonzero(am != bm)[0], [5])
+    assert np.array_equal(np.nonzero(av != bv)[0], [300, 600])
+    aw, bw = a.w[0].cpu().numpy(), b.w[0].cpu().numpy()
+    assert np.isnan(bw[[5, 300]]).all() and np.isfinite(np.delete(bw, [5, 300])).all()
+    rest = np.delete(np.arange(n), [5, 300, 600])
+    # both are within U |w| + 1e-6 of the update, at most 3.2 lr, of the formula
+    assert np.all(np.abs(aw - bw)[rest] <= 2 * (2.0 ** -24 * np.abs(aw)[rest] + 3.2e-6 * LR))
+
+
 def test_rounding_has_the_value_as_its_mean():
     """65,536 equal moments between two neighbours: the stored ones' mean is
     within 6 standard deviations (spacing / 2 / sqrt(n) at most) of it, and a
