@@ -776,8 +776,9 @@ ADAMW_API int adamw_list_last_norm(adamw_list* list, double* norm_out, float* sc
  *   rows = 0 is accepted: dweight and dbias become 0 (or stay, accumulating).
  * Every array must be aligned to its elements; outputs must not overlap
  * inputs.  Rows whose arrays all start at the same place within 16 bytes are
- * read and written in vectors, whatever that place is; otherwise the array
- * that differs from x goes element by element.
+ * read and written in vectors, whatever that place is; an output that differs
+ * from x costs a pass through shared memory, and a dy that does is read
+ * element by element.
  * Asynchronous on `stream`.  Errors: ADAMW_EINVAL, ADAMW_ECUDA.
  */
 ADAMW_API int layernorm_create(int32_t cols, layernorm_ctx** out);

@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
     dy += at.start;
     dx += at.start;
     const int edge = at.edge - at.start;
-    const bool dy_cut = is_cut<kRows>(dy), dx_cut = is_cut<kRows>(dx);
+    const bool dy_cut = is_cut<kRows>(dy);
+    const int shift = kRows >= kShifted ? head_of(dx) : 0;  // dx's boundaries after x's
     const int64_t x_step = groups * a.x_stride, dy_step = groups * a.dy_stride,
                   dx_step = groups * a.dx_stride;
     struct Scalars {
@@ -192,11 +193,19 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
                 for (int p = 0; p < kPairs; ++p)
                     g[p] = mul2(both(now.rstd),
                                 fma2(d[p], both(slope), fma2(g[p], w[v][p], both(-m1))));
-                if (at.has(v))
-                    store_vec<kRows>(dx + v * kStride, dx_cut, g);
+                if (kRows >= kShifted && shift)
+                    *ring.at(stage, 0, v) = narrow_as<T>(g);
+                else if (at.has(v))
+                    store_vec(dx + v * kStride, narrow_as<T>(g));
             }
             if (at.has_edge())
                 store_one(dx + edge, now.rstd * (de * slope + (ge - m1)));
+        }
+        if constexpr (kRows >= kShifted) {
+            group_barrier<kGroup>();
+            if (live && shift)
+                store_shifted(at, ring, stage, dx, shift);
+            group_barrier<kGroup>();  // before the next copies into this stage
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
         r += groups;
@@ -333,10 +342,11 @@ int launch_ln_backward_typed(const LnBackward& a, int sm_count, int32_t* parts, 
         constexpr int G = decltype(layout)::kGroup, U = decltype(layout)::kUnits;
         constexpr int R = G > 8 ? G : 16;  // lanes for head and tail
         if (!aligned)
-            return rows_alike(a.x, a.x_stride, a.dy, a.dy_stride, sizeof(T)) &&
-                           rows_alike(a.x, a.x_stride, a.dx, a.dx_stride, sizeof(T))
+            return !rows_alike(a.x, a.x_stride, a.dy, a.dy_stride, sizeof(T))
+                       ? launch_one<T, R, U, kMixed>(a, sm_count, parts, s)
+                   : rows_alike(a.x, a.x_stride, a.dx, a.dx_stride, sizeof(T))
                        ? launch_one<T, R, U, kRagged>(a, sm_count, parts, s)
-                       : launch_one<T, R, U, kMixed>(a, sm_count, parts, s);
+                       : launch_one<T, R, U, kShifted>(a, sm_count, parts, s);
         return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, parts, s)
                                    : launch_one<T, G, U, kAligned>(a, sm_count, parts, s);
     });

@@ -96,12 +96,13 @@ __device__ __forceinline__ int head_of(const T* p)
 
 // How the rows lie.  kFull: they fill the group's vectors, each at a 16-byte
 // boundary.  kAligned: they end before the last of them.  kRagged: anywhere,
-// but those of all arrays alike (mod 16 bytes).  kMixed: anywhere; arrays
-// other than x may be cut elsewhere and then go element by element.
-enum Rows { kFull, kAligned, kRagged, kMixed };
+// but those of all arrays alike (mod 16 bytes).  kShifted: the output is cut
+// elsewhere than x; it is cut anew in shared memory.  kMixed: dy too, which
+// then is read element by element.
+enum Rows { kFull, kAligned, kRagged, kShifted, kMixed };
 
 // Which columns a thread holds: vectors at column(v) = start + v kStride, and
-// (kRagged, kMixed) one element of the head or the tail at edge, or -1.
+// (from kRagged on) one element of the head or the tail at edge, or -1.
 template <typename T, int kGroup, Rows kRows>
 struct Columns {
     static constexpr int kStride = kGroup * kE<T>;
@@ -149,18 +150,47 @@ __device__ __forceinline__ void load_vec(const T* p, bool aligned, float2 (&f)[k
             f[i] = make_float2(detail::load1(p + 2 * i), detail::load1(p + 2 * i + 1));
     }
 }
-template <Rows kRows, typename T>
-__device__ __forceinline__ void store_vec(T* p, bool aligned, const float2 (&f)[kP<T>])
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, uint4 q)
 {
-    if (kRows != kMixed || aligned) {
-        __stcs(reinterpret_cast<uint4*>(p), narrow_as<T>(f));
-    } else {
+    __stcs(reinterpret_cast<uint4*>(p), q);
+}
+// The elements [lo, hi) of a vector, at p.
+__device__ __forceinline__ void store_some(float* p, uint4 q, int lo, int hi)
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < kP<T>; ++i) {
-            store_one(p + 2 * i, f[i].x);
-            store_one(p + 2 * i + 1, f[i].y);
-        }
+    for (int i = 0; i < 4; ++i)
+        if (i >= lo && i < hi)
+            p[i] = __uint_as_float(w[i]);
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, uint4 q, int lo, int hi)  // 16-bit types
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i >= lo && i < hi)
+            reinterpret_cast<uint16_t*>(p)[i] = uint16_t(w[i / 2] >> (16 * (i & 1)));
+}
+// The vector that starts `bytes` (below 16, a multiple of an element) into a
+// and ends in b.
+template <typename T>
+__device__ __forceinline__ uint4 joined(uint4 a, uint4 b, int bytes)
+{
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+        w[i] = bytes & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        w[i] = bytes & 4 ? w[i + 1] : w[i];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (bytes & 2));
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // One weight (or bias); `none` where there is no array.
@@ -203,7 +233,7 @@ __device__ __forceinline__ void load_weights(const void* w, bool f32, int c, boo
 // for its own copies only and no barrier is needed.
 template <typename T, int kThreads, int kVecs, int kArrays, int kStages>
 struct Ring {
-    static constexpr int kDepth = kStages;
+    static constexpr int kDepth = kStages, kVectors = kVecs;
     static constexpr int kBytes = kStages * kArrays * kVecs * kThreads * 16;
     uint4* base;
 
@@ -266,6 +296,45 @@ __device__ __forceinline__ void group_sum(float (&s)[kCount], float (*slots)[kCo
                 s[i] += slots[turn][i][w];
         }
         turn ^= 1;
+    }
+}
+
+template <int kGroup>
+__device__ __forceinline__ void group_barrier()
+{
+    if constexpr (kGroup > 32)
+        __syncthreads();
+    else
+        __syncwarp();
+}
+
+// A row of the output whose vectors are not x's: every thread has
+// put its vectors into array 0 of the ring's stage, and each now takes the
+// vector of `out` that starts `shift` elements into its own and ends in the
+// next; what is left at the two ends goes element by element.  (Rows 1034
+// apart into rows 1021 apart, 32768 x 1021 bf16, all of it element by element
+// and this way: 73 and 39 us forward, 68 and 66 backward; 8192 x 8189: 211
+// and 71, 223 and 153.)
+// out: this thread's first vector.
+template <typename T, int kGroup, Rows kRows, typename R>
+__device__ __forceinline__ void store_shifted(const Columns<T, kGroup, kRows>& at, const R& ring,
+                                              int stage, T* out, int shift)
+{
+#pragma unroll
+    for (int v = 0; v < R::kVectors; ++v) {
+        if (!at.has(v))
+            continue;
+        T* const p = out + v * at.kStride;
+        const uint4 q = *ring.at(stage, 0, v);
+        if (at.column(v) + kE<T> < at.end) {
+            const uint4* const next = at.lane + 1 < kGroup ? ring.at(stage, 0, v) + 1
+                                                           : ring.at(stage, 0, v + 1) + 1 - kGroup;
+            store_vec(p + shift, joined<T>(q, *next, shift * int(sizeof(T))));
+        } else {
+            store_some(p, q, shift, kE<T>);
+        }
+        if (v == 0 && at.lane == 0)
+            store_some(p, q, 0, shift);
     }
 }
 

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
     x += at.start;  // this thread's first vector of row r
     y += at.start;
     const int edge = at.edge - at.start;
-    const bool y_cut = is_cut<kRows>(y);
+    const int shift = kRows == kShifted ? head_of(y) : 0;  // y's boundaries after x's
     const int64_t x_step = groups * a.x_stride, y_step = groups * a.y_stride;
     float next_edge[kStages];  // [i]: of the row i + 1 turns ahead
     auto fetch = [&](int stage, int ahead, float& e) {
@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
             for (int p = 0; p < kP<T>; ++p)
                 sums = add2(sums, f[v][p]);
         }
+        const int mine = stage;
         stage = stage + 1 == kStages ? 0 : stage + 1;
         float total[1] = {sums.x + sums.y};
         group_sum<kGroup>(total, slots, turn);
@@ -133,8 +134,10 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
 #pragma unroll
                 for (int p = 0; p < kP<T>; ++p)
                     o[p] = fma2(mul2(f[v][p], both(rstd)), w[v][p], b[v][p]);
-                if (at.has(v))
-                    store_vec<kRows>(y + v * kStride, y_cut, o);
+                if (kRows == kShifted && shift)
+                    *ring.at(mine, 0, v) = narrow_as<T>(o);
+                else if (at.has(v))
+                    store_vec(y + v * kStride, narrow_as<T>(o));
             }
             if (at.has_edge())
                 store_one(y + edge, fe * rstd * we + be);
@@ -144,6 +147,12 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
                 if (a.rstd)
                     a.rstd[r] = rstd;
             }
+        }
+        if constexpr (kRows == kShifted) {
+            group_barrier<kGroup>();
+            if (live && shift)
+                store_shifted(at, ring, mine, y, shift);
+            group_barrier<kGroup>();  // before the next copies into this stage
         }
         r += groups;
         x += x_step;
@@ -224,7 +233,7 @@ int launch_typed(const LnForward& a, int sm_count, cudaStream_t s)
         if (!aligned)
             return rows_alike(a.x, a.x_stride, a.y, a.y_stride, sizeof(T))
                        ? launch_one<T, R, U, kRagged>(a, sm_count, s)
-                       : launch_one<T, R, U, kMixed>(a, sm_count, s);
+                       : launch_one<T, R, U, kShifted>(a, sm_count, s);
         return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, s)
                                    : launch_one<T, G, U, kAligned>(a, sm_count, s);
     });
