@@ -248,58 +248,125 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
     }
 }
 
-// Rows that do not fit a block's registers.  dx: two looks at each row, the
-// second from L2.
-constexpr int kWideThreads = 512;
-
+// Rows that do not fit a block's registers.  dx: two looks at each row.
 template <typename T>
-__global__ void __launch_bounds__(kWideThreads) k_ln_backward_wide(LnBackward a)
+__global__ void __launch_bounds__(kWideThreads, 2) k_ln_backward_wide(LnBackward a)
 {
     __shared__ float slots[2][2][16];
     int turn = 0;
-    const int cols = a.cols;
+    const float inv = 1.0f / float(a.cols);
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T* const x = static_cast<const T*>(a.x) + r * a.x_stride;
-        const T* const dy = static_cast<const T*>(a.dy) + r * a.dy_stride;
-        T* const dx = static_cast<T*>(a.dx) + r * a.dx_stride;
+        const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
+        const WideColumns<T> at(a.cols, threadIdx.x, x);
+        x += at.start;
+        const T* const dy = static_cast<const T*>(a.dy) + r * a.dy_stride + at.start;
+        T* const dx = static_cast<T*>(a.dx) + r * a.dx_stride + at.start;
         const float mean = a.mean[r], rstd = a.rstd[r];
-        float s1 = 0.0f, s2 = 0.0f;
-        for (int c = threadIdx.x; c < cols; c += kWideThreads) {
-            const float g = detail::load1(dy + c) * weight_at<T>(a.weight, a.w_f32, c, 1.0f);
-            s1 += g;
-            s2 += g * (detail::load1(x + c) - mean) * rstd;
+        const int edge = at.edge - at.start;
+        float de = 0.0f, ge = 0.0f;
+        if (at.has_edge()) {
+            de = detail::load1(x + edge) - mean;
+            ge = detail::load1(dy + edge) * weight_at<T>(a.weight, a.w_f32, at.edge, 1.0f);
         }
-        float s[2] = {s1, s2};
+        float2 s1 = make_float2(ge, 0.0f), s2 = make_float2(ge * (de * rstd), 0.0f);
+        each_vector<T, 2>(at, [&](int v, const float2(&f)[2][kP<T>]) {
+            float2 w[kP<T>];
+            load_weights<T>(a.weight, a.w_f32, at.column(v), true, 1.0f, w);
+#pragma unroll
+            for (int p = 0; p < kP<T>; ++p) {
+                const float2 gw = mul2(f[1][p], w[p]);
+                s1 = add2(s1, gw);
+                s2 = fma2(gw, mul2(add2(f[0][p], both(-mean)), both(rstd)), s2);
+            }
+        }, x, dy);
+        float s[2] = {s1.x + s1.y, s2.x + s2.y};
         group_sum<kWideThreads>(s, slots, turn);
-        const float m1 = s[0] / float(cols), m2 = s[1] / float(cols);
-        for (int c = threadIdx.x; c < cols; c += kWideThreads) {
-            const float g = detail::load1(dy + c) * weight_at<T>(a.weight, a.w_f32, c, 1.0f);
-            store_one(dx + c, rstd * (g - m1 - (detail::load1(x + c) - mean) * rstd * m2));
-        }
+        const float m1 = s[0] * inv, slope = -rstd * (s[1] * inv);
+        const bool dx_cut = is_cut<kMixed>(dx);
+        each_vector<T, 2>(at, [&](int v, const float2(&f)[2][kP<T>]) {
+            float2 w[kP<T>], o[kP<T>];
+            load_weights<T>(a.weight, a.w_f32, at.column(v), true, 1.0f, w);
+#pragma unroll
+            for (int p = 0; p < kP<T>; ++p)
+                o[p] = mul2(both(rstd), fma2(add2(f[0][p], both(-mean)), both(slope),
+                                             fma2(f[1][p], w[p], both(-m1))));
+            store_any(dx + v * at.kStride, dx_cut, narrow_as<T>(o));
+        }, x, dy);
+        if (at.has_edge())
+            store_one(dx + edge, rstd * (de * slope + (ge - m1)));
     }
 }
 
-// The column sums of such rows: a thread per column, a strip of rows per
-// block of the grid's second dimension.
+// The column sums of such rows: a vector of columns per thread; strip q of the
+// rows (the grid's second dimension) is q, q + 32, ..., whose vectors are the
+// same, as 32 is a multiple of kRowStep.
+constexpr int kColumnThreads = 128, kAtOnce = 4;  // rows on their way
+
 template <typename T>
-__global__ void __launch_bounds__(256) k_ln_columns_wide(LnBackward a)
+__global__ void __launch_bounds__(kColumnThreads) k_ln_columns_wide(LnBackward a)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.cols)
-        return;
-    const int64_t lo = a.rows * blockIdx.y / gridDim.y, hi = a.rows * (blockIdx.y + 1) / gridDim.y;
-    const T* x = static_cast<const T*>(a.x) + lo * a.x_stride + c;
-    const T* dy = static_cast<const T*>(a.dy) + lo * a.dy_stride + c;
-    float dw = 0.0f, db = 0.0f;
-    for (int64_t r = lo; r < hi; ++r, x += a.x_stride, dy += a.dy_stride) {
-        const float g = detail::load1(dy);
-        dw += g * (detail::load1(x) - a.mean[r]) * a.rstd[r];
-        db += g;
+    const int vector = blockIdx.x * kColumnThreads + threadIdx.x;
+    const int64_t first = blockIdx.y;
+    const T* x = static_cast<const T*>(a.x) + first * a.x_stride;
+    const T* dy = static_cast<const T*>(a.dy) + first * a.dy_stride;
+    const Columns<T, 1, kMixed> at(a.cols, vector, x);  // vector 0 of lane `vector`
+    float* const mine = a.partials + first * 2 * a.cols;
+    const int64_t x_step = kLnWideParts * a.x_stride, dy_step = kLnWideParts * a.dy_stride;
+    if (at.has(0)) {
+        const T* const dy0 = dy + at.start;
+        const T* const x0 = x + at.start;
+        const bool dy_cut = is_cut<kMixed>(dy0);
+        float2 dw[kP<T>], db[kP<T>];
+        clear(dw);
+        clear(db);
+        int64_t i = 0;  // rows done
+        for (int64_t r = first; r < a.rows; r += kAtOnce * kLnWideParts, i += kAtOnce) {
+            float2 f[kAtOnce][kP<T>], g[kAtOnce][kP<T>];
+            float mean[kAtOnce], rstd[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int64_t row = r + u * kLnWideParts;
+                if (row < a.rows) {
+                    load_vec<kMixed>(x0 + (i + u) * x_step, true, f[u]);
+                    load_vec<kMixed>(dy0 + (i + u) * dy_step, dy_cut, g[u]);
+                    mean[u] = a.mean[row];
+                    rstd[u] = a.rstd[row];
+                } else {
+                    clear(f[u]);
+                    clear(g[u]);
+                    mean[u] = rstd[u] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+                for (int p = 0; p < kP<T>; ++p) {
+                    const float2 d = add2(f[u][p], both(-mean[u]));
+                    dw[p] = fma2(g[u][p], mul2(d, both(rstd[u])), dw[p]);
+                    db[p] = add2(g[u][p], db[p]);
+                }
+        }
+#pragma unroll
+        for (int p = 0; p < kP<T>; ++p) {
+            mine[at.start + 2 * p] = dw[p].x;
+            mine[at.start + 2 * p + 1] = dw[p].y;
+            mine[a.cols + at.start + 2 * p] = db[p].x;
+            mine[a.cols + at.start + 2 * p + 1] = db[p].y;
+        }
     }
-    float* const mine = a.partials + int64_t(blockIdx.y) * 2 * a.cols;
-    mine[c] = dw;
-    mine[a.cols + c] = db;
+    if (at.has_edge()) {
+        float dw = 0.0f, db = 0.0f;
+        const T* xe = x + at.edge;
+        const T* ge = dy + at.edge;
+        for (int64_t r = first; r < a.rows; r += kLnWideParts, xe += x_step, ge += dy_step) {
+            const float g = detail::load1(ge);
+            dw += g * ((detail::load1(xe) - a.mean[r]) * a.rstd[r]);
+            db += g;
+        }
+        mine[at.edge] = dw;
+        mine[a.cols + at.edge] = db;
+    }
 }
 
 template <typename T, int G, int U, Rows kRows>
@@ -332,7 +399,8 @@ int launch_ln_backward_typed(const LnBackward& a, int sm_count, int32_t* parts, 
         if (e != cudaSuccess || !a.sums)
             return int(e);
         k_ln_columns_wide<T>
-            <<<dim3(unsigned(detail::ceil_div(a.cols, 256)), unsigned(*parts)), 256, 0, s>>>(a);
+            <<<dim3(unsigned(detail::ceil_div(a.cols, kColumnThreads * kE<T>)), unsigned(*parts)),
+               kColumnThreads, 0, s>>>(a);
         return int(cudaGetLastError());
     }
     const bool aligned = a.cols % kE<T> == 0 && rows_aligned(a.x, a.x_stride, sizeof(T)) &&

@@ -338,6 +338,69 @@ __device__ __forceinline__ void store_shifted(const Columns<T, kGroup, kRows>& a
     }
 }
 
+// Rows that do not fit a block's registers: a block looks at a row several
+// times, the later ones from L2.  4096 x 32768 bf16 takes 191 us forward and
+// 430 backward (element by element: 395 and 887).  Rows spread over clusters
+// of blocks, held in registers, took 227 and 387 (16392 columns: 303 and 481,
+// where this takes 236 and 436): each row waits for the cluster's barriers.
+constexpr int kWideThreads = 512;
+template <typename T>
+using WideColumns = Columns<T, kWideThreads, kMixed>;
+
+// A vector as it lies in memory.
+template <typename T>
+__device__ __forceinline__ uint4 load_raw(const T* p, bool aligned)
+{
+    if (aligned)
+        return __ldg(reinterpret_cast<const uint4*>(p));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+        } else {
+            const uint16_t* const h = reinterpret_cast<const uint16_t*>(p) + 2 * i;
+            w[i] = uint32_t(__ldg(h)) | uint32_t(__ldg(h + 1)) << 16;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Calls f(v, vectors) for a thread's vectors of a row of each array, kAtOnce
+// of them on their way; p...: where its first lies.
+template <typename T, int kAtOnce, typename C, typename F, typename... P>
+__device__ __forceinline__ void each_vector(const C& at, F f, const P*... p)
+{
+    constexpr int kArrays = sizeof...(P);
+    const T* const from[kArrays] = {p...};
+    for (int v = 0; at.has(v); v += kAtOnce) {
+        uint4 q[kAtOnce][kArrays];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+            if (at.has(v + u)) {
+#pragma unroll
+                for (int i = 0; i < kArrays; ++i)
+                    q[u][i] = load_raw(from[i] + (v + u) * C::kStride, is_cut<kMixed>(from[i]));
+            }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+            if (at.has(v + u)) {
+                float2 x[kArrays][kP<T>];
+#pragma unroll
+                for (int i = 0; i < kArrays; ++i)
+                    widen_as<T>(q[u][i], x[i]);
+                f(v + u, x);
+            }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_any(T* p, bool aligned, uint4 q)
+{
+    if (aligned)
+        store_vec(p, q);
+    else
+        store_some(p, q, 0, kE<T>);
+}
+
 // Threads of a block that holds such groups.
 template <int kGroup>
 constexpr int kBlockThreads = kGroup > 32 ? kGroup : 256;

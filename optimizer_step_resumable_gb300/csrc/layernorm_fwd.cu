@@ -160,42 +160,53 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
     }
 }
 
-// Rows that do not fit a block's registers: three looks at the row, the
-// later two from L2 or L1.
-constexpr int kWideThreads = 512;
-
-__device__ __forceinline__ float wide_sum(float x, float (*slots)[1][16], int& turn)
-{
-    float s[1] = {x};
-    group_sum<kWideThreads>(s, slots, turn);
-    return s[0];
-}
-
+// Rows that do not fit a block's registers: three looks at the row.
 template <typename T>
-__global__ void __launch_bounds__(kWideThreads) k_ln_forward_wide(LnForward a)
+__global__ void __launch_bounds__(kWideThreads, 2) k_ln_forward_wide(LnForward a)
 {
     __shared__ float slots[2][1][16];
     int turn = 0;
-    const int cols = a.cols;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T* const x = static_cast<const T*>(a.x) + r * a.x_stride;
-        T* const y = static_cast<T*>(a.y) + r * a.y_stride;
-        float sum = 0.0f;
-        for (int c = threadIdx.x; c < cols; c += kWideThreads)
-            sum += detail::load1(x + c);
-        const float mean = wide_sum(sum, slots, turn) / float(cols);
-        float squares = 0.0f;
-        for (int c = threadIdx.x; c < cols; c += kWideThreads) {
-            const float d = detail::load1(x + c) - mean;
-            squares += d * d;
-        }
-        const float var = wide_sum(squares, slots, turn) / float(cols);
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
-        for (int c = threadIdx.x; c < cols; c += kWideThreads) {
-            const float w = weight_at<T>(a.weight, a.w_f32, c, 1.0f);
-            const float b = weight_at<T>(a.bias, a.w_f32, c, 0.0f);
-            store_one(y + c, (detail::load1(x + c) - mean) * rstd * w + b);
-        }
+        const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
+        const WideColumns<T> at(a.cols, threadIdx.x, x);
+        x += at.start;
+        T* const y = static_cast<T*>(a.y) + r * a.y_stride + at.start;
+        const int edge = at.edge - at.start;
+        float fe = at.has_edge() ? detail::load1(x + edge) : 0.0f;
+        float2 sums = make_float2(fe, 0.0f);
+        each_vector<T, 4>(at, [&](int, const float2(&f)[1][kP<T>]) {
+#pragma unroll
+            for (int p = 0; p < kP<T>; ++p)
+                sums = add2(sums, f[0][p]);
+        }, x);
+        float total[1] = {sums.x + sums.y};
+        group_sum<kWideThreads>(total, slots, turn);
+        const float mean = total[0] / float(a.cols);
+        fe = at.has_edge() ? fe - mean : 0.0f;
+        float2 squares = make_float2(fe * fe, 0.0f);
+        each_vector<T, 4>(at, [&](int, const float2(&f)[1][kP<T>]) {
+#pragma unroll
+            for (int p = 0; p < kP<T>; ++p) {
+                const float2 d = add2(f[0][p], both(-mean));
+                squares = fma2(d, d, squares);
+            }
+        }, x);
+        total[0] = squares.x + squares.y;
+        group_sum<kWideThreads>(total, slots, turn);
+        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(total[0] / float(a.cols) + a.eps));
+        const bool y_cut = is_cut<kMixed>(y);
+        each_vector<T, 2>(at, [&](int v, const float2(&f)[1][kP<T>]) {
+            float2 w[kP<T>], b[kP<T>], o[kP<T>];
+            load_weights<T>(a.weight, a.w_f32, at.column(v), true, 1.0f, w);
+            load_weights<T>(a.bias, a.w_f32, at.column(v), true, 0.0f, b);
+#pragma unroll
+            for (int p = 0; p < kP<T>; ++p)
+                o[p] = fma2(mul2(add2(f[0][p], both(-mean)), both(rstd)), w[p], b[p]);
+            store_any(y + v * at.kStride, y_cut, narrow_as<T>(o));
+        }, x);
+        if (at.has_edge())
+            store_one(y + edge, fe * rstd * weight_at<T>(a.weight, a.w_f32, at.edge, 1.0f) +
+                                    weight_at<T>(a.bias, a.w_f32, at.edge, 0.0f));
         if (threadIdx.x == 0) {
             if (a.mean)
                 a.mean[r] = mean;

@@ -136,6 +136,22 @@ def test_wide_rows(kind, cols):
     run(9, cols, kind, "f32", seed=cols)
 
 
+# rows that are looked at several times
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [24_576, 24_577, 65_528, 65_536, 65_537, 81_920, 131_071, 131_072,
+                                  131_073])
+def test_rows_wider_than_a_block(kind, cols):
+    run(5, cols, kind, kind, seed=cols, accumulate=True)
+
+
+@pytest.mark.parametrize("pad,at", [((8, 8, 8), (0, 0, 0)), ((3, 3, 3), (1, 1, 1)),
+                                    ((1, 5, 2), (0, 3, 6)), ((13, 13, 0), (0, 0, 0))])
+@pytest.mark.parametrize("cols", [16_400, 17_011])
+def test_rows_wider_than_a_block_at_strides_and_places(cols, pad, at):
+    run(301, cols, "bf16", "f32", seed=cols, pad=pad, at=at)
+    run(19, cols, "f32", "f32", seed=cols, pad=pad, at=at)
+
+
 def test_widest_rows():
     run(2, 1 << 18, "bf16")
 
