@@ -9,8 +9,8 @@
 // the formats' largest finite values 448 and 57344 by at least the factor
 // rounding can add -- so scaling is exact both ways and the only rounding
 // is the one to the 8-bit value.  Infinities and NaNs do not count for the
-// scale: they spoil no element but their own (m keeps both as NaN).  v gets the wider format: it ranges over
-// the square of the gradients' range.
+// scale: they spoil no element but their own (m keeps both as NaN).  v gets
+// the wider format: it ranges over the square of the gradients' range.
 //
 // That rounding is random, up or down to a neighbour with the value as the
 // mean.  With beta2 = 0.999 one step changes v by about 0.1%, against a
