@@ -22,7 +22,7 @@
 //
 // The moments are formed in single IEEE roundings in a fixed order (no fused
 // multiply-add), so the stored bytes follow from the formulas on any machine.
-// An element takes 55 instructions: memory and instructions bind the update
+// An element takes 59 instructions: memory and instructions bind the update
 // about equally (without the arithmetic, 304 instead of 327 us).
 #pragma once
 
