@@ -54,23 +54,23 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
     const int edge = at.edge - at.start;
     const int shift = kRows == kShifted ? head_of(y) : 0;  // y's boundaries after x's
     const int64_t x_step = groups * a.x_stride, y_step = groups * a.y_stride;
-    float next_edge[kStages];  // [i]: of the row i + 1 turns ahead
-    auto fetch = [&](int stage, int ahead, float& e) {
+    auto fetch = [&](int stage, int ahead) {
         const T* const row = x + ahead * x_step;
-        e = 0.0f;
         if (r + ahead * groups < a.rows) {
 #pragma unroll
             for (int v = 0; v < kVecs; ++v)
                 if (at.has(v))
                     ring.copy(stage, 0, v, row + v * kStride);
-            if (at.has_edge())
-                e = detail::load1(row + edge);
         }
         commit_copies();
     };
+    auto edge_of = [&](const T* row, bool live) {
+        return live && at.has_edge() ? detail::load1(row + edge) : 0.0f;
+    };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i)
-        fetch(i, i, next_edge[i]);
+        fetch(i, i);
+    float next_edge = edge_of(x, r < a.rows);
 
     float2 w[kVecs][kP<T>], b[kVecs][kP<T>];
 #pragma unroll
@@ -88,11 +88,8 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
     // every thread takes part in every sum: the rows past the end are empty
     for (int64_t block_r = first; block_r < a.rows; block_r += groups) {
         const bool live = r < a.rows;
-        fetch(stage == 0 ? kStages - 1 : stage - 1, kStages - 1, next_edge[kStages - 1]);
-        float fe = next_edge[0];
-#pragma unroll
-        for (int i = 0; i + 1 < kStages; ++i)
-            next_edge[i] = next_edge[i + 1];
+        fetch(stage == 0 ? kStages - 1 : stage - 1, kStages - 1);
+        float fe = next_edge;
         wait_copies<kStages - 1>();
         float2 f[kVecs][kP<T>];
         float2 sums = make_float2(fe, 0.0f);
@@ -110,6 +107,9 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
         stage = stage + 1 == kStages ? 0 : stage + 1;
         float total[1] = {sums.x + sums.y};
         group_sum<kGroup>(total, slots, turn);
+        // asked for after this row's was used: the wait for a load is one for
+        // all that the same instruction has asked for
+        next_edge = edge_of(x + x_step, r + groups < a.rows);
         const float mean = total[0] * inv;
         fe = at.has_edge() ? fe - mean : 0.0f;
         float2 squares = make_float2(fe * fe, 0.0f);
@@ -228,6 +228,20 @@ int launch_one(const LnForward& a, int sm_count, cudaStream_t s)
     return int(cudaGetLastError());
 }
 
+template <typename T, int G, int U>
+int launch_aligned(const LnForward& a, int sm_count, cudaStream_t s)
+{
+    return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, s)
+                               : launch_one<T, G, U, kAligned>(a, sm_count, s);
+}
+template <typename T, int G, int U>
+int launch_ragged(const LnForward& a, int sm_count, cudaStream_t s)
+{
+    return rows_alike(a.x, a.x_stride, a.y, a.y_stride, sizeof(T))
+               ? launch_one<T, G, U, kRagged>(a, sm_count, s)
+               : launch_one<T, G, U, kShifted>(a, sm_count, s);
+}
+
 template <typename T>
 int launch_typed(const LnForward& a, int sm_count, cudaStream_t s)
 {
@@ -238,15 +252,25 @@ int launch_typed(const LnForward& a, int sm_count, cudaStream_t s)
     }
     const bool aligned = a.cols % kE<T> == 0 && rows_aligned(a.x, a.x_stride, sizeof(T)) &&
                          rows_aligned(a.y, a.y_stride, sizeof(T));
+    // Where the backward pass's layouts are not the forward pass's best.  Four
+    // vectors of float32 a thread rather than eight: 16384 x 4096 83 and 96 us,
+    // 8192 x 8192 90 and 96 (2500 columns: 66 and 61; up to 2048 and from 4097
+    // to 6144: no gain).  Ragged rows of 16-bit types in more groups of fewer
+    // threads, which hide the first warp's head and tail: 32768 x 2047 54 and 66
+    // us (whole vectors: 50 and 46).
+    if constexpr (sizeof(T) == 4) {
+        if (aligned && a.cols > 2816 && a.cols <= 4096)
+            return launch_aligned<T, 256, 2>(a, sm_count, s);
+        if (aligned && a.cols > 6144 && a.cols <= 8192)
+            return launch_aligned<T, 512, 2>(a, sm_count, s);
+    } else if (!aligned && a.cols > 1024 && a.cols <= 2048) {
+        return launch_ragged<T, 64, 4>(a, sm_count, s);
+    }
     return with_layout(a.cols, aligned, [&](auto layout) {
         constexpr int G = decltype(layout)::kGroup, U = decltype(layout)::kUnits;
         constexpr int R = G > 8 ? G : 16;  // lanes for head and tail
-        if (!aligned)
-            return rows_alike(a.x, a.x_stride, a.y, a.y_stride, sizeof(T))
-                       ? launch_one<T, R, U, kRagged>(a, sm_count, s)
-                       : launch_one<T, R, U, kShifted>(a, sm_count, s);
-        return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, s)
-                                   : launch_one<T, G, U, kAligned>(a, sm_count, s);
+        return aligned ? launch_aligned<T, G, U>(a, sm_count, s)
+                       : launch_ragged<T, R, U>(a, sm_count, s);
     });
 }
 

@@ -136,6 +136,16 @@ def test_wide_rows(kind, cols):
     run(9, cols, kind, "f32", seed=cols)
 
 
+# both sides of the forward pass's own borders between layouts
+@pytest.mark.parametrize("kind,cols", [("f32", 2816), ("f32", 2820), ("f32", 2823), ("f32", 4092),
+                                       ("f32", 4100), ("f32", 6144), ("f32", 6148), ("f32", 8188),
+                                       ("bf16", 1026), ("bf16", 1499), ("f16", 1999), ("bf16", 2047),
+                                       ("bf16", 2050)])
+def test_forward_layouts(kind, cols):
+    run(45, cols, kind, "f32", seed=cols)
+    run(45, cols, kind, "f32", seed=cols, pad=(13, 13, 0))
+
+
 # rows that are looked at several times
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("cols", [24_576, 24_577, 65_528, 65_536, 65_537, 81_920, 131_071, 131_072,
