@@ -55,7 +55,7 @@ inline int list_norm_blocks(int32_t n_units)
     return n_units < 1 ? 1 : n_units > kNormBlocksMax ? kNormBlocksMax : n_units;
 }
 
-// Per-block partial sums of g^2 over the list (one double per block).
+// Per-block partial sums of g^2 over the list (8 bytes per block).
 int launch_list_norm(const ListView& list, int32_t g_dtype, double* partials, void* stream);
 // The update of the units with 32-bit (plain) and with 8-bit states; k.fin
 // finishes the norm from the partials.  key: the random numbers' key of this

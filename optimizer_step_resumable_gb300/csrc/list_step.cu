@@ -12,8 +12,8 @@
 // update with a 16-bit gradient and weight copy: 28 with 32-bit states (w 8,
 // m and v 16, g 2, copy 2), 16.06 with 8-bit ones (w 8, m and v 4, scales
 // 16/256, g 2, copy 2); the norm reads g once more.  On GB300, 110M
-// parameters in 196 tensors: 493 us and 326 us a step (the copy's bandwidth
-// would take 489 and 294 for these bytes); 570M in 8 bits 1607 us (1523).  The
+// parameters in 196 tensors: 492 us and 325 us a step (the copy's bandwidth
+// would take 489 and 294 for these bytes); 570M in 8 bits 1612 us (1523).  The
 // norm kernel's share is 46 us: 33 for g, the rest for writing back what the
 // step before left in L2.
 #include <cstdint>
@@ -42,23 +42,98 @@ constexpr int kLane = kBlockElems / 32;  // elements of a block per lane
 // The norm.
 // ---------------------------------------------------------------------------
 
+// A sum of two floats, hi the rounded one: 48 bits.  Binary64 additions run at
+// 1/64 of float32's rate: with them a third of the norm kernel's time went into
+// a thread's sums, and joining the threads' and the blocks' sums took 1 to 2 us
+// of every step (a million elements in 8 bits: 14.5 us, not 12.4).
+struct Sum2 {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum2 add(Sum2 a, Sum2 b)
+{
+    const float s = __fadd_rn(a.hi, b.hi);
+    const float back = __fsub_rn(s, a.hi);
+    // s + e is the exact sum of the his
+    const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, back)), __fsub_rn(b.hi, back));
+    const float lo = __fadd_rn(e, __fadd_rn(a.lo, b.lo));
+    const float hi = __fadd_rn(s, lo);
+    return Sum2{hi, __fsub_rn(lo, __fsub_rn(hi, s))};
+}
+
+// A partial sum of squares, in 8 bytes: a Sum2 or, with the top bit set, a
+// binary64 number, for what float32 does not hold.
+__device__ __forceinline__ uint2 pack(Sum2 s)
+{
+    return make_uint2(__float_as_uint(s.lo), __float_as_uint(s.hi));
+}
+__device__ __forceinline__ uint2 pack(double d)
+{
+    return make_uint2(uint32_t(__double2loint(d)), uint32_t(__double2hiint(d)) | 0x80000000u);
+}
+__device__ __forceinline__ bool is_double(uint2 p) { return p.y >> 31; }
+__device__ __forceinline__ Sum2 sum_of(uint2 p)
+{
+    return Sum2{__uint_as_float(p.y), __uint_as_float(p.x)};
+}
+__device__ __forceinline__ double value_of(uint2 p)
+{
+    return is_double(p) ? __hiloint2double(int(p.y & 0x7fffffffu), int(p.x))
+                        : double(__uint_as_float(p.y)) + double(__uint_as_float(p.x));
+}
+// The sum over the first kLanes lanes of a warp, in lane 0.  more, and its
+// binary64 share, where any lane has one.
+template <int kLanes>
+__device__ __forceinline__ uint2 warp_sum(Sum2 s, bool more, double share)
+{
+    if (__any_sync(0xffffffffu, more)) {
+        share += double(s.hi) + double(s.lo);
+#pragma unroll
+        for (int d = kLanes / 2; d > 0; d >>= 1)
+            share += __shfl_down_sync(0xffffffffu, share, d);
+        return pack(share);
+    }
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1)
+        s = add(s, Sum2{__shfl_down_sync(0xffffffffu, s.hi, d),
+                        __shfl_down_sync(0xffffffffu, s.lo, d)});
+    return pack(s);
+}
+// The sum over a block, in thread 0; called once in a kernel.
+template <int kThreads>
+__device__ __forceinline__ uint2 block_sum(Sum2 s, bool more, double share)
+{
+    constexpr int kWarps = kThreads / 32;
+    __shared__ uint2 warps[kWarps];
+    const int lane = threadIdx.x & 31;
+    uint2 p = warp_sum<32>(s, more, share);
+    if (lane == 0)
+        warps[threadIdx.x >> 5] = p;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        p = lane < kWarps ? warps[lane] : make_uint2(0u, 0u);
+        more = is_double(p);
+        p = warp_sum<kWarps>(more ? Sum2{0.0f, 0.0f} : sum_of(p), more, more ? value_of(p) : 0.0);
+    }
+    return p;
+}
+
 // Level 1 of the norm.  Block b takes the contiguous units [U b / P,
 // U (b + 1) / P), tensor by tensor: within a tensor it streams, with no table
 // between two loads.  Each thread has two sets of kSet loads, one on the way
-// while the other is summed: a run of normdev::run_sumsq, added to a sum of
-// two floats (48 bits; binary64 additions run at 1/64 of the rate and took a
-// third of the kernel's time).  Default L2 priority: the update reads g next.
+// while the other is summed: a run of normdev::run_sumsq.  Default L2
+// priority: the update reads g next.
 template <typename G>
 __global__ void __launch_bounds__(kNormThreads, 4)
-    k_list_norm(ListView list, double* __restrict__ partials)
+    k_list_norm(ListView list, uint2* __restrict__ partials)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kSet = sizeof(G) == 2 ? 4 : 2;
     constexpr int kTile = kNormThreads * kLane;  // elements of the block's one load
     const int32_t lo = int32_t(int64_t(list.n_units) * blockIdx.x / gridDim.x);
     const int32_t hi = int32_t(int64_t(list.n_units) * (blockIdx.x + 1) / gridDim.x);
-    double acc = 0.0;
-    float sum_hi = 0.0f, sum_lo = 0.0f;
+    Sum2 acc{0.0f, 0.0f};
+    bool more = false;  // runs that float32 does not hold
+    double share = 0.0;
     for (int32_t u = lo; u < hi;) {
         const ListUnit unit = list.units[u];
         const ListTensor& t = list.tensors[unit.tensor];
@@ -75,8 +150,12 @@ __global__ void __launch_bounds__(kNormThreads, 4)
         auto load = [&](detail::Raw8<G>(&to)[kSet]) {
 #pragma unroll
             for (int p = 0; p < kSet; ++p, i += kTile)
-                to[p] = aligned && end - i >= kLane ? detail::load8_cg(g + i)
-                                                    : detail::load8_part(g + i, end - i);
+                if (aligned && end - i >= kLane)
+                    to[p] = detail::load8_cg(g + i);
+                else if (end > i)
+                    to[p] = detail::load8_part(g + i, end - i);
+                else
+                    to[p] = detail::Raw8<G>{};
         };
         auto sum = [&](const detail::Raw8<G>(&from)[kSet], int32_t begin) {
             if (begin + int32_t(threadIdx.x) * kLane >= end)
@@ -86,15 +165,18 @@ __global__ void __launch_bounds__(kNormThreads, 4)
             for (int p = 0; p < kSet; ++p)
                 detail::widen8(from[p], y[2 * p], y[2 * p + 1]);
             float r;
-            if (normdev::run_sumsq_fast<2 * kSet>(y, r) && r <= 0x1p100f) {
-                // sum + part is the exact sum of the runs but for 2^-24 of part
-                const float next = __fadd_rn(sum_hi, r);
-                const float back = __fsub_rn(next, sum_hi);
-                sum_lo = __fadd_rn(sum_lo, __fadd_rn(__fsub_rn(sum_hi, __fsub_rn(next, back)),
+            if (normdev::run_sumsq_fast<2 * kSet>(y, r) && r <= 0x1p80f) {  // below 2^128 in all
+                const float next = __fadd_rn(acc.hi, r);
+                const float back = __fsub_rn(next, acc.hi);
+                acc.lo = __fadd_rn(acc.lo, __fadd_rn(__fsub_rn(acc.hi, __fsub_rn(next, back)),
                                                      __fsub_rn(r, back)));
-                sum_hi = next;
+                acc.hi = next;
             } else {
-                acc += normdev::run_sumsq<2 * kSet>(y);
+                const double d = normdev::run_sumsq<2 * kSet>(y);
+                if (__double2hiint(d) | __double2loint(d)) {  // not a run of zeros
+                    share += d;
+                    more = true;
+                }
             }
         };
         load(x[0]);
@@ -108,9 +190,9 @@ __global__ void __launch_bounds__(kNormThreads, 4)
                 sum(x[1], done + kSpan);
         }
     }
-    acc = detail::block_sum<kNormThreads>(acc + (double(sum_hi) + double(sum_lo)));
+    const uint2 p = block_sum<kNormThreads>(acc, more, share);
     if (threadIdx.x == 0)
-        partials[blockIdx.x] = acc;
+        partials[blockIdx.x] = p;
 }
 
 // ---------------------------------------------------------------------------
@@ -440,11 +522,21 @@ __global__ void __launch_bounds__(kStepThreads, 4)
         }
         if (i == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            double total = 0.0;
-            for (int q = threadIdx.x; q < k.fin.nparts; q += kStepThreads)
-                total += __ldcg(k.fin.partials + q);
-            total = detail::block_sum<kStepThreads>(total);
+            Sum2 sum{0.0f, 0.0f};
+            bool more = false;
+            double share = 0.0;
+            for (int q = threadIdx.x; q < k.fin.nparts; q += kStepThreads) {
+                const uint2 p = __ldcg(reinterpret_cast<const uint2*>(k.fin.partials) + q);
+                if (is_double(p)) {
+                    share += value_of(p);
+                    more = true;
+                } else {
+                    sum = add(sum, sum_of(p));
+                }
+            }
+            const uint2 all = block_sum<kStepThreads>(sum, more, share);
             if (threadIdx.x == 0) {
+                const double total = value_of(all);
                 const bool mine = publish && blockIdx.x == 0;
                 const NormResult r = normdev::make_result(total, k.fin.clip, k.fin.grad_scale,
                                                           mine ? k.fin.d_res->seq + 1u : 0u);
@@ -532,12 +624,13 @@ int launch_list_norm(const ListView& list, int32_t g_dtype, double* partials, vo
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int blocks = list_norm_blocks(list.n_units);
+    uint2* const p = reinterpret_cast<uint2*>(partials);
     if (g_dtype == kDtypeBF16)
-        k_list_norm<__nv_bfloat16><<<blocks, kNormThreads, 0, s>>>(list, partials);
+        k_list_norm<__nv_bfloat16><<<blocks, kNormThreads, 0, s>>>(list, p);
     else if (g_dtype == kDtypeF16)
-        k_list_norm<__half><<<blocks, kNormThreads, 0, s>>>(list, partials);
+        k_list_norm<__half><<<blocks, kNormThreads, 0, s>>>(list, p);
     else
-        k_list_norm<float><<<blocks, kNormThreads, 0, s>>>(list, partials);
+        k_list_norm<float><<<blocks, kNormThreads, 0, s>>>(list, p);
     return int(cudaGetLastError());
 }
 
