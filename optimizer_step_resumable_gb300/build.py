@@ -43,7 +43,7 @@ def _sources():
                                                  "norm_dev.cuh", "adamw_dev.cuh", "api_util.h",
                                                  "list.h", "state8_dev.cuh", "layernorm.h",
                                                  "layernorm_dev.cuh", "layernorm_bwd.cuh",
-                                                 "packed_dev.cuh")]
+                                                 "packed_dev.cuh", "early_dev.cuh")]
             + [os.path.join(INCLUDE, "adamw_ckpt.h")])
 
 

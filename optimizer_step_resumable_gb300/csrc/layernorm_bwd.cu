@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "early_dev.cuh"
 #include "layernorm.h"
 
 namespace osr {
@@ -21,7 +22,8 @@ constexpr int kCols = 32, kSlices = 32;  // of a block
 // 0: dweight, 1: dbias.
 __global__ void __launch_bounds__(kCols * kSlices) k_ln_grads(LnGrads g)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    detail::wait_before();
+    detail::go_ahead();
     __shared__ float sums[kSlices][kCols];
     const int lane = threadIdx.x % kCols, slice = threadIdx.x / kCols;
     const int c = blockIdx.x * kCols + lane;
@@ -69,16 +71,8 @@ int launch_ln_backward(const LnBackward& a, int32_t dtype, int sm_count, int32_t
 
 int launch_ln_grads(const LnGrads& g, void* stream)
 {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(detail::ceil_div(g.cols, kCols)), 2);
-    cfg.blockDim = dim3(kCols * kSlices);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return int(cudaLaunchKernelEx(&cfg, &k_ln_grads, g));
+    return detail::launch_early(&k_ln_grads, dim3(unsigned(detail::ceil_div(g.cols, kCols)), 2),
+                                kCols * kSlices, 0, static_cast<cudaStream_t>(stream), g);
 }
 
 }  // namespace osr

@@ -13,8 +13,8 @@
 // and k_ln_grads (layernorm_bwd.cu) joins the blocks' shares in a fixed order.
 // (A second kernel's many blocks are faster at it than the last block of the
 // first: 14.5 against 23.8 us for 8192 x 768 bf16.)  On GB300 65536 x 4096
-// bf16 takes 242 us, 6.6 TB/s; 5003 x 1021 float32, whose rows start anywhere,
-// 19 us, of which the second kernel and its wait are 5.
+// bf16 takes 240 us, 6.7 TB/s; 5003 x 1021 float32, whose rows start anywhere,
+// 17 us, of which the second kernel and its wait are 5.
 #pragma once
 
 #include <cstdint>
@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kBackwardBlocks<kGroup
     constexpr int kGroups = kThreads / kGroup;
     constexpr int kVecs = kUnits * 8 / kE<T>;
     constexpr int kPairs = kP<T>;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    detail::wait_before();
+    detail::go_ahead();
     extern __shared__ __align__(16) unsigned char raw[];
     const BackwardRing<T, kGroup, kUnits> ring{reinterpret_cast<uint4*>(raw)};
     constexpr int kStages = BackwardRing<T, kGroup, kUnits>::kDepth;
@@ -305,7 +306,7 @@ constexpr int kColumnThreads = 128, kAtOnce = 4;  // rows on their way
 template <typename T>
 __global__ void __launch_bounds__(kColumnThreads) k_ln_columns_wide(LnBackward a)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    detail::go_ahead();
     const int vector = blockIdx.x * kColumnThreads + threadIdx.x;
     const int64_t first = blockIdx.y;
     const T* x = static_cast<const T*>(a.x) + first * a.x_stride;
@@ -381,8 +382,7 @@ int launch_one(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s
         most = ln_parts_max(a.cols);
     const int64_t blocks = row_blocks(a.rows, kThreads / G, most);
     *parts = int32_t(blocks);
-    kernel<<<unsigned(blocks), kThreads, kSmem, s>>>(a);
-    return int(cudaGetLastError());
+    return detail::launch_early(kernel, dim3(unsigned(blocks)), kThreads, kSmem, s, a);
 }
 
 }  // namespace

@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "early_dev.cuh"
 #include "layernorm.h"
 #include "packed_dev.cuh"
 

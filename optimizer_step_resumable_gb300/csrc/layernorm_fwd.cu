@@ -5,8 +5,7 @@
 // variance for the backward pass.  HBM-bound: every element is read once and
 // written once; the mean and then the squares of the differences are summed
 // from registers, so the variance loses nothing to cancellation.  On GB300
-// 65536 x 4096 bf16 takes 171 us, 6.3 TB/s; 8192 x 768 7.7 us and one token 4.2,
-// of which 2 are a launch.
+// 65536 x 4096 bf16 takes 168 us, 6.4 TB/s; 8192 x 768 6.2 us and one token 2.7.
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -37,6 +36,8 @@ __global__ void __launch_bounds__(kBlockThreads<kGroup>, (kForwardBlocks<kGroup,
     constexpr int kThreads = kBlockThreads<kGroup>;
     constexpr int kGroups = kThreads / kGroup;
     constexpr int kVecs = kUnits * 8 / kE<T>;
+    detail::wait_before();
+    detail::go_ahead();
     extern __shared__ __align__(16) unsigned char raw[];
     const ForwardRing<T, kGroup, kUnits> ring{reinterpret_cast<uint4*>(raw)};
     constexpr int kStages = ForwardRing<T, kGroup, kUnits>::kDepth;
@@ -224,8 +225,7 @@ int launch_one(const LnForward& a, int sm_count, cudaStream_t s)
     auto* const kernel = &k_ln_forward<T, G, U, kRows>;
     static const int cap = resident_blocks(kernel, kThreads, kSmem);
     const int64_t blocks = row_blocks(a.rows, kThreads / G, int64_t(cap) * sm_count);
-    kernel<<<unsigned(blocks), kThreads, kSmem, s>>>(a);
-    return int(cudaGetLastError());
+    return detail::launch_early(kernel, dim3(unsigned(blocks)), kThreads, kSmem, s, a);
 }
 
 template <typename T, int G, int U>

@@ -12,8 +12,8 @@
 // update with a 16-bit gradient and weight copy: 28 with 32-bit states (w 8,
 // m and v 16, g 2, copy 2), 16.06 with 8-bit ones (w 8, m and v 4, scales
 // 16/256, g 2, copy 2); the norm reads g once more.  On GB300, 110M
-// parameters in 196 tensors: 492 us and 325 us a step (the copy's bandwidth
-// would take 489 and 294 for these bytes); 570M in 8 bits 1612 us (1523).  The
+// parameters in 196 tensors: 490 us and 325 us a step (the copy's bandwidth
+// would take 489 and 294 for these bytes); 570M in 8 bits 1620 us (1523).  The
 // norm kernel's share is 46 us: 33 for g, the rest for writing back what the
 // step before left in L2.
 #include <cstdint>
@@ -23,6 +23,7 @@
 
 #include "adamw_dev.cuh"
 #include "common.cuh"
+#include "early_dev.cuh"
 #include "list.h"
 #include "norm_dev.cuh"
 #include "state8_dev.cuh"
@@ -126,7 +127,6 @@ template <typename G>
 __global__ void __launch_bounds__(kNormThreads, 4)
     k_list_norm(ListView list, uint2* __restrict__ partials)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kSet = sizeof(G) == 2 ? 4 : 2;
     constexpr int kTile = kNormThreads * kLane;  // elements of the block's one load
     const int32_t lo = int32_t(int64_t(list.n_units) * blockIdx.x / gridDim.x);
@@ -141,6 +141,10 @@ __global__ void __launch_bounds__(kNormThreads, 4)
         const int32_t units = (left - 1) / kUnitElems + 1;  // to the tensor's end
         const int32_t mine = units < hi - u ? units : hi - u;
         const int32_t end = mine < units ? mine * kUnitElems : left;
+        if (u == lo) {  // the tables are no kernel's output
+            detail::wait_before();
+            detail::go_ahead();
+        }
         u += mine;
         const G* const g = static_cast<const G*>(t.g) + e0;
         const bool aligned = t.flags & kListVec;
@@ -190,6 +194,8 @@ __global__ void __launch_bounds__(kNormThreads, 4)
                 sum(x[1], done + kSpan);
         }
     }
+    if (lo == hi)
+        detail::wait_before();
     const uint2 p = block_sum<kNormThreads>(acc, more, share);
     if (threadIdx.x == 0)
         partials[blockIdx.x] = p;
@@ -521,7 +527,8 @@ __global__ void __launch_bounds__(kStepThreads, 4)
             }
         }
         if (i == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+            detail::wait_before();
+            detail::go_ahead();
             Sum2 sum{0.0f, 0.0f};
             bool more = false;
             double share = 0.0;
@@ -586,19 +593,12 @@ int launch_step_typed(const ListView& list, int32_t w_lp_dtype, const StepScalar
     static const int per_sm = detail::resident_blocks(reinterpret_cast<const void*>(kernel),
                                                       kStepThreads, 1, &err);
     const int32_t most = per_sm * sm_count;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(list.n_units < 1 ? 1 : list.n_units > most ? most : list.n_units));
-    cfg.blockDim = dim3(kStepThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     StepScalars kk = k;
     if (int64_t(list.n_units) * kUnitElems < kDynamicChunksMinN)
         kk.chunk_ctr = nullptr;
-    return int(cudaLaunchKernelEx(&cfg, kernel, list, kk, key, publish, zero_grad, w_lp_dtype));
+    const int32_t blocks = list.n_units < 1 ? 1 : list.n_units > most ? most : list.n_units;
+    return detail::launch_early(kernel, dim3(unsigned(blocks)), kStepThreads, 0, s, list, kk, key,
+                                publish, zero_grad, w_lp_dtype);
 }
 
 template <typename G>
@@ -624,14 +624,15 @@ int launch_list_norm(const ListView& list, int32_t g_dtype, double* partials, vo
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int blocks = list_norm_blocks(list.n_units);
-    uint2* const p = reinterpret_cast<uint2*>(partials);
+    auto launch = [&](void (*kernel)(ListView, uint2*)) {
+        return detail::launch_early(kernel, dim3(unsigned(blocks)), kNormThreads, 0, s, list,
+                                    reinterpret_cast<uint2*>(partials));
+    };
     if (g_dtype == kDtypeBF16)
-        k_list_norm<__nv_bfloat16><<<blocks, kNormThreads, 0, s>>>(list, p);
-    else if (g_dtype == kDtypeF16)
-        k_list_norm<__half><<<blocks, kNormThreads, 0, s>>>(list, p);
-    else
-        k_list_norm<float><<<blocks, kNormThreads, 0, s>>>(list, p);
-    return int(cudaGetLastError());
+        return launch(&k_list_norm<__nv_bfloat16>);
+    if (g_dtype == kDtypeF16)
+        return launch(&k_list_norm<__half>);
+    return launch(&k_list_norm<float>);
 }
 
 int launch_list_step(const ListView& plain, const ListView& eight, int32_t g_dtype,

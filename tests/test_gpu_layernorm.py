@@ -283,6 +283,69 @@ def test_same_bits_every_time():
             assert all(torch.equal(a, b) for a, b in zip(first, now))
 
 
+def chained(wait, steps=6, rows=300, cols=768):
+    """Forward, backward and list step in a chain where each reads what the one
+    before wrote; `wait`: with the device idle between any two."""
+    torch.manual_seed(3)
+    x = torch.randn(rows, cols, device="cuda").bfloat16()
+    w, b = torch.ones(cols, device="cuda"), torch.zeros(cols, device="cuda")
+    dw, db = torch.zeros(cols, device="cuda"), torch.zeros(cols, device="cuda")
+    state = [[torch.zeros(cols, device="cuda") for _ in range(2)] for _ in range(2)]
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    rest = torch.cuda.synchronize if wait else lambda: None
+    with osr.layernorm_create(cols) as ln, osr.adamw_list_create([w, b], [dw, db], *state) as lst:
+        rest()
+        for t in range(1, steps + 1):
+            osr.layernorm_forward(ln, x, w, b, y=y, mean=mean, rstd=rstd)
+            rest()
+            osr.layernorm_forward(ln, y, w, b, y=x, mean=mean, rstd=rstd)
+            rest()
+            osr.layernorm_backward(ln, x, y, w, mean, rstd, dx=dx, dweight=dw, dbias=db,
+                                   accumulate=True)
+            rest()
+            osr.layernorm_backward(ln, dx, y, w, mean, rstd, dx=x, dweight=dw, dbias=db,
+                                   accumulate=True)
+            rest()
+            osr.adamw_list_step(lst, t, 1e-2, 0.1, 1.0, zero_grad=t % 2 == 0)
+            rest()
+    return [x, y, dx, w, b, dw, db, mean, rstd] + state[0] + state[1]
+
+
+def test_kernels_in_a_row_wait_for_one_another():
+    """A kernel is set up while the one before it still runs."""
+    want = chained(True)
+    for _ in range(5):
+        for got, ref in zip(chained(False), want):
+            assert torch.equal(got, ref)
+
+
+def test_captured_calls():
+    want = chained(True, steps=1)
+    x, w, b = (t.clone() for t in (want[0], want[3], want[4]))
+    y, mean, rstd = torch.empty_like(x), *(torch.empty(300, device="cuda") for _ in range(2))
+    dx, dw, db = torch.empty_like(x), torch.zeros_like(w), torch.zeros_like(b)
+
+    def passes(ln):
+        osr.layernorm_forward(ln, x, w, b, y=y, mean=mean, rstd=rstd)
+        osr.layernorm_backward(ln, y, x, w, mean, rstd, dx=dx, dweight=dw, dbias=db)
+
+    with osr.layernorm_create(768) as ln:
+        passes(ln)
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (y, mean, rstd, dx, dw, db)]
+        for t in (y, mean, rstd, dx, dw, db):
+            t.zero_()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            passes(ln)
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip((y, mean, rstd, dx, dw, db), want):
+            assert torch.equal(got, ref)
+
+
 def test_no_rows():
     for cols in (768, 20_000):
         x = torch.empty(0, cols, device="cuda")
