@@ -430,7 +430,8 @@ __device__ __forceinline__ void store_block(const ListTensor& t, int32_t i, int3
 // adds the norm's partials up in the same fixed order (the same bits
 // everywhere; block 0 of the kernel that runs first publishes the result),
 // as the fused kernel of the flat state does.  The first unit's inputs are
-// asked for before that: the norm kernel writes none of them.
+// asked for before that: the norm kernel writes none of them, and all before
+// it has completed when it lets this one go ahead.
 //
 // A block takes one unit after another, a warp of it one block of elements.
 // Its first warp keeps the tables ahead of it through shared memory: in the
