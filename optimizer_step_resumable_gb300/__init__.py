@@ -703,12 +703,12 @@ def layernorm_destroy(ln: LayerNorm):
 # tensor once (60 to 200 ns each) and make no calls of their own unless one
 # fails.
 
-def _rows(t, ln: LayerNorm, name: str):
+def _rows(t, shape, ln: LayerNorm, name: str):
     """(address, row stride, rows) of a tensor of shape (..., cols) whose rows
-    are evenly spaced."""
+    are evenly spaced; shape: the tensor's."""
     cols = ln.cols
-    if t.get_device() != ln.device or t.dim() < 1 or t.shape[-1] != cols:
-        if not t.is_cuda or t.dim() < 1 or t.shape[-1] != cols:
+    if t.get_device() != ln.device or not shape or shape[-1] != cols:
+        if not t.is_cuda or not shape or shape[-1] != cols:
             raise TypeError(f"{name} must be a CUDA tensor of shape (..., {cols})")
         _same_device(t, name, ln)
     if t.is_contiguous():
@@ -753,7 +753,7 @@ _DTYPES = {}  # torch dtype -> DTYPE_*
 
 def _code(t) -> int:
     code = _DTYPES.get(t.dtype)
-    if code is None:
+    if code is None:  # the first call
         import torch
         _DTYPES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
                         torch.float16: DTYPE_F16})
@@ -767,17 +767,18 @@ def layernorm_forward(ln: LayerNorm, x, weight=None, bias=None, eps: float = 1e-
                       mean=None, rstd=None, stream=None):
     """(y, mean, rstd) of the rows of x (..., cols); outputs not given are
     allocated.  weight and bias: float32 or the type of x; None: 1 and 0."""
-    xp, xs, rows = _rows(x, ln, "x")
-    code = _code(x)
+    shape, kind = x.shape, x.dtype
+    xp, xs, rows = _rows(x, shape, ln, "x")
+    code = _DTYPES.get(kind) or _code(x)
     if y is None or mean is None or rstd is None:
         import torch
         new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
-        y = new(x.shape, x.dtype) if y is None else y
-        mean = new(x.shape[:-1], torch.float32) if mean is None else mean
-        rstd = new(x.shape[:-1], torch.float32) if rstd is None else rstd
-    if y.dtype is not x.dtype or y.shape != x.shape:
+        y = new(shape, kind) if y is None else y
+        mean = new(shape[:-1], torch.float32) if mean is None else mean
+        rstd = new(shape[:-1], torch.float32) if rstd is None else rstd
+    if y.dtype is not kind or y.shape != shape:
         raise TypeError("y must have the type and shape of x")
-    yp, ys, _ = _rows(y, ln, "y")
+    yp, ys, _ = _rows(y, shape, ln, "y")
     wp = bp = None
     w_code = DTYPE_F32
     if weight is not None:
@@ -800,16 +801,16 @@ def layernorm_backward(ln: LayerNorm, dy, x, weight, mean, rstd, dx=None, dweigh
     """(dx, dweight, dbias) from the gradient dy of y and the forward pass's
     x, mean, rstd; dx is allocated if not given, dweight and dbias are
     computed if given.  accumulate: add into dweight and dbias."""
-    xp, xs, rows = _rows(x, ln, "x")
-    code = _code(x)
+    kind, shape = x.dtype, x.shape
+    xp, xs, rows = _rows(x, shape, ln, "x")
+    code = _DTYPES.get(kind) or _code(x)
     if dx is None:
         import torch
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    kind, shape = x.dtype, x.shape
+        dx = torch.empty(shape, dtype=kind, device=x.device)
     if dy.dtype is not kind or dx.dtype is not kind or dy.shape != shape or dx.shape != shape:
         raise TypeError("dy and dx must have the type and shape of x")
-    gp, gs, _ = _rows(dy, ln, "dy")
-    dp, ds, _ = _rows(dx, ln, "dx")
+    gp, gs, _ = _rows(dy, shape, ln, "dy")
+    dp, ds, _ = _rows(dx, shape, ln, "dx")
     wp = dwp = dbp = None
     w_code = g_code = DTYPE_F32
     if weight is not None:
