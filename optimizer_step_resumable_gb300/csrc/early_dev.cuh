@@ -11,7 +11,8 @@ namespace detail {
 // when that one has completed, and go_ahead lets the next such kernel be set
 // up.  Every kernel that calls go_ahead has waited first (or was launched in
 // plain order): so when one starts, all but the one directly before it have
-// completed.  Back to back, a plain launch costs about 2 us more on GB300: the
+// completed.  What any of them wrote is visible to it only after its own wait:
+// before that it reads nothing that a kernel writes.  Back to back, a plain launch costs about 2 us more on GB300: the
 // layer norm of one token 4.2 us and 2.7, of 8192 x 768 bf16 8.3 and 6.2, a list
 // of 400,000 elements 10.3 and 7.4.
 __device__ __forceinline__ void go_ahead()

@@ -429,9 +429,11 @@ __device__ __forceinline__ void store_block(const ListTensor& t, int32_t i, int3
 // The update of the list's units of one kind of state.  Every block first
 // adds the norm's partials up in the same fixed order (the same bits
 // everywhere; block 0 of the kernel that runs first publishes the result),
-// as the fused kernel of the flat state does.  The first unit's inputs are
-// asked for before that: the norm kernel writes none of them, and all before
-// it has completed when it lets this one go ahead.
+// as the fused kernel of the flat state does, while its first unit's inputs
+// are on their way.  Before the wait only the tables are read, which no kernel
+// writes: that the kernels before the norm have completed when this one starts
+// does not make what they wrote (w, m, v, g, the counters) visible to it; its
+// own wait does.
 //
 // A block takes one unit after another, a warp of it one block of elements.
 // Its first warp keeps the tables ahead of it through shared memory: in the
@@ -517,6 +519,10 @@ __global__ void __launch_bounds__(kStepThreads, 4)
         const bool any = unit >= 0 && left + lane * kLane > 0;
         float w[kLane], g[kLane];
         Moments<k8> x;
+        if (i == 0) {
+            detail::wait_before();
+            detail::go_ahead();
+        }
         if (any)
             load_block<G, k8>(t, e, left, vec, w, g, x);
         if (threadIdx.x < 32 && unit >= 0) {
@@ -528,8 +534,6 @@ __global__ void __launch_bounds__(kStepThreads, 4)
             }
         }
         if (i == 0) {
-            detail::wait_before();
-            detail::go_ahead();
             Sum2 sum{0.0f, 0.0f};
             bool more = false;
             double share = 0.0;

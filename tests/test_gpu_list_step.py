@@ -502,6 +502,32 @@ def test_on_another_stream_and_in_a_graph():
         assert a.bytes() == b.bytes()
 
 
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("g", ["f32", "bf16"])
+@pytest.mark.parametrize("eight", [(0, 0, 0, 0), (1, 1, 1, 1), (0, 1, 0, 1)])
+def test_steps_in_a_row_wait_for_one_another(eight, g, shift):
+    """Every step reads what the one before and the kernel between them wrote,
+    in every block's first unit and in the later ones: the bytes of a run with
+    the device idle between any two calls."""
+    sizes = [5_000_000, 70_001, 3, 5_000_003]
+
+    def steps(rest):
+        st = State(sizes, 13, g, eight, shift, copy="bf16")
+        with st.make() as lst:
+            for t in range(1, 7):
+                rest()
+                osr.adamw_list_step(lst, t, LR, WD, 0.5, seed=t)
+                rest()
+                if t % 2:
+                    for x in st.g:
+                        x.mul_(-0.75)
+        return st.bytes()
+
+    want = steps(torch.cuda.synchronize)
+    for _ in range(2):
+        assert steps(lambda: None) == want
+
+
 def test_nothing_outside_the_tensors_is_written():
     """Sentinels before and after every array of odd-sized tensors."""
     n, pad = 1283, 64
