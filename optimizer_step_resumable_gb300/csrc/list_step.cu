@@ -16,6 +16,7 @@
 // would take 489 and 294 for these bytes); 570M in 8 bits 1620 us (1523).  The
 // norm kernel's share is 46 us: 33 for g, the rest for writing back what the
 // step before left in L2.
+#include <cfloat>
 #include <cstdint>
 #include <type_traits>
 
@@ -265,28 +266,36 @@ __device__ __forceinline__ void load_block(const ListTensor& t, int32_t i, int32
     }
 }
 
-// adamw_elem with a shorter way for moments that have died away (rows no token
-// has touched for hundreds of steps) or never lived: the correctly rounded
-// square root and quotient take a slow path for zeros and subnormal numbers
-// (an update of such a state took 232 us, not 188).  The approximate ones, to
-// 2^-23, change the denominator by less than 2^-70 and the update by less than
-// 2^-120 / denom: w gets the same bits unless eps or w itself is as small.
+// When an update cannot be seen in w.  |m| < tiny makes it at most `most`
+// whatever v is: with u = round(step_size round(m / denom)), denom >= eps,
+// every step monotone, most = round(step_size round(2^-100 / eps)).  tiny is
+// 2^-100, or 0 where that bound is no number (eps = 0).
+struct Unseen {
+    float tiny, most;
+};
+
+// adamw_elem's bits, without its root and quotient for moments that have died
+// away (rows no token has touched for hundreds of steps) or never lived: those
+// two take a slow path for zeros and subnormal numbers (110M parameters of
+// dead m, or of zeros: 598 and 504 us, not 492).  If w d - most and w d + most round to the same
+// number, so does w d - u for every u between; for m = 0, u is 0.
 __device__ __forceinline__ void adamw_elem_any(float& w, float g, float& m, float& v, float s,
-                                               const StepScalars& k, float d)
+                                               const StepScalars& k, float d, const Unseen& un)
 {
     const float gh = __fmul_rn(g, s);
     const float m1 = __fmaf_rn(k.beta1, m, __fmul_rn(k.omb1, gh));
     const float v1 = __fmaf_rn(k.beta2, v, __fmul_rn(__fmul_rn(k.omb2, gh), gh));
-    if (fabsf(m1) < 0x1p-100f || v1 < 0x1p-96f) {
-        float root;
-        asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v1));
-        const float denom = __fmaf_rn(root, k.inv_sqrt_bc2, k.eps);
-        w = __fmaf_rn(w, d, -__fmul_rn(k.step_size, __fdividef(m1, denom)));
-        m = m1;
-        v = v1;
-    } else {
-        adamwdev::adamw_elem(w, g, m, v, s, k, d);
+    if (fabsf(m1) < un.tiny && v1 >= 0.0f) {
+        const float most = m1 == 0.0f ? 0.0f : un.most;
+        const float low = __fmaf_rn(w, d, -most), high = __fmaf_rn(w, d, most);
+        if (__float_as_uint(low) == __float_as_uint(high)) {
+            w = low;
+            m = m1;
+            v = v1;
+            return;
+        }
     }
+    adamwdev::adamw_elem(w, g, m, v, s, k, d);
 }
 
 // The update of a block, in registers.  8-bit states: m, v become the new
@@ -294,15 +303,17 @@ __device__ __forceinline__ void adamw_elem_any(float& w, float g, float& m, floa
 // leaves the block's largest values alone.
 __device__ __forceinline__ void update_block(const ListTensor&, int32_t, float (&w)[kLane],
                                              const float (&g)[kLane], Moments<false>& x, float s,
-                                             const StepScalars& k, float d, uint32_t)
+                                             const StepScalars& k, float d, uint32_t,
+                                             const Unseen& un)
 {
 #pragma unroll
     for (int j = 0; j < kLane; ++j)
-        adamw_elem_any(w[j], g[j], x.m[j], x.v[j], s, k, d);
+        adamw_elem_any(w[j], g[j], x.m[j], x.v[j], s, k, d, un);
 }
 __device__ __forceinline__ void update_block(const ListTensor& t, int32_t i, float (&w)[kLane],
                                              const float (&g)[kLane], Moments<true>& x, float s,
-                                             const StepScalars& k, float d, uint32_t key)
+                                             const StepScalars& k, float d, uint32_t key,
+                                             const Unseen&)
 {
     // A scale is a power of two, so beta times the scale times the value is
     // rounded as beta times the widened value is.
@@ -460,8 +471,8 @@ __device__ __forceinline__ void copy_async(void* to, const void* from)
 
 template <typename G, bool k8>
 __global__ void __launch_bounds__(kStepThreads, 4)
-    k_list_step(ListView list, StepScalars k, uint32_t key, bool publish, bool zero_grad,
-                int32_t w_lp_dtype)
+    k_list_step(ListView list, StepScalars k, Unseen un, uint32_t key, bool publish,
+                bool zero_grad, int32_t w_lp_dtype)
 {
     const int lane = threadIdx.x & 31;
     const int32_t lane_e0 = int32_t(threadIdx.x >> 5) * kBlockElems + lane * kLane;
@@ -565,7 +576,8 @@ __global__ void __launch_bounds__(kStepThreads, 4)
         if (unit < 0)
             break;
         if (any) {
-            update_block(t, e, w, g, x, s, k, (t.flags & kListDecay) ? k.decay : 1.0f, key);
+            update_block(t, e, w, g, x, s, k, (t.flags & kListDecay) ? k.decay : 1.0f, key,
+                         un);
             store_block<G, k8>(t, e, left, vec, w, x, zero_grad, w_lp_dtype);
             if constexpr (k8) {
                 if (lane == 0) {
@@ -602,8 +614,10 @@ int launch_step_typed(const ListView& list, int32_t w_lp_dtype, const StepScalar
     if (int64_t(list.n_units) * kUnitElems < kDynamicChunksMinN)
         kk.chunk_ctr = nullptr;
     const int32_t blocks = list.n_units < 1 ? 1 : list.n_units > most ? most : list.n_units;
-    return detail::launch_early(kernel, dim3(unsigned(blocks)), kStepThreads, 0, s, list, kk, key,
-                                publish, zero_grad, w_lp_dtype);
+    const float bound = k.step_size * (0x1p-100f / k.eps);
+    const Unseen un{bound <= FLT_MAX ? 0x1p-100f : 0.0f, bound};
+    return detail::launch_early(kernel, dim3(unsigned(blocks)), kStepThreads, 0, s, list, kk, un,
+                                key, publish, zero_grad, w_lp_dtype);
 }
 
 template <typename G>
