@@ -731,6 +731,7 @@ ADAMW_API int ckpt_sha256_backend(void);
  * of (seed, t, 256 B_k + i), B_k the number of blocks of the tensors before
  * it: the same seed, steps and inputs give the same bytes, so a run resumed
  * from copies of w, m, v and the scales continues bit for bit.
+ * An eps above 0 and below 2^-126 counts as 2^-126 here.
  * Errors: ADAMW_EINVAL, ADAMW_ECUDA, ADAMW_ESTATE (a step before the arrays
  * are bound), ADAMW_ENONFINITE (adamw_list_last_norm).
  */

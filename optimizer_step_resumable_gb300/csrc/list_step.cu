@@ -628,6 +628,9 @@ int launch_step(const ListView& plain, const ListView& eight, int32_t w_lp_dtype
     // own counters
     StepScalars k8 = k;
     k8.chunk_ctr = k.chunk_ctr + 2;
+    // state8::weight takes a subnormal denominator for 0, and 0 / 0 would be NaN
+    if (k8.eps > 0.0f && k8.eps < FLT_MIN)
+        k8.eps = FLT_MIN;
     int e = cudaSuccess;
     if (plain.n_units > 0 || eight.n_units == 0)
         e = launch_step_typed<G, false>(plain, w_lp_dtype, k, key, true, zero_grad, sm_count, s);

@@ -468,6 +468,26 @@ def test_hyperparameters():
         assert float((st.w[0].double() - want).abs().max()) <= 1e-6 * LR + 2.0 ** -24 * 0.2
 
 
+@pytest.mark.parametrize("eps", [1e-45, 1e-42, 1e-39, 1.1e-38, 2e-38])
+@pytest.mark.parametrize("eight", [0, 1])
+def test_eps_below_the_normal_numbers(eight, eps):
+    """An element that never had a gradient has m = v = 0 and keeps its decayed
+    weight, as 0 / eps is 0 for any eps above 0."""
+    n = 600
+    st = State([n], 5, eight=[eight])
+    st.g[0][::2] = 0.0
+    if not eight:
+        st.m[0].zero_()
+        st.v[0].zero_()
+    w = st.w[0].clone()
+    with st.make() as lst:
+        osr.adamw_list_set_hparams(lst, B1, B2, eps)
+        osr.adamw_list_step(lst, 1, LR, WD, float("inf"))
+    assert torch.equal(st.w[0][::2], w[::2] * float(np.float32(1 - LR * WD)))
+    step = (st.w[0][1::2].double() - w[1::2].double() * (1 - LR * WD)).abs()
+    assert float((step - LR).abs().max()) <= 1e-6 * LR + 2.0 ** -24 * 0.2
+
+
 @pytest.mark.parametrize("sizes", [[], [0], [0, 0, 0]])
 def test_lists_without_elements(sizes):
     st = State(sizes, 1)
