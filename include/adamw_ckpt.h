@@ -759,9 +759,9 @@ ADAMW_API int adamw_list_last_norm(adamw_list* list, double* norm_out, float* sc
  * and, for the gradient dy of y, with xhat = (x - mean) rstd, a = dy weight:
  *   dx = rstd (a - sum(a) / cols - xhat sum(a xhat) / cols)
  *   dweight = sum over rows of dy xhat;  dbias = sum over rows of dy.
- * Statistics, sums and products are float32 (the variance from the
- * differences, in a second look at the row in registers); inputs are widened
- * exactly and each output is rounded once.
+ * Statistics, sums and products are float32 (the variance and the mean's last
+ * bits from the differences, in a second look at the row in registers); inputs
+ * are widened exactly and each output is rounded once.
  *
  * layernorm_create: for rows of cols elements, 1 <= cols <= 2^18; owns the
  *   backward pass's partial sums (the only allocation), so calls of

@@ -274,9 +274,11 @@ constexpr int stages_for(int stage_bytes, int blocks, int want, int most)
 // The sums of kCount values over a group, in a fixed order, in every thread.
 // `slots` (groups of a block): the warps' sums, two sets used in turn, so that
 // one barrier per call is enough.
-template <int kGroup, int kCount>
-__device__ __forceinline__ void group_sum(float (&s)[kCount], float (*slots)[kCount][16], int& turn)
+template <int kGroup, int kCount, int kMost>
+__device__ __forceinline__ void group_sum(float (&s)[kCount], float (&slots)[2][kMost][16],
+                                          int& turn)
 {
+    static_assert(kCount <= kMost, "a slot for each sum");
     constexpr int kLanes = kGroup < 32 ? kGroup : 32;
 #pragma unroll
     for (int d = kLanes / 2; d > 0; d >>= 1)
@@ -298,6 +300,25 @@ __device__ __forceinline__ void group_sum(float (&s)[kCount], float (*slots)[kCo
         }
         turn ^= 1;
     }
+}
+
+// The statistics of a row from a first mean and, of the differences d from it,
+// their sum and the sum of their squares.  The first mean errs by up to a few
+// 2^-24 of mean |x|, which moves every difference and adds its square to the
+// variance; but the differences are exact where that error matters, so their
+// mean e is what the first mean lacks.  xhat = d rstd + shift.
+struct Statistics {
+    float mean, rstd, shift;
+};
+__device__ __forceinline__ Statistics statistics_of(float mean, const float (&d)[2], float inv,
+                                                    float eps)
+{
+    float e = d[0] * inv;
+    if (!(fabsf(e) < __uint_as_float(0x7f800000u)))
+        e = 0.0f;  // the sums' infinities and NaNs say it all
+    const float var = __fmaf_rn(-e, e, d[1] * inv);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn((var < 0.0f ? 0.0f : var) + eps));
+    return Statistics{mean + e, rstd, -e * rstd};
 }
 
 template <int kGroup>
