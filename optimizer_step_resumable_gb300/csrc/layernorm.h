@@ -2,6 +2,7 @@
 // its kernels share.  Not part of the ABI.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include "internal.h"
@@ -64,10 +65,20 @@ inline int64_t ln_partials(int32_t cols)
     return int64_t(parts) * 2 * cols;
 }
 
-int launch_ln_forward(const LnForward& a, int32_t dtype, int sm_count, void* stream);
+// Resident blocks per SM of the kernels of one pass, on the context's device
+// and for its cols, which leave one kernel for each element type and way the
+// rows lie (layernorm_dev.cuh); 0: not asked for yet, so the kernel may not
+// have been allowed its shared memory on this device either.
+constexpr int kLnDtypes = 3, kLnRows = 5;
+struct LnBlocks {
+    std::atomic<int> per_sm[kLnDtypes][kLnRows] = {};
+};
+
+int launch_ln_forward(const LnForward& a, int32_t dtype, int sm_count, LnBlocks& known,
+                      void* stream);
 // Writes dx and, if a.sums, *parts partial sums.
-int launch_ln_backward(const LnBackward& a, int32_t dtype, int sm_count, int32_t* parts,
-                       void* stream);
+int launch_ln_backward(const LnBackward& a, int32_t dtype, int sm_count, LnBlocks& known,
+                       int32_t* parts, void* stream);
 int launch_ln_grads(const LnGrads& g, void* stream);
 
 }  // namespace osr

@@ -15,6 +15,7 @@ struct layernorm_ctx {
     int sm_count = 0;
     int32_t cols = 0;
     float* d_partials = nullptr;
+    osr::LnBlocks forward, backward;
 };
 
 namespace {
@@ -144,7 +145,7 @@ int layernorm_forward(layernorm_ctx* ctx, const void* d_x, int64_t x_stride, int
     const osr::LnForward a{d_x,    x_stride, d_weight, d_bias, d_y,        y_stride,
                            d_mean, d_rstd,   rows,     ctx->cols, float(eps),
                            w_dtype == ADAMW_DTYPE_F32};
-    const int e = osr::launch_ln_forward(a, x_dtype, ctx->sm_count, stream);
+    const int e = osr::launch_ln_forward(a, x_dtype, ctx->sm_count, ctx->forward, stream);
     return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "layer norm launch");
 }
 
@@ -180,7 +181,7 @@ int layernorm_backward(layernorm_ctx* ctx, const void* d_dy, int64_t dy_stride, 
         const osr::LnBackward a{d_dy,   dy_stride, d_x,       x_stride, d_weight,
                                 d_mean, d_rstd,    d_dx,      dx_stride, rows,
                                 ctx->cols, w_dtype == ADAMW_DTYPE_F32, sums, ctx->d_partials};
-        e = osr::launch_ln_backward(a, x_dtype, ctx->sm_count, &parts, stream);
+        e = osr::launch_ln_backward(a, x_dtype, ctx->sm_count, ctx->backward, &parts, stream);
     }
     if (e == cudaSuccess && sums)
         e = osr::launch_ln_grads(osr::LnGrads{ctx->d_partials, parts, ctx->cols, d_dweight,

@@ -11,7 +11,8 @@
 namespace osr {
 
 template <typename T>
-int launch_ln_backward_typed(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s);
+int launch_ln_backward_typed(const LnBackward& a, int sm_count, std::atomic<int>* known,
+                             int32_t* parts, cudaStream_t s);
 
 namespace {
 
@@ -58,15 +59,15 @@ __global__ void __launch_bounds__(kCols * kSlices) k_ln_grads(LnGrads g)
 
 }  // namespace
 
-int launch_ln_backward(const LnBackward& a, int32_t dtype, int sm_count, int32_t* parts,
-                       void* stream)
+int launch_ln_backward(const LnBackward& a, int32_t dtype, int sm_count, LnBlocks& known,
+                       int32_t* parts, void* stream)
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == kDtypeBF16)
-        return launch_ln_backward_typed<__nv_bfloat16>(a, sm_count, parts, s);
+        return launch_ln_backward_typed<__nv_bfloat16>(a, sm_count, known.per_sm[dtype], parts, s);
     if (dtype == kDtypeF16)
-        return launch_ln_backward_typed<__half>(a, sm_count, parts, s);
-    return launch_ln_backward_typed<float>(a, sm_count, parts, s);
+        return launch_ln_backward_typed<__half>(a, sm_count, known.per_sm[dtype], parts, s);
+    return launch_ln_backward_typed<float>(a, sm_count, known.per_sm[dtype], parts, s);
 }
 
 int launch_ln_grads(const LnGrads& g, void* stream)

@@ -371,13 +371,17 @@ __global__ void __launch_bounds__(kColumnThreads) k_ln_columns_wide(LnBackward a
 }
 
 template <typename T, int G, int U, Rows kRows>
-int launch_one(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s)
+int launch_one(const LnBackward& a, int sm_count, std::atomic<int>* known, int32_t* parts,
+               cudaStream_t s)
 {
     constexpr int kThreads = kBlockThreads<G>;
     constexpr int kSmem = BackwardRing<T, G, U>::kBytes;
     auto* const kernel = &k_ln_backward<T, G, U, kRows>;
-    static const int cap = resident_blocks(kernel, kThreads, kSmem);
-    int64_t most = int64_t(cap) * sm_count;
+    int per_sm = 0;
+    const cudaError_t e = resident_blocks(kernel, kThreads, kSmem, known[kRows], &per_sm);
+    if (e != cudaSuccess)
+        return int(e);
+    int64_t most = int64_t(per_sm) * sm_count;
     if (most > ln_parts_max(a.cols))
         most = ln_parts_max(a.cols);
     const int64_t blocks = row_blocks(a.rows, kThreads / G, most);
@@ -388,7 +392,8 @@ int launch_one(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s
 }  // namespace
 
 template <typename T>
-int launch_ln_backward_typed(const LnBackward& a, int sm_count, int32_t* parts, cudaStream_t s)
+int launch_ln_backward_typed(const LnBackward& a, int sm_count, std::atomic<int>* known,
+                             int32_t* parts, cudaStream_t s)
 {
     if (a.cols > kLnRegisterCols) {
         const int64_t most = int64_t(sm_count) * 4;
@@ -411,12 +416,12 @@ int launch_ln_backward_typed(const LnBackward& a, int sm_count, int32_t* parts, 
         constexpr int R = G > 8 ? G : 16;  // lanes for head and tail
         if (!aligned)
             return !rows_alike(a.x, a.x_stride, a.dy, a.dy_stride, sizeof(T))
-                       ? launch_one<T, R, U, kMixed>(a, sm_count, parts, s)
+                       ? launch_one<T, R, U, kMixed>(a, sm_count, known, parts, s)
                    : rows_alike(a.x, a.x_stride, a.dx, a.dx_stride, sizeof(T))
-                       ? launch_one<T, R, U, kRagged>(a, sm_count, parts, s)
-                       : launch_one<T, R, U, kShifted>(a, sm_count, parts, s);
-        return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, parts, s)
-                                   : launch_one<T, G, U, kAligned>(a, sm_count, parts, s);
+                       ? launch_one<T, R, U, kRagged>(a, sm_count, known, parts, s)
+                       : launch_one<T, R, U, kShifted>(a, sm_count, known, parts, s);
+        return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, known, parts, s)
+                                   : launch_one<T, G, U, kAligned>(a, sm_count, known, parts, s);
     });
 }
 

@@ -3,6 +3,7 @@
 
 namespace osr {
 
-template int launch_ln_backward_typed<__half>(const LnBackward&, int, int32_t*, cudaStream_t);
+template int launch_ln_backward_typed<__half>(const LnBackward&, int, std::atomic<int>*, int32_t*,
+                                             cudaStream_t);
 
 }  // namespace osr

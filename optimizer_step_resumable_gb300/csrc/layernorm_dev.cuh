@@ -101,6 +101,7 @@ __device__ __forceinline__ int head_of(const T* p)
 // elsewhere than x; it is cut anew in shared memory.  kMixed: dy too, which
 // then is read element by element.
 enum Rows { kFull, kAligned, kRagged, kShifted, kMixed };
+static_assert(kMixed < kLnRows, "a place in LnBlocks for each");
 
 // Which columns a thread holds: vectors at column(v) = start + v kStride, and
 // (from kRagged on) one element of the head or the tail at edge, or -1.
@@ -449,17 +450,28 @@ int with_layout(int cols, bool aligned, F f)
     return f(Layout<512, 4>());
 }
 
-// Resident blocks of a kernel per SM, which is allowed its shared memory
-// first.
+// Resident blocks of a kernel per SM of the current device, which is allowed
+// its shared memory there first.  Only an answer is kept in `known`.
 template <typename F>
-inline int resident_blocks(F* kernel, int threads, int smem)
+inline cudaError_t resident_blocks(F* kernel, int threads, int smem, std::atomic<int>& known,
+                                   int* per_sm)
 {
-    int n = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess)
-        return 1;
-    return n < 1 ? 1 : n;
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+        if (e == cudaSuccess && n < 1)
+            return cudaErrorLaunchOutOfResources;
+        if (e != cudaSuccess) {
+            cudaGetLastError();  // returned here, not by a later call
+            return e;
+        }
+        known.store(n, std::memory_order_relaxed);
+    }
+    *per_sm = n;
+    return cudaSuccess;
 }
 
 // Blocks for `rows` rows, of `most` at once: the groups step by a multiple of

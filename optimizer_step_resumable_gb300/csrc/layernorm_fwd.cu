@@ -228,32 +228,35 @@ __global__ void __launch_bounds__(kWideThreads, 2) k_ln_forward_wide(LnForward a
 }
 
 template <typename T, int G, int U, Rows kRows>
-int launch_one(const LnForward& a, int sm_count, cudaStream_t s)
+int launch_one(const LnForward& a, int sm_count, std::atomic<int>* known, cudaStream_t s)
 {
     constexpr int kThreads = kBlockThreads<G>;
     constexpr int kSmem = ForwardRing<T, G, U>::kBytes;
     auto* const kernel = &k_ln_forward<T, G, U, kRows>;
-    static const int cap = resident_blocks(kernel, kThreads, kSmem);
-    const int64_t blocks = row_blocks(a.rows, kThreads / G, int64_t(cap) * sm_count);
+    int per_sm = 0;
+    const cudaError_t e = resident_blocks(kernel, kThreads, kSmem, known[kRows], &per_sm);
+    if (e != cudaSuccess)
+        return int(e);
+    const int64_t blocks = row_blocks(a.rows, kThreads / G, int64_t(per_sm) * sm_count);
     return detail::launch_early(kernel, dim3(unsigned(blocks)), kThreads, kSmem, s, a);
 }
 
 template <typename T, int G, int U>
-int launch_aligned(const LnForward& a, int sm_count, cudaStream_t s)
+int launch_aligned(const LnForward& a, int sm_count, std::atomic<int>* known, cudaStream_t s)
 {
-    return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, s)
-                               : launch_one<T, G, U, kAligned>(a, sm_count, s);
+    return a.cols == G * U * 8 ? launch_one<T, G, U, kFull>(a, sm_count, known, s)
+                               : launch_one<T, G, U, kAligned>(a, sm_count, known, s);
 }
 template <typename T, int G, int U>
-int launch_ragged(const LnForward& a, int sm_count, cudaStream_t s)
+int launch_ragged(const LnForward& a, int sm_count, std::atomic<int>* known, cudaStream_t s)
 {
     return rows_alike(a.x, a.x_stride, a.y, a.y_stride, sizeof(T))
-               ? launch_one<T, G, U, kRagged>(a, sm_count, s)
-               : launch_one<T, G, U, kShifted>(a, sm_count, s);
+               ? launch_one<T, G, U, kRagged>(a, sm_count, known, s)
+               : launch_one<T, G, U, kShifted>(a, sm_count, known, s);
 }
 
 template <typename T>
-int launch_typed(const LnForward& a, int sm_count, cudaStream_t s)
+int launch_typed(const LnForward& a, int sm_count, std::atomic<int>* known, cudaStream_t s)
 {
     if (a.cols > kLnRegisterCols) {
         const int64_t most = int64_t(sm_count) * 4;
@@ -270,30 +273,31 @@ int launch_typed(const LnForward& a, int sm_count, cudaStream_t s)
     // us (whole vectors: 50 and 46).
     if constexpr (sizeof(T) == 4) {
         if (aligned && a.cols > 2816 && a.cols <= 4096)
-            return launch_aligned<T, 256, 2>(a, sm_count, s);
+            return launch_aligned<T, 256, 2>(a, sm_count, known, s);
         if (aligned && a.cols > 6144 && a.cols <= 8192)
-            return launch_aligned<T, 512, 2>(a, sm_count, s);
+            return launch_aligned<T, 512, 2>(a, sm_count, known, s);
     } else if (!aligned && a.cols > 1024 && a.cols <= 2048) {
-        return launch_ragged<T, 64, 4>(a, sm_count, s);
+        return launch_ragged<T, 64, 4>(a, sm_count, known, s);
     }
     return with_layout(a.cols, aligned, [&](auto layout) {
         constexpr int G = decltype(layout)::kGroup, U = decltype(layout)::kUnits;
         constexpr int R = G > 8 ? G : 16;  // lanes for head and tail
-        return aligned ? launch_aligned<T, G, U>(a, sm_count, s)
-                       : launch_ragged<T, R, U>(a, sm_count, s);
+        return aligned ? launch_aligned<T, G, U>(a, sm_count, known, s)
+                       : launch_ragged<T, R, U>(a, sm_count, known, s);
     });
 }
 
 }  // namespace
 
-int launch_ln_forward(const LnForward& a, int32_t dtype, int sm_count, void* stream)
+int launch_ln_forward(const LnForward& a, int32_t dtype, int sm_count, LnBlocks& known,
+                      void* stream)
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == kDtypeBF16)
-        return launch_typed<__nv_bfloat16>(a, sm_count, s);
+        return launch_typed<__nv_bfloat16>(a, sm_count, known.per_sm[dtype], s);
     if (dtype == kDtypeF16)
-        return launch_typed<__half>(a, sm_count, s);
-    return launch_typed<float>(a, sm_count, s);
+        return launch_typed<__half>(a, sm_count, known.per_sm[dtype], s);
+    return launch_typed<float>(a, sm_count, known.per_sm[dtype], s);
 }
 
 }  // namespace osr

@@ -57,12 +57,18 @@ inline int list_norm_blocks(int32_t n_units)
 
 // Per-block partial sums of g^2 over the list (8 bytes per block).
 int launch_list_norm(const ListView& list, int32_t g_dtype, double* partials, void* stream);
+// Blocks that the current device keeps resident, of the update of each kind
+// of state.
+struct ListBlocks {
+    int32_t plain, eight;
+};
+int list_step_blocks(int32_t g_dtype, int sm_count, ListBlocks* most);
 // The update of the units with 32-bit (plain) and with 8-bit states; k.fin
 // finishes the norm from the partials.  key: the random numbers' key of this
 // step (8-bit states).
 int launch_list_step(const ListView& plain, const ListView& eight, int32_t g_dtype,
                      int32_t w_lp_dtype, const StepScalars& k, uint32_t key, bool zero_grad,
-                     int sm_count, void* stream);
+                     const ListBlocks& most, void* stream);
 
 // The 32-bit hash behind the random rounding: xor-shifts and odd
 // multipliers, each invertible, so distinct words stay distinct.

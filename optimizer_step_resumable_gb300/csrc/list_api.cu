@@ -32,6 +32,7 @@ struct adamw_list {
     cudaEvent_t ev_norm = nullptr;
     bool bound = false, launched = false;
     int32_t g_dtype = ADAMW_DTYPE_F32, w_lp_dtype = ADAMW_DTYPE_BF16;
+    osr::ListBlocks most{};  // of the bound g_dtype's kernels
 
     static constexpr size_t kHead = 256;
     osr::NormResult* d_res() const { return reinterpret_cast<osr::NormResult*>(d_scratch); }
@@ -200,7 +201,15 @@ int bind_list(adamw_list* l, float* const* d_w, void* const* d_g, int32_t g_dtyp
         if (ranges[i].begin < ranges[i - 1].end)
             return fail(ADAMW_EINVAL, "%s[%d] overlaps %s[%d]", ranges[i].name, ranges[i].tensor,
                         ranges[i - 1].name, ranges[i - 1].tensor);
+    osr::ListBlocks most;
+    {
+        DeviceScope scope(l->device);
+        const int e = osr::list_step_blocks(g_dtype, l->sm_count, &most);
+        if (e != cudaSuccess)
+            return cuda_fail(cudaError_t(e), "the update's blocks per SM");
+    }
     l->bound = false;
+    l->most = most;
     l->tensors.swap(table);
     const int rc = upload(l);
     if (rc != ADAMW_OK)
@@ -331,7 +340,7 @@ int adamw_list_step(adamw_list* list, int32_t t, double lr, double wd, double cl
     if (e == cudaSuccess)
         e = osr::launch_list_step(plain, eight, list->g_dtype, list->w_lp_dtype, k,
                                   osr::rounding_key(seed, t), (flags & ADAMW_ZERO_GRAD) != 0,
-                                  list->sm_count, stream);
+                                  list->most, stream);
     if (e != cudaSuccess)
         return cuda_fail(cudaError_t(e), "list step launch");
     // for adamw_list_last_norm; a captured step is not one the host can wait for

@@ -601,15 +601,24 @@ __global__ void __launch_bounds__(kStepThreads, 4)
     }
 }
 
+template <typename G>
+int blocks_typed(int sm_count, ListBlocks* most)
+{
+    cudaError_t e = cudaSuccess;
+    most->plain = detail::resident_blocks(reinterpret_cast<const void*>(&k_list_step<G, false>),
+                                          kStepThreads, sm_count, &e);
+    most->eight = detail::resident_blocks(reinterpret_cast<const void*>(&k_list_step<G, true>),
+                                          kStepThreads, sm_count, &e);
+    if (e != cudaSuccess)
+        cudaGetLastError();  // returned here, not by a later call
+    return int(e);
+}
+
 template <typename G, bool k8>
 int launch_step_typed(const ListView& list, int32_t w_lp_dtype, const StepScalars& k,
-                      uint32_t key, bool publish, bool zero_grad, int sm_count, cudaStream_t s)
+                      uint32_t key, bool publish, bool zero_grad, int32_t most, cudaStream_t s)
 {
     auto* const kernel = &k_list_step<G, k8>;
-    cudaError_t err = cudaSuccess;
-    static const int per_sm = detail::resident_blocks(reinterpret_cast<const void*>(kernel),
-                                                      kStepThreads, 1, &err);
-    const int32_t most = per_sm * sm_count;
     StepScalars kk = k;
     if (int64_t(list.n_units) * kUnitElems < kDynamicChunksMinN)
         kk.chunk_ctr = nullptr;
@@ -622,7 +631,8 @@ int launch_step_typed(const ListView& list, int32_t w_lp_dtype, const StepScalar
 
 template <typename G>
 int launch_step(const ListView& plain, const ListView& eight, int32_t w_lp_dtype,
-                const StepScalars& k, uint32_t key, bool zero_grad, int sm_count, cudaStream_t s)
+                const StepScalars& k, uint32_t key, bool zero_grad, const ListBlocks& most,
+                cudaStream_t s)
 {
     // a list without elements still publishes its norm; each kernel has its
     // own counters
@@ -633,10 +643,11 @@ int launch_step(const ListView& plain, const ListView& eight, int32_t w_lp_dtype
         k8.eps = FLT_MIN;
     int e = cudaSuccess;
     if (plain.n_units > 0 || eight.n_units == 0)
-        e = launch_step_typed<G, false>(plain, w_lp_dtype, k, key, true, zero_grad, sm_count, s);
+        e = launch_step_typed<G, false>(plain, w_lp_dtype, k, key, true, zero_grad,
+                                        most.plain, s);
     if (e == cudaSuccess && eight.n_units > 0)
         e = launch_step_typed<G, true>(eight, w_lp_dtype, k8, key, plain.n_units == 0, zero_grad,
-                                       sm_count, s);
+                                       most.eight, s);
     return e;
 }
 
@@ -657,16 +668,25 @@ int launch_list_norm(const ListView& list, int32_t g_dtype, double* partials, vo
     return launch(&k_list_norm<float>);
 }
 
+int list_step_blocks(int32_t g_dtype, int sm_count, ListBlocks* most)
+{
+    if (g_dtype == kDtypeBF16)
+        return blocks_typed<__nv_bfloat16>(sm_count, most);
+    if (g_dtype == kDtypeF16)
+        return blocks_typed<__half>(sm_count, most);
+    return blocks_typed<float>(sm_count, most);
+}
+
 int launch_list_step(const ListView& plain, const ListView& eight, int32_t g_dtype,
                      int32_t w_lp_dtype, const StepScalars& k, uint32_t key, bool zero_grad,
-                     int sm_count, void* stream)
+                     const ListBlocks& most, void* stream)
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (g_dtype == kDtypeBF16)
-        return launch_step<__nv_bfloat16>(plain, eight, w_lp_dtype, k, key, zero_grad, sm_count, s);
+        return launch_step<__nv_bfloat16>(plain, eight, w_lp_dtype, k, key, zero_grad, most, s);
     if (g_dtype == kDtypeF16)
-        return launch_step<__half>(plain, eight, w_lp_dtype, k, key, zero_grad, sm_count, s);
-    return launch_step<float>(plain, eight, w_lp_dtype, k, key, zero_grad, sm_count, s);
+        return launch_step<__half>(plain, eight, w_lp_dtype, k, key, zero_grad, most, s);
+    return launch_step<float>(plain, eight, w_lp_dtype, k, key, zero_grad, most, s);
 }
 
 }  // namespace osr
