@@ -775,8 +775,9 @@ ADAMW_API int adamw_list_last_norm(adamw_list* list, double* norm_out, float* sc
  *   rounded once;
  *   LAYERNORM_ACCUMULATE adds the sum to what is there, in float32.
  *   rows = 0 is accepted: dweight and dbias become 0 (or stay, accumulating).
- * Every array must be aligned to its elements; outputs must not overlap
- * inputs.  Rows whose arrays all start at the same place within 16 bytes are
+ * Every array must be aligned to its elements; no output may share a byte
+ * with an input or another output (ADAMW_EINVAL; rows that lie between one
+ * another do not).  Rows whose arrays all start at the same place within 16 bytes are
  * read and written in vectors, whatever that place is; an output that differs
  * from x costs a pass through shared memory, and a dy that does is read
  * element by element.

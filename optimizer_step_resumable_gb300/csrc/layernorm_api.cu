@@ -75,6 +75,75 @@ int check_rows(const void* p, int64_t stride, int64_t rows, int32_t cols, size_t
     return ADAMW_OK;
 }
 
+// `rows` pieces of `bytes` each, `stride` bytes apart (0 for a single one); a
+// vector is one piece.
+struct Pieces {
+    uintptr_t begin;
+    int64_t stride, rows, bytes;
+    const char* name;
+};
+Pieces rows_of(const void* p, int64_t stride, int64_t rows, int64_t cols, size_t size,
+               const char* name)
+{
+    return Pieces{reinterpret_cast<uintptr_t>(p), rows > 1 ? stride * int64_t(size) : 0, rows,
+                  cols * int64_t(size), name};
+}
+Pieces vector_of(const void* p, int64_t n, size_t size, const char* name)
+{
+    return Pieces{reinterpret_cast<uintptr_t>(p), 0, p && n ? 1 : 0, n * int64_t(size), name};
+}
+
+// Whether a piece of `bytes` at `begin` shares a byte with some row of b.
+bool touches(uintptr_t begin, int64_t bytes, const Pieces& b)
+{
+    // the last row that starts before the piece's end
+    const int64_t before = int64_t(begin - b.begin) + bytes - 1;
+    if (before < 0)
+        return false;
+    int64_t j = b.rows > 1 ? before / b.stride : 0;
+    j = j < b.rows ? j : b.rows - 1;
+    return j * b.stride + b.bytes > int64_t(begin - b.begin);
+}
+// Whether any byte belongs to both.  Rows of two arrays may lie between one
+// another (columns of one matrix), so the ranges alone do not say.
+bool overlap(const Pieces& a, const Pieces& b)
+{
+    if (a.rows == 0 || b.rows == 0)
+        return false;
+    const uintptr_t a_end = a.begin + uintptr_t((a.rows - 1) * a.stride + a.bytes);
+    const uintptr_t b_end = b.begin + uintptr_t((b.rows - 1) * b.stride + b.bytes);
+    if (a.begin >= b_end || b.begin >= a_end)
+        return false;
+    const Pieces &few = a.rows < b.rows ? a : b, &many = a.rows < b.rows ? b : a;
+    // rows as far apart as the other's lie alike to it: the first that is
+    // within the other's range, and the one before it, stand for all
+    const bool alike = few.rows > 1 && few.stride == many.stride;
+    int64_t i = 0, end = few.rows;
+    if (alike) {
+        const int64_t ahead = int64_t(many.begin - few.begin);
+        i = ahead > 0 ? ahead / few.stride : 0;
+        end = i + 2 < end ? i + 2 : end;
+    }
+    for (; i < end; ++i)
+        if (touches(few.begin + uintptr_t(i * few.stride), few.bytes, many))
+            return true;
+    return false;
+}
+// Outputs share no byte with an input or with one another.
+template <int kOut, int kIn>
+int check_apart(const Pieces (&out)[kOut], const Pieces (&in)[kIn])
+{
+    for (int i = 0; i < kOut; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j]))
+                return fail(ADAMW_EINVAL, "%s overlaps %s", out[i].name, out[j].name);
+        for (int j = 0; j < kIn; ++j)
+            if (overlap(out[i], in[j]))
+                return fail(ADAMW_EINVAL, "%s overlaps %s", out[i].name, in[j].name);
+    }
+    return ADAMW_OK;
+}
+
 int check_common(const layernorm_ctx* ctx, int32_t x_dtype, int32_t w_dtype, int64_t rows)
 {
     if (!ctx)
@@ -139,6 +208,15 @@ int layernorm_forward(layernorm_ctx* ctx, const void* d_x, int64_t x_stride, int
         return rc;
     if (!(eps >= 0.0 && std::isfinite(eps)))
         return fail(ADAMW_EINVAL, "eps=%g must be finite and >= 0", eps);
+    const int64_t cols = ctx->cols;
+    const Pieces out[] = {rows_of(d_y, y_stride, rows, cols, s, "d_y"),
+                          vector_of(d_mean, rows, 4, "d_mean"),
+                          vector_of(d_rstd, rows, 4, "d_rstd")};
+    const Pieces in[] = {rows_of(d_x, x_stride, rows, cols, s, "d_x"),
+                         vector_of(d_weight, cols, ws, "d_weight"),
+                         vector_of(d_bias, cols, ws, "d_bias")};
+    if ((rc = check_apart(out, in)))
+        return rc;
     if (rows == 0)
         return ADAMW_OK;
     DeviceScope scope(ctx->device);
@@ -172,6 +250,17 @@ int layernorm_backward(layernorm_ctx* ctx, const void* d_dy, int64_t dy_stride, 
         (rc = check_array(d_rstd, 4, rows == 0, "d_rstd")) ||
         (rc = check_array(d_dweight, gs, true, "d_dweight")) ||
         (rc = check_array(d_dbias, gs, true, "d_dbias")))
+        return rc;
+    const int64_t cols = ctx->cols;
+    const Pieces out[] = {rows_of(d_dx, dx_stride, rows, cols, s, "d_dx"),
+                          vector_of(d_dweight, cols, gs, "d_dweight"),
+                          vector_of(d_dbias, cols, gs, "d_dbias")};
+    const Pieces in[] = {rows_of(d_dy, dy_stride, rows, cols, s, "d_dy"),
+                         rows_of(d_x, x_stride, rows, cols, s, "d_x"),
+                         vector_of(d_weight, cols, size_of(w_dtype), "d_weight"),
+                         vector_of(d_mean, rows, 4, "d_mean"),
+                         vector_of(d_rstd, rows, 4, "d_rstd")};
+    if ((rc = check_apart(out, in)))
         return rc;
     DeviceScope scope(ctx->device);
     const bool sums = d_dweight || d_dbias;
