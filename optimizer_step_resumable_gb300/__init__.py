@@ -763,19 +763,40 @@ def _code(t) -> int:
     return code
 
 
+def _allocator(ln: LayerNorm, stream):
+    """new(shape, dtype): an uninitialised tensor of the call's stream; the
+    current stream's free memory may still be in use there."""
+    import torch
+
+    def new(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=ln.device)
+
+    if stream is None:
+        return new
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=ln.device)
+
+    def new_there(shape, dtype):
+        with torch.cuda.stream(stream):
+            return new(shape, dtype)
+
+    return new_there
+
+
 def layernorm_forward(ln: LayerNorm, x, weight=None, bias=None, eps: float = 1e-5, y=None,
                       mean=None, rstd=None, stream=None):
     """(y, mean, rstd) of the rows of x (..., cols); outputs not given are
-    allocated.  weight and bias: float32 or the type of x; None: 1 and 0."""
+    allocated, for the stream if one is given.  weight and bias: float32 or
+    the type of x; None: 1 and 0."""
     shape, kind = x.shape, x.dtype
     xp, xs, rows = _rows(x, shape, ln, "x")
     code = _DTYPES.get(kind) or _code(x)
     if y is None or mean is None or rstd is None:
-        import torch
-        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
+        from torch import float32
+        new = _allocator(ln, stream)
         y = new(shape, kind) if y is None else y
-        mean = new(shape[:-1], torch.float32) if mean is None else mean
-        rstd = new(shape[:-1], torch.float32) if rstd is None else rstd
+        mean = new(shape[:-1], float32) if mean is None else mean
+        rstd = new(shape[:-1], float32) if rstd is None else rstd
     if y.dtype is not kind or y.shape != shape:
         raise TypeError("y must have the type and shape of x")
     yp, ys, _ = _rows(y, shape, ln, "y")
@@ -799,14 +820,14 @@ def layernorm_forward(ln: LayerNorm, x, weight=None, bias=None, eps: float = 1e-
 def layernorm_backward(ln: LayerNorm, dy, x, weight, mean, rstd, dx=None, dweight=None,
                        dbias=None, accumulate: bool = False, stream=None):
     """(dx, dweight, dbias) from the gradient dy of y and the forward pass's
-    x, mean, rstd; dx is allocated if not given, dweight and dbias are
-    computed if given.  accumulate: add into dweight and dbias."""
+    x, mean, rstd; dx is allocated if not given (for the stream if one is),
+    dweight and dbias are computed if given.  accumulate: add into dweight and
+    dbias."""
     kind, shape = x.dtype, x.shape
     xp, xs, rows = _rows(x, shape, ln, "x")
     code = _DTYPES.get(kind) or _code(x)
     if dx is None:
-        import torch
-        dx = torch.empty(shape, dtype=kind, device=x.device)
+        dx = _allocator(ln, stream)(shape, kind)
     if dy.dtype is not kind or dx.dtype is not kind or dy.shape != shape or dx.shape != shape:
         raise TypeError("dy and dx must have the type and shape of x")
     gp, gs, _ = _rows(dy, shape, ln, "dy")
