@@ -16,9 +16,8 @@ constexpr int kBlockElems = ADAMW_STATE_BLOCK;
 constexpr int kUnitBlocks = 8;
 constexpr int kUnitElems = kUnitBlocks * kBlockElems;
 
-constexpr uint32_t kListState8 = 1u;  // m, v in 8 bits with block scales
-constexpr uint32_t kListDecay = 2u;   // weight decay applies
-constexpr uint32_t kListVec = 4u;     // every array at its vector alignment
+constexpr uint32_t kListDecay = 1u;  // weight decay applies
+constexpr uint32_t kListVec = 2u;    // every array at its vector alignment
 
 // One tensor of the list, in device memory.
 struct alignas(16) ListTensor {
@@ -70,8 +69,9 @@ int launch_list_step(const ListView& plain, const ListView& eight, int32_t g_dty
                      int32_t w_lp_dtype, const StepScalars& k, uint32_t key, bool zero_grad,
                      const ListBlocks& most, void* stream);
 
-// The 32-bit hash behind the random rounding: xor-shifts and odd
-// multipliers, each invertible, so distinct words stay distinct.
+// The 32-bit hash behind the random rounding: xor-shifts and odd multipliers
+// (the first two of the 32-bit primes published with xxHash), each invertible,
+// so distinct words stay distinct.
 #ifdef __CUDACC__
 #define OSR_BOTH __host__ __device__
 #else

@@ -160,7 +160,7 @@ int bind_list(adamw_list* l, float* const* d_w, void* const* d_g, int32_t g_dtyp
         osr::ListTensor& t = table[i];
         const int32_t k = int32_t(i);
         const int64_t n = t.numel;
-        t.flags = (l->state8[i] ? osr::kListState8 : 0u) | (l->decay[i] ? osr::kListDecay : 0u);
+        t.flags = l->decay[i] ? osr::kListDecay : 0u;
         if (n == 0)
             continue;
         const int64_t blocks = (n + osr::kBlockElems - 1) / osr::kBlockElems;
