@@ -362,10 +362,11 @@ __device__ __forceinline__ void store_shifted(const Columns<T, kGroup, kRows>& a
 }
 
 // Rows that do not fit a block's registers: a block looks at a row several
-// times, the later ones from L2.  4096 x 32768 bf16 takes 191 us forward and
-// 430 backward (element by element: 395 and 887).  Rows spread over clusters
-// of blocks, held in registers, took 227 and 387 (16392 columns: 303 and 481,
-// where this takes 236 and 436): each row waits for the cluster's barriers.
+// times, the later ones from L2.  4096 x 32768 bf16, weights too, takes 195 us
+// forward and 422 backward, 8192 x 16392 224 and 440 (element by element the
+// first took 395 and 887).  Rows spread over clusters of blocks, held in
+// registers, took 227 and 387 (303 and 481): each row waits for the cluster's
+// barriers.
 constexpr int kWideThreads = 512;
 template <typename T>
 using WideColumns = Columns<T, kWideThreads, kMixed>;

@@ -12,7 +12,7 @@
 // update with a 16-bit gradient and weight copy: 28 with 32-bit states (w 8,
 // m and v 16, g 2, copy 2), 16.06 with 8-bit ones (w 8, m and v 4, scales
 // 16/256, g 2, copy 2); the norm reads g once more.  On GB300, 110M
-// parameters in 196 tensors: 490 us and 325 us a step (the copy's bandwidth
+// parameters in 196 tensors: 491 us and 325 us a step (the copy's bandwidth
 // would take 489 and 294 for these bytes); 570M in 8 bits 1620 us (1523).  The
 // norm kernel's share is 46 us: 33 for g, the rest for writing back what the
 // step before left in L2.
