@@ -266,15 +266,16 @@ int launch_typed(const LnForward& a, int sm_count, std::atomic<int>* known, cuda
     const bool aligned = a.cols % kE<T> == 0 && rows_aligned(a.x, a.x_stride, sizeof(T)) &&
                          rows_aligned(a.y, a.y_stride, sizeof(T));
     // Where the backward pass's layouts are not the forward pass's best.  Four
-    // vectors of float32 a thread rather than eight: 16384 x 4096 83 and 96 us,
-    // 8192 x 8192 90 and 96 (2500 columns: 66 and 61; up to 2048 and from 4097
-    // to 6144: no gain).  Ragged rows of 16-bit types in more groups of fewer
-    // threads, which hide the first warp's head and tail: 32768 x 2047 54 and 66
-    // us (whole vectors: 50 and 46).
+    // vectors of float32 a thread rather than eight pay where they fill most of
+    // the block (us for 65.5M elements, four and eight: 2820 columns 98 and 95,
+    // 2980 96 and 96, 3040 89 and 93, 4096 82 and 92; 5000 107 and 81, 6148 108
+    // and 94, 7420 101 and 92, 7680 90 and 95, 8192 88 and 94).  Ragged rows of
+    // 16-bit types in more groups of fewer threads, which hide the first warp's
+    // head and tail: 32768 x 2047 53 and 61 us, 65536 x 1100 75 and 103.
     if constexpr (sizeof(T) == 4) {
-        if (aligned && a.cols > 2816 && a.cols <= 4096)
+        if (aligned && a.cols > 3000 && a.cols <= 4096)
             return launch_aligned<T, 256, 2>(a, sm_count, known, s);
-        if (aligned && a.cols > 6144 && a.cols <= 8192)
+        if (aligned && a.cols > 7500 && a.cols <= 8192)
             return launch_aligned<T, 512, 2>(a, sm_count, known, s);
     } else if (!aligned && a.cols > 1024 && a.cols <= 2048) {
         return launch_ragged<T, 64, 4>(a, sm_count, known, s);

@@ -146,6 +146,12 @@ def test_forward_layouts(kind, cols):
     run(45, cols, kind, "f32", seed=cols, pad=(13, 13, 0))
 
 
+@pytest.mark.parametrize("cols", [2980, 3000, 3004, 3006, 7424, 7500, 7504, 7506])
+def test_forward_layouts_of_float32_rows(cols):
+    run(45, cols, "f32", "f32", seed=cols)
+    run(45, cols, "f32", "f32", seed=cols, pad=(4, 0, 8))
+
+
 # rows that are looked at several times
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("cols", [24_576, 24_577, 65_528, 65_536, 65_537, 81_920, 131_071, 131_072,
