@@ -306,18 +306,24 @@ __device__ __forceinline__ void group_sum(float (&s)[kCount], float (&slots)[2][
 // The statistics of a row from a first mean and, of the differences d from it,
 // their sum and the sum of their squares.  The first mean errs by up to a few
 // 2^-24 of mean |x|, which moves every difference and adds its square to the
-// variance; but the differences are exact where that error matters, so their
-// mean e is what the first mean lacks.  xhat = d rstd + shift.
+// variance.  Where that is much beside the spread the differences are exact,
+// and their mean e is what the first mean lacks.  Elsewhere e is the rounding
+// of the differences, below 2^-24 of the spread, where the first mean may be
+// exact (sums of 16-bit values often are): an e below 2^-22 of the spread
+// counts for nothing.  xhat = d rstd + shift.
 struct Statistics {
     float mean, rstd, shift;
 };
 __device__ __forceinline__ Statistics statistics_of(float mean, const float (&d)[2], float inv,
                                                     float eps)
 {
+    const float square = d[1] * inv;
     float e = d[0] * inv;
-    if (!(fabsf(e) < __uint_as_float(0x7f800000u)))
-        e = 0.0f;  // the sums' infinities and NaNs say it all
-    const float var = __fmaf_rn(-e, e, d[1] * inv);
+    float var = __fmaf_rn(-e, e, square);
+    if (!(e * e > 0x1p-44f * var)) {  // also where the sums are no numbers
+        e = 0.0f;
+        var = square;
+    }
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn((var < 0.0f ? 0.0f : var) + eps));
     return Statistics{mean + e, rstd, -e * rstd};
 }

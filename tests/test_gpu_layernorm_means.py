@@ -95,6 +95,35 @@ def test_rows_far_from_zero(cols, mean, spread, pad, at):
         check(x, w, b, *osr.layernorm_forward(ln, x, w, b, eps=EPS))
 
 
+@pytest.mark.parametrize("cols", WIDTHS)
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("pad,at", [(0, 0), (3, 1)])
+def test_means_of_exact_sums(cols, kind, pad, at):
+    """Multiples of 2^-6 below 4, whose sums float32 holds in any order: the
+    mean is the sum times 1 / cols in two roundings, however close to 0."""
+    dtype, _ = TYPES[kind]
+    r = torch.Generator(device="cuda").manual_seed(cols)
+    rows = 33
+    whole = torch.randint(-255, 256, (rows, cols + pad), generator=r, device="cuda")
+    for k in range(rows):  # the sum: -16 to 16
+        left = int(whole[k, :cols].sum()) - (k - 16)
+        # taken from as many elements as it needs, without leaving the range
+        change = torch.where(whole[k, :cols] * left > 0, whole[k, :cols], 0)
+        take = change.abs().cumsum(0)
+        part = (abs(left) - (take - change.abs())).clamp(min=0).minimum(change.abs())
+        whole[k, :cols] -= change.sign() * part
+        assert int(whole[k, :cols].sum()) == k - 16
+    pool = torch.zeros(rows * (cols + pad) + at, device="cuda", dtype=dtype)
+    pool[at:] = (whole.float() / 64).flatten().to(dtype)
+    x = pool[at:].view(rows, cols + pad)[:, :cols]
+    with osr.layernorm_create(cols) as ln:
+        y, mean, rstd = osr.layernorm_forward(ln, x, eps=EPS)
+    mu = x.double().mean(1)
+    assert bool(((mean.double() - mu).abs() <= 2.01 * U * mu.abs()).all()), float(
+        ((mean.double() - mu).abs() / mu.abs().clamp(min=1e-30)).max())
+    check(x, None, None, y, mean, rstd)
+
+
 def test_means_that_are_not_numbers():
     """The mean of a row with an infinity is that infinity; of a row whose sum
     leaves float32's range, an infinity; of a row with a NaN, NaN."""
