@@ -103,9 +103,27 @@ extern "C" {
 /* layernorm_backward flags. */
 #define LAYERNORM_ACCUMULATE 1 /* add into dweight and dbias, do not replace  */
 
+/* Activations of the linear layer. */
+#define LINEAR_NONE 0
+#define LINEAR_RELU 1
+#define LINEAR_GELU 2      /* z (1 + erf(z / sqrt 2)) / 2                      */
+#define LINEAR_GELU_TANH 3 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define LINEAR_SILU 4      /* z / (1 + e^-z)                                   */
+
+/* linear_forward, linear_backward and linear_cross_entropy_* flags. */
+#define LINEAR_IN_OUT 1          /* the weight's rows are inputs: in x out     */
+#define LINEAR_GRAD_IN_OUT 2     /* the same of dweight                        */
+#define LINEAR_ACCUMULATE 4      /* add into dweight and dbias, do not replace */
+/* linear_workspace and linear_cross_entropy_workspace flags. */
+#define LINEAR_FOR_BACKWARD 1
+#define LINEAR_FOR_ANY_ADDRESS 2 /* rows that do not start on 16 bytes         */
+
 typedef struct adamw_ctx adamw_ctx;
 typedef struct adamw_list adamw_list;
 typedef struct layernorm_ctx layernorm_ctx;
+typedef struct linear_ctx linear_ctx;
+typedef struct linear_ce_ctx linear_ce_ctx;
+typedef struct distill_ctx distill_ctx;
 
 /*
  * Creates a context for a flat state of n_params float32 values split into
@@ -795,6 +813,160 @@ ADAMW_API int layernorm_backward(layernorm_ctx* ctx, const void* d_dy, int64_t d
                                  const float* d_rstd, void* d_dx, int64_t dx_stride,
                                  void* d_dweight, void* d_dbias, int32_t grad_dtype,
                                  int64_t rows, int32_t flags, void* stream);
+
+/*
+ * The linear layer: a matrix product with bias, activation and residual in
+ * its epilogue, and its backward pass ([B] "The pairing rule": the
+ * projections and k_mlp_fwd / k_mlp_bwd, whose backward pass reads the
+ * pre-activation; "Accumulation across micro-batches").  For `rows` rows x
+ * of `in` elements, a weight of out x in:
+ *   z = x weight^T + bias;  y = act(z) + residual
+ * and for the gradient dy of y:
+ *   dz = dy act'(z);  dx = dz weight;  dweight = dz^T x;
+ *   dbias = sum over the rows of dz     (the residual's gradient is dy)
+ * Matrix products take 16-bit factors on the tensor cores and sum in float32
+ * (over ranges of the inner dimension joined in order: the same bits every
+ * time); bias, activation and residual are float32, each output is rounded
+ * once.  dz is a factor of two products, so it is rounded to dy's type if
+ * there is an activation; dbias sums the unrounded values.
+ *
+ * linear_create: 1 <= in, out <= 2^24, in x out < 2^40; nothing on the
+ *   device but a pinned word.  Calls with one context may run at the same
+ *   time if their workspaces differ.
+ * linear_workspace: bytes of device memory, on a 256-byte boundary, that a
+ *   call on `rows` rows needs (0: none); the caller's, only used while the
+ *   call runs on the device.  flags: LINEAR_FOR_BACKWARD;
+ *   LINEAR_FOR_ANY_ADDRESS if a matrix that is read (x, weight, dy) may have
+ *   rows that do not start on 16-byte boundaries, which are then copied.
+ * x, weight, dy, dx, y, z, residual: dtype (BF16 or F16); rows *_stride
+ *   elements apart, elements of a row adjacent.  weight: out rows of in, or in
+ *   rows of out with LINEAR_IN_OUT.  bias: bias_dtype (float32 or dtype); may
+ *   be NULL, as may residual and z.  residual may be y itself.  The backward
+ *   pass needs z if there is an activation.
+ * dx may be NULL (not wanted: the weight is not read then); dweight, dbias:
+ *   grad_dtype (any), each may be NULL (without dweight x is not read);
+ *   dweight with LINEAR_GRAD_IN_OUT is in x out.  LINEAR_ACCUMULATE adds to
+ *   what is there, in float32.  rows = 0 is accepted: dweight and dbias
+ *   become 0 (or stay, accumulating).  rows <= 2^30.
+ * Every array must be aligned to its elements; no output may share a byte
+ * with an input or another output, but for residual as above (ADAMW_EINVAL).
+ * Asynchronous on `stream`.  Errors: ADAMW_EINVAL, ADAMW_ECUDA, ADAMW_ESTATE
+ * (a kernel of an earlier call of this context gave up waiting and its
+ * outputs are not valid; reported once).
+ */
+ADAMW_API int linear_create(int32_t in_features, int32_t out_features, linear_ctx** out);
+ADAMW_API int linear_destroy(linear_ctx* ctx);
+ADAMW_API int linear_workspace(linear_ctx* ctx, int64_t rows, int32_t flags, int64_t* bytes);
+ADAMW_API int linear_forward(linear_ctx* ctx, const void* d_x, int64_t x_stride,
+                             const void* d_weight, int64_t weight_stride, int32_t dtype,
+                             const void* d_bias, int32_t bias_dtype, const void* d_residual,
+                             int64_t residual_stride, int32_t activation, void* d_y,
+                             int64_t y_stride, void* d_z, int64_t z_stride, int64_t rows,
+                             int32_t flags, void* d_workspace, int64_t workspace_bytes,
+                             void* stream);
+ADAMW_API int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride,
+                              const void* d_x, int64_t x_stride, const void* d_weight,
+                              int64_t weight_stride, int32_t dtype, const void* d_z,
+                              int64_t z_stride, int32_t activation, void* d_dx,
+                              int64_t dx_stride, void* d_dweight, int64_t dweight_stride,
+                              void* d_dbias, int32_t grad_dtype, int64_t rows, int32_t flags,
+                              void* d_workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * The cross entropy of a language model's head, without its logits ([B] "The
+ * pairing rule": k_loss_fwd / k_loss_bwd; the head is the tied embedding).
+ * For `rows` rows x of `dim` elements, a weight of vocab x dim and a target
+ * each:
+ *   l = x weight^T;  lse = log sum exp l;
+ *   loss = lse - l[target] + z_loss lse^2
+ * and the gradient of sum(scale dloss loss):
+ *   dl = scale dloss ((1 + 2 z_loss lse) exp(l - lse) - [target])
+ *   dx = dl weight;  dweight = dl^T x.
+ * A target below 0 is none: the row's loss is 0 and it adds nothing to the
+ * gradients (its x must be finite: 0 times it is added to dweight).  A
+ * target of vocab or more gives a NaN loss and NaN gradients, which the
+ * optimizer step refuses.  lse is written for every row.
+ * Logits are sums in float32 and are never stored.  The backward pass
+ * computes them again, for a piece of the vocabulary at a time, and keeps dl
+ * of that piece in the workspace, rounded to dtype (for binary16 after the
+ * product with a power of two that keeps the largest in range), as it is a
+ * factor of two products.
+ *
+ * linear_cross_entropy_create: 1 <= dim <= 2^20, 1 <= vocab <= 2^24; nothing
+ *   on the device but a pinned word.  Calls with one context may run at the
+ *   same time if their workspaces differ.
+ * linear_cross_entropy_workspace: as linear_workspace.  Forward: 8 rows
+ *   vocab / 128 bytes; backward: mostly a piece's dl, 256 MiB at most
+ *   (or 256 columns).
+ * x, weight, dx: dtype (BF16 or F16); the weight vocab rows of dim, or dim
+ *   rows of vocab with LINEAR_IN_OUT; rows *_stride elements apart.  target:
+ *   int64.  loss, lse, dloss: float32, one a row; lse may be NULL in the
+ *   forward pass, dloss NULL: 1.
+ * dx may be NULL (not wanted), as may dweight: grad_dtype (any), dim x vocab
+ *   with LINEAR_GRAD_IN_OUT; LINEAR_ACCUMULATE adds to what is there, in
+ *   float32.  rows = 0 is accepted: dweight becomes 0 (or stays).
+ * Every array must be aligned to its elements; no output may share a byte
+ * with an input or another output (ADAMW_EINVAL).
+ * Asynchronous on `stream`; the same inputs give the same bits.  Errors:
+ * ADAMW_EINVAL, ADAMW_ECUDA, ADAMW_ESTATE (as linear_forward).
+ */
+ADAMW_API int linear_cross_entropy_create(int32_t dim, int32_t vocab, linear_ce_ctx** out);
+ADAMW_API int linear_cross_entropy_destroy(linear_ce_ctx* ctx);
+ADAMW_API int linear_cross_entropy_workspace(linear_ce_ctx* ctx, int64_t rows, int32_t flags,
+                                             int64_t* bytes);
+ADAMW_API int linear_cross_entropy_forward(linear_ce_ctx* ctx, const void* d_x, int64_t x_stride,
+                                           const void* d_weight, int64_t weight_stride,
+                                           int32_t dtype, const int64_t* d_target, double z_loss,
+                                           float* d_loss, float* d_lse, int64_t rows,
+                                           int32_t flags, void* d_workspace,
+                                           int64_t workspace_bytes, void* stream);
+ADAMW_API int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x_stride,
+                                            const void* d_weight, int64_t weight_stride,
+                                            int32_t dtype, const int64_t* d_target,
+                                            const float* d_lse, const float* d_dloss,
+                                            double scale, double z_loss, void* d_dx,
+                                            int64_t dx_stride, void* d_dweight,
+                                            int64_t dweight_stride, int32_t grad_dtype,
+                                            int64_t rows, int32_t flags, void* d_workspace,
+                                            int64_t workspace_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top logits: for each of `rows` rows of the
+ * student's vocab logits l (of linear_forward, for instance), and k entries
+ * (id, value) of the teacher's,
+ *   q = softmax(value / T) over the row's entries;  p = softmax(l / T)
+ *   lse = log sum exp(l / T);  loss = T^2 sum q (log q - log p[id])
+ * and the gradient of sum(scale dloss loss):
+ *   dl = scale dloss T (p - sum of q over the entries with that id).
+ * An entry with an id below 0, or a value of -infinity, is none; a row
+ * without entries has loss 0 and a zero gradient, whatever its logits.  An
+ * id of vocab or more gives a NaN loss and a row of NaN gradients.
+ *
+ * distill_create: 1 <= vocab <= 2^30, 1 <= k <= 1024; nothing on the device,
+ *   so calls with one context may run at the same time.
+ * logits, dlogits: dtype (any), rows *_stride elements apart; dlogits may be
+ *   logits itself.  ids: int64, values: values_dtype (any), both rows x k
+ *   without gaps.  loss, lse, dloss: float32, one a row; lse may be NULL in
+ *   the forward pass, dloss NULL: 1.  0 <= rows < 2^31.
+ * Everything is float32 inside; each gradient is rounded once.  Every array
+ * must be aligned to its elements (rows of logits and dlogits that start at
+ * the same place within 16 bytes are read and written in vectors); no output
+ * may share a byte with an input or another output, but for dlogits as above
+ * (ADAMW_EINVAL).
+ * Asynchronous on `stream`; the same inputs give the same bits.  Errors:
+ * ADAMW_EINVAL, ADAMW_ECUDA.
+ */
+ADAMW_API int distill_create(int32_t vocab, int32_t k, distill_ctx** out);
+ADAMW_API int distill_destroy(distill_ctx* ctx);
+ADAMW_API int distill_forward(distill_ctx* ctx, const void* d_logits, int64_t logits_stride,
+                              int32_t dtype, const int64_t* d_ids, const void* d_values,
+                              int32_t values_dtype, double temperature, float* d_loss,
+                              float* d_lse, int64_t rows, void* stream);
+ADAMW_API int distill_backward(distill_ctx* ctx, const void* d_logits, int64_t logits_stride,
+                               int32_t dtype, const int64_t* d_ids, const void* d_values,
+                               int32_t values_dtype, double temperature, const float* d_lse,
+                               const float* d_dloss, double scale, void* d_dlogits,
+                               int64_t dlogits_stride, int64_t rows, void* stream);
 
 /* Name of a status code, and the last failure's explanation (this thread). */
 ADAMW_API const char* adamw_strerror(int status);

@@ -27,6 +27,9 @@ ZERO_GRAD = 1
 TENSOR_NORMS = 2
 STATE_BLOCK = 256
 LAYERNORM_ACCUMULATE = 1
+LINEAR_IN_OUT, LINEAR_GRAD_IN_OUT, LINEAR_ACCUMULATE = 1, 2, 4
+LINEAR_FOR_BACKWARD, LINEAR_FOR_ANY_ADDRESS = 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 LAUNCH_NO_PDL = 1
 LAUNCH_NO_ONEPASS = 2
 LAUNCH_TEST_BARRIER_TIMEOUT = 4
@@ -128,6 +131,34 @@ SIGNATURES = {
     "layernorm_backward": (_c.c_int, [_vp, _vp, _c.c_int64, _vp, _c.c_int64, _c.c_int32, _vp,
                                       _c.c_int32, _vp, _vp, _vp, _c.c_int64, _vp, _vp,
                                       _c.c_int32, _c.c_int64, _c.c_int32, _vp]),
+    "linear_create": (_c.c_int, [_c.c_int32, _c.c_int32, _c.POINTER(_vp)]),
+    "linear_destroy": (_c.c_int, [_vp]),
+    "linear_workspace": (_c.c_int, [_vp, _c.c_int64, _c.c_int32, _c.POINTER(_c.c_int64)]),
+    "linear_forward": (_c.c_int, [_vp, _vp, _c.c_int64, _vp, _c.c_int64, _c.c_int32, _vp,
+                                  _c.c_int32, _vp, _c.c_int64, _c.c_int32, _vp, _c.c_int64, _vp,
+                                  _c.c_int64, _c.c_int64, _c.c_int32, _vp, _c.c_int64, _vp]),
+    "linear_backward": (_c.c_int, [_vp, _vp, _c.c_int64, _vp, _c.c_int64, _vp, _c.c_int64,
+                                   _c.c_int32, _vp, _c.c_int64, _c.c_int32, _vp, _c.c_int64, _vp,
+                                   _c.c_int64, _vp, _c.c_int32, _c.c_int64, _c.c_int32, _vp,
+                                   _c.c_int64, _vp]),
+    "linear_cross_entropy_create": (_c.c_int, [_c.c_int32, _c.c_int32, _c.POINTER(_vp)]),
+    "linear_cross_entropy_destroy": (_c.c_int, [_vp]),
+    "linear_cross_entropy_workspace": (_c.c_int, [_vp, _c.c_int64, _c.c_int32,
+                                                  _c.POINTER(_c.c_int64)]),
+    "linear_cross_entropy_forward": (_c.c_int, [_vp, _vp, _c.c_int64, _vp, _c.c_int64, _c.c_int32,
+                                                _vp, _c.c_double, _vp, _vp, _c.c_int64,
+                                                _c.c_int32, _vp, _c.c_int64, _vp]),
+    "linear_cross_entropy_backward": (_c.c_int, [_vp, _vp, _c.c_int64, _vp, _c.c_int64, _c.c_int32,
+                                                 _vp, _vp, _vp, _c.c_double, _c.c_double, _vp,
+                                                 _c.c_int64, _vp, _c.c_int64, _c.c_int32,
+                                                 _c.c_int64, _c.c_int32, _vp, _c.c_int64, _vp]),
+    "distill_create": (_c.c_int, [_c.c_int32, _c.c_int32, _c.POINTER(_vp)]),
+    "distill_destroy": (_c.c_int, [_vp]),
+    "distill_forward": (_c.c_int, [_vp, _vp, _c.c_int64, _c.c_int32, _vp, _vp, _c.c_int32,
+                                   _c.c_double, _vp, _vp, _c.c_int64, _vp]),
+    "distill_backward": (_c.c_int, [_vp, _vp, _c.c_int64, _c.c_int32, _vp, _vp, _c.c_int32,
+                                    _c.c_double, _vp, _vp, _c.c_double, _vp, _c.c_int64,
+                                    _c.c_int64, _vp]),
     "adamw_strerror": (_c.c_char_p, [_c.c_int]),
     "adamw_last_error": (_c.c_char_p, []),
 }
@@ -850,6 +881,401 @@ def layernorm_backward(ln: LayerNorm, dy, x, weight, mean, rstd, dx=None, dweigh
     if st != OK:
         _check(st, "layernorm_backward")
     return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+# Linear layer
+# ---------------------------------------------------------------------------
+class Linear(_Owner):
+    """Owner of one ``linear_ctx*``: a weight of ``out`` rows of ``cols``
+    elements."""
+
+    _destroy = "linear_destroy"
+    _workspace = "linear_workspace"
+
+    def __init__(self, handle: int, cols: int, out: int, device=None):
+        super().__init__(handle, device)
+        self.cols, self.out = cols, out
+        self._bytes = {}  # workspaces by (rows, flags)
+
+
+def linear_create(in_features: int, out_features: int) -> Linear:
+    import torch
+    out = ctypes.c_void_p()
+    _check(library().linear_create(int(in_features), int(out_features), ctypes.byref(out)),
+           "linear_create")
+    return Linear(out.value, int(in_features), int(out_features), torch.cuda.current_device())
+
+
+def linear_destroy(lin: Linear):
+    lin.close()
+
+
+def _half(t, name: str) -> int:
+    code = _code(t)
+    if code == DTYPE_F32:
+        raise TypeError(f"{name} must be bfloat16 or float16")
+    return code
+
+
+def _spaced(t, shape, cols: int, ctx, name: str):
+    """(address, row stride, rows) of a tensor of shape (..., cols) with evenly
+    spaced rows whose elements are adjacent; shape: the tensor's."""
+    if t.get_device() != ctx.device or not shape or shape[-1] != cols:
+        if not t.is_cuda or not shape or shape[-1] != cols:
+            raise TypeError(f"{name} must be a CUDA tensor of shape (..., {cols})")
+        _same_device(t, name, ctx)
+    if t.is_contiguous():
+        return t.data_ptr(), cols, t.numel() // cols
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, cols)
+        except RuntimeError:
+            raise TypeError(f"{name}: rows must be evenly spaced") from None
+    if t.stride(1) != 1 and cols > 1:
+        raise TypeError(f"{name}: the elements of a row must be adjacent")
+    rows = t.shape[0]
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols, rows
+
+
+def _either_way(t, out: int, cols: int, ctx, name: str):
+    """(address, row stride, whether it is stored (in, out)) of an (out, in)
+    matrix in which the elements along one of the dimensions are adjacent."""
+    shape = t.shape
+    if t.get_device() != ctx.device or len(shape) != 2 or shape[0] != out or shape[1] != cols:
+        if not t.is_cuda or tuple(shape) != (out, cols):
+            raise TypeError(f"{name} must be a CUDA tensor of shape ({out}, {cols})")
+        _same_device(t, name, ctx)
+    a, b = t.stride()
+    if b == 1 or cols == 1:
+        return t.data_ptr(), a if out > 1 else cols, False
+    if a == 1 or out == 1:
+        return t.data_ptr(), b, True
+    raise TypeError(f"{name}: the elements along one dimension must be adjacent")
+
+
+def _work(ctx, rows: int, flags: int, pointers, workspace, stream):
+    """(address, bytes, tensor) of the workspace of a call whose matrices lie at
+    the (address, stride) pairs `pointers`."""
+    for p, s in pointers:
+        if p & 15 or s & 7:
+            flags |= LINEAR_FOR_ANY_ADDRESS
+    need = ctx._bytes.get((rows, flags))
+    if need is None:
+        n = ctypes.c_int64()
+        _check(getattr(library(), ctx._workspace)(ctx.handle, rows, flags, ctypes.byref(n)),
+               ctx._workspace)
+        if len(ctx._bytes) > 256:
+            ctx._bytes.clear()
+        need = ctx._bytes[rows, flags] = n.value
+    if workspace is not None:
+        if workspace.get_device() != ctx.device or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous CUDA tensor of the context's device")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if not need:
+        return None, 0, None
+    from torch import uint8
+    t = _allocator(ctx, stream)((need,), uint8)
+    return t.data_ptr(), need, t
+
+
+def linear_workspace(lin: Linear, rows: int, flags: int = 0) -> int:
+    """Bytes of device memory that a call on `rows` rows needs; flags:
+    LINEAR_FOR_BACKWARD, LINEAR_FOR_ANY_ADDRESS."""
+    n = ctypes.c_int64()
+    _check(library().linear_workspace(lin.handle, int(rows), flags, ctypes.byref(n)),
+           "linear_workspace")
+    return n.value
+
+
+def _activation(name: str) -> int:
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation {name!r} is not one of {', '.join(ACTIVATIONS)}")
+    return code
+
+
+def linear_forward(lin: Linear, x, weight, bias=None, residual=None, activation: str = "none",
+                   y=None, z=None, workspace=None, stream=None):
+    """y = act(x weight^T + bias) + residual for x (..., in) and weight (out,
+    in), stored either way, both bfloat16 or float16; y is allocated if not
+    given (for the stream if one is) and may be residual.  z, if given, gets
+    x weight^T + bias, which the backward pass of an activation reads.
+    workspace: a CUDA tensor of linear_workspace bytes (None: allocated)."""
+    shape, kind = x.shape, x.dtype
+    xp, xs, rows = _spaced(x, shape, lin.cols, lin, "x")
+    code = _half(x, "x")
+    wp, ws, in_out = _either_way(weight, lin.out, lin.cols, lin, "weight")
+    act = _activation(activation)
+    shape = (*shape[:-1], lin.out)
+    if y is None:
+        y = _allocator(lin, stream)(shape, kind)
+    bp = rp = zp = None
+    b_code, rs, zs = DTYPE_F32, 0, 0
+    if bias is not None:
+        bp, b_code = _vector(bias, lin.out, "bias", lin)
+    if weight.dtype is not kind:
+        raise TypeError("weight must have the type of x")
+    for t, name in ((y, "y"), (residual, "residual"), (z, "z")):
+        if t is not None and (t.dtype is not kind or t.shape != shape):
+            raise TypeError(f"{name} must have the type of x and the shape {tuple(shape)}")
+    yp, ys, _ = _spaced(y, shape, lin.out, lin, "y")
+    if residual is not None:
+        rp, rs, _ = _spaced(residual, shape, lin.out, lin, "residual")
+    if z is not None:
+        zp, zs, _ = _spaced(z, shape, lin.out, lin, "z")
+    mem, size, keep = _work(lin, rows, 0, ((xp, xs), (wp, ws)), workspace, stream)
+    st = (_lib or library()).linear_forward(
+        lin.handle, xp, xs, wp, ws, code, bp, b_code, rp, rs, act, yp, ys, zp, zs, rows,
+        LINEAR_IN_OUT if in_out else 0, mem, size, _stream(stream, lin.device))
+    if st != OK:
+        _check(st, "linear_forward")
+    return y
+
+
+def linear_backward(lin: Linear, dy, x, weight, z=None, activation: str = "none", dx=None,
+                    dweight=None, dbias=None, accumulate: bool = False, workspace=None,
+                    stream=None):
+    """(dx, dweight, dbias) from the gradient dy of y.  dx is allocated if not
+    given (for the stream if one is) and left out if False; dweight (out, in),
+    stored either way, and dbias are computed if given, added to what is there
+    if accumulate.  z: the forward pass's, for an activation."""
+    kind, shape = dy.dtype, dy.shape
+    gp, gs, rows = _spaced(dy, shape, lin.out, lin, "dy")
+    code = _half(dy, "dy")
+    act = _activation(activation)
+    wp, ws, in_out = _either_way(weight, lin.out, lin.cols, lin, "weight")
+    x_shape = (*shape[:-1], lin.cols)
+    if dx is None:
+        dx = _allocator(lin, stream)(x_shape, kind)
+    elif dx is False:
+        dx = None
+    if weight.dtype is not kind:
+        raise TypeError("weight must have the type of dy")
+    for t, name, s in ((x, "x", x_shape), (dx, "dx", x_shape), (z, "z", shape)):
+        if t is not None and (t.dtype is not kind or t.shape != s):
+            raise TypeError(f"{name} must have the type of dy and the shape {tuple(s)}")
+    if act and z is None:
+        raise TypeError("z is needed: the activation's derivative is taken there")
+    xp, xs, _ = _spaced(x, x_shape, lin.cols, lin, "x")
+    zp = dp = dwp = dbp = None
+    zs = ds = dws = 0
+    g_code, flags = DTYPE_F32, LINEAR_IN_OUT if in_out else 0
+    if act:
+        zp, zs, _ = _spaced(z, shape, lin.out, lin, "z")
+    if dx is not None:
+        dp, ds, _ = _spaced(dx, x_shape, lin.cols, lin, "dx")
+    if dweight is not None:
+        dwp, dws, turned = _either_way(dweight, lin.out, lin.cols, lin, "dweight")
+        g_code = _code(dweight)
+        flags |= LINEAR_GRAD_IN_OUT if turned else 0
+    if dbias is not None:
+        dbp, b_code = _vector(dbias, lin.out, "dbias", lin)
+        if dwp is not None and b_code != g_code:
+            raise TypeError("dweight and dbias must have one type")
+        g_code = b_code
+    mem, size, keep = _work(lin, rows, LINEAR_FOR_BACKWARD, ((xp, xs), (wp, ws), (gp, gs)),
+                            workspace, stream)
+    st = (_lib or library()).linear_backward(
+        lin.handle, gp, gs, xp, xs, wp, ws, code, zp, zs, act, dp, ds, dwp, dws, dbp, g_code,
+        rows, flags | (LINEAR_ACCUMULATE if accumulate else 0), mem, size,
+        _stream(stream, lin.device))
+    if st != OK:
+        _check(st, "linear_backward")
+    return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy over a vocabulary, without its logits
+# ---------------------------------------------------------------------------
+class LinearCrossEntropy(_Owner):
+    """Owner of one ``linear_ce_ctx*``: a head of ``out`` (the vocabulary)
+    rows of ``cols`` elements."""
+
+    _destroy = "linear_cross_entropy_destroy"
+    _workspace = "linear_cross_entropy_workspace"
+
+    def __init__(self, handle: int, cols: int, vocab: int, device=None):
+        super().__init__(handle, device)
+        self.cols, self.out = cols, vocab
+        self._bytes = {}
+
+
+def linear_cross_entropy_create(dim: int, vocab: int) -> LinearCrossEntropy:
+    import torch
+    out = ctypes.c_void_p()
+    _check(library().linear_cross_entropy_create(int(dim), int(vocab), ctypes.byref(out)),
+           "linear_cross_entropy_create")
+    return LinearCrossEntropy(out.value, int(dim), int(vocab), torch.cuda.current_device())
+
+
+def linear_cross_entropy_destroy(ce: LinearCrossEntropy):
+    ce.close()
+
+
+def linear_cross_entropy_workspace(ce: LinearCrossEntropy, rows: int, flags: int = 0) -> int:
+    """Bytes of device memory that a call on `rows` rows needs; flags:
+    LINEAR_FOR_BACKWARD, LINEAR_FOR_ANY_ADDRESS."""
+    n = ctypes.c_int64()
+    _check(library().linear_cross_entropy_workspace(ce.handle, int(rows), flags, ctypes.byref(n)),
+           "linear_cross_entropy_workspace")
+    return n.value
+
+
+def _targets(t, rows: int, ctx) -> int:
+    import torch
+    if t.dtype is not torch.int64:
+        raise TypeError("target must be int64")
+    if t.get_device() != ctx.device or t.numel() != rows or not t.is_contiguous():
+        _refuse_vector(t, rows, "target", ctx)
+    return t.data_ptr()
+
+
+def linear_cross_entropy_forward(ce: LinearCrossEntropy, x, weight, target, z_loss: float = 0.0,
+                                 loss=None, lse=None, workspace=None, stream=None):
+    """(loss, lse), float32, of the rows of x (..., dim) with the head weight
+    (vocab, dim), stored either way, and a target each (below 0: none);
+    outputs not given are allocated, for the stream if one is given."""
+    shape = x.shape
+    xp, xs, rows = _spaced(x, shape, ce.cols, ce, "x")
+    code = _half(x, "x")
+    wp, ws, in_out = _either_way(weight, ce.out, ce.cols, ce, "weight")
+    if weight.dtype is not x.dtype:
+        raise TypeError("weight must have the type of x")
+    if loss is None or lse is None:
+        from torch import float32
+        new = _allocator(ce, stream)
+        loss = new(shape[:-1], float32) if loss is None else loss
+        lse = new(shape[:-1], float32) if lse is None else lse
+    mem, size, keep = _work(ce, rows, 0, ((xp, xs), (wp, ws)), workspace, stream)
+    st = (_lib or library()).linear_cross_entropy_forward(
+        ce.handle, xp, xs, wp, ws, code, _targets(target, rows, ce), z_loss,
+        _row_values(loss, rows, "loss", ce), _row_values(lse, rows, "lse", ce), rows,
+        LINEAR_IN_OUT if in_out else 0, mem, size, _stream(stream, ce.device))
+    if st != OK:
+        _check(st, "linear_cross_entropy_forward")
+    return loss, lse
+
+
+def linear_cross_entropy_backward(ce: LinearCrossEntropy, x, weight, target, lse, dloss=None,
+                                  scale: float = 1.0, z_loss: float = 0.0, dx=None, dweight=None,
+                                  accumulate: bool = False, workspace=None, stream=None):
+    """(dx, dweight) of sum(scale dloss loss), lse from the forward pass; dx is
+    allocated if not given (for the stream if one is) and left out if False;
+    dweight, stored either way, is computed if given, added to what is there if
+    accumulate.  dloss: float32, one a row (None: 1)."""
+    shape, kind = x.shape, x.dtype
+    xp, xs, rows = _spaced(x, shape, ce.cols, ce, "x")
+    code = _half(x, "x")
+    wp, ws, in_out = _either_way(weight, ce.out, ce.cols, ce, "weight")
+    if dx is None:
+        dx = _allocator(ce, stream)(shape, kind)
+    elif dx is False:
+        dx = None
+    if weight.dtype is not kind or dx is not None and (dx.dtype is not kind or dx.shape != shape):
+        raise TypeError("weight and dx must have the type of x, dx its shape")
+    dp = dwp = None
+    ds = dws = 0
+    g_code, flags = DTYPE_F32, LINEAR_IN_OUT if in_out else 0
+    if dx is not None:
+        dp, ds, _ = _spaced(dx, shape, ce.cols, ce, "dx")
+    if dweight is not None:
+        dwp, dws, turned = _either_way(dweight, ce.out, ce.cols, ce, "dweight")
+        g_code = _code(dweight)
+        flags |= LINEAR_GRAD_IN_OUT if turned else 0
+    mem, size, keep = _work(ce, rows, LINEAR_FOR_BACKWARD, ((xp, xs), (wp, ws)), workspace, stream)
+    st = (_lib or library()).linear_cross_entropy_backward(
+        ce.handle, xp, xs, wp, ws, code, _targets(target, rows, ce),
+        _row_values(lse, rows, "lse", ce),
+        None if dloss is None else _row_values(dloss, rows, "dloss", ce), scale, z_loss, dp, ds,
+        dwp, dws, g_code, rows, flags | (LINEAR_ACCUMULATE if accumulate else 0), mem, size,
+        _stream(stream, ce.device))
+    if st != OK:
+        _check(st, "linear_cross_entropy_backward")
+    return dx, dweight
+
+
+# ---------------------------------------------------------------------------
+# Distillation from a teacher's top logits
+# ---------------------------------------------------------------------------
+class Distillation(_Owner):
+    """Owner of one ``distill_ctx*``: rows of ``cols`` logits (the vocabulary)
+    and ``k`` entries of the teacher's."""
+
+    _destroy = "distill_destroy"
+
+    def __init__(self, handle: int, vocab: int, k: int, device=None):
+        super().__init__(handle, device)
+        self.cols, self.k = vocab, k
+
+
+def distill_create(vocab: int, k: int) -> Distillation:
+    import torch
+    out = ctypes.c_void_p()
+    _check(library().distill_create(int(vocab), int(k), ctypes.byref(out)), "distill_create")
+    return Distillation(out.value, int(vocab), int(k), torch.cuda.current_device())
+
+
+def distill_destroy(ds: Distillation):
+    ds.close()
+
+
+def _entries(ds: Distillation, ids, values, rows: int):
+    """(ids, values, values' type) of the teacher's rows x k entries."""
+    import torch
+    if ids.dtype is not torch.int64:
+        raise TypeError("ids must be int64")
+    for t, name in ((ids, "ids"), (values, "values")):
+        if not t.shape or t.shape[-1] != ds.k:
+            raise TypeError(f"{name} must have the shape (..., {ds.k})")
+        if t.get_device() != ds.device or t.numel() != rows * ds.k or not t.is_contiguous():
+            _refuse_vector(t, rows * ds.k, name, ds)
+    return ids.data_ptr(), values.data_ptr(), _code(values)
+
+
+def distill_forward(ds: Distillation, logits, ids, values, temperature: float = 1.0, loss=None,
+                    lse=None, stream=None):
+    """(loss, lse), float32, of the rows of logits (..., vocab) against the
+    teacher's entries ids, values (..., k); an id below 0 is none.  Outputs not
+    given are allocated, for the stream if one is given."""
+    shape = logits.shape
+    lp, ls, rows = _spaced(logits, shape, ds.cols, ds, "logits")
+    ip, vp, v_code = _entries(ds, ids, values, rows)
+    if loss is None or lse is None:
+        from torch import float32
+        new = _allocator(ds, stream)
+        loss = new(shape[:-1], float32) if loss is None else loss
+        lse = new(shape[:-1], float32) if lse is None else lse
+    st = (_lib or library()).distill_forward(
+        ds.handle, lp, ls, _code(logits), ip, vp, v_code, temperature,
+        _row_values(loss, rows, "loss", ds), _row_values(lse, rows, "lse", ds), rows,
+        _stream(stream, ds.device))
+    if st != OK:
+        _check(st, "distill_forward")
+    return loss, lse
+
+
+def distill_backward(ds: Distillation, logits, ids, values, lse, temperature: float = 1.0,
+                     dloss=None, scale: float = 1.0, dlogits=None, stream=None):
+    """dlogits of sum(scale dloss loss), lse from the forward pass; allocated
+    if not given (for the stream if one is); may be logits.  dloss: float32,
+    one a row (None: 1)."""
+    shape, kind = logits.shape, logits.dtype
+    lp, ls, rows = _spaced(logits, shape, ds.cols, ds, "logits")
+    ip, vp, v_code = _entries(ds, ids, values, rows)
+    if dlogits is None:
+        dlogits = _allocator(ds, stream)(shape, kind)
+    if dlogits.dtype is not kind or dlogits.shape != shape:
+        raise TypeError("dlogits must have the type and shape of logits")
+    dp, dst, _ = _spaced(dlogits, shape, ds.cols, ds, "dlogits")
+    st = (_lib or library()).distill_backward(
+        ds.handle, lp, ls, _code(logits), ip, vp, v_code, temperature,
+        _row_values(lse, rows, "lse", ds),
+        None if dloss is None else _row_values(dloss, rows, "dloss", ds), scale, dp, dst, rows,
+        _stream(stream, ds.device))
+    if st != OK:
+        _check(st, "distill_backward")
+    return dlogits
 
 
 def ckpt_pack(ctx: Context, step: int, w, m, v, main_stream=None, side_stream=None):

@@ -1,0 +1,285 @@
+// cross_entropy.cu -- loss and gradient of a softmax over a large vocabulary.
+//
+// Logits are 2 vocab dim operations a row and never leave the tensor memory:
+// the epilogue of each tile turns 256 of them a row into a maximum and a sum
+// of exponentials (forward), or into the logits' gradient, in 16 bits, for a
+// piece of the vocabulary (backward).  In powers of two: with l' = l log2 e,
+// a row's m = max l' and s = sum 2^(l' - m) give lse = (m + log2 s) ln 2; the
+// rounding of m cancels.
+#include <cmath>
+
+#include "cross_entropy.h"
+#include "gemm.cuh"
+#include "linear_dev.cuh"
+
+namespace osr {
+namespace {
+
+using namespace detail;
+
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// What exponentials are taken relative to: never -inf, of which the
+// difference to itself is no number.
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
+
+struct PartsEpilogue {
+    struct Params {
+        const int64_t* target;
+        float2* parts;
+        float* at;
+    };
+    int32_t row, part;
+    int64_t target;
+    float most = -INFINITY, sum = 0.0f;  // most in units of the logits
+
+    __device__ PartsEpilogue(const Params& p, const GemmShape& s, int32_t r, const GemmItem& it,
+                             int32_t half)
+        : row(r), part(it.tile_n * kCeParts + half), target(r < s.m ? p.target[r] : -1)
+    {
+    }
+    template <int C>
+    __device__ __forceinline__ void chunk(const Params& p, const GemmShape& s, int32_t column,
+                                          float (&v)[C], float*)
+    {
+        if (column >= s.n)
+            return;
+        if (column + C > s.n)
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                if (column + i >= s.n)
+                    v[i] = -INFINITY;
+        const int64_t off = target - column;
+        if (off >= 0 && off < C && row < s.m) {
+            float at = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                at = off == i ? v[i] : at;
+            if (target < s.n)
+                p.at[row] = at;
+        }
+        float top[4] = {fmaxf(most, v[0]), v[1], v[2], v[3]};
+#pragma unroll
+        for (int i = 4; i < C; ++i)
+            top[i % 4] = fmaxf(top[i % 4], v[i]);
+        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const float base = reference(now) * kLog2E;
+        float add[4] = {sum * exp2_fast(fmaf(most, kLog2E, -base)), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            add[i % 4] += exp2_fast(fmaf(v[i], kLog2E, -base));
+        sum = (add[0] + add[1]) + (add[2] + add[3]);
+        most = now;
+    }
+    __device__ void end(const Params& p, const GemmShape& s)
+    {
+        if (row < s.m)
+            p.parts[int64_t(part) * s.m + row] = make_float2(reference(most) * kLog2E, sum);
+    }
+};
+
+// A block joins the parts of 32 rows: eight threads a row, each every eighth.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) k_ce_join(const CeJoin a)
+{
+    __shared__ float2 part[8][32];
+    wait_before();
+    go_ahead();
+    const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
+    const int64_t row = int64_t(blockIdx.x) * 32 + lane;
+    float most = -INFINITY, sum = 0.0f;
+    if (row < a.rows)
+#pragma unroll 8
+        for (int32_t i = group; i < a.count; i += 8) {
+            const float2 p = __ldcg(a.parts + i * a.rows + row);
+            // a part without columns has the sum 0, whatever its maximum
+            const float now = p.y == 0.0f ? most : fmaxf(most, p.x);
+            const float base = reference(now);
+            sum = sum * exp2f(most - base) + p.y * exp2f(fminf(p.x - base, 0.0f));
+            most = now;
+        }
+    part[group][lane] = make_float2(reference(most), sum);
+    __syncthreads();
+    if (group > 0 || row >= a.rows)
+        return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+        top = part[g][lane].y == 0.0f ? top : fmaxf(top, part[g][lane].x);
+    const float base = reference(top);
+    float total = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+        total += part[g][lane].y * exp2f(fminf(part[g][lane].x - base, 0.0f));
+    const float lse = (base + log2f(total)) * kLn2;
+    if (a.lse)
+        a.lse[row] = lse;
+    const int64_t t = a.target[row];
+    a.loss[row] = t < 0          ? 0.0f
+                  : t >= a.vocab ? NAN
+                                 : lse - a.at[row] + a.z_loss * lse * lse;
+}
+
+// One block: the largest factor, then the rows' factors.
+constexpr int kRowsThreads = 1024;
+__global__ void __launch_bounds__(kRowsThreads) k_ce_rows(const CeRows a)
+{
+    __shared__ float largest[32];
+    wait_before();
+    go_ahead();
+    const float scale = float(a.scale), z2 = float(2.0 * a.z_loss);
+    const auto factors = [&](int64_t r) {
+        const int64_t t = a.target[r];
+        if (t < 0)
+            return make_float2(0.0f, 0.0f);
+        if (t >= a.vocab)
+            return make_float2(NAN, NAN);
+        const float g = scale * (a.dloss ? a.dloss[r] : 1.0f);
+        return make_float2(g * fmaf(z2, a.lse[r], 1.0f), g);
+    };
+    float most = 0.0f;
+    for (int64_t r = threadIdx.x; r < a.rows; r += kRowsThreads) {
+        const float2 f = factors(r);
+        most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, off));
+    if (threadIdx.x % 32 == 0)
+        largest[threadIdx.x / 32] = most;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        most = fmaxf(most, largest[i]);
+    // The gradient of a logit is at most twice the largest factor.  binary16
+    // ends at 65504 and loses bits below 2^-14, so the largest goes to
+    // [2^14, 2^15); bfloat16 has float32's range.
+    int shift = 0;
+    if (!a.bf16 && most > 0.0f && most < INFINITY)
+        shift = min(max(14 - (int(__float_as_uint(most) >> 23) - 127), -100), 100);
+    const float norm = __uint_as_float(uint32_t(127 + shift) << 23);
+    for (int64_t r = threadIdx.x; r < a.rows; r += kRowsThreads) {
+        const float2 f = factors(r);
+        a.factors[r] = make_float2(f.x * norm, f.y * norm);
+    }
+    if (threadIdx.x == 0)
+        *a.unnorm = __uint_as_float(uint32_t(127 - shift) << 23);
+}
+
+struct GradientEpilogue {
+    struct Params {
+        const int64_t* target;
+        const float* lse;
+        const float2* factors;
+        uint16_t* gradient;
+        int64_t stride;
+        int32_t first;
+        bool bf16;
+    };
+    int32_t row;
+    bool counts;
+    int64_t target;  // in the piece
+    float base;
+    float2 factor;
+
+    __device__ GradientEpilogue(const Params& p, const GemmShape& s, int32_t r, const GemmItem&,
+                                int32_t)
+        : row(r), counts(false), target(-1), base(0.0f), factor(make_float2(0.0f, 0.0f))
+    {
+        if (r >= s.m)
+            return;
+        factor = p.factors[r];
+        const int64_t t = p.target[r];
+        counts = t >= 0;
+        base = p.lse[r] * kLog2E;
+        target = t - p.first;
+    }
+    template <int C>
+    __device__ __forceinline__ void chunk(const Params& p, const GemmShape& s, int32_t column,
+                                          float (&v)[C], float*)
+    {
+        if (column >= s.n || row >= s.m)
+            return;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            v[i] = exp2_fast(fmaf(v[i], kLog2E, -base)) * factor.x;
+        const int64_t off = target - column;
+        if (off >= 0 && off < C)
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                v[i] -= off == i ? factor.y : 0.0f;
+        if (!counts)  // whatever its logits
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                v[i] = 0.0f;
+        uint16_t* const to = p.gradient + row * p.stride + column;
+#pragma unroll
+        for (int i = 0; i < C; i += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[j] = narrow32(v[i + 2 * j], v[i + 2 * j + 1], p.bf16);
+            store32(to + i, w);
+        }
+    }
+    __device__ void end(const Params&, const GemmShape&) {}
+};
+
+template <typename E>
+int run(const GemmOperand& x, const GemmOperand& weight, bool bf16, const typename E::Params& p,
+        int sm_count, int32_t* gave_up, void* stream)
+{
+    CUtensorMap mx, mw;
+    int e = gemm_map(x, 128, bf16, &mx);
+    if (e == cudaSuccess)
+        e = gemm_map(weight, kCeColumns / 2, bf16, &mw);
+    if (e != cudaSuccess)
+        return e;
+    GemmShape s{};
+    s.m = int32_t(x.outer);
+    s.n = int32_t(weight.outer);
+    s.tiles_m = (s.m + kGemmTileM - 1) / kGemmTileM;
+    s.tiles_n = (s.n + kCeColumns - 1) / kCeColumns;
+    s.splits = 1;
+    s.blocks = int32_t((x.inner + kGemmInner - 1) / kGemmInner);
+    s.what = mma_what(bf16, x.across, weight.across, kGemmTileM, kCeColumns);
+    s.a_across = x.across;
+    s.b_across = weight.across;
+    s.gave_up = gave_up;
+    return gemm_launch<kCeColumns, E>(mx, mw, s, p, sm_count, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+int launch_ce_parts(const CeForward& a, int sm_count, int32_t* gave_up, void* stream)
+{
+    return run<PartsEpilogue>(a.x, a.weight, a.bf16, {a.target, a.parts, a.at}, sm_count, gave_up,
+                              stream);
+}
+
+int launch_ce_join(const CeJoin& a, void* stream)
+{
+    return launch_early(k_ce_join, dim3(unsigned((a.rows + 31) / 32)), kJoinThreads, 0,
+                        static_cast<cudaStream_t>(stream), a);
+}
+
+int launch_ce_rows(const CeRows& a, void* stream)
+{
+    return launch_early(k_ce_rows, dim3(1), kRowsThreads, 0, static_cast<cudaStream_t>(stream), a);
+}
+
+int launch_ce_gradient(const CeGradient& a, int sm_count, int32_t* gave_up, void* stream)
+{
+    return run<GradientEpilogue>(a.x, a.weight, a.bf16,
+                                 {a.target, a.lse, a.factors, static_cast<uint16_t*>(a.gradient),
+                                  a.stride, a.first, a.bf16},
+                                 sm_count, gave_up, stream);
+}
+
+}  // namespace osr

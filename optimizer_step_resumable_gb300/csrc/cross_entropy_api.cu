@@ -1,0 +1,385 @@
+// cross_entropy_api.cu -- the C ABI entry points of the cross entropy over a
+// vocabulary (linear_cross_entropy_* of include/adamw_ckpt.h).
+#include <cmath>
+#include <cstdint>
+#include <new>
+
+#include <cuda_runtime.h>
+
+#include "api_util.h"
+#include "arrays.h"
+#include "cross_entropy.h"
+#include "linear.h"
+#include "product_ctx.h"
+
+struct linear_ce_ctx {
+    osr::ProductContext base;
+    int32_t dim = 0, vocab = 0;
+};
+
+namespace {
+
+using osr::check_apart;
+using osr::check_array;
+using osr::check_rows;
+using osr::cuda_fail;
+using osr::DeviceScope;
+using osr::fail;
+using osr::gemm_readable;
+using osr::GemmOperand;
+using osr::kCeColumns;
+using osr::kCeParts;
+using osr::known_dtype;
+using osr::LinearProduct;
+using osr::on_vectors;
+using osr::Pieces;
+using osr::readable;
+using osr::rows_of;
+using osr::size_of;
+using osr::vector_of;
+using osr::whole;
+using osr::Workspace;
+
+constexpr int32_t kMaxDim = 1 << 20, kMaxVocab = 1 << 24;
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+// The gradient of a piece's logits takes this many bytes at most (or 256
+// columns).
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+
+int64_t tiles(int64_t vocab) { return (vocab + kCeColumns - 1) / kCeColumns; }
+
+// Columns of a piece: equal pieces of whole tiles.
+int64_t piece_columns(int64_t rows, int64_t vocab)
+{
+    int64_t most = kPieceBytes / (2 * rows) / kCeColumns;
+    most = most > 1 ? most : 1;
+    const int64_t all = tiles(vocab), pieces = (all + most - 1) / most;
+    return (all + pieces - 1) / pieces * kCeColumns;
+}
+
+struct Needs {
+    bool backward, copy_x, copy_weight, in_out, dx, dweight, grad_in_out;
+};
+struct Parts {
+    void* x = nullptr;
+    void* weight = nullptr;
+    float2* parts = nullptr;  // forward
+    float* at = nullptr;
+    float2* factors = nullptr;  // backward
+    float* unnorm = nullptr;
+    void* gradient = nullptr;
+    float* dx = nullptr;  // the sum over the pieces so far
+    float* partials = nullptr;
+    int64_t piece = 0;
+};
+
+int64_t lay_out(const linear_ce_ctx* c, int64_t rows, const Needs& n, void* memory, Parts* p)
+{
+    Workspace w(memory);
+    const int sms = c->base.sm_count;
+    if (n.copy_x)
+        p->x = w.take(2 * rows * whole(c->dim));
+    if (n.copy_weight)
+        p->weight = w.take(2 * (n.in_out ? c->dim * whole(c->vocab) : c->vocab * whole(c->dim)));
+    if (!n.backward) {
+        p->parts = static_cast<float2*>(w.take(8 * rows * kCeParts * tiles(c->vocab)));
+        p->at = static_cast<float*>(w.take(4 * rows));
+        return w.bytes();
+    }
+    p->piece = piece_columns(rows, c->vocab);
+    p->factors = static_cast<float2*>(w.take(8 * rows));
+    p->unnorm = static_cast<float*>(w.take(4));
+    p->gradient = w.take(2 * rows * p->piece);
+    int64_t partials = 0;
+    // of the first piece, and of the last, which may be shorter
+    const int64_t last = c->vocab - (c->vocab - 1) / p->piece * p->piece;
+    const int64_t sizes[] = {c->vocab < p->piece ? c->vocab : p->piece, last};
+    for (const int64_t columns : sizes) {
+        if (n.dx) {
+            const int64_t s = osr::linear_plan(rows, c->dim, columns, false, sms).partials;
+            partials = partials > s ? partials : s;
+        }
+        if (n.dweight) {
+            const int64_t s = osr::linear_plan(n.grad_in_out ? c->dim : columns,
+                                               n.grad_in_out ? columns : c->dim, rows, true, sms)
+                                  .partials;
+            partials = partials > s ? partials : s;
+        }
+    }
+    if (n.dx && p->piece < c->vocab)
+        p->dx = static_cast<float*>(w.take(4 * rows * whole(c->dim)));
+    if (partials)
+        p->partials = static_cast<float*>(w.take(4 * partials));
+    return w.bytes();
+}
+
+int check_common(linear_ce_ctx* ctx, int32_t dtype, int64_t rows, int32_t flags, int32_t known)
+{
+    if (!ctx)
+        return fail(ADAMW_EINVAL, "ctx is NULL");
+    if (dtype != ADAMW_DTYPE_BF16 && dtype != ADAMW_DTYPE_F16)
+        return fail(ADAMW_EINVAL, "dtype=%d is not BF16 or F16", dtype);
+    if (rows < 0 || rows > kMaxRows)
+        return fail(ADAMW_EINVAL, "rows=%lld outside [0, 2^30]", (long long)rows);
+    if (flags & ~known)
+        return fail(ADAMW_EINVAL, "unknown flags 0x%x", flags);
+    return ADAMW_OK;
+}
+
+int64_t high(const linear_ce_ctx* c, bool in_out) { return in_out ? c->dim : c->vocab; }
+int32_t wide(const linear_ce_ctx* c, bool in_out) { return in_out ? c->vocab : c->dim; }
+
+}  // namespace
+
+extern "C" {
+
+int linear_cross_entropy_create(int32_t dim, int32_t vocab, linear_ce_ctx** out)
+{
+    osr::clear_error();
+    if (!out)
+        return fail(ADAMW_EINVAL, "out is NULL");
+    *out = nullptr;
+    if (dim < 1 || dim > kMaxDim)
+        return fail(ADAMW_EINVAL, "dim=%d outside [1, 2^20]", dim);
+    if (vocab < 1 || vocab > kMaxVocab)
+        return fail(ADAMW_EINVAL, "vocab=%d outside [1, 2^24]", vocab);
+    linear_ce_ctx* c = new (std::nothrow) linear_ce_ctx;
+    if (!c)
+        return fail(ADAMW_EINVAL, "out of host memory");
+    c->dim = dim;
+    c->vocab = vocab;
+    const int rc = osr::product_create(&c->base);
+    if (rc != ADAMW_OK) {
+        osr::product_free(&c->base);
+        delete c;
+        return rc;
+    }
+    *out = c;
+    return ADAMW_OK;
+}
+
+int linear_cross_entropy_destroy(linear_ce_ctx* ctx)
+{
+    osr::clear_error();
+    if (ctx) {
+        osr::product_free(&ctx->base);
+        delete ctx;
+    }
+    return ADAMW_OK;
+}
+
+int linear_cross_entropy_workspace(linear_ce_ctx* ctx, int64_t rows, int32_t flags, int64_t* bytes)
+{
+    osr::clear_error();
+    const int rc = check_common(ctx, ADAMW_DTYPE_BF16, rows, flags,
+                                LINEAR_FOR_BACKWARD | LINEAR_FOR_ANY_ADDRESS);
+    if (rc != ADAMW_OK)
+        return rc;
+    if (!bytes)
+        return fail(ADAMW_EINVAL, "bytes is NULL");
+    *bytes = 0;
+    if (rows == 0)
+        return ADAMW_OK;
+    const bool back = flags & LINEAR_FOR_BACKWARD, any = flags & LINEAR_FOR_ANY_ADDRESS;
+    // the most that any layout of the weight and its gradient takes
+    for (int layout = 0; layout < 4; ++layout) {
+        Parts p;
+        const Needs n{back, any, any, (layout & 1) != 0, back, back, (layout & 2) != 0};
+        const int64_t b = lay_out(ctx, rows, n, nullptr, &p);
+        *bytes = *bytes > b ? *bytes : b;
+    }
+    return ADAMW_OK;
+}
+
+int linear_cross_entropy_forward(linear_ce_ctx* ctx, const void* d_x, int64_t x_stride,
+                                 const void* d_weight, int64_t weight_stride, int32_t dtype,
+                                 const int64_t* d_target, double z_loss, float* d_loss,
+                                 float* d_lse, int64_t rows, int32_t flags, void* d_workspace,
+                                 int64_t workspace_bytes, void* stream)
+{
+    osr::clear_error();
+    int rc = check_common(ctx, dtype, rows, flags, LINEAR_IN_OUT);
+    if (rc != ADAMW_OK)
+        return rc;
+    const bool in_out = flags & LINEAR_IN_OUT;
+    const int64_t w_rows = high(ctx, in_out);
+    const int32_t w_cols = wide(ctx, in_out), dim = ctx->dim;
+    if ((rc = check_rows(d_x, x_stride, rows, dim, 2, "d_x")) ||
+        (rc = check_rows(d_weight, weight_stride, w_rows, w_cols, 2, "d_weight")) ||
+        (rc = check_array(d_target, 8, rows == 0, "d_target")) ||
+        (rc = check_array(d_loss, 4, rows == 0, "d_loss")) ||
+        (rc = check_array(d_lse, 4, true, "d_lse")))
+        return rc;
+    if (!std::isfinite(float(z_loss)))
+        return fail(ADAMW_EINVAL, "z_loss=%g is not finite", z_loss);
+    const Pieces outs[] = {vector_of(d_loss, rows, 4, "d_loss"),
+                           vector_of(d_lse, rows, 4, "d_lse")};
+    const Pieces ins[] = {rows_of(d_x, x_stride, rows, dim, 2, "d_x"),
+                          rows_of(d_weight, weight_stride, w_rows, w_cols, 2, "d_weight"),
+                          vector_of(d_target, rows, 8, "d_target")};
+    if ((rc = check_apart(outs, ins)))
+        return rc;
+    if ((rc = osr::product_state(&ctx->base)))
+        return rc;
+    if (rows == 0)
+        return ADAMW_OK;
+    Needs n{};
+    n.copy_x = !gemm_readable(d_x, rows > 1 ? x_stride : 0);
+    n.copy_weight = !gemm_readable(d_weight, w_rows > 1 ? weight_stride : 0);
+    n.in_out = in_out;
+    Parts p;
+    if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
+                                   lay_out(ctx, rows, n, d_workspace, &p))))
+        return rc;
+    DeviceScope scope(ctx->base.device);
+    int e = readable(&d_x, &x_stride, rows, dim, p.x, stream);
+    if (e == cudaSuccess)
+        e = readable(&d_weight, &weight_stride, w_rows, w_cols, p.weight, stream);
+    if (e == cudaSuccess)
+        e = osr::launch_ce_parts(
+            osr::CeForward{GemmOperand{d_x, rows, dim, x_stride, false},
+                           GemmOperand{d_weight, ctx->vocab, dim, weight_stride, in_out},
+                           dtype == ADAMW_DTYPE_BF16, d_target, p.parts, p.at},
+            ctx->base.sm_count, ctx->base.gave_up, stream);
+    if (e == cudaSuccess)
+        e = osr::launch_ce_join(osr::CeJoin{p.parts, int32_t(kCeParts * tiles(ctx->vocab)), p.at,
+                                            d_target, rows, ctx->vocab, float(z_loss), d_loss,
+                                            d_lse},
+                                stream);
+    return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "cross entropy launch");
+}
+
+int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x_stride,
+                                  const void* d_weight, int64_t weight_stride, int32_t dtype,
+                                  const int64_t* d_target, const float* d_lse,
+                                  const float* d_dloss, double scale, double z_loss, void* d_dx,
+                                  int64_t dx_stride, void* d_dweight, int64_t dweight_stride,
+                                  int32_t grad_dtype, int64_t rows, int32_t flags,
+                                  void* d_workspace, int64_t workspace_bytes, void* stream)
+{
+    osr::clear_error();
+    int rc = check_common(ctx, dtype, rows, flags,
+                          LINEAR_IN_OUT | LINEAR_GRAD_IN_OUT | LINEAR_ACCUMULATE);
+    if (rc != ADAMW_OK)
+        return rc;
+    if (!known_dtype(grad_dtype))
+        return fail(ADAMW_EINVAL, "grad_dtype=%d is not F32, BF16 or F16", grad_dtype);
+    const bool in_out = flags & LINEAR_IN_OUT, grad_in_out = flags & LINEAR_GRAD_IN_OUT;
+    const int64_t w_rows = high(ctx, in_out), g_rows = d_dweight ? high(ctx, grad_in_out) : 0;
+    const int64_t w_read = rows ? w_rows : 0;
+    const int32_t w_cols = wide(ctx, in_out), g_cols = wide(ctx, grad_in_out);
+    const int32_t dim = ctx->dim, vocab = ctx->vocab;
+    const int64_t dx_rows = d_dx ? rows : 0;
+    const size_t gs = size_of(grad_dtype);
+    if ((rc = check_rows(d_x, x_stride, rows, dim, 2, "d_x")) ||
+        (rc = check_rows(d_weight, weight_stride, w_read, w_cols, 2, "d_weight")) ||
+        (rc = check_array(d_target, 8, rows == 0, "d_target")) ||
+        (rc = check_array(d_lse, 4, rows == 0, "d_lse")) ||
+        (rc = check_array(d_dloss, 4, true, "d_dloss")) ||
+        (rc = check_rows(d_dx, dx_stride, dx_rows, dim, 2, "d_dx")) ||
+        (rc = check_rows(d_dweight, dweight_stride, g_rows, g_cols, gs, "d_dweight")))
+        return rc;
+    if (!std::isfinite(float(z_loss)))
+        return fail(ADAMW_EINVAL, "z_loss=%g is not finite", z_loss);
+    if (!std::isfinite(float(scale)))
+        return fail(ADAMW_EINVAL, "scale=%g is not finite", scale);
+    const Pieces outs[] = {rows_of(d_dx, dx_stride, dx_rows, dim, 2, "d_dx"),
+                           rows_of(d_dweight, dweight_stride, g_rows, g_cols, gs, "d_dweight")};
+    const Pieces ins[] = {rows_of(d_x, x_stride, rows, dim, 2, "d_x"),
+                          rows_of(d_weight, weight_stride, w_read, w_cols, 2, "d_weight"),
+                          vector_of(d_target, rows, 8, "d_target"),
+                          vector_of(d_lse, rows, 4, "d_lse"),
+                          vector_of(d_dloss, rows, 4, "d_dloss")};
+    if ((rc = check_apart(outs, ins)))
+        return rc;
+    if ((rc = osr::product_state(&ctx->base)))
+        return rc;
+    DeviceScope scope(ctx->base.device);
+    const int sms = ctx->base.sm_count;
+    osr::LinearOut dw{};
+    dw.out = d_dweight;
+    dw.stride = dweight_stride;
+    dw.dtype = grad_dtype;
+    dw.alpha = 1.0f;
+    dw.accumulate = (flags & LINEAR_ACCUMULATE) != 0;
+    dw.vectors = on_vectors(d_dweight, dweight_stride, g_rows, gs);
+    int e = cudaSuccess;
+    if (rows == 0) {
+        if (d_dweight)
+            e = osr::launch_linear_zero(dw, g_rows, g_cols, sms, stream);
+        return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "cross entropy launch");
+    }
+    if (!d_dx && !d_dweight)
+        return ADAMW_OK;
+    Needs n{};
+    n.backward = true;
+    n.copy_x = !gemm_readable(d_x, rows > 1 ? x_stride : 0);
+    n.copy_weight = !gemm_readable(d_weight, w_rows > 1 ? weight_stride : 0);
+    n.in_out = in_out;
+    n.dx = d_dx;
+    n.dweight = d_dweight;
+    n.grad_in_out = grad_in_out;
+    Parts p;
+    if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
+                                   lay_out(ctx, rows, n, d_workspace, &p))))
+        return rc;
+    const bool bf16 = dtype == ADAMW_DTYPE_BF16;
+    e = readable(&d_x, &x_stride, rows, dim, p.x, stream);
+    if (e == cudaSuccess)
+        e = readable(&d_weight, &weight_stride, w_rows, w_cols, p.weight, stream);
+    if (e == cudaSuccess)
+        e = osr::launch_ce_rows(osr::CeRows{d_target, d_lse, d_dloss, scale, z_loss, rows, vocab,
+                                            bf16, p.factors, p.unnorm},
+                                stream);
+    for (int64_t first = 0; first < vocab && e == cudaSuccess; first += p.piece) {
+        const int64_t columns = vocab - first < p.piece ? vocab - first : p.piece;
+        const uint16_t* const w =
+            static_cast<const uint16_t*>(d_weight) + first * (in_out ? 1 : weight_stride);
+        e = osr::launch_ce_gradient(
+            osr::CeGradient{GemmOperand{d_x, rows, dim, x_stride, false},
+                            GemmOperand{w, columns, dim, weight_stride, in_out}, bf16, d_target,
+                            d_lse, p.factors, int32_t(first), p.gradient, p.piece},
+            sms, ctx->base.gave_up, stream);
+        if (e == cudaSuccess && d_dx) {
+            // the pieces' sum in float32; the last one leaves with it
+            const bool last = first + columns == vocab;
+            LinearProduct m{};
+            m.a = GemmOperand{p.gradient, rows, columns, p.piece, false};
+            m.b = GemmOperand{w, dim, columns, weight_stride, !in_out};
+            m.bf16 = bf16;
+            m.to.out = last ? d_dx : p.dx;
+            m.to.stride = last ? dx_stride : whole(dim);
+            m.to.dtype = last ? dtype : ADAMW_DTYPE_F32;
+            if (first > 0) {
+                m.to.residual = p.dx;
+                m.to.residual_stride = whole(dim);
+                m.to.residual_dtype = ADAMW_DTYPE_F32;
+            }
+            m.to.alpha = 1.0f;
+            m.to.alpha_factor = p.unnorm;
+            m.to.vectors = last ? on_vectors(d_dx, dx_stride, rows, 2) : 1;
+            e = osr::linear_product(m, osr::linear_plan(rows, dim, columns, false, sms), p.partials,
+                                    sms, ctx->base.gave_up, stream);
+        }
+        if (e == cudaSuccess && d_dweight) {
+            LinearProduct m{};
+            m.a = GemmOperand{p.gradient, columns, rows, p.piece, true};
+            m.b = GemmOperand{d_x, dim, rows, x_stride, true};
+            m.bf16 = bf16;
+            m.to = dw;
+            m.to.out = static_cast<char*>(d_dweight) +
+                       int64_t(gs) * first * (grad_in_out ? 1 : dweight_stride);
+            m.to.alpha_factor = p.unnorm;
+            if (grad_in_out) {
+                const GemmOperand a = m.a;
+                m.a = m.b;
+                m.b = a;
+            }
+            e = osr::linear_product(m, osr::linear_plan(m.a.outer, m.b.outer, rows, true, sms),
+                                    p.partials, sms, ctx->base.gave_up, stream);
+        }
+    }
+    return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "cross entropy launch");
+}
+
+}  // extern "C"

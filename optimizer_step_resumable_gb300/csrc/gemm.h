@@ -1,0 +1,50 @@
+// gemm.h -- the tiled matrix product on the tensor cores that the linear
+// layer and the cross entropy share: what the host code that plans and
+// launches it needs.  Not part of the ABI.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+
+#include "internal.h"
+
+namespace osr {
+
+// A matrix of 16-bit elements as an operand.  `outer` is the dimension that
+// appears in the product, `inner` the one that is summed over.  `across`:
+// elements that are adjacent in memory are neighbours in the outer dimension.
+struct GemmOperand {
+    const void* p;
+    int64_t outer, inner;
+    int64_t stride;  // elements between two rows of memory
+    bool across;
+};
+
+// What the kernel is told about one product of `m` x `n` over the inner
+// dimension, in tiles of 256 x BN shared by two blocks, the inner dimension
+// cut into `splits` ranges of blocks of 64.
+struct GemmShape {
+    int32_t m, n;
+    int32_t tiles_m, tiles_n, splits, blocks;
+    uint32_t what;  // mma_what
+    int32_t a_across, b_across;
+    int32_t* gave_up;  // set to 1 if a wait ran out (host memory)
+};
+
+constexpr int kGemmTileM = 256, kGemmInner = 64;
+
+// Whether the tiled copies can read a matrix: its address and row distance on
+// 16-byte boundaries.
+inline bool gemm_readable(const void* p, int64_t stride)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0;
+}
+
+// Resolves the driver's encoder of tensor maps, once a process; cudaError_t.
+int gemm_init();
+// The map of an operand whose tile in a block is `rows` x 64 of the outer and
+// the inner dimension.
+int gemm_map(const GemmOperand& o, int rows, bool bf16, CUtensorMap* map);
+
+}  // namespace osr

@@ -1,0 +1,77 @@
+// linear.h -- the linear layer: what its entry points (linear_api.cu) and its
+// kernels share.  Not part of the ABI.
+#pragma once
+
+#include <cstdint>
+
+#include "gemm.h"
+#include "internal.h"
+
+namespace osr {
+
+// Where a product goes: out = act(alpha sum + bias) + residual, or added to
+// what is there.  The row distances are in elements.
+struct LinearOut {
+    void* out;
+    int64_t stride;
+    int32_t dtype;  // of out and z
+    const void* bias;  // NULL: 0; one per column
+    int32_t bias_dtype;
+    const void* residual;  // NULL: none; may be out
+    int64_t residual_stride;
+    int32_t residual_dtype;
+    void* z;  // NULL: not kept
+    int64_t z_stride;
+    int32_t act;
+    int32_t accumulate;
+    float alpha;
+    const float* alpha_factor;  // on the device, multiplies alpha; NULL: 1
+    int32_t vectors;            // rows of out, residual and z on 32-byte boundaries
+};
+
+// out (rows x columns) from a (rows x inner) and b (columns x inner).
+struct LinearProduct {
+    GemmOperand a, b;
+    bool bf16;
+    LinearOut to;
+};
+// How it is computed: in tiles of 256 x bn with the inner dimension in
+// `splits` ranges whose sums a second kernel joins; swapped: the tile's long
+// side lies along the columns, for products of few rows.
+struct LinearPlan {
+    bool swapped;
+    int32_t bn, splits;
+    int64_t partials;  // float32 sums in the workspace
+};
+// a_across: whether a's outer dimension is the adjacent one.
+LinearPlan linear_plan(int64_t rows, int64_t columns, int64_t inner, bool a_across, int sm_count);
+int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partials, int sm_count,
+                   int32_t* gave_up, void* stream);
+// A product over nothing.
+int launch_linear_zero(const LinearOut& to, int64_t rows, int64_t columns, int sm_count,
+                       void* stream);
+
+// dz = dy act'(z), rounded to their type, into rows of `stride` elements, and
+// its column sums (of the unrounded values), which a second kernel joins.
+struct LinearSlope {
+    const void* dy;
+    int64_t dy_stride;
+    const void* z;  // NULL if act is LINEAR_NONE
+    int64_t z_stride;
+    int32_t act;
+    bool bf16;
+    void* dz;  // NULL: not wanted
+    int64_t stride;
+    int64_t rows, columns;
+    float* partials;  // strips x columns; NULL: no sums
+    int32_t strips;
+};
+int linear_strips(int64_t rows, int64_t columns, int sm_count);
+int launch_linear_slope(const LinearSlope& a, void* stream);
+int launch_linear_bias_grad(const float* partials, int32_t strips, int64_t columns, void* dbias,
+                            int32_t dtype, bool accumulate, void* stream);
+// Rows of 16-bit elements, copied to where the tiled copies can read them.
+int launch_copy_rows(const void* from, int64_t from_stride, void* to, int64_t to_stride,
+                     int64_t rows, int64_t columns, void* stream);
+
+}  // namespace osr

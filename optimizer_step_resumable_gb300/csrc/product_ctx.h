@@ -1,0 +1,115 @@
+// product_ctx.h -- what the contexts of operators made of tiled products
+// share: their device, the word in which a kernel says that a wait of its ran
+// out, and the division of a call's workspace.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "api_util.h"
+#include "gemm.h"
+#include "linear.h"
+
+namespace osr {
+
+struct ProductContext {
+    int device = -1;
+    int sm_count = 0;
+    int32_t* h_gave_up = nullptr;  // pinned, mapped
+    int32_t* gave_up = nullptr;    // its device address
+};
+
+inline int product_create(ProductContext* c)
+{
+    cudaError_t e = cudaGetDevice(&c->device);
+    if (e != cudaSuccess) {
+        c->device = -1;
+        return cuda_fail(e, "cudaGetDevice");
+    }
+    CUDA_TRY(cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device));
+    e = cudaError_t(gemm_init());
+    if (e != cudaSuccess)
+        return cuda_fail(e, "cuTensorMapEncodeTiled");
+    CUDA_TRY(cudaHostAlloc(reinterpret_cast<void**>(&c->h_gave_up), sizeof(int32_t),
+                           cudaHostAllocMapped | cudaHostAllocPortable));
+    *c->h_gave_up = 0;
+    CUDA_TRY(cudaHostGetDevicePointer(reinterpret_cast<void**>(&c->gave_up), c->h_gave_up, 0));
+    return ADAMW_OK;
+}
+
+// cudaFreeHost waits for the device's work.
+inline void product_free(ProductContext* c)
+{
+    if (c->device >= 0 && c->h_gave_up) {
+        DeviceScope scope(c->device);
+        cudaFreeHost(c->h_gave_up);
+    }
+}
+
+inline int product_state(ProductContext* c)
+{
+    volatile int32_t* const word = c->h_gave_up;
+    if (!*word)
+        return ADAMW_OK;
+    *word = 0;
+    return fail(ADAMW_ESTATE,
+                "a kernel of an earlier call gave up waiting: its outputs are not valid");
+}
+
+// Parts of a call's workspace, each on a 256-byte boundary.
+class Workspace {
+public:
+    explicit Workspace(void* memory) : memory_(static_cast<char*>(memory)) {}
+    void* take(int64_t bytes)
+    {
+        char* const p = memory_ ? memory_ + used_ : nullptr;
+        used_ += (bytes + 255) / 256 * 256;
+        return p;
+    }
+    int64_t bytes() const { return used_; }
+
+private:
+    char* memory_;
+    int64_t used_ = 0;
+};
+
+inline int check_workspace(const void* memory, int64_t bytes, int64_t needed)
+{
+    if (needed == 0)
+        return ADAMW_OK;
+    if (!memory)
+        return fail(ADAMW_EINVAL, "d_workspace is NULL: the call needs %lld bytes",
+                    (long long)needed);
+    if (reinterpret_cast<uintptr_t>(memory) % 256)
+        return fail(ADAMW_EINVAL, "d_workspace is not on a 256-byte boundary");
+    if (bytes < needed)
+        return fail(ADAMW_EINVAL, "workspace of %lld bytes: the call needs %lld", (long long)bytes,
+                    (long long)needed);
+    return ADAMW_OK;
+}
+
+// A row's elements in whole 16-byte vectors.
+inline int64_t whole(int64_t elements) { return (elements + 7) / 8 * 8; }
+
+// Whether rows start on 32-byte boundaries.
+inline bool on_vectors(const void* p, int64_t stride, int64_t rows, size_t size)
+{
+    return reinterpret_cast<uintptr_t>(p) % 32 == 0 &&
+           (rows <= 1 || stride * int64_t(size) % 32 == 0);
+}
+
+// Makes p, rows of `columns` elements `stride` apart, one that the tiled copies
+// can read: a copy of it in `copy`, unless that is NULL.
+inline int readable(const void** p, int64_t* stride, int64_t rows, int64_t columns, void* copy,
+                    void* stream)
+{
+    if (!copy)
+        return cudaSuccess;
+    const int e = launch_copy_rows(*p, *stride, copy, whole(columns), rows, columns, stream);
+    *p = copy;
+    *stride = whole(columns);
+    return e;
+}
+
+}  // namespace osr
