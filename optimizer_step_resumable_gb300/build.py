@@ -28,7 +28,8 @@ CUDA_SOURCES = ["norm.cu", "step.cu", "onepass.cu", "ranks.cu", "pack.cu", "api.
                 "writer.cu", "graph.cu", "noalloc.cu", "list_step.cu", "list_api.cu",
                 "layernorm_fwd.cu", "layernorm_bwd.cu", "layernorm_bwd_f32.cu",
                 "layernorm_bwd_bf16.cu", "layernorm_bwd_f16.cu", "layernorm_api.cu",
-                "gemm.cu", "linear_gemm.cu", "linear_rows.cu", "linear_api.cu",
+                "gemm.cu", "linear_gemm.cu", "linear_gemm_f32.cu", "linear_gemm_bf16.cu",
+                "linear_gemm_f16.cu", "linear_rows.cu", "linear_api.cu",
                 "cross_entropy.cu", "cross_entropy_api.cu", "distill.cu", "distill_api.cu"]
 CXX_SOURCES = ["ckpt_io.cpp", "manifest.cpp", "sha256.cpp"]
 
@@ -47,7 +48,7 @@ def _sources():
                                                  "layernorm_dev.cuh", "layernorm_bwd.cuh",
                                                  "packed_dev.cuh", "early_dev.cuh", "arrays.h",
                                                  "gemm.h", "gemm.cuh", "tensor_dev.cuh", "linear.h",
-                                                 "linear_dev.cuh", "product_ctx.h",
+                                                 "linear_dev.cuh", "linear_gemm.cuh", "product_ctx.h",
                                                  "cross_entropy.h", "distill.h")]
             + [os.path.join(INCLUDE, "adamw_ckpt.h")])
 

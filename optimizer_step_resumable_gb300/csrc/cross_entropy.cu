@@ -9,8 +9,7 @@
 #include <cmath>
 
 #include "cross_entropy.h"
-#include "gemm.cuh"
-#include "linear_dev.cuh"
+#include "linear_gemm.cuh"
 
 namespace osr {
 namespace {
@@ -39,13 +38,13 @@ struct PartsEpilogue {
     int64_t target;
     float most = -INFINITY, sum = 0.0f;  // most in units of the logits
 
-    __device__ PartsEpilogue(const Params& p, const GemmShape& s, int32_t r, const GemmItem& it,
-                             int32_t half)
+    __device__ PartsEpilogue(const Params& p, const GemmShape& s, int32_t r, int32_t, int32_t,
+                             const GemmItem& it, int32_t half, float*)
         : row(r), part(it.tile_n * kCeParts + half), target(r < s.m ? p.target[r] : -1)
     {
     }
     template <int C>
-    __device__ __forceinline__ void chunk(const Params& p, const GemmShape& s, int32_t column,
+    __device__ __forceinline__ void chunk(const Params& p, const GemmShape& s, int32_t column, int,
                                           float (&v)[C], float*)
     {
         if (column >= s.n)
@@ -188,8 +187,8 @@ struct GradientEpilogue {
     float base;
     float2 factor;
 
-    __device__ GradientEpilogue(const Params& p, const GemmShape& s, int32_t r, const GemmItem&,
-                                int32_t)
+    __device__ GradientEpilogue(const Params& p, const GemmShape& s, int32_t r, int32_t, int32_t,
+                                const GemmItem&, int32_t, float*)
         : row(r), counts(false), target(-1), base(0.0f), factor(make_float2(0.0f, 0.0f))
     {
         if (r >= s.m)
@@ -201,7 +200,7 @@ struct GradientEpilogue {
         target = t - p.first;
     }
     template <int C>
-    __device__ __forceinline__ void chunk(const Params& p, const GemmShape& s, int32_t column,
+    __device__ __forceinline__ void chunk(const Params& p, const GemmShape& s, int32_t column, int,
                                           float (&v)[C], float*)
     {
         if (column >= s.n || row >= s.m)
@@ -235,24 +234,10 @@ template <typename E>
 int run(const GemmOperand& x, const GemmOperand& weight, bool bf16, const typename E::Params& p,
         int sm_count, int32_t* gave_up, void* stream)
 {
-    CUtensorMap mx, mw;
-    int e = gemm_map(x, 128, bf16, &mx);
-    if (e == cudaSuccess)
-        e = gemm_map(weight, kCeColumns / 2, bf16, &mw);
-    if (e != cudaSuccess)
-        return e;
     GemmShape s{};
-    s.m = int32_t(x.outer);
-    s.n = int32_t(weight.outer);
-    s.tiles_m = (s.m + kGemmTileM - 1) / kGemmTileM;
-    s.tiles_n = (s.n + kCeColumns - 1) / kCeColumns;
-    s.splits = 1;
-    s.blocks = int32_t((x.inner + kGemmInner - 1) / kGemmInner);
-    s.what = mma_what(bf16, x.across, weight.across, kGemmTileM, kCeColumns);
-    s.a_across = x.across;
-    s.b_across = weight.across;
+    s.splits = s.chains = 1;
     s.gave_up = gave_up;
-    return gemm_launch<kCeColumns, E>(mx, mw, s, p, sm_count, static_cast<cudaStream_t>(stream));
+    return gemm_run<kCeColumns, E>(x, weight, s, bf16, p, sm_count, stream);
 }
 
 }  // namespace

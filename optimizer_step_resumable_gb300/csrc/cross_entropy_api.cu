@@ -96,12 +96,13 @@ int64_t lay_out(const linear_ce_ctx* c, int64_t rows, const Needs& n, void* memo
     const int64_t sizes[] = {c->vocab < p->piece ? c->vocab : p->piece, last};
     for (const int64_t columns : sizes) {
         if (n.dx) {
-            const int64_t s = osr::linear_plan(rows, c->dim, columns, false, sms).partials;
+            const int64_t s = osr::linear_plan(rows, c->dim, columns, false, false, sms).partials;
             partials = partials > s ? partials : s;
         }
         if (n.dweight) {
             const int64_t s = osr::linear_plan(n.grad_in_out ? c->dim : columns,
-                                               n.grad_in_out ? columns : c->dim, rows, true, sms)
+                                               n.grad_in_out ? columns : c->dim, rows, true, false,
+                                               sms)
                                   .partials;
             partials = partials > s ? partials : s;
         }
@@ -301,10 +302,11 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
     dw.stride = dweight_stride;
     dw.dtype = grad_dtype;
     dw.alpha = 1.0f;
-    dw.accumulate = (flags & LINEAR_ACCUMULATE) != 0;
     dw.vectors = on_vectors(d_dweight, dweight_stride, g_rows, gs);
     int e = cudaSuccess;
     if (rows == 0) {
+        if (flags & LINEAR_ACCUMULATE)
+            osr::accumulate_into(dw);
         if (d_dweight)
             e = osr::launch_linear_zero(dw, g_rows, g_cols, sms, stream);
         return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "cross entropy launch");
@@ -358,8 +360,8 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
             m.to.alpha = 1.0f;
             m.to.alpha_factor = p.unnorm;
             m.to.vectors = last ? on_vectors(d_dx, dx_stride, rows, 2) : 1;
-            e = osr::linear_product(m, osr::linear_plan(rows, dim, columns, false, sms), p.partials,
-                                    sms, ctx->base.gave_up, stream);
+            e = osr::linear_product(m, osr::linear_plan(rows, dim, columns, false, false, sms),
+                                    p.partials, sms, ctx->base.gave_up, stream);
         }
         if (e == cudaSuccess && d_dweight) {
             LinearProduct m{};
@@ -375,8 +377,12 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
                 m.a = m.b;
                 m.b = a;
             }
-            e = osr::linear_product(m, osr::linear_plan(m.a.outer, m.b.outer, rows, true, sms),
-                                    p.partials, sms, ctx->base.gave_up, stream);
+            if (flags & LINEAR_ACCUMULATE)
+                osr::accumulate_into(m.to);
+            e = osr::linear_product(
+                m, osr::linear_plan(m.a.outer, m.b.outer, rows, true,
+                                    grad_dtype == ADAMW_DTYPE_F32, sms),
+                p.partials, sms, ctx->base.gave_up, stream);
         }
     }
     return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "cross entropy launch");

@@ -44,8 +44,9 @@ int gemm_map(const GemmOperand& o, int rows, bool bf16, CUtensorMap* map)
     // a single row may be given any distance
     const int64_t apart = high > 1 ? o.stride : (wide + 7) / 8 * 8;
     const cuuint64_t stride[1] = {cuuint64_t(apart) * 2};
-    // 64 elements are the 128 bytes of a swizzled row; never more than 64 rows
-    const cuuint32_t box[2] = {64, cuuint32_t(o.across || rows > 64 ? 64 : rows)};
+    // 64 elements are the 128 bytes of a swizzled row; across, further ones are
+    // copies of their own
+    const cuuint32_t box[2] = {64, cuuint32_t(o.across ? 64 : rows)};
     const cuuint32_t each[2] = {1, 1};
     const CUresult r = encode(
         map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,

@@ -32,10 +32,12 @@ constexpr int kGemmEpilogueWarps = 8;
 template <int BN>
 struct GemmRing {
     static constexpr int kRowsB = BN / 2;  // of B's tile, in a block
-    static constexpr int kBytesA = 128 * kGemmInner * 2, kBytesB = kRowsB * kGemmInner * 2;
+    // across, B comes in whole 64 rows
+    static constexpr int kWholeB = kRowsB < 64 ? kRowsB : (kRowsB + 63) / 64 * 64;
+    static constexpr int kBytesA = 128 * kGemmInner * 2, kBytesB = kWholeB * kGemmInner * 2;
     static constexpr int kStage = kBytesA + kBytesB;
     static constexpr int kStages = (192 * 1024) / kStage;
-    static constexpr int kAccColumns = BN;            // of tensor memory, a tile
+    static constexpr int kAccColumns = BN > 128 ? 256 : BN;  // of tensor memory, a tile
     static constexpr int kColumns = 2 * kAccColumns;  // a power of two from 32 to 512
     // tiles start on 1024 bytes; each warp of the epilogue has 32 x 33 floats
     static constexpr int kWarpStage = 32 * 33 * 4;
@@ -43,12 +45,12 @@ struct GemmRing {
 };
 
 struct GemmItem {
-    int32_t m0, tile_n, split, first, last;  // rows, tile of columns, inner blocks
+    int32_t m0, tile_n, split, chain, first, last;  // rows, tile of columns, inner blocks
 };
 
 // Items in bands of 8 tiles of rows: the tiles that run at a time form a
 // rectangle, whose rows and columns of A and B stay in L2.
-__device__ __forceinline__ GemmItem gemm_item(const GemmShape& s, int32_t item)
+__device__ __forceinline__ GemmItem gemm_item(const GemmShape& s, int32_t item, int32_t chain)
 {
     const int32_t tiles = s.tiles_m * s.tiles_n;
     GemmItem it;
@@ -58,15 +60,27 @@ __device__ __forceinline__ GemmItem gemm_item(const GemmShape& s, int32_t item)
     const int32_t high = min(8, s.tiles_m - 8 * band);
     it.tile_n = r / high;
     it.m0 = (8 * band + r - it.tile_n * high) * kGemmTileM;
-    it.first = int32_t(int64_t(s.blocks) * it.split / s.splits);
-    it.last = int32_t(int64_t(s.blocks) * (it.split + 1) / s.splits);
+    it.chain = chain;
+    const int64_t parts = int64_t(s.splits) * s.chains, part = int64_t(it.split) * s.chains + chain;
+    it.first = int32_t(s.blocks * part / parts);
+    it.last = int32_t(s.blocks * (part + 1) / parts);
     return it;
+}
+// The next item of a pair: its chains one after another, then `pairs` further.
+__device__ __forceinline__ void gemm_next(const GemmShape& s, int32_t pairs, int32_t& item,
+                                          int32_t& chain)
+{
+    if (++chain == s.chains) {
+        chain = 0;
+        item += pairs;
+    }
 }
 
 // E: the epilogue.  E::Params is its arguments; an object of E is made for
-// each tile and thread by E(params, shape, row, item, half of the columns),
-// gets the sums of its row by chunk(params, shape, column, values, 32 x 33
-// floats of shared memory of the warp's own) and ends with end(params, shape).
+// each tile and thread by E(params, shape, row, first column, columns, item,
+// which half of the tile's columns, 32 x 33 floats of shared memory of the warp's own), gets the
+// sums of its row by chunk(params, shape, column, number of the chunk, values,
+// those floats) and ends with end(params, shape).
 template <int BN, typename E>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -115,9 +129,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (warp == 0 && elect_one()) {
         uint32_t stage = 0, phase = 0;
         const uint32_t full_first = in_block(full, 0);
+        // of both blocks' tiles
+        const uint32_t bytes =
+            2 * (R::kBytesA + (s.b_across ? R::kBytesB : R::kRowsB * kGemmInner * 2));
         bool ok = true;
-        for (int32_t item = pair; item < items && ok; item += pairs) {
-            const GemmItem it = gemm_item(s, item);
+        for (int32_t item = pair, chain = 0; item < items && ok; gemm_next(s, pairs, item, chain)) {
+            const GemmItem it = gemm_item(s, item, chain);
             const int32_t row_a = it.m0 + 128 * int32_t(rank);
             const int32_t row_b = it.tile_n * BN + R::kRowsB * int32_t(rank);
             for (int32_t k = it.first; k < it.last; ++k) {
@@ -125,18 +142,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 if (!ok)
                     break;
                 if (rank == 0)
-                    barrier_expect(full + 8 * stage, 2 * R::kStage);
+                    barrier_expect(full + 8 * stage, bytes);
                 const uint32_t bar = full_first + 8 * stage;
                 const uint32_t to = ring + stage * R::kStage;
                 const int32_t inner = k * kGemmInner;
+                if (!s.a_across) {
+                    load_tile(to, &map_a, inner, row_a, bar);
+                } else {
+                    load_tile(to, &map_a, row_a, inner, bar);
+                    load_tile(to + 8192, &map_a, row_a + 64, inner, bar);
+                }
+                if (!s.b_across) {
+                    load_tile(to + R::kBytesA, &map_b, inner, row_b, bar);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 128; i += 64)
-                    load_tile(to + i * 128, &map_a, s.a_across ? row_a + i : inner,
-                              s.a_across ? inner : row_a + i, bar);
-#pragma unroll
-                for (int i = 0; i < R::kRowsB; i += 64)
-                    load_tile(to + R::kBytesA + i * 128, &map_b, s.b_across ? row_b + i : inner,
-                              s.b_across ? inner : row_b + i, bar);
+                    for (int i = 0; i < R::kRowsB; i += 64)
+                        load_tile(to + R::kBytesA + i * 128, &map_b, row_b + i, inner, bar);
+                }
                 if (++stage == R::kStages) {
                     stage = 0;
                     phase ^= 1;
@@ -162,8 +184,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const uint32_t step_a = s.a_across ? 2048 : 32, step_b = s.b_across ? 2048 : 32;
         int32_t n = 0;
         bool ok = true;
-        for (int32_t item = pair; item < items && ok; item += pairs, ++n) {
-            const GemmItem it = gemm_item(s, item);
+        for (int32_t item = pair, chain = 0; item < items && ok;
+             gemm_next(s, pairs, item, chain), ++n) {
+            const GemmItem it = gemm_item(s, item, chain);
             const int32_t slot = n & 1;
             ok = barrier_wait(sums_empty + 8 * slot, ((n >> 1) & 1) ^ 1, dead);
             if (!ok)
@@ -198,35 +221,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         float* const stage = reinterpret_cast<float*>(
             raw + (ring - smem_address(raw)) + R::kStages * R::kStage + (warp - 4) * R::kWarpStage);
         int32_t n = 0;
-        for (int32_t item = pair; item < items; item += pairs, ++n) {
-            const GemmItem it = gemm_item(s, item);
+        for (int32_t item = pair, chain = 0; item < items; gemm_next(s, pairs, item, chain), ++n) {
+            const GemmItem it = gemm_item(s, item, chain);
             const int32_t slot = n & 1;
             const int32_t row = it.m0 + 128 * int32_t(rank) + 32 * int32_t(quarter) +
                                 int32_t(threadIdx.x % 32);
             const int32_t column = it.tile_n * BN + kHalf * int32_t(half);
-            E epilogue(e, s, row, it, int32_t(half));
+            E epilogue(e, s, row, column, kHalf, it, int32_t(half), stage);
             const bool ok = barrier_wait(sums_full + 8 * slot, (n >> 1) & 1, dead);
             if (!__all_sync(0xFFFFFFFFu, ok))
                 break;
             after_sync();
             const uint32_t from = tmem + uint32_t(slot * R::kAccColumns) + half * kHalf +
                                   ((32 * quarter) << 16);
-            float v[2][kChunk];
-            tmem_read(from, v[0]);
 #pragma unroll
             for (int c = 0; c < kHalf / kChunk; ++c) {
+                float v[kChunk];
                 __syncwarp();
-                tmem_wait(v[c & 1]);
-                if (c + 1 < kHalf / kChunk) {
-                    tmem_read(from + (c + 1) * kChunk, v[(c + 1) & 1]);
-                } else {
-                    // all of this thread's sums are in registers
+                tmem_read(from + c * kChunk, v);
+                tmem_wait(v);
+                if (c + 1 == kHalf / kChunk) {  // all of this thread's sums are in registers
                     before_sync();
                     __syncwarp();
                     if (threadIdx.x % 32 == 0)
                         barrier_arrive_at(done + 8 * slot);
                 }
-                epilogue.chunk(e, s, column + c * kChunk, v[c & 1], stage);
+                epilogue.chunk(e, s, column + c * kChunk, c, v, stage);
             }
             epilogue.end(e, s);
             __syncwarp();

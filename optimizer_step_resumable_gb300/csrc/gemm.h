@@ -23,10 +23,12 @@ struct GemmOperand {
 
 // What the kernel is told about one product of `m` x `n` over the inner
 // dimension, in tiles of 256 x BN shared by two blocks, the inner dimension
-// cut into `splits` ranges of blocks of 64.
+// cut into `splits` ranges of blocks of 64, and each of those into `chains`
+// that one pair of blocks sums up one after another: the tensor cores cut
+// their sums, so long ones lose bits.
 struct GemmShape {
     int32_t m, n;
-    int32_t tiles_m, tiles_n, splits, blocks;
+    int32_t tiles_m, tiles_n, splits, chains, blocks;
     uint32_t what;  // mma_what
     int32_t a_across, b_across;
     int32_t* gave_up;  // set to 1 if a wait ran out (host memory)

@@ -9,8 +9,8 @@
 
 namespace osr {
 
-// Where a product goes: out = act(alpha sum + bias) + residual, or added to
-// what is there.  The row distances are in elements.
+// Where a product goes: out = act(alpha sum + bias) + residual, which may be
+// out itself: added to what is there.  The row distances are in elements.
 struct LinearOut {
     void* out;
     int64_t stride;
@@ -23,7 +23,6 @@ struct LinearOut {
     void* z;  // NULL: not kept
     int64_t z_stride;
     int32_t act;
-    int32_t accumulate;
     float alpha;
     const float* alpha_factor;  // on the device, multiplies alpha; NULL: 1
     int32_t vectors;            // rows of out, residual and z on 32-byte boundaries
@@ -35,16 +34,27 @@ struct LinearProduct {
     bool bf16;
     LinearOut to;
 };
+// Makes a product add to what is there.
+inline void accumulate_into(LinearOut& o)
+{
+    o.residual = o.out;
+    o.residual_stride = o.stride;
+    o.residual_dtype = o.dtype;
+}
+
 // How it is computed: in tiles of 256 x bn with the inner dimension in
-// `splits` ranges whose sums a second kernel joins; swapped: the tile's long
-// side lies along the columns, for products of few rows.
+// `splits` ranges whose sums a second kernel joins, each in `chains` (see
+// GemmShape); swapped: the tile's long side lies along the columns, for
+// products of few rows.
 struct LinearPlan {
     bool swapped;
-    int32_t bn, splits;
+    int32_t bn, splits, chains;
     int64_t partials;  // float32 sums in the workspace
 };
-// a_across: whether a's outer dimension is the adjacent one.
-LinearPlan linear_plan(int64_t rows, int64_t columns, int64_t inner, bool a_across, int sm_count);
+// a_across: whether a's outer dimension is the adjacent one; f32: out is
+// float32.
+LinearPlan linear_plan(int64_t rows, int64_t columns, int64_t inner, bool a_across, bool f32,
+                       int sm_count);
 int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partials, int sm_count,
                    int32_t* gave_up, void* stream);
 // A product over nothing.

@@ -54,13 +54,13 @@ struct Needs {
     bool backward, copy_x, copy_weight, dz;
     bool in_out;  // the weight, for its copy
     bool dx, dweight, dbias;
-    bool grad_in_out;
+    bool grad_in_out, grad_f32;
 };
 
-LinearPlan plan_dweight(const linear_ctx* c, int64_t rows, bool grad_in_out)
+LinearPlan plan_dweight(const linear_ctx* c, int64_t rows, bool grad_in_out, bool f32)
 {
     return osr::linear_plan(grad_in_out ? c->in : c->out, grad_in_out ? c->out : c->in, rows, true,
-                            c->base.sm_count);
+                            f32, c->base.sm_count);
 }
 
 int64_t lay_out(const linear_ctx* c, int64_t rows, const Needs& n, void* memory, Parts* p)
@@ -73,17 +73,17 @@ int64_t lay_out(const linear_ctx* c, int64_t rows, const Needs& n, void* memory,
         p->weight = w.take(2 * (n.in_out ? c->in * whole(c->out) : c->out * whole(c->in)));
     int64_t partials = 0;
     if (!n.backward) {
-        p->forward = osr::linear_plan(rows, c->out, c->in, false, sms);
+        p->forward = osr::linear_plan(rows, c->out, c->in, false, false, sms);
         partials = p->forward.partials;
     } else {
         if (n.dz)
             p->dy = w.take(2 * rows * whole(c->out));
         if (n.dx) {
-            p->dx = osr::linear_plan(rows, c->in, c->out, false, sms);
+            p->dx = osr::linear_plan(rows, c->in, c->out, false, false, sms);
             partials = p->dx.partials;
         }
         if (n.dweight) {
-            p->dweight = plan_dweight(c, rows, n.grad_in_out);
+            p->dweight = plan_dweight(c, rows, n.grad_in_out, n.grad_f32);
             partials = partials > p->dweight.partials ? partials : p->dweight.partials;
         }
         if (n.dbias) {
@@ -173,7 +173,8 @@ int linear_workspace(linear_ctx* ctx, int64_t rows, int32_t flags, int64_t* byte
     // the most that any layout of the weight and its gradient takes
     for (int layout = 0; layout < 4; ++layout) {
         Parts p;
-        const Needs n{back, any, any, back, (layout & 1) != 0, back, back, back, (layout & 2) != 0};
+        const Needs n{back, any, any, back, (layout & 1) != 0, back, back, back, (layout & 2) != 0,
+                      false};
         const int64_t b = lay_out(ctx, rows, n, nullptr, &p);
         *bytes = *bytes > b ? *bytes : b;
     }
@@ -304,6 +305,7 @@ int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride, const 
     n.copy_weight = w_read && !gemm_readable(d_weight, w_rows > 1 ? weight_stride : 0);
     n.in_out = in_out;
     n.grad_in_out = grad_in_out;
+    n.grad_f32 = grad_dtype == ADAMW_DTYPE_F32;
     n.dx = dx_rows;
     n.dweight = d_dweight && rows;
     n.dbias = d_dbias && rows;
@@ -355,7 +357,8 @@ int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride, const 
         m.to.stride = dweight_stride;
         m.to.dtype = grad_dtype;
         m.to.alpha = 1.0f;
-        m.to.accumulate = accumulate;
+        if (accumulate)
+            osr::accumulate_into(m.to);
         m.to.vectors = on_vectors(d_dweight, dweight_stride, g_rows, gs);
         if (rows == 0) {
             e = osr::launch_linear_zero(m.to, g_rows, g_cols, sms, stream);

@@ -1,0 +1,274 @@
+// linear_gemm.cuh -- the epilogue of the linear layer's products, a translation
+// unit for each type of the output.
+#pragma once
+
+#include "gemm.cuh"
+#include "linear_dev.cuh"
+
+namespace osr {
+
+struct StoreParams {
+    LinearOut o;
+    int64_t rows, columns;
+    int64_t split_stride;  // elements of out from one split's sums to the next's
+};
+
+// Tiles of 256 x bn (128, 192 or 256), the product's rows along the long side.
+int linear_store_f32(int bn, const GemmOperand& a, const GemmOperand& b, const GemmShape& s,
+                     bool bf16, const StoreParams& p, int sm_count, void* stream);
+int linear_store_bf16(int bn, const GemmOperand& a, const GemmOperand& b, const GemmShape& s,
+                      bool bf16, const StoreParams& p, int sm_count, void* stream);
+int linear_store_f16(int bn, const GemmOperand& a, const GemmOperand& b, const GemmShape& s,
+                     bool bf16, const StoreParams& p, int sm_count, void* stream);
+
+namespace detail {
+
+// Launches a product's tiles.
+template <int BN, typename E>
+inline int gemm_run(const GemmOperand& a, const GemmOperand& b, GemmShape s, bool bf16,
+                    const typename E::Params& p, int sm_count, void* stream)
+{
+    CUtensorMap ma, mb;
+    int e = gemm_map(a, 128, bf16, &ma);
+    if (e == cudaSuccess)
+        e = gemm_map(b, BN / 2, bf16, &mb);
+    if (e != cudaSuccess)
+        return e;
+    s.m = int32_t(a.outer);
+    s.n = int32_t(b.outer);
+    s.tiles_m = (s.m + kGemmTileM - 1) / kGemmTileM;
+    s.tiles_n = (s.n + BN - 1) / BN;
+    s.blocks = int32_t((a.inner + kGemmInner - 1) / kGemmInner);
+    s.what = mma_what(bf16, a.across, b.across, kGemmTileM, BN);
+    s.a_across = a.across;
+    s.b_across = b.across;
+    return gemm_launch<BN, E>(ma, mb, s, p, sm_count, static_cast<cudaStream_t>(stream));
+}
+
+template <int kType>
+constexpr int kSize = kType == ADAMW_DTYPE_F32 ? 4 : 2;
+template <int kType>
+__device__ __forceinline__ float get(const char* p)
+{
+    return load_as(p, 0, kType);
+}
+
+// The tile's rows are the product's: a thread has a row's neighbouring
+// columns, 32 at a time.  Rows on 32-byte boundaries go out from each thread,
+// whole sectors at a time, and what is added to them comes in the same way,
+// two chunks ahead (one, if it is float32).  Others go through shared memory,
+// so that a warp's lanes have neighbouring columns of one row, eight rows at a
+// time.
+template <int kOut>
+struct StoreEpilogue {
+    using Params = StoreParams;
+    static constexpr bool kF32 = kOut == ADAMW_DTYPE_F32, kBf16 = kOut == ADAMW_DTYPE_BF16;
+
+    int32_t row, end_column;  // of the columns that are this thread's
+    float alpha;
+    bool vectors, add, add_f32, bias;
+    char* out;        // the row
+    const char* from;  // what is added to it
+    float lane_bias[4];  // of the chunks, for the lane's column
+    uint32_t ahead[32];
+
+    __device__ StoreEpilogue(const Params& p, const GemmShape&, int32_t r, int32_t column,
+                             int32_t count, const GemmItem& it, int32_t, float* stage)
+        : row(r), end_column(column + count < p.columns ? column + count : int32_t(p.columns)),
+          alpha(p.o.alpha), vectors(p.o.vectors), bias(p.o.bias)
+    {
+        const LinearOut& o = p.o;
+        if (o.alpha_factor)
+            alpha *= *o.alpha_factor;
+        out = static_cast<char*>(o.out) +
+              (it.split * p.split_stride + int64_t(r) * o.stride) * kSize<kOut>;
+        // a later chain adds to what the one before it left there
+        const bool again = kF32 && it.chain > 0;
+        add = again || o.residual;
+        add_f32 = again || o.residual_dtype == ADAMW_DTYPE_F32;
+        from = again ? out
+                     : static_cast<const char*>(o.residual) +
+                           int64_t(r) * o.residual_stride * (add_f32 ? 4 : 2);
+        if (bias) {
+            const int lane = threadIdx.x % 32;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                lane_bias[c] = column + 32 * c + lane < end_column
+                                   ? load_as(o.bias, column + 32 * c + lane, o.bias_dtype)
+                                   : 0.0f;
+            if (vectors) {  // for all lanes to read
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    stage[32 * c + lane] = lane_bias[c];
+                __syncwarp();
+            }
+        }
+        if (add && vectors) {
+            fetch(p, column, 0);
+            if (!add_f32)
+                fetch(p, column + 32, 1);
+        }
+    }
+    // What is added to the 32 columns from `column`; `slot`: of two, for the
+    // 16-bit types.
+    __device__ __forceinline__ void fetch(const Params& p, int32_t column, int slot)
+    {
+        if (row >= p.rows || column + 32 > end_column)
+            return;
+        if (add_f32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                load32(from + (int64_t(column) + 8 * i) * 4,
+                       *reinterpret_cast<uint32_t(*)[8]>(ahead + 8 * i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                load32(from + (int64_t(column) + 16 * i) * 2,
+                       *reinterpret_cast<uint32_t(*)[8]>(ahead + 16 * slot + 8 * i));
+        }
+    }
+    __device__ static __forceinline__ void store(char* to, const float (&v)[32])
+    {
+        uint32_t w[8];
+        if constexpr (kF32) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = __float_as_uint(v[i + j]);
+                store32(to + i * 4, w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 16) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = narrow32(v[i + 2 * j], v[i + 2 * j + 1], kBf16);
+                store32(to + i * 2, w);
+            }
+        }
+    }
+    template <int C>
+    __device__ __forceinline__ void chunk(const Params& p, const GemmShape&, int32_t column, int c,
+                                          float (&v)[C], float* stage)
+    {
+        static_assert(C == 32, "");
+        const LinearOut& o = p.o;
+        if (column >= p.columns)
+            return;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] *= alpha;
+        if (vectors && column + 32 <= p.columns) {
+            if (bias)
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 b = *reinterpret_cast<const float4*>(stage + 32 * c + i);
+                    v[i] += b.x, v[i + 1] += b.y, v[i + 2] += b.z, v[i + 3] += b.w;
+                }
+            if (o.z && row < p.rows)
+                store(static_cast<char*>(o.z) + (int64_t(row) * o.z_stride + column) * kSize<kOut>,
+                      v);
+            if (o.act != LINEAR_NONE)
+                with_activation(o.act, [&](auto act) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = activated<decltype(act)::value>(v[i]);
+                });
+            if (add) {
+                if (add_f32) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] += __uint_as_float(ahead[i]);
+                    fetch(p, column + 32, 0);
+                } else {
+                    // float32 products add 16-bit values nowhere
+                    if constexpr (!kF32) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t w = ahead[16 * (c & 1) + i];
+                            v[2 * i] += widen16(w & 0xFFFFu, kBf16);
+                            v[2 * i + 1] += widen16(w >> 16, kBf16);
+                        }
+                    }
+                    fetch(p, column + 64, c & 1);
+                }
+            }
+            if (row < p.rows)
+                store(out + int64_t(column) * kSize<kOut>, v);
+            return;
+        }
+        const int lane = threadIdx.x % 32;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            stage[lane * 33 + i] = v[i];
+        __syncwarp();
+        // the warp's rows, from its first lane's
+        const int32_t left = p.rows - (row - lane) < 32 ? int32_t(p.rows - (row - lane)) : 32;
+        const int32_t mine = column + lane;
+        if (mine < p.columns) {
+            const int64_t out_step = o.stride * kSize<kOut>, z_step = o.z_stride * kSize<kOut>;
+            const int64_t add_step = (from == out ? o.stride : o.residual_stride) *
+                                     (add_f32 ? 4 : 2);
+            char* to = out - lane * out_step + int64_t(mine) * kSize<kOut>;
+            const char* more = from - lane * add_step + int64_t(mine) * (add_f32 ? 4 : 2);
+            char* z = static_cast<char*>(o.z) +
+                      (int64_t(row - lane) * o.z_stride + mine) * kSize<kOut>;
+            const float b = bias ? lane_bias[c] : 0.0f;
+            for (int r = 0; r < left; r += 8) {
+                float f[8], a[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    f[i] = stage[(r + i) * 33 + lane] + b;
+                    a[i] = 0.0f;
+                }
+                if (add) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (r + i < left)
+                            a[i] = add_f32 ? get<ADAMW_DTYPE_F32>(more + i * add_step)
+                                           : get<kF32 ? ADAMW_DTYPE_BF16 : kOut>(more +
+                                                                                 i * add_step);
+                    more += 8 * add_step;
+                }
+                if (o.z) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (r + i < left)
+                            store_as(z + i * z_step, 0, kOut, f[i]);
+                    z += 8 * z_step;
+                }
+                if (o.act != LINEAR_NONE)
+                    with_activation(o.act, [&](auto act) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            f[i] = activated<decltype(act)::value>(f[i]);
+                    });
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (r + i < left)
+                        store_as(to + i * out_step, 0, kOut, f[i] + a[i]);
+                to += 8 * out_step;
+            }
+        }
+        __syncwarp();
+    }
+    __device__ void end(const Params&, const GemmShape&) {}
+};
+
+template <int kOut>
+inline int linear_store(int bn, const GemmOperand& a, const GemmOperand& b, const GemmShape& s,
+                        bool bf16, const StoreParams& p, int sm_count, void* stream)
+{
+    using E = StoreEpilogue<kOut>;
+    switch (bn) {
+    case 128: return gemm_run<128, E>(a, b, s, bf16, p, sm_count, stream);
+    case 192: return gemm_run<192, E>(a, b, s, bf16, p, sm_count, stream);
+    default: return gemm_run<256, E>(a, b, s, bf16, p, sm_count, stream);
+    }
+}
+
+}  // namespace detail
+}  // namespace osr

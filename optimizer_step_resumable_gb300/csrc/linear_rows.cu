@@ -9,74 +9,101 @@ namespace {
 
 using namespace detail;
 
-// A block has 256 neighbouring columns, eight a thread, and every eighth row
-// of its strip a thread; the eight partial sums of a column meet in shared
+// A block has 256 neighbouring columns of a strip of the rows, a warp every
+// eighth row, a thread eight columns: neighbours in one vector, or, where
+// rows do not start on vectors, every 32nd.  kAtOnce rows of a thread are on
+// their way at a time.  The eight warps' sums of a column meet in shared
 // memory.
 constexpr int kSlopeThreads = 256, kSlopeColumns = 256;
 
-// Eight 16-bit values; vectors: p is on a 16-byte boundary.
-__device__ __forceinline__ void load8(const uint16_t* p, int count, bool vectors, bool bf16,
-                                      float (&v)[8])
+__device__ __forceinline__ void widen8(uint4 q, bool bf16, float (&v)[8])
 {
-    if (vectors && count >= 8) {
-        const uint4 r = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = widen16(w[i] & 0xFFFFu, bf16);
-            v[2 * i + 1] = widen16(w[i] >> 16, bf16);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = i < count ? widen16(p[i], bf16) : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = widen16(w[i] & 0xFFFFu, bf16);
+        v[2 * i + 1] = widen16(w[i] >> 16, bf16);
     }
 }
+// Eight elements of a row from p; `step` apart, those before `count` of them.
+template <bool kVector>
+__device__ __forceinline__ uint4 load8(const uint16_t* p, int step, int count)
+{
+    if (kVector && count >= 8)
+        return __ldcs(reinterpret_cast<const uint4*>(p));
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w[i] = i < count ? p[i * step] : 0u;
+    return make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16),
+                      w[6] | (w[7] << 16));
+}
 
-template <int kAct>
+template <int kAct, bool kVector>
 __global__ void __launch_bounds__(kSlopeThreads) k_linear_slope(const LinearSlope a)
 {
     __shared__ float sums[8][kSlopeColumns + 8];
     wait_before();
     go_ahead();
+    constexpr int kAtOnce = 4;
     const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
-    const int64_t column = int64_t(blockIdx.x) * kSlopeColumns + 8 * lane;
+    const int place = kVector ? 8 * lane : lane, step = kVector ? 1 : 32;
+    const int64_t column = int64_t(blockIdx.x) * kSlopeColumns + place;
     const int64_t left = a.columns - column;
-    const int count = int(left < 8 ? (left < 0 ? 0 : left) : 8);
+    const int count = left <= 0 ? 0 : int(left >= 8 * step ? 8 : (left + step - 1) / step);
     const int64_t first = a.rows * blockIdx.y / a.strips;
     const int64_t last = a.rows * (blockIdx.y + 1) / a.strips;
-    const bool dy_vectors = reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && a.dy_stride % 8 == 0;
-    const bool z_vectors = reinterpret_cast<uintptr_t>(a.z) % 16 == 0 && a.z_stride % 8 == 0;
+    const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + (first + group) * a.dy_stride + column;
+    const uint16_t* z = static_cast<const uint16_t*>(a.z) + (first + group) * a.z_stride + column;
+    uint16_t* dz = static_cast<uint16_t*>(a.dz) + (first + group) * a.stride + column;
     float total[8] = {};
-    if (count > 0)
-#pragma unroll 4
-        for (int64_t r = first + group; r < last; r += 8) {
-            float g[8];
-            load8(static_cast<const uint16_t*>(a.dy) + r * a.dy_stride + column, count,
-                  dy_vectors, a.bf16, g);
-            if constexpr (kAct != LINEAR_NONE) {
-                float z[8];
-                load8(static_cast<const uint16_t*>(a.z) + r * a.z_stride + column, count,
-                      z_vectors, a.bf16, z);
+    for (int64_t r = first + group; r < last && count > 0; r += 8 * kAtOnce) {
+        uint4 g[kAtOnce], x[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+            if (r + 8 * k < last) {
+                g[k] = load8<kVector>(dy + 8 * k * a.dy_stride, step, count);
+                if constexpr (kAct != LINEAR_NONE)
+                    x[k] = load8<kVector>(z + 8 * k * a.z_stride, step, count);
+            }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+            if (r + 8 * k < last) {
+                float f[8];
+                widen8(g[k], a.bf16, f);
+                if constexpr (kAct != LINEAR_NONE) {
+                    float s[8];
+                    widen8(x[k], a.bf16, s);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        f[i] *= slope<kAct>(s[i]);
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    g[i] *= slope<kAct>(z[i]);
-            }
+                    total[i] += f[i];
+                if (a.dz) {
+                    uint16_t* const to = dz + 8 * k * a.stride;
+                    if constexpr (kVector) {  // the stride is a multiple of eight
+                        *reinterpret_cast<uint4*>(to) =
+                            make_uint4(narrow32(f[0], f[1], a.bf16), narrow32(f[2], f[3], a.bf16),
+                                       narrow32(f[4], f[5], a.bf16), narrow32(f[6], f[7], a.bf16));
+                    } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                total[i] += g[i];
-            if (a.dz) {  // rows of whole vectors: the stride is a multiple of eight
-                const uint4 w = make_uint4(
-                    narrow32(g[0], g[1], a.bf16), narrow32(g[2], g[3], a.bf16),
-                    narrow32(g[4], g[5], a.bf16), narrow32(g[6], g[7], a.bf16));
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dz) + r * a.stride + column) = w;
+                        for (int i = 0; i < 8; ++i)
+                            if (i < count)
+                                to[i * step] = narrow16(f[i], a.bf16);
+                    }
+                }
             }
-        }
+        dy += 8 * kAtOnce * a.dy_stride;
+        z += 8 * kAtOnce * a.z_stride;
+        dz += 8 * kAtOnce * a.stride;
+    }
     if (!a.partials)
         return;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        sums[group][8 * lane + i] = total[i];
+        sums[group][place + i * step] = total[i];
     __syncthreads();
     const int64_t mine = int64_t(blockIdx.x) * kSlopeColumns + threadIdx.x;
     if (mine < a.columns) {
@@ -88,31 +115,32 @@ __global__ void __launch_bounds__(kSlopeThreads) k_linear_slope(const LinearSlop
     }
 }
 
-// dbias from the strips' sums, in order: four interleaved sums a column, one
-// for each quarter of the block.
-constexpr int kBiasThreads = 256;
+// dbias from the strips' sums: a block has 32 columns, a warp every 32nd strip
+// of them, then a column, whose 32 sums it joins.
+constexpr int kBiasThreads = 1024;
 __global__ void __launch_bounds__(kBiasThreads)
     k_linear_bias_grad(const float* partials, int32_t strips, int64_t columns, void* dbias,
                        int32_t dtype, bool accumulate)
 {
-    __shared__ float sums[4][64];
+    __shared__ float sums[32][33];
     wait_before();
     go_ahead();
-    const int lane = threadIdx.x % 64, part = threadIdx.x / 64;
-    const int64_t column = int64_t(blockIdx.x) * 64 + lane;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t base = int64_t(blockIdx.x) * 32;
     float s = 0.0f;
-    if (column < columns)
-#pragma unroll 8
-        for (int32_t i = part; i < strips; i += 4)
-            s += __ldcg(partials + i * columns + column);
-    sums[part][lane] = s;
+    if (base + lane < columns)
+#pragma unroll 4
+        for (int32_t i = warp; i < strips; i += 32)
+            s += __ldcg(partials + i * columns + base + lane);
+    sums[warp][lane] = s;
     __syncthreads();
-    if (part == 0 && column < columns) {
-        float v = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
-        if (accumulate)
-            v += load_as(dbias, column, dtype);
-        store_as(dbias, column, dtype, v);
-    }
+    s = sums[lane][warp];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    const int64_t column = base + warp;
+    if (lane == 0 && column < columns)
+        store_as(dbias, column, dtype, accumulate ? s + load_as(dbias, column, dtype) : s);
 }
 
 constexpr int kCopyThreads = 256;
@@ -144,33 +172,43 @@ __global__ void __launch_bounds__(kCopyThreads)
 int linear_strips(int64_t rows, int64_t columns, int sm_count)
 {
     const int64_t across = (columns + kSlopeColumns - 1) / kSlopeColumns;
-    int64_t strips = (int64_t(sm_count) * 6 + across - 1) / across;
+    int64_t strips = (int64_t(sm_count) * 4 + across - 1) / across;
     const int64_t most = (rows + 31) / 32;  // four rows a thread at least
     strips = strips < most ? strips : most;
-    strips = strips < 1024 ? strips : 1024;
+    strips = strips < 128 ? strips : 128;
     return int(strips > 1 ? strips : 1);
 }
 
 int launch_linear_slope(const LinearSlope& a, void* stream)
 {
     const dim3 grid(unsigned((a.columns + kSlopeColumns - 1) / kSlopeColumns), unsigned(a.strips));
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const auto launch = [&](void (*kernel)(LinearSlope)) {
-        return launch_early(kernel, grid, kSlopeThreads, 0, st, a);
+    const auto on_vector = [](const void* p, int64_t stride) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0;
+    };
+    const bool vector = on_vector(a.dy, a.rows > 1 ? a.dy_stride : 0) &&
+                        (a.act == LINEAR_NONE || on_vector(a.z, a.rows > 1 ? a.z_stride : 0));
+    const auto launch = [&](void (*vectors)(LinearSlope), void (*others)(LinearSlope)) {
+        return launch_early(vector ? vectors : others, grid, kSlopeThreads, 0,
+                            static_cast<cudaStream_t>(stream), a);
     };
     switch (a.act) {
-    case LINEAR_RELU: return launch(k_linear_slope<LINEAR_RELU>);
-    case LINEAR_GELU: return launch(k_linear_slope<LINEAR_GELU>);
-    case LINEAR_GELU_TANH: return launch(k_linear_slope<LINEAR_GELU_TANH>);
-    case LINEAR_SILU: return launch(k_linear_slope<LINEAR_SILU>);
-    default: return launch(k_linear_slope<LINEAR_NONE>);
+    case LINEAR_RELU:
+        return launch(k_linear_slope<LINEAR_RELU, true>, k_linear_slope<LINEAR_RELU, false>);
+    case LINEAR_GELU:
+        return launch(k_linear_slope<LINEAR_GELU, true>, k_linear_slope<LINEAR_GELU, false>);
+    case LINEAR_GELU_TANH:
+        return launch(k_linear_slope<LINEAR_GELU_TANH, true>,
+                      k_linear_slope<LINEAR_GELU_TANH, false>);
+    case LINEAR_SILU:
+        return launch(k_linear_slope<LINEAR_SILU, true>, k_linear_slope<LINEAR_SILU, false>);
+    default: return launch(k_linear_slope<LINEAR_NONE, true>, k_linear_slope<LINEAR_NONE, false>);
     }
 }
 
 int launch_linear_bias_grad(const float* partials, int32_t strips, int64_t columns, void* dbias,
                             int32_t dtype, bool accumulate, void* stream)
 {
-    return launch_early(k_linear_bias_grad, dim3(unsigned((columns + 63) / 64)), kBiasThreads, 0,
+    return launch_early(k_linear_bias_grad, dim3(unsigned((columns + 31) / 32)), kBiasThreads, 0,
                         static_cast<cudaStream_t>(stream), partials, strips, columns, dbias, dtype,
                         accumulate);
 }
