@@ -30,7 +30,9 @@ using osr::GemmOperand;
 using osr::kCeColumns;
 using osr::kCeParts;
 using osr::known_dtype;
+using osr::LinearPlan;
 using osr::LinearProduct;
+using osr::LinearSize;
 using osr::on_vectors;
 using osr::Pieces;
 using osr::readable;
@@ -59,7 +61,31 @@ int64_t piece_columns(int64_t rows, int64_t vocab)
 
 struct Needs {
     bool backward, copy_x, copy_weight, in_out, dx, dweight, grad_in_out;
+    bool grad_f32, grad_mixed;  // neither float32 nor the other matrices' type
 };
+// How the products of a piece of `columns` are computed.
+struct Plans {
+    LinearPlan dx{}, dweight{};
+    bool together = false;  // in one launch
+};
+Plans make_plans(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Needs& n)
+{
+    Plans p;
+    const int sms = c->base.sm_count;
+    const LinearSize dx{rows, c->dim, columns, false, false};
+    const LinearSize dw{n.grad_in_out ? c->dim : columns, n.grad_in_out ? columns : c->dim, rows,
+                        true, n.grad_f32};
+    if (n.dx && n.dweight && !n.grad_mixed) {
+        p.together = osr::linear_plan_two(dx, dw, sms, &p.dx, &p.dweight);
+    } else {
+        if (n.dx)
+            p.dx = osr::linear_plan(dx, sms);
+        if (n.dweight)
+            p.dweight = osr::linear_plan(dw, sms);
+    }
+    return p;
+}
+
 struct Parts {
     void* x = nullptr;
     void* weight = nullptr;
@@ -69,14 +95,17 @@ struct Parts {
     float* unnorm = nullptr;
     void* gradient = nullptr;
     float* dx = nullptr;  // the sum over the pieces so far
-    float* partials = nullptr;
+    float* dx_partials = nullptr;
+    float* dweight_partials = nullptr;
     int64_t piece = 0;
+    Plans plans, last;  // of the pieces, and of the last, which may be shorter
 };
+
+int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
 
 int64_t lay_out(const linear_ce_ctx* c, int64_t rows, const Needs& n, void* memory, Parts* p)
 {
     Workspace w(memory);
-    const int sms = c->base.sm_count;
     if (n.copy_x)
         p->x = w.take(2 * rows * whole(c->dim));
     if (n.copy_weight)
@@ -90,27 +119,15 @@ int64_t lay_out(const linear_ce_ctx* c, int64_t rows, const Needs& n, void* memo
     p->factors = static_cast<float2*>(w.take(8 * rows));
     p->unnorm = static_cast<float*>(w.take(4));
     p->gradient = w.take(2 * rows * p->piece);
-    int64_t partials = 0;
-    // of the first piece, and of the last, which may be shorter
-    const int64_t last = c->vocab - (c->vocab - 1) / p->piece * p->piece;
-    const int64_t sizes[] = {c->vocab < p->piece ? c->vocab : p->piece, last};
-    for (const int64_t columns : sizes) {
-        if (n.dx) {
-            const int64_t s = osr::linear_plan(rows, c->dim, columns, false, false, sms).partials;
-            partials = partials > s ? partials : s;
-        }
-        if (n.dweight) {
-            const int64_t s = osr::linear_plan(n.grad_in_out ? c->dim : columns,
-                                               n.grad_in_out ? columns : c->dim, rows, true, false,
-                                               sms)
-                                  .partials;
-            partials = partials > s ? partials : s;
-        }
-    }
+    const int64_t end = c->vocab - (c->vocab - 1) / p->piece * p->piece;
+    p->last = make_plans(c, rows, end, n);
+    p->plans = c->vocab > p->piece ? make_plans(c, rows, p->piece, n) : p->last;
     if (n.dx && p->piece < c->vocab)
         p->dx = static_cast<float*>(w.take(4 * rows * whole(c->dim)));
-    if (partials)
-        p->partials = static_cast<float*>(w.take(4 * partials));
+    if (const int64_t sums = larger(p->plans.dx.partials, p->last.dx.partials))
+        p->dx_partials = static_cast<float*>(w.take(4 * sums));
+    if (const int64_t sums = larger(p->plans.dweight.partials, p->last.dweight.partials))
+        p->dweight_partials = static_cast<float*>(w.take(4 * sums));
     return w.bytes();
 }
 
@@ -184,10 +201,14 @@ int linear_cross_entropy_workspace(linear_ce_ctx* ctx, int64_t rows, int32_t fla
     const bool back = flags & LINEAR_FOR_BACKWARD, any = flags & LINEAR_FOR_ANY_ADDRESS;
     // the most that any layout of the weight and its gradient takes
     for (int layout = 0; layout < 4; ++layout) {
-        Parts p;
-        const Needs n{back, any, any, (layout & 1) != 0, back, back, (layout & 2) != 0};
-        const int64_t b = lay_out(ctx, rows, n, nullptr, &p);
-        *bytes = *bytes > b ? *bytes : b;
+        Needs n{back, any, any, (layout & 1) != 0, back, back, (layout & 2) != 0};
+        // dx and dweight in one launch, or each on its own
+        for (int apart = 0; apart < (back ? 2 : 1); ++apart) {
+            n.grad_mixed = apart != 0;
+            Parts p;
+            const int64_t b = lay_out(ctx, rows, n, nullptr, &p);
+            *bytes = *bytes > b ? *bytes : b;
+        }
     }
     return ADAMW_OK;
 }
@@ -241,7 +262,7 @@ int linear_cross_entropy_forward(linear_ce_ctx* ctx, const void* d_x, int64_t x_
             osr::CeForward{GemmOperand{d_x, rows, dim, x_stride, false},
                            GemmOperand{d_weight, ctx->vocab, dim, weight_stride, in_out},
                            dtype == ADAMW_DTYPE_BF16, d_target, p.parts, p.at},
-            ctx->base.sm_count, ctx->base.gave_up, stream);
+            ctx->base.gave_up, stream);
     if (e == cudaSuccess)
         e = osr::launch_ce_join(osr::CeJoin{p.parts, int32_t(kCeParts * tiles(ctx->vocab)), p.at,
                                             d_target, rows, ctx->vocab, float(z_loss), d_loss,
@@ -297,18 +318,18 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
         return rc;
     DeviceScope scope(ctx->base.device);
     const int sms = ctx->base.sm_count;
-    osr::LinearOut dw{};
-    dw.out = d_dweight;
-    dw.stride = dweight_stride;
-    dw.dtype = grad_dtype;
-    dw.alpha = 1.0f;
-    dw.vectors = on_vectors(d_dweight, dweight_stride, g_rows, gs);
+    osr::LinearOut whole_dweight{};
+    whole_dweight.out = d_dweight;
+    whole_dweight.stride = dweight_stride;
+    whole_dweight.dtype = grad_dtype;
+    whole_dweight.alpha = 1.0f;
+    whole_dweight.vectors = on_vectors(d_dweight, dweight_stride, g_rows, gs);
     int e = cudaSuccess;
     if (rows == 0) {
         if (flags & LINEAR_ACCUMULATE)
-            osr::accumulate_into(dw);
+            osr::accumulate_into(whole_dweight);
         if (d_dweight)
-            e = osr::launch_linear_zero(dw, g_rows, g_cols, sms, stream);
+            e = osr::launch_linear_zero(whole_dweight, g_rows, g_cols, sms, stream);
         return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "cross entropy launch");
     }
     if (!d_dx && !d_dweight)
@@ -321,6 +342,8 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
     n.dx = d_dx;
     n.dweight = d_dweight;
     n.grad_in_out = grad_in_out;
+    n.grad_f32 = grad_dtype == ADAMW_DTYPE_F32;
+    n.grad_mixed = !n.grad_f32 && grad_dtype != dtype;
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
                                    lay_out(ctx, rows, n, d_workspace, &p))))
@@ -341,48 +364,45 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
             osr::CeGradient{GemmOperand{d_x, rows, dim, x_stride, false},
                             GemmOperand{w, columns, dim, weight_stride, in_out}, bf16, d_target,
                             d_lse, p.factors, int32_t(first), p.gradient, p.piece},
-            sms, ctx->base.gave_up, stream);
-        if (e == cudaSuccess && d_dx) {
-            // the pieces' sum in float32; the last one leaves with it
-            const bool last = first + columns == vocab;
-            LinearProduct m{};
-            m.a = GemmOperand{p.gradient, rows, columns, p.piece, false};
-            m.b = GemmOperand{w, dim, columns, weight_stride, !in_out};
-            m.bf16 = bf16;
-            m.to.out = last ? d_dx : p.dx;
-            m.to.stride = last ? dx_stride : whole(dim);
-            m.to.dtype = last ? dtype : ADAMW_DTYPE_F32;
-            if (first > 0) {
-                m.to.residual = p.dx;
-                m.to.residual_stride = whole(dim);
-                m.to.residual_dtype = ADAMW_DTYPE_F32;
-            }
-            m.to.alpha = 1.0f;
-            m.to.alpha_factor = p.unnorm;
-            m.to.vectors = last ? on_vectors(d_dx, dx_stride, rows, 2) : 1;
-            e = osr::linear_product(m, osr::linear_plan(rows, dim, columns, false, false, sms),
-                                    p.partials, sms, ctx->base.gave_up, stream);
+            ctx->base.gave_up, stream);
+        const bool last = first + columns == vocab;
+        const Plans& plans = last ? p.last : p.plans;
+        LinearProduct x{}, dw{};
+        x.bf16 = dw.bf16 = bf16;
+        x.a = GemmOperand{p.gradient, rows, columns, p.piece, false};
+        x.b = GemmOperand{w, dim, columns, weight_stride, !in_out};
+        // the pieces' sum in float32; the last one leaves with it
+        x.to.out = last ? d_dx : p.dx;
+        x.to.stride = last ? dx_stride : whole(dim);
+        x.to.dtype = last ? dtype : ADAMW_DTYPE_F32;
+        if (first > 0) {
+            x.to.residual = p.dx;
+            x.to.residual_stride = whole(dim);
+            x.to.residual_dtype = ADAMW_DTYPE_F32;
         }
-        if (e == cudaSuccess && d_dweight) {
-            LinearProduct m{};
-            m.a = GemmOperand{p.gradient, columns, rows, p.piece, true};
-            m.b = GemmOperand{d_x, dim, rows, x_stride, true};
-            m.bf16 = bf16;
-            m.to = dw;
-            m.to.out = static_cast<char*>(d_dweight) +
-                       int64_t(gs) * first * (grad_in_out ? 1 : dweight_stride);
-            m.to.alpha_factor = p.unnorm;
-            if (grad_in_out) {
-                const GemmOperand a = m.a;
-                m.a = m.b;
-                m.b = a;
-            }
-            if (flags & LINEAR_ACCUMULATE)
-                osr::accumulate_into(m.to);
-            e = osr::linear_product(
-                m, osr::linear_plan(m.a.outer, m.b.outer, rows, true,
-                                    grad_dtype == ADAMW_DTYPE_F32, sms),
-                p.partials, sms, ctx->base.gave_up, stream);
+        x.to.alpha = 1.0f;
+        x.to.alpha_factor = p.unnorm;
+        x.to.vectors = last ? on_vectors(d_dx, dx_stride, rows, 2) : 1;
+        const GemmOperand by_vocab{p.gradient, columns, rows, p.piece, true};
+        const GemmOperand by_dim{d_x, dim, rows, x_stride, true};
+        dw.a = grad_in_out ? by_dim : by_vocab;
+        dw.b = grad_in_out ? by_vocab : by_dim;
+        dw.to = whole_dweight;
+        dw.to.out = static_cast<char*>(d_dweight) +
+                    int64_t(gs) * first * (grad_in_out ? 1 : dweight_stride);
+        dw.to.alpha_factor = p.unnorm;
+        if (flags & LINEAR_ACCUMULATE)
+            osr::accumulate_into(dw.to);
+        int32_t* const gave_up = ctx->base.gave_up;
+        if (e == cudaSuccess && plans.together) {
+            e = osr::linear_product_two(x, plans.dx, p.dx_partials, dw, plans.dweight,
+                                        p.dweight_partials, sms, gave_up, stream);
+        } else {
+            if (e == cudaSuccess && d_dx)
+                e = osr::linear_product(x, plans.dx, p.dx_partials, sms, gave_up, stream);
+            if (e == cudaSuccess && d_dweight)
+                e = osr::linear_product(dw, plans.dweight, p.dweight_partials, sms, gave_up,
+                                        stream);
         }
     }
     return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "cross entropy launch");

@@ -12,9 +12,18 @@
 //   2      tensor memory
 //   4..11  epilogue: warp w has the rows 32 (w % 4).. of the block's half of
 //          the tile, and one half of the columns
+//   3      of the pair's first block: asks for the pair's next item
 // Sums take two halves of the tensor memory in turn, so that the epilogue of
 // one tile runs beside the products of the next.
+//
+// The grid has a pair of blocks for each item, a tile or a part of one; those
+// that run take over the items of those that have not started, in order, so
+// the long ones come first.  A launch may hold two products (`second`): what a
+// tile of one leaves idle at the end the other fills, and the start of a
+// launch, some 5 us, is paid once.
 #pragma once
+
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -44,8 +53,57 @@ struct GemmRing {
     static constexpr int kSmem = kStages * kStage + 1024 + kGemmEpilogueWarps * kWarpStage;
 };
 
+// Items that the warps of a block may be apart: the copies run ahead of the
+// products, and the epilogue behind.
+constexpr int kGemmAnswers = 4;
+
 struct GemmItem {
     int32_t m0, tile_n, split, chain, first, last;  // rows, tile of columns, inner blocks
+};
+
+// The items of a pair, as each of its roles walks through them: the first is
+// the block's own, the others arrive in a ring of answers.
+struct GemmWalk {
+    uint32_t answers, full, empty;  // shared memory; `empty` in the first block
+    int32_t item;                   // -1: no more
+    uint32_t slot = 0, phase = 0;
+
+    __device__ __forceinline__ GemmWalk(uint32_t answers_, uint32_t full_, uint32_t empty_)
+        : answers(answers_), full(full_), empty(empty_), item(int32_t(blockIdx.x / 2))
+    {
+    }
+    // For one thread.
+    __device__ __forceinline__ bool next(volatile int* dead)
+    {
+        if (!barrier_wait(full + 8 * slot, phase, dead))
+            return false;
+        const int32_t block = next_block(answers + 16 * slot);
+        barrier_arrive_at(empty + 8 * slot);
+        item = block < 0 ? -1 : block / 2;
+        step();
+        return true;
+    }
+    // For a warp, whose first lane arrives.
+    __device__ __forceinline__ bool next_of_warp(volatile int* dead)
+    {
+        const bool ok = barrier_wait(full + 8 * slot, phase, dead);
+        if (!__all_sync(0xFFFFFFFFu, ok))
+            return false;
+        const int32_t block = next_block(answers + 16 * slot);
+        __syncwarp();
+        if (threadIdx.x % 32 == 0)
+            barrier_arrive_at(empty + 8 * slot);
+        item = block < 0 ? -1 : block / 2;
+        step();
+        return true;
+    }
+    __device__ __forceinline__ void step()
+    {
+        if (++slot == kGemmAnswers) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
 };
 
 // Items in bands of 8 tiles of rows: the tiles that run at a time form a
@@ -66,29 +124,31 @@ __device__ __forceinline__ GemmItem gemm_item(const GemmShape& s, int32_t item, 
     it.last = int32_t(s.blocks * (part + 1) / parts);
     return it;
 }
-// The next item of a pair: its chains one after another, then `pairs` further.
-__device__ __forceinline__ void gemm_next(const GemmShape& s, int32_t pairs, int32_t& item,
-                                          int32_t& chain)
-{
-    if (++chain == s.chains) {
-        chain = 0;
-        item += pairs;
-    }
-}
-
-// E: the epilogue.  E::Params is its arguments; an object of E is made for
+// E, E2: the products' epilogues (E2 void: one product).  E::Params is its arguments; an object of E is made for
 // each tile and thread by E(params, shape, row, first column, columns, item,
 // which half of the tile's columns, 32 x 33 floats of shared memory of the warp's own), gets the
 // sums of its row by chunk(params, shape, column, number of the chunk, values,
-// those floats) and ends with end(params, shape).
-template <int BN, typename E>
+// those floats) and ends with end(params, shape); E::kUnroll chunks are
+// unrolled.
+template <typename E>
+struct ParamsOf {
+    using type = typename E::Params;
+};
+template <>
+struct ParamsOf<void> {
+    struct type {};
+};
+template <int BN, typename E, typename E2>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-           const __grid_constant__ GemmShape s, const __grid_constant__ typename E::Params e)
+           const __grid_constant__ GemmShape shape, const __grid_constant__ typename E::Params e,
+           const __grid_constant__ CUtensorMap map_a2, const __grid_constant__ CUtensorMap map_b2,
+           const __grid_constant__ GemmShape shape2, const __grid_constant__ typename ParamsOf<E2>::type e2)
 {
     using R = GemmRing<BN>;
     extern __shared__ unsigned char raw[];
-    __shared__ alignas(8) uint64_t bars[2 * R::kStages + 4];
+    __shared__ alignas(8) uint64_t bars[2 * R::kStages + 4 + 2 * kGemmAnswers];
+    __shared__ alignas(16) uint4 answers[kGemmAnswers];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     volatile int* const dead = &gave_up;
@@ -97,6 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const uint32_t ring = (smem_address(raw) + 1023) & ~1023u;
     const uint32_t full = smem_address(bars), empty = full + 8 * R::kStages;
     const uint32_t sums_full = empty + 8 * R::kStages, sums_empty = sums_full + 16;
+    const uint32_t next_full = sums_empty + 16, next_empty = next_full + 8 * kGemmAnswers;
 
     if (threadIdx.x == 0) {
         gave_up = 0;
@@ -107,6 +168,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         for (int i = 0; i < 2; ++i) {
             barrier_init(sums_full + 8 * i, 1);
             barrier_init(sums_empty + 8 * i, 2 * kGemmEpilogueWarps);
+        }
+        for (int i = 0; i < kGemmAnswers; ++i) {
+            barrier_init(next_full + 8 * i, 1);
+            // both blocks' copies and epilogues, the products
+            barrier_init(next_empty + 8 * i, 2 * (1 + kGemmEpilogueWarps) + 1);
         }
         barriers_visible();
         prefetch_map(&map_a);
@@ -123,47 +189,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     wait_before();
     go_ahead();
 
-    const int32_t items = s.tiles_m * s.tiles_n * s.splits;
-    const int32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    constexpr bool kTwo = !std::is_void_v<E2>;
+    // items of the first product
+    const int32_t count = shape.tiles_m * shape.tiles_n * shape.splits;
+    GemmWalk walk(smem_address(answers), next_full, in_block(next_empty, 0));
+    bool ok = true;
 
     if (warp == 0 && elect_one()) {
         uint32_t stage = 0, phase = 0;
         const uint32_t full_first = in_block(full, 0);
-        // of both blocks' tiles
-        const uint32_t bytes =
-            2 * (R::kBytesA + (s.b_across ? R::kBytesB : R::kRowsB * kGemmInner * 2));
-        bool ok = true;
-        for (int32_t item = pair, chain = 0; item < items && ok; gemm_next(s, pairs, item, chain)) {
-            const GemmItem it = gemm_item(s, item, chain);
-            const int32_t row_a = it.m0 + 128 * int32_t(rank);
-            const int32_t row_b = it.tile_n * BN + R::kRowsB * int32_t(rank);
-            for (int32_t k = it.first; k < it.last; ++k) {
-                ok = barrier_wait(empty + 8 * stage, phase ^ 1, dead);
-                if (!ok)
-                    break;
-                if (rank == 0)
-                    barrier_expect(full + 8 * stage, bytes);
-                const uint32_t bar = full_first + 8 * stage;
-                const uint32_t to = ring + stage * R::kStage;
-                const int32_t inner = k * kGemmInner;
-                if (!s.a_across) {
-                    load_tile(to, &map_a, inner, row_a, bar);
-                } else {
-                    load_tile(to, &map_a, row_a, inner, bar);
-                    load_tile(to + 8192, &map_a, row_a + 64, inner, bar);
-                }
-                if (!s.b_across) {
-                    load_tile(to + R::kBytesA, &map_b, inner, row_b, bar);
-                } else {
+        while (walk.item >= 0) {
+            const bool second = kTwo && walk.item >= count;
+            const GemmShape& s = second ? shape2 : shape;
+            const CUtensorMap* const a = second ? &map_a2 : &map_a;
+            const CUtensorMap* const b = second ? &map_b2 : &map_b;
+            // of both blocks' tiles
+            const uint32_t bytes =
+                2 * (R::kBytesA + (s.b_across ? R::kBytesB : R::kRowsB * kGemmInner * 2));
+            for (int32_t chain = 0; chain < s.chains && ok; ++chain) {
+                const GemmItem it = gemm_item(s, second ? walk.item - count : walk.item, chain);
+                const int32_t row_a = it.m0 + 128 * int32_t(rank);
+                const int32_t row_b = it.tile_n * BN + R::kRowsB * int32_t(rank);
+                for (int32_t k = it.first; k < it.last; ++k) {
+                    ok = barrier_wait(empty + 8 * stage, phase ^ 1, dead);
+                    if (!ok)
+                        break;
+                    if (rank == 0)
+                        barrier_expect(full + 8 * stage, bytes);
+                    const uint32_t bar = full_first + 8 * stage;
+                    const uint32_t to = ring + stage * R::kStage;
+                    const int32_t inner = k * kGemmInner;
+                    if (!s.a_across) {
+                        load_tile(to, a, inner, row_a, bar);
+                    } else {
+                        load_tile(to, a, row_a, inner, bar);
+                        load_tile(to + 8192, a, row_a + 64, inner, bar);
+                    }
+                    if (!s.b_across) {
+                        load_tile(to + R::kBytesA, b, inner, row_b, bar);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < R::kRowsB; i += 64)
-                        load_tile(to + R::kBytesA + i * 128, &map_b, row_b + i, inner, bar);
-                }
-                if (++stage == R::kStages) {
-                    stage = 0;
-                    phase ^= 1;
+                        for (int i = 0; i < R::kRowsB; i += 64)
+                            load_tile(to + R::kBytesA + i * 128, b, row_b + i, inner, bar);
+                    }
+                    if (++stage == R::kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
             }
+            ok = ok && walk.next(dead);
+            if (!ok)
+                break;
         }
         // the pair's products still read what this block's last tiles hold, and
         // say so at its barriers: the block outlives that
@@ -181,38 +258,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         }
     } else if (warp == 1 && rank == 0 && elect_one()) {
         uint32_t stage = 0, phase = 0;
-        const uint32_t step_a = s.a_across ? 2048 : 32, step_b = s.b_across ? 2048 : 32;
         int32_t n = 0;
-        bool ok = true;
-        for (int32_t item = pair, chain = 0; item < items && ok;
-             gemm_next(s, pairs, item, chain), ++n) {
-            const GemmItem it = gemm_item(s, item, chain);
-            const int32_t slot = n & 1;
-            ok = barrier_wait(sums_empty + 8 * slot, ((n >> 1) & 1) ^ 1, dead);
-            if (!ok)
-                break;
-            after_sync();
-            const uint32_t d = tmem + uint32_t(slot * R::kAccColumns);
-            for (int32_t k = it.first; k < it.last; ++k) {
-                ok = barrier_wait(full + 8 * stage, phase, dead);
+        while (walk.item >= 0) {
+            const bool second = kTwo && walk.item >= count;
+            const GemmShape& s = second ? shape2 : shape;
+            const uint32_t step_a = s.a_across ? 2048 : 32, step_b = s.b_across ? 2048 : 32;
+            for (int32_t chain = 0; chain < s.chains && ok; ++chain, ++n) {
+                const GemmItem it = gemm_item(s, second ? walk.item - count : walk.item, chain);
+                const int32_t slot = n & 1;
+                ok = barrier_wait(sums_empty + 8 * slot, ((n >> 1) & 1) ^ 1, dead);
                 if (!ok)
                     break;
                 after_sync();
-                const uint32_t at = ring + stage * R::kStage;
-                const uint64_t a = tile_descriptor(at, 8192);
-                const uint64_t b = tile_descriptor(at + R::kBytesA, 8192);
+                const uint32_t d = tmem + uint32_t(slot * R::kAccColumns);
+                for (int32_t k = it.first; k < it.last; ++k) {
+                    ok = barrier_wait(full + 8 * stage, phase, dead);
+                    if (!ok)
+                        break;
+                    after_sync();
+                    const uint32_t at = ring + stage * R::kStage;
+                    const uint64_t a = tile_descriptor(at, 8192);
+                    const uint64_t b = tile_descriptor(at + R::kBytesA, 8192);
 #pragma unroll
-                for (int i = 0; i < kGemmInner / 16; ++i)
-                    mma_pair(d, a + ((i * step_a) >> 4), b + ((i * step_b) >> 4), s.what,
-                             k > it.first || i > 0);
-                commit_pair(empty + 8 * stage);
-                if (++stage == R::kStages) {
-                    stage = 0;
-                    phase ^= 1;
+                    for (int i = 0; i < kGemmInner / 16; ++i)
+                        mma_pair(d, a + ((i * step_a) >> 4), b + ((i * step_b) >> 4), s.what,
+                                 k > it.first || i > 0);
+                    commit_pair(empty + 8 * stage);
+                    if (++stage == R::kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
+                if (ok)
+                    commit_pair(sums_full + 8 * slot);
             }
-            if (ok)
-                commit_pair(sums_full + 8 * slot);
+            ok = ok && walk.next(dead);
+            if (!ok)
+                break;
+        }
+    } else if (warp == 3 && rank == 0 && elect_one()) {
+        const uint32_t other = in_block(next_full, 1);
+        uint32_t slot = 0, phase = 0;
+        while (ok) {
+            ok = barrier_wait(next_empty + 8 * slot, phase ^ 1, dead);
+            if (!ok)
+                break;
+            barrier_expect(next_full + 8 * slot, 16);
+            barrier_expect_at(other + 8 * slot, 16);
+            ask_next(walk.answers + 16 * slot, next_full + 8 * slot);
+            ok = barrier_wait(next_full + 8 * slot, phase, dead);
+            if (ok && next_block(walk.answers + 16 * slot) < 0)
+                break;
+            if (++slot == kGemmAnswers) {
+                slot = 0;
+                phase ^= 1;
+            }
         }
     } else if (warp >= 4) {
         constexpr int kHalf = BN / 2, kChunk = kHalf < 32 ? kHalf : 32;
@@ -221,20 +321,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         float* const stage = reinterpret_cast<float*>(
             raw + (ring - smem_address(raw)) + R::kStages * R::kStage + (warp - 4) * R::kWarpStage);
         int32_t n = 0;
-        for (int32_t item = pair, chain = 0; item < items; gemm_next(s, pairs, item, chain), ++n) {
+        // One tile by the epilogue F; false if a wait ran out.
+        const auto tile = [&](auto* kind, const GemmShape& s, const auto& params, int32_t item,
+                              int32_t chain) {
+            using F = std::remove_pointer_t<decltype(kind)>;
             const GemmItem it = gemm_item(s, item, chain);
             const int32_t slot = n & 1;
             const int32_t row = it.m0 + 128 * int32_t(rank) + 32 * int32_t(quarter) +
                                 int32_t(threadIdx.x % 32);
             const int32_t column = it.tile_n * BN + kHalf * int32_t(half);
-            E epilogue(e, s, row, column, kHalf, it, int32_t(half), stage);
-            const bool ok = barrier_wait(sums_full + 8 * slot, (n >> 1) & 1, dead);
-            if (!__all_sync(0xFFFFFFFFu, ok))
-                break;
+            F epilogue(params, s, row, column, kHalf, it, int32_t(half), stage);
+            const bool there = barrier_wait(sums_full + 8 * slot, (n >> 1) & 1, dead);
+            if (!__all_sync(0xFFFFFFFFu, there))
+                return false;
             after_sync();
             const uint32_t from = tmem + uint32_t(slot * R::kAccColumns) + half * kHalf +
                                   ((32 * quarter) << 16);
-#pragma unroll
+            constexpr int kUnroll = F::kUnroll;
+#pragma unroll kUnroll
             for (int c = 0; c < kHalf / kChunk; ++c) {
                 float v[kChunk];
                 __syncwarp();
@@ -246,10 +350,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     if (threadIdx.x % 32 == 0)
                         barrier_arrive_at(done + 8 * slot);
                 }
-                epilogue.chunk(e, s, column + c * kChunk, c, v, stage);
+                epilogue.chunk(params, s, column + c * kChunk, c, v, stage);
             }
-            epilogue.end(e, s);
+            epilogue.end(params, s);
             __syncwarp();
+            ++n;
+            return true;
+        };
+        while (walk.item >= 0) {
+            if (!kTwo || walk.item < count) {
+                for (int32_t chain = 0; chain < shape.chains && ok; ++chain)
+                    ok = tile(static_cast<E*>(nullptr), shape, e, walk.item, chain);
+            }
+            if constexpr (kTwo)
+                if (walk.item >= count)
+                    for (int32_t chain = 0; chain < shape2.chains && ok; ++chain)
+                        ok = tile(static_cast<E2*>(nullptr), shape2, e2, walk.item - count, chain);
+            ok = ok && walk.next_of_warp(dead);
+            if (!ok)
+                break;
         }
     }
     __syncwarp();
@@ -259,24 +378,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     after_sync();
     if (warp == 2)
         tmem_free(tmem, R::kColumns);
-    if (threadIdx.x == 0 && *dead && s.gave_up)
-        *static_cast<volatile int32_t*>(s.gave_up) = 1;
+    if (threadIdx.x == 0 && *dead && shape.gave_up)
+        *static_cast<volatile int32_t*>(shape.gave_up) = 1;
 }
 
-// Launches it on as many pairs of blocks as there are items, or pairs of SMs.
+// One product as the kernel takes it.
+template <typename E>
+struct GemmPart {
+    CUtensorMap a, b;
+    GemmShape s{};  // all zero: none
+    typename ParamsOf<E>::type e{};
+};
+// Fills in what follows from the operands; s has the splits and chains.
 template <int BN, typename E>
-inline int gemm_launch(const CUtensorMap& a, const CUtensorMap& b, const GemmShape& s,
-                       const typename E::Params& e, int sm_count, cudaStream_t stream)
+inline int gemm_part(const GemmOperand& a, const GemmOperand& b, GemmShape s, bool bf16,
+                     const typename E::Params& e, GemmPart<E>* part)
+{
+    int rc = gemm_map(a, 128, bf16, &part->a);
+    if (rc == cudaSuccess)
+        rc = gemm_map(b, BN / 2, bf16, &part->b);
+    s.m = int32_t(a.outer);
+    s.n = int32_t(b.outer);
+    s.tiles_m = (s.m + kGemmTileM - 1) / kGemmTileM;
+    s.tiles_n = (s.n + BN - 1) / BN;
+    s.blocks = int32_t((a.inner + kGemmInner - 1) / kGemmInner);
+    s.what = mma_what(bf16, a.across, b.across, kGemmTileM, BN);
+    s.a_across = a.across;
+    s.b_across = b.across;
+    part->s = s;
+    part->e = e;
+    return rc;
+}
+
+// Launches a pair of blocks for each item of one or two products.
+template <int BN, typename E, typename E2>
+inline int gemm_launch(const GemmPart<E>& p, const GemmPart<E2>& q, cudaStream_t stream)
 {
     using R = GemmRing<BN>;
-    const int64_t items = int64_t(s.tiles_m) * s.tiles_n * s.splits;
-    const int pairs = int(items < sm_count / 2 ? items : sm_count / 2);
+    const int64_t items = int64_t(p.s.tiles_m) * p.s.tiles_n * p.s.splits +
+                          int64_t(q.s.tiles_m) * q.s.tiles_n * q.s.splits;
+    if (items >= int64_t(1) << 30)
+        return int(cudaErrorInvalidValue);
     const cudaError_t err = cudaFuncSetAttribute(
-        k_gemm<BN, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
+        k_gemm<BN, E, E2>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
     if (err != cudaSuccess)
         return int(err);
-    return launch_early(k_gemm<BN, E>, dim3(unsigned(2 * pairs)), kGemmThreads, R::kSmem, stream, a,
-                        b, s, e);
+    return launch_early(k_gemm<BN, E, E2>, dim3(unsigned(2 * items)), kGemmThreads, R::kSmem,
+                        stream, p.a, p.b, p.s, p.e, q.a, q.b, q.s, q.e);
+}
+template <int BN, typename E>
+inline int gemm_run(const GemmOperand& a, const GemmOperand& b, const GemmShape& s, bool bf16,
+                    const typename E::Params& e, cudaStream_t stream)
+{
+    GemmPart<E> p;
+    const int rc = gemm_part<BN, E>(a, b, s, bf16, e, &p);
+    if (rc != cudaSuccess)
+        return rc;
+    GemmPart<void> none;
+    none.a = p.a;
+    none.b = p.b;
+    return gemm_launch<BN, E, void>(p, none, stream);
 }
 
 }  // namespace detail

@@ -53,10 +53,21 @@ struct LinearPlan {
 };
 // a_across: whether a's outer dimension is the adjacent one; f32: out is
 // float32.
-LinearPlan linear_plan(int64_t rows, int64_t columns, int64_t inner, bool a_across, bool f32,
-                       int sm_count);
+struct LinearSize {
+    int64_t rows, columns, inner;
+    bool a_across, f32;
+};
+LinearPlan linear_plan(const LinearSize& p, int sm_count);
+// Plans of two products that do not depend on one another; true if they go in
+// one launch.
+bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, LinearPlan* p_plan,
+                     LinearPlan* q_plan);
 int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partials, int sm_count,
                    int32_t* gave_up, void* stream);
+// Two plain products (neither bias nor activation nor z) in one launch.
+int linear_product_two(const LinearProduct& p, const LinearPlan& p_plan, float* p_partials,
+                       const LinearProduct& q, const LinearPlan& q_plan, float* q_partials,
+                       int sm_count, int32_t* gave_up, void* stream);
 // A product over nothing.
 int launch_linear_zero(const LinearOut& to, int64_t rows, int64_t columns, int sm_count,
                        void* stream);

@@ -28,6 +28,7 @@ using osr::GemmOperand;
 using osr::known_dtype;
 using osr::LinearPlan;
 using osr::LinearProduct;
+using osr::LinearSize;
 using osr::on_vectors;
 using osr::Pieces;
 using osr::readable;
@@ -40,59 +41,68 @@ using osr::Workspace;
 constexpr int32_t kMaxFeatures = 1 << 24;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 
+struct Needs {
+    bool backward, copy_x, copy_weight, dz;
+    bool in_out;  // the weight, for its copy
+    bool dx, dweight, dbias;
+    bool grad_in_out, grad_f32, grad_mixed;  // neither float32 nor the other matrices' type
+};
+// How a call is computed; a function of the sizes and needs.
+struct Plans {
+    LinearPlan forward{}, dx{}, dweight{};
+    bool together = false;  // dx and dweight in one launch
+    int32_t strips = 0;
+};
+Plans make_plans(const linear_ctx* c, int64_t rows, const Needs& n)
+{
+    Plans p;
+    const int sms = c->base.sm_count;
+    if (!n.backward) {
+        p.forward = osr::linear_plan(LinearSize{rows, c->out, c->in, false, false}, sms);
+        return p;
+    }
+    const LinearSize dx{rows, c->in, c->out, false, false};
+    const LinearSize dw{n.grad_in_out ? c->in : c->out, n.grad_in_out ? c->out : c->in, rows, true,
+                        n.grad_f32};
+    if (n.dx && n.dweight && !n.grad_mixed) {
+        p.together = osr::linear_plan_two(dx, dw, sms, &p.dx, &p.dweight);
+    } else {
+        if (n.dx)
+            p.dx = osr::linear_plan(dx, sms);
+        if (n.dweight)
+            p.dweight = osr::linear_plan(dw, sms);
+    }
+    if (n.dbias)
+        p.strips = osr::linear_strips(rows, c->out, sms);
+    return p;
+}
+
 // Where the parts of a call's workspace lie; NULL where the call needs none.
 struct Parts {
     void* x = nullptr;
     void* weight = nullptr;
     void* dy = nullptr;  // dz, or a copy of dy
     float* partials = nullptr;
+    float* dweight_partials = nullptr;
     float* sums = nullptr;
-    LinearPlan forward{}, dx{}, dweight{};
-    int32_t strips = 0;
 };
-struct Needs {
-    bool backward, copy_x, copy_weight, dz;
-    bool in_out;  // the weight, for its copy
-    bool dx, dweight, dbias;
-    bool grad_in_out, grad_f32;
-};
-
-LinearPlan plan_dweight(const linear_ctx* c, int64_t rows, bool grad_in_out, bool f32)
-{
-    return osr::linear_plan(grad_in_out ? c->in : c->out, grad_in_out ? c->out : c->in, rows, true,
-                            f32, c->base.sm_count);
-}
-
-int64_t lay_out(const linear_ctx* c, int64_t rows, const Needs& n, void* memory, Parts* p)
+int64_t lay_out(const linear_ctx* c, int64_t rows, const Needs& n, const Plans& plans,
+                void* memory, Parts* p)
 {
     Workspace w(memory);
-    const int sms = c->base.sm_count;
     if (n.copy_x)
         p->x = w.take(2 * rows * whole(c->in));
     if (n.copy_weight)
         p->weight = w.take(2 * (n.in_out ? c->in * whole(c->out) : c->out * whole(c->in)));
-    int64_t partials = 0;
-    if (!n.backward) {
-        p->forward = osr::linear_plan(rows, c->out, c->in, false, false, sms);
-        partials = p->forward.partials;
-    } else {
-        if (n.dz)
-            p->dy = w.take(2 * rows * whole(c->out));
-        if (n.dx) {
-            p->dx = osr::linear_plan(rows, c->in, c->out, false, false, sms);
-            partials = p->dx.partials;
-        }
-        if (n.dweight) {
-            p->dweight = plan_dweight(c, rows, n.grad_in_out, n.grad_f32);
-            partials = partials > p->dweight.partials ? partials : p->dweight.partials;
-        }
-        if (n.dbias) {
-            p->strips = osr::linear_strips(rows, c->out, sms);
-            p->sums = static_cast<float*>(w.take(4 * int64_t(p->strips) * c->out));
-        }
-    }
-    if (partials)
-        p->partials = static_cast<float*>(w.take(4 * partials));
+    if (n.dz)
+        p->dy = w.take(2 * rows * whole(c->out));
+    if (n.dbias)
+        p->sums = static_cast<float*>(w.take(4 * int64_t(plans.strips) * c->out));
+    const int64_t sums = n.backward ? plans.dx.partials : plans.forward.partials;
+    if (sums)
+        p->partials = static_cast<float*>(w.take(4 * sums));
+    if (plans.dweight.partials)
+        p->dweight_partials = static_cast<float*>(w.take(4 * plans.dweight.partials));
     return w.bytes();
 }
 
@@ -172,11 +182,14 @@ int linear_workspace(linear_ctx* ctx, int64_t rows, int32_t flags, int64_t* byte
     const bool back = flags & LINEAR_FOR_BACKWARD, any = flags & LINEAR_FOR_ANY_ADDRESS;
     // the most that any layout of the weight and its gradient takes
     for (int layout = 0; layout < 4; ++layout) {
-        Parts p;
-        const Needs n{back, any, any, back, (layout & 1) != 0, back, back, back, (layout & 2) != 0,
-                      false};
-        const int64_t b = lay_out(ctx, rows, n, nullptr, &p);
-        *bytes = *bytes > b ? *bytes : b;
+        Needs n{back, any, any, back, (layout & 1) != 0, back, back, back, (layout & 2) != 0};
+        // dx and dweight in one launch, or each on its own
+        for (int apart = 0; apart < (back ? 2 : 1); ++apart) {
+            n.grad_mixed = apart != 0;
+            Parts p;
+            const int64_t b = lay_out(ctx, rows, n, make_plans(ctx, rows, n), nullptr, &p);
+            *bytes = *bytes > b ? *bytes : b;
+        }
     }
     return ADAMW_OK;
 }
@@ -222,9 +235,10 @@ int linear_forward(linear_ctx* ctx, const void* d_x, int64_t x_stride, const voi
     n.copy_x = !gemm_readable(d_x, rows > 1 ? x_stride : 0);
     n.copy_weight = !gemm_readable(d_weight, w_rows > 1 ? weight_stride : 0);
     n.in_out = in_out;
+    const Plans plans = make_plans(ctx, rows, n);
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
-                                   lay_out(ctx, rows, n, d_workspace, &p))))
+                                   lay_out(ctx, rows, n, plans, d_workspace, &p))))
         return rc;
     DeviceScope scope(ctx->base.device);
     int e = readable(&d_x, &x_stride, rows, in, p.x, stream);
@@ -251,7 +265,7 @@ int linear_forward(linear_ctx* ctx, const void* d_x, int64_t x_stride, const voi
     m.to.vectors = on_vectors(d_y, y_stride, rows, 2) &&
                    (!d_residual || on_vectors(d_residual, residual_stride, rows, 2)) &&
                    (!d_z || on_vectors(d_z, z_stride, rows, 2));
-    e = osr::linear_product(m, p.forward, p.partials, ctx->base.sm_count, ctx->base.gave_up, stream);
+    e = osr::linear_product(m, plans.forward, p.partials, ctx->base.sm_count, ctx->base.gave_up, stream);
     return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "linear layer launch");
 }
 
@@ -306,13 +320,15 @@ int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride, const 
     n.in_out = in_out;
     n.grad_in_out = grad_in_out;
     n.grad_f32 = grad_dtype == ADAMW_DTYPE_F32;
+    n.grad_mixed = !n.grad_f32 && grad_dtype != dtype;
     n.dx = dx_rows;
     n.dweight = d_dweight && rows;
     n.dbias = d_dbias && rows;
     n.dz = rows && (d_dx || d_dweight) && (act || !gemm_readable(d_dy, rows > 1 ? dy_stride : 0));
+    const Plans plans = rows ? make_plans(ctx, rows, n) : Plans{};
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
-                                   lay_out(ctx, rows, n, d_workspace, &p))))
+                                   lay_out(ctx, rows, n, plans, d_workspace, &p))))
         return rc;
     int e = cudaSuccess;
     if (n.dz || n.dbias) {
@@ -328,52 +344,50 @@ int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride, const 
         s.rows = rows;
         s.columns = out;
         s.partials = p.sums;
-        s.strips = n.dbias ? p.strips : osr::linear_strips(rows, out, sms);
+        s.strips = n.dbias ? plans.strips : osr::linear_strips(rows, out, sms);
         e = osr::launch_linear_slope(s, stream);
     }
     if (e == cudaSuccess && d_dbias)
-        e = osr::launch_linear_bias_grad(p.sums, n.dbias ? p.strips : 0, out, d_dbias, grad_dtype,
-                                         accumulate, stream);
+        e = osr::launch_linear_bias_grad(p.sums, n.dbias ? plans.strips : 0, out, d_dbias,
+                                         grad_dtype, accumulate, stream);
     const void* dz = n.dz ? p.dy : d_dy;
     const int64_t dz_stride = n.dz ? whole(out) : dy_stride;
-    if (e == cudaSuccess && n.dx) {
+    if (e == cudaSuccess && n.dx)
         e = readable(&d_weight, &weight_stride, w_rows, w_cols, p.weight, stream);
-        LinearProduct m{};
-        m.a = GemmOperand{dz, rows, out, dz_stride, false};
-        m.b = GemmOperand{d_weight, in, out, weight_stride, !in_out};
-        m.bf16 = dtype == ADAMW_DTYPE_BF16;
-        m.to.out = d_dx;
-        m.to.stride = dx_stride;
-        m.to.dtype = dtype;
-        m.to.alpha = 1.0f;
-        m.to.vectors = on_vectors(d_dx, dx_stride, rows, 2);
-        if (e == cudaSuccess)
-            e = osr::linear_product(m, p.dx, p.partials, sms, ctx->base.gave_up, stream);
-    }
-    if (e == cudaSuccess && d_dweight) {
-        LinearProduct m{};
-        m.bf16 = dtype == ADAMW_DTYPE_BF16;
-        m.to.out = d_dweight;
-        m.to.stride = dweight_stride;
-        m.to.dtype = grad_dtype;
-        m.to.alpha = 1.0f;
-        if (accumulate)
-            osr::accumulate_into(m.to);
-        m.to.vectors = on_vectors(d_dweight, dweight_stride, g_rows, gs);
-        if (rows == 0) {
-            e = osr::launch_linear_zero(m.to, g_rows, g_cols, sms, stream);
-        } else {
-            e = readable(&d_x, &x_stride, rows, in, p.x, stream);
-            m.a = GemmOperand{dz, out, rows, dz_stride, true};
-            m.b = GemmOperand{d_x, in, rows, x_stride, true};
-            if (grad_in_out) {
-                const GemmOperand a = m.a;
-                m.a = m.b;
-                m.b = a;
-            }
-            if (e == cudaSuccess)
-                e = osr::linear_product(m, p.dweight, p.partials, sms, ctx->base.gave_up, stream);
-        }
+    if (e == cudaSuccess && n.dweight)
+        e = readable(&d_x, &x_stride, rows, in, p.x, stream);
+    if (e != cudaSuccess)
+        return cuda_fail(cudaError_t(e), "linear layer launch");
+    LinearProduct x{}, w{};  // of dx and dweight
+    x.bf16 = w.bf16 = dtype == ADAMW_DTYPE_BF16;
+    x.a = GemmOperand{dz, rows, out, dz_stride, false};
+    x.b = GemmOperand{d_weight, in, out, weight_stride, !in_out};
+    x.to.out = d_dx;
+    x.to.stride = dx_stride;
+    x.to.dtype = dtype;
+    x.to.alpha = 1.0f;
+    x.to.vectors = on_vectors(d_dx, dx_stride, rows, 2);
+    const GemmOperand by_out{dz, out, rows, dz_stride, true}, by_in{d_x, in, rows, x_stride, true};
+    w.a = grad_in_out ? by_in : by_out;
+    w.b = grad_in_out ? by_out : by_in;
+    w.to.out = d_dweight;
+    w.to.stride = dweight_stride;
+    w.to.dtype = grad_dtype;
+    w.to.alpha = 1.0f;
+    w.to.vectors = on_vectors(d_dweight, dweight_stride, g_rows, gs);
+    if (accumulate)
+        osr::accumulate_into(w.to);
+    int32_t* const gave_up = ctx->base.gave_up;
+    if (plans.together) {
+        e = osr::linear_product_two(x, plans.dx, p.partials, w, plans.dweight, p.dweight_partials,
+                                    sms, gave_up, stream);
+    } else {
+        if (n.dx)
+            e = osr::linear_product(x, plans.dx, p.partials, sms, gave_up, stream);
+        if (e == cudaSuccess && n.dweight)
+            e = osr::linear_product(w, plans.dweight, p.dweight_partials, sms, gave_up, stream);
+        if (e == cudaSuccess && d_dweight && rows == 0)
+            e = osr::launch_linear_zero(w.to, g_rows, g_cols, sms, stream);
     }
     return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "linear layer launch");
 }

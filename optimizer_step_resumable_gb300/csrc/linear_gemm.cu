@@ -20,6 +20,7 @@ __device__ __forceinline__ LinearOut with_factor(const LinearOut& o)
 // neighbouring columns of one row of the product.
 struct SwappedEpilogue {
     using Params = StoreParams;
+    static constexpr int kUnroll = 1;
     int32_t column;
     int32_t split;
     bool again;  // a later chain
@@ -73,8 +74,8 @@ struct SwappedEpilogue {
 };
 
 // out = finish(sum over the splits, in order).  What bounds it: the sums' way
-// from L2; a thread has eight neighbouring ones (or one, where rows are not
-// whole vectors), of four splits at a time.
+// from L2.  Their rows are whole vectors; a thread has one, of four splits at
+// a time.
 constexpr int kJoinThreads = 256;
 struct JoinParams {
     LinearOut o;
@@ -82,37 +83,40 @@ struct JoinParams {
     int64_t rows, columns;
     int32_t splits;
 };
-template <bool kVector>
 __global__ void __launch_bounds__(kJoinThreads) k_linear_join(const JoinParams p)
 {
     wait_before();
     go_ahead();
     const LinearOut o = with_factor(p.o);
-    const int64_t each = p.rows * p.columns;
-    constexpr int kEach = kVector ? 8 : 1;
-    for (int64_t i = (int64_t(blockIdx.x) * kJoinThreads + threadIdx.x) * kEach; i < each;
-         i += int64_t(gridDim.x) * kJoinThreads * kEach) {
-        const int64_t row = i / p.columns, column = i - row * p.columns;
-        float v[kEach] = {};
+    const int64_t vectors = (p.columns + 7) / 8, all = p.rows * vectors;
+    for (int64_t i = int64_t(blockIdx.x) * kJoinThreads + threadIdx.x; i < all;
+         i += int64_t(gridDim.x) * kJoinThreads) {
+        const int64_t row = i / vectors, column = (i - row * vectors) * 8;
+        float v[8] = {};
         for (int32_t s = 0; s < p.splits; s += 4) {
-            uint32_t w[4][kEach] = {};
+            uint32_t w[4][8] = {};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (s + j < p.splits) {
-                    const float* const from = p.partials + (s + j) * each + i;
-                    if constexpr (kVector)
-                        load32(from, w[j]);
-                    else
-                        w[j][0] = __float_as_uint(__ldcg(from));
-                }
+                if (s + j < p.splits)
+                    load32(p.partials + ((s + j) * all + i) * 8, w[j]);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int c = 0; c < kEach; ++c)
+                for (int c = 0; c < 8; ++c)
                     v[c] += __uint_as_float(w[j][c]);
         }
         with_activation(o.act, [&](auto act) {
-            finish_some<decltype(act)::value, kEach>(o, row, column, v);
+            constexpr int kAct = decltype(act)::value;
+            if (column + 8 <= p.columns) {
+                finish_some<kAct>(o, row, column, v);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (column + c < p.columns) {
+                        float f[1] = {v[c]};
+                        finish_some<kAct>(o, row, column + c, f);
+                    }
+            }
         });
     }
 }
@@ -120,104 +124,210 @@ __global__ void __launch_bounds__(kJoinThreads) k_linear_join(const JoinParams p
 int join(const LinearOut& o, const float* partials, int64_t rows, int64_t columns, int32_t splits,
          int sm_count, cudaStream_t stream)
 {
-    const bool vector = columns % 8 == 0;
-    const int64_t work = rows * columns / (vector ? 8 : 1);
-    const int64_t want = (work + kJoinThreads - 1) / kJoinThreads, most = int64_t(sm_count) * 8;
-    return launch_early(vector ? k_linear_join<true> : k_linear_join<false>,
-                        dim3(unsigned(want < most ? want : most)), kJoinThreads, 0, stream,
-                        JoinParams{o, partials, rows, columns, splits});
+    const int64_t want = (rows * ((columns + 7) / 8) + kJoinThreads - 1) / kJoinThreads;
+    const int64_t most = int64_t(sm_count) * 8;
+    return launch_early(k_linear_join, dim3(unsigned(want < most ? want : most)), kJoinThreads, 0,
+                        stream, JoinParams{o, partials, rows, columns, splits});
+}
+
+// Microseconds that a pair of blocks takes for a block of the inner dimension
+// of a tile of 256 x bn (8192 x 4096 x 8192: 283, 324 and 414 us in tiles of 256,
+// 192 and 128 columns, 64 blocks in 14, 19 and 27 turns), and for the start and
+// the last epilogue of a launch (8192 x 768 x 768: 15.8, 12.9 and 14.4 us).
+double block_us(int bn)
+{
+    return bn == 256 ? 0.316 : bn == 192 ? 0.27 : bn == 128 ? 0.24 : bn == 64 ? 0.2 : 0.18;
+}
+double launch_us(int bn) { return 3.0 + 0.016 * bn; }
+// Sums of a divided inner dimension go to L2 and back, and a launch joins them.
+double join_us(int64_t elements, int64_t splits)
+{
+    return splits > 1 ? 4.0 + double(elements) * double(splits) * 8.0 / 6e6 : 0.0;
+}
+
+int64_t inner_blocks(int64_t inner) { return (inner + kGemmInner - 1) / kGemmInner; }
+int64_t tiles_of(int64_t m, int64_t n, int bn)
+{
+    return ((m + kGemmTileM - 1) / kGemmTileM) * ((n + bn - 1) / bn);
+}
+
+// The tensor cores cut each addition, by up to 2^-24 of the sum: 16384
+// products in a row lose 2e-5 of it, which shows in float32 and not in 16
+// bits.  Chains of at most 96 blocks, 6144 products, lose 7e-6.
+void finish_plan(const LinearSize& p, LinearPlan* plan)
+{
+    const int64_t each = (inner_blocks(p.inner) + plan->splits - 1) / plan->splits;
+    plan->chains = p.f32 ? int32_t((each + 95) / 96) : 1;
+    plan->partials =
+        plan->splits > 1 ? plan->splits * p.rows * ((p.columns + 7) / 8 * 8) : 0;
+}
+
+// The time until `n` long items and `m` short ones, taken in this order by
+// whichever pair is free, are done.
+double busy_us(int64_t n, double long_us, int64_t m, double short_us, int64_t pairs)
+{
+    const int64_t rounds = n / pairs, ahead = n - rounds * pairs;
+    const double low = double(rounds) * long_us, high = ahead ? low + long_us : low;
+    if (m == 0)
+        return high;
+    // the short ones fill the pairs up to t, each pair at most one beyond
+    const double total = double(n) * long_us + double(m) * short_us;
+    double t = total / double(pairs);
+    t = t > low ? t : low;
+    for (int i = 0; i < 64; ++i) {
+        const int64_t fit =
+            int64_t((t - low) / short_us + 1e-9) * (pairs - ahead) +
+            (t > high ? int64_t((t - high) / short_us + 1e-9) * ahead : 0);
+        if (fit >= m)
+            break;
+        t += short_us / 8;
+    }
+    return t > high ? t : high;
+}
+
+StoreProduct store_product(const LinearProduct& p, const LinearPlan& plan, float* partials,
+                           int32_t* gave_up)
+{
+    StoreProduct s{p.a, p.b, GemmShape{}, StoreParams{p.to, p.a.outer, p.b.outer, 0}};
+    s.s.splits = plan.splits;
+    s.s.chains = plan.chains;
+    s.s.gave_up = gave_up;
+    if (plan.splits > 1) {
+        LinearOut sums{};
+        sums.out = partials;
+        sums.stride = (p.b.outer + 7) / 8 * 8;
+        sums.alpha = 1.0f;
+        sums.dtype = sums.residual_dtype = ADAMW_DTYPE_F32;
+        sums.vectors = 1;
+        s.p.o = sums;
+        s.p.split_stride = p.a.outer * sums.stride;
+    }
+    return s;
+}
+int join_product(const LinearProduct& p, const LinearPlan& plan, const float* partials,
+                 int sm_count, void* stream)
+{
+    if (plan.splits == 1)
+        return cudaSuccess;
+    return join(p.to, partials, p.a.outer, p.b.outer, plan.splits, sm_count,
+                static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
 
-namespace {
-
-// Microseconds that a pair of blocks takes for a block of the inner dimension
-// of a tile, and for a tile besides.
-constexpr double block_us(int bn) { return bn == 256 ? 0.30 : bn == 192 ? 0.24 : bn == 128 ? 0.18 : 0.16; }
-constexpr double kTileUs = 0.6;
-
-}  // namespace
-
-LinearPlan linear_plan(int64_t rows, int64_t columns, int64_t inner, bool a_across, bool f32,
-                       int sm_count)
+LinearPlan linear_plan(const LinearSize& p, int sm_count)
 {
     LinearPlan best{};
-    const bool swapped = rows <= 128 && rows < columns;
-    const int64_t m = swapped ? columns : rows, n = swapped ? rows : columns;
-    const int64_t blocks = (inner + kGemmInner - 1) / kGemmInner, pairs = sm_count / 2;
+    const bool swapped = p.rows <= 128 && p.rows < p.columns;
+    const int64_t m = swapped ? p.columns : p.rows, n = swapped ? p.rows : p.columns;
+    const int64_t blocks = inner_blocks(p.inner), pairs = sm_count / 2;
     // rows of fewer than 64 outer elements cannot be copied across
-    const int least = swapped && !(a_across || n > 64) ? (n > 32 ? 64 : 32) : 128;
+    const int least = swapped && !(p.a_across || n > 64) ? (n > 32 ? 64 : 32) : 128;
     const int widths[] = {least, 192, 256};
     // Time goes by the turns that the busiest pair takes; cutting the inner
-    // dimension fills the GPU better, and joining the sums costs their way to
-    // L2 and back and a launch.
+    // dimension fills the GPU better.
     double least_us = 0.0;
     for (const int bn : widths) {
         if (bn > least && (swapped || n <= bn - 64))
             continue;
-        const int64_t tiles = ((m + kGemmTileM - 1) / kGemmTileM) * ((n + bn - 1) / bn);
+        const int64_t tiles = tiles_of(m, n, bn);
         for (int64_t s = 1; s <= 32 && s <= (blocks + 3) / 4; ++s) {
             const double turns = double((tiles * s + pairs - 1) / pairs);
-            const double tile = double((blocks + s - 1) / s) * block_us(bn);
-            // the last tile's epilogue has nothing beside it
-            double us = turns * (tile > kTileUs ? tile : kTileUs) + kTileUs * bn / 128.0;
-            if (s > 1)
-                us += 3.0 + double(m) * double(n) * double(s) * 8.0 / 6e6;
+            const double us = turns * double((blocks + s - 1) / s) * block_us(bn) +
+                              launch_us(bn) + join_us(m * n, s);
             if (best.bn == 0 || us < least_us) {
                 least_us = us;
                 best.bn = bn;
                 best.splits = int32_t(s);
             }
+            if (tiles >= 4 * pairs)
+                break;  // enough turns
         }
     }
     best.swapped = swapped;
-    best.partials = best.splits > 1 ? best.splits * rows * columns : 0;
-    // The tensor cores cut each addition, by up to 2^-24 of the sum: 16384
-    // products in a row lose 2e-5 of it, which shows in float32 and not in 16
-    // bits.  Chains of at most 64 blocks, 4096 products, lose a quarter.
-    const int64_t each = (blocks + best.splits - 1) / best.splits;
-    best.chains = f32 ? int32_t((each + 63) / 64) : 1;
+    finish_plan(p, &best);
     return best;
+}
+
+bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, LinearPlan* p_plan,
+                     LinearPlan* q_plan)
+{
+    *p_plan = linear_plan(p, sm_count);
+    *q_plan = linear_plan(q, sm_count);
+    // tiles of 256 x 256 have to fit both
+    if (p_plan->swapped || p.rows <= 128 || p.columns <= 128 || q.rows <= 128 || q.columns <= 128)
+        return false;
+    const int64_t pairs = sm_count / 2, blocks[] = {inner_blocks(p.inner), inner_blocks(q.inner)};
+    const int64_t tiles[] = {tiles_of(p.rows, p.columns, 256), tiles_of(q.rows, q.columns, 256)};
+    const int64_t sizes[] = {p.rows * p.columns, q.rows * q.columns};
+    static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24};
+    int best[2] = {1, 1};
+    double least_us = 0.0;
+    for (const int s : kSplits) {
+        if (s > 1 && (s > (blocks[0] + 3) / 4 || tiles[0] * (s - 1) >= 4 * pairs))
+            break;
+        for (const int t : kSplits) {
+            if (t > 1 && (t > (blocks[1] + 3) / 4 || tiles[1] * (t - 1) >= 4 * pairs))
+                break;
+            const double a = double((blocks[0] + s - 1) / s) * block_us(256);
+            const double b = double((blocks[1] + t - 1) / t) * block_us(256);
+            const int64_t n = tiles[0] * s, m = tiles[1] * t;
+            const double us = (a >= b ? busy_us(n, a, m, b, pairs) : busy_us(m, b, n, a, pairs)) +
+                              join_us(sizes[0], s) + join_us(sizes[1], t);
+            if (least_us == 0.0 || us < least_us) {
+                least_us = us;
+                best[0] = s;
+                best[1] = t;
+            }
+        }
+    }
+    *p_plan = LinearPlan{false, 256, best[0], 1, 0};
+    *q_plan = LinearPlan{false, 256, best[1], 1, 0};
+    finish_plan(p, p_plan);
+    finish_plan(q, q_plan);
+    return true;
 }
 
 int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partials, int sm_count,
                    int32_t* gave_up, void* stream)
 {
-    const int64_t rows = p.a.outer, columns = p.b.outer;
-    StoreParams params{p.to, rows, columns, 0};
-    if (plan.splits > 1) {
-        LinearOut sums{};
-        sums.out = partials;
-        sums.stride = columns;
-        sums.alpha = 1.0f;
-        sums.dtype = sums.residual_dtype = ADAMW_DTYPE_F32;
-        sums.vectors = columns % 8 == 0;
-        params.o = sums;
-        params.split_stride = rows * columns;
-    }
-    GemmShape s{};
-    s.splits = plan.splits;
-    s.chains = plan.chains;
-    s.gave_up = gave_up;
+    StoreProduct s = store_product(p, plan, partials, gave_up);
     int e;
     if (plan.swapped) {
-        e = plan.bn == 32   ? gemm_run<32, SwappedEpilogue>(p.b, p.a, s, p.bf16, params, sm_count,
-                                                            stream)
-            : plan.bn == 64 ? gemm_run<64, SwappedEpilogue>(p.b, p.a, s, p.bf16, params, sm_count,
-                                                            stream)
-                            : gemm_run<128, SwappedEpilogue>(p.b, p.a, s, p.bf16, params, sm_count,
-                                                             stream);
+        const auto run = plan.bn == 32   ? gemm_run<32, SwappedEpilogue>
+                         : plan.bn == 64 ? gemm_run<64, SwappedEpilogue>
+                                         : gemm_run<128, SwappedEpilogue>;
+        e = run(s.b, s.a, s.s, p.bf16, s.p, static_cast<cudaStream_t>(stream));
+    } else if (s.p.o.dtype == ADAMW_DTYPE_F32) {
+        e = linear_store_f32(plan.bn, s, p.bf16, stream);
     } else {
-        const auto store = params.o.dtype == ADAMW_DTYPE_F32    ? linear_store_f32
-                           : params.o.dtype == ADAMW_DTYPE_BF16 ? linear_store_bf16
-                                                                : linear_store_f16;
-        e = store(plan.bn, p.a, p.b, s, p.bf16, params, sm_count, stream);
+        const bool plain = !s.p.o.bias && !s.p.o.z && s.p.o.act == LINEAR_NONE;
+        const auto store =
+            s.p.o.dtype == ADAMW_DTYPE_BF16 ? linear_store_bf16 : linear_store_f16;
+        e = store(plan.bn, s, plain, p.bf16, stream);
     }
-    if (e != cudaSuccess || plan.splits == 1)
-        return e;
-    return join(p.to, partials, rows, columns, plan.splits, sm_count,
-                static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? join_product(p, plan, partials, sm_count, stream) : e;
+}
+
+int linear_product_two(const LinearProduct& p, const LinearPlan& p_plan, float* p_partials,
+                       const LinearProduct& q, const LinearPlan& q_plan, float* q_partials,
+                       int sm_count, int32_t* gave_up, void* stream)
+{
+    const StoreProduct a = store_product(p, p_plan, p_partials, gave_up);
+    const StoreProduct b = store_product(q, q_plan, q_partials, gave_up);
+    // the longer items first
+    const bool turned = inner_blocks(q.a.inner) / q_plan.splits >
+                        inner_blocks(p.a.inner) / p_plan.splits;
+    const StoreProduct &first = turned ? b : a, &second = turned ? a : b;
+    int e;
+    switch (first.p.o.dtype) {
+    case ADAMW_DTYPE_F32: e = linear_store_two_f32(first, second, p.bf16, stream); break;
+    case ADAMW_DTYPE_BF16: e = linear_store_two_bf16(first, second, stream); break;
+    default: e = linear_store_two_f16(first, second, stream);
+    }
+    if (e == cudaSuccess)
+        e = join_product(p, p_plan, p_partials, sm_count, stream);
+    return e == cudaSuccess ? join_product(q, q_plan, q_partials, sm_count, stream) : e;
 }
 
 int launch_linear_zero(const LinearOut& to, int64_t rows, int64_t columns, int sm_count,

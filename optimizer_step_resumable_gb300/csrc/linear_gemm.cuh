@@ -13,37 +13,25 @@ struct StoreParams {
     int64_t split_stride;  // elements of out from one split's sums to the next's
 };
 
-// Tiles of 256 x bn (128, 192 or 256), the product's rows along the long side.
-int linear_store_f32(int bn, const GemmOperand& a, const GemmOperand& b, const GemmShape& s,
-                     bool bf16, const StoreParams& p, int sm_count, void* stream);
-int linear_store_bf16(int bn, const GemmOperand& a, const GemmOperand& b, const GemmShape& s,
-                      bool bf16, const StoreParams& p, int sm_count, void* stream);
-int linear_store_f16(int bn, const GemmOperand& a, const GemmOperand& b, const GemmShape& s,
-                     bool bf16, const StoreParams& p, int sm_count, void* stream);
+// One product, ready for its tiles; its sums go where p says.
+struct StoreProduct {
+    GemmOperand a, b;
+    GemmShape s;  // splits, chains
+    StoreParams p;
+};
+// Tiles of 256 x bn (128, 192 or 256), the product's rows along the long side,
+// for an output of the type; `plain`: neither bias nor activation nor z, which
+// float32 outputs never have.
+int linear_store_f32(int bn, const StoreProduct& p, bool bf16, void* stream);
+int linear_store_bf16(int bn, const StoreProduct& p, bool plain, bool bf16, void* stream);
+int linear_store_f16(int bn, const StoreProduct& p, bool plain, bool bf16, void* stream);
+// Two plain products in one launch, in tiles of 256 x 256; the types of their
+// outputs, float32 or bf16's 16-bit type.
+int linear_store_two_f32(const StoreProduct& p, const StoreProduct& q, bool bf16, void* stream);
+int linear_store_two_bf16(const StoreProduct& p, const StoreProduct& q, void* stream);
+int linear_store_two_f16(const StoreProduct& p, const StoreProduct& q, void* stream);
 
 namespace detail {
-
-// Launches a product's tiles.
-template <int BN, typename E>
-inline int gemm_run(const GemmOperand& a, const GemmOperand& b, GemmShape s, bool bf16,
-                    const typename E::Params& p, int sm_count, void* stream)
-{
-    CUtensorMap ma, mb;
-    int e = gemm_map(a, 128, bf16, &ma);
-    if (e == cudaSuccess)
-        e = gemm_map(b, BN / 2, bf16, &mb);
-    if (e != cudaSuccess)
-        return e;
-    s.m = int32_t(a.outer);
-    s.n = int32_t(b.outer);
-    s.tiles_m = (s.m + kGemmTileM - 1) / kGemmTileM;
-    s.tiles_n = (s.n + BN - 1) / BN;
-    s.blocks = int32_t((a.inner + kGemmInner - 1) / kGemmInner);
-    s.what = mma_what(bf16, a.across, b.across, kGemmTileM, BN);
-    s.a_across = a.across;
-    s.b_across = b.across;
-    return gemm_launch<BN, E>(ma, mb, s, p, sm_count, static_cast<cudaStream_t>(stream));
-}
 
 template <int kType>
 constexpr int kSize = kType == ADAMW_DTYPE_F32 ? 4 : 2;
@@ -59,9 +47,11 @@ __device__ __forceinline__ float get(const char* p)
 // two chunks ahead (one, if it is float32).  Others go through shared memory,
 // so that a warp's lanes have neighbouring columns of one row, eight rows at a
 // time.
-template <int kOut>
+// kPlain: neither bias nor activation nor z.
+template <int kOut, bool kPlain>
 struct StoreEpilogue {
     using Params = StoreParams;
+    static constexpr int kUnroll = 4;
     static constexpr bool kF32 = kOut == ADAMW_DTYPE_F32, kBf16 = kOut == ADAMW_DTYPE_BF16;
 
     int32_t row, end_column;  // of the columns that are this thread's
@@ -75,7 +65,7 @@ struct StoreEpilogue {
     __device__ StoreEpilogue(const Params& p, const GemmShape&, int32_t r, int32_t column,
                              int32_t count, const GemmItem& it, int32_t, float* stage)
         : row(r), end_column(column + count < p.columns ? column + count : int32_t(p.columns)),
-          alpha(p.o.alpha), vectors(p.o.vectors), bias(p.o.bias)
+          alpha(p.o.alpha), vectors(p.o.vectors), bias(!kPlain && p.o.bias)
     {
         const LinearOut& o = p.o;
         if (o.alpha_factor)
@@ -89,7 +79,7 @@ struct StoreEpilogue {
         from = again ? out
                      : static_cast<const char*>(o.residual) +
                            int64_t(r) * o.residual_stride * (add_f32 ? 4 : 2);
-        if (bias) {
+        if (!kPlain && bias) {
             const int lane = threadIdx.x % 32;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -161,16 +151,16 @@ struct StoreEpilogue {
         for (int i = 0; i < 32; ++i)
             v[i] *= alpha;
         if (vectors && column + 32 <= p.columns) {
-            if (bias)
+            if (!kPlain && bias)
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                     const float4 b = *reinterpret_cast<const float4*>(stage + 32 * c + i);
                     v[i] += b.x, v[i + 1] += b.y, v[i + 2] += b.z, v[i + 3] += b.w;
                 }
-            if (o.z && row < p.rows)
+            if (!kPlain && o.z && row < p.rows)
                 store(static_cast<char*>(o.z) + (int64_t(row) * o.z_stride + column) * kSize<kOut>,
                       v);
-            if (o.act != LINEAR_NONE)
+            if (!kPlain && o.act != LINEAR_NONE)
                 with_activation(o.act, [&](auto act) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -216,7 +206,7 @@ struct StoreEpilogue {
             const char* more = from - lane * add_step + int64_t(mine) * (add_f32 ? 4 : 2);
             char* z = static_cast<char*>(o.z) +
                       (int64_t(row - lane) * o.z_stride + mine) * kSize<kOut>;
-            const float b = bias ? lane_bias[c] : 0.0f;
+            const float b = !kPlain && bias ? lane_bias[c] : 0.0f;
             for (int r = 0; r < left; r += 8) {
                 float f[8], a[8];
 #pragma unroll
@@ -233,14 +223,14 @@ struct StoreEpilogue {
                                                                                  i * add_step);
                     more += 8 * add_step;
                 }
-                if (o.z) {
+                if (!kPlain && o.z) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         if (r + i < left)
                             store_as(z + i * z_step, 0, kOut, f[i]);
                     z += 8 * z_step;
                 }
-                if (o.act != LINEAR_NONE)
+                if (!kPlain && o.act != LINEAR_NONE)
                     with_activation(o.act, [&](auto act) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -258,15 +248,28 @@ struct StoreEpilogue {
     __device__ void end(const Params&, const GemmShape&) {}
 };
 
-template <int kOut>
-inline int linear_store(int bn, const GemmOperand& a, const GemmOperand& b, const GemmShape& s,
-                        bool bf16, const StoreParams& p, int sm_count, void* stream)
+template <int kOut, int kOut2>
+inline int store_two(const StoreProduct& p, const StoreProduct& q, bool bf16, void* stream)
 {
-    using E = StoreEpilogue<kOut>;
+    using E = StoreEpilogue<kOut, true>;
+    using E2 = StoreEpilogue<kOut2, true>;
+    GemmPart<E> one;
+    GemmPart<E2> two;
+    int e = gemm_part<256, E>(p.a, p.b, p.s, bf16, p.p, &one);
+    if (e == cudaSuccess)
+        e = gemm_part<256, E2>(q.a, q.b, q.s, bf16, q.p, &two);
+    return e == cudaSuccess ? gemm_launch<256, E, E2>(one, two, static_cast<cudaStream_t>(stream))
+                            : e;
+}
+template <int kOut, bool kPlain>
+inline int store_one(int bn, const StoreProduct& p, bool bf16, void* stream)
+{
+    using E = StoreEpilogue<kOut, kPlain>;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (bn) {
-    case 128: return gemm_run<128, E>(a, b, s, bf16, p, sm_count, stream);
-    case 192: return gemm_run<192, E>(a, b, s, bf16, p, sm_count, stream);
-    default: return gemm_run<256, E>(a, b, s, bf16, p, sm_count, stream);
+    case 128: return gemm_run<128, E>(p.a, p.b, p.s, bf16, p.p, st);
+    case 192: return gemm_run<192, E>(p.a, p.b, p.s, bf16, p.p, st);
+    default: return gemm_run<256, E>(p.a, p.b, p.s, bf16, p.p, st);
     }
 }
 

@@ -3,10 +3,10 @@
 
 namespace osr {
 
-int linear_store_bf16(int bn, const GemmOperand& a, const GemmOperand& b, const GemmShape& s,
-                      bool bf16, const StoreParams& p, int sm_count, void* stream)
+int linear_store_bf16(int bn, const StoreProduct& p, bool plain, bool bf16, void* stream)
 {
-    return detail::linear_store<ADAMW_DTYPE_BF16>(bn, a, b, s, bf16, p, sm_count, stream);
+    return plain ? detail::store_one<ADAMW_DTYPE_BF16, true>(bn, p, bf16, stream)
+                 : detail::store_one<ADAMW_DTYPE_BF16, false>(bn, p, bf16, stream);
 }
 
 }  // namespace osr
