@@ -29,7 +29,7 @@ __device__ __forceinline__ float exp2_fast(float x)
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
 
 struct PartsEpilogue {
-    static constexpr int kUnroll = 1;
+    static constexpr int kUnroll = 4;
     struct Params {
         const int64_t* target;
         float2* parts;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_ce_rows(const CeRows a)
 }
 
 struct GradientEpilogue {
-    static constexpr int kUnroll = 1;
+    static constexpr int kUnroll = 4;
     struct Params {
         const int64_t* target;
         const float* lse;
@@ -234,19 +234,21 @@ struct GradientEpilogue {
 
 template <typename E>
 int run(const GemmOperand& x, const GemmOperand& weight, bool bf16, const typename E::Params& p,
-        int32_t* gave_up, void* stream)
+        int sm_count, int32_t* gave_up, void* stream)
 {
     GemmShape s{};
     s.splits = s.chains = 1;
     s.gave_up = gave_up;
-    return gemm_run<kCeColumns, E>(x, weight, s, bf16, p, static_cast<cudaStream_t>(stream));
+    return gemm_run<kCeColumns, E>(x, weight, s, bf16, p, sm_count,
+                                   static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
 
-int launch_ce_parts(const CeForward& a, int32_t* gave_up, void* stream)
+int launch_ce_parts(const CeForward& a, int sm_count, int32_t* gave_up, void* stream)
 {
-    return run<PartsEpilogue>(a.x, a.weight, a.bf16, {a.target, a.parts, a.at}, gave_up, stream);
+    return run<PartsEpilogue>(a.x, a.weight, a.bf16, {a.target, a.parts, a.at}, sm_count, gave_up,
+                              stream);
 }
 
 int launch_ce_join(const CeJoin& a, void* stream)
@@ -260,12 +262,12 @@ int launch_ce_rows(const CeRows& a, void* stream)
     return launch_early(k_ce_rows, dim3(1), kRowsThreads, 0, static_cast<cudaStream_t>(stream), a);
 }
 
-int launch_ce_gradient(const CeGradient& a, int32_t* gave_up, void* stream)
+int launch_ce_gradient(const CeGradient& a, int sm_count, int32_t* gave_up, void* stream)
 {
     return run<GradientEpilogue>(a.x, a.weight, a.bf16,
                                  {a.target, a.lse, a.factors, static_cast<uint16_t*>(a.gradient),
                                   a.stride, a.first, a.bf16},
-                                 gave_up, stream);
+                                 sm_count, gave_up, stream);
 }
 
 }  // namespace osr

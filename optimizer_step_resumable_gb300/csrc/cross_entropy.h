@@ -24,7 +24,7 @@ struct CeForward {
     float2* parts;  // parts x rows
     float* at;      // the target's logit, one a row
 };
-int launch_ce_parts(const CeForward& a, int32_t* gave_up, void* stream);
+int launch_ce_parts(const CeForward& a, int sm_count, int32_t* gave_up, void* stream);
 // Second kernel: joins them.
 struct CeJoin {
     const float2* parts;
@@ -67,6 +67,6 @@ struct CeGradient {
     void* gradient;
     int64_t stride;
 };
-int launch_ce_gradient(const CeGradient& a, int32_t* gave_up, void* stream);
+int launch_ce_gradient(const CeGradient& a, int sm_count, int32_t* gave_up, void* stream);
 
 }  // namespace osr

@@ -262,7 +262,7 @@ int linear_cross_entropy_forward(linear_ce_ctx* ctx, const void* d_x, int64_t x_
             osr::CeForward{GemmOperand{d_x, rows, dim, x_stride, false},
                            GemmOperand{d_weight, ctx->vocab, dim, weight_stride, in_out},
                            dtype == ADAMW_DTYPE_BF16, d_target, p.parts, p.at},
-            ctx->base.gave_up, stream);
+            ctx->base.sm_count, ctx->base.gave_up, stream);
     if (e == cudaSuccess)
         e = osr::launch_ce_join(osr::CeJoin{p.parts, int32_t(kCeParts * tiles(ctx->vocab)), p.at,
                                             d_target, rows, ctx->vocab, float(z_loss), d_loss,
@@ -364,7 +364,7 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
             osr::CeGradient{GemmOperand{d_x, rows, dim, x_stride, false},
                             GemmOperand{w, columns, dim, weight_stride, in_out}, bf16, d_target,
                             d_lse, p.factors, int32_t(first), p.gradient, p.piece},
-            ctx->base.gave_up, stream);
+            sms, ctx->base.gave_up, stream);
         const bool last = first + columns == vocab;
         const Plans& plans = last ? p.last : p.plans;
         LinearProduct x{}, dw{};

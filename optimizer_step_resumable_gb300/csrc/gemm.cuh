@@ -16,11 +16,13 @@
 // Sums take two halves of the tensor memory in turn, so that the epilogue of
 // one tile runs beside the products of the next.
 //
-// The grid has a pair of blocks for each item, a tile or a part of one; those
-// that run take over the items of those that have not started, in order, so
-// the long ones come first.  A launch may hold two products (`second`): what a
-// tile of one leaves idle at the end the other fills, and the start of a
-// launch, some 5 us, is paid once.
+// An item is a tile or a part of one.  The items of one product take alike long
+// and are dealt out to as many pairs of blocks as the GPU has room for.  A
+// launch may hold two products: what the one leaves idle at the end the other
+// fills, and the start of a launch, some 5 us, is paid once.  Its grid has a
+// pair of blocks for each item; those that run take over the items of those
+// that have not started, in order, so the longer product comes first.  (One
+// product that way takes longer: asking costs about 1 us a tile.)
 #pragma once
 
 #include <type_traits>
@@ -61,20 +63,32 @@ struct GemmItem {
     int32_t m0, tile_n, split, chain, first, last;  // rows, tile of columns, inner blocks
 };
 
-// The items of a pair, as each of its roles walks through them: the first is
-// the block's own, the others arrive in a ring of answers.
+// The items of a pair, as each of its roles walks through them.  The first is
+// the block's own.  kAsk: the others arrive in a ring of answers; else they are
+// every `gridDim.x / 2`-th.
+template <bool kAsk>
 struct GemmWalk {
     uint32_t answers, full, empty;  // shared memory; `empty` in the first block
-    int32_t item;                   // -1: no more
+    int32_t items, item;            // -1: no more
     uint32_t slot = 0, phase = 0;
 
-    __device__ __forceinline__ GemmWalk(uint32_t answers_, uint32_t full_, uint32_t empty_)
-        : answers(answers_), full(full_), empty(empty_), item(int32_t(blockIdx.x / 2))
+    __device__ __forceinline__ GemmWalk(uint32_t answers_, uint32_t full_, uint32_t empty_,
+                                        int32_t items_)
+        : answers(answers_), full(full_), empty(empty_), items(items_),
+          item(int32_t(blockIdx.x / 2))
     {
+    }
+    __device__ __forceinline__ bool count_on()
+    {
+        item += int32_t(gridDim.x / 2);
+        item = item < items ? item : -1;
+        return true;
     }
     // For one thread.
     __device__ __forceinline__ bool next(volatile int* dead)
     {
+        if constexpr (!kAsk)
+            return count_on();
         if (!barrier_wait(full + 8 * slot, phase, dead))
             return false;
         const int32_t block = next_block(answers + 16 * slot);
@@ -86,6 +100,8 @@ struct GemmWalk {
     // For a warp, whose first lane arrives.
     __device__ __forceinline__ bool next_of_warp(volatile int* dead)
     {
+        if constexpr (!kAsk)
+            return count_on();
         const bool ok = barrier_wait(full + 8 * slot, phase, dead);
         if (!__all_sync(0xFFFFFFFFu, ok))
             return false;
@@ -192,7 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     constexpr bool kTwo = !std::is_void_v<E2>;
     // items of the first product
     const int32_t count = shape.tiles_m * shape.tiles_n * shape.splits;
-    GemmWalk walk(smem_address(answers), next_full, in_block(next_empty, 0));
+    GemmWalk<kTwo> walk(smem_address(answers), next_full, in_block(next_empty, 0), count);
     bool ok = true;
 
     if (warp == 0 && elect_one()) {
@@ -296,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             if (!ok)
                 break;
         }
-    } else if (warp == 3 && rank == 0 && elect_one()) {
+    } else if (kTwo && warp == 3 && rank == 0 && elect_one()) {
         const uint32_t other = in_block(next_full, 1);
         uint32_t slot = 0, phase = 0;
         while (ok) {
@@ -410,9 +426,10 @@ inline int gemm_part(const GemmOperand& a, const GemmOperand& b, GemmShape s, bo
     return rc;
 }
 
-// Launches a pair of blocks for each item of one or two products.
+// Launches the items of one or two products.
 template <int BN, typename E, typename E2>
-inline int gemm_launch(const GemmPart<E>& p, const GemmPart<E2>& q, cudaStream_t stream)
+inline int gemm_launch(const GemmPart<E>& p, const GemmPart<E2>& q, int sm_count,
+                       cudaStream_t stream)
 {
     using R = GemmRing<BN>;
     const int64_t items = int64_t(p.s.tiles_m) * p.s.tiles_n * p.s.splits +
@@ -423,12 +440,13 @@ inline int gemm_launch(const GemmPart<E>& p, const GemmPart<E2>& q, cudaStream_t
         k_gemm<BN, E, E2>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
     if (err != cudaSuccess)
         return int(err);
-    return launch_early(k_gemm<BN, E, E2>, dim3(unsigned(2 * items)), kGemmThreads, R::kSmem,
-                        stream, p.a, p.b, p.s, p.e, q.a, q.b, q.s, q.e);
+    const int64_t most = std::is_void_v<E2> ? sm_count / 2 : items;
+    return launch_early(k_gemm<BN, E, E2>, dim3(unsigned(2 * (items < most ? items : most))),
+                        kGemmThreads, R::kSmem, stream, p.a, p.b, p.s, p.e, q.a, q.b, q.s, q.e);
 }
 template <int BN, typename E>
 inline int gemm_run(const GemmOperand& a, const GemmOperand& b, const GemmShape& s, bool bf16,
-                    const typename E::Params& e, cudaStream_t stream)
+                    const typename E::Params& e, int sm_count, cudaStream_t stream)
 {
     GemmPart<E> p;
     const int rc = gemm_part<BN, E>(a, b, s, bf16, e, &p);
@@ -437,7 +455,7 @@ inline int gemm_run(const GemmOperand& a, const GemmOperand& b, const GemmShape&
     GemmPart<void> none;
     none.a = p.a;
     none.b = p.b;
-    return gemm_launch<BN, E, void>(p, none, stream);
+    return gemm_launch<BN, E, void>(p, none, sm_count, stream);
 }
 
 }  // namespace detail

@@ -297,14 +297,14 @@ int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partia
         const auto run = plan.bn == 32   ? gemm_run<32, SwappedEpilogue>
                          : plan.bn == 64 ? gemm_run<64, SwappedEpilogue>
                                          : gemm_run<128, SwappedEpilogue>;
-        e = run(s.b, s.a, s.s, p.bf16, s.p, static_cast<cudaStream_t>(stream));
+        e = run(s.b, s.a, s.s, p.bf16, s.p, sm_count, static_cast<cudaStream_t>(stream));
     } else if (s.p.o.dtype == ADAMW_DTYPE_F32) {
-        e = linear_store_f32(plan.bn, s, p.bf16, stream);
+        e = linear_store_f32(plan.bn, s, p.bf16, sm_count, stream);
     } else {
         const bool plain = !s.p.o.bias && !s.p.o.z && s.p.o.act == LINEAR_NONE;
         const auto store =
             s.p.o.dtype == ADAMW_DTYPE_BF16 ? linear_store_bf16 : linear_store_f16;
-        e = store(plan.bn, s, plain, p.bf16, stream);
+        e = store(plan.bn, s, plain, p.bf16, sm_count, stream);
     }
     return e == cudaSuccess ? join_product(p, plan, partials, sm_count, stream) : e;
 }

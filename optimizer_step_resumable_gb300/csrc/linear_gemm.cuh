@@ -22,9 +22,11 @@ struct StoreProduct {
 // Tiles of 256 x bn (128, 192 or 256), the product's rows along the long side,
 // for an output of the type; `plain`: neither bias nor activation nor z, which
 // float32 outputs never have.
-int linear_store_f32(int bn, const StoreProduct& p, bool bf16, void* stream);
-int linear_store_bf16(int bn, const StoreProduct& p, bool plain, bool bf16, void* stream);
-int linear_store_f16(int bn, const StoreProduct& p, bool plain, bool bf16, void* stream);
+int linear_store_f32(int bn, const StoreProduct& p, bool bf16, int sm_count, void* stream);
+int linear_store_bf16(int bn, const StoreProduct& p, bool plain, bool bf16, int sm_count,
+                      void* stream);
+int linear_store_f16(int bn, const StoreProduct& p, bool plain, bool bf16, int sm_count,
+                     void* stream);
 // Two plain products in one launch, in tiles of 256 x 256; the types of their
 // outputs, float32 or bf16's 16-bit type.
 int linear_store_two_f32(const StoreProduct& p, const StoreProduct& q, bool bf16, void* stream);
@@ -258,18 +260,19 @@ inline int store_two(const StoreProduct& p, const StoreProduct& q, bool bf16, vo
     int e = gemm_part<256, E>(p.a, p.b, p.s, bf16, p.p, &one);
     if (e == cudaSuccess)
         e = gemm_part<256, E2>(q.a, q.b, q.s, bf16, q.p, &two);
-    return e == cudaSuccess ? gemm_launch<256, E, E2>(one, two, static_cast<cudaStream_t>(stream))
-                            : e;
+    return e == cudaSuccess
+               ? gemm_launch<256, E, E2>(one, two, 0, static_cast<cudaStream_t>(stream))
+               : e;
 }
 template <int kOut, bool kPlain>
-inline int store_one(int bn, const StoreProduct& p, bool bf16, void* stream)
+inline int store_one(int bn, const StoreProduct& p, bool bf16, int sm_count, void* stream)
 {
     using E = StoreEpilogue<kOut, kPlain>;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (bn) {
-    case 128: return gemm_run<128, E>(p.a, p.b, p.s, bf16, p.p, st);
-    case 192: return gemm_run<192, E>(p.a, p.b, p.s, bf16, p.p, st);
-    default: return gemm_run<256, E>(p.a, p.b, p.s, bf16, p.p, st);
+    case 128: return gemm_run<128, E>(p.a, p.b, p.s, bf16, p.p, sm_count, st);
+    case 192: return gemm_run<192, E>(p.a, p.b, p.s, bf16, p.p, sm_count, st);
+    default: return gemm_run<256, E>(p.a, p.b, p.s, bf16, p.p, sm_count, st);
     }
 }
 

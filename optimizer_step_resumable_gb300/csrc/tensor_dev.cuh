@@ -151,9 +151,7 @@ __device__ __forceinline__ int32_t next_block(uint32_t answer)
                  "selp.u32 %0, 1, 0, p;\n\t"
                  "mov.b32 %1, 0;\n\t"
                  "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 "
-                 "{%1, y, z, w}, a;\n\t"
-                 // the next answer comes by the other way into shared memory
-                 "fence.proxy.async.shared::cta;\n\t}"
+                 "{%1, y, z, w}, a;\n\t}"
                  : "=r"(is), "=r"(x)
                  : "r"(answer)
                  : "memory");
