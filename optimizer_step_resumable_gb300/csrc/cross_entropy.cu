@@ -16,20 +16,30 @@ namespace {
 
 using namespace detail;
 
-constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+constexpr float kLn2 = 0.69314718055994531f;
 
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // What exponentials are taken relative to: never -inf, of which the
 // difference to itself is no number.
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
 
+// v[i], bit by bit of i: a chain of comparisons becomes a place in memory, and
+// with it all of v.
+template <int C>
+__device__ __forceinline__ float pick(const float (&v)[C], int32_t i)
+{
+    if constexpr (C == 1) {
+        return v[0];
+    } else {
+        float half[C / 2];
+#pragma unroll
+        for (int j = 0; j < C / 2; ++j)
+            half[j] = i & (C / 2) ? v[j + C / 2] : v[j];
+        return pick(half, i & (C / 2 - 1));
+    }
+}
+
 struct PartsEpilogue {
-    static constexpr int kUnroll = 4;
+    static constexpr int kUnroll = 2;
     struct Params {
         const int64_t* target;
         float2* parts;
@@ -56,25 +66,23 @@ struct PartsEpilogue {
                 if (column + i >= s.n)
                     v[i] = -INFINITY;
         const int64_t off = target - column;
-        if (off >= 0 && off < C && row < s.m) {
-            float at = 0.0f;
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-                at = off == i ? v[i] : at;
-            if (target < s.n)
-                p.at[row] = at;
-        }
+        if (off >= 0 && off < C && row < s.m && target < s.n)
+            p.at[row] = pick(v, int32_t(off));
         float top[4] = {fmaxf(most, v[0]), v[1], v[2], v[3]};
 #pragma unroll
         for (int i = 4; i < C; ++i)
             top[i % 4] = fmaxf(top[i % 4], v[i]);
         const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         const float base = reference(now) * kLog2E;
-        float add[4] = {sum * exp2_fast(fmaf(most, kLog2E, -base)), 0.0f, 0.0f, 0.0f};
+        float2 add[2] = {make_float2(sum * exp2_fast(fmaf(most, kLog2E, -base)), 0.0f),
+                         make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-            add[i % 4] += exp2_fast(fmaf(v[i], kLog2E, -base));
-        sum = (add[0] + add[1]) + (add[2] + add[3]);
+        for (int i = 0; i < C; i += 2)
+            add[i / 2 % 2] = packed::add2(
+                add[i / 2 % 2],
+                exp2_fast(packed::fma2(make_float2(v[i], v[i + 1]), packed::both(kLog2E),
+                                       packed::both(-base))));
+        sum = (add[0].x + add[1].x) + (add[0].y + add[1].y);
         most = now;
     }
     __device__ void end(const Params& p, const GemmShape& s)
@@ -172,6 +180,9 @@ __global__ void __launch_bounds__(kRowsThreads) k_ce_rows(const CeRows a)
         *a.unnorm = __uint_as_float(uint32_t(127 - shift) << 23);
 }
 
+// p factor.x is 2^(l' - lse' + log2 |factor.x|), with factor.x's sign put on
+// the rounded values: no product an element.
+template <bool kBf16>
 struct GradientEpilogue {
     static constexpr int kUnroll = 4;
     struct Params {
@@ -181,24 +192,25 @@ struct GradientEpilogue {
         uint16_t* gradient;
         int64_t stride;
         int32_t first;
-        bool bf16;
     };
     int32_t row;
     bool counts;
     int64_t target;  // in the piece
-    float base;
-    float2 factor;
+    float base, minus;
+    uint32_t sign;
 
     __device__ GradientEpilogue(const Params& p, const GemmShape& s, int32_t r, int32_t, int32_t,
                                 const GemmItem&, int32_t, float*)
-        : row(r), counts(false), target(-1), base(0.0f), factor(make_float2(0.0f, 0.0f))
+        : row(r), counts(false), target(-1), base(0.0f), minus(0.0f), sign(0)
     {
         if (r >= s.m)
             return;
-        factor = p.factors[r];
+        const float2 factor = p.factors[r];
         const int64_t t = p.target[r];
         counts = t >= 0;
-        base = p.lse[r] * kLog2E;
+        base = log2f(fabsf(factor.x)) - p.lse[r] * kLog2E;
+        minus = factor.y;
+        sign = factor.x < 0.0f ? 0x80008000u : 0u;
         target = t - p.first;
     }
     template <int C>
@@ -207,27 +219,34 @@ struct GradientEpilogue {
     {
         if (column >= s.n || row >= s.m)
             return;
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            v[i] = exp2_fast(fmaf(v[i], kLog2E, -base)) * factor.x;
         const int64_t off = target - column;
-        if (off >= 0 && off < C)
+        const bool here = off >= 0 && off < C;
+        uint32_t w[C / 2];
 #pragma unroll
-            for (int i = 0; i < C; ++i)
-                v[i] -= off == i ? factor.y : 0.0f;
+        for (int i = 0; i < C; i += 2) {
+            const float2 e = exp2_fast(packed::fma2(make_float2(v[i], v[i + 1]),
+                                                    packed::both(kLog2E), packed::both(base)));
+            v[i] = e.x, v[i + 1] = e.y;
+            w[i / 2] = narrow32(e.x, e.y, kBf16) ^ sign;
+        }
+        if (here) {
+            // the target's place anew
+            const float e = pick(v, int32_t(off)), at = (sign ? -e : e) - minus;
+            const uint32_t half = narrow16(at, kBf16);
+#pragma unroll
+            for (int i = 0; i < C / 2; ++i) {
+                w[i] = int32_t(off) == 2 * i ? (w[i] & 0xFFFF0000u) | half : w[i];
+                w[i] = int32_t(off) == 2 * i + 1 ? (w[i] & 0xFFFFu) | (half << 16) : w[i];
+            }
+        }
         if (!counts)  // whatever its logits
 #pragma unroll
-            for (int i = 0; i < C; ++i)
-                v[i] = 0.0f;
+            for (int i = 0; i < C / 2; ++i)
+                w[i] = 0;
         uint16_t* const to = p.gradient + row * p.stride + column;
 #pragma unroll
-        for (int i = 0; i < C; i += 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                w[j] = narrow32(v[i + 2 * j], v[i + 2 * j + 1], p.bf16);
-            store32(to + i, w);
-        }
+        for (int i = 0; i < C / 2; i += 8)
+            store32(to + 2 * i, *reinterpret_cast<const uint32_t(*)[8]>(w + i));
     }
     __device__ void end(const Params&, const GemmShape&) {}
 };
@@ -264,10 +283,15 @@ int launch_ce_rows(const CeRows& a, void* stream)
 
 int launch_ce_gradient(const CeGradient& a, int sm_count, int32_t* gave_up, void* stream)
 {
-    return run<GradientEpilogue>(a.x, a.weight, a.bf16,
-                                 {a.target, a.lse, a.factors, static_cast<uint16_t*>(a.gradient),
-                                  a.stride, a.first, a.bf16},
-                                 sm_count, gave_up, stream);
+    const auto launch = [&](auto epilogue) {
+        using E = decltype(epilogue);
+        return run<std::remove_pointer_t<E>>(
+            a.x, a.weight, a.bf16,
+            {a.target, a.lse, a.factors, static_cast<uint16_t*>(a.gradient), a.stride, a.first},
+            sm_count, gave_up, stream);
+    };
+    return a.bf16 ? launch(static_cast<GradientEpilogue<true>*>(nullptr))
+                  : launch(static_cast<GradientEpilogue<false>*>(nullptr));
 }
 
 }  // namespace osr

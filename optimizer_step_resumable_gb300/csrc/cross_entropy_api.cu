@@ -2,6 +2,7 @@
 // vocabulary (linear_cross_entropy_* of include/adamw_ckpt.h).
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <new>
 
 #include <cuda_runtime.h>
@@ -11,11 +12,6 @@
 #include "cross_entropy.h"
 #include "linear.h"
 #include "product_ctx.h"
-
-struct linear_ce_ctx {
-    osr::ProductContext base;
-    int32_t dim = 0, vocab = 0;
-};
 
 namespace {
 
@@ -42,24 +38,7 @@ using osr::vector_of;
 using osr::whole;
 using osr::Workspace;
 
-constexpr int32_t kMaxDim = 1 << 20, kMaxVocab = 1 << 24;
-constexpr int64_t kMaxRows = int64_t(1) << 30;
-// The gradient of a piece's logits takes this many bytes at most (or 256
-// columns).
-constexpr int64_t kPieceBytes = int64_t(256) << 20;
-
-int64_t tiles(int64_t vocab) { return (vocab + kCeColumns - 1) / kCeColumns; }
-
-// Columns of a piece: equal pieces of whole tiles.
-int64_t piece_columns(int64_t rows, int64_t vocab)
-{
-    int64_t most = kPieceBytes / (2 * rows) / kCeColumns;
-    most = most > 1 ? most : 1;
-    const int64_t all = tiles(vocab), pieces = (all + most - 1) / most;
-    return (all + pieces - 1) / pieces * kCeColumns;
-}
-
-struct Needs {
+struct Needs {  // without gaps: compared byte by byte
     bool backward, copy_x, copy_weight, in_out, dx, dweight, grad_in_out;
     bool grad_f32, grad_mixed;  // neither float32 nor the other matrices' type
 };
@@ -68,6 +47,35 @@ struct Plans {
     LinearPlan dx{}, dweight{};
     bool together = false;  // in one launch
 };
+// The pieces that the vocabulary is divided into for the backward pass.
+struct Pieced {
+    int64_t columns = 0;
+    Plans plans, last;  // of the pieces, and of the last, which may be shorter
+};
+
+}  // namespace
+
+struct linear_ce_ctx {
+    osr::ProductContext base;
+    int32_t dim = 0, vocab = 0;
+    // the last backward call's pieces, which take as long to find as some
+    // launches
+    int64_t rows = -1;
+    Needs needs{};
+    Pieced pieced;
+};
+
+namespace {
+
+
+constexpr int32_t kMaxDim = 1 << 20, kMaxVocab = 1 << 24;
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+// The gradient of a piece's logits takes this many bytes at most (or 256
+// columns).
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+
+int64_t tiles(int64_t vocab) { return (vocab + kCeColumns - 1) / kCeColumns; }
+
 Plans make_plans(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Needs& n)
 {
     Plans p;
@@ -86,6 +94,58 @@ Plans make_plans(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Ne
     return p;
 }
 
+// The time of a piece, as far as it depends on the division.
+double piece_us(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Needs& n)
+{
+    const LinearSize logits{rows, columns, c->dim, false, false};
+    const LinearSize dx{rows, c->dim, columns, false, false};
+    const LinearSize dw{n.grad_in_out ? c->dim : columns, n.grad_in_out ? columns : c->dim, rows,
+                        true, false};
+    const int sms = c->base.sm_count;
+    return osr::linear_us(logits, nullptr, sms) +
+           (n.dx && n.dweight && !n.grad_mixed
+                ? osr::linear_us(dx, &dw, sms)
+                : (n.dx ? osr::linear_us(dx, nullptr, sms) : 0.0) +
+                      (n.dweight ? osr::linear_us(dw, nullptr, sms) : 0.0));
+}
+
+// Pieces of whole tiles.  Tiles of products are as good as they fill the pairs
+// of blocks in the end: the number of columns with the least time of all those
+// that kPieceBytes allows, down to half of them (8192 x 768 x 32000 backward:
+// 797 us in two equal pieces of 63 tiles, @@ so).
+Pieced find_pieces(const linear_ce_ctx* c, int64_t rows, const Needs& n)
+{
+    Pieced p;
+    const int64_t all = tiles(c->vocab);
+    int64_t most = kPieceBytes / (2 * rows) / kCeColumns;
+    most = most < 1 ? 1 : most > all ? all : most;
+    double least_us = 0.0;
+    for (int64_t t = most; t >= (most + 1) / 2; --t) {
+        const int64_t columns = t * kCeColumns, rest = (all - 1) / t;
+        const int64_t end = c->vocab - rest * columns;
+        const double us = double(rest) * piece_us(c, rows, columns, n) + piece_us(c, rows, end, n);
+        if (p.columns == 0 || us < least_us) {
+            least_us = us;
+            p.columns = columns;
+        }
+        if (t < most - 64)
+            break;
+    }
+    const int64_t end = c->vocab - (c->vocab - 1) / p.columns * p.columns;
+    p.last = make_plans(c, rows, end, n);
+    p.plans = c->vocab > p.columns ? make_plans(c, rows, p.columns, n) : p.last;
+    return p;
+}
+const Pieced& pieces_of(linear_ce_ctx* c, int64_t rows, const Needs& n)
+{
+    if (rows != c->rows || std::memcmp(&n, &c->needs, sizeof n) != 0) {
+        c->pieced = find_pieces(c, rows, n);
+        c->rows = rows;
+        c->needs = n;
+    }
+    return c->pieced;
+}
+
 struct Parts {
     void* x = nullptr;
     void* weight = nullptr;
@@ -97,13 +157,12 @@ struct Parts {
     float* dx = nullptr;  // the sum over the pieces so far
     float* dx_partials = nullptr;
     float* dweight_partials = nullptr;
-    int64_t piece = 0;
-    Plans plans, last;  // of the pieces, and of the last, which may be shorter
 };
 
 int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
 
-int64_t lay_out(const linear_ce_ctx* c, int64_t rows, const Needs& n, void* memory, Parts* p)
+int64_t lay_out(const linear_ce_ctx* c, int64_t rows, const Needs& n, const Pieced& pieced,
+                void* memory, Parts* p)
 {
     Workspace w(memory);
     if (n.copy_x)
@@ -115,18 +174,14 @@ int64_t lay_out(const linear_ce_ctx* c, int64_t rows, const Needs& n, void* memo
         p->at = static_cast<float*>(w.take(4 * rows));
         return w.bytes();
     }
-    p->piece = piece_columns(rows, c->vocab);
     p->factors = static_cast<float2*>(w.take(8 * rows));
     p->unnorm = static_cast<float*>(w.take(4));
-    p->gradient = w.take(2 * rows * p->piece);
-    const int64_t end = c->vocab - (c->vocab - 1) / p->piece * p->piece;
-    p->last = make_plans(c, rows, end, n);
-    p->plans = c->vocab > p->piece ? make_plans(c, rows, p->piece, n) : p->last;
-    if (n.dx && p->piece < c->vocab)
+    p->gradient = w.take(2 * rows * pieced.columns);
+    if (n.dx && pieced.columns < c->vocab)
         p->dx = static_cast<float*>(w.take(4 * rows * whole(c->dim)));
-    if (const int64_t sums = larger(p->plans.dx.partials, p->last.dx.partials))
+    if (const int64_t sums = larger(pieced.plans.dx.partials, pieced.last.dx.partials))
         p->dx_partials = static_cast<float*>(w.take(4 * sums));
-    if (const int64_t sums = larger(p->plans.dweight.partials, p->last.dweight.partials))
+    if (const int64_t sums = larger(pieced.plans.dweight.partials, pieced.last.dweight.partials))
         p->dweight_partials = static_cast<float*>(w.take(4 * sums));
     return w.bytes();
 }
@@ -206,7 +261,8 @@ int linear_cross_entropy_workspace(linear_ce_ctx* ctx, int64_t rows, int32_t fla
         for (int apart = 0; apart < (back ? 2 : 1); ++apart) {
             n.grad_mixed = apart != 0;
             Parts p;
-            const int64_t b = lay_out(ctx, rows, n, nullptr, &p);
+            const int64_t b = lay_out(ctx, rows, n, back ? find_pieces(ctx, rows, n) : Pieced{},
+                                      nullptr, &p);
             *bytes = *bytes > b ? *bytes : b;
         }
     }
@@ -251,7 +307,7 @@ int linear_cross_entropy_forward(linear_ce_ctx* ctx, const void* d_x, int64_t x_
     n.in_out = in_out;
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
-                                   lay_out(ctx, rows, n, d_workspace, &p))))
+                                   lay_out(ctx, rows, n, Pieced{}, d_workspace, &p))))
         return rc;
     DeviceScope scope(ctx->base.device);
     int e = readable(&d_x, &x_stride, rows, dim, p.x, stream);
@@ -344,9 +400,10 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
     n.grad_in_out = grad_in_out;
     n.grad_f32 = grad_dtype == ADAMW_DTYPE_F32;
     n.grad_mixed = !n.grad_f32 && grad_dtype != dtype;
+    const Pieced& pieced = pieces_of(ctx, rows, n);
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
-                                   lay_out(ctx, rows, n, d_workspace, &p))))
+                                   lay_out(ctx, rows, n, pieced, d_workspace, &p))))
         return rc;
     const bool bf16 = dtype == ADAMW_DTYPE_BF16;
     e = readable(&d_x, &x_stride, rows, dim, p.x, stream);
@@ -356,20 +413,20 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
         e = osr::launch_ce_rows(osr::CeRows{d_target, d_lse, d_dloss, scale, z_loss, rows, vocab,
                                             bf16, p.factors, p.unnorm},
                                 stream);
-    for (int64_t first = 0; first < vocab && e == cudaSuccess; first += p.piece) {
-        const int64_t columns = vocab - first < p.piece ? vocab - first : p.piece;
+    for (int64_t first = 0; first < vocab && e == cudaSuccess; first += pieced.columns) {
+        const int64_t columns = vocab - first < pieced.columns ? vocab - first : pieced.columns;
         const uint16_t* const w =
             static_cast<const uint16_t*>(d_weight) + first * (in_out ? 1 : weight_stride);
         e = osr::launch_ce_gradient(
             osr::CeGradient{GemmOperand{d_x, rows, dim, x_stride, false},
                             GemmOperand{w, columns, dim, weight_stride, in_out}, bf16, d_target,
-                            d_lse, p.factors, int32_t(first), p.gradient, p.piece},
+                            d_lse, p.factors, int32_t(first), p.gradient, pieced.columns},
             sms, ctx->base.gave_up, stream);
         const bool last = first + columns == vocab;
-        const Plans& plans = last ? p.last : p.plans;
+        const Plans& plans = last ? pieced.last : pieced.plans;
         LinearProduct x{}, dw{};
         x.bf16 = dw.bf16 = bf16;
-        x.a = GemmOperand{p.gradient, rows, columns, p.piece, false};
+        x.a = GemmOperand{p.gradient, rows, columns, pieced.columns, false};
         x.b = GemmOperand{w, dim, columns, weight_stride, !in_out};
         // the pieces' sum in float32; the last one leaves with it
         x.to.out = last ? d_dx : p.dx;
@@ -383,7 +440,7 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
         x.to.alpha = 1.0f;
         x.to.alpha_factor = p.unnorm;
         x.to.vectors = last ? on_vectors(d_dx, dx_stride, rows, 2) : 1;
-        const GemmOperand by_vocab{p.gradient, columns, rows, p.piece, true};
+        const GemmOperand by_vocab{p.gradient, columns, rows, pieced.columns, true};
         const GemmOperand by_dim{d_x, dim, rows, x_stride, true};
         dw.a = grad_in_out ? by_dim : by_vocab;
         dw.b = grad_in_out ? by_vocab : by_dim;

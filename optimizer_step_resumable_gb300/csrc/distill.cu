@@ -18,14 +18,8 @@ namespace {
 using namespace detail;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+constexpr float kLn2 = 0.69314718055994531f;
 
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
 
 template <typename T>

@@ -62,6 +62,9 @@ LinearPlan linear_plan(const LinearSize& p, int sm_count);
 // one launch.
 bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, LinearPlan* p_plan,
                      LinearPlan* q_plan);
+// About how many microseconds one or two (q not NULL) products take in whole
+// tiles of 256 x 256.
+double linear_us(const LinearSize& p, const LinearSize* q, int sm_count);
 int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partials, int sm_count,
                    int32_t* gave_up, void* stream);
 // Two plain products (neither bias nor activation nor z) in one launch.

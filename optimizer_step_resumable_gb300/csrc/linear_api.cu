@@ -1,6 +1,7 @@
 // linear_api.cu -- the C ABI entry points of the linear layer (linear_* of
 // include/adamw_ckpt.h).
 #include <cstdint>
+#include <cstring>
 #include <new>
 
 #include <cuda_runtime.h>
@@ -9,11 +10,6 @@
 #include "arrays.h"
 #include "linear.h"
 #include "product_ctx.h"
-
-struct linear_ctx {
-    osr::ProductContext base;
-    int32_t in = 0, out = 0;
-};
 
 namespace {
 
@@ -38,10 +34,7 @@ using osr::vector_of;
 using osr::whole;
 using osr::Workspace;
 
-constexpr int32_t kMaxFeatures = 1 << 24;
-constexpr int64_t kMaxRows = int64_t(1) << 30;
-
-struct Needs {
+struct Needs {  // without gaps: compared byte by byte
     bool backward, copy_x, copy_weight, dz;
     bool in_out;  // the weight, for its copy
     bool dx, dweight, dbias;
@@ -53,6 +46,24 @@ struct Plans {
     bool together = false;  // dx and dweight in one launch
     int32_t strips = 0;
 };
+
+}  // namespace
+
+struct linear_ctx {
+    osr::ProductContext base;
+    int32_t in = 0, out = 0;
+    // the last call's plans, which take as long to make as some launches
+    int64_t rows = -1;
+    Needs needs{};
+    Plans plans;
+};
+
+namespace {
+
+
+constexpr int32_t kMaxFeatures = 1 << 24;
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+
 Plans make_plans(const linear_ctx* c, int64_t rows, const Needs& n)
 {
     Plans p;
@@ -75,6 +86,16 @@ Plans make_plans(const linear_ctx* c, int64_t rows, const Needs& n)
     if (n.dbias)
         p.strips = osr::linear_strips(rows, c->out, sms);
     return p;
+}
+
+const Plans& plans_of(linear_ctx* c, int64_t rows, const Needs& n)
+{
+    if (rows != c->rows || std::memcmp(&n, &c->needs, sizeof n) != 0) {
+        c->plans = make_plans(c, rows, n);
+        c->rows = rows;
+        c->needs = n;
+    }
+    return c->plans;
 }
 
 // Where the parts of a call's workspace lie; NULL where the call needs none.
@@ -235,7 +256,7 @@ int linear_forward(linear_ctx* ctx, const void* d_x, int64_t x_stride, const voi
     n.copy_x = !gemm_readable(d_x, rows > 1 ? x_stride : 0);
     n.copy_weight = !gemm_readable(d_weight, w_rows > 1 ? weight_stride : 0);
     n.in_out = in_out;
-    const Plans plans = make_plans(ctx, rows, n);
+    const Plans& plans = plans_of(ctx, rows, n);
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
                                    lay_out(ctx, rows, n, plans, d_workspace, &p))))
@@ -325,7 +346,7 @@ int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride, const 
     n.dweight = d_dweight && rows;
     n.dbias = d_dbias && rows;
     n.dz = rows && (d_dx || d_dweight) && (act || !gemm_readable(d_dy, rows > 1 ? dy_stride : 0));
-    const Plans plans = rows ? make_plans(ctx, rows, n) : Plans{};
+    const Plans none, &plans = rows ? plans_of(ctx, rows, n) : none;
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
                                    lay_out(ctx, rows, n, plans, d_workspace, &p))))

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include "linear.h"
+#include "packed_dev.cuh"
 
 namespace osr {
 namespace detail {
@@ -116,71 +117,147 @@ __device__ __forceinline__ void store_some(void* p, int64_t i, int32_t dtype, bo
         store_as(p, i + j, dtype, v[j]);
 }
 
-// 1 / (1 + e^-x).  For x below -87 e^-x overflows and the quotient is 0, as
-// the value is to float32's range.
-__device__ __forceinline__ float logistic(float x)
+__device__ __forceinline__ float exp2_fast(float x)
 {
-    return __fdividef(1.0f, 1.0f + __expf(-x));
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 exp2_fast(float2 x)
+{
+    return make_float2(exp2_fast(x.x), exp2_fast(x.y));
+}
+__device__ __forceinline__ float2 inverse_fast(float2 x)
+{
+    float2 y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
+    return y;
+}
+// sign(z) |x|, for x >= 0; and -|z|.
+__device__ __forceinline__ float2 signed_as(float2 x, float2 z)
+{
+    return make_float2(copysignf(x.x, z.x), copysignf(x.y, z.y));
+}
+__device__ __forceinline__ float2 minus_abs(float2 z)
+{
+    return make_float2(-fabsf(z.x), -fabsf(z.y));
+}
+__device__ __forceinline__ float2 at_least(float2 z, float a)
+{
+    return make_float2(fmaxf(z.x, a), fmaxf(z.y, a));
 }
 
-// What gelu and its slope are made of: e = e^(-z^2 / 2) and the normal
-// distribution at z, (1 + erf(z / sqrt 2)) / 2, by formula 7.1.26 of Abramowitz
-// and Stegun's handbook, which is within 1.5e-7 of erf: one power of two and
-// one reciprocal, where erff() takes some 40 instructions, which showed (a
-// tile's 32768 elements have 6000 cycles beside the products of 768 inputs).
-struct Normal {
-    float e, below;
-};
-__device__ __forceinline__ Normal normal(float z)
-{
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-    float p = fmaf(t, 1.061405429f, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float e = __expf(-x * x), h = 0.5f * p * t * e;
-    return Normal{e, z < 0.0f ? h : 1.0f - h};
-}
-
+constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kGeluScale = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
+// Beyond +-kFar every activation here is z or 0 to float32, and every slope 1
+// or 0; what would multiply an infinity by 0 takes z no further.
+constexpr float kFar = 100.0f;
+
+// 1 / (1 + 2^x): 0 where 2^x overflows.
+__device__ __forceinline__ float2 logistic(float2 x)
+{
+    return inverse_fast(packed::add2(exp2_fast(x), packed::both(1.0f)));
+}
+
+// What gelu and its slope are made of, at -|z| >= -kFar: e = e^(-z^2 / 2) and
+// the normal distribution, (1 + erf(z / sqrt 2)) / 2, by formula 7.1.26 of
+// Abramowitz and Stegun's handbook, which is within 1.5e-7 of erf: a power of
+// two and a reciprocal, and products in pairs, where erff() takes some 40
+// instructions an element.  That showed: the 32768 elements of a block's tile
+// have 6000 cycles beside the products of 768 inputs.
+struct Normal {
+    float2 e, tail;
+};
+__device__ __forceinline__ Normal normal(float2 below)
+{
+    using namespace packed;
+    const float2 t = inverse_fast(
+        fma2(below, both(-0.3275911f * 0.70710678118654752f), both(1.0f)));
+    float2 p = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+    p = fma2(p, t, both(0.5f * 1.421413741f));
+    p = fma2(p, t, both(0.5f * -0.284496736f));
+    p = fma2(p, t, both(0.5f * 0.254829592f));
+    const float2 e = exp2_fast(mul2(mul2(below, below), both(-0.5f * kLog2E)));
+    return Normal{e, mul2(mul2(p, t), e)};
+}
 
 template <int kAct>
-__device__ __forceinline__ float activated(float z)
+__device__ __forceinline__ float2 activated(float2 z)
 {
-    if constexpr (kAct == LINEAR_RELU)
-        return z < 0.0f ? 0.0f : z;  // a NaN stays one
-    else if constexpr (kAct == LINEAR_GELU)
-        return z * normal(z).below;
-    else if constexpr (kAct == LINEAR_GELU_TANH)
+    using namespace packed;
+    if constexpr (kAct == LINEAR_RELU) {
+        // a NaN stays one
+        return make_float2(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);
+    } else if constexpr (kAct == LINEAR_GELU) {
+        // max(z, 0) - |z| (1 - distribution at |z|)
+        const float2 below = at_least(minus_abs(z), -kFar);
+        const float2 g = fma2(below, normal(below).tail, at_least(z, 0.0f));
+        return make_float2(z.x != z.x ? z.x : g.x, z.y != z.y ? z.y : g.y);
+    } else if constexpr (kAct == LINEAR_GELU_TANH) {
         // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
-        return z * logistic(2.0f * kGeluScale * (z + kGeluCube * z * z * z));
-    else if constexpr (kAct == LINEAR_SILU)
-        return z * logistic(z);
-    else
+        constexpr float k = -2.0f * kGeluScale * kLog2E;
+        const float2 w = fma2(mul2(z, z), both(k * kGeluCube), both(k));
+        return mul2(z, logistic(mul2(z, w)));
+    } else if constexpr (kAct == LINEAR_SILU) {
+        return mul2(z, logistic(mul2(z, both(-kLog2E))));
+    } else {
         return z;
+    }
 }
 
 // The derivative of activated() at z.
 template <int kAct>
-__device__ __forceinline__ float slope(float z)
+__device__ __forceinline__ float2 slope(float2 z)
 {
+    using namespace packed;
     if constexpr (kAct == LINEAR_RELU)
-        return z > 0.0f ? 1.0f : 0.0f;
-    else if constexpr (kAct == LINEAR_GELU) {
-        const Normal n = normal(z);
-        return fmaf(z * 0.39894228040143268f, n.e, n.below);
+        return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
+    // fminf and fmaxf lose a NaN: it comes back below
+    const float2 near = make_float2(fminf(fmaxf(z.x, -kFar), kFar), fminf(fmaxf(z.y, -kFar), kFar));
+    float2 s;
+    if constexpr (kAct == LINEAR_GELU) {
+        const Normal n = normal(minus_abs(near));
+        const float2 d = signed_as(fma2(n.tail, both(-1.0f), both(0.5f)), near);
+        s = fma2(mul2(near, both(0.39894228040143268f)), n.e, add2(d, both(0.5f)));
     } else if constexpr (kAct == LINEAR_GELU_TANH) {
-        const float g = logistic(2.0f * kGeluScale * (z + kGeluCube * z * z * z));
-        const float t = g * (1.0f - g);  // 0 for large |z|, whose square may overflow
-        return t > 0.0f ? g + z * (2.0f * kGeluScale) * t * (1.0f + 3.0f * kGeluCube * z * z)
-                        : g;
-    } else if constexpr (kAct == LINEAR_SILU) {
-        const float g = logistic(z);
-        return g * (1.0f + z * (1.0f - g));
-    } else
-        return 1.0f;
+        constexpr float k = -2.0f * kGeluScale * kLog2E;
+        const float2 square = mul2(near, near);
+        const float2 g = logistic(mul2(near, fma2(square, both(k * kGeluCube), both(k))));
+        const float2 t = mul2(mul2(near, g), fma2(g, both(-1.0f), both(1.0f)));
+        s = fma2(t, fma2(square, both(6.0f * kGeluScale * kGeluCube), both(2.0f * kGeluScale)), g);
+    } else {
+        const float2 g = logistic(mul2(near, both(-kLog2E)));
+        s = mul2(g, fma2(near, fma2(g, both(-1.0f), both(1.0f)), both(1.0f)));
+    }
+    return make_float2(z.x != z.x ? z.x : s.x, z.y != z.y ? z.y : s.y);
+}
+
+// act, or the products of g with its slopes, of N values.
+template <int kAct, int N>
+__device__ __forceinline__ void activate_all(float (&v)[N])
+{
+    if constexpr (kAct == LINEAR_NONE)
+        return;
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+        const float2 y = activated<kAct>(make_float2(v[i], v[i + 1]));
+        v[i] = y.x, v[i + 1] = y.y;
+    }
+    if constexpr (N % 2)
+        v[N - 1] = activated<kAct>(make_float2(v[N - 1], 0.0f)).x;
+}
+template <int kAct, int N>
+__device__ __forceinline__ void times_slopes(float (&g)[N], const float (&z)[N])
+{
+    static_assert(N % 2 == 0, "");
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 s = packed::mul2(make_float2(g[i], g[i + 1]),
+                                      slope<kAct>(make_float2(z[i], z[i + 1])));
+        g[i] = s.x, g[i + 1] = s.y;
+    }
 }
 
 template <typename F>
@@ -210,9 +287,7 @@ __device__ __forceinline__ void finish_some(const LinearOut& o, int64_t row, int
     }
     if (o.z)
         store_some(o.z, row * o.z_stride + column, o.dtype, whole, v);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        v[i] = activated<kAct>(v[i]);
+    activate_all<kAct>(v);
     if (o.residual) {
         float more[N];
         load_some(o.residual, row * o.residual_stride + column, o.residual_dtype, whole, more);

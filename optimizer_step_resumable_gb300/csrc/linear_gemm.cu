@@ -54,11 +54,7 @@ struct SwappedEpilogue {
                 if (i < count)
                     store_as(o.z, (row + i) * o.z_stride + column, o.dtype, v[i]);
         if (o.act != LINEAR_NONE)
-            with_activation(o.act, [&](auto act) {
-#pragma unroll
-                for (int i = 0; i < C; ++i)
-                    v[i] = activated<decltype(act)::value>(v[i]);
-            });
+            with_activation(o.act, [&](auto act) { activate_all<decltype(act)::value>(v); });
         if (o.residual)
 #pragma unroll
             for (int i = 0; i < C; ++i)
@@ -247,6 +243,18 @@ LinearPlan linear_plan(const LinearSize& p, int sm_count)
     best.swapped = swapped;
     finish_plan(p, &best);
     return best;
+}
+
+double linear_us(const LinearSize& p, const LinearSize* q, int sm_count)
+{
+    const int64_t pairs = sm_count / 2, n = tiles_of(p.rows, p.columns, 256);
+    const double a = double(inner_blocks(p.inner)) * block_us(256);
+    if (!q)
+        return launch_us(256) + busy_us(n, a, 0, a, pairs);
+    const int64_t m = tiles_of(q->rows, q->columns, 256);
+    const double b = double(inner_blocks(q->inner)) * block_us(256);
+    return launch_us(256) +
+           (a >= b ? busy_us(n, a, m, b, pairs) : busy_us(m, b, n, a, pairs));
 }
 
 bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, LinearPlan* p_plan,

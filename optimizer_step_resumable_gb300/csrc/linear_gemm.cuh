@@ -149,9 +149,10 @@ struct StoreEpilogue {
         const LinearOut& o = p.o;
         if (column >= p.columns)
             return;
+        if (alpha != 1.0f)
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            v[i] *= alpha;
+            for (int i = 0; i < 32; ++i)
+                v[i] *= alpha;
         if (vectors && column + 32 <= p.columns) {
             if (!kPlain && bias)
 #pragma unroll
@@ -163,11 +164,7 @@ struct StoreEpilogue {
                 store(static_cast<char*>(o.z) + (int64_t(row) * o.z_stride + column) * kSize<kOut>,
                       v);
             if (!kPlain && o.act != LINEAR_NONE)
-                with_activation(o.act, [&](auto act) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = activated<decltype(act)::value>(v[i]);
-                });
+                with_activation(o.act, [&](auto act) { activate_all<decltype(act)::value>(v); });
             if (add) {
                 if (add_f32) {
 #pragma unroll
@@ -233,11 +230,7 @@ struct StoreEpilogue {
                     z += 8 * z_step;
                 }
                 if (!kPlain && o.act != LINEAR_NONE)
-                    with_activation(o.act, [&](auto act) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            f[i] = activated<decltype(act)::value>(f[i]);
-                    });
+                    with_activation(o.act, [&](auto act) { activate_all<decltype(act)::value>(f); });
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (r + i < left)

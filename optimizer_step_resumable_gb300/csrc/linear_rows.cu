@@ -74,9 +74,7 @@ __global__ void __launch_bounds__(kSlopeThreads) k_linear_slope(const LinearSlop
                 if constexpr (kAct != LINEAR_NONE) {
                     float s[8];
                     widen8(x[k], a.bf16, s);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        f[i] *= slope<kAct>(s[i]);
+                    times_slopes<kAct>(f, s);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
