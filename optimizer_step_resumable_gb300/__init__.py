@@ -954,29 +954,52 @@ def _either_way(t, out: int, cols: int, ctx, name: str):
     raise TypeError(f"{name}: the elements along one dimension must be adjacent")
 
 
-def _work(ctx, rows: int, flags: int, pointers, workspace, stream):
-    """(address, bytes, tensor) of the workspace of a call whose matrices lie at
-    the (address, stride) pairs `pointers`."""
-    for p, s in pointers:
-        if p & 15 or s & 7:
-            flags |= LINEAR_FOR_ANY_ADDRESS
-    need = ctx._bytes.get((rows, flags))
-    if need is None:
-        n = ctypes.c_int64()
-        _check(getattr(library(), ctx._workspace)(ctx.handle, rows, flags, ctypes.byref(n)),
-               ctx._workspace)
-        if len(ctx._bytes) > 256:
-            ctx._bytes.clear()
-        need = ctx._bytes[rows, flags] = n.value
-    if workspace is not None:
-        if workspace.get_device() != ctx.device or not workspace.is_contiguous():
-            raise TypeError("workspace must be a contiguous CUDA tensor of the context's device")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    if not need:
-        return None, 0, None
-    from torch import uint8
-    t = _allocator(ctx, stream)((need,), uint8)
-    return t.data_ptr(), need, t
+_alloc = _free = None  # the caching allocator's own calls
+
+
+class _Scratch:
+    """Workspace of one call: an address and its bytes, on the call's stream.
+    Given back as soon as the call has been made: what the stream does next with
+    the memory comes after it."""
+
+    __slots__ = ("ptr", "bytes", "own")
+
+    def __init__(self, ctx, rows: int, flags: int, workspace, stream: int):
+        global _alloc, _free
+        need = ctx._bytes.get((rows, flags))
+        if need is None:
+            n = ctypes.c_int64()
+            _check(getattr(library(), ctx._workspace)(ctx.handle, rows, flags, ctypes.byref(n)),
+                   ctx._workspace)
+            if len(ctx._bytes) > 256:
+                ctx._bytes.clear()
+            need = ctx._bytes[rows, flags] = n.value
+        self.own = False
+        if workspace is not None:
+            if workspace.get_device() != ctx.device or not workspace.is_contiguous():
+                raise TypeError("workspace must be a contiguous CUDA tensor of the context's device")
+            self.ptr = workspace.data_ptr()
+            self.bytes = workspace.numel() * workspace.element_size()
+        elif not need:
+            self.ptr, self.bytes = None, 0
+        else:
+            import torch
+            if _alloc is None:
+                _alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
+                _free = torch._C._cuda_cudaCachingAllocator_raw_delete
+            self.bytes, self.own = need, True
+            if torch._C._cuda_getDevice() == ctx.device:
+                self.ptr = _alloc(need, stream)  # a tensor would take 3 us to make
+            else:
+                with torch.cuda.device(ctx.device):
+                    self.ptr = _alloc(need, stream)
+
+    def done(self):
+        if self.own:
+            self.own = False
+            _free(self.ptr)
+
+    __del__ = done
 
 
 def linear_workspace(lin: Linear, rows: int, flags: int = 0) -> int:
@@ -1024,10 +1047,13 @@ def linear_forward(lin: Linear, x, weight, bias=None, residual=None, activation:
         rp, rs, _ = _spaced(residual, shape, lin.out, lin, "residual")
     if z is not None:
         zp, zs, _ = _spaced(z, shape, lin.out, lin, "z")
-    mem, size, keep = _work(lin, rows, 0, ((xp, xs), (wp, ws)), workspace, stream)
+    stream = _stream(stream, lin.device)
+    mem = _Scratch(lin, rows, LINEAR_FOR_ANY_ADDRESS if (xp | wp) & 15 or (xs | ws) & 7 else 0,
+                   workspace, stream)
     st = (_lib or library()).linear_forward(
         lin.handle, xp, xs, wp, ws, code, bp, b_code, rp, rs, act, yp, ys, zp, zs, rows,
-        LINEAR_IN_OUT if in_out else 0, mem, size, _stream(stream, lin.device))
+        LINEAR_IN_OUT if in_out else 0, mem.ptr, mem.bytes, stream)
+    mem.done()
     if st != OK:
         _check(st, "linear_forward")
     return y
@@ -1074,12 +1100,14 @@ def linear_backward(lin: Linear, dy, x, weight, z=None, activation: str = "none"
         if dwp is not None and b_code != g_code:
             raise TypeError("dweight and dbias must have one type")
         g_code = b_code
-    mem, size, keep = _work(lin, rows, LINEAR_FOR_BACKWARD, ((xp, xs), (wp, ws), (gp, gs)),
-                            workspace, stream)
+    stream = _stream(stream, lin.device)
+    mem = _Scratch(lin, rows, LINEAR_FOR_BACKWARD | (
+        LINEAR_FOR_ANY_ADDRESS if (xp | wp | gp) & 15 or (xs | ws | gs) & 7 else 0), workspace,
+        stream)
     st = (_lib or library()).linear_backward(
         lin.handle, gp, gs, xp, xs, wp, ws, code, zp, zs, act, dp, ds, dwp, dws, dbp, g_code,
-        rows, flags | (LINEAR_ACCUMULATE if accumulate else 0), mem, size,
-        _stream(stream, lin.device))
+        rows, flags | (LINEAR_ACCUMULATE if accumulate else 0), mem.ptr, mem.bytes, stream)
+    mem.done()
     if st != OK:
         _check(st, "linear_backward")
     return dx, dweight, dbias
@@ -1147,11 +1175,15 @@ def linear_cross_entropy_forward(ce: LinearCrossEntropy, x, weight, target, z_lo
         new = _allocator(ce, stream)
         loss = new(shape[:-1], float32) if loss is None else loss
         lse = new(shape[:-1], float32) if lse is None else lse
-    mem, size, keep = _work(ce, rows, 0, ((xp, xs), (wp, ws)), workspace, stream)
+    target = _targets(target, rows, ce)
+    out = _row_values(loss, rows, "loss", ce), _row_values(lse, rows, "lse", ce)
+    stream = _stream(stream, ce.device)
+    mem = _Scratch(ce, rows, LINEAR_FOR_ANY_ADDRESS if (xp | wp) & 15 or (xs | ws) & 7 else 0,
+                   workspace, stream)
     st = (_lib or library()).linear_cross_entropy_forward(
-        ce.handle, xp, xs, wp, ws, code, _targets(target, rows, ce), z_loss,
-        _row_values(loss, rows, "loss", ce), _row_values(lse, rows, "lse", ce), rows,
-        LINEAR_IN_OUT if in_out else 0, mem, size, _stream(stream, ce.device))
+        ce.handle, xp, xs, wp, ws, code, target, z_loss, *out, rows,
+        LINEAR_IN_OUT if in_out else 0, mem.ptr, mem.bytes, stream)
+    mem.done()
     if st != OK:
         _check(st, "linear_cross_entropy_forward")
     return loss, lse
@@ -1183,13 +1215,16 @@ def linear_cross_entropy_backward(ce: LinearCrossEntropy, x, weight, target, lse
         dwp, dws, turned = _either_way(dweight, ce.out, ce.cols, ce, "dweight")
         g_code = _code(dweight)
         flags |= LINEAR_GRAD_IN_OUT if turned else 0
-    mem, size, keep = _work(ce, rows, LINEAR_FOR_BACKWARD, ((xp, xs), (wp, ws)), workspace, stream)
+    target = _targets(target, rows, ce)
+    given = (_row_values(lse, rows, "lse", ce),
+             None if dloss is None else _row_values(dloss, rows, "dloss", ce))
+    stream = _stream(stream, ce.device)
+    mem = _Scratch(ce, rows, LINEAR_FOR_BACKWARD | (
+        LINEAR_FOR_ANY_ADDRESS if (xp | wp) & 15 or (xs | ws) & 7 else 0), workspace, stream)
     st = (_lib or library()).linear_cross_entropy_backward(
-        ce.handle, xp, xs, wp, ws, code, _targets(target, rows, ce),
-        _row_values(lse, rows, "lse", ce),
-        None if dloss is None else _row_values(dloss, rows, "dloss", ce), scale, z_loss, dp, ds,
-        dwp, dws, g_code, rows, flags | (LINEAR_ACCUMULATE if accumulate else 0), mem, size,
-        _stream(stream, ce.device))
+        ce.handle, xp, xs, wp, ws, code, target, *given, scale, z_loss, dp, ds, dwp, dws, g_code,
+        rows, flags | (LINEAR_ACCUMULATE if accumulate else 0), mem.ptr, mem.bytes, stream)
+    mem.done()
     if st != OK:
         _check(st, "linear_cross_entropy_backward")
     return dx, dweight

@@ -214,13 +214,11 @@ struct GradientEpilogue {
         target = t - p.first;
     }
     template <int C>
-    __device__ __forceinline__ void chunk(const Params& p, const GemmShape& s, int32_t column, int,
-                                          float (&v)[C], float*)
+    __device__ __forceinline__ void chunk(const Params& p, const GemmShape& s, int32_t column, int c,
+                                          float (&v)[C], float* stage)
     {
-        if (column >= s.n || row >= s.m)
-            return;
         const int64_t off = target - column;
-        const bool here = off >= 0 && off < C;
+        const bool here = off >= 0 && off < C && counts;
         uint32_t w[C / 2];
 #pragma unroll
         for (int i = 0; i < C; i += 2) {
@@ -243,10 +241,16 @@ struct GradientEpilogue {
 #pragma unroll
             for (int i = 0; i < C / 2; ++i)
                 w[i] = 0;
-        uint16_t* const to = p.gradient + row * p.stride + column;
+        uint4* const strip = reinterpret_cast<uint4*>(stage);
 #pragma unroll
-        for (int i = 0; i < C / 2; i += 8)
-            store32(to + 2 * i, *reinterpret_cast<const uint32_t(*)[8]>(w + i));
+        for (int i = 0; i < C / 8; ++i)
+            strip_put(strip, (c & 1) * (C / 8) + i,
+                      make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+        if (c & 1) {  // whole tiles fit the rows of the gradient
+            const int32_t first = row - int32_t(threadIdx.x % 32);
+            strip_write(strip, p.gradient + first * p.stride + column - C, p.stride, s.m - first,
+                        2 * C);
+        }
     }
     __device__ void end(const Params&, const GemmShape&) {}
 };

@@ -17,9 +17,15 @@ namespace {
 
 using namespace detail;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+// Small blocks, many of them: what one waits for, others' loads fill (8192 x
+// 32000 bf16 forward in blocks of 512 threads, each row's teacher read by all of
+// them at the end: 154 us, against 80).
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kAtOnce = 4;  // vectors of a thread on their way
 constexpr float kLn2 = 0.69314718055994531f;
 
+// What exponentials are taken relative to: never -inf, of which the
+// difference to itself is no number.
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
 
 template <typename T>
@@ -43,29 +49,56 @@ __device__ __forceinline__ void put(T* p, float x)
     else
         *reinterpret_cast<uint16_t*>(p) = narrow16(x, kBf16<T>);
 }
+// The pairs of a vector.
 template <typename T>
-__device__ __forceinline__ void widen(uint4 q, float (&f)[kE<T>])
-{
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if constexpr (sizeof(T) == 4) {
-            f[i] = __uint_as_float(w[i]);
-        } else {
-            f[2 * i] = widen16(w[i] & 0xFFFFu, kBf16<T>);
-            f[2 * i + 1] =
-                kBf16<T> ? __uint_as_float(w[i] & 0xFFFF0000u) : widen16(w[i] >> 16, false);
-        }
-}
-template <typename T>
-__device__ __forceinline__ uint4 narrow(const float (&f)[kE<T>])
+__device__ __forceinline__ float2 pair_of(const uint32_t (&w)[4], int i)
 {
     if constexpr (sizeof(T) == 4)
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                          __float_as_uint(f[3]));
+        return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else if constexpr (kBf16<T>)
+        return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     else
-        return make_uint4(narrow32(f[0], f[1], kBf16<T>), narrow32(f[2], f[3], kBf16<T>),
-                          narrow32(f[4], f[5], kBf16<T>), narrow32(f[6], f[7], kBf16<T>));
+        return __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+}
+// A vector of -inf.
+template <typename T>
+__device__ __forceinline__ uint4 nothing()
+{
+    const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : kBf16<T> ? 0xFF80FF80u : 0xFC00FC00u;
+    return make_uint4(w, w, w, w);
+}
+// The largest element of `N` vectors; NaN are passed over, as by fmaxf.
+template <typename T, int N>
+__device__ __forceinline__ float largest(const uint4 (&q)[N])
+{
+    if constexpr (sizeof(T) == 4) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            top = fmaxf(fmaxf(top, fmaxf(__uint_as_float(q[i].x), __uint_as_float(q[i].y))),
+                        fmaxf(__uint_as_float(q[i].z), __uint_as_float(q[i].w)));
+        return top;
+    } else {
+        using P = std::conditional_t<kBf16<T>, __nv_bfloat162, __half2>;
+        const auto as = [](const uint32_t& w) { return *reinterpret_cast<const P*>(&w); };
+        P top = as(q[0].x);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            top = __hmax2(__hmax2(top, __hmax2(as(q[i].x), as(q[i].y))),
+                          __hmax2(as(q[i].z), as(q[i].w)));
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&top);
+        return fmaxf(widen16(w & 0xFFFFu, kBf16<T>), widen16(w >> 16, kBf16<T>));
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 narrow(const float2 (&f)[kE<T> / 2])
+{
+    if constexpr (sizeof(T) == 4)
+        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y),
+                          __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+    else
+        return make_uint4(narrow32(f[0].x, f[0].y, kBf16<T>), narrow32(f[1].x, f[1].y, kBf16<T>),
+                          narrow32(f[2].x, f[2].y, kBf16<T>), narrow32(f[3].x, f[3].y, kBf16<T>));
 }
 
 // A row: a head of elements up to a 16-byte boundary, whole vectors, a tail.
@@ -91,8 +124,18 @@ struct Row {
     }
 };
 
-// (maximum, sum of 2^(x - maximum)) over the block, in every thread.
-__device__ float2 join_block(float most, float sum, float2 (&slots)[kWarps])
+// kAtOnce vectors of a row from v on, -inf behind its end.
+template <typename T>
+__device__ __forceinline__ void load_vectors(const uint4* body, int32_t v, int32_t end,
+                                             uint4 (&q)[kAtOnce])
+{
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+        q[i] = v + i * kThreads < end ? __ldcs(body + v + i * kThreads) : nothing<T>();
+}
+
+// (maximum, sum of 2^(x - maximum)) over a warp.
+__device__ __forceinline__ void join_warp(float& most, float& sum)
 {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -102,206 +145,206 @@ __device__ float2 join_block(float most, float sum, float2 (&slots)[kWarps])
         sum = sum * exp2f(most - base) + s * exp2f(m - base);
         most = now;
     }
-    __syncthreads();  // the slots of the call before
-    if (threadIdx.x % 32 == 0)
-        slots[threadIdx.x / 32] = make_float2(most, sum);
-    __syncthreads();
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        top = fmaxf(top, slots[w].x);
-    const float base = reference(top);
-    float total = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        total += slots[w].y * exp2f(slots[w].x - base);
-    return make_float2(top, total);
+}
+__device__ __forceinline__ void join_value(float x, float& most, float& sum)
+{
+    const float now = fmaxf(most, x), base = reference(now);
+    sum = sum * exp2f(most - base) + exp2f(x - base);
+    most = now;
 }
 
-// The teacher's row: ids, values in powers of two, the row's logits there,
-// and whether an id is past the vocabulary.
-struct Teacher {
-    int32_t id[kDistillMost];
-    float q[kDistillMost];
-    float at[kDistillMost];
-    int32_t past;
+// An entry of the teacher's row: its id (-1: none, -2: past the vocabulary) and
+// its value in powers of two, -inf where there is none.
+struct Entry {
+    int32_t id;
+    float v;
 };
-// Whether there is an entry at all; total: their maximum and sum.
-template <typename T>
-__device__ __forceinline__ bool read_teacher(const Distill& a, int64_t row, const T* logits,
-                                             Teacher& t, float2 (&slots)[kWarps], float2& total)
+__device__ __forceinline__ Entry entry_of(const Distill& a, int64_t row, int32_t j, float unit)
 {
-    const float unit = kLog2E / a.temperature;
-    if (threadIdx.x == 0)
-        t.past = 0;
-    __syncthreads();
-    float most = -INFINITY;
-    for (int32_t j = threadIdx.x; j < a.k; j += kThreads) {
-        const int64_t id = a.ids[row * a.k + j];
-        const bool there = id >= 0 && id < a.vocab;
-        if (id >= a.vocab)
-            t.past = 1;
-        const float v = id >= 0 ? load_as(a.values, row * a.k + j, a.values_dtype) * unit
-                                : -INFINITY;
-        t.id[j] = there ? int32_t(id) : -1;
-        t.q[j] = v;
-        t.at[j] = there ? one(logits + id) : 0.0f;
-        most = fmaxf(most, v);
-    }
-    float sum = 0.0f;
-    const float base = reference(most);
-    for (int32_t j = threadIdx.x; j < a.k; j += kThreads)
-        sum += exp2f(t.q[j] - base);
-    total = join_block(most, sum, slots);
-    return total.y != 0.0f;
+    if (j >= a.k)
+        return Entry{-1, -INFINITY};
+    const int64_t id = a.ids[row * a.k + j];
+    const float v = load_as(a.values, row * a.k + j, a.values_dtype) * unit;
+    return Entry{id < 0 ? -1 : id >= a.vocab ? -2 : int32_t(id), id < 0 ? -INFINITY : v};
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) k_distill_forward(const Distill a)
+__global__ void __launch_bounds__(kThreads, 5) k_distill_forward(const Distill a)
 {
-    __shared__ Teacher t;
+    using namespace packed;
     __shared__ float2 slots[kWarps];
-    __shared__ float sums[kWarps];
     wait_before();
     go_ahead();
     const int64_t r = blockIdx.x;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const T* const logits = static_cast<const T*>(a.logits) + r * a.stride;
     const float unit = kLog2E / a.temperature;
-    float most = -INFINITY, sum = 0.0f;  // of l unit
     const Row<T> row(logits, a.vocab);
     const uint4* const body = row.body();
-    constexpr int kAtOnce = 4, kMany = kAtOnce * kE<T>;
+    // the first warp has the teacher's entries, 32 at a time; the first of them
+    // are on their way beside the row
+    Entry first{-1, -INFINITY};
+    if (warp == 0)
+        first = entry_of(a, r, lane, unit);
+    uint4 q[kAtOnce];
+    load_vectors<T>(body, threadIdx.x, row.vectors, q);
+    const float first_at = first.id >= 0 ? one(logits + first.id) : 0.0f;
+    const int32_t edge = row.edge(threadIdx.x);
+    const float edge_value = edge >= 0 ? one(logits + edge) : -INFINITY;
+
+    float most = -INFINITY, sum = 0.0f;  // of l unit
     for (int32_t v = threadIdx.x; v < row.vectors; v += kAtOnce * kThreads) {
-        float f[kMany];
-        uint4 q[kAtOnce] = {};
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i)
-            if (v + i * kThreads < row.vectors)
-                q[i] = __ldcs(body + v + i * kThreads);
+        const float now = fmaxf(most, largest<T>(q) * unit), base = reference(now);
+        float2 add = make_float2(sum * exp2_fast(most - base), 0.0f);
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            float g[kE<T>];
-            widen<T>(q[i], g);
+            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
-            for (int j = 0; j < kE<T>; ++j)
-                f[i * kE<T> + j] = v + i * kThreads < row.vectors ? g[j] : -INFINITY;
+            for (int j = 0; j < kE<T> / 2; ++j)
+                add = add2(add, exp2_fast(fma2(pair_of<T>(w, j), both(unit), both(-base))));
         }
-        float top = f[0];
-#pragma unroll
-        for (int j = 1; j < kMany; ++j)
-            top = fmaxf(top, f[j]);
-        const float now = fmaxf(most, top * unit), base = reference(now);
-        sum *= exp2_fast(most - base);
-        float add[4] = {};
-#pragma unroll
-        for (int j = 0; j < kMany; ++j)
-            add[j % 4] += exp2_fast(fmaf(f[j], unit, -base));
-        sum += (add[0] + add[1]) + (add[2] + add[3]);
+        sum = add.x + add.y;
         most = now;
+        load_vectors<T>(body, v + kAtOnce * kThreads, row.vectors, q);
     }
-    const int32_t edge = row.edge(threadIdx.x);
-    if (edge >= 0) {
-        const float x = one(logits + edge) * unit, now = fmaxf(most, x), base = reference(now);
-        sum = sum * exp2_fast(most - base) + exp2_fast(x - base);
-        most = now;
+    if (edge >= 0)
+        join_value(edge_value * unit, most, sum);
+    join_warp(most, sum);
+    if (lane == 0)
+        slots[warp] = make_float2(most, sum);
+    __syncthreads();
+    if (warp > 0)
+        return;
+    const float2 mine = lane < kWarps ? slots[lane] : make_float2(-INFINITY, 0.0f);
+    most = mine.x;
+    sum = mine.y;
+    join_warp(most, sum);
+    const float lse2 = reference(most) + log2f(sum);
+
+    float top = first.v, total = first.v == -INFINITY ? 0.0f : 1.0f;
+    if (first.v != first.v)  // NaN
+        top = -INFINITY, total = first.v;
+    bool past = first.id == -2;
+    for (int32_t j = 32 + lane; j < a.k; j += 32) {
+        const Entry e = entry_of(a, r, j, unit);
+        past |= e.id == -2;
+        join_value(e.v, top, total);
     }
-    const float2 all = join_block(most, sum, slots);
-    const float lse2 = reference(all.x) + log2f(all.y);
-    float2 total;
-    const bool some = read_teacher(a, r, logits, t, slots, total);
-    const float base = reference(total.x), log_total = log2f(total.y);
+    join_warp(top, total);
+    past = __any_sync(0xFFFFFFFFu, past);
     float loss = 0.0f;
-    if (some)
-        for (int32_t j = threadIdx.x; j < a.k; j += kThreads) {
-            const float log_q = t.q[j] - base - log_total, q = exp2f(log_q);
-            if (q != 0.0f)
-                loss += q * (log_q - (t.at[j] * unit - lse2));
+    if (total != 0.0f) {
+        const float base = reference(top), log_total = log2f(total);
+        for (int32_t j = lane; j < a.k; j += 32) {
+            const Entry e = j == lane ? first : entry_of(a, r, j, unit);
+            const float log_q = e.v - base - log_total, p = exp2f(log_q);
+            if (p != 0.0f && e.id >= 0)
+                loss += p * (log_q - ((j == lane ? first_at : one(logits + e.id)) * unit - lse2));
         }
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         loss += __shfl_xor_sync(0xFFFFFFFFu, loss, off);
-    if (threadIdx.x % 32 == 0)
-        sums[threadIdx.x / 32] = loss;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        loss = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            loss += sums[w];
-        loss *= a.temperature * a.temperature * kLn2;
-        a.loss[r] = t.past ? NAN : loss;
+    if (lane == 0) {
+        a.loss[r] = past ? NAN : loss * (a.temperature * a.temperature * kLn2);
         if (a.lse)
             a.lse[r] = lse2 * kLn2;
     }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) k_distill_backward(const Distill a)
+__global__ void __launch_bounds__(kThreads, 5) k_distill_backward(const Distill a)
 {
-    __shared__ Teacher t;
-    __shared__ float2 slots[kWarps];
+    using namespace packed;
+    __shared__ int32_t ids[kDistillMost];
+    __shared__ float values[kDistillMost], at[kDistillMost];
+    __shared__ float2 teacher;
+    __shared__ bool id_past;
     wait_before();
     go_ahead();
     const int64_t r = blockIdx.x;
+    const int lane = threadIdx.x % 32;
     const T* const logits = static_cast<const T*>(a.logits) + r * a.stride;
     T* const out = static_cast<T*>(a.dlogits) + r * a.dlogits_stride;
     const float unit = kLog2E / a.temperature;
-    float2 total;
-    // before anything is written: out may be the logits
-    const bool some = read_teacher(a, r, logits, t, slots, total);
-    const float factor = a.temperature * a.scale * (a.dloss ? a.dloss[r] : 1.0f);
-    const float base = a.lse_in[r] * kLog2E;
-    const bool past = t.past;
-    const auto gradient = [&](float l) {
-        const float g = exp2_fast(fmaf(l, unit, -base)) * factor;
-        return past ? NAN : some ? g : 0.0f;
-    };
     const Row<T> row(logits, a.vocab);
     const uint4* const body = row.body();
+    uint4 q[kAtOnce];
+    load_vectors<T>(body, threadIdx.x, row.vectors, q);
+    const int32_t edge = row.edge(threadIdx.x);
+    const float edge_value = edge >= 0 ? one(logits + edge) : 0.0f;
+    const float factor = a.temperature * a.scale * (a.dloss ? a.dloss[r] : 1.0f);
+    const float base = a.lse_in[r] * kLog2E;
+    // the first warp reads the teacher's entries, and the logits there before
+    // anything is written: out may be the logits
+    if (threadIdx.x < 32) {
+        float top = -INFINITY, total = 0.0f;
+        bool past = false;
+        for (int32_t j = lane; j < a.k; j += 32) {
+            const Entry e = entry_of(a, r, j, unit);
+            past |= e.id == -2;
+            ids[j] = e.id;
+            values[j] = e.v;
+            at[j] = e.id >= 0 ? one(logits + e.id) : 0.0f;
+            join_value(e.v, top, total);
+        }
+        join_warp(top, total);
+        past = __any_sync(0xFFFFFFFFu, past);
+        if (lane == 0) {
+            teacher = make_float2(reference(top), total);
+            id_past = past;
+        }
+    }
+    __syncthreads();
+    const bool past = id_past, some = teacher.y != 0.0f;
+    // T scale (p): p times factor, or what a row without entries or with a bad
+    // one gets instead
+    const float flat = past ? NAN : 0.0f;
+    const bool is_flat = past || !some;
+    const auto gradient = [&](float2 l) {
+        const float2 g = mul2(exp2_fast(fma2(l, both(unit), both(-base))), both(factor));
+        return is_flat ? both(flat) : g;
+    };
     if ((reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(out)) % 16 == 0) {
         uint4* const to = reinterpret_cast<uint4*>(out + row.head);
-        constexpr int kAtOnce = 4;
         for (int32_t v = threadIdx.x; v < row.vectors; v += kAtOnce * kThreads) {
-            uint4 q[kAtOnce];
+            uint4 next[kAtOnce];
+            load_vectors<T>(body, v + kAtOnce * kThreads, row.vectors, next);
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
+            for (int i = 0; i < kAtOnce; ++i) {
+                const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                float2 f[kE<T> / 2];
+#pragma unroll
+                for (int j = 0; j < kE<T> / 2; ++j)
+                    f[j] = gradient(pair_of<T>(w, j));
                 if (v + i * kThreads < row.vectors)
-                    q[i] = __ldcs(body + v + i * kThreads);
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
-                if (v + i * kThreads < row.vectors) {
-                    float f[kE<T>];
-                    widen<T>(q[i], f);
-#pragma unroll
-                    for (int j = 0; j < kE<T>; ++j)
-                        f[j] = gradient(f[j]);
                     to[v + i * kThreads] = narrow<T>(f);
-                }
+                q[i] = next[i];
+            }
         }
-        const int32_t edge = row.edge(threadIdx.x);
         if (edge >= 0)
-            put(out + edge, gradient(one(logits + edge)));
+            put(out + edge, gradient(make_float2(edge_value, 0.0f)).x);
     } else {
 #pragma unroll 8
         for (int32_t c = threadIdx.x; c < a.vocab; c += kThreads)
-            put(out + c, gradient(one(logits + c)));
+            put(out + c, gradient(make_float2(one(logits + c), 0.0f)).x);
     }
-    if (!some || past)
+    if (is_flat)
         return;
     // the teacher's probabilities, at the k places; an id that is there twice
     // gets the sum both times
-    const float top = reference(total.x), inverse = 1.0f / total.y;
+    const float inverse = 1.0f / teacher.y;
     for (int32_t j = threadIdx.x; j < a.k; j += kThreads)
-        t.q[j] = exp2f(t.q[j] - top) * inverse;
+        values[j] = exp2f(values[j] - teacher.x) * inverse;
     __syncthreads();
     for (int32_t j = threadIdx.x; j < a.k; j += kThreads) {
-        const int32_t id = t.id[j];
+        const int32_t id = ids[j];
         if (id < 0)
             continue;
-        float q = 0.0f;
+        float p = 0.0f;
         for (int32_t i = 0; i < a.k; ++i)
-            q += t.id[i] == id ? t.q[i] : 0.0f;
-        put(out + id, (exp2f(fmaf(t.at[j], unit, -base)) - q) * factor);
+            p += ids[i] == id ? values[i] : 0.0f;
+        put(out + id, (exp2f(fmaf(at[j], unit, -base)) - p) * factor);
     }
 }
 

@@ -63,6 +63,33 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8])
                  : "memory");
 }
 
+// 32 rows of 64 16-bit elements on their way from a warp's lanes, a row each,
+// to memory: through 4 KB of shared memory, so that eight lanes write the 128
+// bytes of a row.  (Each lane writing its own row, 32 bytes at a time, took the
+// cross entropy's gradient @@ us where this takes @@.)  16-byte pieces lie
+// swizzled, at piece XOR row, so that neither way meets a bank twice.
+__device__ __forceinline__ void strip_put(uint4* strip, int piece, uint4 w)
+{
+    const int lane = threadIdx.x % 32;
+    strip[8 * lane + (piece ^ (lane & 7))] = w;
+}
+// `to`: the first row's first element, rows `stride` elements apart, `count` of
+// them and `columns` (a multiple of 8) of each written.
+__device__ __forceinline__ void strip_write(const uint4* strip, uint16_t* to, int64_t stride,
+                                            int32_t count, int32_t columns)
+{
+    const int lane = threadIdx.x % 32, piece = lane % 8;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const int r = i + lane / 8;
+        const uint4 w = strip[8 * r + (piece ^ (r & 7))];
+        if (r < count && 8 * piece < columns)
+            *reinterpret_cast<uint4*>(to + r * stride + 8 * piece) = w;
+    }
+    __syncwarp();
+}
+
 // N elements from place i of p; whole: eight on a vector's boundary.
 template <int N>
 __device__ __forceinline__ void load_some(const void* p, int64_t i, int32_t dtype, bool whole,
