@@ -10,8 +10,9 @@ namespace {
 using namespace detail;
 
 // A block has 256 neighbouring columns of a strip of the rows, a warp every
-// eighth row, a thread eight neighbouring columns.  kAtOnce rows of a thread
-// are on their way at a time.  The eight warps' sums of a column meet in shared
+// eighth row, a thread eight columns: neighbours in one vector, or, where
+// rows do not start on vectors, every 32nd.  kAtOnce rows of a thread are on
+// their way at a time.  The eight warps' sums of a column meet in shared
 // memory.
 constexpr int kSlopeThreads = 256, kSlopeColumns = 256;
 
@@ -24,127 +25,74 @@ __device__ __forceinline__ void widen8(uint4 q, bool bf16, float (&v)[8])
         v[2 * i + 1] = widen16(w[i] >> 16, bf16);
     }
 }
-// A warp's 256 elements of a row from `p` on, eight neighbours a lane, of which
-// there are `count` in all (the rest 0).  The row may start anywhere: the 16-byte
-// pieces of memory that lie within it come as they are, those at its ends
-// element by element, and a lane puts its eight together from two of them.
-struct RowPiece {
-    uint4 here, last;  // last: the one behind the warp's, in lane 31
-};
-__device__ __forceinline__ uint4 piece_of(const uint16_t* p, int32_t from, int32_t count)
+// Eight elements of a row from p; `step` apart, those before `count` of them.
+template <bool kVector>
+__device__ __forceinline__ uint4 load8(const uint16_t* p, int step, int count)
 {
-    if (from >= 0 && from + 8 <= count)
-        return __ldcs(reinterpret_cast<const uint4*>(p + from));
+    if (kVector && count >= 8)
+        return __ldcs(reinterpret_cast<const uint4*>(p));
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        w[i] = from + i >= 0 && from + i < count ? p[from + i] : 0u;
+        w[i] = i < count ? p[i * step] : 0u;
     return make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16),
                       w[6] | (w[7] << 16));
 }
-// Elements from the 16-byte boundary before p to p.
-__device__ __forceinline__ int32_t cut_of(const uint16_t* p)
-{
-    return int32_t(reinterpret_cast<uintptr_t>(p) / 2 % 8);
-}
-__device__ __forceinline__ RowPiece load_piece(const uint16_t* p, int32_t count)
-{
-    const int lane = threadIdx.x % 32;
-    const int32_t cut = cut_of(p);
-    RowPiece r;
-    r.here = piece_of(p, 8 * lane - cut, count);
-    r.last = make_uint4(0, 0, 0, 0);
-    if (lane == 31 && cut)
-        r.last = piece_of(p, 256 - cut, count);
-    return r;
-}
-// Of rows that start on 16-byte boundaries.
-template <typename Piece>
-__device__ __forceinline__ Piece load_as_piece(const uint16_t* p, int32_t count)
-{
-    if constexpr (std::is_same_v<Piece, RowPiece>)
-        return load_piece(p, count);
-    else
-        return piece_of(p, 8 * (threadIdx.x % 32), count);
-}
-__device__ __forceinline__ uint4 join_piece(uint4 r, const uint16_t*) { return r; }
-// For a whole warp, with the p that the piece was loaded from.
-__device__ __forceinline__ uint4 join_piece(const RowPiece& r, const uint16_t* p)
-{
-    const int32_t cut = cut_of(p);
-    if (cut == 0)
-        return r.here;
-    const bool end = threadIdx.x % 32 == 31;
-    uint32_t w[8] = {r.here.x, r.here.y, r.here.z, r.here.w};
-    const uint32_t last[4] = {r.last.x, r.last.y, r.last.z, r.last.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[i], 1);
-        w[4 + i] = end ? last[i] : next;
-    }
-    // whole words, then half of one
-    if (cut & 4)
-#pragma unroll
-        for (int i = 0; i < 6; ++i)
-            w[i] = w[i + 2];
-    if (cut & 2)
-#pragma unroll
-        for (int i = 0; i < 5; ++i)
-            w[i] = w[i + 1];
-    if (cut & 1)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
-// kRagged: rows of dy or z do not start on 16-byte boundaries.
-template <int kAct, bool kRagged>
-__global__ void __launch_bounds__(kSlopeThreads, 2) k_linear_slope(const LinearSlope a)
+template <int kAct, bool kVector>
+__global__ void __launch_bounds__(kSlopeThreads, 4)
+    k_linear_slope(const LinearSlope a)
 {
     __shared__ float sums[8][kSlopeColumns + 8];
     wait_before();
     go_ahead();
-    constexpr int kAtOnce = kRagged ? 2 : 4;
+    constexpr int kAtOnce = kAct == LINEAR_NONE ? 4 : 2;
     const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
-    const int64_t base = int64_t(blockIdx.x) * kSlopeColumns;
-    const int32_t count = int32_t(a.columns - base < kSlopeColumns ? a.columns - base
-                                                                   : kSlopeColumns);
+    const int place = kVector ? 8 * lane : lane, step = kVector ? 1 : 32;
+    const int64_t column = int64_t(blockIdx.x) * kSlopeColumns + place;
+    const int64_t left = a.columns - column;
+    const int count = left <= 0 ? 0 : int(left >= 8 * step ? 8 : (left + step - 1) / step);
     const int64_t first = a.rows * blockIdx.y / a.strips;
     const int64_t last = a.rows * (blockIdx.y + 1) / a.strips;
-    const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + (first + group) * a.dy_stride + base;
-    const uint16_t* z = static_cast<const uint16_t*>(a.z) + (first + group) * a.z_stride + base;
-    uint16_t* dz =
-        static_cast<uint16_t*>(a.dz) + (first + group) * a.stride + base + 8 * lane;
+    const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + (first + group) * a.dy_stride + column;
+    const uint16_t* z = static_cast<const uint16_t*>(a.z) + (first + group) * a.z_stride + column;
+    uint16_t* dz = static_cast<uint16_t*>(a.dz) + (first + group) * a.stride + column;
     float total[8] = {};
-    for (int64_t r = first + group; r < last; r += 8 * kAtOnce) {
-        using Piece = std::conditional_t<kRagged, RowPiece, uint4>;
-        Piece g[kAtOnce], x[kAtOnce];
+    for (int64_t r = first + group; r < last && count > 0; r += 8 * kAtOnce) {
+        uint4 g[kAtOnce], x[kAtOnce];
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k)
             if (r + 8 * k < last) {
-                g[k] = load_as_piece<Piece>(dy + 8 * k * a.dy_stride, count);
+                g[k] = load8<kVector>(dy + 8 * k * a.dy_stride, step, count);
                 if constexpr (kAct != LINEAR_NONE)
-                    x[k] = load_as_piece<Piece>(z + 8 * k * a.z_stride, count);
+                    x[k] = load8<kVector>(z + 8 * k * a.z_stride, step, count);
             }
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k)
             if (r + 8 * k < last) {
                 float f[8];
-                widen8(join_piece(g[k], dy + 8 * k * a.dy_stride), a.bf16, f);
+                widen8(g[k], a.bf16, f);
                 if constexpr (kAct != LINEAR_NONE) {
                     float s[8];
-                    widen8(join_piece(x[k], z + 8 * k * a.z_stride), a.bf16, s);
+                    widen8(x[k], a.bf16, s);
                     times_slopes<kAct>(f, s);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     total[i] += f[i];
-                // rows of whole vectors: the stride is a multiple of eight
-                if (a.dz && 8 * lane < count)
-                    *reinterpret_cast<uint4*>(dz + 8 * k * a.stride) =
-                        make_uint4(narrow32(f[0], f[1], a.bf16), narrow32(f[2], f[3], a.bf16),
-                                   narrow32(f[4], f[5], a.bf16), narrow32(f[6], f[7], a.bf16));
+                if (a.dz) {
+                    uint16_t* const to = dz + 8 * k * a.stride;
+                    if constexpr (kVector) {  // the stride is a multiple of eight
+                        *reinterpret_cast<uint4*>(to) =
+                            make_uint4(narrow32(f[0], f[1], a.bf16), narrow32(f[2], f[3], a.bf16),
+                                       narrow32(f[4], f[5], a.bf16), narrow32(f[6], f[7], a.bf16));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i < count)
+                                to[i * step] = narrow16(f[i], a.bf16);
+                    }
+                }
             }
         dy += 8 * kAtOnce * a.dy_stride;
         z += 8 * kAtOnce * a.z_stride;
@@ -154,14 +102,15 @@ __global__ void __launch_bounds__(kSlopeThreads, 2) k_linear_slope(const LinearS
         return;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        sums[group][8 * lane + i] = total[i];
+        sums[group][place + i * step] = total[i];
     __syncthreads();
-    if (int32_t(threadIdx.x) < count) {
+    const int64_t mine = int64_t(blockIdx.x) * kSlopeColumns + threadIdx.x;
+    if (mine < a.columns) {
         float s = 0.0f;
 #pragma unroll
         for (int g = 0; g < 8; ++g)
             s += sums[g][threadIdx.x];
-        a.partials[blockIdx.y * a.columns + base + threadIdx.x] = s;
+        a.partials[blockIdx.y * a.columns + mine] = s;
     }
 }
 
@@ -193,7 +142,6 @@ __global__ void __launch_bounds__(kBiasThreads)
         store_as(dbias, column, dtype, accumulate ? s + load_as(dbias, column, dtype) : s);
 }
 
-// A warp has 256 columns of every so many rows, four of them on their way.
 constexpr int kCopyThreads = 256;
 __global__ void __launch_bounds__(kCopyThreads)
     k_copy_rows(const uint16_t* from, int64_t from_stride, uint16_t* to, int64_t to_stride,
@@ -201,27 +149,20 @@ __global__ void __launch_bounds__(kCopyThreads)
 {
     wait_before();
     go_ahead();
-    constexpr int kAtOnce = 4;
-    const int lane = threadIdx.x % 32;
-    const int64_t base = int64_t(blockIdx.x) * 256;
-    const int32_t count = int32_t(columns - base < 256 ? columns - base : 256);
-    const int64_t step = int64_t(gridDim.y) * (kCopyThreads / 32);
-    from += base;
-    to += base + 8 * lane;
-    for (int64_t r = int64_t(blockIdx.y) * (kCopyThreads / 32) + threadIdx.x / 32; r < rows;
-         r += kAtOnce * step) {
-        RowPiece w[kAtOnce];
+    const int64_t vectors = (columns + 7) / 8;
+    for (int64_t i = int64_t(blockIdx.x) * kCopyThreads + threadIdx.x; i < rows * vectors;
+         i += int64_t(gridDim.x) * kCopyThreads) {
+        const int64_t r = i / vectors, c = (i - r * vectors) * 8;
+        const uint16_t* const p = from + r * from_stride + c;
+        const int count = int(columns - c < 8 ? columns - c : 8);
+        uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k)
-            if (r + k * step < rows)
-                w[k] = load_piece(from + (r + k * step) * from_stride, count);
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k)
-            if (r + k * step < rows) {
-                const uint4 v = join_piece(w[k], from + (r + k * step) * from_stride);
-                if (8 * lane < count)
-                    *reinterpret_cast<uint4*>(to + (r + k * step) * to_stride) = v;
-            }
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = 2 * j < count ? p[2 * j] : 0u;
+            const uint32_t hi = 2 * j + 1 < count ? p[2 * j + 1] : 0u;
+            w[j] = lo | (hi << 16);
+        }
+        *reinterpret_cast<uint4*>(to + r * to_stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -240,24 +181,26 @@ int linear_strips(int64_t rows, int64_t columns, int sm_count)
 int launch_linear_slope(const LinearSlope& a, void* stream)
 {
     const dim3 grid(unsigned((a.columns + kSlopeColumns - 1) / kSlopeColumns), unsigned(a.strips));
-    const bool ragged =
-        !gemm_readable(a.dy, a.rows > 1 ? a.dy_stride : 0) ||
-        (a.act != LINEAR_NONE && !gemm_readable(a.z, a.rows > 1 ? a.z_stride : 0));
-    const auto launch = [&](void (*even)(LinearSlope), void (*uneven)(LinearSlope)) {
-        return launch_early(ragged ? uneven : even, grid, kSlopeThreads, 0,
+    const auto on_vector = [](const void* p, int64_t stride) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0;
+    };
+    const bool vector = on_vector(a.dy, a.rows > 1 ? a.dy_stride : 0) &&
+                        (a.act == LINEAR_NONE || on_vector(a.z, a.rows > 1 ? a.z_stride : 0));
+    const auto launch = [&](void (*vectors)(LinearSlope), void (*others)(LinearSlope)) {
+        return launch_early(vector ? vectors : others, grid, kSlopeThreads, 0,
                             static_cast<cudaStream_t>(stream), a);
     };
     switch (a.act) {
     case LINEAR_RELU:
-        return launch(k_linear_slope<LINEAR_RELU, false>, k_linear_slope<LINEAR_RELU, true>);
+        return launch(k_linear_slope<LINEAR_RELU, true>, k_linear_slope<LINEAR_RELU, false>);
     case LINEAR_GELU:
-        return launch(k_linear_slope<LINEAR_GELU, false>, k_linear_slope<LINEAR_GELU, true>);
+        return launch(k_linear_slope<LINEAR_GELU, true>, k_linear_slope<LINEAR_GELU, false>);
     case LINEAR_GELU_TANH:
-        return launch(k_linear_slope<LINEAR_GELU_TANH, false>,
-                      k_linear_slope<LINEAR_GELU_TANH, true>);
+        return launch(k_linear_slope<LINEAR_GELU_TANH, true>,
+                      k_linear_slope<LINEAR_GELU_TANH, false>);
     case LINEAR_SILU:
-        return launch(k_linear_slope<LINEAR_SILU, false>, k_linear_slope<LINEAR_SILU, true>);
-    default: return launch(k_linear_slope<LINEAR_NONE, false>, k_linear_slope<LINEAR_NONE, true>);
+        return launch(k_linear_slope<LINEAR_SILU, true>, k_linear_slope<LINEAR_SILU, false>);
+    default: return launch(k_linear_slope<LINEAR_NONE, true>, k_linear_slope<LINEAR_NONE, false>);
     }
 }
 
@@ -272,11 +215,8 @@ int launch_linear_bias_grad(const float* partials, int32_t strips, int64_t colum
 int launch_copy_rows(const void* from, int64_t from_stride, void* to, int64_t to_stride,
                      int64_t rows, int64_t columns, void* stream)
 {
-    const int64_t across = (columns + 255) / 256;
-    int64_t blocks = (rows + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
-    const int64_t most = across < 2048 ? 2048 / across : 1;
-    blocks = blocks < most ? blocks : most;
-    return launch_early(k_copy_rows, dim3(unsigned(across), unsigned(blocks)), kCopyThreads, 0,
+    const int64_t want = (rows * ((columns + 7) / 8) + kCopyThreads - 1) / kCopyThreads;
+    return launch_early(k_copy_rows, dim3(unsigned(want < 4096 ? want : 4096)), kCopyThreads, 0,
                         static_cast<cudaStream_t>(stream), static_cast<const uint16_t*>(from),
                         from_stride, static_cast<uint16_t*>(to), to_stride, rows, columns);
 }
