@@ -12,17 +12,15 @@
 //   2      tensor memory
 //   4..11  epilogue: warp w has the rows 32 (w % 4).. of the block's half of
 //          the tile, and one half of the columns
-//   3      of the pair's first block: asks for the pair's next item
 // Sums take two halves of the tensor memory in turn, so that the epilogue of
 // one tile runs beside the products of the next.
 //
 // An item is a tile or a part of one.  The items of one product take alike long
-// and are dealt out to as many pairs of blocks as the GPU has room for.  A
-// launch may hold two products: what the one leaves idle at the end the other
-// fills, and the start of a launch, some 5 us, is paid once.  Its grid has a
-// pair of blocks for each item; those that run take over the items of those
-// that have not started, in order, so the longer product comes first.  (One
-// product that way takes longer: asking costs about 1 us a tile.)
+// and are dealt out in turn.  A launch may hold two products: what the one
+// leaves idle at the end the other fills, and the start of a launch, some 5 us,
+// is paid once.  The longer items are dealt out first, the others so that all
+// pairs end together (GemmDeal).  (Items handed out by the hardware, by taking
+// over clusters that have not started, cost about 1 us a tile.)
 #pragma once
 
 #include <type_traits>
@@ -55,72 +53,25 @@ struct GemmRing {
     static constexpr int kSmem = kStages * kStage + 1024 + kGemmEpilogueWarps * kWarpStage;
 };
 
-// Items that the warps of a block may be apart: the copies run ahead of the
-// products, and the epilogue behind.
-constexpr int kGemmAnswers = 4;
-
 struct GemmItem {
     int32_t m0, tile_n, split, chain, first, last;  // rows, tile of columns, inner blocks
 };
 
-// The items of a pair, as each of its roles walks through them.  The first is
-// the block's own.  kAsk: the others arrive in a ring of answers; else they are
-// every `gridDim.x / 2`-th.
-template <bool kAsk>
-struct GemmWalk {
-    uint32_t answers, full, empty;  // shared memory; `empty` in the first block
-    int32_t items, item;            // -1: no more
-    uint32_t slot = 0, phase = 0;
-
-    __device__ __forceinline__ GemmWalk(uint32_t answers_, uint32_t full_, uint32_t empty_,
-                                        int32_t items_)
-        : answers(answers_), full(full_), empty(empty_), items(items_),
-          item(int32_t(blockIdx.x / 2))
-    {
-    }
-    __device__ __forceinline__ bool count_on()
-    {
-        item += int32_t(gridDim.x / 2);
-        item = item < items ? item : -1;
-        return true;
-    }
-    // For one thread.
-    __device__ __forceinline__ bool next(volatile int* dead)
-    {
-        if constexpr (!kAsk)
-            return count_on();
-        if (!barrier_wait(full + 8 * slot, phase, dead))
-            return false;
-        const int32_t block = next_block(answers + 16 * slot);
-        barrier_arrive_at(empty + 8 * slot);
-        item = block < 0 ? -1 : block / 2;
-        step();
-        return true;
-    }
-    // For a warp, whose first lane arrives.
-    __device__ __forceinline__ bool next_of_warp(volatile int* dead)
-    {
-        if constexpr (!kAsk)
-            return count_on();
-        const bool ok = barrier_wait(full + 8 * slot, phase, dead);
-        if (!__all_sync(0xFFFFFFFFu, ok))
-            return false;
-        const int32_t block = next_block(answers + 16 * slot);
-        __syncwarp();
-        if (threadIdx.x % 32 == 0)
-            barrier_arrive_at(empty + 8 * slot);
-        item = block < 0 ? -1 : block / 2;
-        step();
-        return true;
-    }
-    __device__ __forceinline__ void step()
-    {
-        if (++slot == kGemmAnswers) {
-            slot = 0;
-            phase ^= 1;
-        }
-    }
-};
+// The i-th item of pair p, or -1; those of the second product follow the
+// first's.
+__device__ __forceinline__ int32_t gemm_dealt(const GemmDeal& d, int32_t p, int32_t i)
+{
+    const int32_t longs = (d.longs - p + d.pairs - 1) / d.pairs;
+    if (i < longs)
+        return p + i * d.pairs;
+    const int32_t j = i - longs;
+    if (j >= (p < d.ahead ? d.after : d.before))
+        return -1;
+    const int32_t k = j < d.after ? j * d.pairs + p
+                                  : d.after * d.pairs + (j - d.after) * (d.pairs - d.ahead) +
+                                        (p - d.ahead);
+    return k < d.shorts ? d.longs + k : -1;
+}
 
 // Items in bands of 8 tiles of rows: the tiles that run at a time form a
 // rectangle, whose rows and columns of A and B stay in L2.
@@ -159,12 +110,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
            const __grid_constant__ GemmShape shape, const __grid_constant__ typename E::Params e,
            const __grid_constant__ CUtensorMap map_a2, const __grid_constant__ CUtensorMap map_b2,
-           const __grid_constant__ GemmShape shape2, const __grid_constant__ typename ParamsOf<E2>::type e2)
+           const __grid_constant__ GemmShape shape2,
+           const __grid_constant__ typename ParamsOf<E2>::type e2, const GemmDeal deal)
 {
     using R = GemmRing<BN>;
     extern __shared__ unsigned char raw[];
-    __shared__ alignas(8) uint64_t bars[2 * R::kStages + 4 + 2 * kGemmAnswers];
-    __shared__ alignas(16) uint4 answers[kGemmAnswers];
+    __shared__ alignas(8) uint64_t bars[2 * R::kStages + 4];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     volatile int* const dead = &gave_up;
@@ -173,7 +124,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const uint32_t ring = (smem_address(raw) + 1023) & ~1023u;
     const uint32_t full = smem_address(bars), empty = full + 8 * R::kStages;
     const uint32_t sums_full = empty + 8 * R::kStages, sums_empty = sums_full + 16;
-    const uint32_t next_full = sums_empty + 16, next_empty = next_full + 8 * kGemmAnswers;
 
     if (threadIdx.x == 0) {
         gave_up = 0;
@@ -184,11 +134,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         for (int i = 0; i < 2; ++i) {
             barrier_init(sums_full + 8 * i, 1);
             barrier_init(sums_empty + 8 * i, 2 * kGemmEpilogueWarps);
-        }
-        for (int i = 0; i < kGemmAnswers; ++i) {
-            barrier_init(next_full + 8 * i, 1);
-            // both blocks' copies and epilogues, the products
-            barrier_init(next_empty + 8 * i, 2 * (1 + kGemmEpilogueWarps) + 1);
         }
         barriers_visible();
         prefetch_map(&map_a);
@@ -207,15 +152,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
     constexpr bool kTwo = !std::is_void_v<E2>;
     // items of the first product
-    const int32_t count = shape.tiles_m * shape.tiles_n * shape.splits;
-    GemmWalk<kTwo> walk(smem_address(answers), next_full, in_block(next_empty, 0), count);
+    const int32_t count = deal.longs, pair = int32_t(blockIdx.x / 2);
+    int32_t turn = 0, item = gemm_dealt(deal, pair, 0);
+    const auto next = [&] { item = gemm_dealt(deal, pair, ++turn); };
     bool ok = true;
 
     if (warp == 0 && elect_one()) {
         uint32_t stage = 0, phase = 0;
         const uint32_t full_first = in_block(full, 0);
-        while (walk.item >= 0) {
-            const bool second = kTwo && walk.item >= count;
+        while (item >= 0) {
+            const bool second = kTwo && item >= count;
             const GemmShape& s = second ? shape2 : shape;
             const CUtensorMap* const a = second ? &map_a2 : &map_a;
             const CUtensorMap* const b = second ? &map_b2 : &map_b;
@@ -223,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const uint32_t bytes =
                 2 * (R::kBytesA + (s.b_across ? R::kBytesB : R::kRowsB * kGemmInner * 2));
             for (int32_t chain = 0; chain < s.chains && ok; ++chain) {
-                const GemmItem it = gemm_item(s, second ? walk.item - count : walk.item, chain);
+                const GemmItem it = gemm_item(s, second ? item - count : item, chain);
                 const int32_t row_a = it.m0 + 128 * int32_t(rank);
                 const int32_t row_b = it.tile_n * BN + R::kRowsB * int32_t(rank);
                 for (int32_t k = it.first; k < it.last; ++k) {
@@ -254,9 +200,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     }
                 }
             }
-            ok = ok && walk.next(dead);
             if (!ok)
                 break;
+            next();
         }
         // the pair's products still read what this block's last tiles hold, and
         // say so at its barriers: the block outlives that
@@ -275,12 +221,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     } else if (warp == 1 && rank == 0 && elect_one()) {
         uint32_t stage = 0, phase = 0;
         int32_t n = 0;
-        while (walk.item >= 0) {
-            const bool second = kTwo && walk.item >= count;
+        while (item >= 0) {
+            const bool second = kTwo && item >= count;
             const GemmShape& s = second ? shape2 : shape;
             const uint32_t step_a = s.a_across ? 2048 : 32, step_b = s.b_across ? 2048 : 32;
             for (int32_t chain = 0; chain < s.chains && ok; ++chain, ++n) {
-                const GemmItem it = gemm_item(s, second ? walk.item - count : walk.item, chain);
+                const GemmItem it = gemm_item(s, second ? item - count : item, chain);
                 const int32_t slot = n & 1;
                 ok = barrier_wait(sums_empty + 8 * slot, ((n >> 1) & 1) ^ 1, dead);
                 if (!ok)
@@ -308,27 +254,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 if (ok)
                     commit_pair(sums_full + 8 * slot);
             }
-            ok = ok && walk.next(dead);
             if (!ok)
                 break;
-        }
-    } else if (kTwo && warp == 3 && rank == 0 && elect_one()) {
-        const uint32_t other = in_block(next_full, 1);
-        uint32_t slot = 0, phase = 0;
-        while (ok) {
-            ok = barrier_wait(next_empty + 8 * slot, phase ^ 1, dead);
-            if (!ok)
-                break;
-            barrier_expect(next_full + 8 * slot, 16);
-            barrier_expect_at(other + 8 * slot, 16);
-            ask_next(walk.answers + 16 * slot, next_full + 8 * slot);
-            ok = barrier_wait(next_full + 8 * slot, phase, dead);
-            if (ok && next_block(walk.answers + 16 * slot) < 0)
-                break;
-            if (++slot == kGemmAnswers) {
-                slot = 0;
-                phase ^= 1;
-            }
+            next();
         }
     } else if (warp >= 4) {
         constexpr int kHalf = BN / 2, kChunk = kHalf < 32 ? kHalf : 32;
@@ -338,10 +266,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             raw + (ring - smem_address(raw)) + R::kStages * R::kStage + (warp - 4) * R::kWarpStage);
         int32_t n = 0;
         // One tile by the epilogue F; false if a wait ran out.
-        const auto tile = [&](auto* kind, const GemmShape& s, const auto& params, int32_t item,
+        const auto tile = [&](auto* kind, const GemmShape& s, const auto& params, int32_t which,
                               int32_t chain) {
             using F = std::remove_pointer_t<decltype(kind)>;
-            const GemmItem it = gemm_item(s, item, chain);
+            const GemmItem it = gemm_item(s, which, chain);
             const int32_t slot = n & 1;
             const int32_t row = it.m0 + 128 * int32_t(rank) + 32 * int32_t(quarter) +
                                 int32_t(threadIdx.x % 32);
@@ -373,18 +301,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             ++n;
             return true;
         };
-        while (walk.item >= 0) {
-            if (!kTwo || walk.item < count) {
+        while (item >= 0) {
+            if (!kTwo || item < count) {
                 for (int32_t chain = 0; chain < shape.chains && ok; ++chain)
-                    ok = tile(static_cast<E*>(nullptr), shape, e, walk.item, chain);
+                    ok = tile(static_cast<E*>(nullptr), shape, e, item, chain);
             }
             if constexpr (kTwo)
-                if (walk.item >= count)
+                if (item >= count)
                     for (int32_t chain = 0; chain < shape2.chains && ok; ++chain)
-                        ok = tile(static_cast<E2*>(nullptr), shape2, e2, walk.item - count, chain);
-            ok = ok && walk.next_of_warp(dead);
+                        ok = tile(static_cast<E2*>(nullptr), shape2, e2, item - count, chain);
             if (!ok)
                 break;
+            next();
         }
     }
     __syncwarp();
@@ -426,23 +354,22 @@ inline int gemm_part(const GemmOperand& a, const GemmOperand& b, GemmShape s, bo
     return rc;
 }
 
-// Launches the items of one or two products.
+inline int64_t gemm_items(const GemmShape& s)
+{
+    return int64_t(s.tiles_m) * s.tiles_n * s.splits;
+}
+// Launches the items of one or two products; deal: as gemm_deal makes it.
 template <int BN, typename E, typename E2>
-inline int gemm_launch(const GemmPart<E>& p, const GemmPart<E2>& q, int sm_count,
+inline int gemm_launch(const GemmPart<E>& p, const GemmPart<E2>& q, const GemmDeal& deal,
                        cudaStream_t stream)
 {
     using R = GemmRing<BN>;
-    const int64_t items = int64_t(p.s.tiles_m) * p.s.tiles_n * p.s.splits +
-                          int64_t(q.s.tiles_m) * q.s.tiles_n * q.s.splits;
-    if (items >= int64_t(1) << 30)
-        return int(cudaErrorInvalidValue);
     const cudaError_t err = cudaFuncSetAttribute(
         k_gemm<BN, E, E2>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
     if (err != cudaSuccess)
         return int(err);
-    const int64_t most = std::is_void_v<E2> ? sm_count / 2 : items;
-    return launch_early(k_gemm<BN, E, E2>, dim3(unsigned(2 * (items < most ? items : most))),
-                        kGemmThreads, R::kSmem, stream, p.a, p.b, p.s, p.e, q.a, q.b, q.s, q.e);
+    return launch_early(k_gemm<BN, E, E2>, dim3(unsigned(2 * deal.pairs)), kGemmThreads, R::kSmem,
+                        stream, p.a, p.b, p.s, p.e, q.a, q.b, q.s, q.e, deal);
 }
 template <int BN, typename E>
 inline int gemm_run(const GemmOperand& a, const GemmOperand& b, const GemmShape& s, bool bf16,
@@ -455,7 +382,11 @@ inline int gemm_run(const GemmOperand& a, const GemmOperand& b, const GemmShape&
     GemmPart<void> none;
     none.a = p.a;
     none.b = p.b;
-    return gemm_launch<BN, E, void>(p, none, sm_count, stream);
+    const int64_t items = gemm_items(p.s);
+    if (items >= int64_t(1) << 30)
+        return int(cudaErrorInvalidValue);
+    const int pairs = int(items < sm_count / 2 ? items : sm_count / 2);
+    return gemm_launch<BN, E, void>(p, none, GemmDeal{pairs, int32_t(items), 0, 0, 0, 0}, stream);
 }
 
 }  // namespace detail

@@ -34,6 +34,14 @@ struct GemmShape {
     int32_t* gave_up;  // set to 1 if a wait ran out (host memory)
 };
 
+// How the items of two products are dealt out to the pairs of blocks, the long
+// items first: pair p gets every `pairs`-th of the `longs`, then, of the
+// `shorts`, `after` if it has one long more than others (p < ahead), else
+// `before`.
+struct GemmDeal {
+    int32_t pairs, longs, ahead, shorts, after, before;
+};
+
 constexpr int kGemmTileM = 256, kGemmInner = 64;
 
 // Whether the tiled copies can read a matrix: its address and row distance on

@@ -158,27 +158,51 @@ void finish_plan(const LinearSize& p, LinearPlan* plan)
         plan->splits > 1 ? plan->splits * p.rows * ((p.columns + 7) / 8 * 8) : 0;
 }
 
-// The time until `n` long items and `m` short ones, taken in this order by
-// whichever pair is free, are done.
-double busy_us(int64_t n, double long_us, int64_t m, double short_us, int64_t pairs)
+// Deals `n` long items and `m` short ones out to the pairs; the time until all
+// are done.
+double deal_out(int64_t n, double long_us, int64_t m, double short_us, int64_t pairs,
+                GemmDeal* deal)
 {
     const int64_t rounds = n / pairs, ahead = n - rounds * pairs;
-    const double low = double(rounds) * long_us, high = ahead ? low + long_us : low;
-    if (m == 0)
-        return high;
-    // the short ones fill the pairs up to t, each pair at most one beyond
-    const double total = double(n) * long_us + double(m) * short_us;
-    double t = total / double(pairs);
-    t = t > low ? t : low;
-    for (int i = 0; i < 64; ++i) {
-        const int64_t fit =
-            int64_t((t - low) / short_us + 1e-9) * (pairs - ahead) +
-            (t > high ? int64_t((t - high) / short_us + 1e-9) * ahead : 0);
-        if (fit >= m)
-            break;
-        t += short_us / 8;
+    const double low = double(rounds) * long_us, high = low + long_us;
+    int64_t after = 0, before = 0;
+    double best = ahead ? high : low;
+    if (m > 0) {
+        // `before` goes up until all short ones are dealt out; a pair that is
+        // ahead takes as many as end no later, or, where that is enough, one more
+        const double even = (double(n) * long_us + double(m) * short_us) / double(pairs);
+        int64_t b = int64_t((even - low) / short_us) - 2;
+        best = 0.0;
+        for (b = b > 0 ? b : 0;; ++b) {
+            const double end = low + double(b) * short_us;
+            if (best != 0.0 && best <= end)
+                break;
+            int64_t a = end > high ? int64_t((end - high) / short_us + 1e-9) : 0;
+            const bool enough = a * ahead + b * (pairs - ahead) >= m;
+            if (!enough)
+                a = a < b ? a + 1 : b;
+            if (a * ahead + b * (pairs - ahead) < m)
+                continue;
+            const double over = ahead ? high + double(a) * short_us : 0.0;
+            const double us = over > end ? over : end;
+            if (best == 0.0 || us < best) {
+                best = us;
+                after = a;
+                before = b;
+            }
+            if (enough)
+                break;
+        }
     }
-    return t > high ? t : high;
+    if (deal)
+        *deal = GemmDeal{int32_t(pairs), int32_t(n), int32_t(ahead), int32_t(m), int32_t(after),
+                         int32_t(before)};
+    return best;
+}
+// Of a tile of 256 x 256, with what its start and end hold up.
+double item_us(int64_t blocks, int64_t splits)
+{
+    return double((blocks + splits - 1) / splits) * block_us(256) + 0.3;
 }
 
 StoreProduct store_product(const LinearProduct& p, const LinearPlan& plan, float* partials,
@@ -248,13 +272,13 @@ LinearPlan linear_plan(const LinearSize& p, int sm_count)
 double linear_us(const LinearSize& p, const LinearSize* q, int sm_count)
 {
     const int64_t pairs = sm_count / 2, n = tiles_of(p.rows, p.columns, 256);
-    const double a = double(inner_blocks(p.inner)) * block_us(256);
+    const double a = item_us(inner_blocks(p.inner), 1);
     if (!q)
-        return launch_us(256) + busy_us(n, a, 0, a, pairs);
+        return launch_us(256) + deal_out(n, a, 0, a, pairs, nullptr);
     const int64_t m = tiles_of(q->rows, q->columns, 256);
-    const double b = double(inner_blocks(q->inner)) * block_us(256);
-    return launch_us(256) +
-           (a >= b ? busy_us(n, a, m, b, pairs) : busy_us(m, b, n, a, pairs));
+    const double b = item_us(inner_blocks(q->inner), 1);
+    return launch_us(256) + (a >= b ? deal_out(n, a, m, b, pairs, nullptr)
+                                    : deal_out(m, b, n, a, pairs, nullptr));
 }
 
 bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, LinearPlan* p_plan,
@@ -277,10 +301,10 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
         for (const int t : kSplits) {
             if (t > 1 && (t > (blocks[1] + 3) / 4 || tiles[1] * (t - 1) >= 4 * pairs))
                 break;
-            const double a = double((blocks[0] + s - 1) / s) * block_us(256);
-            const double b = double((blocks[1] + t - 1) / t) * block_us(256);
+            const double a = item_us(blocks[0], s), b = item_us(blocks[1], t);
             const int64_t n = tiles[0] * s, m = tiles[1] * t;
-            const double us = (a >= b ? busy_us(n, a, m, b, pairs) : busy_us(m, b, n, a, pairs)) +
+            const double us = (a >= b ? deal_out(n, a, m, b, pairs, nullptr)
+                                      : deal_out(m, b, n, a, pairs, nullptr)) +
                               join_us(sizes[0], s) + join_us(sizes[1], t);
             if (least_us == 0.0 || us < least_us) {
                 least_us = us;
@@ -324,14 +348,26 @@ int linear_product_two(const LinearProduct& p, const LinearPlan& p_plan, float* 
     const StoreProduct a = store_product(p, p_plan, p_partials, gave_up);
     const StoreProduct b = store_product(q, q_plan, q_partials, gave_up);
     // the longer items first
-    const bool turned = inner_blocks(q.a.inner) / q_plan.splits >
-                        inner_blocks(p.a.inner) / p_plan.splits;
+    const double a_us = item_us(inner_blocks(p.a.inner), p_plan.splits);
+    const double b_us = item_us(inner_blocks(q.a.inner), q_plan.splits);
+    const int64_t a_items = tiles_of(p.a.outer, p.b.outer, 256) * p_plan.splits;
+    const int64_t b_items = tiles_of(q.a.outer, q.b.outer, 256) * q_plan.splits;
+    const int64_t items = a_items + b_items, most = sm_count / 2;
+    if (items >= int64_t(1) << 30)
+        return int(cudaErrorInvalidValue);
+    const int64_t pairs = items < most ? items : most;
+    const bool turned = b_us > a_us;
     const StoreProduct &first = turned ? b : a, &second = turned ? a : b;
+    GemmDeal deal;
+    if (turned)
+        deal_out(b_items, b_us, a_items, a_us, pairs, &deal);
+    else
+        deal_out(a_items, a_us, b_items, b_us, pairs, &deal);
     int e;
     switch (first.p.o.dtype) {
-    case ADAMW_DTYPE_F32: e = linear_store_two_f32(first, second, p.bf16, stream); break;
-    case ADAMW_DTYPE_BF16: e = linear_store_two_bf16(first, second, stream); break;
-    default: e = linear_store_two_f16(first, second, stream);
+    case ADAMW_DTYPE_F32: e = linear_store_two_f32(first, second, p.bf16, deal, stream); break;
+    case ADAMW_DTYPE_BF16: e = linear_store_two_bf16(first, second, deal, stream); break;
+    default: e = linear_store_two_f16(first, second, deal, stream);
     }
     if (e == cudaSuccess)
         e = join_product(p, p_plan, p_partials, sm_count, stream);

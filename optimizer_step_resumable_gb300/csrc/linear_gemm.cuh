@@ -29,9 +29,12 @@ int linear_store_f16(int bn, const StoreProduct& p, bool plain, bool bf16, int s
                      void* stream);
 // Two plain products in one launch, in tiles of 256 x 256; the types of their
 // outputs, float32 or bf16's 16-bit type.
-int linear_store_two_f32(const StoreProduct& p, const StoreProduct& q, bool bf16, void* stream);
-int linear_store_two_bf16(const StoreProduct& p, const StoreProduct& q, void* stream);
-int linear_store_two_f16(const StoreProduct& p, const StoreProduct& q, void* stream);
+int linear_store_two_f32(const StoreProduct& p, const StoreProduct& q, bool bf16,
+                         const GemmDeal& deal, void* stream);
+int linear_store_two_bf16(const StoreProduct& p, const StoreProduct& q, const GemmDeal& deal,
+                          void* stream);
+int linear_store_two_f16(const StoreProduct& p, const StoreProduct& q, const GemmDeal& deal,
+                         void* stream);
 
 namespace detail {
 
@@ -244,7 +247,8 @@ struct StoreEpilogue {
 };
 
 template <int kOut, int kOut2>
-inline int store_two(const StoreProduct& p, const StoreProduct& q, bool bf16, void* stream)
+inline int store_two(const StoreProduct& p, const StoreProduct& q, bool bf16,
+                     const GemmDeal& deal, void* stream)
 {
     using E = StoreEpilogue<kOut, true>;
     using E2 = StoreEpilogue<kOut2, true>;
@@ -254,7 +258,7 @@ inline int store_two(const StoreProduct& p, const StoreProduct& q, bool bf16, vo
     if (e == cudaSuccess)
         e = gemm_part<256, E2>(q.a, q.b, q.s, bf16, q.p, &two);
     return e == cudaSuccess
-               ? gemm_launch<256, E, E2>(one, two, 0, static_cast<cudaStream_t>(stream))
+               ? gemm_launch<256, E, E2>(one, two, deal, static_cast<cudaStream_t>(stream))
                : e;
 }
 template <int kOut, bool kPlain>

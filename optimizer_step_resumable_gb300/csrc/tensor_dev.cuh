@@ -62,13 +62,6 @@ __device__ __forceinline__ void barrier_arrive_at(uint32_t bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void barrier_expect_at(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
-                     bar),
-                 "r"(bytes)
-                 : "memory");
-}
 __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity)
 {
     uint32_t done;
@@ -129,33 +122,6 @@ __device__ __forceinline__ void load_tile(uint32_t to, const CUtensorMap* map, i
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-
-// ---- the next cluster of the grid ------------------------------------------
-// Asks for a cluster that has not started yet, to do its work here instead;
-// the answer, 16 bytes, arrives at `to` in both blocks and counts at `bar`.
-__device__ __forceinline__ void ask_next(uint32_t to, uint32_t bar)
-{
-    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
-                 ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(to),
-                 "r"(bar)
-                 : "memory");
-}
-// The first block of that cluster, or -1 if none was left.
-__device__ __forceinline__ int32_t next_block(uint32_t answer)
-{
-    uint32_t is, x;
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 y, z, w;\n\t"
-                 "ld.shared.b128 a, [%2];\n\t"
-                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t"
-                 "mov.b32 %1, 0;\n\t"
-                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 "
-                 "{%1, y, z, w}, a;\n\t}"
-                 : "=r"(is), "=r"(x)
-                 : "r"(answer)
-                 : "memory");
-    return is ? int32_t(x) : -1;
 }
 
 // ---- tcgen05 --------------------------------------------------------------
