@@ -134,27 +134,33 @@ __global__ void __launch_bounds__(kJoinThreads) k_ce_join(const CeJoin a)
                                  : lse - a.at[row] + a.z_loss * lse * lse;
 }
 
-// One block: the largest factor, then the rows' factors.
-constexpr int kRowsThreads = 1024;
-__global__ void __launch_bounds__(kRowsThreads) k_ce_rows(const CeRows a)
+// What the gradient of a row's logits is made of: scale (1 + 2 z lse) and scale.
+__device__ __forceinline__ float2 factors(const CeFactors& f, int64_t row, int64_t target,
+                                          float lse)
+{
+    if (target < 0)
+        return make_float2(0.0f, 0.0f);
+    if (target >= f.vocab)
+        return make_float2(NAN, NAN);
+    const float g = f.scale * (f.dloss ? f.dloss[row] : 1.0f);
+    return make_float2(g * fmaf(f.two_z, lse, 1.0f), g);
+}
+
+// One block: the power of two that brings the rows' largest factor to [2^14,
+// 2^15), and its inverse.  The gradient of a logit is at most twice that;
+// binary16 ends at 65504 and loses bits below 2^-14.
+constexpr int kCeNormThreads = 1024;
+__global__ void __launch_bounds__(kCeNormThreads) k_ce_norm(const CeFactors f, int64_t rows,
+                                                          float* norms)
 {
     __shared__ float largest[32];
     wait_before();
     go_ahead();
-    const float scale = float(a.scale), z2 = float(2.0 * a.z_loss);
-    const auto factors = [&](int64_t r) {
-        const int64_t t = a.target[r];
-        if (t < 0)
-            return make_float2(0.0f, 0.0f);
-        if (t >= a.vocab)
-            return make_float2(NAN, NAN);
-        const float g = scale * (a.dloss ? a.dloss[r] : 1.0f);
-        return make_float2(g * fmaf(z2, a.lse[r], 1.0f), g);
-    };
     float most = 0.0f;
-    for (int64_t r = threadIdx.x; r < a.rows; r += kRowsThreads) {
-        const float2 f = factors(r);
-        most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+#pragma unroll 4
+    for (int64_t r = threadIdx.x; r < rows; r += kCeNormThreads) {
+        const float2 g = factors(f, r, f.target[r], f.lse[r]);
+        most = fmaxf(most, fmaxf(fabsf(g.x), fabsf(g.y)));
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
@@ -162,22 +168,16 @@ __global__ void __launch_bounds__(kRowsThreads) k_ce_rows(const CeRows a)
     if (threadIdx.x % 32 == 0)
         largest[threadIdx.x / 32] = most;
     __syncthreads();
+    if (threadIdx.x > 0)
+        return;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         most = fmaxf(most, largest[i]);
-    // The gradient of a logit is at most twice the largest factor.  binary16
-    // ends at 65504 and loses bits below 2^-14, so the largest goes to
-    // [2^14, 2^15); bfloat16 has float32's range.
     int shift = 0;
-    if (!a.bf16 && most > 0.0f && most < INFINITY)
+    if (most > 0.0f && most < INFINITY)
         shift = min(max(14 - (int(__float_as_uint(most) >> 23) - 127), -100), 100);
-    const float norm = __uint_as_float(uint32_t(127 + shift) << 23);
-    for (int64_t r = threadIdx.x; r < a.rows; r += kRowsThreads) {
-        const float2 f = factors(r);
-        a.factors[r] = make_float2(f.x * norm, f.y * norm);
-    }
-    if (threadIdx.x == 0)
-        *a.unnorm = __uint_as_float(uint32_t(127 - shift) << 23);
+    norms[0] = __uint_as_float(uint32_t(127 + shift) << 23);
+    norms[1] = __uint_as_float(uint32_t(127 - shift) << 23);
 }
 
 // p factor.x is 2^(l' - lse' + log2 |factor.x|), with factor.x's sign put on
@@ -186,9 +186,7 @@ template <bool kBf16>
 struct GradientEpilogue {
     static constexpr int kUnroll = 4;
     struct Params {
-        const int64_t* target;
-        const float* lse;
-        const float2* factors;
+        CeFactors f;
         uint16_t* gradient;
         int64_t stride;
         int32_t first;
@@ -205,10 +203,12 @@ struct GradientEpilogue {
     {
         if (r >= s.m)
             return;
-        const float2 factor = p.factors[r];
-        const int64_t t = p.target[r];
+        const int64_t t = p.f.target[r];
+        const float lse = p.f.lse[r], norm = p.f.norm ? *p.f.norm : 1.0f;
+        const float2 raw = factors(p.f, r, t, lse);
+        const float2 factor = make_float2(raw.x * norm, raw.y * norm);
         counts = t >= 0;
-        base = log2f(fabsf(factor.x)) - p.lse[r] * kLog2E;
+        base = log2f(fabsf(factor.x)) - lse * kLog2E;
         minus = factor.y;
         sign = factor.x < 0.0f ? 0x80008000u : 0u;
         target = t - p.first;
@@ -262,7 +262,7 @@ int run(const GemmOperand& x, const GemmOperand& weight, bool bf16, const typena
     GemmShape s{};
     s.splits = s.chains = 1;
     s.gave_up = gave_up;
-    return gemm_run<kCeColumns, E>(x, weight, s, bf16, p, sm_count,
+    return gemm_run<kCeColumns, E>(x, weight, s, bf16, p, GemmSide{}, sm_count,
                                    static_cast<cudaStream_t>(stream));
 }
 
@@ -280,9 +280,10 @@ int launch_ce_join(const CeJoin& a, void* stream)
                         static_cast<cudaStream_t>(stream), a);
 }
 
-int launch_ce_rows(const CeRows& a, void* stream)
+int launch_ce_norm(const CeFactors& f, int64_t rows, float* norms, void* stream)
 {
-    return launch_early(k_ce_rows, dim3(1), kRowsThreads, 0, static_cast<cudaStream_t>(stream), a);
+    return launch_early(k_ce_norm, dim3(1), kCeNormThreads, 0, static_cast<cudaStream_t>(stream), f,
+                        rows, norms);
 }
 
 int launch_ce_gradient(const CeGradient& a, int sm_count, int32_t* gave_up, void* stream)
@@ -291,7 +292,7 @@ int launch_ce_gradient(const CeGradient& a, int sm_count, int32_t* gave_up, void
         using E = decltype(epilogue);
         return run<std::remove_pointer_t<E>>(
             a.x, a.weight, a.bf16,
-            {a.target, a.lse, a.factors, static_cast<uint16_t*>(a.gradient), a.stride, a.first},
+            {a.factors, static_cast<uint16_t*>(a.gradient), a.stride, a.first},
             sm_count, gave_up, stream);
     };
     return a.bf16 ? launch(static_cast<GradientEpilogue<true>*>(nullptr))

@@ -39,30 +39,25 @@ struct CeJoin {
 };
 int launch_ce_join(const CeJoin& a, void* stream);
 
-// What the gradient of a row's logits is made of: scale (1 + 2 z lse) and
-// scale, both times a power of two that keeps them within the 16-bit type's
-// range; *unnorm undoes it.
-struct CeRows {
+// What the gradient of the rows' logits is made of besides them.
+struct CeFactors {
     const int64_t* target;
     const float* lse;
     const float* dloss;  // NULL: 1
-    double scale, z_loss;
-    int64_t rows;
+    float scale, two_z;  // twice z_loss
     int32_t vocab;
-    bool bf16;
-    float2* factors;
-    float* unnorm;
+    const float* norm;  // multiplies the factors, on the device; NULL: 1
 };
-int launch_ce_rows(const CeRows& a, void* stream);
+// For binary16: norms[0], a power of two that keeps the gradients in its range,
+// and norms[1], which undoes it.
+int launch_ce_norm(const CeFactors& f, int64_t rows, float* norms, void* stream);
 
 // The gradient of the logits of a piece of the vocabulary: rows of `stride`
 // 16-bit elements, a multiple of kCeColumns and at least the piece.
 struct CeGradient {
     GemmOperand x, weight;  // the piece's rows of the weight
     bool bf16;
-    const int64_t* target;
-    const float* lse;
-    const float2* factors;
+    CeFactors factors;
     int32_t first;  // the piece's place in the vocabulary
     void* gradient;
     int64_t stride;

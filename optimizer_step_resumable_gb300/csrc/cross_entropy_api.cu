@@ -18,6 +18,8 @@ namespace {
 using osr::check_apart;
 using osr::check_array;
 using osr::check_rows;
+using osr::copy_of;
+using osr::copy_readable;
 using osr::cuda_fail;
 using osr::DeviceScope;
 using osr::fail;
@@ -31,7 +33,6 @@ using osr::LinearProduct;
 using osr::LinearSize;
 using osr::on_vectors;
 using osr::Pieces;
-using osr::readable;
 using osr::rows_of;
 using osr::size_of;
 using osr::vector_of;
@@ -151,8 +152,7 @@ struct Parts {
     void* weight = nullptr;
     float2* parts = nullptr;  // forward
     float* at = nullptr;
-    float2* factors = nullptr;  // backward
-    float* unnorm = nullptr;
+    float* norms = nullptr;  // backward, binary16
     void* gradient = nullptr;
     float* dx = nullptr;  // the sum over the pieces so far
     float* dx_partials = nullptr;
@@ -174,8 +174,7 @@ int64_t lay_out(const linear_ce_ctx* c, int64_t rows, const Needs& n, const Piec
         p->at = static_cast<float*>(w.take(4 * rows));
         return w.bytes();
     }
-    p->factors = static_cast<float2*>(w.take(8 * rows));
-    p->unnorm = static_cast<float*>(w.take(4));
+    p->norms = static_cast<float*>(w.take(8));
     p->gradient = w.take(2 * rows * pieced.columns);
     if (n.dx && pieced.columns < c->vocab)
         p->dx = static_cast<float*>(w.take(4 * rows * whole(c->dim)));
@@ -310,9 +309,8 @@ int linear_cross_entropy_forward(linear_ce_ctx* ctx, const void* d_x, int64_t x_
                                    lay_out(ctx, rows, n, Pieced{}, d_workspace, &p))))
         return rc;
     DeviceScope scope(ctx->base.device);
-    int e = readable(&d_x, &x_stride, rows, dim, p.x, stream);
-    if (e == cudaSuccess)
-        e = readable(&d_weight, &weight_stride, w_rows, w_cols, p.weight, stream);
+    int e = copy_readable(copy_of(&d_x, &x_stride, rows, dim, p.x),
+                          copy_of(&d_weight, &weight_stride, w_rows, w_cols, p.weight), stream);
     if (e == cudaSuccess)
         e = osr::launch_ce_parts(
             osr::CeForward{GemmOperand{d_x, rows, dim, x_stride, false},
@@ -406,21 +404,22 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
                                    lay_out(ctx, rows, n, pieced, d_workspace, &p))))
         return rc;
     const bool bf16 = dtype == ADAMW_DTYPE_BF16;
-    e = readable(&d_x, &x_stride, rows, dim, p.x, stream);
-    if (e == cudaSuccess)
-        e = readable(&d_weight, &weight_stride, w_rows, w_cols, p.weight, stream);
-    if (e == cudaSuccess)
-        e = osr::launch_ce_rows(osr::CeRows{d_target, d_lse, d_dloss, scale, z_loss, rows, vocab,
-                                            bf16, p.factors, p.unnorm},
-                                stream);
+    e = copy_readable(copy_of(&d_x, &x_stride, rows, dim, p.x),
+                      copy_of(&d_weight, &weight_stride, w_rows, w_cols, p.weight), stream);
+    osr::CeFactors f{d_target, d_lse,  d_dloss, float(scale), float(2.0 * z_loss),
+                     vocab,    nullptr};
+    if (e == cudaSuccess && !bf16) {
+        e = osr::launch_ce_norm(f, rows, p.norms, stream);
+        f.norm = p.norms;
+    }
     for (int64_t first = 0; first < vocab && e == cudaSuccess; first += pieced.columns) {
         const int64_t columns = vocab - first < pieced.columns ? vocab - first : pieced.columns;
         const uint16_t* const w =
             static_cast<const uint16_t*>(d_weight) + first * (in_out ? 1 : weight_stride);
         e = osr::launch_ce_gradient(
             osr::CeGradient{GemmOperand{d_x, rows, dim, x_stride, false},
-                            GemmOperand{w, columns, dim, weight_stride, in_out}, bf16, d_target,
-                            d_lse, p.factors, int32_t(first), p.gradient, pieced.columns},
+                            GemmOperand{w, columns, dim, weight_stride, in_out}, bf16, f,
+                            int32_t(first), p.gradient, pieced.columns},
             sms, ctx->base.gave_up, stream);
         const bool last = first + columns == vocab;
         const Plans& plans = last ? pieced.last : pieced.plans;
@@ -438,7 +437,7 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
             x.to.residual_dtype = ADAMW_DTYPE_F32;
         }
         x.to.alpha = 1.0f;
-        x.to.alpha_factor = p.unnorm;
+        x.to.alpha_factor = bf16 ? nullptr : p.norms + 1;
         x.to.vectors = last ? on_vectors(d_dx, dx_stride, rows, 2) : 1;
         const GemmOperand by_vocab{p.gradient, columns, rows, pieced.columns, true};
         const GemmOperand by_dim{d_x, dim, rows, x_stride, true};
@@ -447,19 +446,19 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
         dw.to = whole_dweight;
         dw.to.out = static_cast<char*>(d_dweight) +
                     int64_t(gs) * first * (grad_in_out ? 1 : dweight_stride);
-        dw.to.alpha_factor = p.unnorm;
+        dw.to.alpha_factor = x.to.alpha_factor;
         if (flags & LINEAR_ACCUMULATE)
             osr::accumulate_into(dw.to);
         int32_t* const gave_up = ctx->base.gave_up;
         if (e == cudaSuccess && plans.together) {
             e = osr::linear_product_two(x, plans.dx, p.dx_partials, dw, plans.dweight,
-                                        p.dweight_partials, sms, gave_up, stream);
+                                        p.dweight_partials, nullptr, sms, gave_up, stream);
         } else {
             if (e == cudaSuccess && d_dx)
-                e = osr::linear_product(x, plans.dx, p.dx_partials, sms, gave_up, stream);
+                e = osr::linear_product(x, plans.dx, p.dx_partials, nullptr, sms, gave_up, stream);
             if (e == cudaSuccess && d_dweight)
-                e = osr::linear_product(dw, plans.dweight, p.dweight_partials, sms, gave_up,
-                                        stream);
+                e = osr::linear_product(dw, plans.dweight, p.dweight_partials, nullptr, sms,
+                                        gave_up, stream);
         }
     }
     return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "cross entropy launch");

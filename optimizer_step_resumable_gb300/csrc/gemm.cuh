@@ -10,6 +10,7 @@
 //          tensor copies; the ring is as long as shared memory allows)
 //   1      of the pair's first block: issues the products (one thread)
 //   2      tensor memory
+//   3      sums that have to be joined meanwhile (GemmSide)
 //   4..11  epilogue: warp w has the rows 32 (w % 4).. of the block's half of
 //          the tile, and one half of the columns
 // Sums take two halves of the tensor memory in turn, so that the epilogue of
@@ -30,6 +31,7 @@
 #include "common.cuh"
 #include "early_dev.cuh"
 #include "gemm.h"
+#include "linear_dev.cuh"
 #include "tensor_dev.cuh"
 
 namespace osr {
@@ -91,6 +93,21 @@ __device__ __forceinline__ GemmItem gemm_item(const GemmShape& s, int32_t item, 
     it.last = int32_t(s.blocks * (part + 1) / parts);
     return it;
 }
+// Warp `w` of `count`: 32 columns at a time.
+__device__ __forceinline__ void gemm_side(const GemmSide& s, int64_t w, int64_t count)
+{
+    if (!s.partials)
+        return;
+    const int lane = threadIdx.x % 32;
+    for (int64_t column = 32 * w + lane; column < s.columns; column += 32 * count) {
+        float sum = 0.0f;
+#pragma unroll 16
+        for (int32_t i = 0; i < s.strips; ++i)
+            sum += __ldcg(s.partials + i * s.columns + column);
+        store_as(s.out, column, s.dtype, s.add ? sum + load_as(s.out, column, s.dtype) : sum);
+    }
+}
+
 // E, E2: the products' epilogues (E2 void: one product).  E::Params is its arguments; an object of E is made for
 // each tile and thread by E(params, shape, row, first column, columns, item,
 // which half of the tile's columns, 32 x 33 floats of shared memory of the warp's own), gets the
@@ -111,7 +128,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
            const __grid_constant__ GemmShape shape, const __grid_constant__ typename E::Params e,
            const __grid_constant__ CUtensorMap map_a2, const __grid_constant__ CUtensorMap map_b2,
            const __grid_constant__ GemmShape shape2,
-           const __grid_constant__ typename ParamsOf<E2>::type e2, const GemmDeal deal)
+           const __grid_constant__ typename ParamsOf<E2>::type e2, const GemmDeal deal,
+           const GemmSide side)
 {
     using R = GemmRing<BN>;
     extern __shared__ unsigned char raw[];
@@ -258,6 +276,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 break;
             next();
         }
+    } else if (warp == 3) {
+        gemm_side(side, blockIdx.x, gridDim.x);
     } else if (warp >= 4) {
         constexpr int kHalf = BN / 2, kChunk = kHalf < 32 ? kHalf : 32;
         const uint32_t quarter = warp % 4, half = (warp - 4) / 4;
@@ -361,7 +381,7 @@ inline int64_t gemm_items(const GemmShape& s)
 // Launches the items of one or two products; deal: as gemm_deal makes it.
 template <int BN, typename E, typename E2>
 inline int gemm_launch(const GemmPart<E>& p, const GemmPart<E2>& q, const GemmDeal& deal,
-                       cudaStream_t stream)
+                       const GemmSide& side, cudaStream_t stream)
 {
     using R = GemmRing<BN>;
     const cudaError_t err = cudaFuncSetAttribute(
@@ -369,11 +389,12 @@ inline int gemm_launch(const GemmPart<E>& p, const GemmPart<E2>& q, const GemmDe
     if (err != cudaSuccess)
         return int(err);
     return launch_early(k_gemm<BN, E, E2>, dim3(unsigned(2 * deal.pairs)), kGemmThreads, R::kSmem,
-                        stream, p.a, p.b, p.s, p.e, q.a, q.b, q.s, q.e, deal);
+                        stream, p.a, p.b, p.s, p.e, q.a, q.b, q.s, q.e, deal, side);
 }
 template <int BN, typename E>
 inline int gemm_run(const GemmOperand& a, const GemmOperand& b, const GemmShape& s, bool bf16,
-                    const typename E::Params& e, int sm_count, cudaStream_t stream)
+                    const typename E::Params& e, const GemmSide& side, int sm_count,
+                    cudaStream_t stream)
 {
     GemmPart<E> p;
     const int rc = gemm_part<BN, E>(a, b, s, bf16, e, &p);
@@ -386,7 +407,8 @@ inline int gemm_run(const GemmOperand& a, const GemmOperand& b, const GemmShape&
     if (items >= int64_t(1) << 30)
         return int(cudaErrorInvalidValue);
     const int pairs = int(items < sm_count / 2 ? items : sm_count / 2);
-    return gemm_launch<BN, E, void>(p, none, GemmDeal{pairs, int32_t(items), 0, 0, 0, 0}, stream);
+    return gemm_launch<BN, E, void>(p, none, GemmDeal{pairs, int32_t(items), 0, 0, 0, 0}, side,
+                                    stream);
 }
 
 }  // namespace detail

@@ -42,6 +42,17 @@ struct GemmDeal {
     int32_t pairs, longs, ahead, shorts, after, before;
 };
 
+// Sums of columns over `strips` rows of float32, in order, written to or (add)
+// added to out.
+struct GemmSide {
+    const float* partials;  // NULL: nothing to do
+    int32_t strips;
+    int64_t columns;
+    void* out;
+    int32_t dtype;
+    bool add;
+};
+
 constexpr int kGemmTileM = 256, kGemmInner = 64;
 
 // Whether the tiled copies can read a matrix: its address and row distance on

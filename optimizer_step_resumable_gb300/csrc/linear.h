@@ -65,18 +65,30 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
 // About how many microseconds one or two (q not NULL) products take in whole
 // tiles of 256 x 256.
 double linear_us(const LinearSize& p, const LinearSize* q, int sm_count);
-int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partials, int sm_count,
-                   int32_t* gave_up, void* stream);
+// side (may be NULL): done in the same launch, by a warp that has nothing else
+// to do, or in one of its own.
+int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partials,
+                   const GemmSide* side, int sm_count, int32_t* gave_up, void* stream);
 // Two plain products (neither bias nor activation nor z) in one launch.
 int linear_product_two(const LinearProduct& p, const LinearPlan& p_plan, float* p_partials,
                        const LinearProduct& q, const LinearPlan& q_plan, float* q_partials,
-                       int sm_count, int32_t* gave_up, void* stream);
+                       const GemmSide* side, int sm_count, int32_t* gave_up, void* stream);
 // A product over nothing.
 int launch_linear_zero(const LinearOut& to, int64_t rows, int64_t columns, int sm_count,
                        void* stream);
 
+// Rows of 16-bit elements, copied to where the tiled copies can read them;
+// `to` NULL: none.
+struct LinearCopy {
+    const void* from;
+    int64_t from_stride;
+    void* to;
+    int64_t to_stride, rows, columns;
+};
+int launch_linear_copies(const LinearCopy& a, const LinearCopy& b, void* stream);
+
 // dz = dy act'(z), rounded to their type, into rows of `stride` elements, and
-// its column sums (of the unrounded values), which a second kernel joins.
+// its column sums (of the unrounded values) in strips; two copies beside it.
 struct LinearSlope {
     const void* dy;
     int64_t dy_stride;
@@ -89,13 +101,11 @@ struct LinearSlope {
     int64_t rows, columns;
     float* partials;  // strips x columns; NULL: no sums
     int32_t strips;
+    LinearCopy copies[2];
 };
 int linear_strips(int64_t rows, int64_t columns, int sm_count);
 int launch_linear_slope(const LinearSlope& a, void* stream);
-int launch_linear_bias_grad(const float* partials, int32_t strips, int64_t columns, void* dbias,
-                            int32_t dtype, bool accumulate, void* stream);
-// Rows of 16-bit elements, copied to where the tiled copies can read them.
-int launch_copy_rows(const void* from, int64_t from_stride, void* to, int64_t to_stride,
-                     int64_t rows, int64_t columns, void* stream);
+// The strips' sums joined, in a launch of its own.
+int launch_linear_bias_grad(const GemmSide& side, void* stream);
 
 }  // namespace osr

@@ -16,18 +16,20 @@ namespace {
 using osr::check_apart;
 using osr::check_array;
 using osr::check_rows;
+using osr::copy_of;
+using osr::copy_readable;
 using osr::cuda_fail;
 using osr::DeviceScope;
 using osr::fail;
 using osr::gemm_readable;
 using osr::GemmOperand;
 using osr::known_dtype;
+using osr::LinearCopy;
 using osr::LinearPlan;
 using osr::LinearProduct;
 using osr::LinearSize;
 using osr::on_vectors;
 using osr::Pieces;
-using osr::readable;
 using osr::rows_of;
 using osr::size_of;
 using osr::vector_of;
@@ -262,9 +264,8 @@ int linear_forward(linear_ctx* ctx, const void* d_x, int64_t x_stride, const voi
                                    lay_out(ctx, rows, n, plans, d_workspace, &p))))
         return rc;
     DeviceScope scope(ctx->base.device);
-    int e = readable(&d_x, &x_stride, rows, in, p.x, stream);
-    if (e == cudaSuccess)
-        e = readable(&d_weight, &weight_stride, w_rows, w_cols, p.weight, stream);
+    int e = copy_readable(copy_of(&d_x, &x_stride, rows, in, p.x),
+                          copy_of(&d_weight, &weight_stride, w_rows, w_cols, p.weight), stream);
     if (e != cudaSuccess)
         return cuda_fail(cudaError_t(e), "linear layer launch");
     LinearProduct m{};
@@ -286,7 +287,8 @@ int linear_forward(linear_ctx* ctx, const void* d_x, int64_t x_stride, const voi
     m.to.vectors = on_vectors(d_y, y_stride, rows, 2) &&
                    (!d_residual || on_vectors(d_residual, residual_stride, rows, 2)) &&
                    (!d_z || on_vectors(d_z, z_stride, rows, 2));
-    e = osr::linear_product(m, plans.forward, p.partials, ctx->base.sm_count, ctx->base.gave_up, stream);
+    e = osr::linear_product(m, plans.forward, p.partials, nullptr, ctx->base.sm_count,
+                            ctx->base.gave_up, stream);
     return e == cudaSuccess ? ADAMW_OK : cuda_fail(cudaError_t(e), "linear layer launch");
 }
 
@@ -351,6 +353,8 @@ int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride, const 
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
                                    lay_out(ctx, rows, n, plans, d_workspace, &p))))
         return rc;
+    const LinearCopy weight_copy = copy_of(&d_weight, &weight_stride, w_rows, w_cols, p.weight);
+    const LinearCopy x_copy = copy_of(&d_x, &x_stride, rows, in, p.x);
     int e = cudaSuccess;
     if (n.dz || n.dbias) {
         osr::LinearSlope s{};
@@ -366,19 +370,21 @@ int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride, const 
         s.columns = out;
         s.partials = p.sums;
         s.strips = n.dbias ? plans.strips : osr::linear_strips(rows, out, sms);
+        s.copies[0] = weight_copy;
+        s.copies[1] = x_copy;
         e = osr::launch_linear_slope(s, stream);
+    } else {
+        e = copy_readable(weight_copy, x_copy, stream);
     }
-    if (e == cudaSuccess && d_dbias)
-        e = osr::launch_linear_bias_grad(p.sums, n.dbias ? plans.strips : 0, out, d_dbias,
-                                         grad_dtype, accumulate, stream);
-    const void* dz = n.dz ? p.dy : d_dy;
-    const int64_t dz_stride = n.dz ? whole(out) : dy_stride;
-    if (e == cudaSuccess && n.dx)
-        e = readable(&d_weight, &weight_stride, w_rows, w_cols, p.weight, stream);
-    if (e == cudaSuccess && n.dweight)
-        e = readable(&d_x, &x_stride, rows, in, p.x, stream);
+    const osr::GemmSide bias{p.sums,  n.dbias ? plans.strips : 0, out, d_dbias, grad_dtype,
+                             accumulate};
+    const osr::GemmSide* side = n.dbias ? &bias : nullptr;
+    if (e == cudaSuccess && d_dbias && (rows == 0 || (!n.dx && !n.dweight)))
+        e = osr::launch_linear_bias_grad(bias, stream);
     if (e != cudaSuccess)
         return cuda_fail(cudaError_t(e), "linear layer launch");
+    const void* dz = n.dz ? p.dy : d_dy;
+    const int64_t dz_stride = n.dz ? whole(out) : dy_stride;
     LinearProduct x{}, w{};  // of dx and dweight
     x.bf16 = w.bf16 = dtype == ADAMW_DTYPE_BF16;
     x.a = GemmOperand{dz, rows, out, dz_stride, false};
@@ -401,12 +407,13 @@ int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride, const 
     int32_t* const gave_up = ctx->base.gave_up;
     if (plans.together) {
         e = osr::linear_product_two(x, plans.dx, p.partials, w, plans.dweight, p.dweight_partials,
-                                    sms, gave_up, stream);
+                                    side, sms, gave_up, stream);
     } else {
         if (n.dx)
-            e = osr::linear_product(x, plans.dx, p.partials, sms, gave_up, stream);
+            e = osr::linear_product(x, plans.dx, p.partials, side, sms, gave_up, stream);
         if (e == cudaSuccess && n.dweight)
-            e = osr::linear_product(w, plans.dweight, p.dweight_partials, sms, gave_up, stream);
+            e = osr::linear_product(w, plans.dweight, p.dweight_partials,
+                                    n.dx ? nullptr : side, sms, gave_up, stream);
         if (e == cudaSuccess && d_dweight && rows == 0)
             e = osr::launch_linear_zero(w.to, g_rows, g_cols, sms, stream);
     }

@@ -208,7 +208,7 @@ double item_us(int64_t blocks, int64_t splits)
 StoreProduct store_product(const LinearProduct& p, const LinearPlan& plan, float* partials,
                            int32_t* gave_up)
 {
-    StoreProduct s{p.a, p.b, GemmShape{}, StoreParams{p.to, p.a.outer, p.b.outer, 0}};
+    StoreProduct s{p.a, p.b, GemmShape{}, StoreParams{p.to, p.a.outer, p.b.outer, 0}, GemmSide{}};
     s.s.splits = plan.splits;
     s.s.chains = plan.chains;
     s.s.gave_up = gave_up;
@@ -231,6 +231,19 @@ int join_product(const LinearProduct& p, const LinearPlan& plan, const float* pa
         return cudaSuccess;
     return join(p.to, partials, p.a.outer, p.b.outer, plan.splits, sm_count,
                 static_cast<cudaStream_t>(stream));
+}
+
+// Gives the sums to the product's launch, unless its few blocks would be long at
+// them.
+int take_side(const GemmSide* side, int64_t items, int sm_count, StoreProduct* s, void* stream)
+{
+    if (!side)
+        return cudaSuccess;
+    const int64_t blocks = 2 * (items < sm_count / 2 ? items : sm_count / 2);
+    if (side->columns > 32 * 4 * blocks)
+        return launch_linear_bias_grad(*side, stream);
+    s->side = *side;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -320,16 +333,20 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
     return true;
 }
 
-int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partials, int sm_count,
-                   int32_t* gave_up, void* stream)
+int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partials,
+                   const GemmSide* side, int sm_count, int32_t* gave_up, void* stream)
 {
     StoreProduct s = store_product(p, plan, partials, gave_up);
-    int e;
+    const int64_t tiles = plan.swapped ? tiles_of(p.b.outer, p.a.outer, plan.bn)
+                                       : tiles_of(p.a.outer, p.b.outer, plan.bn);
+    int e = take_side(side, tiles * plan.splits, sm_count, &s, stream);
+    if (e != cudaSuccess)
+        return e;
     if (plan.swapped) {
         const auto run = plan.bn == 32   ? gemm_run<32, SwappedEpilogue>
                          : plan.bn == 64 ? gemm_run<64, SwappedEpilogue>
                                          : gemm_run<128, SwappedEpilogue>;
-        e = run(s.b, s.a, s.s, p.bf16, s.p, sm_count, static_cast<cudaStream_t>(stream));
+        e = run(s.b, s.a, s.s, p.bf16, s.p, s.side, sm_count, static_cast<cudaStream_t>(stream));
     } else if (s.p.o.dtype == ADAMW_DTYPE_F32) {
         e = linear_store_f32(plan.bn, s, p.bf16, sm_count, stream);
     } else {
@@ -343,10 +360,10 @@ int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partia
 
 int linear_product_two(const LinearProduct& p, const LinearPlan& p_plan, float* p_partials,
                        const LinearProduct& q, const LinearPlan& q_plan, float* q_partials,
-                       int sm_count, int32_t* gave_up, void* stream)
+                       const GemmSide* side, int sm_count, int32_t* gave_up, void* stream)
 {
-    const StoreProduct a = store_product(p, p_plan, p_partials, gave_up);
-    const StoreProduct b = store_product(q, q_plan, q_partials, gave_up);
+    StoreProduct a = store_product(p, p_plan, p_partials, gave_up);
+    StoreProduct b = store_product(q, q_plan, q_partials, gave_up);
     // the longer items first
     const double a_us = item_us(inner_blocks(p.a.inner), p_plan.splits);
     const double b_us = item_us(inner_blocks(q.a.inner), q_plan.splits);
@@ -357,13 +374,15 @@ int linear_product_two(const LinearProduct& p, const LinearPlan& p_plan, float* 
         return int(cudaErrorInvalidValue);
     const int64_t pairs = items < most ? items : most;
     const bool turned = b_us > a_us;
-    const StoreProduct &first = turned ? b : a, &second = turned ? a : b;
+    StoreProduct &first = turned ? b : a, &second = turned ? a : b;
+    int e = take_side(side, items, sm_count, &first, stream);
+    if (e != cudaSuccess)
+        return e;
     GemmDeal deal;
     if (turned)
         deal_out(b_items, b_us, a_items, a_us, pairs, &deal);
     else
         deal_out(a_items, a_us, b_items, b_us, pairs, &deal);
-    int e;
     switch (first.p.o.dtype) {
     case ADAMW_DTYPE_F32: e = linear_store_two_f32(first, second, p.bf16, deal, stream); break;
     case ADAMW_DTYPE_BF16: e = linear_store_two_bf16(first, second, deal, stream); break;

@@ -18,6 +18,7 @@ struct StoreProduct {
     GemmOperand a, b;
     GemmShape s;  // splits, chains
     StoreParams p;
+    GemmSide side;  // of the first of two
 };
 // Tiles of 256 x bn (128, 192 or 256), the product's rows along the long side,
 // for an output of the type; `plain`: neither bias nor activation nor z, which
@@ -258,7 +259,7 @@ inline int store_two(const StoreProduct& p, const StoreProduct& q, bool bf16,
     if (e == cudaSuccess)
         e = gemm_part<256, E2>(q.a, q.b, q.s, bf16, q.p, &two);
     return e == cudaSuccess
-               ? gemm_launch<256, E, E2>(one, two, deal, static_cast<cudaStream_t>(stream))
+               ? gemm_launch<256, E, E2>(one, two, deal, p.side, static_cast<cudaStream_t>(stream))
                : e;
 }
 template <int kOut, bool kPlain>
@@ -267,9 +268,9 @@ inline int store_one(int bn, const StoreProduct& p, bool bf16, int sm_count, voi
     using E = StoreEpilogue<kOut, kPlain>;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (bn) {
-    case 128: return gemm_run<128, E>(p.a, p.b, p.s, bf16, p.p, sm_count, st);
-    case 192: return gemm_run<192, E>(p.a, p.b, p.s, bf16, p.p, sm_count, st);
-    default: return gemm_run<256, E>(p.a, p.b, p.s, bf16, p.p, sm_count, st);
+    case 128: return gemm_run<128, E>(p.a, p.b, p.s, bf16, p.p, p.side, sm_count, st);
+    case 192: return gemm_run<192, E>(p.a, p.b, p.s, bf16, p.p, p.side, sm_count, st);
+    default: return gemm_run<256, E>(p.a, p.b, p.s, bf16, p.p, p.side, sm_count, st);
     }
 }
 

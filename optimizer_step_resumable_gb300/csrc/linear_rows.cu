@@ -39,21 +39,68 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p, int step, int count)
                       w[6] | (w[7] << 16));
 }
 
+// Copies: eight elements a thread, wherever the rows start.
+__device__ __forceinline__ void copy_rows(const LinearCopy& c, int64_t block, int64_t blocks)
+{
+    const int64_t vectors = (c.columns + 7) / 8;
+    for (int64_t i = block * blockDim.x + threadIdx.x; i < c.rows * vectors;
+         i += blocks * blockDim.x) {
+        const int64_t r = i / vectors, at = (i - r * vectors) * 8;
+        const uint16_t* const p = static_cast<const uint16_t*>(c.from) + r * c.from_stride + at;
+        const int count = int(c.columns - at < 8 ? c.columns - at : 8);
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j] = j < count ? p[j] : 0u;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.to) + r * c.to_stride + at) =
+            make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16),
+                       w[6] | (w[7] << 16));
+    }
+}
+constexpr int kCopyThreads = 256;
+int copy_blocks(const LinearCopy& c)
+{
+    if (!c.to)
+        return 0;
+    const int64_t want = (c.rows * ((c.columns + 7) / 8) + kCopyThreads - 1) / kCopyThreads;
+    return int(want < 2048 ? want : 2048);
+}
+__global__ void __launch_bounds__(kCopyThreads)
+    k_linear_copies(const LinearCopy a, const LinearCopy b, int32_t a_blocks)
+{
+    wait_before();
+    go_ahead();
+    if (int32_t(blockIdx.x) < a_blocks)
+        copy_rows(a, blockIdx.x, a_blocks);
+    else
+        copy_rows(b, blockIdx.x - a_blocks, gridDim.x - a_blocks);
+}
+
 template <int kAct, bool kVector>
 __global__ void __launch_bounds__(kSlopeThreads, 4)
-    k_linear_slope(const LinearSlope a)
+    k_linear_slope(const LinearSlope a, int32_t across, int32_t copies0, int32_t copies1)
 {
     __shared__ float sums[8][kSlopeColumns + 8];
     wait_before();
     go_ahead();
+    // the blocks behind the strips' copy
+    const int32_t copier = int32_t(blockIdx.x) - across * a.strips;
+    if (copier >= 0) {
+        if (copier < copies0)
+            copy_rows(a.copies[0], copier, copies0);
+        else
+            copy_rows(a.copies[1], copier - copies0, copies1);
+        return;
+    }
+    const int32_t strip = int32_t(blockIdx.x) / across, part = int32_t(blockIdx.x) % across;
     constexpr int kAtOnce = kAct == LINEAR_NONE ? 4 : 2;
     const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
     const int place = kVector ? 8 * lane : lane, step = kVector ? 1 : 32;
-    const int64_t column = int64_t(blockIdx.x) * kSlopeColumns + place;
+    const int64_t column = int64_t(part) * kSlopeColumns + place;
     const int64_t left = a.columns - column;
     const int count = left <= 0 ? 0 : int(left >= 8 * step ? 8 : (left + step - 1) / step);
-    const int64_t first = a.rows * blockIdx.y / a.strips;
-    const int64_t last = a.rows * (blockIdx.y + 1) / a.strips;
+    const int64_t first = a.rows * strip / a.strips;
+    const int64_t last = a.rows * (strip + 1) / a.strips;
     const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + (first + group) * a.dy_stride + column;
     const uint16_t* z = static_cast<const uint16_t*>(a.z) + (first + group) * a.z_stride + column;
     uint16_t* dz = static_cast<uint16_t*>(a.dz) + (first + group) * a.stride + column;
@@ -104,13 +151,13 @@ __global__ void __launch_bounds__(kSlopeThreads, 4)
     for (int i = 0; i < 8; ++i)
         sums[group][place + i * step] = total[i];
     __syncthreads();
-    const int64_t mine = int64_t(blockIdx.x) * kSlopeColumns + threadIdx.x;
+    const int64_t mine = int64_t(part) * kSlopeColumns + threadIdx.x;
     if (mine < a.columns) {
         float s = 0.0f;
 #pragma unroll
         for (int g = 0; g < 8; ++g)
             s += sums[g][threadIdx.x];
-        a.partials[blockIdx.y * a.columns + mine] = s;
+        a.partials[strip * a.columns + mine] = s;
     }
 }
 
@@ -118,52 +165,27 @@ __global__ void __launch_bounds__(kSlopeThreads, 4)
 // of them, then a column, whose 32 sums it joins.
 constexpr int kBiasThreads = 1024;
 __global__ void __launch_bounds__(kBiasThreads)
-    k_linear_bias_grad(const float* partials, int32_t strips, int64_t columns, void* dbias,
-                       int32_t dtype, bool accumulate)
+    k_linear_bias_grad(const GemmSide s)
 {
     __shared__ float sums[32][33];
     wait_before();
     go_ahead();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t base = int64_t(blockIdx.x) * 32;
-    float s = 0.0f;
-    if (base + lane < columns)
+    float sum = 0.0f;
+    if (base + lane < s.columns)
 #pragma unroll 4
-        for (int32_t i = warp; i < strips; i += 32)
-            s += __ldcg(partials + i * columns + base + lane);
-    sums[warp][lane] = s;
+        for (int32_t i = warp; i < s.strips; i += 32)
+            sum += __ldcg(s.partials + i * s.columns + base + lane);
+    sums[warp][lane] = sum;
     __syncthreads();
-    s = sums[lane][warp];
+    sum = sums[lane][warp];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
-        s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
     const int64_t column = base + warp;
-    if (lane == 0 && column < columns)
-        store_as(dbias, column, dtype, accumulate ? s + load_as(dbias, column, dtype) : s);
-}
-
-constexpr int kCopyThreads = 256;
-__global__ void __launch_bounds__(kCopyThreads)
-    k_copy_rows(const uint16_t* from, int64_t from_stride, uint16_t* to, int64_t to_stride,
-                int64_t rows, int64_t columns)
-{
-    wait_before();
-    go_ahead();
-    const int64_t vectors = (columns + 7) / 8;
-    for (int64_t i = int64_t(blockIdx.x) * kCopyThreads + threadIdx.x; i < rows * vectors;
-         i += int64_t(gridDim.x) * kCopyThreads) {
-        const int64_t r = i / vectors, c = (i - r * vectors) * 8;
-        const uint16_t* const p = from + r * from_stride + c;
-        const int count = int(columns - c < 8 ? columns - c : 8);
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = 2 * j < count ? p[2 * j] : 0u;
-            const uint32_t hi = 2 * j + 1 < count ? p[2 * j + 1] : 0u;
-            w[j] = lo | (hi << 16);
-        }
-        *reinterpret_cast<uint4*>(to + r * to_stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    if (lane == 0 && column < s.columns)
+        store_as(s.out, column, s.dtype, s.add ? sum + load_as(s.out, column, s.dtype) : sum);
 }
 
 }  // namespace
@@ -180,15 +202,18 @@ int linear_strips(int64_t rows, int64_t columns, int sm_count)
 
 int launch_linear_slope(const LinearSlope& a, void* stream)
 {
-    const dim3 grid(unsigned((a.columns + kSlopeColumns - 1) / kSlopeColumns), unsigned(a.strips));
+    const int32_t across = int32_t((a.columns + kSlopeColumns - 1) / kSlopeColumns);
+    const int32_t copies[] = {copy_blocks(a.copies[0]), copy_blocks(a.copies[1])};
+    const dim3 grid(unsigned(across * a.strips + copies[0] + copies[1]));
     const auto on_vector = [](const void* p, int64_t stride) {
         return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0;
     };
     const bool vector = on_vector(a.dy, a.rows > 1 ? a.dy_stride : 0) &&
                         (a.act == LINEAR_NONE || on_vector(a.z, a.rows > 1 ? a.z_stride : 0));
-    const auto launch = [&](void (*vectors)(LinearSlope), void (*others)(LinearSlope)) {
+    using Kernel = void (*)(LinearSlope, int32_t, int32_t, int32_t);
+    const auto launch = [&](Kernel vectors, Kernel others) {
         return launch_early(vector ? vectors : others, grid, kSlopeThreads, 0,
-                            static_cast<cudaStream_t>(stream), a);
+                            static_cast<cudaStream_t>(stream), a, across, copies[0], copies[1]);
     };
     switch (a.act) {
     case LINEAR_RELU:
@@ -204,21 +229,17 @@ int launch_linear_slope(const LinearSlope& a, void* stream)
     }
 }
 
-int launch_linear_bias_grad(const float* partials, int32_t strips, int64_t columns, void* dbias,
-                            int32_t dtype, bool accumulate, void* stream)
+int launch_linear_bias_grad(const GemmSide& side, void* stream)
 {
-    return launch_early(k_linear_bias_grad, dim3(unsigned((columns + 31) / 32)), kBiasThreads, 0,
-                        static_cast<cudaStream_t>(stream), partials, strips, columns, dbias, dtype,
-                        accumulate);
+    return launch_early(k_linear_bias_grad, dim3(unsigned((side.columns + 31) / 32)), kBiasThreads,
+                        0, static_cast<cudaStream_t>(stream), side);
 }
 
-int launch_copy_rows(const void* from, int64_t from_stride, void* to, int64_t to_stride,
-                     int64_t rows, int64_t columns, void* stream)
+int launch_linear_copies(const LinearCopy& a, const LinearCopy& b, void* stream)
 {
-    const int64_t want = (rows * ((columns + 7) / 8) + kCopyThreads - 1) / kCopyThreads;
-    return launch_early(k_copy_rows, dim3(unsigned(want < 4096 ? want : 4096)), kCopyThreads, 0,
-                        static_cast<cudaStream_t>(stream), static_cast<const uint16_t*>(from),
-                        from_stride, static_cast<uint16_t*>(to), to_stride, rows, columns);
+    const int32_t a_blocks = copy_blocks(a);
+    return launch_early(k_linear_copies, dim3(unsigned(a_blocks + copy_blocks(b))), kCopyThreads, 0,
+                        static_cast<cudaStream_t>(stream), a, b, a_blocks);
 }
 
 }  // namespace osr

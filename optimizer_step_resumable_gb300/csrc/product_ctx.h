@@ -100,16 +100,21 @@ inline bool on_vectors(const void* p, int64_t stride, int64_t rows, size_t size)
 }
 
 // Makes p, rows of `columns` elements `stride` apart, one that the tiled copies
-// can read: a copy of it in `copy`, unless that is NULL.
-inline int readable(const void** p, int64_t* stride, int64_t rows, int64_t columns, void* copy,
-                    void* stream)
+// can read: a copy of it in `copy`, unless that is NULL.  The copy is still to
+// be made.
+inline LinearCopy copy_of(const void** p, int64_t* stride, int64_t rows, int64_t columns,
+                          void* copy)
 {
-    if (!copy)
-        return cudaSuccess;
-    const int e = launch_copy_rows(*p, *stride, copy, whole(columns), rows, columns, stream);
-    *p = copy;
-    *stride = whole(columns);
-    return e;
+    const LinearCopy c{*p, *stride, copy, whole(columns), rows, columns};
+    if (copy) {
+        *p = copy;
+        *stride = whole(columns);
+    }
+    return c;
+}
+inline int copy_readable(const LinearCopy& a, const LinearCopy& b, void* stream)
+{
+    return a.to || b.to ? launch_linear_copies(a, b, stream) : int(cudaSuccess);
 }
 
 }  // namespace osr
