@@ -30,7 +30,8 @@ CUDA_SOURCES = ["norm.cu", "step.cu", "onepass.cu", "ranks.cu", "pack.cu", "api.
                 "layernorm_bwd_bf16.cu", "layernorm_bwd_f16.cu", "layernorm_api.cu",
                 "gemm.cu", "linear_gemm.cu", "linear_gemm_f32.cu", "linear_gemm_bf16.cu",
                 "linear_gemm_f16.cu", "linear_gemm_two_f32.cu",
-                "linear_gemm_two_bf16.cu", "linear_gemm_two_f16.cu", "linear_rows.cu", "linear_api.cu",
+                "linear_gemm_two_bf16.cu", "linear_gemm_two_f16.cu", "linear_few.cu", "linear_rows.cu",
+                "linear_api.cu",
                 "cross_entropy.cu", "cross_entropy_api.cu", "distill.cu", "distill_api.cu"]
 CXX_SOURCES = ["ckpt_io.cpp", "manifest.cpp", "sha256.cpp"]
 

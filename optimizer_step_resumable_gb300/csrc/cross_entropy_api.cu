@@ -81,9 +81,9 @@ Plans make_plans(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Ne
 {
     Plans p;
     const int sms = c->base.sm_count;
-    const LinearSize dx{rows, c->dim, columns, false, false};
+    const LinearSize dx{rows, c->dim, columns, false, !n.in_out, false};
     const LinearSize dw{n.grad_in_out ? c->dim : columns, n.grad_in_out ? columns : c->dim, rows,
-                        true, n.grad_f32};
+                        true, true, n.grad_f32};
     if (n.dx && n.dweight && !n.grad_mixed) {
         p.together = osr::linear_plan_two(dx, dw, sms, &p.dx, &p.dweight);
     } else {
@@ -98,10 +98,10 @@ Plans make_plans(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Ne
 // The time of a piece, as far as it depends on the division.
 double piece_us(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Needs& n)
 {
-    const LinearSize logits{rows, columns, c->dim, false, false};
-    const LinearSize dx{rows, c->dim, columns, false, false};
+    const LinearSize logits{rows, columns, c->dim, false, n.in_out, false};
+    const LinearSize dx{rows, c->dim, columns, false, !n.in_out, false};
     const LinearSize dw{n.grad_in_out ? c->dim : columns, n.grad_in_out ? columns : c->dim, rows,
-                        true, false};
+                        true, true, false};
     const int sms = c->base.sm_count;
     return osr::linear_us(logits, nullptr, sms) +
            (n.dx && n.dweight && !n.grad_mixed

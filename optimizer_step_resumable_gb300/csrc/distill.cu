@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, 5) k_distill_forward(const Distill a
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 5) k_distill_backward(const Distill a)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 5)
+    k_distill_backward(const Distill a)
 {
     using namespace packed;
     __shared__ int32_t ids[kDistillMost];

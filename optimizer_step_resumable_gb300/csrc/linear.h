@@ -47,15 +47,16 @@ inline void accumulate_into(LinearOut& o)
 // GemmShape); swapped: the tile's long side lies along the columns, for
 // products of few rows.
 struct LinearPlan {
+    bool few;  // not in tiles at all (linear_few.cu)
     bool swapped;
     int32_t bn, splits, chains;
     int64_t partials;  // float32 sums in the workspace
 };
-// a_across: whether a's outer dimension is the adjacent one; f32: out is
-// float32.
+// *_across: whether the operand's outer dimension is the adjacent one; f32: out
+// is float32.
 struct LinearSize {
     int64_t rows, columns, inner;
-    bool a_across, f32;
+    bool a_across, b_across, f32;
 };
 LinearPlan linear_plan(const LinearSize& p, int sm_count);
 // Plans of two products that do not depend on one another; true if they go in
@@ -73,6 +74,9 @@ int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partia
 int linear_product_two(const LinearProduct& p, const LinearPlan& p_plan, float* p_partials,
                        const LinearProduct& q, const LinearPlan& q_plan, float* q_partials,
                        const GemmSide* side, int sm_count, int32_t* gave_up, void* stream);
+// A product of few rows that lie along the sum, and whether that is faster.
+bool linear_few_pays(const LinearSize& p);
+int linear_few(const LinearProduct& p, int sm_count, void* stream);
 // A product over nothing.
 int launch_linear_zero(const LinearOut& to, int64_t rows, int64_t columns, int sm_count,
                        void* stream);

@@ -71,12 +71,12 @@ Plans make_plans(const linear_ctx* c, int64_t rows, const Needs& n)
     Plans p;
     const int sms = c->base.sm_count;
     if (!n.backward) {
-        p.forward = osr::linear_plan(LinearSize{rows, c->out, c->in, false, false}, sms);
+        p.forward = osr::linear_plan(LinearSize{rows, c->out, c->in, false, n.in_out, false}, sms);
         return p;
     }
-    const LinearSize dx{rows, c->in, c->out, false, false};
+    const LinearSize dx{rows, c->in, c->out, false, !n.in_out, false};
     const LinearSize dw{n.grad_in_out ? c->in : c->out, n.grad_in_out ? c->out : c->in, rows, true,
-                        n.grad_f32};
+                        true, n.grad_f32};
     if (n.dx && n.dweight && !n.grad_mixed) {
         p.together = osr::linear_plan_two(dx, dw, sms, &p.dx, &p.dweight);
     } else {

@@ -299,6 +299,15 @@ __device__ __forceinline__ void with_activation(int32_t act, F&& f)
     }
 }
 
+// With the factor that is on the device.
+__device__ __forceinline__ LinearOut with_factor(const LinearOut& o)
+{
+    LinearOut r = o;
+    if (o.alpha_factor)
+        r.alpha *= *o.alpha_factor;
+    return r;
+}
+
 // N neighbouring elements, from their sums to memory: one, or eight on a
 // vector's boundary if the rows are on vectors.
 template <int kAct, int N>

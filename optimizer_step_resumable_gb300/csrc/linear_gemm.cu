@@ -8,14 +8,6 @@ namespace {
 
 using namespace detail;
 
-__device__ __forceinline__ LinearOut with_factor(const LinearOut& o)
-{
-    LinearOut r = o;
-    if (o.alpha_factor)
-        r.alpha *= *o.alpha_factor;
-    return r;
-}
-
 // The tile's rows are the product's columns: the lanes of a warp have
 // neighbouring columns of one row of the product.
 struct SwappedEpilogue {
@@ -251,6 +243,11 @@ int take_side(const GemmSide* side, int64_t items, int sm_count, StoreProduct* s
 LinearPlan linear_plan(const LinearSize& p, int sm_count)
 {
     LinearPlan best{};
+    if (linear_few_pays(p)) {
+        best.few = true;
+        best.splits = best.chains = 1;
+        return best;
+    }
     const bool swapped = p.rows <= 128 && p.rows < p.columns;
     const int64_t m = swapped ? p.columns : p.rows, n = swapped ? p.rows : p.columns;
     const int64_t blocks = inner_blocks(p.inner), pairs = sm_count / 2;
@@ -300,7 +297,7 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
     *p_plan = linear_plan(p, sm_count);
     *q_plan = linear_plan(q, sm_count);
     // tiles of 256 x 256 have to fit both
-    if (p_plan->swapped || p.rows <= 128 || p.columns <= 128 || q.rows <= 128 || q.columns <= 128)
+    if (p_plan->few || p_plan->swapped || p.rows <= 128 || p.columns <= 128 || q.rows <= 128 || q.columns <= 128)
         return false;
     const int64_t pairs = sm_count / 2, blocks[] = {inner_blocks(p.inner), inner_blocks(q.inner)};
     const int64_t tiles[] = {tiles_of(p.rows, p.columns, 256), tiles_of(q.rows, q.columns, 256)};
@@ -326,8 +323,8 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
             }
         }
     }
-    *p_plan = LinearPlan{false, 256, best[0], 1, 0};
-    *q_plan = LinearPlan{false, 256, best[1], 1, 0};
+    *p_plan = LinearPlan{false, false, 256, best[0], 1, 0};
+    *q_plan = LinearPlan{false, false, 256, best[1], 1, 0};
     finish_plan(p, p_plan);
     finish_plan(q, q_plan);
     return true;
@@ -336,6 +333,10 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
 int linear_product(const LinearProduct& p, const LinearPlan& plan, float* partials,
                    const GemmSide* side, int sm_count, int32_t* gave_up, void* stream)
 {
+    if (plan.few) {
+        const int e = side ? launch_linear_bias_grad(*side, stream) : int(cudaSuccess);
+        return e == cudaSuccess ? linear_few(p, sm_count, stream) : e;
+    }
     StoreProduct s = store_product(p, plan, partials, gave_up);
     const int64_t tiles = plan.swapped ? tiles_of(p.b.outer, p.a.outer, plan.bn)
                                        : tiles_of(p.a.outer, p.b.outer, plan.bn);
