@@ -44,7 +44,7 @@ struct CeFactors {
     const int64_t* target;
     const float* lse;
     const float* dloss;  // NULL: 1
-    float scale, two_z;  // twice z_loss
+    float two_z;  // twice z_loss
     int32_t vocab;
     const float* norm;  // multiplies the factors, on the device; NULL: 1
 };

@@ -376,7 +376,7 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
     whole_dweight.out = d_dweight;
     whole_dweight.stride = dweight_stride;
     whole_dweight.dtype = grad_dtype;
-    whole_dweight.alpha = 1.0f;
+    whole_dweight.alpha = float(scale);
     whole_dweight.vectors = on_vectors(d_dweight, dweight_stride, g_rows, gs);
     int e = cudaSuccess;
     if (rows == 0) {
@@ -406,8 +406,7 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
     const bool bf16 = dtype == ADAMW_DTYPE_BF16;
     e = copy_readable(copy_of(&d_x, &x_stride, rows, dim, p.x),
                       copy_of(&d_weight, &weight_stride, w_rows, w_cols, p.weight), stream);
-    osr::CeFactors f{d_target, d_lse,  d_dloss, float(scale), float(2.0 * z_loss),
-                     vocab,    nullptr};
+    osr::CeFactors f{d_target, d_lse, d_dloss, float(2.0 * z_loss), vocab, nullptr};
     if (e == cudaSuccess && !bf16) {
         e = osr::launch_ce_norm(f, rows, p.norms, stream);
         f.norm = p.norms;
@@ -436,7 +435,7 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
             x.to.residual_stride = whole(dim);
             x.to.residual_dtype = ADAMW_DTYPE_F32;
         }
-        x.to.alpha = 1.0f;
+        x.to.alpha = float(scale);
         x.to.alpha_factor = bf16 ? nullptr : p.norms + 1;
         x.to.vectors = last ? on_vectors(d_dx, dx_stride, rows, 2) : 1;
         const GemmOperand by_vocab{p.gradient, columns, rows, pieced.columns, true};
