@@ -59,8 +59,9 @@ struct Pieced {
 struct linear_ce_ctx {
     osr::ProductContext base;
     int32_t dim = 0, vocab = 0;
-    // the last backward call's pieces, which take as long to find as some
-    // launches
+    // the last piece found and the last backward call's plans, which take as long
+    // to make as some launches
+    int64_t piece_rows = -1, piece = 0;
     int64_t rows = -1;
     Needs needs{};
     Pieced pieced;
@@ -96,42 +97,48 @@ Plans make_plans(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Ne
 }
 
 // The time of a piece, as far as it depends on the division.
-double piece_us(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Needs& n)
+double piece_us(const linear_ce_ctx* c, int64_t rows, int64_t columns)
 {
-    const LinearSize logits{rows, columns, c->dim, false, n.in_out, false};
-    const LinearSize dx{rows, c->dim, columns, false, !n.in_out, false};
-    const LinearSize dw{n.grad_in_out ? c->dim : columns, n.grad_in_out ? columns : c->dim, rows,
-                        true, true, false};
-    const int sms = c->base.sm_count;
-    return osr::linear_us(logits, nullptr, sms) +
-           (n.dx && n.dweight && !n.grad_mixed
-                ? osr::linear_us(dx, &dw, sms)
-                : (n.dx ? osr::linear_us(dx, nullptr, sms) : 0.0) +
-                      (n.dweight ? osr::linear_us(dw, nullptr, sms) : 0.0));
+    const LinearSize logits{rows, columns, c->dim, false, false, false};
+    const LinearSize dx{rows, c->dim, columns, false, true, false};
+    const LinearSize dw{columns, c->dim, rows, true, true, false};
+    return osr::linear_us(logits, nullptr, c->base.sm_count) +
+           osr::linear_us(dx, &dw, c->base.sm_count);
 }
 
-// Pieces of whole tiles.  Tiles of products are as good as they fill the pairs
-// of blocks in the end: the number of columns with the least time of all those
-// that kPieceBytes allows, down to half of them (8192 x 768 x 32000 backward:
-// 797 us in two equal pieces of 63 tiles, @@ so).
-Pieced find_pieces(const linear_ce_ctx* c, int64_t rows, const Needs& n)
+// Columns of a piece, whole tiles.  Tiles of products are as good as they fill
+// the pairs of blocks in the end: the number with the least time of all those
+// that kPieceBytes allows, down to half of them and not more than 64 tiles fewer
+// (8192 x 768 x 32000 backward: 797 us in two equal pieces, 773 so).
+int64_t find_piece(const linear_ce_ctx* c, int64_t rows)
 {
-    Pieced p;
     const int64_t all = tiles(c->vocab);
-    int64_t most = kPieceBytes / (2 * rows) / kCeColumns;
+    int64_t most = kPieceBytes / (2 * rows) / kCeColumns, best = 0;
     most = most < 1 ? 1 : most > all ? all : most;
     double least_us = 0.0;
-    for (int64_t t = most; t >= (most + 1) / 2; --t) {
-        const int64_t columns = t * kCeColumns, rest = (all - 1) / t;
-        const int64_t end = c->vocab - rest * columns;
-        const double us = double(rest) * piece_us(c, rows, columns, n) + piece_us(c, rows, end, n);
-        if (p.columns == 0 || us < least_us) {
+    for (int64_t t = most; t >= (most + 1) / 2 && t >= most - 64; --t) {
+        const int64_t columns = t * kCeColumns, others = (all - 1) / t;
+        const double us = double(others) * piece_us(c, rows, columns) +
+                          piece_us(c, rows, c->vocab - others * columns);
+        if (best == 0 || us < least_us) {
             least_us = us;
-            p.columns = columns;
+            best = columns;
         }
-        if (t < most - 64)
-            break;
     }
+    return best;
+}
+int64_t piece_of(linear_ce_ctx* c, int64_t rows)
+{
+    if (rows != c->piece_rows) {
+        c->piece = find_piece(c, rows);
+        c->piece_rows = rows;
+    }
+    return c->piece;
+}
+Pieced make_pieces(linear_ce_ctx* c, int64_t rows, const Needs& n)
+{
+    Pieced p;
+    p.columns = piece_of(c, rows);
     const int64_t end = c->vocab - (c->vocab - 1) / p.columns * p.columns;
     p.last = make_plans(c, rows, end, n);
     p.plans = c->vocab > p.columns ? make_plans(c, rows, p.columns, n) : p.last;
@@ -140,7 +147,7 @@ Pieced find_pieces(const linear_ce_ctx* c, int64_t rows, const Needs& n)
 const Pieced& pieces_of(linear_ce_ctx* c, int64_t rows, const Needs& n)
 {
     if (rows != c->rows || std::memcmp(&n, &c->needs, sizeof n) != 0) {
-        c->pieced = find_pieces(c, rows, n);
+        c->pieced = make_pieces(c, rows, n);
         c->rows = rows;
         c->needs = n;
     }
@@ -260,7 +267,7 @@ int linear_cross_entropy_workspace(linear_ce_ctx* ctx, int64_t rows, int32_t fla
         for (int apart = 0; apart < (back ? 2 : 1); ++apart) {
             n.grad_mixed = apart != 0;
             Parts p;
-            const int64_t b = lay_out(ctx, rows, n, back ? find_pieces(ctx, rows, n) : Pieced{},
+            const int64_t b = lay_out(ctx, rows, n, back ? make_pieces(ctx, rows, n) : Pieced{},
                                       nullptr, &p);
             *bytes = *bytes > b ? *bytes : b;
         }

@@ -65,9 +65,9 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8])
 
 // 32 rows of 64 16-bit elements on their way from a warp's lanes, a row each,
 // to memory: through 4 KB of shared memory, so that eight lanes write the 128
-// bytes of a row.  (Each lane writing its own row, 32 bytes at a time, took the
-// cross entropy's gradient @@ us where this takes @@.)  16-byte pieces lie
-// swizzled, at piece XOR row, so that neither way meets a bank twice.
+// bytes of a row (the cross entropy's backward pass 773 us with each lane writing
+// its own row, 32 bytes at a time, 765 so).  16-byte pieces lie swizzled, at piece
+// XOR row, so that neither way meets a bank twice.
 __device__ __forceinline__ void strip_put(uint4* strip, int piece, uint4 w)
 {
     const int lane = threadIdx.x % 32;
