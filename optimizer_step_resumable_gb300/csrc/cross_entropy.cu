@@ -218,8 +218,8 @@ struct GradientEpilogue {
         target = t - p.first;
     }
     template <int C>
-    __device__ __forceinline__ void chunk(const Params& p, const GemmShape& s, int32_t column, int c,
-                                          float (&v)[C], float* stage)
+    __device__ __forceinline__ void chunk(const Params& p, const GemmShape& s, int32_t column,
+                                          int c, float (&v)[C], float* stage)
     {
         const int64_t off = target - column;
         const bool here = off >= 0 && off < C && counts;

@@ -93,6 +93,7 @@ __device__ __forceinline__ GemmItem gemm_item(const GemmShape& s, int32_t item, 
     it.last = int32_t(s.blocks * (part + 1) / parts);
     return it;
 }
+
 // Warp `w` of `count`: 32 columns at a time.
 __device__ __forceinline__ void gemm_side(const GemmSide& s, int64_t w, int64_t count)
 {
@@ -108,12 +109,12 @@ __device__ __forceinline__ void gemm_side(const GemmSide& s, int64_t w, int64_t 
     }
 }
 
-// E, E2: the products' epilogues (E2 void: one product).  E::Params is its arguments; an object of E is made for
-// each tile and thread by E(params, shape, row, first column, columns, item,
-// which half of the tile's columns, 32 x 33 floats of shared memory of the warp's own), gets the
-// sums of its row by chunk(params, shape, column, number of the chunk, values,
-// those floats) and ends with end(params, shape); E::kUnroll chunks are
-// unrolled.
+// E, E2: the products' epilogues (E2 void: one product).  E::Params is its
+// arguments.  An object of E is made for each tile and thread by E(params,
+// shape, row, first column, columns, item, which half of the tile's columns, 32 x
+// 33 floats of shared memory of the warp's own); it gets the sums of its row by
+// chunk(params, shape, column, number of the chunk, values, those floats) and
+// ends with end(params, shape).  E::kUnroll chunks are unrolled.
 template <typename E>
 struct ParamsOf {
     using type = typename E::Params;

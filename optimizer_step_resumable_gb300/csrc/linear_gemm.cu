@@ -297,7 +297,8 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
     *p_plan = linear_plan(p, sm_count);
     *q_plan = linear_plan(q, sm_count);
     // tiles of 256 x 256 have to fit both
-    if (p_plan->few || p_plan->swapped || p.rows <= 128 || p.columns <= 128 || q.rows <= 128 || q.columns <= 128)
+    if (p_plan->few || p_plan->swapped || p.rows <= 128 || p.columns <= 128 || q.rows <= 128 ||
+        q.columns <= 128)
         return false;
     const int64_t pairs = sm_count / 2, blocks[] = {inner_blocks(p.inner), inner_blocks(q.inner)};
     const int64_t tiles[] = {tiles_of(p.rows, p.columns, 256), tiles_of(q.rows, q.columns, 256)};

@@ -234,7 +234,8 @@ struct StoreEpilogue {
                     z += 8 * z_step;
                 }
                 if (!kPlain && o.act != LINEAR_NONE)
-                    with_activation(o.act, [&](auto act) { activate_all<decltype(act)::value>(f); });
+                    with_activation(o.act,
+                                    [&](auto act) { activate_all<decltype(act)::value>(f); });
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (r + i < left)

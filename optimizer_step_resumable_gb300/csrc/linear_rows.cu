@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(kSlopeThreads, 4)
     const int count = left <= 0 ? 0 : int(left >= 8 * step ? 8 : (left + step - 1) / step);
     const int64_t first = a.rows * strip / a.strips;
     const int64_t last = a.rows * (strip + 1) / a.strips;
-    const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + (first + group) * a.dy_stride + column;
+    const uint16_t* dy =
+        static_cast<const uint16_t*>(a.dy) + (first + group) * a.dy_stride + column;
     const uint16_t* z = static_cast<const uint16_t*>(a.z) + (first + group) * a.z_stride + column;
     uint16_t* dz = static_cast<uint16_t*>(a.dz) + (first + group) * a.stride + column;
     float total[8] = {};

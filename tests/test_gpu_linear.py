@@ -15,7 +15,8 @@ u = 2^-24 (float32); U = 2^-8 or 2^-11, the rounding of the 16-bit types.
 * Each output is rounded once more.
 * Over many elements the roundings are independent, and one of them has the
   root mean square U / sqrt(3) at most: with two of them, 0.82 U of the
-  output's norm; the bound is U, and the norm of the float32 parts' bars.
+  output's norm, of the coarser type's U; the bound is that U, and the norm of
+  the float32 parts' bars.
 """
 import pytest
 
@@ -54,15 +55,16 @@ def matrix(r, rows, cols, kind, pad=0, at=0, sigma=1.0):
     return t.to(TYPES[kind])[at:at + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
 
 
-def near(got, want, bar, name, small=None):
-    """bar: all errors before the last rounding; small: float32's share of them."""
+def near(got, want, bar, name, small=None, factor=0.0):
+    """bar: all errors before the last rounding; small: float32's share of them;
+    factor: U of the other rounding's type."""
     U, tiny = ROUND[got.dtype]
     off = (got.double() - want).abs()
     bad = ~(off <= bar + U * (want.abs() + bar) + tiny)
     assert not bool(bad.any()), (name, int(bad.sum()), bad.nonzero()[:3].tolist(),
                                  got[bad][:3].tolist(), want[bad][:3].tolist())
     if got.numel() >= 4096 and got.dtype is not torch.float32:
-        most = U * want.norm() + (bar if small is None else small).norm()
+        most = max(U, factor) * want.norm() + (bar if small is None else small).norm()
         assert float(off.norm()) <= float(most) + tiny * got.numel() ** 0.5, name
 
 
@@ -116,7 +118,7 @@ def run(rows, cin, cout, kind="bf16", act="none", in_out=False, bias="x", residu
             near(out, dz @ W, rounded @ W.abs() + sums, "dx", dz_bar @ W.abs() + sums)
         want = dz.T @ X + before[0]
         sums = (rows + 64) * 2 * u * (size.T @ X.abs()) + u * want.abs()
-        near(dw, want, rounded.T @ X.abs() + sums, "dweight", dz_bar.T @ X.abs() + sums)
+        near(dw, want, rounded.T @ X.abs() + sums, "dweight", dz_bar.T @ X.abs() + sums, U)
         want = dz.sum(0) + before[1]
         near(db, want, dz_bar.sum(0) + (rows + 64) * u * dz.abs().sum(0) + u * want.abs(), "dbias")
 
@@ -158,6 +160,27 @@ def test_strides_and_addresses(pad, at):
 def test_long_sums(rows, grad):
     run(rows, 256, 264, "bf16", "none", grad=grad, accumulate=grad == "f32")
     run(rows, 96, 40, "f16", "relu", grad=grad, dx=False)
+
+
+# tiles of 192 columns, whose half a block has is no whole number of copies
+@pytest.mark.parametrize("cin,cout", [(72, 768), (200, 760)])
+@pytest.mark.parametrize("in_out", [False, True])
+def test_tiles_of_192_columns(cin, cout, in_out):
+    run(8100, cin, cout, "bf16", "relu", in_out=in_out, residual=True)
+
+
+def test_chains_of_sums():
+    # so many rows, and so many tiles, that one pair of blocks sums a tile of the
+    # weight's gradient in several chains, added up in its place
+    run(13000, 2048, 4100, "bf16", "none", grad="f32", accumulate=True)
+    run(13000, 2049, 4096, "f16", "silu", grad="f32", grad_in_out=True)
+
+
+# gradients of a third type, and few rows whose weight is small or large
+@pytest.mark.parametrize("rows", [2, 3, 7, 8, 9, 300])
+def test_types_and_few_rows(rows):
+    run(rows, 200, 312, "bf16", "gelu", grad="f16", in_out=rows % 2 == 0)
+    run(rows, 2056, 4104, "f16", "none", grad="bf16", in_out=rows % 2 == 1, residual=True)
 
 
 @pytest.mark.parametrize("rows,cin,cout", [(1, 768, 96), (5, 4096, 1000), (130, 640, 384),
