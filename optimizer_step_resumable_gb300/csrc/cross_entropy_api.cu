@@ -313,7 +313,8 @@ int linear_cross_entropy_forward(linear_ce_ctx* ctx, const void* d_x, int64_t x_
     n.in_out = in_out;
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
-                                   lay_out(ctx, rows, n, Pieced{}, d_workspace, &p))))
+                                   lay_out(ctx, rows, n, Pieced{}, d_workspace, &p), outs,
+                                   ins)))
         return rc;
     DeviceScope scope(ctx->base.device);
     int e = copy_readable(copy_of(&d_x, &x_stride, rows, dim, p.x),
@@ -408,7 +409,8 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
     const Pieced& pieced = pieces_of(ctx, rows, n);
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
-                                   lay_out(ctx, rows, n, pieced, d_workspace, &p))))
+                                   lay_out(ctx, rows, n, pieced, d_workspace, &p), outs,
+                                   ins)))
         return rc;
     const bool bf16 = dtype == ADAMW_DTYPE_BF16;
     e = copy_readable(copy_of(&d_x, &x_stride, rows, dim, p.x),

@@ -261,7 +261,8 @@ int linear_forward(linear_ctx* ctx, const void* d_x, int64_t x_stride, const voi
     const Plans& plans = plans_of(ctx, rows, n);
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
-                                   lay_out(ctx, rows, n, plans, d_workspace, &p))))
+                                   lay_out(ctx, rows, n, plans, d_workspace, &p), outs,
+                                   ins)))
         return rc;
     DeviceScope scope(ctx->base.device);
     int e = copy_readable(copy_of(&d_x, &x_stride, rows, in, p.x),
@@ -351,7 +352,8 @@ int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride, const 
     const Plans none, &plans = rows ? plans_of(ctx, rows, n) : none;
     Parts p;
     if ((rc = osr::check_workspace(d_workspace, workspace_bytes,
-                                   lay_out(ctx, rows, n, plans, d_workspace, &p))))
+                                   lay_out(ctx, rows, n, plans, d_workspace, &p), outs,
+                                   ins)))
         return rc;
     const LinearCopy weight_copy = copy_of(&d_weight, &weight_stride, w_rows, w_cols, p.weight);
     const LinearCopy x_copy = copy_of(&d_x, &x_stride, rows, in, p.x);

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "api_util.h"
+#include "arrays.h"
 #include "gemm.h"
 #include "linear.h"
 
@@ -74,7 +75,9 @@ private:
     int64_t used_ = 0;
 };
 
-inline int check_workspace(const void* memory, int64_t bytes, int64_t needed)
+template <int kOut, int kIn>
+int check_workspace(void* memory, int64_t bytes, int64_t needed, const Pieces (&out)[kOut],
+                    const Pieces (&in)[kIn])
 {
     if (needed == 0)
         return ADAMW_OK;
@@ -86,7 +89,9 @@ inline int check_workspace(const void* memory, int64_t bytes, int64_t needed)
     if (bytes < needed)
         return fail(ADAMW_EINVAL, "workspace of %lld bytes: the call needs %lld", (long long)bytes,
                     (long long)needed);
-    return ADAMW_OK;
+    const Pieces all[] = {vector_of(memory, needed, 1, "d_workspace")};
+    const int rc = check_apart(all, in);
+    return rc == ADAMW_OK ? check_apart(all, out) : rc;
 }
 
 // A row's elements in whole 16-byte vectors.
