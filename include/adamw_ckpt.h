@@ -830,7 +830,8 @@ ADAMW_API int layernorm_backward(layernorm_ctx* ctx, const void* d_dy, int64_t d
  * once.  dz is a factor of two products, so it is rounded to dy's type if
  * there is an activation; dbias sums the unrounded values.  The tensor cores
  * cut their float32 sums instead of rounding them: a float32 dweight is off by
- * up to about 1e-9 of its value for each row, in chains of 6144 rows.
+ * up to about 1e-9 of its value for each row, in chains of 1024 rows that are
+ * rounded as they are added (those from the second on with subnormal sums as 0).
  *
  * linear_create: 1 <= in, out <= 2^24, in x out < 2^40; nothing on the
  *   device but a pinned word.  Calls with one context may run at the same

@@ -206,9 +206,10 @@ int linear_workspace(linear_ctx* ctx, int64_t rows, int32_t flags, int64_t* byte
     // the most that any layout of the weight and its gradient takes
     for (int layout = 0; layout < 4; ++layout) {
         Needs n{back, any, any, back, (layout & 1) != 0, back, back, back, (layout & 2) != 0};
-        // dx and dweight in one launch, or each on its own
-        for (int apart = 0; apart < (back ? 2 : 1); ++apart) {
-            n.grad_mixed = apart != 0;
+        // dx and dweight in one launch, or each on its own; dweight in 16 bits or 32
+        for (int form = 0; form < (back ? 4 : 1); ++form) {
+            n.grad_mixed = (form & 1) != 0;
+            n.grad_f32 = (form & 2) != 0;
             Parts p;
             const int64_t b = lay_out(ctx, rows, n, make_plans(ctx, rows, n), nullptr, &p);
             *bytes = *bytes > b ? *bytes : b;

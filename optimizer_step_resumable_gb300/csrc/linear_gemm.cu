@@ -141,11 +141,16 @@ int64_t tiles_of(int64_t m, int64_t n, int bn)
 
 // The tensor cores cut each addition, by up to 2^-24 of the sum: 16384
 // products in a row lose 2e-5 of it, which shows in float32 and not in 16
-// bits.  Chains of at most 96 blocks, 6144 products, lose 7e-6.
+// bits.  Chains of at most 16 blocks, 1024 products, lose 1.2e-6, and between
+// them the sums are rounded (random values, 8192 products: 1.0e-6 off in the
+// 2-norm, 4.4e-6 in chains of 4096).  Each is added in L2: 8192 x 4096 x 8192 into
+// float32 takes 378 us, 328 in chains of 4096 and 431 in chains of 1365 that the
+// threads read, add to and write back.
+int64_t chains_of(int64_t blocks, bool f32) { return f32 ? (blocks + 15) / 16 : 1; }
 void finish_plan(const LinearSize& p, LinearPlan* plan)
 {
     const int64_t each = (inner_blocks(p.inner) + plan->splits - 1) / plan->splits;
-    plan->chains = p.f32 ? int32_t((each + 95) / 96) : 1;
+    plan->chains = int32_t(chains_of(each, p.f32));
     plan->partials =
         plan->splits > 1 ? plan->splits * p.rows * ((p.columns + 7) / 8 * 8) : 0;
 }
@@ -191,10 +196,12 @@ double deal_out(int64_t n, double long_us, int64_t m, double short_us, int64_t p
                          int32_t(before)};
     return best;
 }
-// Of a tile of 256 x 256, with what its start and end hold up.
-double item_us(int64_t blocks, int64_t splits)
+// Of a tile of 256 x 256, with what its start and end hold up, and each chain
+// after the first.
+double item_us(int64_t blocks, int64_t splits, bool f32)
 {
-    return double((blocks + splits - 1) / splits) * block_us(256) + 0.3;
+    const int64_t each = (blocks + splits - 1) / splits;
+    return double(each) * block_us(256) + 0.3 + 1.3 * double(chains_of(each, f32) - 1);
 }
 
 StoreProduct store_product(const LinearProduct& p, const LinearPlan& plan, float* partials,
@@ -263,7 +270,9 @@ LinearPlan linear_plan(const LinearSize& p, int sm_count)
         const int64_t tiles = tiles_of(m, n, bn);
         for (int64_t s = 1; s <= 32 && s <= (blocks + 3) / 4; ++s) {
             const double turns = double((tiles * s + pairs - 1) / pairs);
-            const double us = turns * double((blocks + s - 1) / s) * block_us(bn) +
+            const int64_t each = (blocks + s - 1) / s;
+            const double us = turns * (double(each) * block_us(bn) +
+                                       1.3 * double(chains_of(each, p.f32) - 1)) +
                               launch_us(bn) + join_us(m * n, s);
             if (best.bn == 0 || us < least_us) {
                 least_us = us;
@@ -282,11 +291,11 @@ LinearPlan linear_plan(const LinearSize& p, int sm_count)
 double linear_us(const LinearSize& p, const LinearSize* q, int sm_count)
 {
     const int64_t pairs = sm_count / 2, n = tiles_of(p.rows, p.columns, 256);
-    const double a = item_us(inner_blocks(p.inner), 1);
+    const double a = item_us(inner_blocks(p.inner), 1, p.f32);
     if (!q)
         return launch_us(256) + deal_out(n, a, 0, a, pairs, nullptr);
     const int64_t m = tiles_of(q->rows, q->columns, 256);
-    const double b = item_us(inner_blocks(q->inner), 1);
+    const double b = item_us(inner_blocks(q->inner), 1, q->f32);
     return launch_us(256) + (a >= b ? deal_out(n, a, m, b, pairs, nullptr)
                                     : deal_out(m, b, n, a, pairs, nullptr));
 }
@@ -303,7 +312,7 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
     const int64_t pairs = sm_count / 2, blocks[] = {inner_blocks(p.inner), inner_blocks(q.inner)};
     const int64_t tiles[] = {tiles_of(p.rows, p.columns, 256), tiles_of(q.rows, q.columns, 256)};
     const int64_t sizes[] = {p.rows * p.columns, q.rows * q.columns};
-    static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24};
+    static const int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 12, 16, 24};
     int best[2] = {1, 1};
     double least_us = 0.0;
     for (const int s : kSplits) {
@@ -312,7 +321,7 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
         for (const int t : kSplits) {
             if (t > 1 && (t > (blocks[1] + 3) / 4 || tiles[1] * (t - 1) >= 4 * pairs))
                 break;
-            const double a = item_us(blocks[0], s), b = item_us(blocks[1], t);
+            const double a = item_us(blocks[0], s, p.f32), b = item_us(blocks[1], t, q.f32);
             const int64_t n = tiles[0] * s, m = tiles[1] * t;
             const double us = (a >= b ? deal_out(n, a, m, b, pairs, nullptr)
                                       : deal_out(m, b, n, a, pairs, nullptr)) +
@@ -367,8 +376,10 @@ int linear_product_two(const LinearProduct& p, const LinearPlan& p_plan, float* 
     StoreProduct a = store_product(p, p_plan, p_partials, gave_up);
     StoreProduct b = store_product(q, q_plan, q_partials, gave_up);
     // the longer items first
-    const double a_us = item_us(inner_blocks(p.a.inner), p_plan.splits);
-    const double b_us = item_us(inner_blocks(q.a.inner), q_plan.splits);
+    const double a_us =
+        item_us(inner_blocks(p.a.inner), p_plan.splits, p.to.dtype == ADAMW_DTYPE_F32);
+    const double b_us =
+        item_us(inner_blocks(q.a.inner), q_plan.splits, q.to.dtype == ADAMW_DTYPE_F32);
     const int64_t a_items = tiles_of(p.a.outer, p.b.outer, 256) * p_plan.splits;
     const int64_t b_items = tiles_of(q.a.outer, q.b.outer, 256) * q_plan.splits;
     const int64_t items = a_items + b_items, most = sm_count / 2;

@@ -50,9 +50,10 @@ __device__ __forceinline__ float get(const char* p)
 // The tile's rows are the product's: a thread has a row's neighbouring
 // columns, 32 at a time.  Rows on 32-byte boundaries go out from each thread,
 // whole sectors at a time, and what is added to them comes in the same way,
-// two chunks ahead (one, if it is float32).  Others go through shared memory,
-// so that a warp's lanes have neighbouring columns of one row, eight rows at a
-// time.
+// two chunks ahead (one, if it is float32).  Rows of float32 go out four at a time
+// instead, 128 bytes of each, through shared memory: a later chain's sums are
+// added to them in L2.  Rows on other boundaries go through shared memory, so
+// that a warp's lanes have neighbouring columns of one row, eight rows at a time.
 // kPlain: neither bias nor activation nor z.
 template <int kOut, bool kPlain>
 struct StoreEpilogue {
@@ -62,7 +63,7 @@ struct StoreEpilogue {
 
     int32_t row, end_column;  // of the columns that are this thread's
     float alpha;
-    bool vectors, add, add_f32, bias;
+    bool vectors, again, add, add_f32, bias;
     char* out;        // the row
     const char* from;  // what is added to it
     float lane_bias[4];  // of the chunks, for the lane's column
@@ -79,7 +80,7 @@ struct StoreEpilogue {
         out = static_cast<char*>(o.out) +
               (it.split * p.split_stride + int64_t(r) * o.stride) * kSize<kOut>;
         // a later chain adds to what the one before it left there
-        const bool again = kF32 && it.chain > 0;
+        again = kF32 && it.chain > 0;
         add = again || o.residual;
         add_f32 = again || o.residual_dtype == ADAMW_DTYPE_F32;
         from = again ? out
@@ -100,7 +101,10 @@ struct StoreEpilogue {
                 __syncwarp();
             }
         }
-        if (add && vectors) {
+        if (kF32) {
+            if (add && !again && vectors)
+                fetch_strip(p, column);
+        } else if (add && vectors) {
             fetch(p, column, 0);
             if (!add_f32)
                 fetch(p, column + 32, 1);
@@ -123,6 +127,64 @@ struct StoreEpilogue {
                 load32(from + (int64_t(column) + 16 * i) * 2,
                        *reinterpret_cast<uint32_t(*)[8]>(ahead + 16 * slot + 8 * i));
         }
+    }
+    // float32, in the strip's order: a lane has four neighbouring columns of every
+    // fourth row, from row lane / 8 of the warp's.
+    __device__ __forceinline__ void fetch_strip(const Params& p, int32_t column)
+    {
+        if (column + 32 > end_column)
+            return;
+        const int32_t lane = threadIdx.x % 32, r = row - lane + lane / 8;
+        const int64_t step = p.o.residual_stride * 4;
+        const char* at = from + (lane / 8 - lane) * step + (int64_t(column) + 4 * (lane % 8)) * 4;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+            if (r + i < p.rows) {
+                const uint4 w = *reinterpret_cast<const uint4*>(at + i * step);
+                ahead[i] = w.x, ahead[i + 1] = w.y, ahead[i + 2] = w.z, ahead[i + 3] = w.w;
+            }
+    }
+    __device__ __forceinline__ void store_strip(const Params& p, int32_t column,
+                                                const float (&v)[32], uint4* strip)
+    {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            strip_put(strip, i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                           __float_as_uint(v[4 * i + 2]),
+                                           __float_as_uint(v[4 * i + 3])));
+        __syncwarp();
+        const int32_t lane = threadIdx.x % 32, piece = lane % 8, first = row - lane;
+        const int64_t step = p.o.stride * 4;
+        char* to = out - lane * step + (int64_t(column) + 4 * piece) * 4;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const int32_t r = i + lane / 8;
+            const uint4 w = strip[8 * r + (piece ^ (r & 7))];
+            float4 f = make_float4(__uint_as_float(w.x), __uint_as_float(w.y),
+                                   __uint_as_float(w.z), __uint_as_float(w.w));
+            if (first + r >= p.rows)
+                continue;
+            if (again) {
+                add_to(to + r * step, f);
+                continue;
+            }
+            if (add) {
+                f.x += __uint_as_float(ahead[i]), f.y += __uint_as_float(ahead[i + 1]);
+                f.z += __uint_as_float(ahead[i + 2]), f.w += __uint_as_float(ahead[i + 3]);
+            }
+            *reinterpret_cast<float4*>(to + r * step) = f;
+        }
+        if (add && !again)
+            fetch_strip(p, column + 32);
+    }
+    // Adds where the values lie: nothing comes back.  A place belongs to one
+    // thread in every chain of its tile, so the order is the chains'.
+    __device__ static __forceinline__ void add_to(char* p, float4 f)
+    {
+        asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(f.x),
+                     "f"(f.y), "f"(f.z), "f"(f.w)
+                     : "memory");
     }
     __device__ static __forceinline__ void store(char* to, const float (&v)[32])
     {
@@ -157,6 +219,10 @@ struct StoreEpilogue {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 v[i] *= alpha;
+        if (kF32 && vectors && column + 32 <= p.columns) {
+            store_strip(p, column, v, reinterpret_cast<uint4*>(stage));
+            return;
+        }
         if (vectors && column + 32 <= p.columns) {
             if (!kPlain && bias)
 #pragma unroll
