@@ -176,6 +176,27 @@ def test_chains_of_sums():
     run(13000, 2049, 4096, "f16", "silu", grad="f32", grad_in_out=True)
 
 
+def test_long_chains_lose_little_of_a_sum_of_equal_signs():
+    # 1024 products are 64 steps of 16; each cuts the sum so far by less than a unit
+    # of its last place, 2^-23 of it, and the sum so far is half of the last one in
+    # the mean: 64 x 2^-24, then 13 roundings of the chains' sums
+    rows, cin, cout = 13000, 2056, 4104
+    r = torch.Generator(device="cuda").manual_seed(5)
+    x = (torch.rand(rows, cin, device="cuda", generator=r) + 0.5).bfloat16()
+    dy = (torch.rand(rows, cout, device="cuda", generator=r) + 0.5).bfloat16()
+    w = torch.zeros(cout, cin, device="cuda", dtype=torch.bfloat16)
+    lin = osr.linear_create(cin, cout)
+    want = dy.double().T @ x.double()
+    first = None
+    for _ in range(2):
+        dw = torch.zeros(cout, cin, device="cuda")
+        osr.linear_backward(lin, dy, x, w, dx=False, dweight=dw, accumulate=True)
+        off = ((dw.double() - want).abs() / want).max().item()
+        assert off < 64 * 2.0 ** -24 + 13 * 2.0 ** -24, off
+        assert first is None or torch.equal(first, dw)
+        first = dw
+
+
 # gradients of a third type, and few rows whose weight is small or large
 @pytest.mark.parametrize("rows", [2, 3, 7, 8, 9, 300])
 def test_types_and_few_rows(rows):
