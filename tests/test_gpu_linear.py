@@ -197,6 +197,13 @@ def test_long_chains_lose_little_of_a_sum_of_equal_signs():
         first = dw
 
 
+@pytest.mark.parametrize("cin,cout,grad_in_out", [(2048, 100, False), (100, 2048, True),
+                                                  (2050, 33, False)])
+def test_chains_of_sums_of_a_narrow_gradient(cin, cout, grad_in_out):
+    # more chains than parts: the tile's long side along the gradient's columns
+    run(40000, cin, cout, "bf16", "none", grad="f32", grad_in_out=grad_in_out, accumulate=True)
+
+
 # gradients of a third type, and few rows whose weight is small or large
 @pytest.mark.parametrize("rows", [2, 3, 7, 8, 9, 300])
 def test_types_and_few_rows(rows):
