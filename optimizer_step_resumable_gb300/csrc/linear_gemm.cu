@@ -147,10 +147,13 @@ int64_t tiles_of(int64_t m, int64_t n, int bn)
 // float32 takes 378 us, 328 in chains of 4096 and 431 in chains of 1365 that the
 // threads read, add to and write back.
 int64_t chains_of(int64_t blocks, bool f32) { return f32 ? (blocks + 15) / 16 : 1; }
+int64_t chains_in(const LinearSize& p, int64_t splits)
+{
+    return chains_of((inner_blocks(p.inner) + splits - 1) / splits, p.f32);
+}
 void finish_plan(const LinearSize& p, LinearPlan* plan)
 {
-    const int64_t each = (inner_blocks(p.inner) + plan->splits - 1) / plan->splits;
-    plan->chains = int32_t(chains_of(each, p.f32));
+    plan->chains = int32_t(chains_in(p, plan->splits));
     plan->partials =
         plan->splits > 1 ? plan->splits * p.rows * ((p.columns + 7) / 8 * 8) : 0;
 }
@@ -198,10 +201,10 @@ double deal_out(int64_t n, double long_us, int64_t m, double short_us, int64_t p
 }
 // Of a tile of 256 x 256, with what its start and end hold up, and each chain
 // after the first.
-double item_us(int64_t blocks, int64_t splits, bool f32)
+double item_us(int64_t blocks, int64_t splits, int64_t chains)
 {
     const int64_t each = (blocks + splits - 1) / splits;
-    return double(each) * block_us(256) + 0.3 + 1.3 * double(chains_of(each, f32) - 1);
+    return double(each) * block_us(256) + 0.3 + 1.3 * double(chains - 1);
 }
 
 StoreProduct store_product(const LinearProduct& p, const LinearPlan& plan, float* partials,
@@ -272,7 +275,7 @@ LinearPlan linear_plan(const LinearSize& p, int sm_count)
             const double turns = double((tiles * s + pairs - 1) / pairs);
             const int64_t each = (blocks + s - 1) / s;
             const double us = turns * (double(each) * block_us(bn) +
-                                       1.3 * double(chains_of(each, p.f32) - 1)) +
+                                       1.3 * double(chains_in(p, s) - 1)) +
                               launch_us(bn) + join_us(m * n, s);
             if (best.bn == 0 || us < least_us) {
                 least_us = us;
@@ -291,11 +294,11 @@ LinearPlan linear_plan(const LinearSize& p, int sm_count)
 double linear_us(const LinearSize& p, const LinearSize* q, int sm_count)
 {
     const int64_t pairs = sm_count / 2, n = tiles_of(p.rows, p.columns, 256);
-    const double a = item_us(inner_blocks(p.inner), 1, p.f32);
+    const double a = item_us(inner_blocks(p.inner), 1, chains_in(p, 1));
     if (!q)
         return launch_us(256) + deal_out(n, a, 0, a, pairs, nullptr);
     const int64_t m = tiles_of(q->rows, q->columns, 256);
-    const double b = item_us(inner_blocks(q->inner), 1, q->f32);
+    const double b = item_us(inner_blocks(q->inner), 1, chains_in(*q, 1));
     return launch_us(256) + (a >= b ? deal_out(n, a, m, b, pairs, nullptr)
                                     : deal_out(m, b, n, a, pairs, nullptr));
 }
@@ -321,7 +324,8 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
         for (const int t : kSplits) {
             if (t > 1 && (t > (blocks[1] + 3) / 4 || tiles[1] * (t - 1) >= 4 * pairs))
                 break;
-            const double a = item_us(blocks[0], s, p.f32), b = item_us(blocks[1], t, q.f32);
+            const double a = item_us(blocks[0], s, chains_in(p, s));
+            const double b = item_us(blocks[1], t, chains_in(q, t));
             const int64_t n = tiles[0] * s, m = tiles[1] * t;
             const double us = (a >= b ? deal_out(n, a, m, b, pairs, nullptr)
                                       : deal_out(m, b, n, a, pairs, nullptr)) +
@@ -375,11 +379,12 @@ int linear_product_two(const LinearProduct& p, const LinearPlan& p_plan, float* 
 {
     StoreProduct a = store_product(p, p_plan, p_partials, gave_up);
     StoreProduct b = store_product(q, q_plan, q_partials, gave_up);
-    // the longer items first
-    const double a_us =
-        item_us(inner_blocks(p.a.inner), p_plan.splits, p.to.dtype == ADAMW_DTYPE_F32);
-    const double b_us =
-        item_us(inner_blocks(q.a.inner), q_plan.splits, q.to.dtype == ADAMW_DTYPE_F32);
+    // the longer items first; an item has the chains of its plan, whatever the type
+    // that its sums leave in (by the type, a piece's dx in float32 counted chains that
+    // it does not have: 8192 x 768 and 32000 words into a float32 dweight ended at 281
+    // us of the model's, where its plan ends at 262)
+    const double a_us = item_us(inner_blocks(p.a.inner), p_plan.splits, p_plan.chains);
+    const double b_us = item_us(inner_blocks(q.a.inner), q_plan.splits, q_plan.chains);
     const int64_t a_items = tiles_of(p.a.outer, p.b.outer, 256) * p_plan.splits;
     const int64_t b_items = tiles_of(q.a.outer, q.b.outer, 256) * q_plan.splits;
     const int64_t items = a_items + b_items, most = sm_count / 2;

@@ -1,0 +1,140 @@
+"""How the tiled products are divided and dealt out, read from the arguments of
+their launches on a runtime that runs nothing (tests/c_abi/fake_products.cpp)."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+import optimizer_step_resumable_gb300 as osr
+from optimizer_step_resumable_gb300 import build as lib_build
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+F32, BF16, F16 = osr.DTYPE_F32, osr.DTYPE_BF16, osr.DTYPE_F16
+WORK = 20 << 40
+
+
+def place(k):
+    """A made-up address, apart from the others."""
+    return k << 40
+
+
+@pytest.fixture(scope="module")
+def fake(lib, tmp_path_factory):
+    """The library's own objects, linked with the fake runtime, driver and launches."""
+    out = tmp_path_factory.mktemp("fake")
+    names = lib_build.CUDA_SOURCES + lib_build.CXX_SOURCES
+    objects = [os.path.join(lib_build.BUILD_DIR, s + ".o") for s in names]
+    if not all(os.path.exists(o) for o in objects):
+        lib_build.build(force=True)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(lib_build.nvcc())), "include")
+    fakes = []
+    for name, more in (("fake_cudart", ["-DcudaLaunchKernelExC=fake_launch"]), ("fake_driver", []),
+                       ("fake_products", [])):
+        fakes.append(str(out / (name + ".o")))
+        subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-I", cuda, *more, "-c",
+                        os.path.join(HERE, "c_abi", name + ".cpp"), "-o", fakes[-1]], check=True)
+
+    def symbols(flag, files):
+        text = subprocess.run(["nm", flag, *files], capture_output=True, text=True, check=True).stdout
+        return {line.split()[-1] for line in text.splitlines() if "cuda" in line}
+
+    missing = symbols("--undefined-only", objects) - symbols("--defined-only", fakes)
+    missing = sorted(s for s in missing if s.lstrip("_").startswith("cuda"))
+    rest = out / "rest.c"
+    rest.write_text("".join(f"long {s}(void) {{ return 0; }}\n" for s in missing))
+    subprocess.run(["gcc", "-fno-builtin", "-fPIC", "-c", str(rest), "-o", str(out / "rest.o")],
+                   check=True)
+    path = str(out / "libfake.so")
+    subprocess.run(["g++", "-shared", "-Wl,-Bsymbolic", "-o", path, *objects, *fakes,
+                    str(out / "rest.o"), "-ldl", "-lpthread"], check=True)
+    f = ctypes.CDLL(path)
+    for name, (res, args) in osr.SIGNATURES.items():
+        getattr(f, name).restype = res
+        getattr(f, name).argtypes = args
+    f.fake_product.restype = ctypes.POINTER(ctypes.c_int)
+    return f
+
+
+SHAPE = ("m", "n", "tiles_m", "tiles_n", "splits", "chains", "blocks")
+DEAL = ("pairs", "longs", "ahead", "shorts", "after", "before")
+
+
+def launches(f, call):
+    """The products of a call: (first's shape, second's or None, the deal)."""
+    f.fake_products_clear()
+    assert call() == osr.OK, f.adamw_last_error()
+    out = []
+    for i in range(f.fake_products()):
+        p = f.fake_product(i)
+        one, two = (dict(zip(SHAPE, p[7 * k:7 * k + 7])) for k in (0, 1))
+        out.append((one, two if two["blocks"] else None, dict(zip(DEAL, p[14:20]))))
+    return out
+
+
+def create(f, kind, *sizes):
+    h = ctypes.c_void_p()
+    assert getattr(f, kind + "_create")(*sizes, ctypes.byref(h)) == osr.OK
+    return h
+
+
+def ce_backward(f, dim, vocab, rows, dtype, grad, flags=0, dx=True, dw=True):
+    ce = create(f, "linear_cross_entropy", dim, vocab)
+    n = ctypes.c_int64()
+    assert f.linear_cross_entropy_workspace(ce, rows, osr.LINEAR_FOR_BACKWARD,
+                                            ctypes.byref(n)) == osr.OK
+    got = launches(f, lambda: f.linear_cross_entropy_backward(
+        ce, place(1), dim, place(2), dim, dtype, place(3), place(5), None, 1.0, 0.0,
+        place(6) if dx else None, dim, place(8) if dw else None, dim, grad, rows, flags, WORK,
+        n.value, None))
+    f.linear_cross_entropy_destroy(ce)
+    return got
+
+
+def backward(f, cin, cout, rows, dtype, grad, flags=0, dx=True, dw=True):
+    lin = create(f, "linear", cin, cout)
+    n = ctypes.c_int64()
+    assert f.linear_workspace(lin, rows, osr.LINEAR_FOR_BACKWARD, ctypes.byref(n)) == osr.OK
+    got = launches(f, lambda: f.linear_backward(
+        lin, place(1), cout, place(2), cin, place(3), cin, dtype, None, 0, 0,
+        place(6) if dx else None, cin, place(8) if dw else None, cin, None, grad, rows, flags,
+        WORK, n.value, None))
+    f.linear_destroy(lin)
+    return got
+
+
+# Microseconds that an item takes, as the planner has it: its blocks of the inner
+# dimension, its start and end, and each chain after the first.
+def item_us(shape):
+    each = -(-shape["blocks"] // shape["splits"])
+    return 0.316 * each + 0.3 + 1.3 * (shape["chains"] - 1)
+
+
+def items(shape):
+    return shape["tiles_m"] * shape["tiles_n"] * shape["splits"]
+
+
+def ends(deal, long_us, short_us):
+    """When the last pair of blocks is done."""
+    rounds = deal["longs"] // deal["pairs"]
+    late = (rounds + 1) * long_us + deal["after"] * short_us if deal["ahead"] else 0.0
+    return max(late, rounds * long_us + deal["before"] * short_us)
+
+
+@pytest.mark.parametrize("dim,vocab,rows,grad", [
+    (768, 32000, 8192, F32), (768, 32000, 8192, BF16), (2048, 50000, 16384, F32),
+    (1024, 100000, 4096, F32), (640, 70001, 8192, F32)])
+def test_two_products_are_dealt_out_by_the_time_they_take(fake, dim, vocab, rows, grad):
+    # the pieces of a vocabulary write dx in float32 but for the last one
+    for one, two, deal in ce_backward(fake, dim, vocab, rows, BF16, grad, osr.LINEAR_ACCUMULATE):
+        if two is None:
+            continue
+        long_us, short_us = item_us(one), item_us(two)
+        assert long_us >= short_us
+        assert (deal["longs"], deal["shorts"]) == (items(one), items(two))
+        assert deal["ahead"] == deal["longs"] % deal["pairs"]
+        others, left = deal["pairs"] - deal["ahead"], deal["shorts"]
+        best = min(ends(dict(deal, after=a, before=b), long_us, short_us)
+                   for b in range(-(-left // others) + 1) for a in range(b + 1)
+                   if a * deal["ahead"] + b * others >= left)
+        assert ends(deal, long_us, short_us) <= best + 1e-6, (one, two, deal, best)
