@@ -832,6 +832,9 @@ ADAMW_API int layernorm_backward(layernorm_ctx* ctx, const void* d_dy, int64_t d
  * cut their float32 sums instead of rounding them: a float32 dweight is off by
  * up to about 1e-9 of its value for each row, in chains of 1024 rows that are
  * rounded as they are added (those from the second on with subnormal sums as 0).
+ * 16-bit outputs of more than 2^14 (binary16) or 2^17 products (bfloat16) are
+ * summed in chains of that many, so the cut is less than a quarter of their
+ * rounding at any length.
  *
  * linear_create: 1 <= in, out <= 2^24, in x out < 2^40; nothing on the
  *   device but a pinned word.  Calls with one context may run at the same

@@ -40,9 +40,13 @@ using osr::whole;
 using osr::Workspace;
 
 struct Needs {  // without gaps: compared byte by byte
-    bool backward, copy_x, copy_weight, in_out, dx, dweight, grad_in_out;
+    bool f16, backward, copy_x, copy_weight, in_out, dx, dweight, grad_in_out;
     bool grad_f32, grad_mixed;  // neither float32 nor the other matrices' type
 };
+int64_t chain_of(bool f16)
+{
+    return osr::linear_chain(f16 ? ADAMW_DTYPE_F16 : ADAMW_DTYPE_BF16);
+}
 // How the products of a piece of `columns` are computed.
 struct Plans {
     LinearPlan dx{}, dweight{};
@@ -78,13 +82,16 @@ constexpr int64_t kPieceBytes = int64_t(256) << 20;
 
 int64_t tiles(int64_t vocab) { return (vocab + kCeColumns - 1) / kCeColumns; }
 
-Plans make_plans(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Needs& n)
+// last: dx leaves in its own type; before, the sum so far stays in float32.
+Plans make_plans(const linear_ce_ctx* c, int64_t rows, int64_t columns, bool last, const Needs& n)
 {
     Plans p;
     const int sms = c->base.sm_count;
-    const LinearSize dx{rows, c->dim, columns, false, !n.in_out, false};
+    const LinearSize dx{rows, c->dim, columns, false, !n.in_out, !last, chain_of(n.f16)};
     const LinearSize dw{n.grad_in_out ? c->dim : columns, n.grad_in_out ? columns : c->dim, rows,
-                        true, true, n.grad_f32};
+                        true, true, n.grad_f32,
+                        n.grad_f32 ? osr::linear_chain(ADAMW_DTYPE_F32)
+                                   : chain_of(n.f16 != n.grad_mixed)};
     if (n.dx && n.dweight && !n.grad_mixed) {
         p.together = osr::linear_plan_two(dx, dw, sms, &p.dx, &p.dweight);
     } else {
@@ -96,12 +103,13 @@ Plans make_plans(const linear_ce_ctx* c, int64_t rows, int64_t columns, const Ne
     return p;
 }
 
-// The time of a piece, as far as it depends on the division.
+// The time of a piece, as far as it depends on the division, the same for all types.
 double piece_us(const linear_ce_ctx* c, int64_t rows, int64_t columns)
 {
-    const LinearSize logits{rows, columns, c->dim, false, false, false};
-    const LinearSize dx{rows, c->dim, columns, false, true, false};
-    const LinearSize dw{columns, c->dim, rows, true, true, false};
+    const int64_t chain = osr::linear_chain(ADAMW_DTYPE_BF16);
+    const LinearSize logits{rows, columns, c->dim, false, false, false, chain};
+    const LinearSize dx{rows, c->dim, columns, false, true, false, chain};
+    const LinearSize dw{columns, c->dim, rows, true, true, false, chain};
     return osr::linear_us(logits, nullptr, c->base.sm_count) +
            osr::linear_us(dx, &dw, c->base.sm_count);
 }
@@ -140,8 +148,8 @@ Pieced make_pieces(linear_ce_ctx* c, int64_t rows, const Needs& n)
     Pieced p;
     p.columns = piece_of(c, rows);
     const int64_t end = c->vocab - (c->vocab - 1) / p.columns * p.columns;
-    p.last = make_plans(c, rows, end, n);
-    p.plans = c->vocab > p.columns ? make_plans(c, rows, p.columns, n) : p.last;
+    p.last = make_plans(c, rows, end, true, n);
+    p.plans = c->vocab > p.columns ? make_plans(c, rows, p.columns, false, n) : p.last;
     return p;
 }
 const Pieced& pieces_of(linear_ce_ctx* c, int64_t rows, const Needs& n)
@@ -262,11 +270,14 @@ int linear_cross_entropy_workspace(linear_ce_ctx* ctx, int64_t rows, int32_t fla
     const bool back = flags & LINEAR_FOR_BACKWARD, any = flags & LINEAR_FOR_ANY_ADDRESS;
     // the most that any layout of the weight and its gradient takes
     for (int layout = 0; layout < 4; ++layout) {
-        Needs n{back, any, any, (layout & 1) != 0, back, back, (layout & 2) != 0};
-        // dx and dweight in one launch, or each on its own; dweight in 16 bits or 32
-        for (int form = 0; form < (back ? 4 : 1); ++form) {
+        Needs n{false, back, any, any, (layout & 1) != 0, back, back, (layout & 2) != 0};
+        // dx and dweight in one launch, or each on its own; dweight in 16 bits or 32;
+        // either 16-bit type, where they differ
+        const int forms = !back ? 1 : osr::linear_long(rows, ctx->vocab, 0) ? 8 : 4;
+        for (int form = 0; form < forms; ++form) {
             n.grad_mixed = (form & 1) != 0;
             n.grad_f32 = (form & 2) != 0;
+            n.f16 = (form & 4) != 0;
             Parts p;
             const int64_t b = lay_out(ctx, rows, n, back ? make_pieces(ctx, rows, n) : Pieced{},
                                       nullptr, &p);
@@ -398,6 +409,7 @@ int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x, int64_t x
     if (!d_dx && !d_dweight)
         return ADAMW_OK;
     Needs n{};
+    n.f16 = dtype == ADAMW_DTYPE_F16;
     n.backward = true;
     n.copy_x = !gemm_readable(d_x, rows > 1 ? x_stride : 0);
     n.copy_weight = !gemm_readable(d_weight, w_rows > 1 ? weight_stride : 0);

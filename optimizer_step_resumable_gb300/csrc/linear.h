@@ -43,20 +43,37 @@ inline void accumulate_into(LinearOut& o)
 }
 
 // How it is computed: in tiles of 256 x bn with the inner dimension in
-// `splits` ranges whose sums a second kernel joins, each in `chains` (see
-// GemmShape); swapped: the tile's long side lies along the columns, for
+// `splits` ranges, each in `chains` (see GemmShape), and the sums joined by a
+// second kernel if there are `partials`; swapped: the tile's long side lies along the columns, for
 // products of few rows.
 struct LinearPlan {
     bool few;  // not in tiles at all (linear_few.cu)
     bool swapped;
     int32_t bn, splits, chains;
-    int64_t partials;  // float32 sums in the workspace
+    int64_t partials;  // float32 sums in the workspace; 0: they go out as they are
 };
+// How many blocks of the inner dimension (kGemmInner products each) the tensor
+// cores may sum in one go for an output of the type.  They cut instead of rounding:
+// a sum of equal signs loses 1.7 x 2^-24 of itself for each 16 products of binary16
+// (measured from 4096 to 32768 products; of bfloat16, whose products have fewer bits,
+// 0.8 to 1.5).  So 2^14 products lose 1.0e-4, 0.21 of binary16's rounding, 2^17
+// at most 8.3e-4, 0.21 of bfloat16's, and 1024 at most 6.5e-6.
+inline int64_t linear_chain(int32_t dtype)
+{
+    return dtype == ADAMW_DTYPE_F32 ? 16 : dtype == ADAMW_DTYPE_BF16 ? 2048 : 256;
+}
+// Whether a sum over one of these may need chains for a 16-bit output.
+inline bool linear_long(int64_t a, int64_t b, int64_t c)
+{
+    const int64_t most = linear_chain(ADAMW_DTYPE_F16) * kGemmInner;
+    return a > most || b > most || c > most;
+}
 // *_across: whether the operand's outer dimension is the adjacent one; f32: out
-// is float32.
+// is float32; chain: linear_chain of the type that the sum is rounded to in the end.
 struct LinearSize {
     int64_t rows, columns, inner;
     bool a_across, b_across, f32;
+    int64_t chain;
 };
 LinearPlan linear_plan(const LinearSize& p, int sm_count);
 // Plans of two products that do not depend on one another; true if they go in

@@ -24,6 +24,7 @@ using osr::fail;
 using osr::gemm_readable;
 using osr::GemmOperand;
 using osr::known_dtype;
+using osr::linear_chain;
 using osr::LinearCopy;
 using osr::LinearPlan;
 using osr::LinearProduct;
@@ -37,7 +38,7 @@ using osr::whole;
 using osr::Workspace;
 
 struct Needs {  // without gaps: compared byte by byte
-    bool backward, copy_x, copy_weight, dz;
+    bool f16, backward, copy_x, copy_weight, dz;
     bool in_out;  // the weight, for its copy
     bool dx, dweight, dbias;
     bool grad_in_out, grad_f32, grad_mixed;  // neither float32 nor the other matrices' type
@@ -66,17 +67,21 @@ namespace {
 constexpr int32_t kMaxFeatures = 1 << 24;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 
+int64_t chain_of(bool f16) { return linear_chain(f16 ? ADAMW_DTYPE_F16 : ADAMW_DTYPE_BF16); }
+
 Plans make_plans(const linear_ctx* c, int64_t rows, const Needs& n)
 {
     Plans p;
     const int sms = c->base.sm_count;
     if (!n.backward) {
-        p.forward = osr::linear_plan(LinearSize{rows, c->out, c->in, false, n.in_out, false}, sms);
+        p.forward = osr::linear_plan(
+            LinearSize{rows, c->out, c->in, false, n.in_out, false, chain_of(n.f16)}, sms);
         return p;
     }
-    const LinearSize dx{rows, c->in, c->out, false, !n.in_out, false};
+    const LinearSize dx{rows, c->in, c->out, false, !n.in_out, false, chain_of(n.f16)};
     const LinearSize dw{n.grad_in_out ? c->in : c->out, n.grad_in_out ? c->out : c->in, rows, true,
-                        true, n.grad_f32};
+                        true, n.grad_f32,
+                        n.grad_f32 ? linear_chain(ADAMW_DTYPE_F32) : chain_of(n.f16 != n.grad_mixed)};
     if (n.dx && n.dweight && !n.grad_mixed) {
         p.together = osr::linear_plan_two(dx, dw, sms, &p.dx, &p.dweight);
     } else {
@@ -205,11 +210,15 @@ int linear_workspace(linear_ctx* ctx, int64_t rows, int32_t flags, int64_t* byte
     const bool back = flags & LINEAR_FOR_BACKWARD, any = flags & LINEAR_FOR_ANY_ADDRESS;
     // the most that any layout of the weight and its gradient takes
     for (int layout = 0; layout < 4; ++layout) {
-        Needs n{back, any, any, back, (layout & 1) != 0, back, back, back, (layout & 2) != 0};
-        // dx and dweight in one launch, or each on its own; dweight in 16 bits or 32
-        for (int form = 0; form < (back ? 4 : 1); ++form) {
+        Needs n{false, back, any, any, back, (layout & 1) != 0, back, back, back, (layout & 2) != 0};
+        // dx and dweight in one launch, or each on its own; dweight in 16 bits or 32;
+        // either 16-bit type, where they differ
+        for (int form = 0; form < (osr::linear_long(rows, ctx->in, ctx->out) ? 8 : 4); ++form) {
             n.grad_mixed = (form & 1) != 0;
             n.grad_f32 = (form & 2) != 0;
+            n.f16 = (form & 4) != 0;
+            if (!back && (n.grad_mixed || n.grad_f32))
+                continue;
             Parts p;
             const int64_t b = lay_out(ctx, rows, n, make_plans(ctx, rows, n), nullptr, &p);
             *bytes = *bytes > b ? *bytes : b;
@@ -256,6 +265,7 @@ int linear_forward(linear_ctx* ctx, const void* d_x, int64_t x_stride, const voi
     if (rows == 0)
         return ADAMW_OK;
     Needs n{};
+    n.f16 = dtype == ADAMW_DTYPE_F16;
     n.copy_x = !gemm_readable(d_x, rows > 1 ? x_stride : 0);
     n.copy_weight = !gemm_readable(d_weight, w_rows > 1 ? weight_stride : 0);
     n.in_out = in_out;
@@ -339,6 +349,7 @@ int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stride, const 
     DeviceScope scope(ctx->base.device);
     const int sms = ctx->base.sm_count;
     Needs n{};
+    n.f16 = dtype == ADAMW_DTYPE_F16;
     n.backward = true;
     n.copy_x = x_read && !gemm_readable(d_x, rows > 1 ? x_stride : 0);
     n.copy_weight = w_read && !gemm_readable(d_weight, w_rows > 1 ? weight_stride : 0);

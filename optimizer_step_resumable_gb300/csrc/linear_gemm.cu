@@ -127,12 +127,6 @@ double block_us(int bn)
     return bn == 256 ? 0.316 : bn == 192 ? 0.27 : bn == 128 ? 0.24 : bn == 64 ? 0.2 : 0.18;
 }
 double launch_us(int bn) { return 3.0 + 0.016 * bn; }
-// Sums of a divided inner dimension go to L2 and back, and a launch joins them.
-double join_us(int64_t elements, int64_t splits)
-{
-    return splits > 1 ? 4.0 + double(elements) * double(splits) * 8.0 / 6e6 : 0.0;
-}
-
 int64_t inner_blocks(int64_t inner) { return (inner + kGemmInner - 1) / kGemmInner; }
 int64_t tiles_of(int64_t m, int64_t n, int bn)
 {
@@ -140,22 +134,34 @@ int64_t tiles_of(int64_t m, int64_t n, int bn)
 }
 
 // The tensor cores cut each addition, by up to 2^-24 of the sum: 16384
-// products in a row lose 2e-5 of it, which shows in float32 and not in 16
-// bits.  Chains of at most 16 blocks, 1024 products, lose 1.2e-6, and between
-// them the sums are rounded (random values, 8192 products: 1.0e-6 off in the
-// 2-norm, 4.4e-6 in chains of 4096).  Each is added in L2: 8192 x 4096 x 8192 into
-// float32 takes 378 us, 328 in chains of 4096 and 431 in chains of 1365 that the
-// threads read, add to and write back.
-int64_t chains_of(int64_t blocks, bool f32) { return f32 ? (blocks + 15) / 16 : 1; }
+// products in a row lose 2e-5 of it, which shows in float32.  Chains of at most 16
+// blocks, 1024 products, lose 1.2e-6, and between them the sums are rounded (random
+// values, 8192 products: 1.0e-6 off in the 2-norm, 4.4e-6 in chains of 4096).  Each
+// is added in L2: 8192 x 4096 x 8192 into float32 takes 378 us, 328 in chains of 4096
+// and 431 in chains of 1365 that the threads read, add to and write back.
+// 16-bit outputs have chains as soon as the cut could pass a quarter of their rounding
+// (linear_chain); those add up in float32 in the workspace, and the join rounds them
+// (2^20 rows of equal signs into a binary16 dweight: 5.8e-4 off at most, 8.0e-4 in one
+// go; 65536 x 2048 x 4096 backward 1204 to 1262 us).
 int64_t chains_in(const LinearSize& p, int64_t splits)
 {
-    return chains_of((inner_blocks(p.inner) + splits - 1) / splits, p.f32);
+    const int64_t each = (inner_blocks(p.inner) + splits - 1) / splits;
+    return (each + p.chain - 1) / p.chain;
+}
+// Whether the sums go to L2 and back, for a launch to join.
+bool joined(const LinearSize& p, int64_t splits)
+{
+    return splits > 1 || (!p.f32 && chains_in(p, splits) > 1);
+}
+double join_us(const LinearSize& p, int64_t splits)
+{
+    return joined(p, splits) ? 4.0 + double(p.rows * p.columns) * double(splits) * 8.0 / 6e6 : 0.0;
 }
 void finish_plan(const LinearSize& p, LinearPlan* plan)
 {
     plan->chains = int32_t(chains_in(p, plan->splits));
     plan->partials =
-        plan->splits > 1 ? plan->splits * p.rows * ((p.columns + 7) / 8 * 8) : 0;
+        joined(p, plan->splits) ? plan->splits * p.rows * ((p.columns + 7) / 8 * 8) : 0;
 }
 
 // Deals `n` long items and `m` short ones out to the pairs; the time until all
@@ -214,7 +220,7 @@ StoreProduct store_product(const LinearProduct& p, const LinearPlan& plan, float
     s.s.splits = plan.splits;
     s.s.chains = plan.chains;
     s.s.gave_up = gave_up;
-    if (plan.splits > 1) {
+    if (plan.partials) {
         LinearOut sums{};
         sums.out = partials;
         sums.stride = (p.b.outer + 7) / 8 * 8;
@@ -229,7 +235,7 @@ StoreProduct store_product(const LinearProduct& p, const LinearPlan& plan, float
 int join_product(const LinearProduct& p, const LinearPlan& plan, const float* partials,
                  int sm_count, void* stream)
 {
-    if (plan.splits == 1)
+    if (!plan.partials)
         return cudaSuccess;
     return join(p.to, partials, p.a.outer, p.b.outer, plan.splits, sm_count,
                 static_cast<cudaStream_t>(stream));
@@ -276,7 +282,7 @@ LinearPlan linear_plan(const LinearSize& p, int sm_count)
             const int64_t each = (blocks + s - 1) / s;
             const double us = turns * (double(each) * block_us(bn) +
                                        1.3 * double(chains_in(p, s) - 1)) +
-                              launch_us(bn) + join_us(m * n, s);
+                              launch_us(bn) + join_us(p, s);
             if (best.bn == 0 || us < least_us) {
                 least_us = us;
                 best.bn = bn;
@@ -314,7 +320,6 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
         return false;
     const int64_t pairs = sm_count / 2, blocks[] = {inner_blocks(p.inner), inner_blocks(q.inner)};
     const int64_t tiles[] = {tiles_of(p.rows, p.columns, 256), tiles_of(q.rows, q.columns, 256)};
-    const int64_t sizes[] = {p.rows * p.columns, q.rows * q.columns};
     static const int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 12, 16, 24};
     int best[2] = {1, 1};
     double least_us = 0.0;
@@ -329,7 +334,7 @@ bool linear_plan_two(const LinearSize& p, const LinearSize& q, int sm_count, Lin
             const int64_t n = tiles[0] * s, m = tiles[1] * t;
             const double us = (a >= b ? deal_out(n, a, m, b, pairs, nullptr)
                                       : deal_out(m, b, n, a, pairs, nullptr)) +
-                              join_us(sizes[0], s) + join_us(sizes[1], t);
+                              join_us(p, s) + join_us(q, t);
             if (least_us == 0.0 || us < least_us) {
                 least_us = us;
                 best[0] = s;

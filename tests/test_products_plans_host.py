@@ -138,3 +138,55 @@ def test_two_products_are_dealt_out_by_the_time_they_take(fake, dim, vocab, rows
                    for b in range(-(-left // others) + 1) for a in range(b + 1)
                    if a * deal["ahead"] + b * others >= left)
         assert ends(deal, long_us, short_us) <= best + 1e-6, (one, two, deal, best)
+
+
+# each 16 products of equal signs lose up to 1.7 x 2^-24 of the sum: these many lose
+# less than a quarter of the type's rounding, 2^-13 or 2^-10
+CHAIN = {F16: 1 << 14, BF16: 1 << 17, F32: 1 << 10}
+
+
+def products_in_a_row(shape):
+    return -(-shape["blocks"] // (shape["splits"] * shape["chains"])) * 64
+
+
+@pytest.mark.parametrize("rows", [1000, 16384, 16385, 100000, 131072, 131073, 1 << 20, (1 << 22) + 7])
+@pytest.mark.parametrize("cin,cout", [(4096, 16128), (768, 768), (2048, 100), (100, 2048)])
+def test_sums_for_16_bits_are_in_chains_where_the_cut_would_show(fake, rows, cin, cout):
+    for dtype in (F16, BF16):
+        for grad in (F16, BF16, F32):
+            for dx in (False, True):
+                shapes = [s for one, two, _ in backward(fake, cin, cout, rows, dtype, grad, dx=dx)
+                          for s in (one, two) if s and s["blocks"] == -(-rows // 64)]
+                assert shapes, "no product over the rows"
+                for s in shapes:
+                    assert products_in_a_row(s) <= CHAIN[grad], (s, dtype, grad)
+                    if rows <= CHAIN[grad]:
+                        assert s["chains"] == 1 or grad == F32
+
+
+@pytest.mark.parametrize("features", [40000, 300000])
+def test_long_sums_of_outputs_and_inputs_too(fake, features):
+    for dtype in (F16, BF16):
+        lin = create(fake, "linear", features, 64)
+        n = ctypes.c_int64()
+        assert fake.linear_workspace(lin, 500, 0, ctypes.byref(n)) == osr.OK
+        (one, _, _), = launches(fake, lambda: fake.linear_forward(
+            lin, place(1), features, place(2), features, dtype, None, dtype, None, 0, 0, place(4), 64,
+            None, 0, 500, 0, WORK, n.value, None))
+        assert products_in_a_row(one) <= CHAIN[dtype], one
+        fake.linear_destroy(lin)
+        for one, two, _ in backward(fake, 64, features, 500, dtype, dtype, dw=False):
+            assert two is None and products_in_a_row(one) <= CHAIN[dtype], one
+
+
+@pytest.mark.parametrize("rows,vocab", [(300, 1 << 20), (200000, 5000), (70000, 40000)])
+def test_long_sums_of_the_cross_entropys_gradients(fake, rows, vocab):
+    for dtype in (F16, BF16):
+        for grad in (F16, BF16, F32):
+            got = ce_backward(fake, 512, vocab, rows, dtype, grad)
+            for one, two, _ in got:
+                for s in (one, two):
+                    if s is None or s["blocks"] == 512 // 64:
+                        continue  # the logits
+                    over_rows = s["blocks"] == -(-rows // 64)
+                    assert products_in_a_row(s) <= CHAIN[grad if over_rows else dtype], s
