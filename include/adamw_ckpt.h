@@ -829,12 +829,13 @@ ADAMW_API int layernorm_backward(layernorm_ctx* ctx, const void* d_dy, int64_t d
  * time); bias, activation and residual are float32, each output is rounded
  * once.  dz is a factor of two products, so it is rounded to dy's type if
  * there is an activation; dbias sums the unrounded values.  The tensor cores
- * cut their float32 sums instead of rounding them: a float32 dweight is off by
- * up to about 1e-9 of its value for each row, in chains of 1024 rows that are
- * rounded as they are added (those from the second on with subnormal sums as 0).
- * 16-bit outputs of more than 2^14 (binary16) or 2^17 products (bfloat16) are
- * summed in chains of that many, so the cut is less than a quarter of their
- * rounding at any length.
+ * cut their float32 sums instead of rounding them, by up to 2^-23 of the sum of
+ * the terms' sizes for each 16 products.  A float32 dweight is summed in chains
+ * of 1024 rows, so by up to 7.6e-6 of it, and the chains are rounded as they are
+ * added (those from the second on with subnormal sums as 0).  16-bit
+ * outputs of more than 2^14 (binary16) or 2^17 products (bfloat16) are summed in
+ * chains of that many, so the cut is less than a quarter of their rounding at
+ * any length.
  *
  * linear_create: 1 <= in, out <= 2^24, in x out < 2^40; nothing on the
  *   device but a pinned word.  Calls with one context may run at the same

@@ -133,10 +133,11 @@ int64_t tiles_of(int64_t m, int64_t n, int bn)
     return ((m + kGemmTileM - 1) / kGemmTileM) * ((n + bn - 1) / bn);
 }
 
-// The tensor cores cut each addition, by up to 2^-24 of the sum: 16384
-// products in a row lose 2e-5 of it, which shows in float32.  Chains of at most 16
-// blocks, 1024 products, lose 1.2e-6, and between them the sums are rounded (random
-// values, 8192 products: 1.0e-6 off in the 2-norm, 4.4e-6 in chains of 4096).  Each
+// The tensor cores cut each addition, by up to 2^-23 of the sum for each 16
+// products of equal signs (1.7 x 2^-24 measured, see linear_chain): 16384 in a row
+// lose 1.0e-4 of it, which shows in float32.  Chains of at most 16 blocks, 1024
+// products, lose 6.5e-6, and between them the sums are rounded (random values, 8192
+// products: 1.0e-6 off in the 2-norm, 4.4e-6 in chains of 4096).  Each
 // is added in L2: 8192 x 4096 x 8192 into float32 takes 378 us, 328 in chains of 4096
 // and 431 in chains of 1365 that the threads read, add to and write back.
 // 16-bit outputs have chains as soon as the cut could pass a quarter of their rounding

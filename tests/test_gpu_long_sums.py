@@ -1,4 +1,5 @@
-"""Sums over hundreds of thousands of rows into 16-bit gradients.
+"""Sums over many rows: 16-bit gradients over hundreds of thousands, float32 ones
+in chains of 1024.
 
 The tensor cores cut their float32 sums: of equal signs, each 16 products lose up to
 1.7 x 2^-24 of the sum.  Chains of 2^14 products (binary16) and 2^17 (bfloat16)
@@ -103,3 +104,33 @@ def test_cross_entropy():
     # other way, and errs by 2^-20: so dl is p
     assert float(off.abs().max()) <= 1.25 * U["f16"] + 2.0 ** -19
     assert bool((dw[8:] == dw[8]).all())
+
+
+# a float32 gradient: chains of 1024 products, 64 steps of 16, lose less than 2^-23 of
+# the sum for each; wide ones and narrow ones, whose tiles lie the other way round
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,cin,cout,grad_in_out", [
+    (13000, 2056, 4104, False), (40000, 2048, 100, False), (40000, 100, 2048, True),
+    (40000, 2050, 33, False), (5000, 768, 768, True)])
+def test_float32_gradients_keep_their_bits(kind, rows, cin, cout, grad_in_out):
+    r = torch.Generator(device="cuda").manual_seed(11)
+    w = torch.zeros(cout, cin, device="cuda", dtype=TYPES[kind])
+    cut, roundings = 64 * 2.0 ** -23, (-(-rows // 1024) + 1) * 2.0 ** -24
+    with osr.linear_create(cin, cout) as lin:
+        def gradient(x, dy):
+            dw = torch.zeros((cin, cout) if grad_in_out else (cout, cin), device="cuda")
+            dw = dw.T if grad_in_out else dw
+            osr.linear_backward(lin, dy, x, w, dx=False, dweight=dw, accumulate=True)
+            return dw
+
+        x, dy = positive(r, rows, cin, kind), positive(r, rows, cout, kind)
+        want = dy.double().T @ x.double()
+        dw = gradient(x, dy)
+        assert float((dw.double() / want - 1).abs().max()) <= cut + roundings
+        assert torch.equal(dw, gradient(x, dy))
+        # of either sign: a chain's partial sums are no larger than its terms' norm in
+        # the mean, so the cuts' norm is no larger than that share of the gradient's
+        x, dy = (torch.randn(rows, n, device="cuda", generator=r).to(TYPES[kind])
+                 for n in (cin, cout))
+        want = dy.double().T @ x.double()
+        assert float((gradient(x, dy).double() - want).norm()) <= (cut + roundings) * float(want.norm())
