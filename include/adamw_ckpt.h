@@ -894,7 +894,10 @@ ADAMW_API int linear_backward(linear_ctx* ctx, const void* d_dy, int64_t dy_stri
  * gradients (its x must be finite: 0 times it is added to dweight).  A
  * target of vocab or more gives a NaN loss and NaN gradients, which the
  * optimizer step refuses.  lse is written for every row.
- * Logits are sums in float32 and are never stored.  The backward pass
+ * Logits are sums in float32 and are never stored.  They are cut, not rounded,
+ * by up to 2^-23 of the sum of their terms' sizes for each 16 of `dim`, and not
+ * in chains: loss and lse are off by up to dim 2^-27 of that (768: 5.7e-6 of it),
+ * besides a few units in the last place.  The backward pass
  * computes them again, for a piece of the vocabulary at a time, and keeps dl
  * of that piece in the workspace, rounded to dtype (for binary16 after the
  * product with a power of two that keeps the largest in range), as it is a
