@@ -836,6 +836,9 @@ ADAMW_API int layernorm_backward(layernorm_ctx* ctx, const void* d_dy, int64_t d
  * outputs of more than 2^14 (binary16) or 2^17 products (bfloat16) are summed in
  * chains of that many, so the cut is less than a quarter of their rounding at
  * any length.
+ * Of any activation, a z of NaN gives NaN, and so does its slope; at infinity the
+ * value is infinity and the slope 1, at -infinity both are 0 (the formulas' limits),
+ * so dz there is 0 for a finite dy.
  *
  * linear_create: 1 <= in, out <= 2^24, in x out < 2^40; nothing on the
  *   device but a pinned word.  Calls with one context may run at the same

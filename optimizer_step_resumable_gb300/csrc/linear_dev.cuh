@@ -236,10 +236,12 @@ __device__ __forceinline__ float2 activated(float2 z)
     } else if constexpr (kAct == LINEAR_GELU_TANH) {
         // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
         constexpr float k = -2.0f * kGeluScale * kLog2E;
-        const float2 w = fma2(mul2(z, z), both(k * kGeluCube), both(k));
-        return mul2(z, logistic(mul2(z, w)));
+        const float2 near = at_least(z, -kFar);
+        const float2 w = fma2(mul2(near, near), both(k * kGeluCube), both(k));
+        return mul2(near, logistic(mul2(near, w)));
     } else if constexpr (kAct == LINEAR_SILU) {
-        return mul2(z, logistic(mul2(z, both(-kLog2E))));
+        const float2 near = at_least(z, -kFar);
+        return mul2(near, logistic(mul2(near, both(-kLog2E))));
     } else {
         return z;
     }
@@ -250,8 +252,10 @@ template <int kAct>
 __device__ __forceinline__ float2 slope(float2 z)
 {
     using namespace packed;
-    if constexpr (kAct == LINEAR_RELU)
-        return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
+    if constexpr (kAct == LINEAR_RELU) {
+        const auto one = [](float x) { return x > 0.0f ? 1.0f : x != x ? x : 0.0f; };
+        return make_float2(one(z.x), one(z.y));
+    }
     const float2 near = at_most(at_least(z, -kFar), kFar);
     if constexpr (kAct == LINEAR_GELU) {
         const Normal n = normal(minus_abs(near));

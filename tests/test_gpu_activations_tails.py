@@ -93,3 +93,46 @@ def test_slopes(act, kind, pad):
     check(dx, slope, size, kind, 500)
     off = (db.double() - slope.sum(0)).abs()
     assert bool((off <= FEW * size.sum(0) + rows * 500 * 2.0 ** -126).all())
+
+
+INF, NAN = float("inf"), float("nan")
+
+
+# z through the bias: infinities and NaN beside ordinary values, in each of the kernels
+# that finish sums
+@pytest.mark.parametrize("rows,cin", [(1, 64), (5, 64), (40, 64), (40, 4096), (300, 64)])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("residual", [False, True])
+def test_values_at_infinity_and_nan(act, rows, cin, residual):
+    z = torch.zeros(264, device="cuda")
+    z[::4], z[1::4], z[2::4] = INF, -INF, NAN
+    x = torch.zeros(rows, cin, device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros(264, cin, device="cuda", dtype=torch.bfloat16)
+    res = torch.full((rows, 264), 3.0, device="cuda", dtype=torch.bfloat16) if residual else None
+    with osr.linear_create(cin, 264) as lin:
+        y = osr.linear_forward(lin, x, w, bias=z, residual=res, activation=act).float()
+    more = 3.0 if residual else 0.0
+    assert bool((y[:, ::4] == INF).all()) and bool((y[:, 1::4] == more).all())
+    assert bool(y[:, 2::4].isnan().all()) and bool((y[:, 3::4] == more).all())
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("cols", [264, 261])
+def test_slopes_at_infinity_and_nan(act, cols):
+    rows = 33
+    z = torch.zeros(rows, cols, device="cuda", dtype=torch.float16)
+    z[:, ::4], z[:, 1::4], z[5, 2::4] = INF, -INF, NAN
+    dy = torch.full((rows, cols), 2.0, device="cuda", dtype=torch.float16)
+    w = torch.eye(cols, device="cuda", dtype=torch.float16)
+    db = torch.empty(cols, device="cuda")
+    with osr.linear_create(cols, cols) as lin:
+        dx, _, _ = osr.linear_backward(lin, dy, dy, w, z=z, activation=act, dbias=db)
+    at_zero = 0.0 if act == "relu" else 1.0  # 2 act'(0)
+    want = torch.full((cols,), at_zero, device="cuda")
+    want[::4], want[1::4] = 2.0, 0.0
+    assert bool(((dx.float() - want).abs() <= 2.0 ** -10)[torch.arange(rows) != 5].all())
+    assert bool(dx[5].isnan().all())  # a factor of all sums of its row
+    want = (rows * want)
+    want[2::4] = NAN
+    assert bool(db[2::4].isnan().all())
+    assert bool(((db - want).abs() <= rows * 2.0 ** -10)[~want.isnan()].all())
