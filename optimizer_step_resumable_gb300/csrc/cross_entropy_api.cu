@@ -2,7 +2,6 @@
 // vocabulary (linear_cross_entropy_* of include/adamw_ckpt.h).
 #include <cmath>
 #include <cstdint>
-#include <cstring>
 #include <new>
 
 #include <cuda_runtime.h>
@@ -63,12 +62,9 @@ struct Pieced {
 struct linear_ce_ctx {
     osr::ProductContext base;
     int32_t dim = 0, vocab = 0;
-    // the last piece found and the last backward call's plans, which take as long
-    // to make as some launches
+    // the last piece found, which takes as long as some launches
     int64_t piece_rows = -1, piece = 0;
-    int64_t rows = -1;
-    Needs needs{};
-    Pieced pieced;
+    osr::RecentPlans<Needs, Pieced> pieced;
 };
 
 namespace {
@@ -154,12 +150,7 @@ Pieced make_pieces(linear_ce_ctx* c, int64_t rows, const Needs& n)
 }
 const Pieced& pieces_of(linear_ce_ctx* c, int64_t rows, const Needs& n)
 {
-    if (rows != c->rows || std::memcmp(&n, &c->needs, sizeof n) != 0) {
-        c->pieced = make_pieces(c, rows, n);
-        c->rows = rows;
-        c->needs = n;
-    }
-    return c->pieced;
+    return c->pieced.of(rows, n, [&] { return make_pieces(c, rows, n); });
 }
 
 struct Parts {

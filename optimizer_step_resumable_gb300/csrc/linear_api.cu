@@ -1,7 +1,6 @@
 // linear_api.cu -- the C ABI entry points of the linear layer (linear_* of
 // include/adamw_ckpt.h).
 #include <cstdint>
-#include <cstring>
 #include <new>
 
 #include <cuda_runtime.h>
@@ -55,10 +54,7 @@ struct Plans {
 struct linear_ctx {
     osr::ProductContext base;
     int32_t in = 0, out = 0;
-    // the last call's plans, which take as long to make as some launches
-    int64_t rows = -1;
-    Needs needs{};
-    Plans plans;
+    osr::RecentPlans<Needs, Plans> plans;
 };
 
 namespace {
@@ -97,12 +93,7 @@ Plans make_plans(const linear_ctx* c, int64_t rows, const Needs& n)
 
 const Plans& plans_of(linear_ctx* c, int64_t rows, const Needs& n)
 {
-    if (rows != c->rows || std::memcmp(&n, &c->needs, sizeof n) != 0) {
-        c->plans = make_plans(c, rows, n);
-        c->rows = rows;
-        c->needs = n;
-    }
-    return c->plans;
+    return c->plans.of(rows, n, [&] { return make_plans(c, rows, n); });
 }
 
 // Where the parts of a call's workspace lie; NULL where the call needs none.

@@ -190,3 +190,36 @@ def test_long_sums_of_the_cross_entropys_gradients(fake, rows, vocab):
                         continue  # the logits
                     over_rows = s["blocks"] == -(-rows // 64)
                     assert products_in_a_row(s) <= CHAIN[grad if over_rows else dtype], s
+
+
+def test_calls_in_turn_with_one_context_are_planned_as_alone(fake):
+    # more different calls than a context keeps plans of, in every order
+    cin, cout = 768, 1536
+    work = ctypes.c_int64(1 << 40)
+
+    def calls(lin, rows, dtype):
+        yield lambda: fake.linear_forward(
+            lin, place(1), cin, place(2), cin, dtype, None, dtype, None, 0, 0, place(4), cout, None,
+            0, rows, 0, WORK, work, None)
+        for grad, dx in ((F32, True), (dtype, True), (F32, False)):
+            yield lambda grad=grad, dx=dx: fake.linear_backward(
+                lin, place(1), cout, place(2), cin, place(3), cin, dtype, None, 0, 0,
+                place(6) if dx else None, cin, place(8), cin, None, grad, rows, 0, WORK, work, None)
+
+    def alone(rows, dtype):
+        lin = create(fake, "linear", cin, cout)
+        got = [launches(fake, c) for c in calls(lin, rows, dtype)]
+        fake.linear_destroy(lin)
+        return got
+
+    sizes = [(rows, dtype) for rows in (40, 1000, 300000) for dtype in (F16, BF16)]
+    want = {s: alone(*s) for s in sizes}
+    assert len({str(w) for w in want.values()}) > 3
+    lin = create(fake, "linear", cin, cout)
+    for turn in range(2):
+        for s in sizes if turn == 0 else reversed(sizes):
+            assert [launches(fake, c) for c in calls(lin, *s)] == want[s]
+    for i in range(4):
+        for s in sizes:
+            assert launches(fake, list(calls(lin, *s))[i]) == want[s][i]
+    fake.linear_destroy(lin)
