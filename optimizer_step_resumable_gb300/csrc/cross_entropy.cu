@@ -150,9 +150,10 @@ __device__ __forceinline__ float2 factors(const CeFactors& f, int64_t row, int64
     return make_float2(g * fmaf(f.two_z, lse, 1.0f), g);
 }
 
-// One block: the power of two that brings the rows' largest factor to [2^14,
-// 2^15), and its inverse.  The gradient of a logit is at most twice that;
-// binary16 ends at 65504 and loses bits below 2^-14.
+// One block: the power of two that brings the largest that a row's gradient of a
+// logit can be to [2^14, 2^15), and its inverse: p factor.x, and at the target
+// p factor.x - factor.y, for any p from 0 to 1.  Binary16 ends at 65504 and loses
+// bits below 2^-14.
 constexpr int kCeNormThreads = 1024;
 __global__ void __launch_bounds__(kCeNormThreads) k_ce_norm(const CeFactors f, int64_t rows,
                                                           float* norms)
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kCeNormThreads) k_ce_norm(const CeFactors f, i
 #pragma unroll 4
     for (int64_t r = threadIdx.x; r < rows; r += kCeNormThreads) {
         const float2 g = factors(f, r, f.target[r], f.lse[r]);
-        most = fmaxf(most, fmaxf(fabsf(g.x), fabsf(g.y)));
+        most = fmaxf(most, fmaxf(fmaxf(fabsf(g.x), fabsf(g.y)), fabsf(g.x - g.y)));
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)

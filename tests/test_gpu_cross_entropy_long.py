@@ -1,5 +1,5 @@
-"""The cross entropy of wide inputs: what the logits' sums may lose, and gradients
-of several pieces of the vocabulary.
+"""The cross entropy of wide inputs: what the logits' sums may lose, gradients of
+several pieces of the vocabulary, and the largest that binary16 has to hold.
 
 A logit is cut by up to 2^-23 of the sum of its terms' sizes for each 16 inputs;
 loss and lse err by as much as the logits, and by a few units of the logits'
@@ -87,3 +87,31 @@ def test_gradients_over_pieces(kind, grad, grad_in_out):
     assert rounded ** 0.5 <= most
     off = (dx.double() - want_dx).norm()
     assert float(off) <= (2 * U[kind] + 2.0 ** -17) * float(want_dx.norm())
+
+
+@pytest.mark.parametrize("g", [1.0, 1.9999, 3.9, 6e-5, 1.9999 * 2.0 ** 100])
+@pytest.mark.parametrize("factor", [-1.0, -0.5, -3.0, 1.0])
+def test_factors_of_opposite_signs_stay_in_range(g, factor):
+    # a penalty that turns the sign of p's factor: the target's place gets p factor g - g,
+    # up to twice the larger of both
+    rows, dim, vocab = 40, 64, 300
+    x = torch.ones(rows, dim, device="cuda", dtype=torch.float16)
+    w = torch.zeros(vocab, dim, device="cuda", dtype=torch.float16)
+    w[7] = 0.5  # its logit is 32, the others 0: p is 1 to 300 e^-32
+    target = torch.full((rows,), 7, device="cuda")
+    dloss = torch.full((rows,), g, device="cuda")
+    scale = 1.0 / g
+    z_loss = (factor - 1) / (2 * 32.0)
+    dw = torch.empty(vocab, dim, device="cuda")
+    with osr.linear_cross_entropy_create(dim, vocab) as ce:
+        _, lse = osr.linear_cross_entropy_forward(ce, x, w, target, z_loss=z_loss)
+        dx, _ = osr.linear_cross_entropy_backward(ce, x, w, target, lse, dloss=dloss, scale=scale,
+                                                  z_loss=z_loss, dweight=dw)
+    # dl = factor - 1 in units of g.  It errs by its rounding, U of itself, and by p's
+    # error: the exponent is a difference of numbers near 46 (32 in powers of two),
+    # each rounded, 46 x 2^-24 twice, times log 2: below 2^-17 of |factor|, also where
+    # dl is 0.  Then the output's rounding.
+    want = factor - 1.0
+    off = U["f16"] * abs(want) + 2.0 ** -17 * (abs(factor) + 1)
+    assert bool(((dx.double() - want * 0.5).abs() <= off + 2.0 ** -12 * abs(want)).all())
+    assert bool(((dw[7].double() - want * rows).abs() <= off * rows).all())
