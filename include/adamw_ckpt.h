@@ -955,7 +955,8 @@ ADAMW_API int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x,
  *   dl = scale dloss T (p - sum of q over the entries with that id).
  * An entry with an id below 0, or a value of -infinity, is none; a row
  * without entries has loss 0 and a zero gradient, whatever its logits.  An
- * id of vocab or more gives a NaN loss and a row of NaN gradients.
+ * id of vocab or more, unless its entry is none by its value, gives a NaN loss
+ * and a row of NaN gradients.
  *
  * distill_create: 1 <= vocab <= 2^30, 1 <= k <= 1024; nothing on the device,
  *   so calls with one context may run at the same time.

@@ -154,7 +154,8 @@ __device__ __forceinline__ void join_value(float x, float& most, float& sum)
 }
 
 // An entry of the teacher's row: its id (-1: none, -2: past the vocabulary) and
-// its value in powers of two, -inf where there is none.
+// its value in powers of two, -inf where there is none.  A value of -inf is none
+// also past the vocabulary, where a wider teacher has its masked words.
 struct Entry {
     int32_t id;
     float v;
@@ -165,7 +166,9 @@ __device__ __forceinline__ Entry entry_of(const Distill& a, int64_t row, int32_t
         return Entry{-1, -INFINITY};
     const int64_t id = a.ids[row * a.k + j];
     const float v = load_as(a.values, row * a.k + j, a.values_dtype) * unit;
-    return Entry{id < 0 ? -1 : id >= a.vocab ? -2 : int32_t(id), id < 0 ? -INFINITY : v};
+    if (id < 0)
+        return Entry{-1, -INFINITY};
+    return Entry{id < a.vocab ? int32_t(id) : v == -INFINITY ? -1 : -2, v};
 }
 
 template <typename T>
