@@ -964,6 +964,7 @@ ADAMW_API int linear_cross_entropy_backward(linear_ce_ctx* ctx, const void* d_x,
  *   logits itself.  ids: int64, values: values_dtype (any), both rows x k
  *   without gaps.  loss, lse, dloss: float32, one a row; lse may be NULL in
  *   the forward pass, dloss NULL: 1.  0 <= rows < 2^31.
+ * temperature: T, from 2^-60 to 2^60.
  * Everything is float32 inside; each gradient is rounded once.  Every array
  * must be aligned to its elements (rows of logits and dlogits that start at
  * the same place within 16 bytes are read and written in vectors); no output

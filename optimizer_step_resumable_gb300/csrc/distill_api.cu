@@ -43,10 +43,9 @@ int check_common(const distill_ctx* ctx, const void* d_logits, int64_t stride, i
         return fail(ADAMW_EINVAL, "values_dtype=%d is not F32, BF16 or F16", values_dtype);
     if (rows < 0 || rows > INT32_MAX)
         return fail(ADAMW_EINVAL, "rows=%lld outside [0, 2^31 - 1]", (long long)rows);
-    if (!(float(temperature) > 0.0f && std::isfinite(float(temperature)) &&
-          std::isfinite(1.0f / float(temperature))))
-        return fail(ADAMW_EINVAL, "temperature=%g must be finite and > 0, as its inverse",
-                    temperature);
+    // beyond, T^2 or log2(e) / T leaves float32: the loss would be 0, infinity or NaN
+    if (!(temperature >= std::ldexp(1.0, -60) && temperature <= std::ldexp(1.0, 60)))
+        return fail(ADAMW_EINVAL, "temperature=%g outside [2^-60, 2^60]", temperature);
     int rc;
     if ((rc = check_rows(d_logits, stride, rows, ctx->vocab, size_of(dtype), "d_logits")) ||
         (rc = check_array(d_ids, 8, rows == 0, "d_ids")) ||

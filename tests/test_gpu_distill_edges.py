@@ -48,3 +48,15 @@ def test_masked_entries_past_the_vocabulary_are_none(kind, k):
     values[1, 3], values[2, k - 1] = 0.5, NAN
     loss, _, dl = both(logits, ids, values)
     assert loss.isnan().tolist() == dl.isnan().all(1).tolist() == [i in (1, 2) for i in range(8)]
+
+
+@pytest.mark.parametrize("t", [2.0 ** -60, 2.0 ** -30, 2.0 ** -8, 2.0 ** 8])
+def test_temperatures_of_any_size(t):
+    # logits and values in units of t: T^2 times the loss and T times the gradient of T = 1
+    logits, ids, values = inputs(20, 1000, 8)
+    loss, lse, dl = both(logits, ids, values)
+    got = both(logits * t, ids, values * t, temperature=t)
+    assert torch.allclose(got[1], lse, rtol=2.0 ** -20)
+    assert torch.allclose(got[0] / t ** 2, loss, rtol=2.0 ** -18, atol=2.0 ** -18)
+    assert torch.allclose(got[2] / t, dl, rtol=2.0 ** -18, atol=2.0 ** -22)
+    assert bool((got[0] > 0).all())
