@@ -966,6 +966,7 @@ class _Scratch:
 
     def __init__(self, ctx, rows: int, flags: int, workspace, stream: int):
         global _alloc, _free
+        self.own = False
         need = ctx._bytes.get((rows, flags))
         if need is None:
             n = ctypes.c_int64()
@@ -974,7 +975,6 @@ class _Scratch:
             if len(ctx._bytes) > 256:
                 ctx._bytes.clear()
             need = ctx._bytes[rows, flags] = n.value
-        self.own = False
         if workspace is not None:
             if workspace.get_device() != ctx.device or not workspace.is_contiguous():
                 raise TypeError("workspace must be a contiguous CUDA tensor of the context's device")
@@ -987,12 +987,13 @@ class _Scratch:
             if _alloc is None:
                 _alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
                 _free = torch._C._cuda_cudaCachingAllocator_raw_delete
-            self.bytes, self.own = need, True
+            self.bytes = need
             if torch._C._cuda_getDevice() == ctx.device:
                 self.ptr = _alloc(need, stream)  # a tensor would take 3 us to make
             else:
                 with torch.cuda.device(ctx.device):
                     self.ptr = _alloc(need, stream)
+            self.own = True
 
     def done(self):
         if self.own:
