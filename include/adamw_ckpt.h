@@ -862,8 +862,10 @@ ADAMW_API int layernorm_backward(layernorm_ctx* ctx, const void* d_dy, int64_t d
  * with an input or another output, but for residual as above, nor the
  * workspace with any of them (ADAMW_EINVAL).
  * Asynchronous on `stream`.  Errors: ADAMW_EINVAL, ADAMW_ECUDA, ADAMW_ESTATE
- * (a kernel of an earlier call of this context gave up waiting and its
- * outputs are not valid; reported once).
+ * (a kernel of an earlier call of this context gave up waiting, after four
+ * seconds, and its outputs are not valid; reported once).  A graph's replay
+ * makes no call: once it has run, linear_forward with rows = 0, which launches
+ * nothing, reports of it.
  */
 ADAMW_API int linear_create(int32_t in_features, int32_t out_features, linear_ctx** out);
 ADAMW_API int linear_destroy(linear_ctx* ctx);

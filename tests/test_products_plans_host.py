@@ -223,3 +223,24 @@ def test_calls_in_turn_with_one_context_are_planned_as_alone(fake):
         for s in sizes:
             assert launches(fake, list(calls(lin, *s))[i]) == want[s][i]
     fake.linear_destroy(lin)
+
+
+@pytest.mark.parametrize("kind", ["linear", "linear_cross_entropy"])
+def test_a_call_without_rows_reports_a_kernel_that_gave_up(fake, kind):
+    # how a caller who replays a graph asks: no launch, the state once
+    h = create(fake, kind, 64, 48)
+
+    def ask():
+        if kind == "linear":
+            return fake.linear_forward(h, None, 64, place(2), 64, BF16, None, BF16, None, 0, 0, None,
+                                       48, None, 0, 0, 0, None, 0, None)
+        return fake.linear_cross_entropy_forward(h, None, 64, place(2), 64, BF16, None, 0.0, None,
+                                                 None, 0, 0, None, 0, None)
+
+    before = fake.fake_launches()
+    assert ask() == osr.OK
+    # the context's word in host memory, behind device and SM count
+    word = ctypes.cast(h.value + 8, ctypes.POINTER(ctypes.POINTER(ctypes.c_int32))).contents
+    word[0] = 1
+    assert ask() == osr.ESTATE and b"gave up" in fake.adamw_last_error()
+    assert ask() == osr.OK and fake.fake_launches() == before
