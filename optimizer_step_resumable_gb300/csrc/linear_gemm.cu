@@ -120,8 +120,11 @@ int join(const LinearOut& o, const float* partials, int64_t rows, int64_t column
 
 // Microseconds that a pair of blocks takes for a block of the inner dimension
 // of a tile of 256 x bn (8192 x 4096 x 8192: 283, 324 and 414 us in tiles of 256,
-// 192 and 128 columns, 64 blocks in 14, 19 and 27 turns), and for the start and
-// the last epilogue of a launch (8192 x 768 x 768: 15.8, 12.9 and 14.4 us).
+// 192 and 128 columns, 64 blocks in 14, 19 and 27 turns; few rows of 76 x 256
+// outputs, 16 and 32 blocks: 0.21, 0.19 and 0.14 us in tiles of 128, 64 and 32 columns
+// with the weight in L2, 0.37 in all of them with the weight from memory, which no
+// constant here stands for), and for the start and the last epilogue of a launch (8192 x
+// 768 x 768: 15.8, 12.9 and 14.4 us).
 double block_us(int bn)
 {
     return bn == 256 ? 0.316 : bn == 192 ? 0.27 : bn == 128 ? 0.24 : bn == 64 ? 0.2 : 0.18;
