@@ -134,3 +134,39 @@ def test_float32_gradients_keep_their_bits(kind, rows, cin, cout, grad_in_out):
                  for n in (cin, cout))
         want = dy.double().T @ x.double()
         assert float((gradient(x, dy).double() - want).norm()) <= (cut + roundings) * float(want.norm())
+
+
+def test_chains_through_the_workspace_in_a_graph_and_on_streams():
+    # a binary16 gradient over more rows than one chain takes, beside dx: captured and
+    # replayed over garbage, and two calls at a time with one context
+    rows, cin, cout = 40000, 600, 520
+    r = torch.Generator(device="cuda").manual_seed(13)
+    x, dy = positive(r, rows, cin, "f16"), positive(r, rows, cout, "f16", 2.0 ** -8)
+    w = positive(r, cout, cin, "f16")
+    with osr.linear_create(cin, cout) as lin:
+        def step(stream=None):
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream())
+            dw = torch.empty(cout, cin, device="cuda", dtype=torch.float16)
+            db = torch.empty(cout, device="cuda", dtype=torch.float16)
+            dx, _, _ = osr.linear_backward(lin, dy, x, w, dweight=dw, dbias=db, stream=stream)
+            return dx, dw, db
+
+        first = step()
+        check(first[1], dy.double().T @ x.double(), rows, "f16")
+        torch.cuda.synchronize()
+        both = [step(torch.cuda.Stream()) for _ in range(2)]
+        torch.cuda.synchronize()
+        for got in both:
+            assert all(torch.equal(a, b) for a, b in zip(first, got))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            captured = step()
+        for _ in range(3):
+            for t in captured:
+                t.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(first, captured))
+        # asks whether a replayed kernel gave up: no rows, no launch
+        osr.linear_forward(lin, x[:0], w)
