@@ -44,8 +44,8 @@ inline void accumulate_into(LinearOut& o)
 
 // How it is computed: in tiles of 256 x bn with the inner dimension in
 // `splits` ranges, each in `chains` (see GemmShape), and the sums joined by a
-// second kernel if there are `partials`; swapped: the tile's long side lies along the columns, for
-// products of few rows.
+// second kernel if there are `partials`; swapped: the tile's long side lies along
+// the columns, for products of few rows.
 struct LinearPlan {
     bool few;  // not in tiles at all (linear_few.cu)
     bool swapped;
